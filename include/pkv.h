@@ -162,6 +162,70 @@ kv_status_t kv_slot_mapping(const int32_t* block_tables, int max_blocks_per_seq,
 kv_status_t kv_append(kv_pool_t* pool, int layer, const int32_t* seq_ids, int n_tokens,
                       const void* k, const void* v, const int32_t* slot_mapping, void* stream);
 
+/* ---------------------------------------- append with position rotation */
+
+/* How the rows of a head are rotated.  Pair i of rot_dim / 2 turns by the
+ * angle positions[axis[i]][token] * inv_freq[i] (radians):
+ *   y_a = amplitude * (x_a cos - x_b sin), y_b = amplitude * (x_b cos + x_a sin)
+ * on elements (a, b) = (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved
+ * (the two pairing styles of checkpoints: "Reading Inference Engine
+ * Codebases", Example 2); elements from rot_dim on stay as they are.
+ *   rot_dim    even, 2 .. 256 (and at most the head_dim it is used with)
+ *   num_axes   1 .. 8 positions a token: 1 for text, 3 for image and video
+ *              tokens (time, height, width)
+ *   amplitude  factor on the rotated elements (1 in most models)
+ *   inv_freq   host double[rot_dim / 2], finite
+ *   axis       host int32[rot_dim / 2], each 0 .. num_axes - 1; NULL: all 0 */
+typedef struct {
+    int rot_dim;
+    int interleaved;
+    int num_axes;
+    float amplitude;
+    const double* inv_freq;
+    const int32_t* axis;
+} kv_rope_config_t;
+
+typedef struct kv_rope kv_rope_t;
+
+/* Copies the configuration into a handle (host memory only; a handle serves
+ * any number of threads, devices and captured graphs). */
+kv_status_t kv_rope_create(const kv_rope_config_t* cfg, kv_rope_t** rope_out);
+void kv_rope_destroy(kv_rope_t* rope);
+
+/* kv_append (kv_append_fp8 for an E4M3 pool) with the K rows rotated on the
+ * way, and the step's query rows rotated into q_out, in one kernel.  Angles
+ * are good to 2^-32 of a turn at any position (|inv_freq| up to 2^20); the
+ * rotation is computed in fp32 and rounded once, to the pool's type, or to the E4M3 code nearest to
+ * the fp32 quotient by k_scale.  V rows are stored as kv_append (kv_append_fp8)
+ * stores them.
+ *   k, v          device, n_tokens rows [num_kv_heads][head_dim] in src_dtype
+ *                 (the pool's type; for an E4M3 pool KV_F32, KV_F16 or
+ *                 KV_BF16), consecutive tokens k_stride (v_stride) elements
+ *                 apart, so slices of a packed projection are taken where
+ *                 they lie
+ *   q, q_out      device, n_tokens rows [num_q_heads][head_dim] in src_dtype,
+ *                 q_stride (q_out_stride) elements apart; q_out may be q
+ *                 itself with the same stride, but overlap q, k or v in no
+ *                 other way.  q NULL: no query rows
+ *   positions     device int32 [num_axes][positions_stride], any sign; the
+ *                 first n_tokens of each row are read
+ *   slot_mapping  device int32[n_tokens]; a negative slot writes no K and V
+ *                 (the query rows are rotated all the same), a slot >=
+ *                 num_blocks*block_size neither, and sets KV_FLAG_BAD_SLOT
+ *   seq_ids       device int32[n_tokens] or NULL; a token whose id is
+ *                 negative is padding: nothing of it is written, q_out neither
+ *   k_scale, v_scale  of an E4M3 pool (finite, > 0); not read otherwise
+ * Rows may have any alignment of their type; 16-byte aligned rows with
+ * rot_dim / 2 and head_dim multiples of 16 bytes are the fast ones.  Two
+ * tokens of one call must not share a slot.  Runs on the pool's device, to
+ * which `stream` must belong.  n_tokens == 0 is a no-op. */
+kv_status_t kv_append_rope(kv_pool_t* pool, int layer, const kv_rope_t* rope, const int32_t* seq_ids,
+                           int n_tokens, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, kv_dtype_t src_dtype, const int32_t* slot_mapping,
+                           const int32_t* positions, int64_t positions_stride, const void* q,
+                           int64_t q_stride, void* q_out, int64_t q_out_stride, int num_q_heads,
+                           float k_scale, float v_scale, void* stream);
+
 /* ------------------------------------------------------- decode attention */
 
 typedef enum {

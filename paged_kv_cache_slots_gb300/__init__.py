@@ -17,7 +17,7 @@ import torch
 from . import build as _build
 
 __all__ = [
-    "KVError", "KVPool", "BlockAllocator", "PrefixCachePool", "kv_pool_bytes", "slot_mapping", "workspace_bytes",
+    "KVError", "KVPool", "Rope", "BlockAllocator", "PrefixCachePool", "kv_pool_bytes", "slot_mapping", "workspace_bytes",
     "paged_decode_attention", "device_status", "library_path", "load_library", "workspace_init",
     "make_workspace", "paged_decode_append_attention", "paged_prefill_attention", "slot_mapping_varlen",
 ]
@@ -51,6 +51,12 @@ class _PoolConfig(ctypes.Structure):
                 ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("device", ctypes.c_int)]
 
 
+class _RopeConfig(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("num_axes", ctypes.c_int),
+                ("amplitude", ctypes.c_float), ("inv_freq", ctypes.POINTER(ctypes.c_double)),
+                ("axis", ctypes.POINTER(ctypes.c_int32))]
+
+
 class _DecodeOptions(ctypes.Structure):
     _fields_ = [("num_ctas", ctypes.c_int), ("ctas_per_sm", ctypes.c_int),
                 ("consumer_warps", ctypes.c_int), ("kernel", ctypes.c_int),
@@ -75,6 +81,10 @@ def _declare(lib):
         "kv_pool_config": (I, [P, ctypes.POINTER(_PoolConfig)]),
         "kv_slot_mapping": (I, [P, I, P, I, I, I, P, P]),
         "kv_append": (I, [P, I, P, I, P, P, P, P]),
+        "kv_rope_create": (I, [ctypes.POINTER(_RopeConfig), ctypes.POINTER(P)]),
+        "kv_rope_destroy": (None, [P]),
+        "kv_append_rope": (I, [P, I, P, P, I, P, I64, P, I64, I, P, P, I64, P, I64, P, I64, I, ctypes.c_float,
+                               ctypes.c_float, P]),
         "paged_decode_workspace_bytes": (I, [I, I, I, I, I, ctypes.POINTER(_DecodeOptions),
                                              ctypes.POINTER(SZ)]),
         "paged_decode_attention": (I, [P, P, P, I, P, I, P, I, I, I, I, I, I, ctypes.c_float, P,
@@ -314,6 +324,55 @@ class KVPool:
         _check(self._lib.kv_append(self._handle, layer, _ptr(seq_ids), n, _ptr(k), _ptr(v),
                                    _ptr(slot_mapping), _stream(k, stream)), self._lib)
 
+    def append_rope(self, layer: int, k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
+                    positions: torch.Tensor, rope: "Rope", q: torch.Tensor | None = None,
+                    q_out: torch.Tensor | None = None, seq_ids: torch.Tensor | None = None, stream=None,
+                    k_scale=None, v_scale=None) -> torch.Tensor | None:
+        """append() with the K rows rotated by `rope` at each token's position, and the query
+        rows q ([n, Hq, D]) rotated into q_out (a new tensor unless given; may be q itself).
+
+        k, v and q may be slices of a packed projection (any stride between tokens, heads
+        contiguous).  positions: int32 [n], or [axes, n] for a rope with several axes.  A negative
+        slot writes no K and V; a token with a negative seq_id writes nothing, q_out neither
+        (a new q_out holds zeros there).  Returns q_out, or None without q."""
+        n, Hkv, D = slot_mapping.shape[0], self.cfg.num_kv_heads, self.cfg.head_dim
+        fp8 = self.dtype == FP8
+        if fp8:
+            _need(k_scale is not None and v_scale is not None, "an E4M3 pool needs k_scale and v_scale")
+            _need(k.dtype in (torch.float32, torch.float16, torch.bfloat16), "k/v must be f32, f16 or bf16")
+        else:
+            _need(k.dtype == self.dtype, "k/v dtype must match the pool")
+        _need(v.dtype == k.dtype and (q is None or q.dtype == k.dtype), "k, v and q share a dtype")
+        _need(k.shape == v.shape == (n, Hkv, D), "k and v must be [n_tokens, num_kv_heads, head_dim]")
+        _need(_rows_whole(k) and _rows_whole(v), "a token's k and v rows must be contiguous")
+        _need(slot_mapping.dtype == torch.int32 and slot_mapping.is_contiguous(), "slot_mapping must be int32 [n_tokens]")
+        _need(seq_ids is None or (seq_ids.dtype == torch.int32 and seq_ids.shape == (n,) and seq_ids.is_contiguous()),
+              "seq_ids must be int32 [n_tokens]")
+        _need(positions.dtype == torch.int32 and positions.stride(-1) in (0, 1) if n > 1 else positions.dtype == torch.int32,
+              "positions must be int32, contiguous along tokens")
+        _need(positions.shape == (rope.num_axes, n) or (rope.num_axes == 1 and positions.shape == (n,)),
+              "positions must be [n_tokens], or [axes, n_tokens]")
+        if n > 1 and positions.stride(-1) == 0:
+            positions = positions.contiguous()
+        if q is not None:
+            _need(q.dim() == 3 and q.shape[0] == n and q.shape[2] == D and _rows_whole(q),
+                  "q must be [n_tokens, num_q_heads, head_dim], a token's rows contiguous")
+            if q_out is None:
+                make = torch.empty if seq_ids is None else torch.zeros
+                q_out = make(q.shape, dtype=q.dtype, device=q.device)
+            _need(q_out.dtype == q.dtype and q_out.shape == q.shape and _rows_whole(q_out), "q_out must be like q")
+        else:
+            _need(q_out is None, "q_out without q")
+        _need(all(t is None or t.device == self.device for t in (k, v, slot_mapping, positions, seq_ids, q, q_out)),
+              "every tensor must be on the pool's device")
+        _check(self._lib.kv_append_rope(
+            self._handle, layer, rope._handle, _ptr(seq_ids), n, _ptr(k), k.stride(0), _ptr(v), v.stride(0),
+            DTYPE_CODE[k.dtype], _ptr(slot_mapping), _ptr(positions),
+            positions.stride(0) if positions.dim() == 2 else n, _ptr(q), 0 if q is None else q.stride(0), _ptr(q_out),
+            0 if q is None else q_out.stride(0), 0 if q is None else q.shape[1], float(k_scale) if fp8 else 1.0,
+            float(v_scale) if fp8 else 1.0, _stream(self.buffer, stream)), self._lib)
+        return q_out
+
     def close(self):
         if getattr(self, "_handle", None):
             self._lib.kv_pool_destroy(self._handle)
@@ -322,6 +381,51 @@ class KVPool:
     def __del__(self):
         try:
             self.close()
+        except Exception:
+            pass
+
+
+def _rows_whole(t: torch.Tensor) -> bool:
+    """[n, heads, D] whose heads lie one after the other (any stride between tokens)."""
+    if t.is_contiguous():
+        return True
+    return t.dim() == 3 and (t.shape[2] == 1 or t.stride(2) == 1) and (t.shape[1] == 1 or t.stride(1) == t.shape[2])
+
+
+class Rope:
+    """Rotation of positions into query and key rows, for KVPool.append_rope.
+
+    inv_freq: the rot_dim / 2 frequencies (radians a position; a sequence or a 1-D tensor).
+    Pairs are elements (i, i + rot_dim / 2) of a head, or (2i, 2i + 1) when interleaved.
+    axes: the axis of each frequency (0 for all unless given), for tokens with several
+    positions (time, height, width).  amplitude: factor on the rotated elements.
+    """
+
+    def __init__(self, inv_freq, interleaved: bool = False, axes=None, amplitude: float = 1.0):
+        lib = load_library()
+        if isinstance(inv_freq, torch.Tensor):
+            _need(inv_freq.dim() == 1, "inv_freq must be 1-D")
+            inv_freq = inv_freq.detach().double().tolist()
+        freq = [float(f) for f in inv_freq]
+        axes = None if axes is None else [int(x) for x in axes]
+        _need(axes is None or len(axes) == len(freq), "one axis per frequency")
+        _need(len(freq) > 0, "inv_freq is empty")
+        self.rot_dim = 2 * len(freq)
+        self.num_axes = 1 if axes is None else max(axes) + 1
+        self.interleaved = bool(interleaved)
+        cfg = _RopeConfig(self.rot_dim, int(self.interleaved), self.num_axes, float(amplitude),
+                          (ctypes.c_double * len(freq))(*freq),
+                          None if axes is None else (ctypes.c_int32 * len(axes))(*axes))
+        handle = ctypes.c_void_p()
+        _check(lib.kv_rope_create(ctypes.byref(cfg), ctypes.byref(handle)), lib)
+        self._handle = handle
+        self._lib = lib
+
+    def __del__(self):
+        try:
+            if getattr(self, "_handle", None):
+                self._lib.kv_rope_destroy(self._handle)
+                self._handle = None
         except Exception:
             pass
 

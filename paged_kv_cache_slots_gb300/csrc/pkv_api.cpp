@@ -212,6 +212,50 @@ struct kv_pool {
     kv_block_allocator_t* alloc = nullptr;  // kv_seq_extend / kv_seq_free, created on first use
 };
 
+// ------------------------------------------------------------------ rope
+struct kv_rope {
+    int rot_dim, interleaved, num_axes;
+    float amplitude;
+    uint64_t phase[kMaxRopePairs];
+    uint8_t axis[kMaxRopePairs];
+};
+
+namespace {
+
+// f / (2 pi) turns, modulo 1, as 64-bit fixed point.  1 / (2 pi) is taken as
+// a double and what that leaves, and the product's own rounding error from an
+// fma: for |f| up to 2^20 the result is the nearest multiple of 2^-64, or its
+// neighbour.
+uint64_t turns_fixed_point(double f) {
+    constexpr double kInv2Pi = 0.15915494309189535, kInv2PiRest = -9.839338337591243e-18;
+    const double hi = f * kInv2Pi;
+    const double lo = std::fma(f, kInv2Pi, -hi) + f * kInv2PiRest;
+    auto fixed = [](double x) {
+        double t = std::ldexp(x - std::rint(x), 64);  // x - rint(x) is exact
+        if (t >= 0x1p63) t -= 0x1p64;
+        return static_cast<uint64_t>(static_cast<int64_t>(std::rint(t)));
+    };
+    return fixed(hi) + fixed(lo);
+}
+
+// Whether rows of `row` bytes, `n` of them `stride` bytes apart, at p and at o
+// can touch one another.
+bool rows_overlap(const void* p, int64_t p_stride, int64_t p_row, const void* o, int64_t o_stride,
+                  int64_t o_row, int64_t n) {
+    const int64_t a = reinterpret_cast<intptr_t>(p), b = reinterpret_cast<intptr_t>(o);
+    const int64_t a_end = a + (n - 1) * p_stride + p_row, b_end = b + (n - 1) * o_stride + o_row;
+    if (a_end <= b || b_end <= a) return false;
+    // Slices of one packed buffer: apart inside every row of it.
+    if (n > 1 && p_stride == o_stride) {
+        int64_t d = (b - a) % p_stride;
+        if (d < 0) d += p_stride;
+        return d < p_row || p_stride - d < o_row;
+    }
+    return true;
+}
+
+}  // namespace
+
 // ---------------------------------------------------------------- allocator
 struct kv_block_allocator {
     int num_blocks = 0, block_size = 0;
@@ -449,6 +493,132 @@ kv_status_t kv_append_fp8(kv_pool_t* p, int layer, const int32_t* seq_ids, int n
                  1, src_dtype, k_scale, v_scale};
     cudaError_t e = launch_append(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "append launch");
+    return KV_OK;
+}
+
+kv_status_t kv_rope_create(const kv_rope_config_t* c, kv_rope_t** out) {
+    if (!c || !out) return fail(KV_ERR_INVALID_ARG, "kv_rope_create: null argument");
+    *out = nullptr;
+    if (c->rot_dim < 2 || c->rot_dim % 2)
+        return fail(KV_ERR_INVALID_ARG, "kv_rope_create: rot_dim %d is not an even number from 2", c->rot_dim);
+    if (c->rot_dim > 2 * kMaxRopePairs)
+        return fail(KV_ERR_UNSUPPORTED, "kv_rope_create: rot_dim %d > %d", c->rot_dim, 2 * kMaxRopePairs);
+    if (c->num_axes < 1 || c->num_axes > 8)
+        return fail(KV_ERR_INVALID_ARG, "kv_rope_create: %d axes (1 .. 8)", c->num_axes);
+    if (!std::isfinite(c->amplitude)) return fail(KV_ERR_INVALID_ARG, "kv_rope_create: amplitude is not finite");
+    if (!c->inv_freq) return fail(KV_ERR_INVALID_ARG, "kv_rope_create: null inv_freq");
+    const int n = c->rot_dim / 2;
+    for (int i = 0; i < n; ++i) {
+        if (!std::isfinite(c->inv_freq[i])) return fail(KV_ERR_INVALID_ARG, "kv_rope_create: inv_freq[%d] is not finite", i);
+        if (c->axis && (c->axis[i] < 0 || c->axis[i] >= c->num_axes))
+            return fail(KV_ERR_INVALID_ARG, "kv_rope_create: axis[%d] = %d of %d axes", i, c->axis[i], c->num_axes);
+    }
+    kv_rope* r = new (std::nothrow) kv_rope;
+    if (!r) return fail(KV_ERR_OUT_OF_MEMORY, "host allocation failed");
+    memset(r, 0, sizeof *r);
+    r->rot_dim = c->rot_dim;
+    r->interleaved = c->interleaved != 0;
+    r->num_axes = c->num_axes;
+    r->amplitude = c->amplitude;
+    for (int i = 0; i < n; ++i) {
+        r->phase[i] = turns_fixed_point(c->inv_freq[i]);
+        r->axis[i] = static_cast<uint8_t>(c->axis ? c->axis[i] : 0);
+    }
+    *out = r;
+    return KV_OK;
+}
+
+void kv_rope_destroy(kv_rope_t* r) { delete r; }
+
+kv_status_t kv_append_rope(kv_pool_t* p, int layer, const kv_rope_t* rope, const int32_t* seq_ids, int n_tokens,
+                           const void* k, int64_t k_stride, const void* v, int64_t v_stride, kv_dtype_t src_dtype,
+                           const int32_t* slot_mapping, const int32_t* positions, int64_t positions_stride,
+                           const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int num_q_heads,
+                           float k_scale, float v_scale, void* stream) {
+    if (!p || !rope) return fail(KV_ERR_INVALID_ARG, "kv_append_rope: null pool or rope");
+    if (n_tokens < 0) return fail(KV_ERR_INVALID_ARG, "kv_append_rope: n_tokens %d", n_tokens);
+    const int D = p->cfg.head_dim, Hkv = p->cfg.num_kv_heads;
+    const bool quant = p->cfg.dtype == KV_FP8_E4M3;
+    if (!valid_dtype(src_dtype)) return fail(KV_ERR_INVALID_ARG, "kv_append_rope: source dtype %d", src_dtype);
+    if (!quant && src_dtype != p->cfg.dtype)
+        return fail(KV_ERR_INVALID_ARG, "kv_append_rope: rows must have the pool's dtype (or the pool be E4M3)");
+    if (quant && (!valid_scale(k_scale) || !valid_scale(v_scale)))
+        return fail(KV_ERR_INVALID_ARG, "kv_append_rope: scales must be finite and > 0");
+    if (rope->rot_dim > D)
+        return fail(KV_ERR_INVALID_ARG, "kv_append_rope: rot_dim %d > head_dim %d", rope->rot_dim, D);
+    void *kc = nullptr, *vc = nullptr;
+    if (kv_status_t st = kv_pool_layer(p, layer, &kc, &vc)) return st;
+    if (!q) num_q_heads = 0;
+    if (num_q_heads < 0 || (q && num_q_heads == 0))
+        return fail(KV_ERR_INVALID_ARG, "kv_append_rope: %d query heads", num_q_heads);
+    if (n_tokens == 0) return KV_OK;
+    if (!k || !v || !slot_mapping || !positions || (q && !q_out))
+        return fail(KV_ERR_INVALID_ARG, "kv_append_rope: null pointer");
+    const int eb = dtype_bytes(src_dtype);
+    const int64_t krow = static_cast<int64_t>(Hkv) * D, qrow = static_cast<int64_t>(num_q_heads) * D;
+    if (krow >= (int64_t{1} << 31) || qrow >= (int64_t{1} << 31))
+        return fail(KV_ERR_UNSUPPORTED, "kv_append_rope: more than 2^31 elements a token");
+    if (n_tokens > 1 && (k_stride < krow || v_stride < krow || (q && (q_stride < qrow || q_out_stride < qrow))))
+        return fail(KV_ERR_INVALID_ARG, "kv_append_rope: a stride is shorter than a token's rows");
+    if (rope->num_axes > 1 && positions_stride < n_tokens)
+        return fail(KV_ERR_INVALID_ARG, "kv_append_rope: positions_stride %lld < %d tokens",
+                    static_cast<long long>(positions_stride), n_tokens);
+    if (!aligned(k, eb) || !aligned(v, eb) || (q && (!aligned(q, eb) || !aligned(q_out, eb))) ||
+        !aligned(slot_mapping, 4) || !aligned(positions, 4) || !aligned(seq_ids, 4))
+        return fail(KV_ERR_INVALID_ARG, "kv_append_rope: a pointer is not aligned to its type");
+    if (q) {
+        const bool in_place = q == q_out && (n_tokens == 1 || q_stride == q_out_stride);
+        if ((!in_place && rows_overlap(q, q_stride * eb, qrow * eb, q_out, q_out_stride * eb, qrow * eb, n_tokens)) ||
+            rows_overlap(k, k_stride * eb, krow * eb, q_out, q_out_stride * eb, qrow * eb, n_tokens) ||
+            rows_overlap(v, v_stride * eb, krow * eb, q_out, q_out_stride * eb, qrow * eb, n_tokens))
+            return fail(KV_ERR_INVALID_ARG, "kv_append_rope: q_out overlaps q (other than in place), k or v");
+    }
+    DeviceGuard g(p->cfg.device);
+    if (!g.ok) return fail(KV_ERR_CUDA, "cannot select device %d", p->cfg.device);
+    uint32_t* status = nullptr;
+    int sms = 0;
+    if (kv_status_t st = device_info(nullptr, &status, &sms, nullptr, nullptr)) return st;
+    RopeArgs a{};
+    a.seq_ids = seq_ids;
+    a.slot_mapping = slot_mapping;
+    a.positions = positions;
+    a.q = q;
+    a.q_out = q_out;
+    a.k = k;
+    a.v = v;
+    a.k_cache = kc;
+    a.v_cache = vc;
+    a.status = status;
+    a.q_stride = q_stride;
+    a.q_out_stride = q_out_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.positions_stride = positions_stride;
+    a.n_tokens = n_tokens;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = Hkv;
+    a.head_dim = D;
+    a.rot_dim = rope->rot_dim;
+    a.block_size = p->cfg.block_size;
+    a.num_blocks = p->cfg.num_blocks;
+    a.src_dtype = src_dtype;
+    a.quant = quant ? 1 : 0;
+    a.interleaved = rope->interleaved;
+    a.pdl = 1;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.amplitude = rope->amplitude;
+    memcpy(a.phase, rope->phase, sizeof a.phase);
+    memcpy(a.axis, rope->axis, sizeof a.axis);
+    uintptr_t bits = 16 | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v);
+    if (n_tokens > 1) bits |= static_cast<uintptr_t>(k_stride * eb) | static_cast<uintptr_t>(v_stride * eb);
+    if (q) {
+        bits |= reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(q_out);
+        if (n_tokens > 1) bits |= static_cast<uintptr_t>(q_stride * eb) | static_cast<uintptr_t>(q_out_stride * eb);
+    }
+    const int align = static_cast<int>(bits & (~bits + 1));
+    cudaError_t e = launch_append_rope(a, align, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rope append launch");
     return KV_OK;
 }
 

@@ -33,6 +33,33 @@ struct AppendArgs {
     float k_scale, v_scale;
 };
 
+// Append with the position rotation on the way (rope.cu).  Strides in
+// elements from one token's rows to the next token's.
+constexpr int kMaxRopePairs = 128;
+
+struct RopeArgs {
+    const int32_t* seq_ids;       // [n_tokens] or nullptr
+    const int32_t* slot_mapping;  // [n_tokens]
+    const int32_t* positions;     // [axes][positions_stride]
+    const void* q;                // [n_tokens] x num_q_heads rows, or nullptr (num_q_heads is 0 then)
+    void* q_out;
+    const void* k;                // [n_tokens] x num_kv_heads rows
+    const void* v;
+    void* k_cache;                // [NB][Hkv][bs][D]
+    void* v_cache;
+    uint32_t* status;
+    int64_t q_stride, q_out_stride, k_stride, v_stride, positions_stride;
+    int n_tokens, num_q_heads, num_kv_heads, head_dim, rot_dim, block_size, num_blocks;
+    int src_dtype;                // q, q_out, k, v; the cache too unless quant
+    int quant;                    // E4M3 pool: codes of x / k_scale (x / v_scale)
+    int interleaved;              // pairs (2i, 2i + 1); else (i, i + rot_dim / 2)
+    int rows_per_cta;             // set by the launcher
+    int pdl;
+    float k_scale, v_scale, amplitude;
+    uint64_t phase[kMaxRopePairs];  // frequency of each pair, 2^-64 turns a position
+    uint8_t axis[kMaxRopePairs];    // axis whose position turns each pair
+};
+
 // Block swap between the pool and a device-addressable host buffer.
 struct SwapArgs {
     char* pool;               // pool base: layer l's K at 2l * layer_bytes, V at (2l + 1) * layer_bytes
@@ -138,6 +165,8 @@ bool decode_plan(int kernel, int dtype, int head_dim, int block_size, int group,
                  int heads_per_stage, int warps_per_head, int smem_budget, DecodePlan* plan);
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
+// align: largest power of two that divides the address of every token's rows.
+cudaError_t launch_append_rope(const RopeArgs& a, int align, int num_sms, cudaStream_t stream);
 cudaError_t launch_slot_mapping(const SlotArgs& a, cudaStream_t stream);
 cudaError_t launch_swap(const SwapArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
