@@ -88,6 +88,7 @@ typedef enum {
 #define KV_FLAG_BAD_SLOT       0x2u /* an append slot >= num_blocks*block_size */
 #define KV_FLAG_BAD_CONTEXT    0x4u /* context_lens[s] < 0 or > max_blocks_per_seq*block_size */
 #define KV_FLAG_TIMEOUT        0x8u /* a kernel gave up a bounded wait */
+#define KV_FLAG_BAD_GROUP      0x20u /* groups that do not cut the sequences into runs in order, or a prefix length < 0 */
 #define KV_FLAG_BAD_PLAN       0x10u /* a launch plan the kernel refuses (never set by this library's own planning) */
 
 /* Human-readable name of a status code (static string). */
@@ -415,6 +416,64 @@ kv_status_t paged_prefill_attention(const void* q, const void* k_cache, const vo
                                     int block_size, kv_dtype_t dtype, float scale, void* out,
                                     kv_dtype_t out_dtype, void* workspace, size_t workspace_bytes,
                                     void* stream);
+
+/* ------------------------------------------------------- shared prefixes */
+
+/* paged_decode_attention for a batch in which groups of sequences share the
+ * blocks of a prefix, each group's prefix read once for all its members
+ * ("Reading Inference Engine Codebases", Examples 12 and 13: requests with
+ * equal beginnings are given the same cached blocks).  The result is that of
+ * paged_decode_attention with the same tables and lengths; only how often the
+ * prefix is read differs.
+ *   group_start  device int32[num_groups + 1], non-decreasing, within
+ *                0 .. num_seqs: group g is the sequences group_start[g] ..
+ *                group_start[g+1] - 1.  Sequences before the first and behind
+ *                the last group belong to none.  A list that does not do this
+ *                sets KV_FLAG_BAD_GROUP, and nothing is shared.
+ *   prefix_lens  device int32[num_groups], >= 0: the first prefix_lens[g]
+ *                tokens are common to group g.  What is shared is whole blocks:
+ *                the table rows of all members hold the same block ids in
+ *                their first prefix_lens[g] / block_size entries (the library
+ *                reads them from one member's row).
+ * A sequence shorter than its group's shared blocks (a padding row of length
+ * 0, say) takes no part in the sharing and may hold other blocks: it is read
+ * through its own table.  A sequence with context 0 gets a zero row.
+ * q, out, dtype f16 or bf16 (KV_F32 is KV_ERR_UNSUPPORTED), head_dim 64 or
+ * 128, block_size a multiple of 16 up to 256 (two stages of a block's K and V
+ * must fit shared memory, as for paged_decode_attention: up to 208 with
+ * head_dim 128), num_q_heads / num_kv_heads in {1, 2, 4, 8}; out_dtype KV_F32
+ * or dtype.  Softmax statistics and sums are fp32.  workspace: device, 256-byte aligned, of at least
+ * paged_shared_prefix_workspace_bytes, needs no initialisation, not to be
+ * shared by two calls in flight at once (two captured graphs that may run at
+ * the same time included).  Worth it from a prefix of a few hundred tokens and
+ * two members on; without any sharing paged_decode_attention is the faster
+ * call. */
+kv_status_t paged_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int num_q_heads,
+                                                int num_kv_heads, int head_dim, int device,
+                                                size_t* bytes_out);
+kv_status_t paged_shared_prefix_attention(const void* q, const void* k_cache, const void* v_cache,
+                                          int num_blocks, const int32_t* block_tables,
+                                          int max_blocks_per_seq, const int32_t* context_lens,
+                                          int num_seqs, const int32_t* group_start,
+                                          const int32_t* prefix_lens, int num_groups,
+                                          int num_q_heads, int num_kv_heads, int head_dim,
+                                          int block_size, kv_dtype_t dtype, float scale, void* out,
+                                          kv_dtype_t out_dtype, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
+/* The same over an E4M3 cache (see paged_decode_attention_fp8): q_dtype KV_F16
+ * or KV_BF16, head_dim 128, out_dtype KV_F32 or q_dtype.  The prefix's codes
+ * are widened exactly to q's type in shared memory. */
+kv_status_t paged_shared_prefix_attention_fp8(const void* q, kv_dtype_t q_dtype, const void* k_cache,
+                                              const void* v_cache, float k_scale, float v_scale,
+                                              int num_blocks, const int32_t* block_tables,
+                                              int max_blocks_per_seq, const int32_t* context_lens,
+                                              int num_seqs, const int32_t* group_start,
+                                              const int32_t* prefix_lens, int num_groups,
+                                              int num_q_heads, int num_kv_heads, int head_dim,
+                                              int block_size, float scale, void* out,
+                                              kv_dtype_t out_dtype, void* workspace,
+                                              size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------- FP8 (E4M3) cache */
 

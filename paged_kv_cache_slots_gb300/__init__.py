@@ -20,6 +20,7 @@ __all__ = [
     "KVError", "KVPool", "Rope", "BlockAllocator", "PrefixCachePool", "kv_pool_bytes", "slot_mapping", "workspace_bytes",
     "paged_decode_attention", "device_status", "library_path", "load_library", "workspace_init",
     "make_workspace", "paged_decode_append_attention", "paged_prefill_attention", "slot_mapping_varlen",
+    "paged_shared_prefix_attention", "shared_prefix_workspace_bytes", "make_shared_prefix_workspace",
 ]
 
 KV_F32, KV_F16, KV_BF16, KV_FP8_E4M3 = 0, 1, 2, 3
@@ -31,6 +32,7 @@ DTYPE_NAMES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat1
 FP8 = torch.float8_e4m3fn
 KERNELS = {"auto": 0, "ffma": 1, "mma": 2}
 FLAG_BAD_BLOCK_ID, FLAG_BAD_SLOT, FLAG_BAD_CONTEXT, FLAG_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+FLAG_BAD_GROUP = 0x20
 
 _lock = threading.Lock()
 _lib = None
@@ -119,6 +121,11 @@ def _declare(lib):
                                         P, SZ, P]),
         "paged_prefill_attention_fp8": (I, [P, I, P, P, ctypes.c_float, ctypes.c_float, I, P, I, P, P, I, I, I,
                                             I, I, I, ctypes.c_float, P, I, P, SZ, P]),
+        "paged_shared_prefix_workspace_bytes": (I, [I, I, I, I, I, I, ctypes.POINTER(SZ)]),
+        "paged_shared_prefix_attention": (I, [P, P, P, I, P, I, P, I, P, P, I, I, I, I, I, I, ctypes.c_float, P, I, P,
+                                              SZ, P]),
+        "paged_shared_prefix_attention_fp8": (I, [P, I, P, P, ctypes.c_float, ctypes.c_float, I, P, I, P, I, P, P, I,
+                                                  I, I, I, I, ctypes.c_float, P, I, P, SZ, P]),
         "kv_swap_bytes": (SZ, [P, I]),
         "kv_swap_out": (I, [P, P, I, P, SZ, P]),
         "kv_swap_in": (I, [P, P, I, P, SZ, P]),
@@ -634,6 +641,72 @@ def paged_prefill_attention(q, k_cache, v_cache, block_tables, query_start, cont
         _ptr(q), _ptr(k_cache), _ptr(v_cache), NB, _ptr(block_tables), block_tables.shape[1],
         _ptr(query_start), _ptr(context_lens), B, T, Hq, Hkv, D, bs, DTYPE_CODE[q.dtype], float(scale),
         _ptr(out), DTYPE_CODE[out_dtype], _ptr(workspace), workspace.numel(), _stream(q, stream))
+    return out
+
+
+def shared_prefix_workspace_bytes(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, device=None) -> int:
+    lib = load_library()
+    dev = torch.device(device if device is not None else "cuda")
+    idx = dev.index if dev.index is not None else torch.cuda.current_device()
+    n = ctypes.c_size_t()
+    _check(lib.paged_shared_prefix_workspace_bytes(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, idx,
+                                                   ctypes.byref(n)), lib)
+    return int(n.value)
+
+
+def make_shared_prefix_workspace(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, device=None) -> torch.Tensor:
+    """A workspace for paged_shared_prefix_attention with these sizes (or smaller ones)."""
+    dev = torch.device(device if device is not None else "cuda")
+    n = shared_prefix_workspace_bytes(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, dev)
+    return torch.empty(n, dtype=torch.uint8, device=dev)
+
+
+def paged_shared_prefix_attention(q, k_cache, v_cache, block_tables, context_lens, group_start, prefix_lens,
+                                  scale: float, out=None, out_dtype=None, workspace=None, stream=None, k_scale=None,
+                                  v_scale=None):
+    """paged_decode_attention of a batch whose sequences share prefixes, each read once for its group.
+
+    Sequences group_start[g] .. group_start[g + 1] - 1 (int32 [groups + 1]) hold the same blocks in their
+    first prefix_lens[g] / block_size table entries (int32 [groups]); a sequence shorter than that, or in
+    no group, is read through its own table throughout.  The other arguments are those of
+    paged_decode_attention; q f16 or bf16, block_size a multiple of 16.
+    """
+    lib = load_library()
+    B, Hq, D = q.shape
+    NB, Hkv, bs, D2 = k_cache.shape
+    _need(D == D2 and v_cache.shape == k_cache.shape, "cache shapes")
+    fp8 = k_cache.dtype == FP8
+    if fp8:
+        _need(v_cache.dtype == FP8 and k_scale is not None and v_scale is not None,
+              "an E4M3 cache needs both caches E4M3 and k_scale, v_scale")
+    else:
+        _need(q.dtype == k_cache.dtype == v_cache.dtype, "q and the caches share a dtype")
+    tables = (block_tables, context_lens, group_start, prefix_lens)
+    _need(all(t.is_contiguous() for t in (q, k_cache, v_cache) + tables), "contiguous inputs")
+    _need(all(t.dtype == torch.int32 for t in tables), "int32 tables")
+    _need(block_tables.dim() == 2 and block_tables.shape[0] == B and context_lens.shape == (B,),
+          "one table row and length per sequence")
+    groups = prefix_lens.shape[0]
+    _need(prefix_lens.dim() == 1 and group_start.shape == (groups + 1,), "group_start [groups + 1], prefix_lens [groups]")
+    out_dtype = out_dtype or q.dtype
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
+    _need(out.dtype == out_dtype and out.shape == (B, Hq, D) and out.is_contiguous(), "out")
+    if workspace is None:
+        workspace = make_shared_prefix_workspace(B, groups, Hq, Hkv, D, q.device)
+    _need(all(t.device == q.device for t in (k_cache, v_cache, out, workspace) + tables),
+          "every tensor must be on q's device")
+    if fp8:
+        _call_on(q, lib, lib.paged_shared_prefix_attention_fp8,
+                 _ptr(q), DTYPE_CODE[q.dtype], _ptr(k_cache), _ptr(v_cache), float(k_scale), float(v_scale), NB,
+                 _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), B, _ptr(group_start), _ptr(prefix_lens),
+                 groups, Hq, Hkv, D, bs, float(scale), _ptr(out), DTYPE_CODE[out_dtype], _ptr(workspace),
+                 workspace.numel(), _stream(q, stream))
+        return out
+    _call_on(q, lib, lib.paged_shared_prefix_attention,
+             _ptr(q), _ptr(k_cache), _ptr(v_cache), NB, _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), B,
+             _ptr(group_start), _ptr(prefix_lens), groups, Hq, Hkv, D, bs, DTYPE_CODE[q.dtype], float(scale), _ptr(out),
+             DTYPE_CODE[out_dtype], _ptr(workspace), workspace.numel(), _stream(q, stream))
     return out
 
 

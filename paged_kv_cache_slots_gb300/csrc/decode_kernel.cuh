@@ -153,7 +153,9 @@ static __device__ void build_prefix(const DecodeArgs& a, int chunks, int32_t* cu
 // kTensor: stages arrive through 2-D tensor maps with a 128-byte swizzle (box
 // of 128 bytes x Hc*bs rows, one box per 128-byte slice of the row);
 // otherwise as two plain contiguous bulk copies.
-template <bool kTensor>
+// kTails: the first skip_blocks[s] entries of a sequence's table row are left
+// out (context_lens counts only what follows them).
+template <bool kTensor, bool kTails>
 static __device__ void produce(const DecodeArgs& a, uint8_t* ring, uint64_t* full, uint64_t* empty,
                         const int32_t* cum, int chunks, int start, int end, int half_bytes,
                         const CUtensorMap* tmk, const CUtensorMap* tmv, volatile int* abort) {
@@ -174,7 +176,8 @@ static __device__ void produce(const DecodeArgs& a, uint8_t* ring, uint64_t* ful
             const int hc = r / nbv;
             const int j = r - hc * nbv - a.phantom;
             if (j >= 0) {
-                int blk = __ldg(a.block_tables + static_cast<int64_t>(s) * a.max_blocks + j);
+                const int64_t entry = static_cast<int64_t>(s) * a.max_blocks + j + (kTails ? a.skip_blocks[s] : 0);
+                int blk = __ldg(a.block_tables + entry);
                 if (blk < 0 || blk >= a.num_blocks) {
                     raise_flag(a.status, kFlagBadBlock);
                     blk = 0;
@@ -637,7 +640,11 @@ __device__ __forceinline__ bool append_row(const DecodeArgs& a, const Policy& po
 // Policy provides: State, begin(), tile(), write_state(), write_partial(),
 // write_final(), kTensor, kScratch, kPairs (and tile2() when kPairs), and
 // kMaxThreads, the largest block it is launched with (its register budget).
-template <class Policy>
+// kTails: the variant that attends to what follows a shared prefix
+// (shared_prefix.cu): it skips the prefix's table entries and writes a partial
+// for every segment, whole pairs too, for the merge with the prefix's parts
+// (launched with fused_reduce 0 and without an append).
+template <class Policy, bool kTails>
 __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
     paged_decode_partial_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmk,
                                 const __grid_constant__ CUtensorMap tmv) {
@@ -691,7 +698,7 @@ __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
     const int end = static_cast<int>((static_cast<int64_t>(blockIdx.x) + 1) * W / P);
     const int warp = tid >> 5, lane = tid & 31;
     if (warp == 0 && start < end) {
-        produce<Policy::kTensor>(a, ring, full, empty, cum, chunks, start, end, half_bytes, &tmk,
+        produce<Policy::kTensor, kTails>(a, ring, full, empty, cum, chunks, start, end, half_bytes, &tmk,
                                  &tmv, abort);
         return;
     }
@@ -759,13 +766,13 @@ __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
             if (ok && j >= 0) {
                 const int n_valid = min(a.block_size, ctx - j * a.block_size);
                 uint8_t* kt = ring + stage * 2 * half_bytes;
-                bool patched = a.k_new && j == nb - 1 && append_row(a, pol, kt, kt + half_bytes, s, h, hw, j, n_valid - 1);
+                bool patched = !kTails && a.k_new && j == nb - 1 && append_row(a, pol, kt, kt + half_bytes, s, h, hw, j, n_valid - 1);
                 if constexpr (Policy::kPairs) {
                     if (two) {
                         const int j1 = j + R;
                         const int n1 = min(a.block_size, ctx - j1 * a.block_size);
                         uint8_t* kt1 = ring + stage2 * 2 * half_bytes;
-                        if (a.k_new && j1 == nb - 1)
+                        if (!kTails && a.k_new && j1 == nb - 1)
                             patched |= append_row(a, pol, kt1, kt1 + half_bytes, s, h, hw, j1, n1 - 1);
                         pol.tile2(st, a, kt, kt + half_bytes, n_valid, kt1, kt1 + half_bytes, n1, hw, G);
                     }
@@ -793,7 +800,7 @@ __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
         // A segment holding none of them is not a part of the pair: it
         // writes nothing and counts no arrival (the same on every warp).
         const int pair_r = pair_a + a.phantom;
-        const bool whole = (pair_r >= start) && (pair_b <= end);
+        const bool whole = !kTails && (pair_r >= start) && (pair_b <= end);
         const bool blocks = max(seg, pair_r) < seg_end;
         const int pair = s * chunks + hc;
         const int64_t sl = (static_cast<int64_t>(blockIdx.x + pair) * Hc + hw) * G;
@@ -819,41 +826,43 @@ __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
             }
             named_barrier_sync(1, NC * 32);
         }
-        // A split pair at the end of the range: once every consumer warp is
-        // past its last stage, the ring's shared memory is free (the producer
-        // issued nothing after the range's last item) and the merge may stage
-        // the parts there, one slice a warp.
-        float* staging = nullptr;
-        int staging_floats = 0;
-        if (R == 1 && a.fused_reduce && seg_end == end && !whole && blocks) {
-            named_barrier_sync(1, NC * 32);
-            staging_floats = (a.stages * 2 * half_bytes / NC / 4) & ~3;
-            staging = reinterpret_cast<float*>(ring) + w * staging_floats;
-        }
-        if (partial && a.fused_reduce) {
-            // The parts: the CTAs holding the pair's blocks.  With fewer
-            // items than CTAs each block has its own CTA.
-            const int ca = cta_of_item(pair_r, W, P);
-            const int cb = cta_of_item(pair_b - 1, W, P);
-            const int nparts = W >= P ? cb - ca + 1 : pair_b - pair_r;
-            constexpr int T = Policy::kMaxThreads, DD = Policy::kD;
-            switch (G) {
-                case 1:
-                    merge_if_last<1, DD, merge_prefetch(1, DD, T)>(a, s, h, hw, pair, nparts, ca, cb, W,
-                                                                  staging, staging_floats);
-                    break;
-                case 2:
-                    merge_if_last<2, DD, merge_prefetch(2, DD, T)>(a, s, h, hw, pair, nparts, ca, cb, W,
-                                                                  staging, staging_floats);
-                    break;
-                case 4:
-                    merge_if_last<4, DD, merge_prefetch(4, DD, T)>(a, s, h, hw, pair, nparts, ca, cb, W,
-                                                                  staging, staging_floats);
-                    break;
-                default:
-                    merge_if_last<8, DD, merge_prefetch(8, DD, T)>(a, s, h, hw, pair, nparts, ca, cb, W,
-                                                                  staging, staging_floats);
-                    break;
+        if constexpr (!kTails) {
+            // A split pair at the end of the range: once every consumer warp is
+            // past its last stage, the ring's shared memory is free (the producer
+            // issued nothing after the range's last item) and the merge may stage
+            // the parts there, one slice a warp.
+            float* staging = nullptr;
+            int staging_floats = 0;
+            if (R == 1 && a.fused_reduce && seg_end == end && !whole && blocks) {
+                named_barrier_sync(1, NC * 32);
+                staging_floats = (a.stages * 2 * half_bytes / NC / 4) & ~3;
+                staging = reinterpret_cast<float*>(ring) + w * staging_floats;
+            }
+            if (partial && a.fused_reduce) {
+                // The parts: the CTAs holding the pair's blocks.  With fewer
+                // items than CTAs each block has its own CTA.
+                const int ca = cta_of_item(pair_r, W, P);
+                const int cb = cta_of_item(pair_b - 1, W, P);
+                const int nparts = W >= P ? cb - ca + 1 : pair_b - pair_r;
+                constexpr int T = Policy::kMaxThreads, DD = Policy::kD;
+                switch (G) {
+                    case 1:
+                        merge_if_last<1, DD, merge_prefetch(1, DD, T)>(a, s, h, hw, pair, nparts, ca, cb, W,
+                                                                      staging, staging_floats);
+                        break;
+                    case 2:
+                        merge_if_last<2, DD, merge_prefetch(2, DD, T)>(a, s, h, hw, pair, nparts, ca, cb, W,
+                                                                      staging, staging_floats);
+                        break;
+                    case 4:
+                        merge_if_last<4, DD, merge_prefetch(4, DD, T)>(a, s, h, hw, pair, nparts, ca, cb, W,
+                                                                      staging, staging_floats);
+                        break;
+                    default:
+                        merge_if_last<8, DD, merge_prefetch(8, DD, T)>(a, s, h, hw, pair, nparts, ca, cb, W,
+                                                                      staging, staging_floats);
+                        break;
+                }
             }
         }
         seg = seg_end;
@@ -863,11 +872,11 @@ __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
 // Launch the partial kernel of `Policy`.  The dynamic shared-memory limit is
 // raised once per device (not on every launch, so that launches captured in
 // a CUDA graph make no attribute calls).
-template <class Policy>
+template <class Policy, bool kTails = false>
 cudaError_t launch_partial(const DecodeArgs& a, const CUtensorMap& tmk, const CUtensorMap& tmv,
                            cudaStream_t stream) {
     static std::atomic<int> configured[64];
-    auto kern = paged_decode_partial_kernel<Policy>;
+    auto kern = paged_decode_partial_kernel<Policy, kTails>;
     const bool cacheable = a.device >= 0 && a.device < 64;
     if (!cacheable || configured[a.device].load() < a.smem_bytes) {
         cudaError_t e =

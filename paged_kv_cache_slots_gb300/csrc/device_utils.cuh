@@ -21,6 +21,7 @@ constexpr uint32_t kFlagBadSlot = 0x2u;
 constexpr uint32_t kFlagBadContext = 0x4u;
 constexpr uint32_t kFlagTimeout = 0x8u;
 constexpr uint32_t kFlagBadPlan = 0x10u;
+constexpr uint32_t kFlagBadGroup = 0x20u;
 
 // A bounded wait gives up after this many nanoseconds of the global timer.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;

@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "pkv_internal.h"
+#include "shared_prefix.cuh"
 
 using namespace pkv;
 
@@ -154,6 +155,34 @@ int auto_heads_per_stage(int num_kv_heads, int block_size, int head_dim, int dty
         return hc;
     }
     return 1;
+}
+
+// Stages for *R warps per head, or for fewer where the ring would hold less
+// than two stages per replica (each replica owns every R-th stage).  keep_warps:
+// an explicit warp count is kept if it fits at all.
+bool plan_warps(int kernel, int kv_dtype, int head_dim, int block_size, int G, int num_seqs, int hc, int budget,
+                bool keep_warps, int* R, DecodePlan* plan) {
+    bool planned = false;
+    for (; *R >= 1; --*R) {
+        planned = decode_plan(kernel, kv_dtype, head_dim, block_size, G, num_seqs, hc, *R, budget, plan);
+        if (planned && (plan->stages >= 2 * *R || *R == 1)) break;
+        if (planned && keep_warps) break;
+    }
+    return planned;
+}
+
+// Phantom items per pair: about the time a CTA loses switching to the
+// next pair (the partial's stores, the merge arrival's release fence,
+// the next q: 3-5 us measured) in stages' worth of streaming, i.e.
+// 300 KiB of stage data: 5 items for 64 KiB stages, 8 (the cap) for the
+// E4M3 stages of 32 KiB (the best of 0, 100, 200, 300 and 400 KiB in an
+// A/B on one box).  Not with too few items to split (fewer than two a
+// CTA even with every table entry used).
+int phantom_items(int num_seqs, int chunks, int max_blocks, int ctas, int stage_half_bytes) {
+    const int64_t stage_bytes = 2 * static_cast<int64_t>(stage_half_bytes);
+    const int64_t max_items = static_cast<int64_t>(num_seqs) * chunks * max_blocks;
+    const int ph = static_cast<int>((int64_t{300} * 1024 + stage_bytes / 2) / stage_bytes);
+    return max_items >= 2 * static_cast<int64_t>(ctas) ? (ph > 8 ? 8 : ph) : 0;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -743,8 +772,7 @@ static kv_status_t decode_impl(const void* q, const void* k_cache, const void* v
     }
     if (kernel == KV_KERNEL_MMA && hc * block_size > 256)
         return fail(KV_ERR_UNSUPPORTED, "heads_per_stage * block_size must be <= 256 for the tensor copies");
-    const int target = o.consumer_warps ? o.consumer_warps : 8;
-    int R = target / hc;
+    int R = (o.consumer_warps ? o.consumer_warps : 8) / hc;
     if (R < 1) R = 1;
     while (hc * R > 15 && R > 1) --R;
     if (hc * R > 15) return fail(KV_ERR_UNSUPPORTED, "more than 15 consumer warps");
@@ -753,15 +781,9 @@ static kv_status_t decode_impl(const void* q, const void* k_cache, const void* v
         const int share = smem_sm / o.ctas_per_sm - 1024;
         if (share < budget) budget = share;
     }
-    // Fewer warps per head when the ring would hold less than two stages per
-    // replica (each replica owns every R-th stage).
     DecodePlan plan{};
-    bool planned = false;
-    for (; R >= 1; --R) {
-        planned = decode_plan(kernel, kv_dtype, head_dim, block_size, G, num_seqs, hc, R, budget, &plan);
-        if (planned && (plan.stages >= 2 * R || R == 1)) break;
-        if (planned && o.consumer_warps) break;  // an explicit warp count is kept if it fits at all
-    }
+    const bool planned = plan_warps(kernel, kv_dtype, head_dim, block_size, G, num_seqs, hc, budget,
+                                    o.consumer_warps != 0, &R, &plan);
     if (!planned) return fail(KV_ERR_UNSUPPORTED, "shared memory cannot hold two stages for these sizes");
 
     char* ws = static_cast<char*>(workspace);
@@ -801,19 +823,7 @@ static kv_status_t decode_impl(const void* q, const void* k_cache, const void* v
     a.pdl = o.no_pdl ? 0 : 1;
     a.early_reads = (o.early_reads && !o.no_pdl) ? 1 : 0;
     a.test_stall = o.test_stall;
-    // Phantom items per pair: about the time a CTA loses switching to the
-    // next pair (the partial's stores, the merge arrival's release fence,
-    // the next q: 3-5 us measured) in stages' worth of streaming, i.e.
-    // 300 KiB of stage data: 5 items for 64 KiB stages, 8 (the cap) for the
-    // E4M3 stages of 32 KiB (the best of 0, 100, 200, 300 and 400 KiB in an
-    // A/B on one box).  Not with too few items to split (fewer than two a
-    // CTA even with every table entry used).
-    {
-        const int64_t stage_bytes = 2 * static_cast<int64_t>(plan.stage_half_bytes);
-        const int64_t max_items = static_cast<int64_t>(num_seqs) * (num_kv_heads / hc) * max_blocks;
-        int ph = static_cast<int>((int64_t{300} * 1024 + stage_bytes / 2) / stage_bytes);
-        a.phantom = max_items >= 2 * static_cast<int64_t>(P) ? (ph > 8 ? 8 : ph) : 0;
-    }
+    a.phantom = phantom_items(num_seqs, num_kv_heads / hc, max_blocks, P, plan.stage_half_bytes);
     a.device = dev;
     a.k_new = k_new;
     a.v_new = v_new;
@@ -1066,6 +1076,233 @@ kv_status_t paged_prefill_attention_fp8(const void* q, kv_dtype_t q_dtype, const
     return prefill_impl(q, k_cache, v_cache, num_blocks, block_tables, max_blocks, query_start, context_lens,
                         num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, q_dtype,
                         KV_FP8_E4M3, k_scale, v_scale, scale, out, out_dtype, workspace, workspace_bytes, stream);
+}
+
+// ------------------------------------------------------- shared prefixes
+namespace {
+
+struct SharedWs {
+    size_t plan, skip, tails, parts, groups, part_o, part_ml, decode, total;
+    int max_units, max_rows;
+    WsLayout d;
+};
+
+// target: parts CTAs that run at once; ctas: the tails kernel's grid.
+SharedWs shared_workspace(int B, int ng, int Hq, int Hkv, int D, int target, int ctas) {
+    SharedWs w;
+    const int64_t G = Hq / Hkv;
+    // Chunks of at least 1 / target of the work, and one more of every (group,
+    // KV head, row tile); their rows likewise (see the plan kernel).
+    w.max_units = static_cast<int>(target + Hkv * (ng + B * G / 128 + 1));
+    w.max_rows = static_cast<int>(int64_t{128} * target + static_cast<int64_t>(B) * Hq);
+    w.plan = 0;
+    w.skip = 256;
+    w.tails = w.skip + align256(static_cast<size_t>(B) * 4);
+    w.parts = w.tails + align256(static_cast<size_t>(B) * 4);
+    w.groups = w.parts + align256(static_cast<size_t>(B) * sizeof(PrefixParts));
+    w.part_o = w.groups + align256(static_cast<size_t>(ng) * sizeof(PrefixGroup));
+    w.part_ml = w.part_o + align256(static_cast<size_t>(w.max_rows) * D * 4);
+    w.decode = w.part_ml + align256(static_cast<size_t>(w.max_rows) * 8);
+    w.d = workspace_layout(B, Hq, Hkv, D, ctas);
+    w.total = w.decode + w.d.total;
+    return w;
+}
+
+kv_status_t shared_sizes(const char* what, int B, int ng, int Hq, int Hkv, int D) {
+    if (B < 0 || ng < 0 || Hq <= 0 || Hkv <= 0 || D <= 0) return fail(KV_ERR_INVALID_ARG, "%s: sizes out of range", what);
+    if (Hq % Hkv) return fail(KV_ERR_INVALID_ARG, "num_q_heads %d is not a multiple of num_kv_heads %d", Hq, Hkv);
+    if (static_cast<int64_t>(B) * Hq >= (int64_t{1} << 30) || static_cast<int64_t>(ng) * Hkv >= (int64_t{1} << 24))
+        return fail(KV_ERR_UNSUPPORTED, "%s: too many sequences or groups", what);
+    return KV_OK;
+}
+
+kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_cache, const void* v_cache,
+                               kv_dtype_t kv_dtype, float k_scale, float v_scale, int num_blocks,
+                               const int32_t* block_tables, int max_blocks, const int32_t* context_lens, int num_seqs,
+                               const int32_t* group_start, const int32_t* prefix_lens, int num_groups,
+                               int num_q_heads, int num_kv_heads, int head_dim, int block_size, float scale, void* out,
+                               kv_dtype_t out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    const char* what = "paged_shared_prefix_attention";
+    const bool fp8 = kv_dtype == KV_FP8_E4M3;
+    if (kv_status_t st = shared_sizes(what, num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim)) return st;
+    if (num_blocks <= 0 || max_blocks <= 0) return fail(KV_ERR_INVALID_ARG, "%s: sizes out of range", what);
+    const int G = num_q_heads / num_kv_heads;
+    if (G != 1 && G != 2 && G != 4 && G != 8)
+        return fail(KV_ERR_UNSUPPORTED, "query heads per KV head must be 1, 2, 4 or 8 (got %d)", G);
+    if (head_dim != 64 && head_dim != 128) return fail(KV_ERR_UNSUPPORTED, "head_dim %d", head_dim);
+    if (block_size < 16 || block_size > 256 || block_size % 16)
+        return fail(KV_ERR_UNSUPPORTED, "%s needs block_size a multiple of 16 up to 256 (got %d)", what, block_size);
+    if (!valid_dtype(dtype) || !valid_dtype(out_dtype)) return fail(KV_ERR_INVALID_ARG, "unknown dtype");
+    if (dtype == KV_F32) return fail(KV_ERR_UNSUPPORTED, "%s takes f16 or bf16", what);
+    if (fp8) {
+        if (head_dim != 128) return fail(KV_ERR_UNSUPPORTED, "an E4M3 cache needs head_dim 128");
+        if (!valid_scale(k_scale) || !valid_scale(v_scale))
+            return fail(KV_ERR_INVALID_ARG, "k_scale and v_scale must be finite and > 0");
+    }
+    if (out_dtype != KV_F32 && out_dtype != dtype)
+        return fail(KV_ERR_UNSUPPORTED, "out_dtype must be KV_F32 or the input dtype");
+    if (!std::isfinite(scale)) return fail(KV_ERR_INVALID_ARG, "scale is not finite");
+    if (static_cast<int64_t>(num_seqs) * num_kv_heads * max_blocks >= (int64_t{1} << 31) ||
+        static_cast<int64_t>(max_blocks) * block_size >= (int64_t{1} << 31) ||
+        static_cast<int64_t>(num_blocks) * num_kv_heads * block_size >= (int64_t{1} << 31))
+        return fail(KV_ERR_UNSUPPORTED, "sizes exceed 32-bit tile / row indices");
+    if (num_seqs == 0) return KV_OK;
+    if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out || !workspace ||
+        (num_groups > 0 && (!group_start || !prefix_lens)))
+        return fail(KV_ERR_INVALID_ARG, "%s: null pointer", what);
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(q, 16) || !aligned(out, 16) ||
+        !aligned(workspace, 256))
+        return fail(KV_ERR_INVALID_ARG,
+                    "alignment: caches, q and out need 16 bytes, the workspace 256 bytes");
+    if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(group_start, 4) || !aligned(prefix_lens, 4))
+        return fail(KV_ERR_INVALID_ARG, "%s: an int32 array is not 4-byte aligned", what);
+    int dev = 0, sms = 0, max_smem = 0;
+    uint32_t* status = nullptr;
+    if (kv_status_t st = device_info(&dev, &status, &sms, &max_smem, nullptr)) return st;
+    const int target = sms * prefix_ctas_per_sm(fp8), ctas = sms;
+    const SharedWs w = shared_workspace(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, target, ctas);
+    if (workspace_bytes < w.total)
+        return fail(KV_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, w.total);
+    // The tails: heads a stage as the decode kernel's default, up to 11 (its
+    // variant for partials is built for 12 warps).
+    int hc = auto_heads_per_stage(num_kv_heads, block_size, head_dim, kv_dtype, true);
+    while (hc > 11 || num_kv_heads % hc) --hc;
+    int R = 8 / hc > 1 ? 8 / hc : 1;
+    DecodePlan plan{};
+    if (!plan_warps(KV_KERNEL_MMA, kv_dtype, head_dim, block_size, G, num_seqs, hc, max_smem, false, &R, &plan))
+        return fail(KV_ERR_UNSUPPORTED, "shared memory cannot hold two stages for these sizes");
+
+    char* ws = static_cast<char*>(workspace);
+    SharedPrefixArgs a{};
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.group_start = group_start;
+    a.prefix_lens = prefix_lens;
+    a.out = out;
+    a.status = status;
+    a.plan = reinterpret_cast<int32_t*>(ws + w.plan);
+    a.skip_blocks = reinterpret_cast<int32_t*>(ws + w.skip);
+    a.tail_lens = reinterpret_cast<int32_t*>(ws + w.tails);
+    a.parts = reinterpret_cast<PrefixParts*>(ws + w.parts);
+    a.groups = reinterpret_cast<PrefixGroup*>(ws + w.groups);
+    a.part_o = reinterpret_cast<float*>(ws + w.part_o);
+    a.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
+    a.num_seqs = num_seqs;
+    a.num_groups = num_groups;
+    a.num_blocks = num_blocks;
+    a.max_blocks = max_blocks;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.block_size = block_size;
+    a.dtype = dtype;
+    a.out_dtype = out_dtype;
+    a.kv_dtype = kv_dtype;
+    a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 *
+                                      static_cast<double>(fp8 ? k_scale : 1.f));
+    a.v_scale = fp8 ? v_scale : 1.f;
+    a.target_units = target;
+    a.max_units = w.max_units;
+    a.max_rows = w.max_rows;
+    a.device = dev;
+    a.smem_bytes = prefix_smem_bytes(head_dim, fp8);
+    if (a.smem_bytes > max_smem) return fail(KV_ERR_UNSUPPORTED, "%s: not enough shared memory on this device", what);
+
+    DecodeArgs d{};
+    d.q = q;
+    d.k_cache = k_cache;
+    d.v_cache = v_cache;
+    d.block_tables = block_tables;
+    d.context_lens = a.tail_lens;
+    d.skip_blocks = a.skip_blocks;
+    d.out = out;
+    d.counters = reinterpret_cast<int32_t*>(ws + w.decode + w.d.counters);
+    d.part_o = reinterpret_cast<float*>(ws + w.decode + w.d.part_o);
+    d.part_ml = reinterpret_cast<float*>(ws + w.decode + w.d.part_ml);
+    d.cum = reinterpret_cast<int32_t*>(ws + w.decode + w.d.cum);
+    d.status = status;
+    d.num_blocks = num_blocks;
+    d.max_blocks = max_blocks;
+    d.num_seqs = num_seqs;
+    d.num_q_heads = num_q_heads;
+    d.num_kv_heads = num_kv_heads;
+    d.head_dim = head_dim;
+    d.block_size = block_size;
+    d.dtype = dtype;
+    d.out_dtype = out_dtype;
+    d.kv_dtype = kv_dtype;
+    d.k_scale = fp8 ? k_scale : 1.f;
+    d.v_scale = a.v_scale;
+    d.scale_log2 = a.scale_log2;
+    d.num_ctas = ctas;
+    d.heads_per_stage = hc;
+    d.warps_per_head = R;
+    d.consumer_warps = hc * R;
+    d.stages = plan.stages;
+    d.smem_bytes = plan.smem_bytes;
+    d.fused_reduce = 0;
+    d.pdl = 1;
+    d.early_reads = 1;  // the launch before it is the parts kernel, which writes partials only
+    d.phantom = phantom_items(num_seqs, num_kv_heads / hc, max_blocks, ctas, plan.stage_half_bytes);
+    d.device = dev;
+    CUtensorMap tk, tv;
+    const int rows = num_blocks * num_kv_heads * block_size;
+    if (kv_status_t st = encode_cache_map(&tk, k_cache, kv_dtype, rows, head_dim, hc * block_size)) return st;
+    if (kv_status_t st = encode_cache_map(&tv, v_cache, kv_dtype, rows, head_dim, hc * block_size)) return st;
+
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_prefix_plan(a, s);
+    if (e != cudaSuccess) return cuda_fail(e, "prefix plan launch");
+    if ((e = launch_prefix_parts(a, s)) != cudaSuccess) return cuda_fail(e, "prefix parts launch");
+    if ((e = launch_decode_tails(d, tk, tv, s)) != cudaSuccess) return cuda_fail(e, "tails launch");
+    if ((e = launch_prefix_merge(a, d, s)) != cudaSuccess) return cuda_fail(e, "prefix merge launch");
+    return KV_OK;
+}
+
+}  // namespace
+
+kv_status_t paged_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads,
+                                                int head_dim, int device, size_t* bytes) {
+    if (!bytes) return fail(KV_ERR_INVALID_ARG, "null bytes_out");
+    if (kv_status_t st = shared_sizes("shared-prefix workspace", num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim))
+        return st;
+    DeviceGuard g(device);
+    if (!g.ok) return fail(KV_ERR_CUDA, "cannot select device %d", device);
+    int sms = 0;
+    if (kv_status_t st = device_info(nullptr, nullptr, &sms, nullptr, nullptr)) return st;
+    // The larger of the two cache kinds' needs.
+    *bytes = shared_workspace(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim,
+                              sms * prefix_ctas_per_sm(false), sms).total;
+    return KV_OK;
+}
+
+kv_status_t paged_shared_prefix_attention(const void* q, const void* k_cache, const void* v_cache, int num_blocks,
+                                          const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
+                                          int num_seqs, const int32_t* group_start, const int32_t* prefix_lens,
+                                          int num_groups, int num_q_heads, int num_kv_heads, int head_dim,
+                                          int block_size, kv_dtype_t dtype, float scale, void* out,
+                                          kv_dtype_t out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    if (dtype == KV_FP8_E4M3)
+        return fail(KV_ERR_INVALID_ARG, "paged_shared_prefix_attention: an E4M3 cache goes to paged_shared_prefix_attention_fp8");
+    return shared_prefix_impl(q, dtype, k_cache, v_cache, dtype, 1.f, 1.f, num_blocks, block_tables, max_blocks,
+                              context_lens, num_seqs, group_start, prefix_lens, num_groups, num_q_heads, num_kv_heads,
+                              head_dim, block_size, scale, out, out_dtype, workspace, workspace_bytes, stream);
+}
+
+kv_status_t paged_shared_prefix_attention_fp8(const void* q, kv_dtype_t q_dtype, const void* k_cache,
+                                              const void* v_cache, float k_scale, float v_scale, int num_blocks,
+                                              const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
+                                              int num_seqs, const int32_t* group_start, const int32_t* prefix_lens,
+                                              int num_groups, int num_q_heads, int num_kv_heads, int head_dim,
+                                              int block_size, float scale, void* out, kv_dtype_t out_dtype,
+                                              void* workspace, size_t workspace_bytes, void* stream) {
+    return shared_prefix_impl(q, q_dtype, k_cache, v_cache, KV_FP8_E4M3, k_scale, v_scale, num_blocks, block_tables,
+                              max_blocks, context_lens, num_seqs, group_start, prefix_lens, num_groups, num_q_heads,
+                              num_kv_heads, head_dim, block_size, scale, out, out_dtype, workspace, workspace_bytes,
+                              stream);
 }
 
 kv_status_t kv_device_status(int device, void* stream, uint32_t* flags_out) {

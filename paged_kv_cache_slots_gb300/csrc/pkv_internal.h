@@ -129,6 +129,7 @@ struct DecodeArgs {
     int test_stall;       // testing only: see kv_decode_options_t
     int device;           // CUDA ordinal the launch targets
     int phantom;          // items without data at the start of every (sequence, head chunk) pair
+    const int32_t* skip_blocks;  // [num_seqs] leading table entries left out (tails of a shared prefix only)
 };
 
 // Multi-token (chunked-prefill) attention and its plan.

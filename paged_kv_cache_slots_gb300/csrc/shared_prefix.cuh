@@ -1,0 +1,64 @@
+// Shared between the kernels of the shared-prefix attention and its host side.
+#pragma once
+
+#include "pkv_internal.h"
+
+namespace pkv {
+
+// One group of sequences, as planned on the device.
+struct PrefixGroup {
+    int unit0;   // first work unit
+    int row0;    // first partial row
+    int seq0;    // first sequence
+    int rows;    // (sequences of the group) x (query heads per KV head)
+    int tiles;   // row tiles of 128
+    int chunks;  // pieces its keys are split into (0: nothing is shared)
+    int blocks;  // shared blocks
+    int lead;    // the member whose table row names them
+};
+
+// Where the prefix parts of a sequence are: part c of KV head h, query head g
+// of it sits in partial row row0 + h * head_stride + c * part_stride + g.
+struct PrefixParts {
+    int row0, part_stride, head_stride, parts;
+};
+
+struct SharedPrefixArgs {
+    const void* q;               // [B][Hq][D]
+    const void* k_cache;
+    const void* v_cache;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* group_start;  // [num_groups + 1]
+    const int32_t* prefix_lens;  // [num_groups]
+    void* out;
+    uint32_t* status;
+    // Workspace.
+    int32_t* plan;               // [0] units, [1] key tiles a chunk
+    int32_t* skip_blocks;        // [B] shared blocks of each sequence's table row
+    int32_t* tail_lens;          // [B] tokens after them
+    PrefixParts* parts;          // [B]
+    PrefixGroup* groups;         // [num_groups]
+    float* part_o;               // [part_rows][D]
+    float* part_ml;              // [part_rows][2]
+    int num_seqs, num_groups, num_blocks, max_blocks, num_q_heads, num_kv_heads, head_dim, block_size;
+    int dtype, out_dtype, kv_dtype;
+    float scale_log2, v_scale;
+    int target_units;            // CTAs that run at once
+    int max_units, max_rows;     // capacity of the grid and of the partial rows
+    int device, smem_bytes;
+};
+
+// Keys of one tile of the prefix kernel.
+constexpr int kPrefixTile = 64;
+
+int prefix_smem_bytes(int head_dim, bool fp8);
+int prefix_ctas_per_sm(bool fp8);
+cudaError_t launch_prefix_plan(const SharedPrefixArgs& a, cudaStream_t stream);
+cudaError_t launch_prefix_parts(const SharedPrefixArgs& a, cudaStream_t stream);
+cudaError_t launch_prefix_merge(const SharedPrefixArgs& a, const DecodeArgs& tails, cudaStream_t stream);
+// The decode kernel over what follows the prefix (decode_tails.cu).
+cudaError_t launch_decode_tails(const DecodeArgs& a, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
+                                cudaStream_t stream);
+
+}  // namespace pkv
