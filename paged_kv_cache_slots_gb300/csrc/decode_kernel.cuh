@@ -108,9 +108,46 @@ __device__ __forceinline__ int clamp_context(const DecodeArgs& a, int s, bool fl
     return c;
 }
 
+// Whether the groups cut the sequences into runs in order (asked by the whole
+// CTA; flagged by the first).
+static __device__ bool groups_in_order(const int32_t* group_start, const int32_t* prefix_lens, int num_groups,
+                                       int num_seqs, uint32_t* status) {
+    int bad = 0;
+    for (int g = threadIdx.x; g < num_groups; g += blockDim.x) {
+        const int s0 = group_start[g], s1 = group_start[g + 1];
+        if (s0 < 0 || s1 > num_seqs || s0 > s1 || prefix_lens[g] < 0) bad = 1;
+    }
+    bad = __syncthreads_or(bad);
+    if (bad && threadIdx.x == 0 && blockIdx.x == 0) raise_flag(status, kFlagBadGroup);
+    return bad == 0;
+}
+
+// Blocks that sequence s, of ctx tokens, shares with its group: 0 if it is in
+// none, or ends inside them.  The groups are in order; *group receives its own.
+__device__ __forceinline__ int shared_blocks(const int32_t* group_start, const int32_t* prefix_lens, int num_groups,
+                                             int block_size, int s, int ctx, int* group) {
+    if (num_groups == 0) return 0;
+    int lo = 0, hi = num_groups;  // the last group that starts at or before s
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (group_start[mid] <= s)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    *group = lo;
+    const int n = prefix_lens[lo] / block_size;
+    return group_start[lo] <= s && s < group_start[lo + 1] && n <= ctx / block_size ? n : 0;
+}
+
 // cum[s] = chunks * sum_{s' < s, ctx_s' > 0} (ceil(ctx_s' / bs) + phantom);
-// cum[num_seqs] = W.
-static __device__ void build_prefix(const DecodeArgs& a, int chunks, int32_t* cum, int32_t* scan) {
+// cum[num_seqs] = W.  kTails: ctx is what follows skip[s] shared blocks.
+template <bool kTails>
+static __device__ void build_prefix(const DecodeArgs& a, int chunks, int32_t* cum, int32_t* scan, int32_t* skip) {
+    int groups = 0;
+    if constexpr (kTails) {
+        if (groups_in_order(a.group_start, a.prefix_lens, a.num_groups, a.num_seqs, a.status)) groups = a.num_groups;
+    }
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int nwarps = blockDim.x >> 5;
     int carry = 0;
@@ -119,7 +156,13 @@ static __device__ void build_prefix(const DecodeArgs& a, int chunks, int32_t* cu
         int v = 0;
         if (s < a.num_seqs) {
             const int c = clamp_context(a, s, blockIdx.x == 0);
-            const int nb = (c + a.block_size - 1) / a.block_size;
+            int nb = (c + a.block_size - 1) / a.block_size;
+            if constexpr (kTails) {
+                int g;
+                const int sb = shared_blocks(a.group_start, a.prefix_lens, groups, a.block_size, s, c, &g);
+                skip[s] = sb;
+                nb -= sb;
+            }
             v = nb > 0 ? (nb + a.phantom) * chunks : 0;
         }
         int x = v;
@@ -153,11 +196,10 @@ static __device__ void build_prefix(const DecodeArgs& a, int chunks, int32_t* cu
 // kTensor: stages arrive through 2-D tensor maps with a 128-byte swizzle (box
 // of 128 bytes x Hc*bs rows, one box per 128-byte slice of the row);
 // otherwise as two plain contiguous bulk copies.
-// kTails: the first skip_blocks[s] entries of a sequence's table row are left
-// out (context_lens counts only what follows them).
+// kTails: the first skip[s] entries of a sequence's table row are left out.
 template <bool kTensor, bool kTails>
 static __device__ void produce(const DecodeArgs& a, uint8_t* ring, uint64_t* full, uint64_t* empty,
-                        const int32_t* cum, int chunks, int start, int end, int half_bytes,
+                        const int32_t* cum, const int32_t* skip, int chunks, int start, int end, int half_bytes,
                         const CUtensorMap* tmk, const CUtensorMap* tmv, volatile int* abort) {
     const int lane = threadIdx.x & 31;
     const uint64_t policy = policy_evict_first();
@@ -176,7 +218,7 @@ static __device__ void produce(const DecodeArgs& a, uint8_t* ring, uint64_t* ful
             const int hc = r / nbv;
             const int j = r - hc * nbv - a.phantom;
             if (j >= 0) {
-                const int64_t entry = static_cast<int64_t>(s) * a.max_blocks + j + (kTails ? a.skip_blocks[s] : 0);
+                const int64_t entry = static_cast<int64_t>(s) * a.max_blocks + j + (kTails ? skip[s] : 0);
                 int blk = __ldg(a.block_tables + entry);
                 if (blk < 0 || blk >= a.num_blocks) {
                     raise_flag(a.status, kFlagBadBlock);
@@ -643,7 +685,10 @@ __device__ __forceinline__ bool append_row(const DecodeArgs& a, const Policy& po
 // kTails: the variant that attends to what follows a shared prefix
 // (shared_prefix.cu): it skips the prefix's table entries and writes a partial
 // for every segment, whole pairs too, for the merge with the prefix's parts
-// (launched with fused_reduce 0 and without an append).
+// (launched with fused_reduce 0 and without an append).  It neither reads what
+// the launch before it (the parts kernel) writes nor writes what that one
+// reads, and that launch's CTAs let it start only after their own wait; so it
+// runs beside that launch and waits for it at its own end, for the merge.
 template <class Policy, bool kTails>
 __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
     paged_decode_partial_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmk,
@@ -657,14 +702,15 @@ __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
     const int chunks = a.num_kv_heads / Hc;
     const int D = a.head_dim;
     const int half_bytes = Hc * a.block_size * D * dtype_bytes(a.kv_dtype);
-    const SmemLayout L = smem_layout(a.stages, half_bytes, a.num_seqs, NC, R, G, D, a.block_size,
-                                     Policy::kScratch);
+    const SmemLayout L = smem_layout(a.stages, half_bytes, kTails ? 2 * a.num_seqs : a.num_seqs, NC, R, G, D,
+                                     a.block_size, Policy::kScratch);
     uint8_t* ring = base + L.ring;
     uint64_t* full = reinterpret_cast<uint64_t*>(base + L.full_bar);
     uint64_t* empty = reinterpret_cast<uint64_t*>(base + L.empty_bar);
     volatile int* abort = reinterpret_cast<volatile int*>(base + L.flags);
     int32_t* scan = reinterpret_cast<int32_t*>(base + L.scan);
     int32_t* cum = reinterpret_cast<int32_t*>(base + L.cum);
+    int32_t* skip = cum + a.num_seqs + 1;  // kTails only
     float* merge = reinterpret_cast<float*>(base + L.merge);
 
     const int tid = threadIdx.x;
@@ -690,19 +736,19 @@ __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
     // prefix, the table entries and the first stages are fetched while that
     // launch finishes; everything else (q, the new rows, the workspace, the
     // outputs) is touched only after waiting for it.
-    if (!a.early_reads) pdl_wait();
-    build_prefix(a, chunks, cum, scan);  // ends with __syncthreads
+    if (!kTails && !a.early_reads) pdl_wait();
+    build_prefix<kTails>(a, chunks, cum, scan, skip);  // ends with __syncthreads
     const int64_t W = cum[a.num_seqs];
     const int P = a.num_ctas;
     const int start = static_cast<int>(static_cast<int64_t>(blockIdx.x) * W / P);
     const int end = static_cast<int>((static_cast<int64_t>(blockIdx.x) + 1) * W / P);
     const int warp = tid >> 5, lane = tid & 31;
     if (warp == 0 && start < end) {
-        produce<Policy::kTensor, kTails>(a, ring, full, empty, cum, chunks, start, end, half_bytes, &tmk,
+        produce<Policy::kTensor, kTails>(a, ring, full, empty, cum, skip, chunks, start, end, half_bytes, &tmk,
                                  &tmv, abort);
         return;
     }
-    if (a.early_reads) pdl_wait();
+    if (!kTails && a.early_reads) pdl_wait();
     // Global writes of the prologue, by the threads that are not producing.
     const int wt = start < end ? tid - 32 : tid;
     const int nwt = start < end ? static_cast<int>(blockDim.x) - 32 : static_cast<int>(blockDim.x);
@@ -717,7 +763,10 @@ __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
         const int64_t o0 = static_cast<int64_t>(s) * a.num_q_heads * D;
         for (int e = wt; e < a.num_q_heads * D; e += nwt) store_out(a.out, o0 + e, 0.f, a.out_dtype);
     }
-    if (start >= end) return;
+    if (start >= end) {
+        if constexpr (kTails) pdl_wait();
+        return;
+    }
 
     const int w = warp - 1;
     const int hw = w % Hc;  // head within the chunk
@@ -738,7 +787,7 @@ __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
         const int pair_b = pair_a + nbv;
         const int seg_end = min(pair_b, end);
         const int h = hc * Hc + hw;
-        const int ctx = clamp_context(a, s, false);
+        const int ctx = clamp_context(a, s, false) - (kTails ? skip[s] * a.block_size : 0);
         pol.begin(st, a, s, h, G);
         const int first = seg + (((rr - (seg - start)) % R) + R) % R;
         // Ring position of item `first` (item t = i - start sits in stage
@@ -867,6 +916,7 @@ __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
         }
         seg = seg_end;
     }
+    if constexpr (kTails) pdl_wait();
 }
 
 // Launch the partial kernel of `Policy`.  The dynamic shared-memory limit is

@@ -1082,7 +1082,7 @@ kv_status_t paged_prefill_attention_fp8(const void* q, kv_dtype_t q_dtype, const
 namespace {
 
 struct SharedWs {
-    size_t plan, skip, tails, parts, groups, part_o, part_ml, decode, total;
+    size_t parts, groups, part_o, part_ml, decode, total;
     int max_units, max_rows;
     WsLayout d;
 };
@@ -1092,13 +1092,10 @@ SharedWs shared_workspace(int B, int ng, int Hq, int Hkv, int D, int target, int
     SharedWs w;
     const int64_t G = Hq / Hkv;
     // Chunks of at least 1 / target of the work, and one more of every (group,
-    // KV head, row tile); their rows likewise (see the plan kernel).
+    // KV head, row tile); their rows likewise (see chunk_tiles).
     w.max_units = static_cast<int>(target + Hkv * (ng + B * G / 128 + 1));
     w.max_rows = static_cast<int>(int64_t{128} * target + static_cast<int64_t>(B) * Hq);
-    w.plan = 0;
-    w.skip = 256;
-    w.tails = w.skip + align256(static_cast<size_t>(B) * 4);
-    w.parts = w.tails + align256(static_cast<size_t>(B) * 4);
+    w.parts = 0;
     w.groups = w.parts + align256(static_cast<size_t>(B) * sizeof(PrefixParts));
     w.part_o = w.groups + align256(static_cast<size_t>(ng) * sizeof(PrefixGroup));
     w.part_ml = w.part_o + align256(static_cast<size_t>(w.max_rows) * D * 4);
@@ -1169,7 +1166,8 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     while (hc > 11 || num_kv_heads % hc) --hc;
     int R = 8 / hc > 1 ? 8 / hc : 1;
     DecodePlan plan{};
-    if (!plan_warps(KV_KERNEL_MMA, kv_dtype, head_dim, block_size, G, num_seqs, hc, max_smem, false, &R, &plan))
+    // (Room in shared memory for each sequence's shared blocks besides its place.)
+    if (!plan_warps(KV_KERNEL_MMA, kv_dtype, head_dim, block_size, G, 2 * num_seqs, hc, max_smem, false, &R, &plan))
         return fail(KV_ERR_UNSUPPORTED, "shared memory cannot hold two stages for these sizes");
 
     char* ws = static_cast<char*>(workspace);
@@ -1183,9 +1181,6 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     a.prefix_lens = prefix_lens;
     a.out = out;
     a.status = status;
-    a.plan = reinterpret_cast<int32_t*>(ws + w.plan);
-    a.skip_blocks = reinterpret_cast<int32_t*>(ws + w.skip);
-    a.tail_lens = reinterpret_cast<int32_t*>(ws + w.tails);
     a.parts = reinterpret_cast<PrefixParts*>(ws + w.parts);
     a.groups = reinterpret_cast<PrefixGroup*>(ws + w.groups);
     a.part_o = reinterpret_cast<float*>(ws + w.part_o);
@@ -1204,7 +1199,8 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 *
                                       static_cast<double>(fp8 ? k_scale : 1.f));
     a.v_scale = fp8 ? v_scale : 1.f;
-    a.target_units = target;
+    a.num_sms = sms;
+    a.ctas_per_sm = prefix_ctas_per_sm(fp8);
     a.max_units = w.max_units;
     a.max_rows = w.max_rows;
     a.device = dev;
@@ -1216,8 +1212,10 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     d.k_cache = k_cache;
     d.v_cache = v_cache;
     d.block_tables = block_tables;
-    d.context_lens = a.tail_lens;
-    d.skip_blocks = a.skip_blocks;
+    d.context_lens = context_lens;
+    d.group_start = group_start;
+    d.prefix_lens = prefix_lens;
+    d.num_groups = num_groups;
     d.out = out;
     d.counters = reinterpret_cast<int32_t*>(ws + w.decode + w.d.counters);
     d.part_o = reinterpret_cast<float*>(ws + w.decode + w.d.part_o);
@@ -1245,7 +1243,6 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     d.smem_bytes = plan.smem_bytes;
     d.fused_reduce = 0;
     d.pdl = 1;
-    d.early_reads = 1;  // the launch before it is the parts kernel, which writes partials only
     d.phantom = phantom_items(num_seqs, num_kv_heads / hc, max_blocks, ctas, plan.stage_half_bytes);
     d.device = dev;
     CUtensorMap tk, tv;
@@ -1254,9 +1251,8 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     if (kv_status_t st = encode_cache_map(&tv, v_cache, kv_dtype, rows, head_dim, hc * block_size)) return st;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_prefix_plan(a, s);
-    if (e != cudaSuccess) return cuda_fail(e, "prefix plan launch");
-    if ((e = launch_prefix_parts(a, s)) != cudaSuccess) return cuda_fail(e, "prefix parts launch");
+    cudaError_t e = launch_prefix_parts(a, s);
+    if (e != cudaSuccess) return cuda_fail(e, "prefix parts launch");
     if ((e = launch_decode_tails(d, tk, tv, s)) != cudaSuccess) return cuda_fail(e, "tails launch");
     if ((e = launch_prefix_merge(a, d, s)) != cudaSuccess) return cuda_fail(e, "prefix merge launch");
     return KV_OK;

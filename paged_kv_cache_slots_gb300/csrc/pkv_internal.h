@@ -129,7 +129,10 @@ struct DecodeArgs {
     int test_stall;       // testing only: see kv_decode_options_t
     int device;           // CUDA ordinal the launch targets
     int phantom;          // items without data at the start of every (sequence, head chunk) pair
-    const int32_t* skip_blocks;  // [num_seqs] leading table entries left out (tails of a shared prefix only)
+    // Tails of shared prefixes only: the groups (see paged_shared_prefix_attention).
+    const int32_t* group_start;  // [num_groups + 1]
+    const int32_t* prefix_lens;  // [num_groups]
+    int num_groups;
 };
 
 // Multi-token (chunked-prefill) attention and its plan.

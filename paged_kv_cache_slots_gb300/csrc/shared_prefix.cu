@@ -10,16 +10,16 @@
 // attended to by all members alike, without a mask, so its scores are one
 // matrix product per KV head: rows = (member, query head of the KV head),
 // columns = prefix keys.  What follows the prefix differs per sequence and is
-// left to the split-context decode kernel.  Four launches:
-//   plan    (one CTA) checks the groups, finds the members (sequences at
-//           least as long as the prefix; shorter ones read their own tables
-//           throughout), and cuts every (group, KV head, 128 rows) into
-//           chunks of key tiles, so that all chunks run at once;
-//   parts   (this file's main kernel) one CTA a chunk: (m, l, O) of 128 rows;
+// left to the split-context decode kernel.  Three launches:
+//   parts   (this file's main kernel) (m, l, O) of 128 rows over a chunk of a
+//           group's keys, one CTA a (group, KV head, row tile, chunk);
 //   tails   the decode kernel over the tokens after the prefix, partials only;
 //   merge   one warp a (sequence, query head).
-// parts and tails are independent: the tails' CTAs start, and stream their
-// first blocks, while the last parts finish.
+// parts and tails are independent and run side by side as far as there is
+// room.  Which sequences share (those at least as long as the prefix; shorter
+// ones read their own tables throughout) and how the keys are cut follows from
+// the groups alone, so every CTA works it out for itself: one warp-wide pass
+// over the groups costs less than a launch that does it for all.
 //
 // The parts kernel is built like the prefill kernel (prefill_tc.cu): a
 // producer brings K and V tiles of 64 keys into swizzled shared memory, one
@@ -36,162 +36,88 @@ namespace pkv {
 
 namespace {
 
-// ------------------------------------------------------------------ plan
+// ------------------------------------------------------------------ units
 
-constexpr int kPlanThreads = 1024;
+constexpr int kMinChunk = 4;  // key tiles, see chunk_tiles
 
-// Sum over the block (every thread gets it).
-__device__ int64_t block_sum(int64_t v, int64_t* buf) {
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if (lane == 0) buf[wid] = v;
-    __syncthreads();
-    int64_t t = 0;
-    for (int i = 0; i < kPlanThreads / 32; ++i) t += buf[i];
-    return t;
+    return v;
 }
 
-// Exclusive prefix sum over the block, in two lists at once; `total` gets the sums.
-__device__ int2 block_scan(int2 v, int2* buf, int2* total) {
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    int2 x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int yx = __shfl_up_sync(0xffffffffu, x.x, o), yy = __shfl_up_sync(0xffffffffu, x.y, o);
-        if (lane >= o) x.x += yx, x.y += yy;
-    }
-    __syncthreads();
-    if (lane == 31) buf[wid] = x;
-    __syncthreads();
-    int2 before = make_int2(0, 0), all = make_int2(0, 0);
-    for (int i = 0; i < kPlanThreads / 32; ++i) {
-        if (i < wid) before.x += buf[i].x, before.y += buf[i].y;
-        all.x += buf[i].x, all.y += buf[i].y;
-    }
-    *total = all;
-    return make_int2(before.x + x.x - v.x, before.y + x.y - v.y);
+// One lane's group, without its place.
+struct GroupShape {
+    int seq0, rows, tiles, keys, blocks;  // keys: tiles of kPrefixTile
+};
+
+__device__ __forceinline__ GroupShape group_shape(const SharedPrefixArgs& a, int g, int G) {
+    GroupShape p{0, 0, 0, 0, 0};
+    if (g >= a.num_groups) return p;
+    p.seq0 = a.group_start[g];
+    p.rows = (a.group_start[g + 1] - p.seq0) * G;
+    p.tiles = (p.rows + 127) / 128;
+    p.blocks = a.prefix_lens[g] / a.block_size;
+    if (p.blocks > a.max_blocks) p.blocks = 0;  // no sequence is that long
+    p.keys = static_cast<int>((static_cast<int64_t>(p.blocks) * a.block_size + kPrefixTile - 1) / kPrefixTile);
+    return p;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) shared_prefix_plan_kernel(const SharedPrefixArgs a) {
-    __shared__ int64_t sums[kPlanThreads / 32];
-    __shared__ int2 scans[kPlanThreads / 32];
-    pdl_allow_next();
-    pdl_wait();
-    const int tid = threadIdx.x;
-    const int B = a.num_seqs, G = a.num_q_heads / a.num_kv_heads, Hkv = a.num_kv_heads;
-    // Groups must cut the sequences into runs in order; a list that does not
-    // is reported, and nothing is shared.
-    int bad = 0;
-    for (int g = tid; g < a.num_groups; g += kPlanThreads) {
-        const int s0 = a.group_start[g], s1 = a.group_start[g + 1];
-        if (s0 < 0 || s1 > B || s0 > s1 || a.prefix_lens[g] < 0) bad = 1;
-        a.groups[g].lead = B;
+// Key tiles a chunk, found alike by every warp that asks (the groups are in order).
+//
+// All chunks should run at once.  With little work a CTA has an SM to itself,
+// and a chunk up to four tiles: below that its start and the merge of its
+// partial cost more than its tiles.  With more, two CTAs share an SM.  Where
+// rounding chunks up to whole tiles gives more CTAs than fit, chunks grow until
+// they do (unless there are more (group, KV head, row tile) triples than that).
+__device__ int chunk_tiles(const SharedPrefixArgs& a, int G) {
+    const int lane = threadIdx.x & 31;
+    const int64_t limit = static_cast<int64_t>(a.num_sms) * a.ctas_per_sm;
+    int64_t work = 0, triples = 0;
+    const GroupShape first = group_shape(a, lane, G);
+    for (int g0 = 0; g0 < a.num_groups; g0 += 32) {
+        const GroupShape p = g0 == 0 ? first : group_shape(a, g0 + lane, G);
+        work += static_cast<int64_t>(p.tiles) * p.keys;
+        triples += p.keys ? p.tiles : 0;
     }
-    bad = __syncthreads_or(bad);
-    if (bad && tid == 0) raise_flag(a.status, kFlagBadGroup);
-    const int ng = bad ? 0 : a.num_groups;
-    // Members, and what is left of every sequence after the shared blocks.
-    for (int s = tid; s < B; s += kPlanThreads) {
-        int ctx = a.context_lens[s];
-        const int cap = a.max_blocks * a.block_size;
-        if (ctx < 0 || ctx > cap) {
-            raise_flag(a.status, kFlagBadContext);
-            ctx = ctx < 0 ? 0 : cap;
-        }
-        int lo = 0, hi = ng;  // the last group that starts at or before s
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.group_start[mid] <= s)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        int skip = 0;
-        if (ng > 0 && a.group_start[lo] <= s && s < a.group_start[lo + 1]) {
-            const int blocks = a.prefix_lens[lo] / a.block_size;
-            if (blocks <= ctx / a.block_size) skip = blocks;
-            if (skip > 0) atomicMin(&a.groups[lo].lead, s);
-        }
-        a.skip_blocks[s] = skip;
-        a.tail_lens[s] = ctx - skip * a.block_size;
-        a.parts[s] = PrefixParts{lo, 0, 0, 0};  // the group, until its parts are placed
-    }
-    __syncthreads();
-    // Key tiles a chunk: all chunks fit on the GPU at once, if that many CTAs
-    // can hold every (group, KV head, row tile) at all.
-    auto shape = [&](int g, int& rows, int& tiles, int& keys) {
-        const int lead = g < ng ? __ldcg(&a.groups[g].lead) : B;
-        rows = tiles = keys = 0;
-        if (lead >= B) return lead;
-        rows = (a.group_start[g + 1] - a.group_start[g]) * G;
-        tiles = (rows + 127) / 128;
-        const int64_t k = static_cast<int64_t>(a.prefix_lens[g] / a.block_size) * a.block_size;
-        keys = static_cast<int>((k + kPrefixTile - 1) / kPrefixTile);
-        return lead;
-    };
-    int64_t work = 0, longest = 0;
-    for (int g = tid; g < ng; g += kPlanThreads) {
-        int rows, tiles, keys;
-        shape(g, rows, tiles, keys);
-        work += static_cast<int64_t>(Hkv) * tiles * keys;
-        longest = keys > longest ? keys : longest;
-    }
-    work = block_sum(work, sums);
-    int64_t per = (work + a.target_units - 1) / a.target_units;
+    work = warp_sum64(work) * a.num_kv_heads;
+    triples = warp_sum64(triples) * a.num_kv_heads;
+    int64_t per = (work + limit - 1) / limit;
+    const int64_t alone = (work + a.num_sms - 1) / a.num_sms;
+    per = max(per, min(alone, static_cast<int64_t>(kMinChunk)));
     if (per < 1) per = 1;
-    for (int round = 0; round < 12; ++round) {
+    if (triples >= limit) return static_cast<int>(per);
+    for (;;) {
         int64_t units = 0;
-        for (int g = tid; g < ng; g += kPlanThreads) {
-            int rows, tiles, keys;
-            shape(g, rows, tiles, keys);
-            units += static_cast<int64_t>(Hkv) * tiles * ((keys + per - 1) / per);
+        for (int g0 = 0; g0 < a.num_groups; g0 += 32) {
+            const GroupShape p = g0 == 0 ? first : group_shape(a, g0 + lane, G);
+            units += static_cast<int64_t>(p.tiles) * ((p.keys + per - 1) / per);
         }
-        units = block_sum(units, sums);
-        if (units <= a.target_units) break;
+        if (warp_sum64(units) * a.num_kv_heads <= limit) return static_cast<int>(per);
         per += (per + 7) / 8;
     }
-    // Place units and partial rows.
-    int2 carry = make_int2(0, 0);
-    for (int g0 = 0; g0 < a.num_groups; g0 += kPlanThreads) {
-        const int g = g0 + tid;
-        int rows = 0, tiles = 0, keys = 0, lead = B;
-        if (g < ng) lead = shape(g, rows, tiles, keys);
-        const int chunks = static_cast<int>((keys + per - 1) / per);
-        int2 total;
-        const int2 at = block_scan(make_int2(Hkv * tiles * chunks, Hkv * chunks * rows), scans, &total);
-        if (g < a.num_groups) {
-            PrefixGroup p;
-            p.unit0 = carry.x + at.x;
-            p.row0 = carry.y + at.y;
-            p.seq0 = g < ng ? a.group_start[g] : 0;
-            p.rows = rows;
-            p.tiles = tiles;
-            p.chunks = chunks;
-            p.blocks = keys ? a.prefix_lens[g] / a.block_size : 0;
-            p.lead = lead;
-            a.groups[g] = p;
+}
+
+// Calls visit(group, on this lane) for 32 groups at a time, in order, until it
+// returns true (on every lane alike).
+template <class F>
+__device__ __forceinline__ void place_groups(const SharedPrefixArgs& a, int G, int per, F visit) {
+    const int lane = threadIdx.x & 31;
+    int unit0 = 0, row0 = 0;
+    for (int g0 = 0; g0 < a.num_groups; g0 += 32) {
+        const GroupShape p = group_shape(a, g0 + lane, G);
+        const int chunks = (p.keys + per - 1) / per;
+        const int units = a.num_kv_heads * p.tiles * chunks, rows = a.num_kv_heads * chunks * p.rows;
+        int u = units, r = rows;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int yu = __shfl_up_sync(0xffffffffu, u, o), yr = __shfl_up_sync(0xffffffffu, r, o);
+            if (lane >= o) u += yu, r += yr;
         }
-        carry.x += total.x;
-        carry.y += total.y;
-        __syncthreads();
-    }
-    if (tid == 0) {
-        a.plan[0] = carry.x;
-        a.plan[1] = static_cast<int>(per);
-    }
-    __syncthreads();
-    for (int s = tid; s < B; s += kPlanThreads) {
-        PrefixParts p{0, 0, 0, 0};
-        if (a.skip_blocks[s] > 0) {
-            const PrefixGroup g = a.groups[a.parts[s].row0];
-            p.row0 = g.row0 + (s - g.seq0) * G;
-            p.part_stride = g.rows;
-            p.head_stride = g.rows * g.chunks;
-            p.parts = g.chunks;
-        }
-        a.parts[s] = p;
+        const PrefixGroup grp{unit0 + u - units, row0 + r - rows, p.seq0, p.rows, p.tiles, chunks, p.blocks, g0 + lane};
+        if (visit(grp, units)) return;
+        unit0 += __shfl_sync(0xffffffffu, u, 31);
+        row0 += __shfl_sync(0xffffffffu, r, 31);
     }
 }
 
@@ -256,33 +182,76 @@ __global__ void __launch_bounds__(Shape<D, kFP8>::kThreads, Shape<D, kFP8>::kCta
     using S = Shape<D, kFP8>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     pdl_wait();
-    pdl_allow_next();  // after the wait: whoever starts now sees the plan
+    pdl_allow_next();  // after the wait: the tails start when all that came before has completed
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = a.num_q_heads / a.num_kv_heads;
+    if (!groups_in_order(a.group_start, a.prefix_lens, a.num_groups, a.num_seqs, a.status)) {
+        // Nothing is shared; the last CTA says so to the merge.
+        if (blockIdx.x == gridDim.x - 1)
+            for (int s = tid; s < a.num_seqs; s += blockDim.x) a.parts[s] = PrefixParts{0, 0, 0, 0};
+        return;
+    }
+    const int per = chunk_tiles(a, G);
+    if (blockIdx.x == gridDim.x - 1) {
+        // The last CTA has no unit: it tells the merge where every sequence's parts are.
+        if (warp == 0)
+            place_groups(a, G, per, [&](const PrefixGroup& g, int) {
+                if (g.index < a.num_groups) a.groups[g.index] = g;
+                return false;
+            });
+        __syncthreads();
+        for (int s = tid; s < a.num_seqs; s += blockDim.x) {
+            const int ctx = min(max(a.context_lens[s], 0), a.max_blocks * a.block_size);
+            int g = 0;
+            PrefixParts p{0, 0, 0, 0};
+            if (shared_blocks(a.group_start, a.prefix_lens, a.num_groups, a.block_size, s, ctx, &g) > 0) {
+                const PrefixGroup grp = a.groups[g];
+                p.row0 = grp.row0 + (s - grp.seq0) * G;
+                p.part_stride = grp.rows;
+                p.head_stride = grp.rows * grp.chunks;
+                p.parts = grp.chunks;
+            }
+            a.parts[s] = p;
+        }
+        return;
+    }
     const int x = blockIdx.x;
-    if (x >= a.plan[0]) return;
+    PrefixGroup grp;
+    grp.chunks = 0;
+    place_groups(a, G, per, [&](const PrefixGroup& g, int units) {
+        const uint32_t mine = __ballot_sync(0xffffffffu, x >= g.unit0 && x < g.unit0 + units);
+        if (!mine) return false;
+        const int src = __ffs(mine) - 1;
+        grp.unit0 = __shfl_sync(0xffffffffu, g.unit0, src);
+        grp.row0 = __shfl_sync(0xffffffffu, g.row0, src);
+        grp.seq0 = __shfl_sync(0xffffffffu, g.seq0, src);
+        grp.rows = __shfl_sync(0xffffffffu, g.rows, src);
+        grp.tiles = __shfl_sync(0xffffffffu, g.tiles, src);
+        grp.chunks = __shfl_sync(0xffffffffu, g.chunks, src);
+        grp.blocks = __shfl_sync(0xffffffffu, g.blocks, src);
+        return true;
+    });
+    if (grp.chunks == 0) return;  // more CTAs than units
+    // The member whose table row names the blocks.
+    int lead = -1;
+    for (int s0 = 0; s0 * G < grp.rows && lead < 0; s0 += 32) {
+        const int s = grp.seq0 + s0 + lane;
+        const uint32_t in = __ballot_sync(0xffffffffu, (s0 + lane) * G < grp.rows && a.context_lens[s] / a.block_size >= grp.blocks);
+        if (in) lead = grp.seq0 + s0 + __ffs(in) - 1;
+    }
+    if (lead < 0) return;  // every sequence of the group is shorter
     // The swizzled layouts need a 1024-byte aligned base.
     if (smem_addr(smem_raw) & 1023u) {
-        if (threadIdx.x == 0) raise_flag(a.status, kFlagBadPlan);
+        if (tid == 0) raise_flag(a.status, kFlagBadPlan);
         return;
     }
     uint8_t* base = smem_raw;
     Bars* B = reinterpret_cast<Bars*>(base + S::kBarOff);
     volatile int* abort = &B->abort;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int G = a.num_q_heads / a.num_kv_heads;
-    int lo = 0, hi = a.num_groups;  // the last group whose units start at or before x
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.groups[mid].unit0 <= x)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    const PrefixGroup grp = a.groups[lo];
     const int u = x - grp.unit0;
     const int rt = u % grp.tiles;  // row tiles of a chunk side by side: they share its K and V in L2
     const int c = (u / grp.tiles) % grp.chunks;
     const int h = u / (grp.tiles * grp.chunks);
-    const int per = a.plan[1];
     const int nkeys = grp.blocks * a.block_size;
     const int key0 = c * per * kNK;
     const int key1 = min(nkeys, key0 + per * kNK);
@@ -342,7 +311,7 @@ __global__ void __launch_bounds__(Shape<D, kFP8>::kThreads, Shape<D, kFP8>::kCta
         // of 16 (block_size is a multiple of 16), each inside one block; runs
         // past the last key are zeros.
         const int bs = a.block_size;
-        const int32_t* table = a.block_tables + static_cast<int64_t>(grp.lead) * a.max_blocks;
+        const int32_t* table = a.block_tables + static_cast<int64_t>(lead) * a.max_blocks;
         const int nruns = (key1 - key0) / 16;
         // Element offset of run r's first row, in rows of the cache.
         auto run_row = [&](int r) -> int64_t {
@@ -637,7 +606,7 @@ __global__ void __launch_bounds__(128) shared_prefix_merge_kernel(const SharedPr
     const int hq = static_cast<int>(row - static_cast<int64_t>(s) * a.num_q_heads);
     const int G = a.num_q_heads / a.num_kv_heads;
     const int h = hq / G, g = hq - h * G;
-    const PrefixParts pp = a.parts[s];
+    const PrefixParts pp = a.num_groups > 0 ? a.parts[s] : PrefixParts{0, 0, 0, 0};
     // The tail's parts: the CTAs that hold its blocks (see decode_plan.cu).
     const int Hc = d.heads_per_stage, chunks = d.num_kv_heads / Hc;
     const int hc = h / Hc, hw = h - hc * Hc;
@@ -671,6 +640,26 @@ __global__ void __launch_bounds__(128) shared_prefix_merge_kernel(const SharedPr
                 ml = __ldcg(reinterpret_cast<const float2*>(d.part_ml + 2 * r));
             }
         }
+        const uint64_t addr = reinterpret_cast<uint64_t>(po);
+        const int cnt = min(32, n - base);
+        // Outputs of eight parts; the first eight are asked for together with
+        // the (max, sum) pairs.
+        float v[8][VD];
+        auto fetch = [&](int k0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, addr, (k0 + k) & 31));
+                const bool get = k0 + k < cnt && src != nullptr;
+                if constexpr (VD == 4) {
+                    const float4 t = get ? __ldcg(reinterpret_cast<const float4*>(src) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    v[k][0] = t.x, v[k][1] = t.y, v[k][2] = t.z, v[k][3] = t.w;
+                } else {
+                    const float2 t = get ? __ldcg(reinterpret_cast<const float2*>(src) + lane) : make_float2(0.f, 0.f);
+                    v[k][0] = t.x, v[k][1] = t.y;
+                }
+            }
+        };
+        fetch(0);
         float mx = ml.x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -684,22 +673,8 @@ __global__ void __launch_bounds__(128) shared_prefix_merge_kernel(const SharedPr
         M = Mn;
 #pragma unroll
         for (int i = 0; i < VD; ++i) acc[i] *= al;
-        const uint64_t addr = reinterpret_cast<uint64_t>(po);
-        const int cnt = min(32, n - base);
         for (int k0 = 0; k0 < cnt; k0 += 8) {
-            float v[8][VD];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, addr, (k0 + k) & 31));
-                const bool get = k0 + k < cnt && src != nullptr;
-                if constexpr (VD == 4) {
-                    const float4 t = get ? __ldcg(reinterpret_cast<const float4*>(src) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    v[k][0] = t.x, v[k][1] = t.y, v[k][2] = t.z, v[k][3] = t.w;
-                } else {
-                    const float2 t = get ? __ldcg(reinterpret_cast<const float2*>(src) + lane) : make_float2(0.f, 0.f);
-                    v[k][0] = t.x, v[k][1] = t.y;
-                }
-            }
+            if (k0 > 0) fetch(k0);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const float wk = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
@@ -727,7 +702,7 @@ cudaError_t launch_parts_t(const SharedPrefixArgs& a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         if (cacheable) configured[a.device].store(1);
     }
-    return launch_kernel(kern, dim3(a.max_units), dim3(S::kThreads), static_cast<size_t>(a.smem_bytes), stream, true, a);
+    return launch_kernel(kern, dim3(a.max_units + 1), dim3(S::kThreads), static_cast<size_t>(a.smem_bytes), stream, true, a);
 }
 
 }  // namespace
@@ -738,10 +713,6 @@ int prefix_smem_bytes(int head_dim, bool fp8) {
 }
 
 int prefix_ctas_per_sm(bool fp8) { return fp8 ? Shape<128, true>::kCtas : Shape<128, false>::kCtas; }
-
-cudaError_t launch_prefix_plan(const SharedPrefixArgs& a, cudaStream_t stream) {
-    return launch_kernel(shared_prefix_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, true, a);
-}
 
 cudaError_t launch_prefix_parts(const SharedPrefixArgs& a, cudaStream_t stream) {
     if (a.kv_dtype == kFP8) {

@@ -5,16 +5,17 @@
 
 namespace pkv {
 
-// One group of sequences, as planned on the device.
+// One group of sequences: its share of the parts kernel's units (CTAs with
+// work) and of the partial rows.
 struct PrefixGroup {
-    int unit0;   // first work unit
+    int unit0;   // first unit
     int row0;    // first partial row
     int seq0;    // first sequence
     int rows;    // (sequences of the group) x (query heads per KV head)
     int tiles;   // row tiles of 128
-    int chunks;  // pieces its keys are split into (0: nothing is shared)
+    int chunks;  // pieces its keys are split into
     int blocks;  // shared blocks
-    int lead;    // the member whose table row names them
+    int index;
 };
 
 // Where the prefix parts of a sequence are: part c of KV head h, query head g
@@ -34,18 +35,15 @@ struct SharedPrefixArgs {
     void* out;
     uint32_t* status;
     // Workspace.
-    int32_t* plan;               // [0] units, [1] key tiles a chunk
-    int32_t* skip_blocks;        // [B] shared blocks of each sequence's table row
-    int32_t* tail_lens;          // [B] tokens after them
     PrefixParts* parts;          // [B]
     PrefixGroup* groups;         // [num_groups]
-    float* part_o;               // [part_rows][D]
-    float* part_ml;              // [part_rows][2]
+    float* part_o;               // [max_rows][D]
+    float* part_ml;              // [max_rows][2]
     int num_seqs, num_groups, num_blocks, max_blocks, num_q_heads, num_kv_heads, head_dim, block_size;
     int dtype, out_dtype, kv_dtype;
     float scale_log2, v_scale;
-    int target_units;            // CTAs that run at once
-    int max_units, max_rows;     // capacity of the grid and of the partial rows
+    int num_sms, ctas_per_sm;    // CTAs of the parts kernel that run at once
+    int max_units, max_rows;     // most units and partial rows
     int device, smem_bytes;
 };
 
@@ -54,7 +52,6 @@ constexpr int kPrefixTile = 64;
 
 int prefix_smem_bytes(int head_dim, bool fp8);
 int prefix_ctas_per_sm(bool fp8);
-cudaError_t launch_prefix_plan(const SharedPrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_parts(const SharedPrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_merge(const SharedPrefixArgs& a, const DecodeArgs& tails, cudaStream_t stream);
 // The decode kernel over what follows the prefix (decode_tails.cu).
