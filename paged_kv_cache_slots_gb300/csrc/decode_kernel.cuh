@@ -145,7 +145,9 @@ __device__ __forceinline__ int shared_blocks(const int32_t* group_start, const i
 template <bool kTails>
 static __device__ void build_prefix(const DecodeArgs& a, int chunks, int32_t* cum, int32_t* scan, int32_t* skip) {
     int groups = 0;
+    int first_ctx = 0;  // of this thread's first sequence, asked for before the groups are looked at
     if constexpr (kTails) {
+        if (threadIdx.x < a.num_seqs) first_ctx = clamp_context(a, threadIdx.x, blockIdx.x == 0);
         if (groups_in_order(a.group_start, a.prefix_lens, a.num_groups, a.num_seqs, a.status)) groups = a.num_groups;
     }
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -155,7 +157,7 @@ static __device__ void build_prefix(const DecodeArgs& a, int chunks, int32_t* cu
         const int s = base + tid;
         int v = 0;
         if (s < a.num_seqs) {
-            const int c = clamp_context(a, s, blockIdx.x == 0);
+            const int c = kTails && base == 0 ? first_ctx : clamp_context(a, s, blockIdx.x == 0);
             int nb = (c + a.block_size - 1) / a.block_size;
             if constexpr (kTails) {
                 int g;
@@ -190,6 +192,17 @@ static __device__ void build_prefix(const DecodeArgs& a, int chunks, int32_t* cu
     }
     if (tid == 0) cum[a.num_seqs] = carry;
     __syncthreads();
+}
+
+// Where the merge finds the parts that the tails' CTAs leave of a pair:
+// (first CTA, parts, -, -) when every CTA holds items, its parts in
+// consecutive CTAs; else (-, parts, item of the first, all items), part k in
+// the CTA that owns item z + k.
+__device__ __forceinline__ int4 tail_parts_of(int pair_r, int blocks, int64_t W, int P) {
+    if (blocks <= 0) return make_int4(0, 0, 0, 0);
+    if (W < P) return make_int4(0, blocks, pair_r, static_cast<int>(W));
+    const int ca = cta_of_item(pair_r, W, P);
+    return make_int4(ca, cta_of_item(pair_r + blocks - 1, W, P) - ca + 1, 0, 0);
 }
 
 // ------------------------------------------------------------------ producer
@@ -752,7 +765,14 @@ __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
     // Global writes of the prologue, by the threads that are not producing.
     const int wt = start < end ? tid - 32 : tid;
     const int nwt = start < end ? static_cast<int>(blockDim.x) - 32 : static_cast<int>(blockDim.x);
-    if (blockIdx.x == 0 && !a.fused_reduce) {
+    if constexpr (kTails) {
+        for (int p = blockIdx.x + P * wt; p < a.num_seqs * chunks; p += P * nwt) {
+            const int s = p / chunks;
+            const int nbv = (cum[s + 1] - cum[s]) / chunks;
+            a.tail_parts[p] = tail_parts_of(cum[s] + (p - s * chunks) * nbv + a.phantom, nbv - a.phantom, W, P);
+        }
+    }
+    if (!kTails && blockIdx.x == 0 && !a.fused_reduce) {
         for (int s = wt; s <= a.num_seqs; s += nwt) a.cum[s] = cum[s];
     }
     // Sequences with no tokens: zero rows (fused merge) and slot -1 (CTA s mod P).

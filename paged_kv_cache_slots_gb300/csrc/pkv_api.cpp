@@ -1082,22 +1082,20 @@ kv_status_t paged_prefill_attention_fp8(const void* q, kv_dtype_t q_dtype, const
 namespace {
 
 struct SharedWs {
-    size_t parts, groups, part_o, part_ml, decode, total;
-    int max_units, max_rows;
+    size_t parts, tails, part_o, part_ml, decode, total;
+    int max_rows;
     WsLayout d;
 };
 
 // target: parts CTAs that run at once; ctas: the tails kernel's grid.
-SharedWs shared_workspace(int B, int ng, int Hq, int Hkv, int D, int target, int ctas) {
+SharedWs shared_workspace(int B, int Hq, int Hkv, int D, int target, int ctas) {
     SharedWs w;
-    const int64_t G = Hq / Hkv;
-    // Chunks of at least 1 / target of the work, and one more of every (group,
-    // KV head, row tile); their rows likewise (see chunk_tiles).
-    w.max_units = static_cast<int>(target + Hkv * (ng + B * G / 128 + 1));
-    w.max_rows = static_cast<int>(int64_t{128} * target + static_cast<int64_t>(B) * Hq);
+    // 128 rows for each CTA's share of the work, and two parts more of every
+    // row (see the units in shared_prefix.cu).
+    w.max_rows = static_cast<int>(int64_t{128} * target + 2 * static_cast<int64_t>(B) * Hq);
     w.parts = 0;
-    w.groups = w.parts + align256(static_cast<size_t>(B) * sizeof(PrefixParts));
-    w.part_o = w.groups + align256(static_cast<size_t>(ng) * sizeof(PrefixGroup));
+    w.tails = align256(static_cast<size_t>(B) * Hkv * sizeof(PrefixParts));
+    w.part_o = w.tails + align256(static_cast<size_t>(B) * Hkv * sizeof(int4));
     w.part_ml = w.part_o + align256(static_cast<size_t>(w.max_rows) * D * 4);
     w.decode = w.part_ml + align256(static_cast<size_t>(w.max_rows) * 8);
     w.d = workspace_layout(B, Hq, Hkv, D, ctas);
@@ -1108,7 +1106,7 @@ SharedWs shared_workspace(int B, int ng, int Hq, int Hkv, int D, int target, int
 kv_status_t shared_sizes(const char* what, int B, int ng, int Hq, int Hkv, int D) {
     if (B < 0 || ng < 0 || Hq <= 0 || Hkv <= 0 || D <= 0) return fail(KV_ERR_INVALID_ARG, "%s: sizes out of range", what);
     if (Hq % Hkv) return fail(KV_ERR_INVALID_ARG, "num_q_heads %d is not a multiple of num_kv_heads %d", Hq, Hkv);
-    if (static_cast<int64_t>(B) * Hq >= (int64_t{1} << 30) || static_cast<int64_t>(ng) * Hkv >= (int64_t{1} << 24))
+    if (static_cast<int64_t>(B) * Hq >= (int64_t{1} << 29) || static_cast<int64_t>(ng) * Hkv >= (int64_t{1} << 24))
         return fail(KV_ERR_UNSUPPORTED, "%s: too many sequences or groups", what);
     return KV_OK;
 }
@@ -1140,9 +1138,13 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
         return fail(KV_ERR_UNSUPPORTED, "out_dtype must be KV_F32 or the input dtype");
     if (!std::isfinite(scale)) return fail(KV_ERR_INVALID_ARG, "scale is not finite");
     if (static_cast<int64_t>(num_seqs) * num_kv_heads * max_blocks >= (int64_t{1} << 31) ||
-        static_cast<int64_t>(max_blocks) * block_size >= (int64_t{1} << 31) ||
+        static_cast<int64_t>(max_blocks) * block_size >= (int64_t{1} << 31) - kPrefixTile ||
         static_cast<int64_t>(num_blocks) * num_kv_heads * block_size >= (int64_t{1} << 31))
         return fail(KV_ERR_UNSUPPORTED, "sizes exceed 32-bit tile / row indices");
+    // Key tiles of all rows of the prefix part, at most.
+    if (((static_cast<int64_t>(num_seqs) * G / 128 + num_groups) * num_kv_heads) *
+            (static_cast<int64_t>(max_blocks) * block_size / kPrefixTile + 1) >= (int64_t{1} << 31))
+        return fail(KV_ERR_UNSUPPORTED, "%s: more than 2^31 tiles of work", what);
     if (num_seqs == 0) return KV_OK;
     if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out || !workspace ||
         (num_groups > 0 && (!group_start || !prefix_lens)))
@@ -1157,7 +1159,7 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     uint32_t* status = nullptr;
     if (kv_status_t st = device_info(&dev, &status, &sms, &max_smem, nullptr)) return st;
     const int target = sms * prefix_ctas_per_sm(fp8), ctas = sms;
-    const SharedWs w = shared_workspace(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, target, ctas);
+    const SharedWs w = shared_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, target, ctas);
     if (workspace_bytes < w.total)
         return fail(KV_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, w.total);
     // The tails: heads a stage as the decode kernel's default, up to 11 (its
@@ -1182,7 +1184,6 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     a.out = out;
     a.status = status;
     a.parts = reinterpret_cast<PrefixParts*>(ws + w.parts);
-    a.groups = reinterpret_cast<PrefixGroup*>(ws + w.groups);
     a.part_o = reinterpret_cast<float*>(ws + w.part_o);
     a.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
     a.num_seqs = num_seqs;
@@ -1201,7 +1202,6 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     a.v_scale = fp8 ? v_scale : 1.f;
     a.num_sms = sms;
     a.ctas_per_sm = prefix_ctas_per_sm(fp8);
-    a.max_units = w.max_units;
     a.max_rows = w.max_rows;
     a.device = dev;
     a.smem_bytes = prefix_smem_bytes(head_dim, fp8);
@@ -1216,6 +1216,7 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     d.group_start = group_start;
     d.prefix_lens = prefix_lens;
     d.num_groups = num_groups;
+    d.tail_parts = reinterpret_cast<int4*>(ws + w.tails);
     d.out = out;
     d.counters = reinterpret_cast<int32_t*>(ws + w.decode + w.d.counters);
     d.part_o = reinterpret_cast<float*>(ws + w.decode + w.d.part_o);
@@ -1270,8 +1271,7 @@ kv_status_t paged_shared_prefix_workspace_bytes(int num_seqs, int num_groups, in
     int sms = 0;
     if (kv_status_t st = device_info(nullptr, nullptr, &sms, nullptr, nullptr)) return st;
     // The larger of the two cache kinds' needs.
-    *bytes = shared_workspace(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim,
-                              sms * prefix_ctas_per_sm(false), sms).total;
+    *bytes = shared_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, sms * prefix_ctas_per_sm(false), sms).total;
     return KV_OK;
 }
 

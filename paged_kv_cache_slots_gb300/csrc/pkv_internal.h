@@ -133,6 +133,7 @@ struct DecodeArgs {
     const int32_t* group_start;  // [num_groups + 1]
     const int32_t* prefix_lens;  // [num_groups]
     int num_groups;
+    int4* tail_parts;            // [num_seqs][Hkv / heads_per_stage] written: see tail_parts_of
 };
 
 // Multi-token (chunked-prefill) attention and its plan.

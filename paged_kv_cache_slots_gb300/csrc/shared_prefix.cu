@@ -38,86 +38,175 @@ namespace {
 
 // ------------------------------------------------------------------ units
 
-constexpr int kMinChunk = 4;  // key tiles, see chunk_tiles
+constexpr int kMinChunk = 4;  // key tiles a CTA
 
-__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+// The prefix part's work is key tiles: every (group, KV head, row tile) triple
+// has the group's tiles, triples in that order.  CTA c of P takes tiles
+// [c W / P, (c + 1) W / P), whatever triples they belong to: all CTAs have the
+// same work to within a tile.  A run of one triple's tiles in one CTA is a
+// segment, and leaves one part.  Part k of a triple comes from the k-th CTA
+// that has tiles of it; a group reserves keys P / W + 2 parts of each of its
+// rows, so all groups together reserve at most 128 P + 2 (all rows).
+
+// a * b / c for 0 <= a, b and c > 0.
+__device__ __forceinline__ int mul_div(int a, int b, int c) {
+    const uint64_t p = static_cast<uint64_t>(static_cast<uint32_t>(a)) * static_cast<uint32_t>(b);
+    if ((p >> 32) == 0) return static_cast<int>(static_cast<uint32_t>(p) / static_cast<uint32_t>(c));
+    return static_cast<int>(p / static_cast<uint32_t>(c));
 }
 
-// One lane's group, without its place.
+// CTA that owns tile x of W.
+__device__ __forceinline__ int cta_of_tile(int x, int W, int P) {
+    const uint64_t p = (static_cast<uint64_t>(x) + 1) * static_cast<uint32_t>(P) - 1;
+    if ((p >> 32) == 0) return static_cast<int>(static_cast<uint32_t>(p) / static_cast<uint32_t>(W));
+    return static_cast<int>(p / static_cast<uint32_t>(W));
+}
+
+// One lane's group.
 struct GroupShape {
-    int seq0, rows, tiles, keys, blocks;  // keys: tiles of kPrefixTile
+    int seq0, rows, tiles, keys, blocks;  // rows: sequences x G; tiles: row tiles; keys: key tiles
 };
 
-__device__ __forceinline__ GroupShape group_shape(const SharedPrefixArgs& a, int g, int G) {
+__device__ __forceinline__ int group_work(const GroupShape& p, int Hkv) { return Hkv * p.tiles * p.keys; }
+
+// Group g's shape; no work for one past the last.  *bad: it is out of order.
+__device__ __forceinline__ GroupShape group_shape(const SharedPrefixArgs& a, int g, int G, bool* bad) {
     GroupShape p{0, 0, 0, 0, 0};
     if (g >= a.num_groups) return p;
-    p.seq0 = a.group_start[g];
-    p.rows = (a.group_start[g + 1] - p.seq0) * G;
-    p.tiles = (p.rows + 127) / 128;
-    p.blocks = a.prefix_lens[g] / a.block_size;
+    const int s0 = a.group_start[g], s1 = a.group_start[g + 1], len = a.prefix_lens[g];
+    if (s0 < 0 || s1 > a.num_seqs || s0 > s1 || len < 0) {
+        *bad = true;
+        return p;
+    }
+    p.seq0 = s0;
+    p.rows = (s1 - s0) * G;
+    p.tiles = (p.rows + 127) >> 7;
+    p.blocks = len / a.block_size;
     if (p.blocks > a.max_blocks) p.blocks = 0;  // no sequence is that long
-    p.keys = static_cast<int>((static_cast<int64_t>(p.blocks) * a.block_size + kPrefixTile - 1) / kPrefixTile);
+    p.keys = (p.blocks * a.block_size + kPrefixTile - 1) / kPrefixTile;
     return p;
 }
 
-// Key tiles a chunk, found alike by every warp that asks (the groups are in order).
-//
-// All chunks should run at once.  With little work a CTA has an SM to itself,
-// and a chunk up to four tiles: below that its start and the merge of its
-// partial cost more than its tiles.  With more, two CTAs share an SM.  Where
-// rounding chunks up to whole tiles gives more CTAs than fit, chunks grow until
-// they do (unless there are more (group, KV head, row tile) triples than that).
-__device__ int chunk_tiles(const SharedPrefixArgs& a, int G) {
+// What every CTA, and every warp of it, works out alike.
+struct Units {
+    GroupShape first;  // this lane's group of the first 32
+    int W, P;          // tiles and CTAs with work; W = 0: nothing is shared
+};
+
+__device__ __forceinline__ Units plan_units(const SharedPrefixArgs& a, int G) {
     const int lane = threadIdx.x & 31;
-    const int64_t limit = static_cast<int64_t>(a.num_sms) * a.ctas_per_sm;
-    int64_t work = 0, triples = 0;
-    const GroupShape first = group_shape(a, lane, G);
-    for (int g0 = 0; g0 < a.num_groups; g0 += 32) {
-        const GroupShape p = g0 == 0 ? first : group_shape(a, g0 + lane, G);
-        work += static_cast<int64_t>(p.tiles) * p.keys;
+    Units u;
+    bool bad = false;
+    u.first = group_shape(a, lane, G, &bad);
+    int work = group_work(u.first, a.num_kv_heads), triples = u.first.keys ? u.first.tiles : 0;
+    for (int g0 = 32; g0 < a.num_groups; g0 += 32) {
+        const GroupShape p = group_shape(a, g0 + lane, G, &bad);
+        work += group_work(p, a.num_kv_heads);
         triples += p.keys ? p.tiles : 0;
     }
-    work = warp_sum64(work) * a.num_kv_heads;
-    triples = warp_sum64(triples) * a.num_kv_heads;
-    int64_t per = (work + limit - 1) / limit;
-    const int64_t alone = (work + a.num_sms - 1) / a.num_sms;
-    per = max(per, min(alone, static_cast<int64_t>(kMinChunk)));
-    if (per < 1) per = 1;
-    if (triples >= limit) return static_cast<int>(per);
-    for (;;) {
-        int64_t units = 0;
-        for (int g0 = 0; g0 < a.num_groups; g0 += 32) {
-            const GroupShape p = g0 == 0 ? first : group_shape(a, g0 + lane, G);
-            units += static_cast<int64_t>(p.tiles) * ((p.keys + per - 1) / per);
-        }
-        if (warp_sum64(units) * a.num_kv_heads <= limit) return static_cast<int>(per);
-        per += (per + 7) / 8;
+    bad = __any_sync(0xffffffffu, bad);
+    work = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(work)));
+    triples = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(triples))) * a.num_kv_heads;
+    u.W = bad ? 0 : work;
+    // With little work a CTA has an SM to itself, and four tiles (below that
+    // its start and the merge of its parts cost more than its tiles); with
+    // more, two share an SM.
+    const int all = a.num_sms * a.ctas_per_sm;
+    int P = u.W / kMinChunk >= all ? all : min(a.num_sms, (u.W + kMinChunk - 1) / kMinChunk);
+    // CTAs that begin with a triple have one segment: worth up to a quarter of
+    // the CTAs while a CTA has few tiles, a sixteenth always.
+    if (triples > 0 && triples <= P) {
+        const int even = P / triples * triples;
+        if ((P - even) * (u.W / P < 16 ? 4 : 16) <= P) P = even;
     }
+    u.P = P > 0 ? P : 1;
+    return u;
 }
 
-// Calls visit(group, on this lane) for 32 groups at a time, in order, until it
-// returns true (on every lane alike).
-template <class F>
-__device__ __forceinline__ void place_groups(const SharedPrefixArgs& a, int G, int per, F visit) {
+// A triple, and a tile in it.
+struct Triple {
+    int seq0, rows, blocks, keys;
+    int h, rt;       // KV head, row tile
+    int tile0;       // first tile of the triple
+    int row0;        // row tile's first partial row, part 0
+    int stride;      // rows from one part to the next
+};
+
+// The triple of tile x, by the whole warp (0 <= x < W).
+__device__ __forceinline__ Triple find_triple(const SharedPrefixArgs& a, const Units& u, int G, int x) {
     const int lane = threadIdx.x & 31;
-    int unit0 = 0, row0 = 0;
+    Triple t{};
+    int tile0 = 0, row0 = 0;
+    bool bad = false;
     for (int g0 = 0; g0 < a.num_groups; g0 += 32) {
-        const GroupShape p = group_shape(a, g0 + lane, G);
-        const int chunks = (p.keys + per - 1) / per;
-        const int units = a.num_kv_heads * p.tiles * chunks, rows = a.num_kv_heads * chunks * p.rows;
-        int u = units, r = rows;
+        const GroupShape p = g0 == 0 ? u.first : group_shape(a, g0 + lane, G, &bad);
+        const int work = group_work(p, a.num_kv_heads);
+        const int parts = mul_div(p.keys, u.P, u.W) + 2;
+        const int rows = p.keys ? a.num_kv_heads * parts * p.rows : 0;
+        int w = work, r = rows;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int yu = __shfl_up_sync(0xffffffffu, u, o), yr = __shfl_up_sync(0xffffffffu, r, o);
-            if (lane >= o) u += yu, r += yr;
+            const int yw = __shfl_up_sync(0xffffffffu, w, o), yr = __shfl_up_sync(0xffffffffu, r, o);
+            if (lane >= o) w += yw, r += yr;
         }
-        const PrefixGroup grp{unit0 + u - units, row0 + r - rows, p.seq0, p.rows, p.tiles, chunks, p.blocks, g0 + lane};
-        if (visit(grp, units)) return;
-        unit0 += __shfl_sync(0xffffffffu, u, 31);
+        const uint32_t mine = __ballot_sync(0xffffffffu, x < tile0 + w);
+        if (mine) {
+            const int src = __ffs(mine) - 1;
+            t.seq0 = __shfl_sync(0xffffffffu, p.seq0, src);
+            t.rows = __shfl_sync(0xffffffffu, p.rows, src);
+            t.blocks = __shfl_sync(0xffffffffu, p.blocks, src);
+            t.keys = __shfl_sync(0xffffffffu, p.keys, src);
+            const int tiles = __shfl_sync(0xffffffffu, p.tiles, src);
+            const int np = __shfl_sync(0xffffffffu, parts, src);
+            const int first = tile0 + __shfl_sync(0xffffffffu, w - work, src);
+            const int k = (x - first) / t.keys;
+            t.h = k / tiles;
+            t.rt = k - t.h * tiles;
+            t.tile0 = first + k * t.keys;
+            t.stride = t.rows;
+            t.row0 = row0 + __shfl_sync(0xffffffffu, r - rows, src) + t.h * np * t.rows + t.rt * 128;
+            return t;
+        }
+        tile0 += __shfl_sync(0xffffffffu, w, 31);
         row0 += __shfl_sync(0xffffffffu, r, 31);
+    }
+    return t;
+}
+
+// Tells the merge where every (sequence, KV head)'s parts are.  One warp.
+__device__ void write_parts_table(const SharedPrefixArgs& a, const Units& u, int G) {
+    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int Hkv = a.num_kv_heads;
+    for (int i = threadIdx.x; i < a.num_seqs * Hkv; i += blockDim.x) a.parts[i] = PrefixParts{0, 0, 0, 0};
+    __syncthreads();
+    if (u.W == 0) return;
+    int tile0 = 0, row0 = 0;
+    bool bad = false;
+    for (int g0 = 0; g0 < a.num_groups; g0 += 32) {
+        const GroupShape p = g0 == 0 ? u.first : group_shape(a, g0 + lane, G, &bad);
+        const int work = group_work(p, Hkv);
+        const int parts = mul_div(p.keys, u.P, u.W) + 2;
+        const int rows = p.keys ? Hkv * parts * p.rows : 0;
+        for (int k = 0; k < 32; ++k) {  // the groups one after the other, a warp's share of the pairs each
+            const int n = __shfl_sync(0xffffffffu, work, k);
+            const int keys = __shfl_sync(0xffffffffu, p.keys, k), tiles = __shfl_sync(0xffffffffu, p.tiles, k);
+            const int grows = __shfl_sync(0xffffffffu, p.rows, k), seq0 = __shfl_sync(0xffffffffu, p.seq0, k);
+            const int np = __shfl_sync(0xffffffffu, parts, k), blocks = __shfl_sync(0xffffffffu, p.blocks, k);
+            const int reserved = __shfl_sync(0xffffffffu, rows, k);
+            const int pairs = n ? grows / G * Hkv : 0;
+            for (int i = warp * 32 + lane; i < pairs; i += warps * 32) {
+                const int s = i / Hkv, h = i - s * Hkv;
+                if (a.context_lens[seq0 + s] / a.block_size < blocks) continue;  // ends inside the prefix
+                const int rt = s * G >> 7;
+                const int first = tile0 + (h * tiles + rt) * keys;
+                const int ca = cta_of_tile(first, u.W, u.P), cb = cta_of_tile(first + keys - 1, u.W, u.P);
+                a.parts[static_cast<int64_t>(seq0 + s) * Hkv + h] =
+                    PrefixParts{row0 + h * np * grows + s * G, grows, cb - ca + 1, 0};
+            }
+            tile0 += n;
+            row0 += reserved;
+        }
     }
 }
 
@@ -134,18 +223,22 @@ struct Shape {
     static constexpr int kKRing = D == 128 ? 3 : 6;           // K stages
     static constexpr int kVRing = D == 128 ? 2 : 4;           // V stages
     static constexpr uint32_t kTile = kSlices * kNK * 128;    // bytes of a K (or V) tile
-    static constexpr uint32_t kQOff = 0;
-    static constexpr uint32_t kKOff = kSlices * kBM * 128;
-    static constexpr uint32_t kVOff = kKOff + kKRing * kTile;
-    static constexpr uint32_t kBarOff = kVOff + kVRing * kTile;
     static constexpr int kProducers = kFP8 ? 4 : 1;           // producer warps
     static constexpr int kThreads = 32 * (5 + kProducers);
     static constexpr int kCtas = kFP8 ? 1 : 2;                // CTAs an SM
+    // E4M3: codes on their way, a ring for each producer warp: its 16 rows of K and of V.
+    static constexpr int kRawRing = kFP8 ? 6 : 0;
+    static constexpr uint32_t kRawStage = 2 * 16 * 128;
+    static constexpr uint32_t kQOff = 0;
+    static constexpr uint32_t kKOff = kSlices * kBM * 128;
+    static constexpr uint32_t kVOff = kKOff + kKRing * kTile;
+    static constexpr uint32_t kRawOff = kVOff + kVRing * kTile;
+    static constexpr uint32_t kBarOff = kRawOff + kProducers * kRawRing * kRawStage;
 };
 
 struct Bars {
     uint64_t kfull[6], kempty[6], vfull[4], vempty[4];
-    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t s_full[2], p_full[2], pv_done[2], q_full;
     uint32_t tmem;
     int abort;
 };
@@ -159,87 +252,46 @@ __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* sr
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
 }
 
-// Eight E4M3 codes -> eight values of DT (exact).
-template <int DT>
-__device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
-    uint32_t h[4] = {e4m3x2_to_half2(static_cast<uint16_t>(lo)), e4m3x2_to_half2(static_cast<uint16_t>(lo >> 16)),
-                     e4m3x2_to_half2(static_cast<uint16_t>(hi)), e4m3x2_to_half2(static_cast<uint16_t>(hi >> 16))};
-    if constexpr (DT == kBF16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-            const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
-            h[i] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-    }
-    return make_uint4(h[0], h[1], h[2], h[3]);
+// 32 bytes to global memory (a whole sector at once).
+__device__ __forceinline__ void store_32(float* p, const float* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(__float_as_uint(v[0])),
+                 "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+                 "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])),
+                 "r"(__float_as_uint(v[7]))
+                 : "memory");
 }
 
-template <int DT, int D, bool kFP8>
+// Eight E4M3 codes -> eight f16 values, exactly, times 2^-8.
+__device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
+    return make_uint4(e4m3x2_odd_bytes_to_half2_shifted(__byte_perm(lo, 0u, 0x1404)),
+                      e4m3x2_odd_bytes_to_half2_shifted(__byte_perm(lo, 0u, 0x3424)),
+                      e4m3x2_odd_bytes_to_half2_shifted(__byte_perm(hi, 0u, 0x1404)),
+                      e4m3x2_odd_bytes_to_half2_shifted(__byte_perm(hi, 0u, 0x3424)));
+}
+
+// QT: q's type.  The tensor cores work in it, or in f16 over an E4M3 cache
+// (whose codes widen to f16 in a few integer operations); a bf16 q is then
+// brought to f16 with a power of two for each row that puts its largest
+// element at 2^13: exact down to 2^-27 of that element.
+template <int QT, int D, bool kFP8>
 __global__ void __launch_bounds__(Shape<D, kFP8>::kThreads, Shape<D, kFP8>::kCtas)
     shared_prefix_parts_kernel(const SharedPrefixArgs a) {
-    using T = typename Elem<DT>::T;
+    using T = typename Elem<QT>::T;
     using S = Shape<D, kFP8>;
+    constexpr int DT = kFP8 ? static_cast<int>(kF16) : QT;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     pdl_wait();
     pdl_allow_next();  // after the wait: the tails start when all that came before has completed
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = a.num_q_heads / a.num_kv_heads;
-    if (!groups_in_order(a.group_start, a.prefix_lens, a.num_groups, a.num_seqs, a.status)) {
-        // Nothing is shared; the last CTA says so to the merge.
-        if (blockIdx.x == gridDim.x - 1)
-            for (int s = tid; s < a.num_seqs; s += blockDim.x) a.parts[s] = PrefixParts{0, 0, 0, 0};
+    const Units units = plan_units(a, G);
+    const int cta = blockIdx.x;
+    if (cta == static_cast<int>(gridDim.x) - 1) {  // the last CTA has no tiles
+        write_parts_table(a, units, G);
         return;
     }
-    const int per = chunk_tiles(a, G);
-    if (blockIdx.x == gridDim.x - 1) {
-        // The last CTA has no unit: it tells the merge where every sequence's parts are.
-        if (warp == 0)
-            place_groups(a, G, per, [&](const PrefixGroup& g, int) {
-                if (g.index < a.num_groups) a.groups[g.index] = g;
-                return false;
-            });
-        __syncthreads();
-        for (int s = tid; s < a.num_seqs; s += blockDim.x) {
-            const int ctx = min(max(a.context_lens[s], 0), a.max_blocks * a.block_size);
-            int g = 0;
-            PrefixParts p{0, 0, 0, 0};
-            if (shared_blocks(a.group_start, a.prefix_lens, a.num_groups, a.block_size, s, ctx, &g) > 0) {
-                const PrefixGroup grp = a.groups[g];
-                p.row0 = grp.row0 + (s - grp.seq0) * G;
-                p.part_stride = grp.rows;
-                p.head_stride = grp.rows * grp.chunks;
-                p.parts = grp.chunks;
-            }
-            a.parts[s] = p;
-        }
-        return;
-    }
-    const int x = blockIdx.x;
-    PrefixGroup grp;
-    grp.chunks = 0;
-    place_groups(a, G, per, [&](const PrefixGroup& g, int units) {
-        const uint32_t mine = __ballot_sync(0xffffffffu, x >= g.unit0 && x < g.unit0 + units);
-        if (!mine) return false;
-        const int src = __ffs(mine) - 1;
-        grp.unit0 = __shfl_sync(0xffffffffu, g.unit0, src);
-        grp.row0 = __shfl_sync(0xffffffffu, g.row0, src);
-        grp.seq0 = __shfl_sync(0xffffffffu, g.seq0, src);
-        grp.rows = __shfl_sync(0xffffffffu, g.rows, src);
-        grp.tiles = __shfl_sync(0xffffffffu, g.tiles, src);
-        grp.chunks = __shfl_sync(0xffffffffu, g.chunks, src);
-        grp.blocks = __shfl_sync(0xffffffffu, g.blocks, src);
-        return true;
-    });
-    if (grp.chunks == 0) return;  // more CTAs than units
-    // The member whose table row names the blocks.
-    int lead = -1;
-    for (int s0 = 0; s0 * G < grp.rows && lead < 0; s0 += 32) {
-        const int s = grp.seq0 + s0 + lane;
-        const uint32_t in = __ballot_sync(0xffffffffu, (s0 + lane) * G < grp.rows && a.context_lens[s] / a.block_size >= grp.blocks);
-        if (in) lead = grp.seq0 + s0 + __ffs(in) - 1;
-    }
-    if (lead < 0) return;  // every sequence of the group is shorter
+    if (units.W == 0 || cta >= units.P) return;
+    const int start = mul_div(cta, units.W, units.P), end = mul_div(cta + 1, units.W, units.P);
     // The swizzled layouts need a 1024-byte aligned base.
     if (smem_addr(smem_raw) & 1023u) {
         if (tid == 0) raise_flag(a.status, kFlagBadPlan);
@@ -248,16 +300,6 @@ __global__ void __launch_bounds__(Shape<D, kFP8>::kThreads, Shape<D, kFP8>::kCta
     uint8_t* base = smem_raw;
     Bars* B = reinterpret_cast<Bars*>(base + S::kBarOff);
     volatile int* abort = &B->abort;
-    const int u = x - grp.unit0;
-    const int rt = u % grp.tiles;  // row tiles of a chunk side by side: they share its K and V in L2
-    const int c = (u / grp.tiles) % grp.chunks;
-    const int h = u / (grp.tiles * grp.chunks);
-    const int nkeys = grp.blocks * a.block_size;
-    const int key0 = c * per * kNK;
-    const int key1 = min(nkeys, key0 + per * kNK);
-    const int nkt = (key1 - key0 + kNK - 1) / kNK;
-    const int nrows = min(kBM, grp.rows - rt * kBM);
-
     if (tid == 0) {
         constexpr int arrivals = kFP8 ? S::kProducers : 32;  // one a producer warp, or one a copying lane
         for (int i = 0; i < S::kKRing; ++i) {
@@ -273,312 +315,383 @@ __global__ void __launch_bounds__(Shape<D, kFP8>::kThreads, Shape<D, kFP8>::kCta
             mbar_init(&B->p_full[i], 4);
             mbar_init(&B->pv_done[i], 1);
         }
+        mbar_init(&B->q_full, 4);
         B->abort = 0;
         fence_barrier_init();
     }
     if (warp == 0) tc_alloc(&B->tmem, kTmemCols);
-    // Query row r of the tile: member (rt * 128 + r) / G, query head h * G + r % G.
-    auto q_row = [&](int r) {
-        const int rr = rt * kBM + min(r, nrows - 1);
-        return (static_cast<int64_t>(grp.seq0 + rr / G) * a.num_q_heads + h * G + rr % G);
-    };
-    if (warp < 4) {  // Q rows into shared memory, 128-byte swizzled K-major
-        const int r = tid;
-        const T* qrow = static_cast<const T*>(a.q) + q_row(r) * D;
-        // A negative scale is applied as |scale| to the scores of -q (a sign
-        // flip is exact), so the row maximum is taken on unscaled scores.
-        const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-#pragma unroll
-        for (int q16 = 0; q16 < D / 8; ++q16) {
-            uint4 v = *reinterpret_cast<const uint4*>(qrow + 8 * q16);
-            v.x ^= flip;
-            v.y ^= flip;
-            v.z ^= flip;
-            v.w ^= flip;
-            *reinterpret_cast<uint4*>(base + S::kQOff + (q16 >> 3) * (kBM * 128) + r * 128 +
-                                      (((q16 & 7) ^ (r & 7)) << 4)) = v;
-        }
-        fence_proxy_async_smem();
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t taddr = B->tmem;
 
+    // Every role walks the CTA's segments; tiles are counted from the CTA's
+    // first (i), so rings and buffers go on over segments.
     if (warp >= 5) {
         // ---- producers: K of tile i, then V of tile i - 1 (K runs one tile
         // ahead: S of a tile is issued before its PV).  The keys come in runs
         // of 16 (block_size is a multiple of 16), each inside one block; runs
         // past the last key are zeros.
         const int bs = a.block_size;
-        const int32_t* table = a.block_tables + static_cast<int64_t>(lead) * a.max_blocks;
-        const int nruns = (key1 - key0) / 16;
-        // Element offset of run r's first row, in rows of the cache.
-        auto run_row = [&](int r) -> int64_t {
-            const int key = key0 + 16 * min(r, nruns - 1);
-            const int lb = key / bs;
-            int blk = table[lb];
-            if (blk < 0 || blk >= a.num_blocks) {
-                raise_flag(a.status, kFlagBadBlock);
-                blk = 0;
+        const int ch = lane & 7, l8 = lane >> 3;
+        int i = 0;  // K tiles asked for so far
+        bool ok = true;
+        [[maybe_unused]] const uint32_t sw0 = static_cast<uint32_t>(ch ^ l8) << 4, sw1 = static_cast<uint32_t>(ch ^ (l8 + 4)) << 4;
+        for (int x = start; x < end && ok;) {
+            const Triple t = find_triple(a, units, G, x);
+            const int n = min(end, t.tile0 + t.keys) - x;  // tiles of the segment
+            const int key0 = (x - t.tile0) * kNK;
+            const int nruns = (min(t.blocks * bs, key0 + n * kNK) - key0) / 16;
+            // The member whose table row names the blocks; without one the
+            // segment's keys are zeros and nobody reads its part.
+            int lead = -1;
+            for (int s0 = 0; s0 * G < t.rows && lead < 0; s0 += 32) {
+                const int s = t.seq0 + s0 + lane;
+                const uint32_t in = __ballot_sync(0xffffffffu, (s0 + lane) * G < t.rows && a.context_lens[s] / bs >= t.blocks);
+                if (in) lead = t.seq0 + s0 + __ffs(in) - 1;
             }
-            return (static_cast<int64_t>(blk) * a.num_kv_heads + h) * bs + (key - lb * bs);
-        };
-        if constexpr (!kFP8) {
-            // Lane l knows where run l of the current 8 tiles starts, and of
-            // the 8 after them.
-            int64_t now = run_row(lane), next = run_row(32 + lane), before = now;
-            const int ch = lane & 7, l8 = lane >> 3;
-            const uint32_t sw0 = static_cast<uint32_t>(ch ^ l8) << 4, sw1 = static_cast<uint32_t>(ch ^ (l8 + 4)) << 4;
-            // Lane e copies chunk e % 8 of rows e / 8 + 4 q of a run.
-            auto load = [&](int j, int64_t rows, const void* cache, uint32_t dst, uint64_t* bar) {
-                const char* c0 = static_cast<const char*>(cache) + l8 * (D * 2) + ch * 16;
+            const int32_t* table = a.block_tables + static_cast<int64_t>(lead < 0 ? 0 : lead) * a.max_blocks;
+            // First cache row of run r of the segment; -1: zeros.
+            auto run_row = [&](int r) -> int64_t {
+                if (r >= nruns || lead < 0) return -1;
+                const int key = key0 + 16 * r;
+                const int lb = key / bs;
+                int blk = table[lb];
+                if (blk < 0 || blk >= a.num_blocks) {
+                    raise_flag(a.status, kFlagBadBlock);
+                    blk = 0;
+                }
+                return (static_cast<int64_t>(blk) * a.num_kv_heads + t.h) * bs + (key - lb * bs);
+            };
+            if constexpr (!kFP8) {
+                // Lane l knows where run l of the current 8 tiles starts, and
+                // of the 8 after them.
+                int64_t now = run_row(lane), next = run_row(32 + lane);
+                // Lane e copies chunk e % 8 of rows e / 8 + 4 q of a run.
+                auto load = [&](int j, int64_t rows, const void* cache, uint32_t dst, uint64_t* bar) {
+                    const char* c0 = static_cast<const char*>(cache) + l8 * (D * 2) + ch * 16;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t row = __shfl_sync(0xffffffffu, rows, (j & 7) * 4 + i);
-                    const bool real = 4 * j + i < nruns;
-                    const char* src = c0 + row * (D * 2);
+                    for (int k = 0; k < 4; ++k) {
+                        const int64_t row = __shfl_sync(0xffffffffu, rows, (j & 7) * 4 + k);
+                        const bool real = row >= 0;
+                        const char* src = c0 + (real ? row : 0) * (D * 2);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t d = dst + (16 * k + 4 * q + l8) * 128 + ((q & 1) ? sw1 : sw0);
+#pragma unroll
+                            for (int sl = 0; sl < S::kSlices; ++sl)
+                                cp_async_16_or_zero(d + sl * (kNK * 128), src + (real ? q * (4 * D * 2) + sl * 128 : 0), real);
+                        }
+                    }
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+                };
+                int64_t before = now;
+                for (int j = 0; j <= n && ok; ++j) {
+                    if (j < n) {
+                        const int st = (i + j) % S::kKRing;
+                        if ((j & 7) == 0 && j > 0) {
+                            before = now;
+                            now = next;
+                            next = run_row(4 * (j + 8) + lane);
+                        }
+                        if (i + j >= S::kKRing)
+                            ok = __all_sync(0xffffffffu, wait(&B->kempty[st], (i + j) / S::kKRing - 1, abort, a.status));
+                        if (!ok) break;
+                        load(j, now, a.k_cache, smem_addr(base + S::kKOff + st * S::kTile), &B->kfull[st]);
+                    }
+                    if (j >= 1) {
+                        const int v = i + j - 1, st = v % S::kVRing;
+                        if (v >= S::kVRing)
+                            ok = __all_sync(0xffffffffu, wait(&B->vempty[st], v / S::kVRing - 1, abort, a.status));
+                        if (!ok) break;
+                        load(j - 1, (j & 7) == 0 && j < n ? before : now, a.v_cache,
+                             smem_addr(base + S::kVOff + st * S::kTile), &B->vfull[st]);
+                    }
+                }
+            } else {
+                // E4M3: warp w brings run w of every tile: its codes travel
+                // through a ring of its own (asynchronous copies, each lane
+                // reading back what it copied) and are widened into the tile.
+                // Lane e takes codes 16 (e % 8) .. of rows e / 8 + 4 q.
+                const int w = warp - 5;
+                const uint32_t raw0 = smem_addr(base + S::kRawOff + w * (S::kRawRing * S::kRawStage)) + lane * 16;
+                int64_t rows = -1;  // lane l: run w of tile l of the current 32
+                auto ask = [&](int j) {
+                    if ((j & 31) == 0) rows = run_row(4 * (j + lane) + w);
+                    const int64_t row = __shfl_sync(0xffffffffu, rows, j & 31);
+                    if (j < n) {
+                        const bool real = row >= 0;
+                        const int64_t off = real ? (row + l8) * D + ch * 16 : 0;
+                        const uint32_t d = raw0 + (j % S::kRawRing) * S::kRawStage;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            cp_async_16_or_zero(d + q * 512, static_cast<const char*>(a.k_cache) + off + (real ? q * 4 * D : 0), real);
+                            cp_async_16_or_zero(d + 2048 + q * 512, static_cast<const char*>(a.v_cache) + off + (real ? q * 4 * D : 0), real);
+                        }
+                    }
+                    asm volatile("cp.async.commit_group;" ::: "memory");  // an empty group past the end
+                };
+                auto put = [&](uint32_t raw, uint32_t off, uint64_t* bar) {
+                    uint8_t* tile = base + off + (ch >> 2) * (kNK * 128);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const uint32_t d = dst + (16 * i + 4 * q + l8) * 128 + ((q & 1) ? sw1 : sw0);
-#pragma unroll
-                        for (int sl = 0; sl < S::kSlices; ++sl)
-                            cp_async_16_or_zero(d + sl * (kNK * 128), src + q * (4 * D * 2) + sl * 128, real);
+                        uint4 r;
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                                     : "r"(raw + q * 512)
+                                     : "memory");
+                        const int row = 16 * w + 4 * q + l8;
+                        const int c0 = (ch & 3) * 2;
+                        *reinterpret_cast<uint4*>(tile + row * 128 + ((c0 ^ (row & 7)) << 4)) = widen8(r.x, r.y);
+                        *reinterpret_cast<uint4*>(tile + row * 128 + (((c0 + 1) ^ (row & 7)) << 4)) = widen8(r.z, r.w);
                     }
-                }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
-            };
-            for (int i = 0; i <= nkt; ++i) {
-                if (i < nkt) {
-                    const int st = i % S::kKRing;
-                    if ((i & 7) == 0 && i > 0) {
-                        before = now;
-                        now = next;
-                        next = run_row(4 * (i + 8) + lane);
-                    }
-                    if (i >= S::kKRing &&
-                        !__all_sync(0xffffffffu, wait(&B->kempty[st], i / S::kKRing - 1, abort, a.status)))
-                        break;
-                    load(i, now, a.k_cache, smem_addr(base + S::kKOff + st * S::kTile), &B->kfull[st]);
-                }
-                if (i >= 1) {
-                    const int j = i - 1, st = j % S::kVRing;
-                    if (j >= S::kVRing &&
-                        !__all_sync(0xffffffffu, wait(&B->vempty[st], j / S::kVRing - 1, abort, a.status)))
-                        break;
-                    load(j, (i & 7) == 0 && i < nkt ? before : now, a.v_cache, smem_addr(base + S::kVOff + st * S::kTile),
-                         &B->vfull[st]);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar);
+                };
+                for (int j = 0; j < S::kRawRing - 1; ++j) ask(j);
+                for (int j = 0; j < n && ok; ++j) {
+                    ask(j + S::kRawRing - 1);
+                    asm volatile("cp.async.wait_group %0;" ::"n"(S::kRawRing - 1) : "memory");  // tile j is here
+                    const uint32_t raw = raw0 + (j % S::kRawRing) * S::kRawStage;
+                    const int sk = (i + j) % S::kKRing, sv = (i + j) % S::kVRing;
+                    if (i + j >= S::kKRing)
+                        ok = __all_sync(0xffffffffu, wait(&B->kempty[sk], (i + j) / S::kKRing - 1, abort, a.status));
+                    if (!ok) break;
+                    put(raw, S::kKOff + sk * S::kTile, &B->kfull[sk]);
+                    if (i + j >= S::kVRing)
+                        ok = __all_sync(0xffffffffu, wait(&B->vempty[sv], (i + j) / S::kVRing - 1, abort, a.status));
+                    if (!ok) break;
+                    put(raw + 2048, S::kVOff + sv * S::kTile, &B->vfull[sv]);
                 }
             }
-            // Every copy issued must land before the CTA can exit.
-            asm volatile("cp.async.wait_all;" ::: "memory");
-        } else {
-            // E4M3: warp w widens run w of every tile, exactly, to q's type.
-            // Lane e takes codes 16 (e % 8) .. of rows e / 8 + 4 q; the codes
-            // of the next tile are loaded before this one's are stored.
-            const int w = warp - 5;
-            const int ch = lane & 7, l8 = lane >> 3;
-            uint4 kr[2][4], vr[2][4];
-            auto fetch = [&](int j, uint4 (&kk)[4], uint4 (&vv)[4]) {
-                if (j >= nkt) return;
-                const bool real = 4 * j + w < nruns;
-                const int64_t off = (run_row(4 * j + w) + l8) * D + ch * 16;
-                const char* ks = static_cast<const char*>(a.k_cache) + off;
-                const char* vs = static_cast<const char*>(a.v_cache) + off;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    kk[q] = real ? __ldg(reinterpret_cast<const uint4*>(ks + q * 4 * D)) : make_uint4(0, 0, 0, 0);
-                    vv[q] = real ? __ldg(reinterpret_cast<const uint4*>(vs + q * 4 * D)) : make_uint4(0, 0, 0, 0);
-                }
-            };
-            auto put = [&](const uint4 (&r)[4], uint32_t off, uint64_t* bar) {
-                uint8_t* t = base + off + (ch >> 2) * (kNK * 128);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int row = 16 * w + 4 * q + l8;
-                    const int c0 = (ch & 3) * 2;
-                    *reinterpret_cast<uint4*>(t + row * 128 + ((c0 ^ (row & 7)) << 4)) = widen8<DT>(r[q].x, r[q].y);
-                    *reinterpret_cast<uint4*>(t + row * 128 + (((c0 + 1) ^ (row & 7)) << 4)) = widen8<DT>(r[q].z, r[q].w);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar);
-            };
-            fetch(0, kr[0], vr[0]);
-            bool ok = true;
-            for (int i0 = 0; i0 < nkt && ok; i0 += 2) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int i = i0 + k;
-                    if (i >= nkt || !ok) continue;
-                    fetch(i + 1, kr[k ^ 1], vr[k ^ 1]);
-                    const int sk = i % S::kKRing, sv = i % S::kVRing;
-                    if (i >= S::kKRing)
-                        ok = __all_sync(0xffffffffu, wait(&B->kempty[sk], i / S::kKRing - 1, abort, a.status));
-                    if (!ok) continue;
-                    put(kr[k], S::kKOff + sk * S::kTile, &B->kfull[sk]);
-                    if (i >= S::kVRing)
-                        ok = __all_sync(0xffffffffu, wait(&B->vempty[sv], i / S::kVRing - 1, abort, a.status));
-                    if (!ok) continue;
-                    put(vr[k], S::kVOff + sv * S::kTile, &B->vfull[sv]);
-                }
-            }
+            i += n;
+            x += n;
         }
+        // Every copy issued must land before the CTA can exit.
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
     } else if (warp == 4) {
-        // ---- MMA issue (one lane)
-        if (lane == 0) {
-            constexpr int bf = DT == kBF16 ? 1 : 0;
-            constexpr uint32_t idS = tc_idesc_f16(bf, false, kNK, kBM);
-            constexpr uint32_t idPV = tc_idesc_f16(bf, true, D, kBM);
-            const uint32_t qa = smem_addr(base + S::kQOff);
-            auto pv = [&](int t) -> bool {
-                const int sv = t % S::kVRing, bt = t & 1;
-                if (!wait(&B->p_full[bt], t >> 1, abort, a.status)) return false;
-                if (!wait(&B->vfull[sv], t / S::kVRing, abort, a.status)) return false;
-                if constexpr (!kFP8) fence_proxy_async_smem();  // lane copies before the tensor cores read them
-                tc_fence_after();
-                const uint32_t va = smem_addr(base + S::kVOff + sv * S::kTile);
+        // ---- MMA issue (one lane; the others only look segments up)
+        constexpr int bf = DT == kBF16 ? 1 : 0;
+        constexpr uint32_t idS = tc_idesc_f16(bf, false, kNK, kBM);
+        constexpr uint32_t idPV = tc_idesc_f16(bf, true, D, kBM);
+        const uint32_t qa = smem_addr(base + S::kQOff);
+        auto pv = [&](int i, bool first) -> bool {
+            const int sv = i % S::kVRing, bt = i & 1;
+            if (!wait(&B->p_full[bt], i >> 1, abort, a.status)) return false;
+            if (!wait(&B->vfull[sv], i / S::kVRing, abort, a.status)) return false;
+            if constexpr (!kFP8) fence_proxy_async_smem();  // lane copies before the tensor cores read them
+            tc_fence_after();
+            const uint32_t va = smem_addr(base + S::kVOff + sv * S::kTile);
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
+            for (int part = 0; part < 2; ++part)
 #pragma unroll
-                    for (int kk = 0; kk < kNK / 16; ++kk)
-                        tc_mma_ts(taddr + 128, taddr + bt * kNK + part * 32 + kk * 8,
-                                  tc_sdesc(va + kk * 16 * 128, kNK * 128, 1024), idPV,
-                                  !(t == 0 && part == 0 && kk == 0));
-                tc_commit(&B->pv_done[bt]);
-                tc_commit(&B->vempty[sv]);
-                return true;
-            };
-            bool ok = true;
-            for (int j = 0; j < nkt && ok; ++j) {
-                const int sk = j % S::kKRing, b = j & 1;
-                ok = wait(&B->kfull[sk], j / S::kKRing, abort, a.status);
-                // S buffer b holds P of tile j - 2 until that PV has completed.
-                if (ok && j >= 2) ok = wait(&B->pv_done[b], (j >> 1) - 1, abort, a.status);
-                if (!ok) break;
-                if constexpr (!kFP8) fence_proxy_async_smem();
-                tc_fence_after();
-                const uint32_t ka = smem_addr(base + S::kKOff + sk * S::kTile);
+                for (int kk = 0; kk < kNK / 16; ++kk)
+                    tc_mma_ts(taddr + 128, taddr + bt * kNK + part * 32 + kk * 8,
+                              tc_sdesc(va + kk * 16 * 128, kNK * 128, 1024), idPV, !(first && part == 0 && kk == 0));
+            tc_commit(&B->pv_done[bt]);
+            tc_commit(&B->vempty[sv]);
+            return true;
+        };
+        int i = 0, seg = 0;
+        bool ok = true;
+        for (int x = start; x < end && ok; ++seg) {
+            const Triple t = find_triple(a, units, G, x);
+            const int n = min(end, t.tile0 + t.keys) - x;
+            if (lane == 0) {
+                ok = wait(&B->q_full, seg, abort, a.status);
+                for (int j = 0; j < n && ok; ++j) {
+                    const int k = i + j, sk = k % S::kKRing, b = k & 1;
+                    ok = wait(&B->kfull[sk], k / S::kKRing, abort, a.status);
+                    // S buffer b holds P of tile k - 2 until that PV has completed.
+                    if (ok && k >= 2) ok = wait(&B->pv_done[b], (k >> 1) - 1, abort, a.status);
+                    if (!ok) break;
+                    if constexpr (!kFP8) fence_proxy_async_smem();
+                    tc_fence_after();
+                    const uint32_t ka = smem_addr(base + S::kKOff + sk * S::kTile);
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    tc_mma(taddr + b * kNK, tc_sdesc(qa + (ks >> 2) * (kBM * 128) + (ks & 3) * 32, 16, 1024),
-                           tc_sdesc(ka + (ks >> 2) * (kNK * 128) + (ks & 3) * 32, 16, 1024), idS, ks > 0);
-                tc_commit(&B->s_full[b]);
-                tc_commit(&B->kempty[sk]);
-                if (j >= 1) ok = pv(j - 1);
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        tc_mma(taddr + b * kNK, tc_sdesc(qa + (ks >> 2) * (kBM * 128) + (ks & 3) * 32, 16, 1024),
+                               tc_sdesc(ka + (ks >> 2) * (kNK * 128) + (ks & 3) * 32, 16, 1024), idS, ks > 0);
+                    tc_commit(&B->s_full[b]);
+                    tc_commit(&B->kempty[sk]);
+                    if (j >= 1) ok = pv(k - 1, j == 1);
+                }
+                if (ok) ok = pv(i + n - 1, n == 1);
             }
-            if (ok) pv(nkt - 1);
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            i += n;
+            x += n;
         }
-        __syncwarp();
     } else {
         // ---- softmax: thread r owns row r (tensor-memory lane r)
         const int r = tid;
         const uint32_t lane_base = taddr + (static_cast<uint32_t>(32 * warp) << 16);
-        float m_ref = 0.f, l = 0.f;
         // |scale| in log2 units; a zero scale is taken as 1e-30, which leaves
         // every finite score's exponent at 0 while masked scores stay -inf.
-        const float sc = fmaxf(fabsf(a.scale_log2), 1e-30f);
+        const float sc0 = fmaxf(fabsf(a.scale_log2), 1e-30f) * (kFP8 ? 256.f : 1.f);  // widened codes are 2^-8 of the value
+        int i = 0;
         bool ok = true;
-        for (int j = 0; j < nkt && ok; ++j) {
-            const int b = j & 1;
-            ok = __all_sync(0xffffffffu, wait(&B->s_full[b], j >> 1, abort, a.status));
-            if (!ok) break;
-            tc_fence_after();
-            float sv[kNK];
+        for (int x = start; x < end && ok;) {
+            const Triple t = find_triple(a, units, G, x);
+            const int n = min(end, t.tile0 + t.keys) - x;
+            const int nrows = min(kBM, t.rows - t.rt * kBM);
+            const int keys = min(t.blocks * a.block_size - (x - t.tile0) * kNK, n * kNK);  // of the segment
+            float sc = sc0;
             {
-                float t0[32], t1[32];
-                tc_ld32(lane_base + b * kNK, t0);
-                tc_ld32(lane_base + b * kNK + 32, t1);
-                tc_wait_ld();
+                // Q row r of the tile (member (rt * 128 + r) / G, query head
+                // h * G + r % G) into shared memory, 128-byte swizzled K-major.
+                // (The previous segment's S are complete: their last was read.)
+                const int rr = t.rt * kBM + min(r, nrows - 1);
+                const T* qrow = static_cast<const T*>(a.q) +
+                                (static_cast<int64_t>(t.seq0 + rr / G) * a.num_q_heads + t.h * G + rr % G) * D;
+                // A negative scale is applied as |scale| to the scores of -q (a
+                // sign flip is exact), so the row maximum is taken on unscaled
+                // scores.
+                const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+                float up = 1.f;
+                if constexpr (kFP8 && QT == kBF16) {
+                    uint32_t top = 0;  // largest |q|, as the bits of a bf16
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    sv[k] = t0[k];
-                    sv[32 + k] = t1[k];
+                    for (int q16 = 0; q16 < D / 8; ++q16) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(qrow + 8 * q16);
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+                    }
+                    const int e = min(max(static_cast<int>(top >> 7) - 127, -100), 127);  // its exponent
+                    up = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
+                    sc *= __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
                 }
+#pragma unroll
+                for (int q16 = 0; q16 < D / 8; ++q16) {
+                    uint4 v = *reinterpret_cast<const uint4*>(qrow + 8 * q16);
+                    if constexpr (kFP8 && QT == kBF16) {
+                        uint32_t* w = &v.x;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const __half2 h = __floats2half2_rn(__uint_as_float(w[k] << 16) * up,
+                                                                __uint_as_float(w[k] & 0xFFFF0000u) * up);
+                            w[k] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                    }
+                    v.x ^= flip;
+                    v.y ^= flip;
+                    v.z ^= flip;
+                    v.w ^= flip;
+                    *reinterpret_cast<uint4*>(base + S::kQOff + (q16 >> 3) * (kBM * 128) + r * 128 +
+                                              (((q16 & 7) ^ (r & 7)) << 4)) = v;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B->q_full);  // one arrival per warp (count 4)
             }
-            const int left = key1 - key0 - j * kNK;  // keys from this tile on
-            if (left < kNK) {
-#pragma unroll
-                for (int k = 0; k < kNK; ++k) sv[k] = k < left ? sv[k] : -INFINITY;
-            }
-            // Row maximum as eight independent chains (short dependency path).
-            float mx[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) mx[k] = sv[k];
-#pragma unroll
-            for (int k = 8; k < kNK; ++k) mx[k & 7] = fmaxf(mx[k & 7], sv[k]);
-            // (The lower limit keeps the exponents of a row whose scores are
-            // all -inf so far at -inf, not NaN.)
-            const float mt = fmaxf(fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                         fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sc,
-                                   -1e30f);
-            bool need = false;
-            if (j == 0)
-                m_ref = mt;
-            else
-                need = mt > m_ref + kLazy;
-            if (__any_sync(0xffffffffu, need)) {
-                // O must be complete up to tile j-1 before it is rescaled.
-                ok = __all_sync(0xffffffffu, wait(&B->pv_done[(j - 1) & 1], (j - 1) >> 1, abort, a.status));
+            float m_ref = 0.f, l = 0.f;
+            for (int j = 0; j < n && ok; ++j) {
+                const int k0 = i + j, b = k0 & 1;
+                ok = __all_sync(0xffffffffu, wait(&B->s_full[b], k0 >> 1, abort, a.status));
                 if (!ok) break;
                 tc_fence_after();
-                const float f = need ? fast_exp2(m_ref - mt) : 1.f;
-                if (need) {
-                    l *= f;
-                    m_ref = mt;
+                float sv[kNK];
+                {
+                    float t0[32], t1[32];
+                    tc_ld32(lane_base + b * kNK, t0);
+                    tc_ld32(lane_base + b * kNK + 32, t1);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        sv[k] = t0[k];
+                        sv[32 + k] = t1[k];
+                    }
                 }
+                const int left = keys - j * kNK;  // keys from this tile on
+                if (left < kNK) {
+#pragma unroll
+                    for (int k = 0; k < kNK; ++k) sv[k] = k < left ? sv[k] : -INFINITY;
+                }
+                // Row maximum as eight independent chains (short dependency path).
+                float mx[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mx[k] = sv[k];
+#pragma unroll
+                for (int k = 8; k < kNK; ++k) mx[k & 7] = fmaxf(mx[k & 7], sv[k]);
+                // (The lower limit keeps the exponents of a row whose scores
+                // are all -inf so far at -inf, not NaN.)
+                const float mt = fmaxf(fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                             fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sc,
+                                       -1e30f);
+                bool need = false;
+                if (j == 0)
+                    m_ref = mt;
+                else
+                    need = mt > m_ref + kLazy;
+                if (__any_sync(0xffffffffu, need)) {
+                    // O must be complete up to the tile before it is rescaled.
+                    ok = __all_sync(0xffffffffu, wait(&B->pv_done[(k0 - 1) & 1], (k0 - 1) >> 1, abort, a.status));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const float f = need ? fast_exp2(m_ref - mt) : 1.f;
+                    if (need) {
+                        l *= f;
+                        m_ref = mt;
+                    }
+#pragma unroll
+                    for (int cb = 0; cb < D / 32; ++cb) {
+                        float o[32];
+                        tc_ld32(lane_base + 128 + 32 * cb, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] *= f;
+                        tc_st32(lane_base + 128 + 32 * cb, o);
+                    }
+                    tc_wait_st();
+                }
+                // P over the S buffer it came from: columns 0-31 the high part,
+                // 32-63 the low part, keys 2k and 2k + 1 in column k.
+                float ps[4] = {0.f, 0.f, 0.f, 0.f};
+                {
+                    uint32_t ph[32], pl[32];
+#pragma unroll
+                    for (int k = 0; k < kNK / 2; ++k) {
+                        const float p0 = fast_exp2(fmaf(sv[2 * k], sc, -m_ref));
+                        const float p1 = fast_exp2(fmaf(sv[2 * k + 1], sc, -m_ref));
+                        ps[k & 3] += p0 + p1;
+                        pack_split<DT>(p0, p1, ph[k], pl[k]);
+                    }
+                    tc_st32u(lane_base + b * kNK, ph);
+                    tc_st32u(lane_base + b * kNK + 32, pl);
+                }
+                l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B->p_full[b]);  // one arrival per warp (count 4)
+            }
+            i += n;
+            if (ok) ok = __all_sync(0xffffffffu, wait(&B->pv_done[(i - 1) & 1], (i - 1) >> 1, abort, a.status));
+            if (ok) {
+                tc_fence_after();
+                const float vs = a.v_scale * (kFP8 ? 256.f : 1.f);
+                const int64_t row = t.row0 + static_cast<int64_t>(cta - cta_of_tile(t.tile0, units.W, units.P)) * t.stride + r;
+                const bool row_ok = r < nrows && row < a.max_rows;
+                float* po = a.part_o + row * D;
 #pragma unroll
                 for (int cb = 0; cb < D / 32; ++cb) {
                     float o[32];
                     tc_ld32(lane_base + 128 + 32 * cb, o);
                     tc_wait_ld();
+                    if (row_ok) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] *= f;
-                    tc_st32(lane_base + 128 + 32 * cb, o);
+                        for (int k = 0; k < 32; ++k) o[k] *= vs;
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) store_32(po + 32 * cb + k, o + k);
+                    }
                 }
-                tc_wait_st();
+                if (row_ok) *reinterpret_cast<float2*>(a.part_ml + 2 * row) = make_float2(m_ref, l);
+                tc_fence_before();  // before the next segment's P, and its PV, are announced
             }
-            // P over the S buffer it came from: columns 0-31 the high part,
-            // 32-63 the low part, keys 2k and 2k + 1 in column k.
-            float ps[4] = {0.f, 0.f, 0.f, 0.f};
-            {
-                uint32_t ph[32], pl[32];
-#pragma unroll
-                for (int k = 0; k < kNK / 2; ++k) {
-                    const float p0 = fast_exp2(fmaf(sv[2 * k], sc, -m_ref));
-                    const float p1 = fast_exp2(fmaf(sv[2 * k + 1], sc, -m_ref));
-                    ps[k & 3] += p0 + p1;
-                    pack_split<DT>(p0, p1, ph[k], pl[k]);
-                }
-                tc_st32u(lane_base + b * kNK, ph);
-                tc_st32u(lane_base + b * kNK + 32, pl);
-            }
-            l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&B->p_full[b]);  // one arrival per warp (count 4)
-        }
-        if (__all_sync(0xffffffffu, ok && !*abort)) {
-            ok = __all_sync(0xffffffffu, wait(&B->pv_done[(nkt - 1) & 1], (nkt - 1) >> 1, abort, a.status));
-            tc_fence_after();
-            const int64_t row = grp.row0 + (static_cast<int64_t>(h) * grp.chunks + c) * grp.rows + rt * kBM + r;
-            const bool row_ok = ok && r < nrows && row < a.max_rows;
-            float* po = a.part_o + row * D;
-#pragma unroll
-            for (int cb = 0; cb < D / 32; ++cb) {
-                float o[32];
-                tc_ld32(lane_base + 128 + 32 * cb, o);
-                tc_wait_ld();
-                if (row_ok) {
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4)
-                        *reinterpret_cast<float4*>(po + 32 * cb + k) =
-                            make_float4(o[k] * a.v_scale, o[k + 1] * a.v_scale, o[k + 2] * a.v_scale, o[k + 3] * a.v_scale);
-                }
-            }
-            if (row_ok) *reinterpret_cast<float2*>(a.part_ml + 2 * row) = make_float2(m_ref, l);
+            x += n;
         }
     }
     tc_fence_before();
@@ -606,18 +719,12 @@ __global__ void __launch_bounds__(128) shared_prefix_merge_kernel(const SharedPr
     const int hq = static_cast<int>(row - static_cast<int64_t>(s) * a.num_q_heads);
     const int G = a.num_q_heads / a.num_kv_heads;
     const int h = hq / G, g = hq - h * G;
-    const PrefixParts pp = a.num_groups > 0 ? a.parts[s] : PrefixParts{0, 0, 0, 0};
-    // The tail's parts: the CTAs that hold its blocks (see decode_plan.cu).
     const int Hc = d.heads_per_stage, chunks = d.num_kv_heads / Hc;
     const int hc = h / Hc, hw = h - hc * Hc;
-    const int items = (d.cum[s + 1] - d.cum[s]) / chunks;
-    const int nb = items > 0 ? items - d.phantom : 0;
-    const int64_t W = d.cum[d.num_seqs], P = d.num_ctas;
-    const int64_t first = d.cum[s] + static_cast<int64_t>(hc) * items + d.phantom;
-    const int ca = nb > 0 ? cta_of_item(first, W, d.num_ctas) : 0;
-    const int cb = nb > 0 ? cta_of_item(first + nb - 1, W, d.num_ctas) : -1;
     const int pair = s * chunks + hc;
-    const int n = pp.parts + (cb - ca + 1);
+    const PrefixParts pp = a.parts[s * a.num_kv_heads + h];
+    const int4 tp = d.tail_parts[pair];
+    const int n = pp.parts + tp.y;
     float M = -INFINITY, L = 0.f, acc[VD];
 #pragma unroll
     for (int i = 0; i < VD; ++i) acc[i] = 0.f;
@@ -627,18 +734,17 @@ __global__ void __launch_bounds__(128) shared_prefix_merge_kernel(const SharedPr
         const float* po = nullptr;
         float2 ml = make_float2(-INFINITY, 0.f);
         if (p < pp.parts) {
-            const int64_t r = pp.row0 + static_cast<int64_t>(h) * pp.head_stride + static_cast<int64_t>(p) * pp.part_stride + g;
+            const int64_t r = pp.row0 + static_cast<int64_t>(p) * pp.stride + g;
             if (r < a.max_rows) {
                 po = a.part_o + r * D;
                 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + 2 * r));
             }
         } else if (p < n) {
-            const int64_t c = ca + (p - pp.parts);
-            if (!cta_is_empty(c, W, P)) {
-                const int64_t r = ((c + pair) * Hc + hw) * G + g;
-                po = d.part_o + r * D;
-                ml = __ldcg(reinterpret_cast<const float2*>(d.part_ml + 2 * r));
-            }
+            const int k = p - pp.parts;
+            const int64_t c = tp.w == 0 ? tp.x + k : cta_of_tile(tp.z + k, tp.w, d.num_ctas);
+            const int64_t r = ((c + pair) * Hc + hw) * G + g;
+            po = d.part_o + r * D;
+            ml = __ldcg(reinterpret_cast<const float2*>(d.part_ml + 2 * r));
         }
         const uint64_t addr = reinterpret_cast<uint64_t>(po);
         const int cnt = min(32, n - base);
@@ -702,7 +808,7 @@ cudaError_t launch_parts_t(const SharedPrefixArgs& a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         if (cacheable) configured[a.device].store(1);
     }
-    return launch_kernel(kern, dim3(a.max_units + 1), dim3(S::kThreads), static_cast<size_t>(a.smem_bytes), stream, true, a);
+    return launch_kernel(kern, dim3(a.num_sms * a.ctas_per_sm + 1), dim3(S::kThreads), static_cast<size_t>(a.smem_bytes), stream, true, a);
 }
 
 }  // namespace

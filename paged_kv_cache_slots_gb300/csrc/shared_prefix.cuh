@@ -5,23 +5,10 @@
 
 namespace pkv {
 
-// One group of sequences: its share of the parts kernel's units (CTAs with
-// work) and of the partial rows.
-struct PrefixGroup {
-    int unit0;   // first unit
-    int row0;    // first partial row
-    int seq0;    // first sequence
-    int rows;    // (sequences of the group) x (query heads per KV head)
-    int tiles;   // row tiles of 128
-    int chunks;  // pieces its keys are split into
-    int blocks;  // shared blocks
-    int index;
-};
-
-// Where the prefix parts of a sequence are: part c of KV head h, query head g
-// of it sits in partial row row0 + h * head_stride + c * part_stride + g.
+// Where the prefix parts of one (sequence, KV head) are: part k of query head g
+// of it sits in partial row row0 + k * stride + g.
 struct PrefixParts {
-    int row0, part_stride, head_stride, parts;
+    int row0, stride, parts, unused;
 };
 
 struct SharedPrefixArgs {
@@ -35,15 +22,14 @@ struct SharedPrefixArgs {
     void* out;
     uint32_t* status;
     // Workspace.
-    PrefixParts* parts;          // [B]
-    PrefixGroup* groups;         // [num_groups]
+    PrefixParts* parts;          // [B][Hkv]
     float* part_o;               // [max_rows][D]
     float* part_ml;              // [max_rows][2]
     int num_seqs, num_groups, num_blocks, max_blocks, num_q_heads, num_kv_heads, head_dim, block_size;
     int dtype, out_dtype, kv_dtype;
     float scale_log2, v_scale;
     int num_sms, ctas_per_sm;    // CTAs of the parts kernel that run at once
-    int max_units, max_rows;     // most units and partial rows
+    int max_rows;                // capacity of the partial rows
     int device, smem_bytes;
 };
 
