@@ -39,6 +39,7 @@
 #include <atomic>
 
 #include "device_utils.cuh"
+#include "prefix_units.cuh"
 
 namespace pkv {
 
@@ -108,48 +109,20 @@ __device__ __forceinline__ int clamp_context(const DecodeArgs& a, int s, bool fl
     return c;
 }
 
-// Whether the groups cut the sequences into runs in order (asked by the whole
-// CTA; flagged by the first).
-static __device__ bool groups_in_order(const int32_t* group_start, const int32_t* prefix_lens, int num_groups,
-                                       int num_seqs, uint32_t* status) {
-    int bad = 0;
-    for (int g = threadIdx.x; g < num_groups; g += blockDim.x) {
-        const int s0 = group_start[g], s1 = group_start[g + 1];
-        if (s0 < 0 || s1 > num_seqs || s0 > s1 || prefix_lens[g] < 0) bad = 1;
-    }
-    bad = __syncthreads_or(bad);
-    if (bad && threadIdx.x == 0 && blockIdx.x == 0) raise_flag(status, kFlagBadGroup);
-    return bad == 0;
-}
-
-// Blocks that sequence s, of ctx tokens, shares with its group: 0 if it is in
-// none, or ends inside them.  The groups are in order; *group receives its own.
-__device__ __forceinline__ int shared_blocks(const int32_t* group_start, const int32_t* prefix_lens, int num_groups,
-                                             int block_size, int s, int ctx, int* group) {
-    if (num_groups == 0) return 0;
-    int lo = 0, hi = num_groups;  // the last group that starts at or before s
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (group_start[mid] <= s)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    *group = lo;
-    const int n = prefix_lens[lo] / block_size;
-    return group_start[lo] <= s && s < group_start[lo + 1] && n <= ctx / block_size ? n : 0;
-}
-
 // cum[s] = chunks * sum_{s' < s, ctx_s' > 0} (ceil(ctx_s' / bs) + phantom);
 // cum[num_seqs] = W.  kTails: ctx is what follows skip[s] shared blocks.
+// Returns the CTAs that share the items (kTails: the SMs that the prefix's
+// parts leave; else the grid).
 template <bool kTails>
-static __device__ void build_prefix(const DecodeArgs& a, int chunks, int32_t* cum, int32_t* scan, int32_t* skip) {
-    int groups = 0;
-    int first_ctx = 0;  // of this thread's first sequence, asked for before the groups are looked at
+static __device__ int build_prefix(const DecodeArgs& a, int chunks, int32_t* cum, int32_t* scan, int32_t* skip) {
+    [[maybe_unused]] Units units;
+    [[maybe_unused]] int first_ctx = 0;  // of this thread's first sequence, asked for before the groups are looked at
     if constexpr (kTails) {
         if (threadIdx.x < a.num_seqs) first_ctx = clamp_context(a, threadIdx.x, blockIdx.x == 0);
-        if (groups_in_order(a.group_start, a.prefix_lens, a.num_groups, a.num_seqs, a.status)) groups = a.num_groups;
+        units = plan_units(a, a.num_q_heads / a.num_kv_heads);
+        if (units.bad && threadIdx.x == 0 && blockIdx.x == 0) raise_flag(a.status, kFlagBadGroup);
     }
+    [[maybe_unused]] int64_t tokens = 0;  // of this thread's sequences, after their shared blocks
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int nwarps = blockDim.x >> 5;
     int carry = 0;
@@ -160,10 +133,10 @@ static __device__ void build_prefix(const DecodeArgs& a, int chunks, int32_t* cu
             const int c = kTails && base == 0 ? first_ctx : clamp_context(a, s, blockIdx.x == 0);
             int nb = (c + a.block_size - 1) / a.block_size;
             if constexpr (kTails) {
-                int g;
-                const int sb = shared_blocks(a.group_start, a.prefix_lens, groups, a.block_size, s, c, &g);
+                const int sb = units.bad ? 0 : shared_blocks(a, s, c);
                 skip[s] = sb;
                 nb -= sb;
+                tokens += c - sb * a.block_size;
             }
             v = nb > 0 ? (nb + a.phantom) * chunks : 0;
         }
@@ -191,16 +164,29 @@ static __device__ void build_prefix(const DecodeArgs& a, int chunks, int32_t* cu
         __syncthreads();
     }
     if (tid == 0) cum[a.num_seqs] = carry;
+    int ctas = a.num_ctas;
+    if constexpr (kTails) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) tokens += __shfl_xor_sync(0xffffffffu, tokens, o);
+        int64_t* sums = reinterpret_cast<int64_t*>(scan);  // 16 warps at most
+        if (lane == 0) sums[wid] = tokens;
+        __syncthreads();
+        tokens = 0;
+        for (int w = 0; w < nwarps; ++w) tokens += sums[w];
+        divide_sms(a, tokens, &units);
+        ctas -= units.P;
+    }
     __syncthreads();
+    return ctas;
 }
 
 // Where the merge finds the parts that the tails' CTAs leave of a pair:
-// (first CTA, parts, -, -) when every CTA holds items, its parts in
-// consecutive CTAs; else (-, parts, item of the first, all items), part k in
+// (first CTA, parts, -, 0) when every CTA holds items, its parts in
+// consecutive CTAs; else (CTAs, parts, item of the first, all items), part k in
 // the CTA that owns item z + k.
 __device__ __forceinline__ int4 tail_parts_of(int pair_r, int blocks, int64_t W, int P) {
     if (blocks <= 0) return make_int4(0, 0, 0, 0);
-    if (W < P) return make_int4(0, blocks, pair_r, static_cast<int>(W));
+    if (W < P) return make_int4(P, blocks, pair_r, static_cast<int>(W));
     const int ca = cta_of_item(pair_r, W, P);
     return make_int4(ca, cta_of_item(pair_r + blocks - 1, W, P) - ca + 1, 0, 0);
 }
@@ -750,9 +736,12 @@ __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
     // launch finishes; everything else (q, the new rows, the workspace, the
     // outputs) is touched only after waiting for it.
     if (!kTails && !a.early_reads) pdl_wait();
-    build_prefix<kTails>(a, chunks, cum, scan, skip);  // ends with __syncthreads
+    const int P = build_prefix<kTails>(a, chunks, cum, scan, skip);  // ends with __syncthreads
     const int64_t W = cum[a.num_seqs];
-    const int P = a.num_ctas;
+    if (kTails && static_cast<int>(blockIdx.x) >= P) {
+        pdl_wait();
+        return;
+    }
     const int start = static_cast<int>(static_cast<int64_t>(blockIdx.x) * W / P);
     const int end = static_cast<int>((static_cast<int64_t>(blockIdx.x) + 1) * W / P);
     const int warp = tid >> 5, lane = tid & 31;
@@ -771,6 +760,9 @@ __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
             const int nbv = (cum[s + 1] - cum[s]) / chunks;
             a.tail_parts[p] = tail_parts_of(cum[s] + (p - s * chunks) * nbv + a.phantom, nbv - a.phantom, W, P);
         }
+        // Sequences without prefix parts (the parts kernel speaks for the others).
+        for (int p = blockIdx.x + P * wt; p < a.num_seqs * a.num_kv_heads; p += P * nwt)
+            if (skip[p / a.num_kv_heads] == 0) a.prefix_parts[p] = make_int4(0, 0, 0, 0);
     }
     if (!kTails && blockIdx.x == 0 && !a.fused_reduce) {
         for (int s = wt; s <= a.num_seqs; s += nwt) a.cum[s] = cum[s];
@@ -951,6 +943,7 @@ cudaError_t launch_partial(const DecodeArgs& a, const CUtensorMap& tmk, const CU
     if (!cacheable || configured[a.device].load() < a.smem_bytes) {
         cudaError_t e =
             cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, a.smem_bytes);
+        if (kTails && e == cudaSuccess) e = prefer_shared_memory(kern);
         if (e != cudaSuccess) return e;
         if (cacheable) configured[a.device].store(a.smem_bytes);
     }

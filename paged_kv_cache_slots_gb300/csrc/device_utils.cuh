@@ -285,6 +285,13 @@ __device__ __forceinline__ void store_out(void* out, int64_t idx, float v, int o
         static_cast<__nv_bfloat16*>(out)[idx] = __float2bfloat16_rn(v);
 }
 
+// Kernels that follow one another without a pause divide an SM's memory alike
+// (all of it shared): an SM divides anew only when it is empty.
+template <class Kernel>
+cudaError_t prefer_shared_memory(Kernel kernel) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+}
+
 // Launch `kernel` on `stream`, optionally as a programmatic dependent of the
 // previous launch in the stream (its prologue may overlap that launch's tail).
 template <typename... KArgs, typename... Args>

@@ -1087,18 +1087,17 @@ struct SharedWs {
     WsLayout d;
 };
 
-// target: parts CTAs that run at once; ctas: the tails kernel's grid.
-SharedWs shared_workspace(int B, int Hq, int Hkv, int D, int target, int ctas) {
+SharedWs shared_workspace(int B, int Hq, int Hkv, int D, int sms) {
     SharedWs w;
     // 128 rows for each CTA's share of the work, and two parts more of every
-    // row (see the units in shared_prefix.cu).
-    w.max_rows = static_cast<int>(int64_t{128} * target + 2 * static_cast<int64_t>(B) * Hq);
+    // row (see prefix_units.cuh).
+    w.max_rows = static_cast<int>(int64_t{128} * sms + 2 * static_cast<int64_t>(B) * Hq);
     w.parts = 0;
-    w.tails = align256(static_cast<size_t>(B) * Hkv * sizeof(PrefixParts));
+    w.tails = align256(static_cast<size_t>(B) * Hkv * sizeof(int4));
     w.part_o = w.tails + align256(static_cast<size_t>(B) * Hkv * sizeof(int4));
     w.part_ml = w.part_o + align256(static_cast<size_t>(w.max_rows) * D * 4);
     w.decode = w.part_ml + align256(static_cast<size_t>(w.max_rows) * 8);
-    w.d = workspace_layout(B, Hq, Hkv, D, ctas);
+    w.d = workspace_layout(B, Hq, Hkv, D, sms);
     w.total = w.decode + w.d.total;
     return w;
 }
@@ -1138,12 +1137,12 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
         return fail(KV_ERR_UNSUPPORTED, "out_dtype must be KV_F32 or the input dtype");
     if (!std::isfinite(scale)) return fail(KV_ERR_INVALID_ARG, "scale is not finite");
     if (static_cast<int64_t>(num_seqs) * num_kv_heads * max_blocks >= (int64_t{1} << 31) ||
-        static_cast<int64_t>(max_blocks) * block_size >= (int64_t{1} << 31) - kPrefixTile ||
+        static_cast<int64_t>(max_blocks) * block_size >= (int64_t{1} << 31) - 64 ||
         static_cast<int64_t>(num_blocks) * num_kv_heads * block_size >= (int64_t{1} << 31))
         return fail(KV_ERR_UNSUPPORTED, "sizes exceed 32-bit tile / row indices");
     // Key tiles of all rows of the prefix part, at most.
     if (((static_cast<int64_t>(num_seqs) * G / 128 + num_groups) * num_kv_heads) *
-            (static_cast<int64_t>(max_blocks) * block_size / kPrefixTile + 1) >= (int64_t{1} << 31))
+            (static_cast<int64_t>(max_blocks) * block_size / 64 + 1) >= (int64_t{1} << 31))
         return fail(KV_ERR_UNSUPPORTED, "%s: more than 2^31 tiles of work", what);
     if (num_seqs == 0) return KV_OK;
     if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out || !workspace ||
@@ -1158,8 +1157,7 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     int dev = 0, sms = 0, max_smem = 0;
     uint32_t* status = nullptr;
     if (kv_status_t st = device_info(&dev, &status, &sms, &max_smem, nullptr)) return st;
-    const int target = sms * prefix_ctas_per_sm(fp8), ctas = sms;
-    const SharedWs w = shared_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, target, ctas);
+    const SharedWs w = shared_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, sms);
     if (workspace_bytes < w.total)
         return fail(KV_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, w.total);
     // The tails: heads a stage as the decode kernel's default, up to 11 (its
@@ -1183,7 +1181,7 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     a.prefix_lens = prefix_lens;
     a.out = out;
     a.status = status;
-    a.parts = reinterpret_cast<PrefixParts*>(ws + w.parts);
+    a.parts = reinterpret_cast<int4*>(ws + w.parts);
     a.part_o = reinterpret_cast<float*>(ws + w.part_o);
     a.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
     a.num_seqs = num_seqs;
@@ -1200,8 +1198,7 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 *
                                       static_cast<double>(fp8 ? k_scale : 1.f));
     a.v_scale = fp8 ? v_scale : 1.f;
-    a.num_sms = sms;
-    a.ctas_per_sm = prefix_ctas_per_sm(fp8);
+    a.num_ctas = sms;
     a.max_rows = w.max_rows;
     a.device = dev;
     a.smem_bytes = prefix_smem_bytes(head_dim, fp8);
@@ -1217,6 +1214,7 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     d.prefix_lens = prefix_lens;
     d.num_groups = num_groups;
     d.tail_parts = reinterpret_cast<int4*>(ws + w.tails);
+    d.prefix_parts = a.parts;
     d.out = out;
     d.counters = reinterpret_cast<int32_t*>(ws + w.decode + w.d.counters);
     d.part_o = reinterpret_cast<float*>(ws + w.decode + w.d.part_o);
@@ -1236,7 +1234,7 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     d.k_scale = fp8 ? k_scale : 1.f;
     d.v_scale = a.v_scale;
     d.scale_log2 = a.scale_log2;
-    d.num_ctas = ctas;
+    d.num_ctas = sms;
     d.heads_per_stage = hc;
     d.warps_per_head = R;
     d.consumer_warps = hc * R;
@@ -1244,7 +1242,7 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     d.smem_bytes = plan.smem_bytes;
     d.fused_reduce = 0;
     d.pdl = 1;
-    d.phantom = phantom_items(num_seqs, num_kv_heads / hc, max_blocks, ctas, plan.stage_half_bytes);
+    d.phantom = phantom_items(num_seqs, num_kv_heads / hc, max_blocks, sms, plan.stage_half_bytes);
     d.device = dev;
     CUtensorMap tk, tv;
     const int rows = num_blocks * num_kv_heads * block_size;
@@ -1270,8 +1268,7 @@ kv_status_t paged_shared_prefix_workspace_bytes(int num_seqs, int num_groups, in
     if (!g.ok) return fail(KV_ERR_CUDA, "cannot select device %d", device);
     int sms = 0;
     if (kv_status_t st = device_info(nullptr, nullptr, &sms, nullptr, nullptr)) return st;
-    // The larger of the two cache kinds' needs.
-    *bytes = shared_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, sms * prefix_ctas_per_sm(false), sms).total;
+    *bytes = shared_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, sms).total;
     return KV_OK;
 }
 

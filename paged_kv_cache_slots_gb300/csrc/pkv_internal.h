@@ -134,6 +134,7 @@ struct DecodeArgs {
     const int32_t* prefix_lens;  // [num_groups]
     int num_groups;
     int4* tail_parts;            // [num_seqs][Hkv / heads_per_stage] written: see tail_parts_of
+    int4* prefix_parts;          // [num_seqs][Hkv] zeroed for sequences that share nothing
 };
 
 // Multi-token (chunked-prefill) attention and its plan.

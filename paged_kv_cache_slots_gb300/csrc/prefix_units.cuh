@@ -1,0 +1,186 @@
+// How the shared-prefix attention divides its work, worked out alike by every
+// CTA of the parts kernel (shared_prefix.cu) and of the tails kernel
+// (decode_kernel.cuh) from the groups and lengths.
+//
+// The prefix part's work is key tiles: every (group, KV head, row tile) triple
+// has its group's tiles, triples in that order.  CTA c of P takes tiles
+// [c W / P, (c + 1) W / P), whatever triples they belong to: all CTAs have the
+// same work to within a tile.  A run of one triple's tiles in one CTA is a
+// segment, and leaves one part.  Part k of a triple comes from the k-th CTA
+// that has tiles of it; a group reserves keys P / W + 2 parts of each of its
+// rows, so all groups together reserve at most 128 P + 2 (all rows).
+//
+// The SMs are divided between the two kernels, one CTA on each, so that they
+// run side by side and end together.
+#pragma once
+
+#include "device_utils.cuh"
+
+namespace pkv {
+
+constexpr int kPrefixRows = 128;  // query rows of a row tile
+constexpr int kPrefixTile = 64;   // keys of a tile
+constexpr int kMinChunk = 4;      // key tiles a CTA: fewer cost less than its start and the merge of its parts
+
+// a * b / c for 0 <= a, b and c > 0.
+__device__ __forceinline__ int mul_div(int a, int b, int c) {
+    const uint64_t p = static_cast<uint64_t>(static_cast<uint32_t>(a)) * static_cast<uint32_t>(b);
+    if ((p >> 32) == 0) return static_cast<int>(static_cast<uint32_t>(p) / static_cast<uint32_t>(c));
+    return static_cast<int>(p / static_cast<uint32_t>(c));
+}
+
+// CTA that owns tile x of W.
+__device__ __forceinline__ int cta_of_tile(int x, int W, int P) {
+    const uint64_t p = (static_cast<uint64_t>(x) + 1) * static_cast<uint32_t>(P) - 1;
+    if ((p >> 32) == 0) return static_cast<int>(static_cast<uint32_t>(p) / static_cast<uint32_t>(W));
+    return static_cast<int>(p / static_cast<uint32_t>(W));
+}
+
+// One lane's group.
+struct GroupShape {
+    int seq0, rows, tiles, keys, blocks;  // rows: sequences x G; tiles: row tiles; keys: key tiles
+};
+
+// Group g's shape; no work for one past the last.  *bad: it is out of order.
+// (Args: SharedPrefixArgs or DecodeArgs.)
+template <class Args>
+__device__ __forceinline__ GroupShape group_shape(const Args& a, int g, int G, bool* bad) {
+    GroupShape p{0, 0, 0, 0, 0};
+    if (g >= a.num_groups) return p;
+    const int s0 = a.group_start[g], s1 = a.group_start[g + 1], len = a.prefix_lens[g];
+    if (s0 < 0 || s1 > a.num_seqs || s0 > s1 || len < 0) {
+        *bad = true;
+        return p;
+    }
+    p.seq0 = s0;
+    p.rows = (s1 - s0) * G;
+    p.tiles = (p.rows + kPrefixRows - 1) / kPrefixRows;
+    p.blocks = len / a.block_size;
+    if (p.blocks > a.max_blocks) p.blocks = 0;  // no sequence is that long
+    p.keys = (p.blocks * a.block_size + kPrefixTile - 1) / kPrefixTile;
+    return p;
+}
+
+// Blocks that sequence s, of ctx tokens, shares with its group: 0 if it is in
+// none, or ends inside them.  The groups are in order.
+template <class Args>
+__device__ __forceinline__ int shared_blocks(const Args& a, int s, int ctx) {
+    if (a.num_groups == 0) return 0;
+    int lo = 0, hi = a.num_groups;  // the last group that starts at or before s
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.group_start[mid] <= s)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const int n = a.prefix_lens[lo] / a.block_size;
+    return a.group_start[lo] <= s && s < a.group_start[lo + 1] && n <= ctx / a.block_size ? n : 0;
+}
+
+// What every warp works out alike.
+struct Units {
+    GroupShape first;  // this lane's group of the first 32
+    int W;             // tiles; 0: nothing is shared
+    int triples;       // (group, KV head, row tile) triples with tiles
+    bool bad;          // the groups are out of order
+    int P;             // CTAs of the parts kernel with work (divide_sms)
+};
+
+template <class Args>
+__device__ __forceinline__ Units plan_units(const Args& a, int G) {
+    const int lane = threadIdx.x & 31;
+    Units u;
+    bool bad = false;
+    u.first = group_shape(a, lane, G, &bad);
+    int work = a.num_kv_heads * u.first.tiles * u.first.keys, triples = u.first.keys ? u.first.tiles : 0;
+    for (int g0 = 32; g0 < a.num_groups; g0 += 32) {
+        const GroupShape p = group_shape(a, g0 + lane, G, &bad);
+        work += a.num_kv_heads * p.tiles * p.keys;
+        triples += p.keys ? p.tiles : 0;
+    }
+    u.bad = __any_sync(0xffffffffu, bad);
+    work = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(work)));
+    triples = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(triples))) * a.num_kv_heads;
+    u.W = u.bad ? 0 : work;
+    u.triples = triples;
+    u.P = 0;
+    return u;
+}
+
+// The parts kernel's share of the SMs, u->P; the tails kernel takes the rest.
+// tail_tokens: tokens of all sequences after their shared blocks.
+//
+// A tile of 128 rows costs a parts CTA about kTileNs, a cached token of one KV
+// head a tails CTA about its bytes at the SM's share of the memory rate.
+template <class Args>
+__device__ __forceinline__ void divide_sms(const Args& a, int64_t tail_tokens, Units* u) {
+    constexpr float kTileNs = 600.f, kNsPerByte = 1.f / 42.f;
+    const int sms = a.num_ctas;
+    if (u->W == 0) return;
+    const float parts = kTileNs * static_cast<float>(u->W);
+    const float tails = kNsPerByte * 2.f * static_cast<float>(tail_tokens) *
+                        static_cast<float>(a.num_kv_heads * a.head_dim * dtype_bytes(a.kv_dtype));
+    int P = static_cast<int>(static_cast<float>(sms) * parts / (parts + tails) + 0.5f);
+    P = min(P, (u->W + kMinChunk - 1) / kMinChunk);
+    P = max(1, min(P, sms - 1));  // a tails CTA there always is: it writes the merge's tables
+    // CTAs that begin with a triple have one segment: worth up to a quarter of
+    // them while a CTA has few tiles, a sixteenth always.
+    if (u->triples <= P) {
+        const int even = P / u->triples * u->triples;
+        if ((P - even) * (u->W / P < 16 ? 4 : 16) <= P) P = even;
+    }
+    u->P = P;
+}
+
+// A triple, and where its parts go.
+struct Triple {
+    int seq0, rows, blocks, keys;
+    int h, rt;       // KV head, row tile
+    int tile0;       // its first tile
+    int row0;        // partial row of the row tile's first row, part 0
+};
+
+// The triple of tile x, by the whole warp (0 <= x < W).  Part k of row r of its
+// row tile is partial row row0 + k * rows + r.
+template <class Args>
+__device__ __forceinline__ Triple find_triple(const Args& a, const Units& u, int G, int x) {
+    const int lane = threadIdx.x & 31;
+    Triple t{};
+    int tile0 = 0, row0 = 0;
+    bool bad = false;
+    for (int g0 = 0; g0 < a.num_groups; g0 += 32) {
+        const GroupShape p = g0 == 0 ? u.first : group_shape(a, g0 + lane, G, &bad);
+        const int work = a.num_kv_heads * p.tiles * p.keys;
+        const int parts = mul_div(p.keys, u.P, u.W) + 2;
+        const int rows = p.keys ? a.num_kv_heads * parts * p.rows : 0;
+        int w = work, r = rows;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int yw = __shfl_up_sync(0xffffffffu, w, o), yr = __shfl_up_sync(0xffffffffu, r, o);
+            if (lane >= o) w += yw, r += yr;
+        }
+        const uint32_t mine = __ballot_sync(0xffffffffu, x < tile0 + w);
+        if (mine) {
+            const int src = __ffs(mine) - 1;
+            t.seq0 = __shfl_sync(0xffffffffu, p.seq0, src);
+            t.rows = __shfl_sync(0xffffffffu, p.rows, src);
+            t.blocks = __shfl_sync(0xffffffffu, p.blocks, src);
+            t.keys = __shfl_sync(0xffffffffu, p.keys, src);
+            const int tiles = __shfl_sync(0xffffffffu, p.tiles, src);
+            const int np = __shfl_sync(0xffffffffu, parts, src);
+            const int first = tile0 + __shfl_sync(0xffffffffu, w - work, src);
+            const int k = (x - first) / t.keys;
+            t.h = k / tiles;
+            t.rt = k - t.h * tiles;
+            t.tile0 = first + k * t.keys;
+            t.row0 = row0 + __shfl_sync(0xffffffffu, r - rows, src) + t.h * np * t.rows + t.rt * kPrefixRows;
+            return t;
+        }
+        tile0 += __shfl_sync(0xffffffffu, w, 31);
+        row0 += __shfl_sync(0xffffffffu, r, 31);
+    }
+    return t;
+}
+
+}  // namespace pkv

@@ -36,199 +36,27 @@ namespace pkv {
 
 namespace {
 
-// ------------------------------------------------------------------ units
-
-constexpr int kMinChunk = 4;  // key tiles a CTA
-
-// The prefix part's work is key tiles: every (group, KV head, row tile) triple
-// has the group's tiles, triples in that order.  CTA c of P takes tiles
-// [c W / P, (c + 1) W / P), whatever triples they belong to: all CTAs have the
-// same work to within a tile.  A run of one triple's tiles in one CTA is a
-// segment, and leaves one part.  Part k of a triple comes from the k-th CTA
-// that has tiles of it; a group reserves keys P / W + 2 parts of each of its
-// rows, so all groups together reserve at most 128 P + 2 (all rows).
-
-// a * b / c for 0 <= a, b and c > 0.
-__device__ __forceinline__ int mul_div(int a, int b, int c) {
-    const uint64_t p = static_cast<uint64_t>(static_cast<uint32_t>(a)) * static_cast<uint32_t>(b);
-    if ((p >> 32) == 0) return static_cast<int>(static_cast<uint32_t>(p) / static_cast<uint32_t>(c));
-    return static_cast<int>(p / static_cast<uint32_t>(c));
-}
-
-// CTA that owns tile x of W.
-__device__ __forceinline__ int cta_of_tile(int x, int W, int P) {
-    const uint64_t p = (static_cast<uint64_t>(x) + 1) * static_cast<uint32_t>(P) - 1;
-    if ((p >> 32) == 0) return static_cast<int>(static_cast<uint32_t>(p) / static_cast<uint32_t>(W));
-    return static_cast<int>(p / static_cast<uint32_t>(W));
-}
-
-// One lane's group.
-struct GroupShape {
-    int seq0, rows, tiles, keys, blocks;  // rows: sequences x G; tiles: row tiles; keys: key tiles
-};
-
-__device__ __forceinline__ int group_work(const GroupShape& p, int Hkv) { return Hkv * p.tiles * p.keys; }
-
-// Group g's shape; no work for one past the last.  *bad: it is out of order.
-__device__ __forceinline__ GroupShape group_shape(const SharedPrefixArgs& a, int g, int G, bool* bad) {
-    GroupShape p{0, 0, 0, 0, 0};
-    if (g >= a.num_groups) return p;
-    const int s0 = a.group_start[g], s1 = a.group_start[g + 1], len = a.prefix_lens[g];
-    if (s0 < 0 || s1 > a.num_seqs || s0 > s1 || len < 0) {
-        *bad = true;
-        return p;
-    }
-    p.seq0 = s0;
-    p.rows = (s1 - s0) * G;
-    p.tiles = (p.rows + 127) >> 7;
-    p.blocks = len / a.block_size;
-    if (p.blocks > a.max_blocks) p.blocks = 0;  // no sequence is that long
-    p.keys = (p.blocks * a.block_size + kPrefixTile - 1) / kPrefixTile;
-    return p;
-}
-
-// What every CTA, and every warp of it, works out alike.
-struct Units {
-    GroupShape first;  // this lane's group of the first 32
-    int W, P;          // tiles and CTAs with work; W = 0: nothing is shared
-};
-
-__device__ __forceinline__ Units plan_units(const SharedPrefixArgs& a, int G) {
-    const int lane = threadIdx.x & 31;
-    Units u;
-    bool bad = false;
-    u.first = group_shape(a, lane, G, &bad);
-    int work = group_work(u.first, a.num_kv_heads), triples = u.first.keys ? u.first.tiles : 0;
-    for (int g0 = 32; g0 < a.num_groups; g0 += 32) {
-        const GroupShape p = group_shape(a, g0 + lane, G, &bad);
-        work += group_work(p, a.num_kv_heads);
-        triples += p.keys ? p.tiles : 0;
-    }
-    bad = __any_sync(0xffffffffu, bad);
-    work = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(work)));
-    triples = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(triples))) * a.num_kv_heads;
-    u.W = bad ? 0 : work;
-    // With little work a CTA has an SM to itself, and four tiles (below that
-    // its start and the merge of its parts cost more than its tiles); with
-    // more, two share an SM.
-    const int all = a.num_sms * a.ctas_per_sm;
-    int P = u.W / kMinChunk >= all ? all : min(a.num_sms, (u.W + kMinChunk - 1) / kMinChunk);
-    // CTAs that begin with a triple have one segment: worth up to a quarter of
-    // the CTAs while a CTA has few tiles, a sixteenth always.
-    if (triples > 0 && triples <= P) {
-        const int even = P / triples * triples;
-        if ((P - even) * (u.W / P < 16 ? 4 : 16) <= P) P = even;
-    }
-    u.P = P > 0 ? P : 1;
-    return u;
-}
-
-// A triple, and a tile in it.
-struct Triple {
-    int seq0, rows, blocks, keys;
-    int h, rt;       // KV head, row tile
-    int tile0;       // first tile of the triple
-    int row0;        // row tile's first partial row, part 0
-    int stride;      // rows from one part to the next
-};
-
-// The triple of tile x, by the whole warp (0 <= x < W).
-__device__ __forceinline__ Triple find_triple(const SharedPrefixArgs& a, const Units& u, int G, int x) {
-    const int lane = threadIdx.x & 31;
-    Triple t{};
-    int tile0 = 0, row0 = 0;
-    bool bad = false;
-    for (int g0 = 0; g0 < a.num_groups; g0 += 32) {
-        const GroupShape p = g0 == 0 ? u.first : group_shape(a, g0 + lane, G, &bad);
-        const int work = group_work(p, a.num_kv_heads);
-        const int parts = mul_div(p.keys, u.P, u.W) + 2;
-        const int rows = p.keys ? a.num_kv_heads * parts * p.rows : 0;
-        int w = work, r = rows;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int yw = __shfl_up_sync(0xffffffffu, w, o), yr = __shfl_up_sync(0xffffffffu, r, o);
-            if (lane >= o) w += yw, r += yr;
-        }
-        const uint32_t mine = __ballot_sync(0xffffffffu, x < tile0 + w);
-        if (mine) {
-            const int src = __ffs(mine) - 1;
-            t.seq0 = __shfl_sync(0xffffffffu, p.seq0, src);
-            t.rows = __shfl_sync(0xffffffffu, p.rows, src);
-            t.blocks = __shfl_sync(0xffffffffu, p.blocks, src);
-            t.keys = __shfl_sync(0xffffffffu, p.keys, src);
-            const int tiles = __shfl_sync(0xffffffffu, p.tiles, src);
-            const int np = __shfl_sync(0xffffffffu, parts, src);
-            const int first = tile0 + __shfl_sync(0xffffffffu, w - work, src);
-            const int k = (x - first) / t.keys;
-            t.h = k / tiles;
-            t.rt = k - t.h * tiles;
-            t.tile0 = first + k * t.keys;
-            t.stride = t.rows;
-            t.row0 = row0 + __shfl_sync(0xffffffffu, r - rows, src) + t.h * np * t.rows + t.rt * 128;
-            return t;
-        }
-        tile0 += __shfl_sync(0xffffffffu, w, 31);
-        row0 += __shfl_sync(0xffffffffu, r, 31);
-    }
-    return t;
-}
-
-// Tells the merge where every (sequence, KV head)'s parts are.  One warp.
-__device__ void write_parts_table(const SharedPrefixArgs& a, const Units& u, int G) {
-    const int lane = threadIdx.x & 31;
-    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int Hkv = a.num_kv_heads;
-    for (int i = threadIdx.x; i < a.num_seqs * Hkv; i += blockDim.x) a.parts[i] = PrefixParts{0, 0, 0, 0};
-    __syncthreads();
-    if (u.W == 0) return;
-    int tile0 = 0, row0 = 0;
-    bool bad = false;
-    for (int g0 = 0; g0 < a.num_groups; g0 += 32) {
-        const GroupShape p = g0 == 0 ? u.first : group_shape(a, g0 + lane, G, &bad);
-        const int work = group_work(p, Hkv);
-        const int parts = mul_div(p.keys, u.P, u.W) + 2;
-        const int rows = p.keys ? Hkv * parts * p.rows : 0;
-        for (int k = 0; k < 32; ++k) {  // the groups one after the other, a warp's share of the pairs each
-            const int n = __shfl_sync(0xffffffffu, work, k);
-            const int keys = __shfl_sync(0xffffffffu, p.keys, k), tiles = __shfl_sync(0xffffffffu, p.tiles, k);
-            const int grows = __shfl_sync(0xffffffffu, p.rows, k), seq0 = __shfl_sync(0xffffffffu, p.seq0, k);
-            const int np = __shfl_sync(0xffffffffu, parts, k), blocks = __shfl_sync(0xffffffffu, p.blocks, k);
-            const int reserved = __shfl_sync(0xffffffffu, rows, k);
-            const int pairs = n ? grows / G * Hkv : 0;
-            for (int i = warp * 32 + lane; i < pairs; i += warps * 32) {
-                const int s = i / Hkv, h = i - s * Hkv;
-                if (a.context_lens[seq0 + s] / a.block_size < blocks) continue;  // ends inside the prefix
-                const int rt = s * G >> 7;
-                const int first = tile0 + (h * tiles + rt) * keys;
-                const int ca = cta_of_tile(first, u.W, u.P), cb = cta_of_tile(first + keys - 1, u.W, u.P);
-                a.parts[static_cast<int64_t>(seq0 + s) * Hkv + h] =
-                    PrefixParts{row0 + h * np * grows + s * G, grows, cb - ca + 1, 0};
-            }
-            tile0 += n;
-            row0 += reserved;
-        }
-    }
-}
-
 // ------------------------------------------------------------------ parts
 
-constexpr int kBM = 128;            // rows a CTA
-constexpr int kNK = kPrefixTile;    // keys a tile
-constexpr uint32_t kTmemCols = 256; // S / P buffers (2 x 64) + O (head_dim)
+constexpr int kBM = kPrefixRows;
+constexpr int kNK = kPrefixTile;
+constexpr int kS = 4;                // S / P buffers in tensor memory, 64 columns each
+constexpr uint32_t kO = kS * kNK;    // the two accumulators, D columns each
+constexpr uint32_t kTmemCols = 512;
 constexpr float kLazy = 8.f;
+constexpr int kIssuers = 2;          // warps that issue MMAs
 
 template <int D, bool kFP8>
 struct Shape {
     static constexpr int kSlices = D / 64;                    // 128-byte slices of a row
-    static constexpr int kKRing = D == 128 ? 3 : 6;           // K stages
-    static constexpr int kVRing = D == 128 ? 2 : 4;           // V stages
+    static constexpr int kKRing = D == 128 ? 4 : 8;           // K stages
+    static constexpr int kVRing = D == 128 ? 3 : 6;           // V stages
     static constexpr uint32_t kTile = kSlices * kNK * 128;    // bytes of a K (or V) tile
-    static constexpr int kProducers = kFP8 ? 4 : 1;           // producer warps
-    static constexpr int kThreads = 32 * (5 + kProducers);
-    static constexpr int kCtas = kFP8 ? 1 : 2;                // CTAs an SM
-    // E4M3: codes on their way, a ring for each producer warp: its 16 rows of K and of V.
-    static constexpr int kRawRing = kFP8 ? 6 : 0;
-    static constexpr uint32_t kRawStage = 2 * 16 * 128;
+    static constexpr int kProducers = 2;                      // producer warps
+    static constexpr int kThreads = 32 * (8 + kIssuers + kProducers);
+    // E4M3: codes on their way, a ring for each producer warp: 32 rows of K and of V.
+    static constexpr int kRawRing = kFP8 ? 4 : 0;
+    static constexpr uint32_t kRawStage = 2 * 32 * 128;
     static constexpr uint32_t kQOff = 0;
     static constexpr uint32_t kKOff = kSlices * kBM * 128;
     static constexpr uint32_t kVOff = kKOff + kKRing * kTile;
@@ -237,8 +65,10 @@ struct Shape {
 };
 
 struct Bars {
-    uint64_t kfull[6], kempty[6], vfull[4], vempty[4];
-    uint64_t s_full[2], p_full[2], pv_done[2], q_full;
+    uint64_t kfull[8], kempty[8], vfull[6], vempty[6];
+    uint64_t s_full[kS], p_full[kS], pv_done[kS], q_full;
+    uint64_t raw[2][4];
+    float2 ml[2][kBM];  // (reference, sum) of each row in each softmax group
     uint32_t tmem;
     int abort;
 };
@@ -261,6 +91,40 @@ __device__ __forceinline__ void store_32(float* p, const float* v) {
                  : "memory");
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one;
+}
+
+// tc_mma, tc_mma_ts and tc_commit issued by the lane with leader != 0 while the
+// whole warp walks the loop: addresses and descriptors are then the same on
+// every lane, and the compiler can keep them in uniform registers.
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                                       bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t leader, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(leader)
+        : "memory");
+}
+
 // Eight E4M3 codes -> eight f16 values, exactly, times 2^-8.
 __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
     return make_uint4(e4m3x2_odd_bytes_to_half2_shifted(__byte_perm(lo, 0u, 0x1404)),
@@ -269,53 +133,66 @@ __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
                       e4m3x2_odd_bytes_to_half2_shifted(__byte_perm(hi, 0u, 0x3424)));
 }
 
+// Tokens after the shared blocks, of all sequences: by the whole CTA.
+__device__ __forceinline__ int64_t count_tail_tokens(const SharedPrefixArgs& a, int64_t* sums) {
+    int64_t tokens = 0;
+    for (int s = threadIdx.x; s < a.num_seqs; s += blockDim.x) {
+        const int c = min(max(a.context_lens[s], 0), a.max_blocks * a.block_size);
+        tokens += c - shared_blocks(a, s, c) * a.block_size;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) tokens += __shfl_xor_sync(0xffffffffu, tokens, o);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = tokens;
+    __syncthreads();
+    tokens = 0;
+    for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) tokens += sums[w];
+    return tokens;
+}
+
 // QT: q's type.  The tensor cores work in it, or in f16 over an E4M3 cache
 // (whose codes widen to f16 in a few integer operations); a bf16 q is then
 // brought to f16 with a power of two for each row that puts its largest
 // element at 2^13: exact down to 2^-27 of that element.
 template <int QT, int D, bool kFP8>
-__global__ void __launch_bounds__(Shape<D, kFP8>::kThreads, Shape<D, kFP8>::kCtas)
-    shared_prefix_parts_kernel(const SharedPrefixArgs a) {
+__global__ void __launch_bounds__(Shape<D, kFP8>::kThreads, 1) shared_prefix_parts_kernel(const SharedPrefixArgs a) {
     using T = typename Elem<QT>::T;
     using S = Shape<D, kFP8>;
     constexpr int DT = kFP8 ? static_cast<int>(kF16) : QT;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ int64_t sums[16];
     pdl_wait();
     pdl_allow_next();  // after the wait: the tails start when all that came before has completed
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = a.num_q_heads / a.num_kv_heads;
-    const Units units = plan_units(a, G);
+    Units units = plan_units(a, G);
+    if (units.W == 0) return;
+    divide_sms(a, count_tail_tokens(a, sums), &units);
     const int cta = blockIdx.x;
-    if (cta == static_cast<int>(gridDim.x) - 1) {  // the last CTA has no tiles
-        write_parts_table(a, units, G);
-        return;
-    }
-    if (units.W == 0 || cta >= units.P) return;
+    if (cta >= units.P) return;
     const int start = mul_div(cta, units.W, units.P), end = mul_div(cta + 1, units.W, units.P);
     // The swizzled layouts need a 1024-byte aligned base.
-    if (smem_addr(smem_raw) & 1023u) {
-        if (tid == 0) raise_flag(a.status, kFlagBadPlan);
-        return;
-    }
-    uint8_t* base = smem_raw;
+    uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     Bars* B = reinterpret_cast<Bars*>(base + S::kBarOff);
     volatile int* abort = &B->abort;
     if (tid == 0) {
-        constexpr int arrivals = kFP8 ? S::kProducers : 32;  // one a producer warp, or one a copying lane
+        // A tile is full with one arrival a producer warp, or one a copying lane.
         for (int i = 0; i < S::kKRing; ++i) {
-            mbar_init(&B->kfull[i], arrivals);
+            mbar_init(&B->kfull[i], kFP8 ? S::kProducers : 32);
             mbar_init(&B->kempty[i], 1);
         }
         for (int i = 0; i < S::kVRing; ++i) {
-            mbar_init(&B->vfull[i], arrivals);
+            mbar_init(&B->vfull[i], kFP8 ? S::kProducers : 32);
             mbar_init(&B->vempty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kS; ++i) {
             mbar_init(&B->s_full[i], 1);
             mbar_init(&B->p_full[i], 4);
             mbar_init(&B->pv_done[i], 1);
         }
-        mbar_init(&B->q_full, 4);
+        mbar_init(&B->q_full, 8);
+        if constexpr (kFP8) {
+            for (int i = 0; i < 2 * S::kRawRing; ++i) mbar_init(&B->raw[i / S::kRawRing][i % S::kRawRing], 1);
+        }
         B->abort = 0;
         fence_barrier_init();
     }
@@ -327,16 +204,16 @@ __global__ void __launch_bounds__(Shape<D, kFP8>::kThreads, Shape<D, kFP8>::kCta
 
     // Every role walks the CTA's segments; tiles are counted from the CTA's
     // first (i), so rings and buffers go on over segments.
-    if (warp >= 5) {
-        // ---- producers: K of tile i, then V of tile i - 1 (K runs one tile
-        // ahead: S of a tile is issued before its PV).  The keys come in runs
-        // of 16 (block_size is a multiple of 16), each inside one block; runs
-        // past the last key are zeros.
+    if (warp >= 8 + kIssuers) {
+        // ---- producers.  The keys come in runs of 16 rows (block_size is a
+        // multiple of 16), each inside one block; runs past the last key are
+        // zeros.
         const int bs = a.block_size;
         const int ch = lane & 7, l8 = lane >> 3;
-        int i = 0;  // K tiles asked for so far
+        const int w = warp - 8 - kIssuers;
+        int i = 0;  // tiles before the segment
+        [[maybe_unused]] int issued = 0;
         bool ok = true;
-        [[maybe_unused]] const uint32_t sw0 = static_cast<uint32_t>(ch ^ l8) << 4, sw1 = static_cast<uint32_t>(ch ^ (l8 + 4)) << 4;
         for (int x = start; x < end && ok;) {
             const Triple t = find_triple(a, units, G, x);
             const int n = min(end, t.tile0 + t.keys) - x;  // tiles of the segment
@@ -352,7 +229,7 @@ __global__ void __launch_bounds__(Shape<D, kFP8>::kThreads, Shape<D, kFP8>::kCta
             }
             const int32_t* table = a.block_tables + static_cast<int64_t>(lead < 0 ? 0 : lead) * a.max_blocks;
             // First cache row of run r of the segment; -1: zeros.
-            auto run_row = [&](int r) -> int64_t {
+            auto run_row = [&](int r) -> int {
                 if (r >= nruns || lead < 0) return -1;
                 const int key = key0 + 16 * r;
                 const int lb = key / bs;
@@ -361,191 +238,227 @@ __global__ void __launch_bounds__(Shape<D, kFP8>::kThreads, Shape<D, kFP8>::kCta
                     raise_flag(a.status, kFlagBadBlock);
                     blk = 0;
                 }
-                return (static_cast<int64_t>(blk) * a.num_kv_heads + t.h) * bs + (key - lb * bs);
+                return (blk * a.num_kv_heads + t.h) * bs + (key - lb * bs);
             };
             if constexpr (!kFP8) {
-                // Lane l knows where run l of the current 8 tiles starts, and
-                // of the 8 after them.
-                int64_t now = run_row(lane), next = run_row(32 + lane);
-                // Lane e copies chunk e % 8 of rows e / 8 + 4 q of a run.
-                auto load = [&](int j, int64_t rows, const void* cache, uint32_t dst, uint64_t* bar) {
-                    const char* c0 = static_cast<const char*>(cache) + l8 * (D * 2) + ch * 16;
+                // One warp brings the K tiles, the other the V tiles.  Lane l
+                // knows where run l of the current 8 tiles starts, and of the 8
+                // after them; lane e copies chunk e % 8 of rows e / 8 + 4 q of a
+                // run.
+                int now = run_row(lane), next = run_row(32 + lane);
+                const char* c0 = static_cast<const char*>(w == 0 ? a.k_cache : a.v_cache) + l8 * (D * 2) + ch * 16;
+                const uint32_t d0 = smem_addr(base + (w == 0 ? S::kKOff : S::kVOff)) + l8 * 128;
+                uint64_t* full = w == 0 ? B->kfull : B->vfull;
+                uint64_t* empty = w == 0 ? B->kempty : B->vempty;
+                const int ring = w == 0 ? S::kKRing : S::kVRing;
+                const uint32_t sw0 = static_cast<uint32_t>(ch ^ l8) << 4, sw1 = static_cast<uint32_t>(ch ^ (l8 + 4)) << 4;
+                int st = i % ring, round = i / ring;
+                for (int j = 0; j < n; ++j) {
+                    if ((j & 7) == 0 && j > 0) {
+                        now = next;
+                        next = run_row(4 * (j + 8) + lane);
+                    }
+                    if (round > 0) ok = __all_sync(0xffffffffu, wait(&empty[st], round - 1, abort, a.status));
+                    if (!ok) break;
+                    const uint32_t dst = d0 + st * S::kTile;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int64_t row = __shfl_sync(0xffffffffu, rows, (j & 7) * 4 + k);
+                        const int row = __shfl_sync(0xffffffffu, now, (j & 7) * 4 + k);
                         const bool real = row >= 0;
-                        const char* src = c0 + (real ? row : 0) * (D * 2);
+                        const char* src = c0 + (real ? static_cast<int64_t>(row) * (D * 2) : 0);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const uint32_t d = dst + (16 * k + 4 * q + l8) * 128 + ((q & 1) ? sw1 : sw0);
+                            const uint32_t d = dst + (16 * k + 4 * q) * 128 + ((q & 1) ? sw1 : sw0);
 #pragma unroll
                             for (int sl = 0; sl < S::kSlices; ++sl)
                                 cp_async_16_or_zero(d + sl * (kNK * 128), src + (real ? q * (4 * D * 2) + sl * 128 : 0), real);
                         }
                     }
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
-                };
-                int64_t before = now;
-                for (int j = 0; j <= n && ok; ++j) {
-                    if (j < n) {
-                        const int st = (i + j) % S::kKRing;
-                        if ((j & 7) == 0 && j > 0) {
-                            before = now;
-                            now = next;
-                            next = run_row(4 * (j + 8) + lane);
-                        }
-                        if (i + j >= S::kKRing)
-                            ok = __all_sync(0xffffffffu, wait(&B->kempty[st], (i + j) / S::kKRing - 1, abort, a.status));
-                        if (!ok) break;
-                        load(j, now, a.k_cache, smem_addr(base + S::kKOff + st * S::kTile), &B->kfull[st]);
-                    }
-                    if (j >= 1) {
-                        const int v = i + j - 1, st = v % S::kVRing;
-                        if (v >= S::kVRing)
-                            ok = __all_sync(0xffffffffu, wait(&B->vempty[st], v / S::kVRing - 1, abort, a.status));
-                        if (!ok) break;
-                        load(j - 1, (j & 7) == 0 && j < n ? before : now, a.v_cache,
-                             smem_addr(base + S::kVOff + st * S::kTile), &B->vfull[st]);
-                    }
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&full[st])) : "memory");
+                    if (++st == ring) st = 0, ++round;
                 }
             } else {
-                // E4M3: warp w brings run w of every tile: its codes travel
-                // through a ring of its own (asynchronous copies, each lane
-                // reading back what it copied) and are widened into the tile.
-                // Lane e takes codes 16 (e % 8) .. of rows e / 8 + 4 q.
-                const int w = warp - 5;
-                const uint32_t raw0 = smem_addr(base + S::kRawOff + w * (S::kRawRing * S::kRawStage)) + lane * 16;
-                int64_t rows = -1;  // lane l: run w of tile l of the current 32
-                auto ask = [&](int j) {
-                    if ((j & 31) == 0) rows = run_row(4 * (j + lane) + w);
-                    const int64_t row = __shfl_sync(0xffffffffu, rows, j & 31);
-                    if (j < n) {
-                        const bool real = row >= 0;
-                        const int64_t off = real ? (row + l8) * D + ch * 16 : 0;
-                        const uint32_t d = raw0 + (j % S::kRawRing) * S::kRawStage;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            cp_async_16_or_zero(d + q * 512, static_cast<const char*>(a.k_cache) + off + (real ? q * 4 * D : 0), real);
-                            cp_async_16_or_zero(d + 2048 + q * 512, static_cast<const char*>(a.v_cache) + off + (real ? q * 4 * D : 0), real);
+                // E4M3: warp w brings runs 2 w and 2 w + 1 of every tile: the
+                // codes travel through a ring of its own and are widened into
+                // the tile.  Lane e takes codes 16 (e % 8) .. of rows e / 8 + 4 q.
+                const uint64_t policy = t.rows > kBM ? policy_evict_last() : policy_evict_first();
+                uint8_t* raw0 = base + S::kRawOff + w * (S::kRawRing * S::kRawStage);
+                int rows = -1;  // lane l: run 2 w + l % 2 of tile l / 2 of the current 16
+                auto ask = [&](int j) {  // in order, each tile once
+                    if ((j & 15) == 0) rows = run_row(4 * (j + (lane >> 1)) + 2 * w + (lane & 1));
+                    const int r0 = __shfl_sync(0xffffffffu, rows, 2 * (j & 15)), r1 = __shfl_sync(0xffffffffu, rows, 2 * (j & 15) + 1);
+                    if (j >= n) return;
+                    ++issued;
+                    if (lane == 0) {
+                        const int st = (i + j) % S::kRawRing;
+                        uint64_t* bar = &B->raw[w][st];
+                        const uint32_t bytes = (r0 >= 0 ? 2 * 16 * D : 0) + (r1 >= 0 ? 2 * 16 * D : 0);
+                        if (bytes == 0) {
+                            mbar_arrive(bar);
+                            return;
+                        }
+                        mbar_arrive_expect_tx(bar, bytes);
+                        uint8_t* d = raw0 + st * S::kRawStage;
+                        for (int k = 0; k < 2; ++k) {
+                            const int row = k ? r1 : r0;
+                            if (row < 0) continue;
+                            const int64_t off = static_cast<int64_t>(row) * D;
+                            bulk_load(d + k * 16 * D, static_cast<const char*>(a.k_cache) + off, 16 * D, bar, policy);
+                            bulk_load(d + (2 + k) * 16 * D, static_cast<const char*>(a.v_cache) + off, 16 * D, bar, policy);
                         }
                     }
-                    asm volatile("cp.async.commit_group;" ::: "memory");  // an empty group past the end
                 };
-                auto put = [&](uint32_t raw, uint32_t off, uint64_t* bar) {
+                auto put = [&](const uint8_t* raw, int real, uint32_t off, uint64_t* bar) {  // real: runs with codes
                     uint8_t* tile = base + off + (ch >> 2) * (kNK * 128);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint4 r;
-                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                                     : "r"(raw + q * 512)
-                                     : "memory");
-                        const int row = 16 * w + 4 * q + l8;
+                    for (int q = 0; q < 8; ++q) {
+                        const uint4 r = q / 4 < real ? *reinterpret_cast<const uint4*>(raw + (4 * q + l8) * D + ch * 16)
+                                                     : make_uint4(0u, 0u, 0u, 0u);
+                        const int row = 32 * w + 4 * q + l8;
                         const int c0 = (ch & 3) * 2;
                         *reinterpret_cast<uint4*>(tile + row * 128 + ((c0 ^ (row & 7)) << 4)) = widen8(r.x, r.y);
                         *reinterpret_cast<uint4*>(tile + row * 128 + (((c0 + 1) ^ (row & 7)) << 4)) = widen8(r.z, r.w);
                     }
-                    fence_proxy_async_smem();
+                    fence_proxy_async_smem();  // the tile before the tensor cores read it, the codes before the next copy
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar);
                 };
                 for (int j = 0; j < S::kRawRing - 1; ++j) ask(j);
                 for (int j = 0; j < n && ok; ++j) {
                     ask(j + S::kRawRing - 1);
-                    asm volatile("cp.async.wait_group %0;" ::"n"(S::kRawRing - 1) : "memory");  // tile j is here
-                    const uint32_t raw = raw0 + (j % S::kRawRing) * S::kRawStage;
+                    const int st = (i + j) % S::kRawRing;
+                    const int real = lead < 0 ? 0 : min(max(nruns - 4 * j - 2 * w, 0), 2);
+                    ok = __all_sync(0xffffffffu, wait(&B->raw[w][st], (i + j) / S::kRawRing, abort, a.status));
+                    if (!ok) break;
+                    const uint8_t* raw = raw0 + st * S::kRawStage;
                     const int sk = (i + j) % S::kKRing, sv = (i + j) % S::kVRing;
                     if (i + j >= S::kKRing)
                         ok = __all_sync(0xffffffffu, wait(&B->kempty[sk], (i + j) / S::kKRing - 1, abort, a.status));
                     if (!ok) break;
-                    put(raw, S::kKOff + sk * S::kTile, &B->kfull[sk]);
+                    put(raw, real, S::kKOff + sk * S::kTile, &B->kfull[sk]);
                     if (i + j >= S::kVRing)
                         ok = __all_sync(0xffffffffu, wait(&B->vempty[sv], (i + j) / S::kVRing - 1, abort, a.status));
                     if (!ok) break;
-                    put(raw + 2048, S::kVOff + sv * S::kTile, &B->vfull[sv]);
+                    put(raw + 2 * 16 * D, real, S::kVOff + sv * S::kTile, &B->vfull[sv]);
                 }
             }
             i += n;
             x += n;
         }
         // Every copy issued must land before the CTA can exit.
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        if constexpr (kFP8) {
+            if (lane == 0) {
+                for (int st = 0; st < S::kRawRing && st < issued; ++st) {
+                    const int last = st + ((issued - 1 - st) / S::kRawRing) * S::kRawRing;
+                    const uint64_t t0 = global_timer_ns();
+                    while (!mbar_try_wait(&B->raw[w][st], (last / S::kRawRing) & 1)) {
+                        if (global_timer_ns() - t0 > kWaitLimitNs) {
+                            raise_flag(a.status, kFlagTimeout);
+                            break;
+                        }
+                    }
+                }
+            }
+        } else {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        }
         __syncwarp();
-    } else if (warp == 4) {
-        // ---- MMA issue (one lane; the others only look segments up)
+    } else if (warp >= 8) {
+        // ---- MMA issue.  Each of the kIssuers warps issues for its own tiles
+        // (all, or those of one parity): S runs ahead of P V by kAhead of them.
         constexpr int bf = DT == kBF16 ? 1 : 0;
         constexpr uint32_t idS = tc_idesc_f16(bf, false, kNK, kBM);
         constexpr uint32_t idPV = tc_idesc_f16(bf, true, D, kBM);
-        const uint32_t qa = smem_addr(base + S::kQOff);
-        auto pv = [&](int i, bool first) -> bool {
-            const int sv = i % S::kVRing, bt = i & 1;
-            if (!wait(&B->p_full[bt], i >> 1, abort, a.status)) return false;
-            if (!wait(&B->vfull[sv], i / S::kVRing, abort, a.status)) return false;
+        constexpr int kStep = kIssuers, kAhead = kS / kIssuers - 1;
+        const int me = warp - 8;
+        const uint32_t leader = elect_one();
+        const uint32_t sbase = smem_addr(base), bars = smem_addr(B);
+        auto bar_of = [&](const uint64_t* p) { return bars + static_cast<uint32_t>(reinterpret_cast<const uint8_t*>(p) - reinterpret_cast<const uint8_t*>(B)); };
+        // All tensor memory is this CTA's: its addresses start at 0.
+        const uint64_t qd = tc_sdesc(sbase + S::kQOff, 16, 1024);
+        auto ready = [&](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, wait(bar, phase, abort, a.status)) != 0; };
+        auto score = [&](int i) -> bool {
+            const int sk = i % S::kKRing, b = i % kS;
+            if (!ready(&B->kfull[sk], i / S::kKRing)) return false;
+            // S buffer b holds P of tile i - kS until that PV has completed.
+            if (i >= kS && !ready(&B->pv_done[b], i / kS - 1)) return false;
             if constexpr (!kFP8) fence_proxy_async_smem();  // lane copies before the tensor cores read them
             tc_fence_after();
-            const uint32_t va = smem_addr(base + S::kVOff + sv * S::kTile);
+            const uint64_t kd = tc_sdesc(sbase + S::kKOff + sk * S::kTile, 16, 1024);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+                mma_ss(leader, b * kNK, qd + (((ks >> 2) * (kBM * 128) + (ks & 3) * 32) >> 4),
+                       kd + (((ks >> 2) * (kNK * 128) + (ks & 3) * 32) >> 4), idS, ks > 0);
+            mma_commit(leader, bar_of(&B->s_full[b]));
+            mma_commit(leader, bar_of(&B->kempty[sk]));
+            return true;
+        };
+        auto pv = [&](int i, bool first) -> bool {
+            const int sv = i % S::kVRing, b = i % kS;
+            if (!ready(&B->p_full[b], i / kS)) return false;
+            if (!ready(&B->vfull[sv], i / S::kVRing)) return false;
+            if constexpr (!kFP8) fence_proxy_async_smem();
+            tc_fence_after();
+            const uint64_t vd = tc_sdesc(sbase + S::kVOff + sv * S::kTile, kNK * 128, 1024);
+            const uint32_t o = kO + (i & 1) * D;
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
                 for (int kk = 0; kk < kNK / 16; ++kk)
-                    tc_mma_ts(taddr + 128, taddr + bt * kNK + part * 32 + kk * 8,
-                              tc_sdesc(va + kk * 16 * 128, kNK * 128, 1024), idPV, !(first && part == 0 && kk == 0));
-            tc_commit(&B->pv_done[bt]);
-            tc_commit(&B->vempty[sv]);
+                    mma_ts(leader, o, b * kNK + part * 32 + kk * 8, vd + ((kk * 16 * 128) >> 4), idPV,
+                           !(first && part == 0 && kk == 0));
+            mma_commit(leader, bar_of(&B->pv_done[b]));
+            mma_commit(leader, bar_of(&B->vempty[sv]));
             return true;
         };
         int i = 0, seg = 0;
         bool ok = true;
         for (int x = start; x < end && ok; ++seg) {
             const Triple t = find_triple(a, units, G, x);
-            const int n = min(end, t.tile0 + t.keys) - x;
-            if (lane == 0) {
-                ok = wait(&B->q_full, seg, abort, a.status);
-                for (int j = 0; j < n && ok; ++j) {
-                    const int k = i + j, sk = k % S::kKRing, b = k & 1;
-                    ok = wait(&B->kfull[sk], k / S::kKRing, abort, a.status);
-                    // S buffer b holds P of tile k - 2 until that PV has completed.
-                    if (ok && k >= 2) ok = wait(&B->pv_done[b], (k >> 1) - 1, abort, a.status);
-                    if (!ok) break;
-                    if constexpr (!kFP8) fence_proxy_async_smem();
-                    tc_fence_after();
-                    const uint32_t ka = smem_addr(base + S::kKOff + sk * S::kTile);
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        tc_mma(taddr + b * kNK, tc_sdesc(qa + (ks >> 2) * (kBM * 128) + (ks & 3) * 32, 16, 1024),
-                               tc_sdesc(ka + (ks >> 2) * (kNK * 128) + (ks & 3) * 32, 16, 1024), idS, ks > 0);
-                    tc_commit(&B->s_full[b]);
-                    tc_commit(&B->kempty[sk]);
-                    if (j >= 1) ok = pv(k - 1, j == 1);
+            const int n = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(min(end, t.tile0 + t.keys) - x)));
+            const int j0 = kIssuers == 1 ? 0 : (me ^ i) & 1;
+            ok = ready(&B->q_full, seg);
+            for (int j = j0, k = 0; j < n && k < kAhead && ok; j += kStep, ++k) ok = score(i + j);
+            for (int j = j0; j < n && ok; j += kStep) {
+                // With one issuer P V goes first: S of the tile after next waits for
+                // the P V before it, which has just been queued behind.
+                if constexpr (kIssuers == 1) {
+                    ok = pv(i + j, j < 2);
+                    if (ok && j + kAhead < n) ok = score(i + j + kAhead);
+                } else {
+                    if (j + kAhead * kStep < n) ok = score(i + j + kAhead * kStep);
+                    if (ok) ok = pv(i + j, j < 2);
                 }
-                if (ok) ok = pv(i + n - 1, n == 1);
             }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             i += n;
             x += n;
         }
     } else {
-        // ---- softmax: thread r owns row r (tensor-memory lane r)
-        const int r = tid;
-        const uint32_t lane_base = taddr + (static_cast<uint32_t>(32 * warp) << 16);
+        // ---- softmax: two groups of four warps; group g takes the tiles whose
+        // count has parity g, with a reference, a sum and an accumulator of its
+        // own.  Thread r of a group owns row r (tensor-memory lane r).
+        const int r = tid & (kBM - 1), grp = tid / kBM;
+        const uint32_t lane_base = taddr + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+        const uint32_t o_base = lane_base + kO + grp * D;
         // |scale| in log2 units; a zero scale is taken as 1e-30, which leaves
         // every finite score's exponent at 0 while masked scores stay -inf.
         const float sc0 = fmaxf(fabsf(a.scale_log2), 1e-30f) * (kFP8 ? 256.f : 1.f);  // widened codes are 2^-8 of the value
         int i = 0;
-        bool ok = true;
-        for (int x = start; x < end && ok;) {
+        bool ok = true;  // (a failed wait skips the work, not the barriers)
+        for (int x = start; x < end;) {
             const Triple t = find_triple(a, units, G, x);
             const int n = min(end, t.tile0 + t.keys) - x;
             const int nrows = min(kBM, t.rows - t.rt * kBM);
             const int keys = min(t.blocks * a.block_size - (x - t.tile0) * kNK, n * kNK);  // of the segment
             float sc = sc0;
             {
-                // Q row r of the tile (member (rt * 128 + r) / G, query head
-                // h * G + r % G) into shared memory, 128-byte swizzled K-major.
-                // (The previous segment's S are complete: their last was read.)
+                // Half of Q row r of the tile (member (rt * 128 + r) / G, query
+                // head h * G + r % G) into shared memory, 128-byte swizzled
+                // K-major.  (The previous segment's S are complete: all were
+                // read before its barriers.)
                 const int rr = t.rt * kBM + min(r, nrows - 1);
-                const T* qrow = static_cast<const T*>(a.q) +
-                                (static_cast<int64_t>(t.seq0 + rr / G) * a.num_q_heads + t.h * G + rr % G) * D;
+                const int s = t.seq0 + rr / G;
+                const T* qrow = static_cast<const T*>(a.q) + (static_cast<int64_t>(s) * a.num_q_heads + t.h * G + rr % G) * D;
                 // A negative scale is applied as |scale| to the scores of -q (a
                 // sign flip is exact), so the row maximum is taken on unscaled
                 // scores.
@@ -556,24 +469,25 @@ __global__ void __launch_bounds__(Shape<D, kFP8>::kThreads, Shape<D, kFP8>::kCta
 #pragma unroll
                     for (int q16 = 0; q16 < D / 8; ++q16) {
                         const uint4 v = *reinterpret_cast<const uint4*>(qrow + 8 * q16);
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        const uint32_t b[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+                        for (int k = 0; k < 4; ++k) top = max(top, max(b[k] & 0x7FFFu, (b[k] >> 16) & 0x7FFFu));
                     }
                     const int e = min(max(static_cast<int>(top >> 7) - 127, -100), 127);  // its exponent
                     up = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
                     sc *= __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
                 }
 #pragma unroll
-                for (int q16 = 0; q16 < D / 8; ++q16) {
+                for (int q = 0; q < D / 16; ++q) {
+                    const int q16 = grp * (D / 16) + q;
                     uint4 v = *reinterpret_cast<const uint4*>(qrow + 8 * q16);
                     if constexpr (kFP8 && QT == kBF16) {
-                        uint32_t* w = &v.x;
+                        uint32_t* b = &v.x;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const __half2 h = __floats2half2_rn(__uint_as_float(w[k] << 16) * up,
-                                                                __uint_as_float(w[k] & 0xFFFF0000u) * up);
-                            w[k] = *reinterpret_cast<const uint32_t*>(&h);
+                            const __half2 h = __floats2half2_rn(__uint_as_float(b[k] << 16) * up,
+                                                                __uint_as_float(b[k] & 0xFFFF0000u) * up);
+                            b[k] = *reinterpret_cast<const uint32_t*>(&h);
                         }
                     }
                     v.x ^= flip;
@@ -585,12 +499,19 @@ __global__ void __launch_bounds__(Shape<D, kFP8>::kThreads, Shape<D, kFP8>::kCta
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&B->q_full);  // one arrival per warp (count 4)
+                if (lane == 0) mbar_arrive(&B->q_full);  // one arrival per warp (count 8)
+                // The CTA with a triple's first tile says where its parts are,
+                // for the members of the row tile.
+                if (x == t.tile0 && grp == 0 && r < nrows && rr % G == 0 && a.context_lens[s] / a.block_size >= t.blocks)
+                    a.parts[static_cast<int64_t>(s) * a.num_kv_heads + t.h] =
+                        make_int4(t.row0 + r, t.rows, cta_of_tile(t.tile0 + t.keys - 1, units.W, units.P) - cta + 1, 0);
             }
-            float m_ref = 0.f, l = 0.f;
-            for (int j = 0; j < n && ok; ++j) {
-                const int k0 = i + j, b = k0 & 1;
-                ok = __all_sync(0xffffffffu, wait(&B->s_full[b], k0 >> 1, abort, a.status));
+            // Unless it has a tile, a group weighs nothing.
+            float m_ref = -1e30f, l = 0.f;
+            const int j0 = (grp ^ i) & 1;
+            for (int j = j0; j < n && ok; j += 2) {
+                const int k0 = i + j, b = k0 % kS;
+                ok = __all_sync(0xffffffffu, wait(&B->s_full[b], k0 / kS, abort, a.status));
                 if (!ok) break;
                 tc_fence_after();
                 float sv[kNK];
@@ -622,13 +543,13 @@ __global__ void __launch_bounds__(Shape<D, kFP8>::kThreads, Shape<D, kFP8>::kCta
                                              fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sc,
                                        -1e30f);
                 bool need = false;
-                if (j == 0)
+                if (j < 2)
                     m_ref = mt;
                 else
                     need = mt > m_ref + kLazy;
                 if (__any_sync(0xffffffffu, need)) {
-                    // O must be complete up to the tile before it is rescaled.
-                    ok = __all_sync(0xffffffffu, wait(&B->pv_done[(k0 - 1) & 1], (k0 - 1) >> 1, abort, a.status));
+                    // O must be complete up to the group's tile before it is rescaled.
+                    ok = __all_sync(0xffffffffu, wait(&B->pv_done[(k0 - 2) % kS], (k0 - 2) / kS, abort, a.status));
                     if (!ok) break;
                     tc_fence_after();
                     const float f = need ? fast_exp2(m_ref - mt) : 1.f;
@@ -639,11 +560,11 @@ __global__ void __launch_bounds__(Shape<D, kFP8>::kThreads, Shape<D, kFP8>::kCta
 #pragma unroll
                     for (int cb = 0; cb < D / 32; ++cb) {
                         float o[32];
-                        tc_ld32(lane_base + 128 + 32 * cb, o);
+                        tc_ld32(o_base + 32 * cb, o);
                         tc_wait_ld();
 #pragma unroll
                         for (int k = 0; k < 32; ++k) o[k] *= f;
-                        tc_st32(lane_base + 128 + 32 * cb, o);
+                        tc_st32(o_base + 32 * cb, o);
                     }
                     tc_wait_st();
                 }
@@ -669,28 +590,41 @@ __global__ void __launch_bounds__(Shape<D, kFP8>::kThreads, Shape<D, kFP8>::kCta
                 if (lane == 0) mbar_arrive(&B->p_full[b]);  // one arrival per warp (count 4)
             }
             i += n;
-            if (ok) ok = __all_sync(0xffffffffu, wait(&B->pv_done[(i - 1) & 1], (i - 1) >> 1, abort, a.status));
+            // Both groups' accumulators into one part: group g writes half of
+            // the columns.
+            B->ml[grp][r] = make_float2(m_ref, l);
+            named_barrier_sync(1, 2 * kBM);
+            if (ok) ok = __all_sync(0xffffffffu, wait(&B->pv_done[(i - 1) % kS], (i - 1) / kS, abort, a.status));
+            if (ok && n > 1) ok = __all_sync(0xffffffffu, wait(&B->pv_done[(i - 2) % kS], (i - 2) / kS, abort, a.status));
             if (ok) {
                 tc_fence_after();
+                const float2 e = B->ml[0][r], o = B->ml[1][r];
+                const float M = fmaxf(e.x, o.x);
+                const float we = fast_exp2(e.x - M), wo = fast_exp2(o.x - M);
                 const float vs = a.v_scale * (kFP8 ? 256.f : 1.f);
-                const int64_t row = t.row0 + static_cast<int64_t>(cta - cta_of_tile(t.tile0, units.W, units.P)) * t.stride + r;
+                const float se = we * vs, so = wo * vs;
+                // A segment of one tile leaves the other group's accumulator as it was.
+                const bool has_e = n > 1 || ((i - 1) & 1) == 0, has_o = n > 1 || ((i - 1) & 1) == 1;
+                const int64_t row = t.row0 + static_cast<int64_t>(cta - cta_of_tile(t.tile0, units.W, units.P)) * t.rows + r;
                 const bool row_ok = r < nrows && row < a.max_rows;
-                float* po = a.part_o + row * D;
+                float* po = a.part_o + row * D + grp * (D / 2);
 #pragma unroll
-                for (int cb = 0; cb < D / 32; ++cb) {
-                    float o[32];
-                    tc_ld32(lane_base + 128 + 32 * cb, o);
+                for (int cb = 0; cb < D / 64; ++cb) {
+                    float v0[32], v1[32];
+                    tc_ld32(lane_base + kO + grp * (D / 2) + 32 * cb, v0);
+                    tc_ld32(lane_base + kO + D + grp * (D / 2) + 32 * cb, v1);
                     tc_wait_ld();
                     if (row_ok) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] *= vs;
+                        for (int k = 0; k < 32; ++k) v0[k] = (has_e ? v0[k] * se : 0.f) + (has_o ? v1[k] * so : 0.f);
 #pragma unroll
-                        for (int k = 0; k < 32; k += 8) store_32(po + 32 * cb + k, o + k);
+                        for (int k = 0; k < 32; k += 8) store_32(po + 32 * cb + k, v0 + k);
                     }
                 }
-                if (row_ok) *reinterpret_cast<float2*>(a.part_ml + 2 * row) = make_float2(m_ref, l);
-                tc_fence_before();  // before the next segment's P, and its PV, are announced
+                if (row_ok && grp == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * row) = make_float2(M, we * e.y + wo * o.y);
+                tc_fence_before();
             }
+            named_barrier_sync(1, 2 * kBM);  // both accumulators read before the next segment's P is announced
             x += n;
         }
     }
@@ -722,9 +656,9 @@ __global__ void __launch_bounds__(128) shared_prefix_merge_kernel(const SharedPr
     const int Hc = d.heads_per_stage, chunks = d.num_kv_heads / Hc;
     const int hc = h / Hc, hw = h - hc * Hc;
     const int pair = s * chunks + hc;
-    const PrefixParts pp = a.parts[s * a.num_kv_heads + h];
+    const int4 pp = a.parts[static_cast<int64_t>(s) * a.num_kv_heads + h];
     const int4 tp = d.tail_parts[pair];
-    const int n = pp.parts + tp.y;
+    const int n = pp.z + tp.y;
     float M = -INFINITY, L = 0.f, acc[VD];
 #pragma unroll
     for (int i = 0; i < VD; ++i) acc[i] = 0.f;
@@ -733,15 +667,15 @@ __global__ void __launch_bounds__(128) shared_prefix_merge_kernel(const SharedPr
         const int p = base + lane;
         const float* po = nullptr;
         float2 ml = make_float2(-INFINITY, 0.f);
-        if (p < pp.parts) {
-            const int64_t r = pp.row0 + static_cast<int64_t>(p) * pp.stride + g;
+        if (p < pp.z) {
+            const int64_t r = pp.x + static_cast<int64_t>(p) * pp.y + g;
             if (r < a.max_rows) {
                 po = a.part_o + r * D;
                 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + 2 * r));
             }
         } else if (p < n) {
-            const int k = p - pp.parts;
-            const int64_t c = tp.w == 0 ? tp.x + k : cta_of_tile(tp.z + k, tp.w, d.num_ctas);
+            const int k = p - pp.z;
+            const int64_t c = tp.w == 0 ? tp.x + k : cta_of_tile(tp.z + k, tp.w, tp.x);
             const int64_t r = ((c + pair) * Hc + hw) * G + g;
             po = d.part_o + r * D;
             ml = __ldcg(reinterpret_cast<const float2*>(d.part_ml + 2 * r));
@@ -797,28 +731,41 @@ __global__ void __launch_bounds__(128) shared_prefix_merge_kernel(const SharedPr
     for (int i = 0; i < VD; ++i) store_out(a.out, o0 + i, n > 0 ? acc[i] * inv : 0.f, a.out_dtype);
 }
 
-template <int DT, int D, bool kFP8>
+template <int QT, int D, bool kFP8>
 cudaError_t launch_parts_t(const SharedPrefixArgs& a, cudaStream_t stream) {
-    using S = Shape<D, kFP8>;
     static std::atomic<int> configured[64];
-    auto kern = shared_prefix_parts_kernel<DT, D, kFP8>;
+    auto kern = shared_prefix_parts_kernel<QT, D, kFP8>;
     const bool cacheable = a.device >= 0 && a.device < 64;
     if (!cacheable || !configured[a.device].load()) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, a.smem_bytes);
+        if (e == cudaSuccess) e = prefer_shared_memory(kern);
         if (e != cudaSuccess) return e;
         if (cacheable) configured[a.device].store(1);
     }
-    return launch_kernel(kern, dim3(a.num_sms * a.ctas_per_sm + 1), dim3(S::kThreads), static_cast<size_t>(a.smem_bytes), stream, true, a);
+    return launch_kernel(kern, dim3(a.num_ctas), dim3(Shape<D, kFP8>::kThreads), static_cast<size_t>(a.smem_bytes),
+                         stream, true, a);
+}
+
+template <int D>
+cudaError_t launch_merge_t(const SharedPrefixArgs& a, const DecodeArgs& tails, cudaStream_t stream) {
+    static std::atomic<int> configured[64];
+    auto kern = shared_prefix_merge_kernel<D>;
+    const bool cacheable = a.device >= 0 && a.device < 64;
+    if (!cacheable || !configured[a.device].load()) {
+        const cudaError_t e = prefer_shared_memory(kern);
+        if (e != cudaSuccess) return e;
+        if (cacheable) configured[a.device].store(1);
+    }
+    const int64_t warps = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
+    return launch_kernel(kern, dim3(static_cast<unsigned>((warps + 3) / 4)), dim3(128), 0, stream, true, a, tails);
 }
 
 }  // namespace
 
 int prefix_smem_bytes(int head_dim, bool fp8) {
     const uint32_t off = fp8 ? Shape<128, true>::kBarOff : head_dim == 64 ? Shape<64, false>::kBarOff : Shape<128, false>::kBarOff;
-    return static_cast<int>(off + sizeof(Bars));
+    return static_cast<int>(off + sizeof(Bars) + 1024);
 }
-
-int prefix_ctas_per_sm(bool fp8) { return fp8 ? Shape<128, true>::kCtas : Shape<128, false>::kCtas; }
 
 cudaError_t launch_prefix_parts(const SharedPrefixArgs& a, cudaStream_t stream) {
     if (a.kv_dtype == kFP8) {
@@ -834,10 +781,8 @@ cudaError_t launch_prefix_parts(const SharedPrefixArgs& a, cudaStream_t stream) 
 }
 
 cudaError_t launch_prefix_merge(const SharedPrefixArgs& a, const DecodeArgs& tails, cudaStream_t stream) {
-    const int64_t warps = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
-    const dim3 grid(static_cast<unsigned>((warps + 3) / 4));
-    if (a.head_dim == 64) return launch_kernel(shared_prefix_merge_kernel<64>, grid, dim3(128), 0, stream, true, a, tails);
-    return launch_kernel(shared_prefix_merge_kernel<128>, grid, dim3(128), 0, stream, true, a, tails);
+    if (a.head_dim == 64) return launch_merge_t<64>(a, tails, stream);
+    return launch_merge_t<128>(a, tails, stream);
 }
 
 }  // namespace pkv

@@ -5,12 +5,6 @@
 
 namespace pkv {
 
-// Where the prefix parts of one (sequence, KV head) are: part k of query head g
-// of it sits in partial row row0 + k * stride + g.
-struct PrefixParts {
-    int row0, stride, parts, unused;
-};
-
 struct SharedPrefixArgs {
     const void* q;               // [B][Hq][D]
     const void* k_cache;
@@ -22,22 +16,19 @@ struct SharedPrefixArgs {
     void* out;
     uint32_t* status;
     // Workspace.
-    PrefixParts* parts;          // [B][Hkv]
+    int4* parts;                 // [B][Hkv] (x, y, z, -): part k < z of query head g of the KV head is
+                                 // partial row x + k * y + g
     float* part_o;               // [max_rows][D]
     float* part_ml;              // [max_rows][2]
     int num_seqs, num_groups, num_blocks, max_blocks, num_q_heads, num_kv_heads, head_dim, block_size;
     int dtype, out_dtype, kv_dtype;
     float scale_log2, v_scale;
-    int num_sms, ctas_per_sm;    // CTAs of the parts kernel that run at once
+    int num_ctas;                // SMs, divided between the parts and the tails
     int max_rows;                // capacity of the partial rows
     int device, smem_bytes;
 };
 
-// Keys of one tile of the prefix kernel.
-constexpr int kPrefixTile = 64;
-
 int prefix_smem_bytes(int head_dim, bool fp8);
-int prefix_ctas_per_sm(bool fp8);
 cudaError_t launch_prefix_parts(const SharedPrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_merge(const SharedPrefixArgs& a, const DecodeArgs& tails, cudaStream_t stream);
 // The decode kernel over what follows the prefix (decode_tails.cu).
