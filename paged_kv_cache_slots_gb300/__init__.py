@@ -30,6 +30,7 @@ CODE_DTYPE = {v: k for k, v in DTYPE_CODE.items()}
 DTYPE_NAMES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16,
                "e4m3": torch.float8_e4m3fn, "fp8": torch.float8_e4m3fn}
 FP8 = torch.float8_e4m3fn
+_ROW_DTYPES = (torch.float32, torch.float16, torch.bfloat16)
 KERNELS = {"auto": 0, "ffma": 1, "mma": 2}
 FLAG_BAD_BLOCK_ID, FLAG_BAD_SLOT, FLAG_BAD_CONTEXT, FLAG_TIMEOUT = 0x1, 0x2, 0x4, 0x8
 FLAG_BAD_GROUP = 0x20
@@ -165,23 +166,33 @@ def _check(status: int, lib=None):
 
 
 def _ptr(t: torch.Tensor | None):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(t: torch.Tensor, stream) -> ctypes.c_void_p:
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(t: torch.Tensor, stream) -> int:
     if stream is None:
+        index = t.get_device()
+        if _raw_stream is not None and index >= 0:
+            return _raw_stream(index)
         stream = torch.cuda.current_stream(t.device)
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _call_on(t: torch.Tensor, lib, fn, *args):
     """Call a library entry point with t's device current: the library takes
     the SM count, the status word and the static scratch of the current
     device, and the stream passed is t's."""
-    if t.device.type != "cuda":  # the library rejects host pointers where it needs device memory
-        _check(fn(*args), lib)
+    index = t.get_device()
+    # A host tensor (index -1): the library rejects host pointers where it needs device memory.
+    if index < 0 or index == torch.cuda.current_device():
+        status = fn(*args)
+        if status:
+            _check(status, lib)
         return
-    with torch.cuda.device(t.device):
+    with torch.cuda.device(index):
         _check(fn(*args), lib)
 
 
@@ -223,6 +234,7 @@ class KVPool:
         self.dtype = dtype
         self.device = device
         self.shape = (num_blocks, num_kv_heads, block_size, head_dim)
+        self._kv_heads, self._head_dim = num_kv_heads, head_dim
         handle = ctypes.c_void_p()
         _check(lib.kv_pool_create(ctypes.byref(self.cfg), _ptr(buffer), buffer.numel(),
                                   ctypes.byref(handle)), lib)
@@ -342,42 +354,58 @@ class KVPool:
         contiguous).  positions: int32 [n], or [axes, n] for a rope with several axes.  A negative
         slot writes no K and V; a token with a negative seq_id writes nothing, q_out neither
         (a new q_out holds zeros there).  Returns q_out, or None without q."""
-        n, Hkv, D = slot_mapping.shape[0], self.cfg.num_kv_heads, self.cfg.head_dim
-        fp8 = self.dtype == FP8
+        n, dt, fp8 = slot_mapping.shape[0], k.dtype, self.dtype == FP8
+        rows = (n, self._kv_heads, self._head_dim)
         if fp8:
             _need(k_scale is not None and v_scale is not None, "an E4M3 pool needs k_scale and v_scale")
-            _need(k.dtype in (torch.float32, torch.float16, torch.bfloat16), "k/v must be f32, f16 or bf16")
+            _need(dt in _ROW_DTYPES, "k/v must be f32, f16 or bf16")
+            k_scale, v_scale = float(k_scale), float(v_scale)
         else:
-            _need(k.dtype == self.dtype, "k/v dtype must match the pool")
-        _need(v.dtype == k.dtype and (q is None or q.dtype == k.dtype), "k, v and q share a dtype")
-        _need(k.shape == v.shape == (n, Hkv, D), "k and v must be [n_tokens, num_kv_heads, head_dim]")
+            _need(dt == self.dtype, "k/v dtype must match the pool")
+            k_scale = v_scale = 1.0
+        _need(v.dtype == dt, "k, v and q share a dtype")
+        _need(k.shape == rows and v.shape == rows, "k and v must be [n_tokens, num_kv_heads, head_dim]")
         _need(_rows_whole(k) and _rows_whole(v), "a token's k and v rows must be contiguous")
-        _need(slot_mapping.dtype == torch.int32 and slot_mapping.is_contiguous(), "slot_mapping must be int32 [n_tokens]")
-        _need(seq_ids is None or (seq_ids.dtype == torch.int32 and seq_ids.shape == (n,) and seq_ids.is_contiguous()),
-              "seq_ids must be int32 [n_tokens]")
-        _need(positions.dtype == torch.int32 and positions.stride(-1) in (0, 1) if n > 1 else positions.dtype == torch.int32,
-              "positions must be int32, contiguous along tokens")
-        _need(positions.shape == (rope.num_axes, n) or (rope.num_axes == 1 and positions.shape == (n,)),
-              "positions must be [n_tokens], or [axes, n_tokens]")
-        if n > 1 and positions.stride(-1) == 0:
+        _need(slot_mapping.dtype == torch.int32 and slot_mapping.dim() == 1 and slot_mapping.is_contiguous(),
+              "slot_mapping must be int32 [n_tokens]")
+        _need(positions.dtype == torch.int32, "positions must be int32")
+        axes = rope.num_axes
+        if positions.dim() == 2:
+            _need(positions.shape == (axes, n), "positions must be [n_tokens], or [axes, n_tokens]")
+        else:
+            _need(axes == 1 and positions.shape == (n,), "positions must be [n_tokens], or [axes, n_tokens]")
+        if n > 1 and positions.stride(-1) != 1:
             positions = positions.contiguous()
+        positions_stride = positions.stride(0) if axes > 1 else n
+        index = self.device.index
+        on = (k.get_device() == index and v.get_device() == index and slot_mapping.get_device() == index
+              and positions.get_device() == index)
+        ids = None
+        if seq_ids is not None:
+            _need(seq_ids.dtype == torch.int32 and seq_ids.shape == (n,) and seq_ids.is_contiguous(),
+                  "seq_ids must be int32 [n_tokens]")
+            on = on and seq_ids.get_device() == index
+            ids = seq_ids.data_ptr()
         if q is not None:
-            _need(q.dim() == 3 and q.shape[0] == n and q.shape[2] == D and _rows_whole(q),
+            _need(q.dtype == dt, "k, v and q share a dtype")
+            _need(q.dim() == 3 and q.shape[0] == n and q.shape[2] == rows[2] and _rows_whole(q),
                   "q must be [n_tokens, num_q_heads, head_dim], a token's rows contiguous")
             if q_out is None:
                 make = torch.empty if seq_ids is None else torch.zeros
-                q_out = make(q.shape, dtype=q.dtype, device=q.device)
-            _need(q_out.dtype == q.dtype and q_out.shape == q.shape and _rows_whole(q_out), "q_out must be like q")
+                q_out = make(q.shape, dtype=dt, device=q.device)
+            _need(q_out.dtype == dt and q_out.shape == q.shape and _rows_whole(q_out), "q_out must be like q")
+            on = on and q.get_device() == index and q_out.get_device() == index
+            query = (q.data_ptr(), q.stride(0), q_out.data_ptr(), q_out.stride(0), q.shape[1])
         else:
             _need(q_out is None, "q_out without q")
-        _need(all(t is None or t.device == self.device for t in (k, v, slot_mapping, positions, seq_ids, q, q_out)),
-              "every tensor must be on the pool's device")
-        _check(self._lib.kv_append_rope(
-            self._handle, layer, rope._handle, _ptr(seq_ids), n, _ptr(k), k.stride(0), _ptr(v), v.stride(0),
-            DTYPE_CODE[k.dtype], _ptr(slot_mapping), _ptr(positions),
-            positions.stride(0) if positions.dim() == 2 else n, _ptr(q), 0 if q is None else q.stride(0), _ptr(q_out),
-            0 if q is None else q_out.stride(0), 0 if q is None else q.shape[1], float(k_scale) if fp8 else 1.0,
-            float(v_scale) if fp8 else 1.0, _stream(self.buffer, stream)), self._lib)
+            query = (None, 0, None, 0, 0)
+        _need(on, "every tensor must be on the pool's device")
+        status = self._lib.kv_append_rope(
+            self._handle, layer, rope._handle, ids, n, k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0),
+            DTYPE_CODE[dt], slot_mapping.data_ptr(), positions.data_ptr(), positions_stride, *query, k_scale, v_scale,
+            _stream(self.buffer, stream))
+        if status:
+            _check(status, self._lib)
         return q_out
 
     def close(self):
@@ -671,7 +699,7 @@ def paged_shared_prefix_attention(q, k_cache, v_cache, block_tables, context_len
     no group, is read through its own table throughout.  The other arguments are those of
     paged_decode_attention; q f16 or bf16, block_size a multiple of 16.
     """
-    lib = load_library()
+    lib = _lib or load_library()
     B, Hq, D = q.shape
     NB, Hkv, bs, D2 = k_cache.shape
     _need(D == D2 and v_cache.shape == k_cache.shape, "cache shapes")
@@ -681,32 +709,38 @@ def paged_shared_prefix_attention(q, k_cache, v_cache, block_tables, context_len
               "an E4M3 cache needs both caches E4M3 and k_scale, v_scale")
     else:
         _need(q.dtype == k_cache.dtype == v_cache.dtype, "q and the caches share a dtype")
-    tables = (block_tables, context_lens, group_start, prefix_lens)
-    _need(all(t.is_contiguous() for t in (q, k_cache, v_cache) + tables), "contiguous inputs")
-    _need(all(t.dtype == torch.int32 for t in tables), "int32 tables")
+    i32 = torch.int32
+    _need(block_tables.dtype == i32 and context_lens.dtype == i32 and group_start.dtype == i32
+          and prefix_lens.dtype == i32, "int32 tables")
+    _need(q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous() and block_tables.is_contiguous()
+          and context_lens.is_contiguous() and group_start.is_contiguous() and prefix_lens.is_contiguous(),
+          "contiguous inputs")
     _need(block_tables.dim() == 2 and block_tables.shape[0] == B and context_lens.shape == (B,),
           "one table row and length per sequence")
+    _need(prefix_lens.dim() == 1, "prefix_lens [groups]")
     groups = prefix_lens.shape[0]
-    _need(prefix_lens.dim() == 1 and group_start.shape == (groups + 1,), "group_start [groups + 1], prefix_lens [groups]")
+    _need(group_start.shape == (groups + 1,), "group_start [groups + 1]")
     out_dtype = out_dtype or q.dtype
     if out is None:
         out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
-    _need(out.dtype == out_dtype and out.shape == (B, Hq, D) and out.is_contiguous(), "out")
+    _need(out.dtype == out_dtype and out.shape == q.shape and out.is_contiguous(), "out")
     if workspace is None:
         workspace = make_shared_prefix_workspace(B, groups, Hq, Hkv, D, q.device)
-    _need(all(t.device == q.device for t in (k_cache, v_cache, out, workspace) + tables),
-          "every tensor must be on q's device")
+    index = q.get_device()
+    _need(k_cache.get_device() == index and v_cache.get_device() == index and out.get_device() == index
+          and workspace.get_device() == index and block_tables.get_device() == index
+          and context_lens.get_device() == index and group_start.get_device() == index
+          and prefix_lens.get_device() == index, "every tensor must be on q's device")
+    sizes = (NB, block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, group_start.data_ptr(),
+             prefix_lens.data_ptr(), groups, Hq, Hkv, D, bs)
+    rest = (float(scale), out.data_ptr(), DTYPE_CODE[out_dtype], workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream(q, stream))
     if fp8:
-        _call_on(q, lib, lib.paged_shared_prefix_attention_fp8,
-                 _ptr(q), DTYPE_CODE[q.dtype], _ptr(k_cache), _ptr(v_cache), float(k_scale), float(v_scale), NB,
-                 _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), B, _ptr(group_start), _ptr(prefix_lens),
-                 groups, Hq, Hkv, D, bs, float(scale), _ptr(out), DTYPE_CODE[out_dtype], _ptr(workspace),
-                 workspace.numel(), _stream(q, stream))
-        return out
-    _call_on(q, lib, lib.paged_shared_prefix_attention,
-             _ptr(q), _ptr(k_cache), _ptr(v_cache), NB, _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), B,
-             _ptr(group_start), _ptr(prefix_lens), groups, Hq, Hkv, D, bs, DTYPE_CODE[q.dtype], float(scale), _ptr(out),
-             DTYPE_CODE[out_dtype], _ptr(workspace), workspace.numel(), _stream(q, stream))
+        _call_on(q, lib, lib.paged_shared_prefix_attention_fp8, q.data_ptr(), DTYPE_CODE[q.dtype], k_cache.data_ptr(),
+                 v_cache.data_ptr(), float(k_scale), float(v_scale), *sizes, *rest)
+    else:
+        _call_on(q, lib, lib.paged_shared_prefix_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                 *sizes, DTYPE_CODE[q.dtype], *rest)
     return out
 
 

@@ -18,7 +18,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "lib")
 LIBRARY = os.path.join(LIB_DIR, "libpkv.so")
 SOURCES = ["append.cu", "rope.cu", "decode_plan.cu", "decode_ffma.cu", "decode_mma.cu", "decode_fp8.cu",
-           "decode_static.cu", "decode_tails.cu", "shared_prefix.cu",
+           "decode_static.cu", "shared_prefix.cu", "shared_prefix_f16.cu",
+           "shared_prefix_bf16.cu", "shared_prefix_fp8.cu",
            "prefix_pool.cpp", "swap.cu", "prefill.cu", "prefill_tc.cu",
            "pkv_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

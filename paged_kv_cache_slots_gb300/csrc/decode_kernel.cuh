@@ -111,16 +111,16 @@ __device__ __forceinline__ int clamp_context(const DecodeArgs& a, int s, bool fl
 
 // cum[s] = chunks * sum_{s' < s, ctx_s' > 0} (ceil(ctx_s' / bs) + phantom);
 // cum[num_seqs] = W.  kTails: ctx is what follows skip[s] shared blocks.
-// Returns the CTAs that share the items (kTails: the SMs that the prefix's
-// parts leave; else the grid).
+// Returns the CTAs that share the items (kTails: those that the prefix's parts
+// leave, see *units; else the grid).
 template <bool kTails>
-static __device__ int build_prefix(const DecodeArgs& a, int chunks, int32_t* cum, int32_t* scan, int32_t* skip) {
-    [[maybe_unused]] Units units;
+static __device__ int build_prefix(const DecodeArgs& a, int chunks, int32_t* cum, int32_t* scan, int32_t* skip,
+                                   [[maybe_unused]] Units* units) {
     [[maybe_unused]] int first_ctx = 0;  // of this thread's first sequence, asked for before the groups are looked at
     if constexpr (kTails) {
         if (threadIdx.x < a.num_seqs) first_ctx = clamp_context(a, threadIdx.x, blockIdx.x == 0);
-        units = plan_units(a, a.num_q_heads / a.num_kv_heads);
-        if (units.bad && threadIdx.x == 0 && blockIdx.x == 0) raise_flag(a.status, kFlagBadGroup);
+        *units = plan_units(a, a.num_q_heads / a.num_kv_heads);
+        if (units->bad && threadIdx.x == 0 && blockIdx.x == 0) raise_flag(a.status, kFlagBadGroup);
     }
     [[maybe_unused]] int64_t tokens = 0;  // of this thread's sequences, after their shared blocks
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -133,7 +133,7 @@ static __device__ int build_prefix(const DecodeArgs& a, int chunks, int32_t* cum
             const int c = kTails && base == 0 ? first_ctx : clamp_context(a, s, blockIdx.x == 0);
             int nb = (c + a.block_size - 1) / a.block_size;
             if constexpr (kTails) {
-                const int sb = units.bad ? 0 : shared_blocks(a, s, c);
+                const int sb = units->bad ? 0 : shared_blocks(a, s, c);
                 skip[s] = sb;
                 nb -= sb;
                 tokens += c - sb * a.block_size;
@@ -173,8 +173,8 @@ static __device__ int build_prefix(const DecodeArgs& a, int chunks, int32_t* cum
         __syncthreads();
         tokens = 0;
         for (int w = 0; w < nwarps; ++w) tokens += sums[w];
-        divide_sms(a, tokens, &units);
-        ctas -= units.P;
+        divide_sms(a, tokens, units);
+        ctas -= units->P;
     }
     __syncthreads();
     return ctas;
@@ -681,21 +681,15 @@ __device__ __forceinline__ bool append_row(const DecodeArgs& a, const Policy& po
 // Policy provides: State, begin(), tile(), write_state(), write_partial(),
 // write_final(), kTensor, kScratch, kPairs (and tile2() when kPairs), and
 // kMaxThreads, the largest block it is launched with (its register budget).
-// kTails: the variant that attends to what follows a shared prefix
-// (shared_prefix.cu): it skips the prefix's table entries and writes a partial
-// for every segment, whole pairs too, for the merge with the prefix's parts
-// (launched with fused_reduce 0 and without an append).  It neither reads what
-// the launch before it (the parts kernel) writes nor writes what that one
-// reads, and that launch's CTAs let it start only after their own wait; so it
-// runs beside that launch and waits for it at its own end, for the merge.
+// kTails: the variant that attends to what follows a shared prefix, as one of
+// the two roles of the shared-prefix kernel (shared_prefix_kernel.cuh): it
+// skips the prefix's table entries and writes a partial for every segment,
+// whole pairs too, for the merge with the prefix's parts (fused_reduce 0, no
+// append).  Its CTAs are the grid's first; false on the others, which have
+// touched nothing but shared memory and have *units.
 template <class Policy, bool kTails>
-__global__ void __launch_bounds__(Policy::kMaxThreads, 1)
-    paged_decode_partial_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmk,
-                                const __grid_constant__ CUtensorMap tmv) {
-    extern __shared__ uint8_t smem_raw[];
-    pdl_allow_next();
-    uint8_t* base = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+__device__ __forceinline__ bool decode_cta(const DecodeArgs& a, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                                           uint8_t* base, [[maybe_unused]] Units* units) {
     const int G = a.num_q_heads / a.num_kv_heads;
     const int Hc = a.heads_per_stage, R = a.warps_per_head, NC = a.consumer_warps;
     const int chunks = a.num_kv_heads / Hc;
@@ -715,7 +709,12 @@ __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
     const int tid = threadIdx.x;
     if (a.stages % R != 0) {  // see decode_plan: the ring must be a multiple of R
         if (tid == 0 && blockIdx.x == 0) raise_flag(a.status, kFlagBadPlan);
-        return;
+        return true;
+    }
+    int P = a.num_ctas;
+    if constexpr (kTails) {
+        P = build_prefix<true>(a, chunks, cum, scan, skip, units);  // ends with __syncthreads
+        if (static_cast<int>(blockIdx.x) >= P) return false;
     }
     if (tid == 0) {
         for (int st = 0; st < a.stages; ++st) {
@@ -729,26 +728,26 @@ __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
             prefetch_tensor_map(&tmv);
         }
     }
-    // Everything above touches only this CTA's shared memory and parameters.
-    // With early_reads the caller promises that the previous launch on the
-    // stream writes neither the tables, the lengths nor the K/V cache, so the
-    // prefix, the table entries and the first stages are fetched while that
-    // launch finishes; everything else (q, the new rows, the workspace, the
-    // outputs) is touched only after waiting for it.
-    if (!kTails && !a.early_reads) pdl_wait();
-    const int P = build_prefix<kTails>(a, chunks, cum, scan, skip);  // ends with __syncthreads
-    const int64_t W = cum[a.num_seqs];
-    if (kTails && static_cast<int>(blockIdx.x) >= P) {
-        pdl_wait();
-        return;
+    if constexpr (kTails) {
+        __syncthreads();
+    } else {
+        // Everything above touches only this CTA's shared memory and parameters.
+        // With early_reads the caller promises that the previous launch on the
+        // stream writes neither the tables, the lengths nor the K/V cache, so the
+        // prefix, the table entries and the first stages are fetched while that
+        // launch finishes; everything else (q, the new rows, the workspace, the
+        // outputs) is touched only after waiting for it.
+        if (!a.early_reads) pdl_wait();
+        build_prefix<false>(a, chunks, cum, scan, skip, units);  // ends with __syncthreads
     }
+    const int64_t W = cum[a.num_seqs];
     const int start = static_cast<int>(static_cast<int64_t>(blockIdx.x) * W / P);
     const int end = static_cast<int>((static_cast<int64_t>(blockIdx.x) + 1) * W / P);
     const int warp = tid >> 5, lane = tid & 31;
     if (warp == 0 && start < end) {
         produce<Policy::kTensor, kTails>(a, ring, full, empty, cum, skip, chunks, start, end, half_bytes, &tmk,
                                  &tmv, abort);
-        return;
+        return true;
     }
     if (!kTails && a.early_reads) pdl_wait();
     // Global writes of the prologue, by the threads that are not producing.
@@ -760,25 +759,24 @@ __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
             const int nbv = (cum[s + 1] - cum[s]) / chunks;
             a.tail_parts[p] = tail_parts_of(cum[s] + (p - s * chunks) * nbv + a.phantom, nbv - a.phantom, W, P);
         }
-        // Sequences without prefix parts (the parts kernel speaks for the others).
+        // Sequences without prefix parts (the parts role speaks for the others).
         for (int p = blockIdx.x + P * wt; p < a.num_seqs * a.num_kv_heads; p += P * nwt)
             if (skip[p / a.num_kv_heads] == 0) a.prefix_parts[p] = make_int4(0, 0, 0, 0);
+        if (warp > NC) return true;  // the grid's blocks are as large as the parts role needs
+    } else {
+        if (blockIdx.x == 0 && !a.fused_reduce) {
+            for (int s = wt; s <= a.num_seqs; s += nwt) a.cum[s] = cum[s];
+        }
+        // Sequences with no tokens: zero rows (fused merge) and slot -1 (CTA s mod P).
+        for (int s = blockIdx.x; s < a.num_seqs; s += P) {
+            if (cum[s + 1] != cum[s]) continue;
+            if (a.slot_out && wt == 0) a.slot_out[s] = -1;
+            if (!a.fused_reduce) continue;
+            const int64_t o0 = static_cast<int64_t>(s) * a.num_q_heads * D;
+            for (int e = wt; e < a.num_q_heads * D; e += nwt) store_out(a.out, o0 + e, 0.f, a.out_dtype);
+        }
     }
-    if (!kTails && blockIdx.x == 0 && !a.fused_reduce) {
-        for (int s = wt; s <= a.num_seqs; s += nwt) a.cum[s] = cum[s];
-    }
-    // Sequences with no tokens: zero rows (fused merge) and slot -1 (CTA s mod P).
-    for (int s = blockIdx.x; s < a.num_seqs; s += P) {
-        if (cum[s + 1] != cum[s]) continue;
-        if (a.slot_out && wt == 0) a.slot_out[s] = -1;
-        if (!a.fused_reduce) continue;
-        const int64_t o0 = static_cast<int64_t>(s) * a.num_q_heads * D;
-        for (int e = wt; e < a.num_q_heads * D; e += nwt) store_out(a.out, o0 + e, 0.f, a.out_dtype);
-    }
-    if (start >= end) {
-        if constexpr (kTails) pdl_wait();
-        return;
-    }
+    if (start >= end) return true;
 
     const int w = warp - 1;
     const int hw = w % Hc;  // head within the chunk
@@ -928,22 +926,32 @@ __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
         }
         seg = seg_end;
     }
-    if constexpr (kTails) pdl_wait();
+    return true;
+}
+
+template <class Policy>
+__global__ void __launch_bounds__(Policy::kMaxThreads, 1)
+    paged_decode_partial_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmk,
+                                const __grid_constant__ CUtensorMap tmv) {
+    extern __shared__ uint8_t smem_raw[];
+    pdl_allow_next();
+    uint8_t* base = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    decode_cta<Policy, false>(a, tmk, tmv, base, nullptr);
 }
 
 // Launch the partial kernel of `Policy`.  The dynamic shared-memory limit is
 // raised once per device (not on every launch, so that launches captured in
 // a CUDA graph make no attribute calls).
-template <class Policy, bool kTails = false>
+template <class Policy>
 cudaError_t launch_partial(const DecodeArgs& a, const CUtensorMap& tmk, const CUtensorMap& tmv,
                            cudaStream_t stream) {
     static std::atomic<int> configured[64];
-    auto kern = paged_decode_partial_kernel<Policy, kTails>;
+    auto kern = paged_decode_partial_kernel<Policy>;
     const bool cacheable = a.device >= 0 && a.device < 64;
     if (!cacheable || configured[a.device].load() < a.smem_bytes) {
         cudaError_t e =
             cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, a.smem_bytes);
-        if (kTails && e == cudaSuccess) e = prefer_shared_memory(kern);
         if (e != cudaSuccess) return e;
         if (cacheable) configured[a.device].store(a.smem_bytes);
     }

@@ -1198,11 +1198,9 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 *
                                       static_cast<double>(fp8 ? k_scale : 1.f));
     a.v_scale = fp8 ? v_scale : 1.f;
-    a.num_ctas = sms;
     a.max_rows = w.max_rows;
-    a.device = dev;
-    a.smem_bytes = prefix_smem_bytes(head_dim, fp8);
-    if (a.smem_bytes > max_smem) return fail(KV_ERR_UNSUPPORTED, "%s: not enough shared memory on this device", what);
+    const int parts_smem = prefix_smem_bytes(head_dim, fp8);
+    if (parts_smem > max_smem) return fail(KV_ERR_UNSUPPORTED, "%s: not enough shared memory on this device", what);
 
     DecodeArgs d{};
     d.q = q;
@@ -1239,7 +1237,7 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     d.warps_per_head = R;
     d.consumer_warps = hc * R;
     d.stages = plan.stages;
-    d.smem_bytes = plan.smem_bytes;
+    d.smem_bytes = plan.smem_bytes > parts_smem ? plan.smem_bytes : parts_smem;
     d.fused_reduce = 0;
     d.pdl = 1;
     d.phantom = phantom_items(num_seqs, num_kv_heads / hc, max_blocks, sms, plan.stage_half_bytes);
@@ -1250,10 +1248,8 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     if (kv_status_t st = encode_cache_map(&tv, v_cache, kv_dtype, rows, head_dim, hc * block_size)) return st;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_prefix_parts(a, s);
-    if (e != cudaSuccess) return cuda_fail(e, "prefix parts launch");
-    if ((e = launch_decode_tails(d, tk, tv, s)) != cudaSuccess) return cuda_fail(e, "tails launch");
-    if ((e = launch_prefix_merge(a, d, s)) != cudaSuccess) return cuda_fail(e, "prefix merge launch");
+    const cudaError_t e = launch_shared_prefix(a, d, tk, tv, s);
+    if (e != cudaSuccess) return cuda_fail(e, "shared-prefix launch");
     return KV_OK;
 }
 

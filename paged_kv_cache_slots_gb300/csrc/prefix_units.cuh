@@ -111,14 +111,16 @@ __device__ __forceinline__ Units plan_units(const Args& a, int G) {
 // The parts kernel's share of the SMs, u->P; the tails kernel takes the rest.
 // tail_tokens: tokens of all sequences after their shared blocks.
 //
-// A tile of 128 rows costs a parts CTA about kTileNs, a cached token of one KV
-// head a tails CTA about its bytes at the SM's share of the memory rate.
+// A tile costs a parts CTA about kTileNs (of 128-element rows), the start and
+// end of a triple kTripleNs; the tails' bytes cost their time at an SM's share
+// of the memory rate.
 template <class Args>
 __device__ __forceinline__ void divide_sms(const Args& a, int64_t tail_tokens, Units* u) {
-    constexpr float kTileNs = 600.f, kNsPerByte = 1.f / 42.f;
+    constexpr float kTripleNs = 3000.f, kNsPerByte = 1.f / 42.f;
+    const float kTileNs = a.head_dim == 64 ? 560.f : 1000.f;
     const int sms = a.num_ctas;
     if (u->W == 0) return;
-    const float parts = kTileNs * static_cast<float>(u->W);
+    const float parts = kTileNs * static_cast<float>(u->W) + kTripleNs * static_cast<float>(u->triples);
     const float tails = kNsPerByte * 2.f * static_cast<float>(tail_tokens) *
                         static_cast<float>(a.num_kv_heads * a.head_dim * dtype_bytes(a.kv_dtype));
     int P = static_cast<int>(static_cast<float>(sms) * parts / (parts + tails) + 0.5f);

@@ -1,648 +1,19 @@
-// Decode attention of a batch in which groups of sequences share the blocks
-// of a long prefix ("Reading Inference Engine Codebases", Examples 12 and 13:
-// requests with equal prompts are given the same cached blocks): each group's
-// prefix is read once for all its members.
-//
-// The mathematics.  For one query row, softmax over a set of keys cut into
-// parts needs of each part only m = max score (or any reference), l = sum of
-// 2^(score - m) and O = sum of 2^(score - m) V; the whole is
-// sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  A group's prefix is
-// attended to by all members alike, without a mask, so its scores are one
-// matrix product per KV head: rows = (member, query head of the KV head),
-// columns = prefix keys.  What follows the prefix differs per sequence and is
-// left to the split-context decode kernel.  Three launches:
-//   parts   (this file's main kernel) (m, l, O) of 128 rows over a chunk of a
-//           group's keys, one CTA a (group, KV head, row tile, chunk);
-//   tails   the decode kernel over the tokens after the prefix, partials only;
-//   merge   one warp a (sequence, query head).
-// parts and tails are independent and run side by side as far as there is
-// room.  Which sequences share (those at least as long as the prefix; shorter
-// ones read their own tables throughout) and how the keys are cut follows from
-// the groups alone, so every CTA works it out for itself: one warp-wide pass
-// over the groups costs less than a launch that does it for all.
-//
-// The parts kernel is built like the prefill kernel (prefill_tc.cu): a
-// producer brings K and V tiles of 64 keys into swizzled shared memory, one
-// lane issues tcgen05 MMAs S = Q K^T (tensor memory, two buffers) and
-// O += P V (P read from tensor memory), four warps hold the softmax, one row a
-// thread.  P enters the product as a high and a low half-precision part, so
-// that the result carries fp32-like weights whatever the output type.
-#include "decode_kernel.cuh"
-#include "mma_frag.cuh"
+// The merge of the shared-prefix attention's parts and the choice of its
+// kernels (see shared_prefix_kernel.cuh).
+#include <atomic>
+
+#include "prefix_units.cuh"
 #include "shared_prefix.cuh"
-#include "tc_utils.cuh"
 
 namespace pkv {
 
 namespace {
 
-// ------------------------------------------------------------------ parts
-
-constexpr int kBM = kPrefixRows;
-constexpr int kNK = kPrefixTile;
-constexpr int kS = 4;                // S / P buffers in tensor memory, 64 columns each
-constexpr uint32_t kO = kS * kNK;    // the two accumulators, D columns each
-constexpr uint32_t kTmemCols = 512;
-constexpr float kLazy = 8.f;
-constexpr int kIssuers = 2;          // warps that issue MMAs
-
-template <int D, bool kFP8>
-struct Shape {
-    static constexpr int kSlices = D / 64;                    // 128-byte slices of a row
-    static constexpr int kKRing = D == 128 ? 4 : 8;           // K stages
-    static constexpr int kVRing = D == 128 ? 3 : 6;           // V stages
-    static constexpr uint32_t kTile = kSlices * kNK * 128;    // bytes of a K (or V) tile
-    static constexpr int kProducers = 2;                      // producer warps
-    static constexpr int kThreads = 32 * (8 + kIssuers + kProducers);
-    // E4M3: codes on their way, a ring for each producer warp: 32 rows of K and of V.
-    static constexpr int kRawRing = kFP8 ? 4 : 0;
-    static constexpr uint32_t kRawStage = 2 * 32 * 128;
-    static constexpr uint32_t kQOff = 0;
-    static constexpr uint32_t kKOff = kSlices * kBM * 128;
-    static constexpr uint32_t kVOff = kKOff + kKRing * kTile;
-    static constexpr uint32_t kRawOff = kVOff + kVRing * kTile;
-    static constexpr uint32_t kBarOff = kRawOff + kProducers * kRawRing * kRawStage;
-};
-
-struct Bars {
-    uint64_t kfull[8], kempty[8], vfull[6], vempty[6];
-    uint64_t s_full[kS], p_full[kS], pv_done[kS], q_full;
-    uint64_t raw[2][4];
-    float2 ml[2][kBM];  // (reference, sum) of each row in each softmax group
-    uint32_t tmem;
-    int abort;
-};
-
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
-    return mbar_wait_bounded(bar, parity & 1u, abort, status);
-}
-
-// 16 bytes global -> shared, or 16 zero bytes.
-__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool real) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
-}
-
-// 32 bytes to global memory (a whole sector at once).
-__device__ __forceinline__ void store_32(float* p, const float* v) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(__float_as_uint(v[0])),
-                 "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
-                 "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])),
-                 "r"(__float_as_uint(v[7]))
-                 : "memory");
-}
-
-// One lane of a converged warp.
-__device__ __forceinline__ uint32_t elect_one() {
-    uint32_t one;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
-    return one;
-}
-
-// tc_mma, tc_mma_ts and tc_commit issued by the lane with leader != 0 while the
-// whole warp walks the loop: addresses and descriptors are then the same on
-// every lane, and the compiler can keep them in uniform registers.
-__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                       bool accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
-        : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
-                                       bool accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
-        : "memory");
-}
-__device__ __forceinline__ void mma_commit(uint32_t leader, uint32_t bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
-        "r"(leader)
-        : "memory");
-}
-
-// Eight E4M3 codes -> eight f16 values, exactly, times 2^-8.
-__device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
-    return make_uint4(e4m3x2_odd_bytes_to_half2_shifted(__byte_perm(lo, 0u, 0x1404)),
-                      e4m3x2_odd_bytes_to_half2_shifted(__byte_perm(lo, 0u, 0x3424)),
-                      e4m3x2_odd_bytes_to_half2_shifted(__byte_perm(hi, 0u, 0x1404)),
-                      e4m3x2_odd_bytes_to_half2_shifted(__byte_perm(hi, 0u, 0x3424)));
-}
-
-// Tokens after the shared blocks, of all sequences: by the whole CTA.
-__device__ __forceinline__ int64_t count_tail_tokens(const SharedPrefixArgs& a, int64_t* sums) {
-    int64_t tokens = 0;
-    for (int s = threadIdx.x; s < a.num_seqs; s += blockDim.x) {
-        const int c = min(max(a.context_lens[s], 0), a.max_blocks * a.block_size);
-        tokens += c - shared_blocks(a, s, c) * a.block_size;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) tokens += __shfl_xor_sync(0xffffffffu, tokens, o);
-    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = tokens;
-    __syncthreads();
-    tokens = 0;
-    for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) tokens += sums[w];
-    return tokens;
-}
-
-// QT: q's type.  The tensor cores work in it, or in f16 over an E4M3 cache
-// (whose codes widen to f16 in a few integer operations); a bf16 q is then
-// brought to f16 with a power of two for each row that puts its largest
-// element at 2^13: exact down to 2^-27 of that element.
-template <int QT, int D, bool kFP8>
-__global__ void __launch_bounds__(Shape<D, kFP8>::kThreads, 1) shared_prefix_parts_kernel(const SharedPrefixArgs a) {
-    using T = typename Elem<QT>::T;
-    using S = Shape<D, kFP8>;
-    constexpr int DT = kFP8 ? static_cast<int>(kF16) : QT;
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ int64_t sums[16];
-    pdl_wait();
-    pdl_allow_next();  // after the wait: the tails start when all that came before has completed
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int G = a.num_q_heads / a.num_kv_heads;
-    Units units = plan_units(a, G);
-    if (units.W == 0) return;
-    divide_sms(a, count_tail_tokens(a, sums), &units);
-    const int cta = blockIdx.x;
-    if (cta >= units.P) return;
-    const int start = mul_div(cta, units.W, units.P), end = mul_div(cta + 1, units.W, units.P);
-    // The swizzled layouts need a 1024-byte aligned base.
-    uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    Bars* B = reinterpret_cast<Bars*>(base + S::kBarOff);
-    volatile int* abort = &B->abort;
-    if (tid == 0) {
-        // A tile is full with one arrival a producer warp, or one a copying lane.
-        for (int i = 0; i < S::kKRing; ++i) {
-            mbar_init(&B->kfull[i], kFP8 ? S::kProducers : 32);
-            mbar_init(&B->kempty[i], 1);
-        }
-        for (int i = 0; i < S::kVRing; ++i) {
-            mbar_init(&B->vfull[i], kFP8 ? S::kProducers : 32);
-            mbar_init(&B->vempty[i], 1);
-        }
-        for (int i = 0; i < kS; ++i) {
-            mbar_init(&B->s_full[i], 1);
-            mbar_init(&B->p_full[i], 4);
-            mbar_init(&B->pv_done[i], 1);
-        }
-        mbar_init(&B->q_full, 8);
-        if constexpr (kFP8) {
-            for (int i = 0; i < 2 * S::kRawRing; ++i) mbar_init(&B->raw[i / S::kRawRing][i % S::kRawRing], 1);
-        }
-        B->abort = 0;
-        fence_barrier_init();
-    }
-    if (warp == 0) tc_alloc(&B->tmem, kTmemCols);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t taddr = B->tmem;
-
-    // Every role walks the CTA's segments; tiles are counted from the CTA's
-    // first (i), so rings and buffers go on over segments.
-    if (warp >= 8 + kIssuers) {
-        // ---- producers.  The keys come in runs of 16 rows (block_size is a
-        // multiple of 16), each inside one block; runs past the last key are
-        // zeros.
-        const int bs = a.block_size;
-        const int ch = lane & 7, l8 = lane >> 3;
-        const int w = warp - 8 - kIssuers;
-        int i = 0;  // tiles before the segment
-        [[maybe_unused]] int issued = 0;
-        bool ok = true;
-        for (int x = start; x < end && ok;) {
-            const Triple t = find_triple(a, units, G, x);
-            const int n = min(end, t.tile0 + t.keys) - x;  // tiles of the segment
-            const int key0 = (x - t.tile0) * kNK;
-            const int nruns = (min(t.blocks * bs, key0 + n * kNK) - key0) / 16;
-            // The member whose table row names the blocks; without one the
-            // segment's keys are zeros and nobody reads its part.
-            int lead = -1;
-            for (int s0 = 0; s0 * G < t.rows && lead < 0; s0 += 32) {
-                const int s = t.seq0 + s0 + lane;
-                const uint32_t in = __ballot_sync(0xffffffffu, (s0 + lane) * G < t.rows && a.context_lens[s] / bs >= t.blocks);
-                if (in) lead = t.seq0 + s0 + __ffs(in) - 1;
-            }
-            const int32_t* table = a.block_tables + static_cast<int64_t>(lead < 0 ? 0 : lead) * a.max_blocks;
-            // First cache row of run r of the segment; -1: zeros.
-            auto run_row = [&](int r) -> int {
-                if (r >= nruns || lead < 0) return -1;
-                const int key = key0 + 16 * r;
-                const int lb = key / bs;
-                int blk = table[lb];
-                if (blk < 0 || blk >= a.num_blocks) {
-                    raise_flag(a.status, kFlagBadBlock);
-                    blk = 0;
-                }
-                return (blk * a.num_kv_heads + t.h) * bs + (key - lb * bs);
-            };
-            if constexpr (!kFP8) {
-                // One warp brings the K tiles, the other the V tiles.  Lane l
-                // knows where run l of the current 8 tiles starts, and of the 8
-                // after them; lane e copies chunk e % 8 of rows e / 8 + 4 q of a
-                // run.
-                int now = run_row(lane), next = run_row(32 + lane);
-                const char* c0 = static_cast<const char*>(w == 0 ? a.k_cache : a.v_cache) + l8 * (D * 2) + ch * 16;
-                const uint32_t d0 = smem_addr(base + (w == 0 ? S::kKOff : S::kVOff)) + l8 * 128;
-                uint64_t* full = w == 0 ? B->kfull : B->vfull;
-                uint64_t* empty = w == 0 ? B->kempty : B->vempty;
-                const int ring = w == 0 ? S::kKRing : S::kVRing;
-                const uint32_t sw0 = static_cast<uint32_t>(ch ^ l8) << 4, sw1 = static_cast<uint32_t>(ch ^ (l8 + 4)) << 4;
-                int st = i % ring, round = i / ring;
-                for (int j = 0; j < n; ++j) {
-                    if ((j & 7) == 0 && j > 0) {
-                        now = next;
-                        next = run_row(4 * (j + 8) + lane);
-                    }
-                    if (round > 0) ok = __all_sync(0xffffffffu, wait(&empty[st], round - 1, abort, a.status));
-                    if (!ok) break;
-                    const uint32_t dst = d0 + st * S::kTile;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int row = __shfl_sync(0xffffffffu, now, (j & 7) * 4 + k);
-                        const bool real = row >= 0;
-                        const char* src = c0 + (real ? static_cast<int64_t>(row) * (D * 2) : 0);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint32_t d = dst + (16 * k + 4 * q) * 128 + ((q & 1) ? sw1 : sw0);
-#pragma unroll
-                            for (int sl = 0; sl < S::kSlices; ++sl)
-                                cp_async_16_or_zero(d + sl * (kNK * 128), src + (real ? q * (4 * D * 2) + sl * 128 : 0), real);
-                        }
-                    }
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&full[st])) : "memory");
-                    if (++st == ring) st = 0, ++round;
-                }
-            } else {
-                // E4M3: warp w brings runs 2 w and 2 w + 1 of every tile: the
-                // codes travel through a ring of its own and are widened into
-                // the tile.  Lane e takes codes 16 (e % 8) .. of rows e / 8 + 4 q.
-                const uint64_t policy = t.rows > kBM ? policy_evict_last() : policy_evict_first();
-                uint8_t* raw0 = base + S::kRawOff + w * (S::kRawRing * S::kRawStage);
-                int rows = -1;  // lane l: run 2 w + l % 2 of tile l / 2 of the current 16
-                auto ask = [&](int j) {  // in order, each tile once
-                    if ((j & 15) == 0) rows = run_row(4 * (j + (lane >> 1)) + 2 * w + (lane & 1));
-                    const int r0 = __shfl_sync(0xffffffffu, rows, 2 * (j & 15)), r1 = __shfl_sync(0xffffffffu, rows, 2 * (j & 15) + 1);
-                    if (j >= n) return;
-                    ++issued;
-                    if (lane == 0) {
-                        const int st = (i + j) % S::kRawRing;
-                        uint64_t* bar = &B->raw[w][st];
-                        const uint32_t bytes = (r0 >= 0 ? 2 * 16 * D : 0) + (r1 >= 0 ? 2 * 16 * D : 0);
-                        if (bytes == 0) {
-                            mbar_arrive(bar);
-                            return;
-                        }
-                        mbar_arrive_expect_tx(bar, bytes);
-                        uint8_t* d = raw0 + st * S::kRawStage;
-                        for (int k = 0; k < 2; ++k) {
-                            const int row = k ? r1 : r0;
-                            if (row < 0) continue;
-                            const int64_t off = static_cast<int64_t>(row) * D;
-                            bulk_load(d + k * 16 * D, static_cast<const char*>(a.k_cache) + off, 16 * D, bar, policy);
-                            bulk_load(d + (2 + k) * 16 * D, static_cast<const char*>(a.v_cache) + off, 16 * D, bar, policy);
-                        }
-                    }
-                };
-                auto put = [&](const uint8_t* raw, int real, uint32_t off, uint64_t* bar) {  // real: runs with codes
-                    uint8_t* tile = base + off + (ch >> 2) * (kNK * 128);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const uint4 r = q / 4 < real ? *reinterpret_cast<const uint4*>(raw + (4 * q + l8) * D + ch * 16)
-                                                     : make_uint4(0u, 0u, 0u, 0u);
-                        const int row = 32 * w + 4 * q + l8;
-                        const int c0 = (ch & 3) * 2;
-                        *reinterpret_cast<uint4*>(tile + row * 128 + ((c0 ^ (row & 7)) << 4)) = widen8(r.x, r.y);
-                        *reinterpret_cast<uint4*>(tile + row * 128 + (((c0 + 1) ^ (row & 7)) << 4)) = widen8(r.z, r.w);
-                    }
-                    fence_proxy_async_smem();  // the tile before the tensor cores read it, the codes before the next copy
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar);
-                };
-                for (int j = 0; j < S::kRawRing - 1; ++j) ask(j);
-                for (int j = 0; j < n && ok; ++j) {
-                    ask(j + S::kRawRing - 1);
-                    const int st = (i + j) % S::kRawRing;
-                    const int real = lead < 0 ? 0 : min(max(nruns - 4 * j - 2 * w, 0), 2);
-                    ok = __all_sync(0xffffffffu, wait(&B->raw[w][st], (i + j) / S::kRawRing, abort, a.status));
-                    if (!ok) break;
-                    const uint8_t* raw = raw0 + st * S::kRawStage;
-                    const int sk = (i + j) % S::kKRing, sv = (i + j) % S::kVRing;
-                    if (i + j >= S::kKRing)
-                        ok = __all_sync(0xffffffffu, wait(&B->kempty[sk], (i + j) / S::kKRing - 1, abort, a.status));
-                    if (!ok) break;
-                    put(raw, real, S::kKOff + sk * S::kTile, &B->kfull[sk]);
-                    if (i + j >= S::kVRing)
-                        ok = __all_sync(0xffffffffu, wait(&B->vempty[sv], (i + j) / S::kVRing - 1, abort, a.status));
-                    if (!ok) break;
-                    put(raw + 2 * 16 * D, real, S::kVOff + sv * S::kTile, &B->vfull[sv]);
-                }
-            }
-            i += n;
-            x += n;
-        }
-        // Every copy issued must land before the CTA can exit.
-        if constexpr (kFP8) {
-            if (lane == 0) {
-                for (int st = 0; st < S::kRawRing && st < issued; ++st) {
-                    const int last = st + ((issued - 1 - st) / S::kRawRing) * S::kRawRing;
-                    const uint64_t t0 = global_timer_ns();
-                    while (!mbar_try_wait(&B->raw[w][st], (last / S::kRawRing) & 1)) {
-                        if (global_timer_ns() - t0 > kWaitLimitNs) {
-                            raise_flag(a.status, kFlagTimeout);
-                            break;
-                        }
-                    }
-                }
-            }
-        } else {
-            asm volatile("cp.async.wait_all;" ::: "memory");
-        }
-        __syncwarp();
-    } else if (warp >= 8) {
-        // ---- MMA issue.  Each of the kIssuers warps issues for its own tiles
-        // (all, or those of one parity): S runs ahead of P V by kAhead of them.
-        constexpr int bf = DT == kBF16 ? 1 : 0;
-        constexpr uint32_t idS = tc_idesc_f16(bf, false, kNK, kBM);
-        constexpr uint32_t idPV = tc_idesc_f16(bf, true, D, kBM);
-        constexpr int kStep = kIssuers, kAhead = kS / kIssuers - 1;
-        const int me = warp - 8;
-        const uint32_t leader = elect_one();
-        const uint32_t sbase = smem_addr(base), bars = smem_addr(B);
-        auto bar_of = [&](const uint64_t* p) { return bars + static_cast<uint32_t>(reinterpret_cast<const uint8_t*>(p) - reinterpret_cast<const uint8_t*>(B)); };
-        // All tensor memory is this CTA's: its addresses start at 0.
-        const uint64_t qd = tc_sdesc(sbase + S::kQOff, 16, 1024);
-        auto ready = [&](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, wait(bar, phase, abort, a.status)) != 0; };
-        auto score = [&](int i) -> bool {
-            const int sk = i % S::kKRing, b = i % kS;
-            if (!ready(&B->kfull[sk], i / S::kKRing)) return false;
-            // S buffer b holds P of tile i - kS until that PV has completed.
-            if (i >= kS && !ready(&B->pv_done[b], i / kS - 1)) return false;
-            if constexpr (!kFP8) fence_proxy_async_smem();  // lane copies before the tensor cores read them
-            tc_fence_after();
-            const uint64_t kd = tc_sdesc(sbase + S::kKOff + sk * S::kTile, 16, 1024);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-                mma_ss(leader, b * kNK, qd + (((ks >> 2) * (kBM * 128) + (ks & 3) * 32) >> 4),
-                       kd + (((ks >> 2) * (kNK * 128) + (ks & 3) * 32) >> 4), idS, ks > 0);
-            mma_commit(leader, bar_of(&B->s_full[b]));
-            mma_commit(leader, bar_of(&B->kempty[sk]));
-            return true;
-        };
-        auto pv = [&](int i, bool first) -> bool {
-            const int sv = i % S::kVRing, b = i % kS;
-            if (!ready(&B->p_full[b], i / kS)) return false;
-            if (!ready(&B->vfull[sv], i / S::kVRing)) return false;
-            if constexpr (!kFP8) fence_proxy_async_smem();
-            tc_fence_after();
-            const uint64_t vd = tc_sdesc(sbase + S::kVOff + sv * S::kTile, kNK * 128, 1024);
-            const uint32_t o = kO + (i & 1) * D;
-#pragma unroll
-            for (int part = 0; part < 2; ++part)
-#pragma unroll
-                for (int kk = 0; kk < kNK / 16; ++kk)
-                    mma_ts(leader, o, b * kNK + part * 32 + kk * 8, vd + ((kk * 16 * 128) >> 4), idPV,
-                           !(first && part == 0 && kk == 0));
-            mma_commit(leader, bar_of(&B->pv_done[b]));
-            mma_commit(leader, bar_of(&B->vempty[sv]));
-            return true;
-        };
-        int i = 0, seg = 0;
-        bool ok = true;
-        for (int x = start; x < end && ok; ++seg) {
-            const Triple t = find_triple(a, units, G, x);
-            const int n = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(min(end, t.tile0 + t.keys) - x)));
-            const int j0 = kIssuers == 1 ? 0 : (me ^ i) & 1;
-            ok = ready(&B->q_full, seg);
-            for (int j = j0, k = 0; j < n && k < kAhead && ok; j += kStep, ++k) ok = score(i + j);
-            for (int j = j0; j < n && ok; j += kStep) {
-                // With one issuer P V goes first: S of the tile after next waits for
-                // the P V before it, which has just been queued behind.
-                if constexpr (kIssuers == 1) {
-                    ok = pv(i + j, j < 2);
-                    if (ok && j + kAhead < n) ok = score(i + j + kAhead);
-                } else {
-                    if (j + kAhead * kStep < n) ok = score(i + j + kAhead * kStep);
-                    if (ok) ok = pv(i + j, j < 2);
-                }
-            }
-            i += n;
-            x += n;
-        }
-    } else {
-        // ---- softmax: two groups of four warps; group g takes the tiles whose
-        // count has parity g, with a reference, a sum and an accumulator of its
-        // own.  Thread r of a group owns row r (tensor-memory lane r).
-        const int r = tid & (kBM - 1), grp = tid / kBM;
-        const uint32_t lane_base = taddr + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-        const uint32_t o_base = lane_base + kO + grp * D;
-        // |scale| in log2 units; a zero scale is taken as 1e-30, which leaves
-        // every finite score's exponent at 0 while masked scores stay -inf.
-        const float sc0 = fmaxf(fabsf(a.scale_log2), 1e-30f) * (kFP8 ? 256.f : 1.f);  // widened codes are 2^-8 of the value
-        int i = 0;
-        bool ok = true;  // (a failed wait skips the work, not the barriers)
-        for (int x = start; x < end;) {
-            const Triple t = find_triple(a, units, G, x);
-            const int n = min(end, t.tile0 + t.keys) - x;
-            const int nrows = min(kBM, t.rows - t.rt * kBM);
-            const int keys = min(t.blocks * a.block_size - (x - t.tile0) * kNK, n * kNK);  // of the segment
-            float sc = sc0;
-            {
-                // Half of Q row r of the tile (member (rt * 128 + r) / G, query
-                // head h * G + r % G) into shared memory, 128-byte swizzled
-                // K-major.  (The previous segment's S are complete: all were
-                // read before its barriers.)
-                const int rr = t.rt * kBM + min(r, nrows - 1);
-                const int s = t.seq0 + rr / G;
-                const T* qrow = static_cast<const T*>(a.q) + (static_cast<int64_t>(s) * a.num_q_heads + t.h * G + rr % G) * D;
-                // A negative scale is applied as |scale| to the scores of -q (a
-                // sign flip is exact), so the row maximum is taken on unscaled
-                // scores.
-                const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-                float up = 1.f;
-                if constexpr (kFP8 && QT == kBF16) {
-                    uint32_t top = 0;  // largest |q|, as the bits of a bf16
-#pragma unroll
-                    for (int q16 = 0; q16 < D / 8; ++q16) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(qrow + 8 * q16);
-                        const uint32_t b[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) top = max(top, max(b[k] & 0x7FFFu, (b[k] >> 16) & 0x7FFFu));
-                    }
-                    const int e = min(max(static_cast<int>(top >> 7) - 127, -100), 127);  // its exponent
-                    up = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
-                    sc *= __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
-                }
-#pragma unroll
-                for (int q = 0; q < D / 16; ++q) {
-                    const int q16 = grp * (D / 16) + q;
-                    uint4 v = *reinterpret_cast<const uint4*>(qrow + 8 * q16);
-                    if constexpr (kFP8 && QT == kBF16) {
-                        uint32_t* b = &v.x;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const __half2 h = __floats2half2_rn(__uint_as_float(b[k] << 16) * up,
-                                                                __uint_as_float(b[k] & 0xFFFF0000u) * up);
-                            b[k] = *reinterpret_cast<const uint32_t*>(&h);
-                        }
-                    }
-                    v.x ^= flip;
-                    v.y ^= flip;
-                    v.z ^= flip;
-                    v.w ^= flip;
-                    *reinterpret_cast<uint4*>(base + S::kQOff + (q16 >> 3) * (kBM * 128) + r * 128 +
-                                              (((q16 & 7) ^ (r & 7)) << 4)) = v;
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&B->q_full);  // one arrival per warp (count 8)
-                // The CTA with a triple's first tile says where its parts are,
-                // for the members of the row tile.
-                if (x == t.tile0 && grp == 0 && r < nrows && rr % G == 0 && a.context_lens[s] / a.block_size >= t.blocks)
-                    a.parts[static_cast<int64_t>(s) * a.num_kv_heads + t.h] =
-                        make_int4(t.row0 + r, t.rows, cta_of_tile(t.tile0 + t.keys - 1, units.W, units.P) - cta + 1, 0);
-            }
-            // Unless it has a tile, a group weighs nothing.
-            float m_ref = -1e30f, l = 0.f;
-            const int j0 = (grp ^ i) & 1;
-            for (int j = j0; j < n && ok; j += 2) {
-                const int k0 = i + j, b = k0 % kS;
-                ok = __all_sync(0xffffffffu, wait(&B->s_full[b], k0 / kS, abort, a.status));
-                if (!ok) break;
-                tc_fence_after();
-                float sv[kNK];
-                {
-                    float t0[32], t1[32];
-                    tc_ld32(lane_base + b * kNK, t0);
-                    tc_ld32(lane_base + b * kNK + 32, t1);
-                    tc_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        sv[k] = t0[k];
-                        sv[32 + k] = t1[k];
-                    }
-                }
-                const int left = keys - j * kNK;  // keys from this tile on
-                if (left < kNK) {
-#pragma unroll
-                    for (int k = 0; k < kNK; ++k) sv[k] = k < left ? sv[k] : -INFINITY;
-                }
-                // Row maximum as eight independent chains (short dependency path).
-                float mx[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) mx[k] = sv[k];
-#pragma unroll
-                for (int k = 8; k < kNK; ++k) mx[k & 7] = fmaxf(mx[k & 7], sv[k]);
-                // (The lower limit keeps the exponents of a row whose scores
-                // are all -inf so far at -inf, not NaN.)
-                const float mt = fmaxf(fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                             fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sc,
-                                       -1e30f);
-                bool need = false;
-                if (j < 2)
-                    m_ref = mt;
-                else
-                    need = mt > m_ref + kLazy;
-                if (__any_sync(0xffffffffu, need)) {
-                    // O must be complete up to the group's tile before it is rescaled.
-                    ok = __all_sync(0xffffffffu, wait(&B->pv_done[(k0 - 2) % kS], (k0 - 2) / kS, abort, a.status));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const float f = need ? fast_exp2(m_ref - mt) : 1.f;
-                    if (need) {
-                        l *= f;
-                        m_ref = mt;
-                    }
-#pragma unroll
-                    for (int cb = 0; cb < D / 32; ++cb) {
-                        float o[32];
-                        tc_ld32(o_base + 32 * cb, o);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] *= f;
-                        tc_st32(o_base + 32 * cb, o);
-                    }
-                    tc_wait_st();
-                }
-                // P over the S buffer it came from: columns 0-31 the high part,
-                // 32-63 the low part, keys 2k and 2k + 1 in column k.
-                float ps[4] = {0.f, 0.f, 0.f, 0.f};
-                {
-                    uint32_t ph[32], pl[32];
-#pragma unroll
-                    for (int k = 0; k < kNK / 2; ++k) {
-                        const float p0 = fast_exp2(fmaf(sv[2 * k], sc, -m_ref));
-                        const float p1 = fast_exp2(fmaf(sv[2 * k + 1], sc, -m_ref));
-                        ps[k & 3] += p0 + p1;
-                        pack_split<DT>(p0, p1, ph[k], pl[k]);
-                    }
-                    tc_st32u(lane_base + b * kNK, ph);
-                    tc_st32u(lane_base + b * kNK + 32, pl);
-                }
-                l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&B->p_full[b]);  // one arrival per warp (count 4)
-            }
-            i += n;
-            // Both groups' accumulators into one part: group g writes half of
-            // the columns.
-            B->ml[grp][r] = make_float2(m_ref, l);
-            named_barrier_sync(1, 2 * kBM);
-            if (ok) ok = __all_sync(0xffffffffu, wait(&B->pv_done[(i - 1) % kS], (i - 1) / kS, abort, a.status));
-            if (ok && n > 1) ok = __all_sync(0xffffffffu, wait(&B->pv_done[(i - 2) % kS], (i - 2) / kS, abort, a.status));
-            if (ok) {
-                tc_fence_after();
-                const float2 e = B->ml[0][r], o = B->ml[1][r];
-                const float M = fmaxf(e.x, o.x);
-                const float we = fast_exp2(e.x - M), wo = fast_exp2(o.x - M);
-                const float vs = a.v_scale * (kFP8 ? 256.f : 1.f);
-                const float se = we * vs, so = wo * vs;
-                // A segment of one tile leaves the other group's accumulator as it was.
-                const bool has_e = n > 1 || ((i - 1) & 1) == 0, has_o = n > 1 || ((i - 1) & 1) == 1;
-                const int64_t row = t.row0 + static_cast<int64_t>(cta - cta_of_tile(t.tile0, units.W, units.P)) * t.rows + r;
-                const bool row_ok = r < nrows && row < a.max_rows;
-                float* po = a.part_o + row * D + grp * (D / 2);
-#pragma unroll
-                for (int cb = 0; cb < D / 64; ++cb) {
-                    float v0[32], v1[32];
-                    tc_ld32(lane_base + kO + grp * (D / 2) + 32 * cb, v0);
-                    tc_ld32(lane_base + kO + D + grp * (D / 2) + 32 * cb, v1);
-                    tc_wait_ld();
-                    if (row_ok) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) v0[k] = (has_e ? v0[k] * se : 0.f) + (has_o ? v1[k] * so : 0.f);
-#pragma unroll
-                        for (int k = 0; k < 32; k += 8) store_32(po + 32 * cb + k, v0 + k);
-                    }
-                }
-                if (row_ok && grp == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * row) = make_float2(M, we * e.y + wo * o.y);
-                tc_fence_before();
-            }
-            named_barrier_sync(1, 2 * kBM);  // both accumulators read before the next segment's P is announced
-            x += n;
-        }
-    }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 0) {
-        tc_fence_after();
-        tc_dealloc(taddr, kTmemCols);
-    }
-}
-
-// ------------------------------------------------------------------ merge
-
 // One warp a (sequence, query head): the prefix's parts, then the parts the
 // decode kernel left of the tail.  Lane l holds (max, sum) of part l of 32;
 // every lane sums D / 32 output elements.
 template <int D>
-__global__ void __launch_bounds__(128) shared_prefix_merge_kernel(const SharedPrefixArgs a, const DecodeArgs d) {
+__global__ void __launch_bounds__(128, 6) shared_prefix_merge_kernel(const SharedPrefixArgs a, const DecodeArgs d) {
     constexpr int VD = D / 32;
     pdl_allow_next();
     pdl_wait();
@@ -728,33 +99,42 @@ __global__ void __launch_bounds__(128) shared_prefix_merge_kernel(const SharedPr
     const float inv = n > 0 ? 1.f / L : 0.f;  // a sequence without tokens: zeros
     const int64_t o0 = row * D + lane * VD;
 #pragma unroll
-    for (int i = 0; i < VD; ++i) store_out(a.out, o0 + i, n > 0 ? acc[i] * inv : 0.f, a.out_dtype);
-}
-
-template <int QT, int D, bool kFP8>
-cudaError_t launch_parts_t(const SharedPrefixArgs& a, cudaStream_t stream) {
-    static std::atomic<int> configured[64];
-    auto kern = shared_prefix_parts_kernel<QT, D, kFP8>;
-    const bool cacheable = a.device >= 0 && a.device < 64;
-    if (!cacheable || !configured[a.device].load()) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, a.smem_bytes);
-        if (e == cudaSuccess) e = prefer_shared_memory(kern);
-        if (e != cudaSuccess) return e;
-        if (cacheable) configured[a.device].store(1);
+    for (int i = 0; i < VD; ++i) acc[i] = n > 0 ? acc[i] * inv : 0.f;
+    if (a.out_dtype == kF32) {
+        float* o = static_cast<float*>(a.out) + o0;
+        if constexpr (VD == 4)
+            *reinterpret_cast<float4*>(o) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        else
+            *reinterpret_cast<float2*>(o) = make_float2(acc[0], acc[1]);
+        return;
     }
-    return launch_kernel(kern, dim3(a.num_ctas), dim3(Shape<D, kFP8>::kThreads), static_cast<size_t>(a.smem_bytes),
-                         stream, true, a);
+    uint32_t w[VD / 2];
+#pragma unroll
+    for (int i = 0; i < VD / 2; ++i) {
+        if (a.out_dtype == kF16) {
+            const __half2 h = __floats2half2_rn(acc[2 * i], acc[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * i], acc[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+    char* o = static_cast<char*>(a.out) + o0 * 2;
+    if constexpr (VD == 4)
+        *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+    else
+        *reinterpret_cast<uint32_t*>(o) = w[0];
 }
 
 template <int D>
 cudaError_t launch_merge_t(const SharedPrefixArgs& a, const DecodeArgs& tails, cudaStream_t stream) {
     static std::atomic<int> configured[64];
     auto kern = shared_prefix_merge_kernel<D>;
-    const bool cacheable = a.device >= 0 && a.device < 64;
-    if (!cacheable || !configured[a.device].load()) {
+    const bool cacheable = tails.device >= 0 && tails.device < 64;
+    if (!cacheable || !configured[tails.device].load()) {
         const cudaError_t e = prefer_shared_memory(kern);
         if (e != cudaSuccess) return e;
-        if (cacheable) configured[a.device].store(1);
+        if (cacheable) configured[tails.device].store(1);
     }
     const int64_t warps = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
     return launch_kernel(kern, dim3(static_cast<unsigned>((warps + 3) / 4)), dim3(128), 0, stream, true, a, tails);
@@ -762,27 +142,14 @@ cudaError_t launch_merge_t(const SharedPrefixArgs& a, const DecodeArgs& tails, c
 
 }  // namespace
 
-int prefix_smem_bytes(int head_dim, bool fp8) {
-    const uint32_t off = fp8 ? Shape<128, true>::kBarOff : head_dim == 64 ? Shape<64, false>::kBarOff : Shape<128, false>::kBarOff;
-    return static_cast<int>(off + sizeof(Bars) + 1024);
-}
-
-cudaError_t launch_prefix_parts(const SharedPrefixArgs& a, cudaStream_t stream) {
-    if (a.kv_dtype == kFP8) {
-        if (a.dtype == kBF16) return launch_parts_t<kBF16, 128, true>(a, stream);
-        return launch_parts_t<kF16, 128, true>(a, stream);
-    }
-    if (a.head_dim == 64) {
-        if (a.dtype == kBF16) return launch_parts_t<kBF16, 64, false>(a, stream);
-        return launch_parts_t<kF16, 64, false>(a, stream);
-    }
-    if (a.dtype == kBF16) return launch_parts_t<kBF16, 128, false>(a, stream);
-    return launch_parts_t<kF16, 128, false>(a, stream);
-}
-
-cudaError_t launch_prefix_merge(const SharedPrefixArgs& a, const DecodeArgs& tails, cudaStream_t stream) {
-    if (a.head_dim == 64) return launch_merge_t<64>(a, tails, stream);
-    return launch_merge_t<128>(a, tails, stream);
+cudaError_t launch_shared_prefix(const SharedPrefixArgs& a, const DecodeArgs& d, const CUtensorMap& tmk,
+                                 const CUtensorMap& tmv, cudaStream_t stream) {
+    cudaError_t e = d.kv_dtype == kFP8    ? launch_attend_fp8(a, d, tmk, tmv, stream)
+                    : d.dtype == kBF16 ? launch_attend_bf16(a, d, tmk, tmv, stream)
+                                       : launch_attend_f16(a, d, tmk, tmv, stream);
+    if (e != cudaSuccess) return e;
+    if (a.head_dim == 64) return launch_merge_t<64>(a, d, stream);
+    return launch_merge_t<128>(a, d, stream);
 }
 
 }  // namespace pkv

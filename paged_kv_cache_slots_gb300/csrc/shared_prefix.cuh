@@ -23,16 +23,18 @@ struct SharedPrefixArgs {
     int num_seqs, num_groups, num_blocks, max_blocks, num_q_heads, num_kv_heads, head_dim, block_size;
     int dtype, out_dtype, kv_dtype;
     float scale_log2, v_scale;
-    int num_ctas;                // SMs, divided between the parts and the tails
     int max_rows;                // capacity of the partial rows
-    int device, smem_bytes;
 };
 
+// Shared memory of the parts role.
 int prefix_smem_bytes(int head_dim, bool fp8);
-cudaError_t launch_prefix_parts(const SharedPrefixArgs& a, cudaStream_t stream);
-cudaError_t launch_prefix_merge(const SharedPrefixArgs& a, const DecodeArgs& tails, cudaStream_t stream);
-// The decode kernel over what follows the prefix (decode_tails.cu).
-cudaError_t launch_decode_tails(const DecodeArgs& a, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
-                                cudaStream_t stream);
+cudaError_t launch_attend_f16(const SharedPrefixArgs& a, const DecodeArgs& d, const CUtensorMap& tmap_k,
+                              const CUtensorMap& tmap_v, cudaStream_t stream);
+cudaError_t launch_attend_bf16(const SharedPrefixArgs& a, const DecodeArgs& d, const CUtensorMap& tmap_k,
+                               const CUtensorMap& tmap_v, cudaStream_t stream);
+cudaError_t launch_attend_fp8(const SharedPrefixArgs& a, const DecodeArgs& d, const CUtensorMap& tmap_k,
+                              const CUtensorMap& tmap_v, cudaStream_t stream);
+cudaError_t launch_shared_prefix(const SharedPrefixArgs& a, const DecodeArgs& d, const CUtensorMap& tmap_k,
+                                 const CUtensorMap& tmap_v, cudaStream_t stream);
 
 }  // namespace pkv

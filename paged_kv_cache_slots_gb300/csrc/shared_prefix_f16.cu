@@ -1,0 +1,18 @@
+// Shared-prefix attention over f16 caches (shared_prefix_kernel.cuh).
+#include "decode_mma.cuh"
+#include "shared_prefix_kernel.cuh"
+
+namespace pkv {
+
+cudaError_t launch_attend_f16(const SharedPrefixArgs& a, const DecodeArgs& d, const CUtensorMap& tmk,
+                               const CUtensorMap& tmv, cudaStream_t stream) {
+    if (d.head_dim == 64) return launch_attend_t<MmaPolicy<kF16, 64, kPartsThreads>, kF16, 64, false>(a, d, tmk, tmv, stream);
+    return launch_attend_t<MmaPolicy<kF16, 128, kPartsThreads>, kF16, 128, false>(a, d, tmk, tmv, stream);
+}
+
+int prefix_smem_bytes(int head_dim, bool fp8) {
+    const uint32_t off = fp8 ? Shape<128, true>::kBarOff : head_dim == 64 ? Shape<64, false>::kBarOff : Shape<128, false>::kBarOff;
+    return static_cast<int>(off + sizeof(Bars) + 1024);
+}
+
+}  // namespace pkv

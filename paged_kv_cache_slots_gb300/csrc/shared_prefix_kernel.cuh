@@ -1,0 +1,619 @@
+// Decode attention of a batch in which groups of sequences share the blocks
+// of a long prefix ("Reading Inference Engine Codebases", Examples 12 and 13:
+// requests with equal prompts are given the same cached blocks): each group's
+// prefix is read once for all its members.
+//
+// The mathematics.  For one query row, softmax over a set of keys cut into
+// parts needs of each part only m = max score (or any reference), l = sum of
+// 2^(score - m) and O = sum of 2^(score - m) V; the whole is
+// sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  A group's prefix is
+// attended to by all members alike, without a mask, so its scores are one
+// matrix product per KV head: rows = (member, query head of the KV head),
+// columns = prefix keys.  What follows the prefix differs per sequence and is
+// left to the split-context decode kernel's code.  Two launches:
+//   attend  one CTA an SM, in one of two roles that run side by side:
+//             parts  (m, l, O) of 128 rows over a range of a group's keys;
+//             tails  the decode kernel over the tokens after the prefix,
+//                    partials only;
+//   merge   one warp a (sequence, query head).
+// Which sequences share (those at least as long as the prefix; shorter ones
+// read their own tables throughout) and how the work is cut follows from the
+// groups and lengths alone, so every CTA works it out for itself
+// (prefix_units.cuh), which costs less than a launch that does it for all.
+//
+// The parts role.  Producer warps bring K and V tiles of 64 keys into swizzled
+// shared memory; two warps issue tcgen05 MMAs, S = Q K^T into tensor memory
+// (four buffers) and O += P V with P read from tensor memory; two groups of
+// four warps hold the softmax, one row a thread.  Tiles alternate between the
+// two groups (and issuers), each with an accumulator of its own: a group's
+// softmax of a tile takes about 1 us, mostly latency, and an issuing warp
+// whose sub-partition also runs softmax warps issues an MMA only every 100
+// cycles or so, where the tensor pipe takes 64; two of each keep it busy.
+// (Measured on 256 sequences, 32 query and 8 KV heads, 32,768 shared tokens:
+// 356 us with one issuing lane, 290 with one warp walking the issue loop
+// converged, so that descriptors stay in uniform registers, 214 with two.)
+// P enters the product as a high and a low half-precision part, so that the
+// result carries fp32-like weights whatever the output type.
+#pragma once
+
+#include "decode_kernel.cuh"
+#include "mma_frag.cuh"
+#include "shared_prefix.cuh"
+#include "tc_utils.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kBM = kPrefixRows;
+constexpr int kNK = kPrefixTile;
+constexpr int kS = 4;                // S / P buffers in tensor memory, 64 columns each
+constexpr uint32_t kO = kS * kNK;    // the two accumulators, D columns each
+constexpr uint32_t kTmemCols = 512;
+constexpr float kLazy = 8.f;
+constexpr int kSoftmaxWarps = 8, kProducers = 2;
+// E4M3: codes on their way to be widened, tiles a producer warp.
+constexpr int kRawRing = 5;
+constexpr uint32_t kRawStage = kNK * 128;
+constexpr int kPartsThreads = 32 * (kSoftmaxWarps + 2 + kProducers);
+
+template <int D, bool kFP8>
+struct Shape {
+    static constexpr int kSlices = D / 64;                    // 128-byte slices of a row
+    static constexpr int kKRing = kFP8 ? 3 : D == 128 ? 6 : 10;  // K stages
+    static constexpr int kVRing = kFP8 ? 3 : D == 128 ? 5 : 10;  // V stages
+    static constexpr uint32_t kTile = kSlices * kNK * 128;    // bytes of a K (or V) tile
+    static constexpr uint32_t kQOff = 0;
+    static constexpr uint32_t kKOff = kSlices * kBM * 128;
+    static constexpr uint32_t kVOff = kKOff + kKRing * kTile;
+    static constexpr uint32_t kRawOff = kVOff + kVRing * kTile;
+    static constexpr uint32_t kBarOff = kRawOff + (kFP8 ? kProducers * kRawRing * kRawStage : 0);
+};
+
+struct Bars {
+    uint64_t kfull[10], kempty[10], vfull[10], vempty[10];
+    uint64_t s_full[kS], p_full[kS], pv_done[kS], q_full;
+    float2 ml[2][kBM];  // (reference, sum) of each row in each softmax group
+    uint32_t tmem;
+    int abort;
+};
+
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+    return mbar_wait_bounded(bar, parity & 1u, abort, status);
+}
+
+// 16 bytes global -> shared, or 16 zero bytes.
+__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+
+// 32 bytes to global memory (a whole sector at once).
+__device__ __forceinline__ void store_32(float* p, const float* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(__float_as_uint(v[0])),
+                 "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+                 "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])),
+                 "r"(__float_as_uint(v[7]))
+                 : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one;
+}
+
+// tc_mma, tc_mma_ts and tc_commit issued by the lane with leader != 0 while the
+// whole warp walks the loop: addresses and descriptors are then the same on
+// every lane, and the compiler can keep them in uniform registers.
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                                       bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t leader, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(leader)
+        : "memory");
+}
+
+// Eight E4M3 codes -> eight f16 values, exactly, times 2^-8.
+__device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
+    return make_uint4(e4m3x2_odd_bytes_to_half2_shifted(__byte_perm(lo, 0u, 0x1404)),
+                      e4m3x2_odd_bytes_to_half2_shifted(__byte_perm(lo, 0u, 0x3424)),
+                      e4m3x2_odd_bytes_to_half2_shifted(__byte_perm(hi, 0u, 0x1404)),
+                      e4m3x2_odd_bytes_to_half2_shifted(__byte_perm(hi, 0u, 0x3424)));
+}
+
+// QT: q's type.  The tensor cores work in it, or in f16 over an E4M3 cache
+// (whose codes widen to f16 in a few integer operations); a bf16 q is then
+// brought to f16 with a power of two for each row that puts its largest
+// element at 2^13: exact down to 2^-27 of that element.
+template <int QT, int D, bool kFP8>
+__device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* base, const Units& units, int cta) {
+    using T = typename Elem<QT>::T;
+    using S = Shape<D, kFP8>;
+    constexpr int DT = kFP8 ? static_cast<int>(kF16) : QT;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = a.num_q_heads / a.num_kv_heads;
+    const int start = mul_div(cta, units.W, units.P), end = mul_div(cta + 1, units.W, units.P);
+    Bars* B = reinterpret_cast<Bars*>(base + S::kBarOff);
+    volatile int* abort = &B->abort;
+    if (tid == 0) {
+        // A tile is full with one arrival of its producer warp, or one a copying lane.
+        for (int i = 0; i < S::kKRing; ++i) {
+            mbar_init(&B->kfull[i], kFP8 ? 1 : 32);
+            mbar_init(&B->kempty[i], 1);
+        }
+        for (int i = 0; i < S::kVRing; ++i) {
+            mbar_init(&B->vfull[i], kFP8 ? 1 : 32);
+            mbar_init(&B->vempty[i], 1);
+        }
+        for (int i = 0; i < kS; ++i) {
+            mbar_init(&B->s_full[i], 1);
+            mbar_init(&B->p_full[i], 4);
+            mbar_init(&B->pv_done[i], 1);
+        }
+        mbar_init(&B->q_full, 8);
+        B->abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0) tc_alloc(&B->tmem, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t taddr = B->tmem;
+
+    // Every role walks the CTA's segments; tiles are counted from the CTA's
+    // first (i), so rings and buffers go on over segments.
+    if (warp >= kSoftmaxWarps + 2) {
+        // ---- producers.  The keys come in runs of 16 rows (block_size is a
+        // multiple of 16), each inside one block; runs past the last key are
+        // zeros.
+        const int bs = a.block_size;
+        const int ch = lane & 7, l8 = lane >> 3;
+        const int w = warp - kSoftmaxWarps - 2;
+        // One warp brings the K tiles, the other the V tiles.
+        const char* cache = static_cast<const char*>(w == 0 ? a.k_cache : a.v_cache);
+        uint8_t* tiles = base + (w == 0 ? S::kKOff : S::kVOff);
+        uint64_t* full = w == 0 ? B->kfull : B->vfull;
+        uint64_t* empty = w == 0 ? B->kempty : B->vempty;
+        const int ring = w == 0 ? S::kKRing : S::kVRing;
+        int i = 0;  // tiles before the segment
+        bool ok = true;
+        for (int x = start; x < end && ok;) {
+            const Triple t = find_triple(a, units, G, x);
+            const int n = min(end, t.tile0 + t.keys) - x;  // tiles of the segment
+            const int key0 = (x - t.tile0) * kNK;
+            const int nruns = (min(t.blocks * bs, key0 + n * kNK) - key0) / 16;
+            // The member whose table row names the blocks; without one the
+            // segment's keys are zeros and nobody reads its part.
+            int lead = -1;
+            for (int s0 = 0; s0 * G < t.rows && lead < 0; s0 += 32) {
+                const int s = t.seq0 + s0 + lane;
+                const uint32_t in = __ballot_sync(0xffffffffu, (s0 + lane) * G < t.rows && a.context_lens[s] / bs >= t.blocks);
+                if (in) lead = t.seq0 + s0 + __ffs(in) - 1;
+            }
+            const int32_t* table = a.block_tables + static_cast<int64_t>(lead < 0 ? 0 : lead) * a.max_blocks;
+            // First cache row of run r of the segment; -1: zeros.
+            auto run_row = [&](int r) -> int {
+                if (r >= nruns || lead < 0) return -1;
+                const int key = key0 + 16 * r;
+                const int lb = key / bs;
+                int blk = table[lb];
+                if (blk < 0 || blk >= a.num_blocks) {
+                    raise_flag(a.status, kFlagBadBlock);
+                    blk = 0;
+                }
+                return (blk * a.num_kv_heads + t.h) * bs + (key - lb * bs);
+            };
+            // Lane l knows where run l of the current 8 tiles starts, and of the 8
+            // after them; lane e takes the 16 bytes e % 8 of rows e / 8 + 4 q of a
+            // run (of both 64-element slices).
+            int now = run_row(lane), next = run_row(32 + lane);
+            auto advance = [&](int j) {  // to tile j
+                if ((j & 7) == 0 && j > 0) {
+                    now = next;
+                    next = run_row(4 * (j + 8) + lane);
+                }
+            };
+            int st = i % ring, round = i / ring;
+            auto vacant = [&]() {
+                return round == 0 || __all_sync(0xffffffffu, wait(&empty[st], round - 1, abort, a.status)) != 0;
+            };
+            if constexpr (!kFP8) {
+                const char* c0 = cache + l8 * (D * 2) + ch * 16;
+                const uint32_t d0 = smem_addr(tiles) + l8 * 128;
+                const uint32_t sw0 = static_cast<uint32_t>(ch ^ l8) << 4, sw1 = static_cast<uint32_t>(ch ^ (l8 + 4)) << 4;
+                for (int j = 0; j < n; ++j) {
+                    advance(j);
+                    ok = vacant();
+                    if (!ok) break;
+                    const uint32_t dst = d0 + st * S::kTile;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int row = __shfl_sync(0xffffffffu, now, (j & 7) * 4 + k);
+                        const bool real = row >= 0;
+                        const char* src = c0 + (real ? static_cast<int64_t>(row) * (D * 2) : 0);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t d = dst + (16 * k + 4 * q) * 128 + ((q & 1) ? sw1 : sw0);
+#pragma unroll
+                            for (int sl = 0; sl < S::kSlices; ++sl)
+                                cp_async_16_or_zero(d + sl * (kNK * 128), src + (real ? q * (4 * D * 2) + sl * 128 : 0), real);
+                        }
+                    }
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&full[st])) : "memory");
+                    if (++st == ring) st = 0, ++round;
+                }
+            } else {
+                // E4M3: the codes travel through a ring of this warp's own (each
+                // lane reads back what it copied) and are widened into the
+                // tile; lane e takes codes 16 (e % 8) .. of a row.
+                const char* c0 = cache + l8 * D + ch * 16;
+                const uint32_t raw0 = smem_addr(base + S::kRawOff + w * (kRawRing * kRawStage)) + lane * 16;
+                auto ask = [&](int j) {  // in order; an empty group past the end
+                    if (j < n) {
+                        advance(j);
+                        const uint32_t d = raw0 + j % kRawRing * kRawStage;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int row = __shfl_sync(0xffffffffu, now, (j & 7) * 4 + k);
+                            const bool real = row >= 0;
+                            const char* src = c0 + (real ? static_cast<int64_t>(row) * D : 0);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                cp_async_16_or_zero(d + (4 * k + q) * 512, src + (real ? 4 * q * D : 0), real);
+                        }
+                    }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                };
+                for (int j = 0; j < kRawRing - 1; ++j) ask(j);
+                for (int j = 0; j < n; ++j) {
+                    ask(j + kRawRing - 1);
+                    asm volatile("cp.async.wait_group %0;" ::"n"(kRawRing - 1) : "memory");  // tile j is here
+                    const uint32_t raw = raw0 + j % kRawRing * kRawStage;
+                    uint8_t* t0 = tiles + st * S::kTile + (ch >> 2) * (kNK * 128);
+                    ok = vacant();
+                    if (!ok) break;
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        uint4 r[8];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(r[q].x), "=r"(r[q].y), "=r"(r[q].z), "=r"(r[q].w)
+                                         : "r"(raw + (8 * hf + q) * 512));
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const int row = 32 * hf + 4 * q + l8;
+                            const int c2 = (ch & 3) * 2;
+                            *reinterpret_cast<uint4*>(t0 + row * 128 + ((c2 ^ (row & 7)) << 4)) = widen8(r[q].x, r[q].y);
+                            *reinterpret_cast<uint4*>(t0 + row * 128 + (((c2 + 1) ^ (row & 7)) << 4)) = widen8(r[q].z, r[q].w);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[st]);
+                    if (++st == ring) st = 0, ++round;
+                }
+            }
+            i += n;
+            x += n;
+        }
+        // Every copy issued must land before the CTA can exit.
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+    } else if (warp >= kSoftmaxWarps) {
+        // ---- MMA issue: each of two warps issues for the tiles of one parity,
+        // S one of them ahead of P V.
+        constexpr int bf = DT == kBF16 ? 1 : 0;
+        constexpr uint32_t idS = tc_idesc_f16(bf, false, kNK, kBM);
+        constexpr uint32_t idPV = tc_idesc_f16(bf, true, D, kBM);
+        const int me = warp - kSoftmaxWarps;
+        const uint32_t leader = elect_one();
+        const uint32_t sbase = smem_addr(base), bars = smem_addr(B);
+        auto bar_of = [&](const uint64_t* p) { return bars + static_cast<uint32_t>(reinterpret_cast<const uint8_t*>(p) - reinterpret_cast<const uint8_t*>(B)); };
+        // All tensor memory is this CTA's: its addresses start at 0.
+        const uint64_t qd = tc_sdesc(sbase + S::kQOff, 16, 1024);
+        auto ready = [&](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, wait(bar, phase, abort, a.status)) != 0; };
+        auto score = [&](int i) -> bool {
+            const int sk = i % S::kKRing, b = i % kS;
+            if (!ready(&B->kfull[sk], i / S::kKRing)) return false;
+            // S buffer b holds P of tile i - kS until that PV has completed.
+            if (i >= kS && !ready(&B->pv_done[b], i / kS - 1)) return false;
+            if constexpr (!kFP8) fence_proxy_async_smem();  // lane copies before the tensor cores read them
+            tc_fence_after();
+            const uint64_t kd = tc_sdesc(sbase + S::kKOff + sk * S::kTile, 16, 1024);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+                mma_ss(leader, b * kNK, qd + (((ks >> 2) * (kBM * 128) + (ks & 3) * 32) >> 4),
+                       kd + (((ks >> 2) * (kNK * 128) + (ks & 3) * 32) >> 4), idS, ks > 0);
+            mma_commit(leader, bar_of(&B->s_full[b]));
+            mma_commit(leader, bar_of(&B->kempty[sk]));
+            return true;
+        };
+        auto pv = [&](int i, bool first) -> bool {
+            const int sv = i % S::kVRing, b = i % kS;
+            if (!ready(&B->p_full[b], i / kS)) return false;
+            if (!ready(&B->vfull[sv], i / S::kVRing)) return false;
+            if constexpr (!kFP8) fence_proxy_async_smem();
+            tc_fence_after();
+            const uint64_t vd = tc_sdesc(sbase + S::kVOff + sv * S::kTile, kNK * 128, 1024);
+            const uint32_t o = kO + (i & 1) * D;
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int kk = 0; kk < kNK / 16; ++kk)
+                    mma_ts(leader, o, b * kNK + part * 32 + kk * 8, vd + ((kk * 16 * 128) >> 4), idPV,
+                           !(first && part == 0 && kk == 0));
+            mma_commit(leader, bar_of(&B->pv_done[b]));
+            mma_commit(leader, bar_of(&B->vempty[sv]));
+            return true;
+        };
+        int i = 0, seg = 0;
+        bool ok = true;
+        for (int x = start; x < end && ok; ++seg) {
+            const Triple t = find_triple(a, units, G, x);
+            const int n = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(min(end, t.tile0 + t.keys) - x)));
+            const int j0 = (me ^ i) & 1;
+            ok = ready(&B->q_full, seg);
+            if (ok && j0 < n) ok = score(i + j0);
+            for (int j = j0; j < n && ok; j += 2) {
+                if (j + 2 < n) ok = score(i + j + 2);
+                if (ok) ok = pv(i + j, j < 2);
+            }
+            i += n;
+            x += n;
+        }
+    } else {
+        // ---- softmax: two groups of four warps; group g takes the tiles whose
+        // count has parity g, with a reference, a sum and an accumulator of its
+        // own.  Thread r of a group owns row r (tensor-memory lane r).
+        const int r = tid & (kBM - 1), grp = tid / kBM;
+        const uint32_t lane_base = taddr + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+        const uint32_t o_base = lane_base + kO + grp * D;
+        // |scale| in log2 units; a zero scale is taken as 1e-30, which leaves
+        // every finite score's exponent at 0 while masked scores stay -inf.
+        const float sc0 = fmaxf(fabsf(a.scale_log2), 1e-30f) * (kFP8 ? 256.f : 1.f);  // widened codes are 2^-8 of the value
+        int i = 0;
+        bool ok = true;  // (a failed wait skips the work, not the barriers)
+        for (int x = start; x < end;) {
+            const Triple t = find_triple(a, units, G, x);
+            const int n = min(end, t.tile0 + t.keys) - x;
+            const int nrows = min(kBM, t.rows - t.rt * kBM);
+            const int keys = min(t.blocks * a.block_size - (x - t.tile0) * kNK, n * kNK);  // of the segment
+            float sc = sc0;
+            {
+                // Half of Q row r of the tile (member (rt * 128 + r) / G, query
+                // head h * G + r % G) into shared memory, 128-byte swizzled
+                // K-major.  (The previous segment's S are complete: all were
+                // read before its barriers.)
+                const int rr = t.rt * kBM + min(r, nrows - 1);
+                const int s = t.seq0 + rr / G;
+                const T* qrow = static_cast<const T*>(a.q) + (static_cast<int64_t>(s) * a.num_q_heads + t.h * G + rr % G) * D;
+                // A negative scale is applied as |scale| to the scores of -q (a
+                // sign flip is exact), so the row maximum is taken on unscaled
+                // scores.
+                const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+                float up = 1.f;
+                if constexpr (kFP8 && QT == kBF16) {
+                    uint32_t top = 0;  // largest |q|, as the bits of a bf16
+#pragma unroll
+                    for (int q16 = 0; q16 < D / 8; ++q16) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(qrow + 8 * q16);
+                        const uint32_t b[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) top = max(top, max(b[k] & 0x7FFFu, (b[k] >> 16) & 0x7FFFu));
+                    }
+                    const int e = min(max(static_cast<int>(top >> 7) - 127, -100), 127);  // its exponent
+                    up = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
+                    sc *= __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
+                }
+#pragma unroll
+                for (int q = 0; q < D / 16; ++q) {
+                    const int q16 = grp * (D / 16) + q;
+                    uint4 v = *reinterpret_cast<const uint4*>(qrow + 8 * q16);
+                    if constexpr (kFP8 && QT == kBF16) {
+                        uint32_t* b = &v.x;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const __half2 h = __floats2half2_rn(__uint_as_float(b[k] << 16) * up,
+                                                                __uint_as_float(b[k] & 0xFFFF0000u) * up);
+                            b[k] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                    }
+                    v.x ^= flip;
+                    v.y ^= flip;
+                    v.z ^= flip;
+                    v.w ^= flip;
+                    *reinterpret_cast<uint4*>(base + S::kQOff + (q16 >> 3) * (kBM * 128) + r * 128 +
+                                              (((q16 & 7) ^ (r & 7)) << 4)) = v;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B->q_full);  // one arrival per warp (count 8)
+                // The CTA with a triple's first tile says where its parts are,
+                // for the members of the row tile.
+                if (x == t.tile0 && grp == 0 && r < nrows && rr % G == 0 && a.context_lens[s] / a.block_size >= t.blocks)
+                    a.parts[static_cast<int64_t>(s) * a.num_kv_heads + t.h] =
+                        make_int4(t.row0 + r, t.rows, cta_of_tile(t.tile0 + t.keys - 1, units.W, units.P) - cta + 1, 0);
+            }
+            // Unless it has a tile, a group weighs nothing.
+            float m_ref = -1e30f, l = 0.f;
+            const int j0 = (grp ^ i) & 1;
+            for (int j = j0; j < n && ok; j += 2) {
+                const int k0 = i + j, b = k0 % kS;
+                ok = __all_sync(0xffffffffu, wait(&B->s_full[b], k0 / kS, abort, a.status));
+                if (!ok) break;
+                tc_fence_after();
+                float sv[kNK];
+                {
+                    float t0[32], t1[32];
+                    tc_ld32(lane_base + b * kNK, t0);
+                    tc_ld32(lane_base + b * kNK + 32, t1);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        sv[k] = t0[k];
+                        sv[32 + k] = t1[k];
+                    }
+                }
+                const int left = keys - j * kNK;  // keys from this tile on
+                if (left < kNK) {
+#pragma unroll
+                    for (int k = 0; k < kNK; ++k) sv[k] = k < left ? sv[k] : -INFINITY;
+                }
+                // Row maximum as eight independent chains (short dependency path).
+                float mx[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mx[k] = sv[k];
+#pragma unroll
+                for (int k = 8; k < kNK; ++k) mx[k & 7] = fmaxf(mx[k & 7], sv[k]);
+                // (The lower limit keeps the exponents of a row whose scores
+                // are all -inf so far at -inf, not NaN.)
+                const float mt = fmaxf(fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                             fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sc,
+                                       -1e30f);
+                bool need = false;
+                if (j < 2)
+                    m_ref = mt;
+                else
+                    need = mt > m_ref + kLazy;
+                if (__any_sync(0xffffffffu, need)) {
+                    // O must be complete up to the group's tile before it is rescaled.
+                    ok = __all_sync(0xffffffffu, wait(&B->pv_done[(k0 - 2) % kS], (k0 - 2) / kS, abort, a.status));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const float f = need ? fast_exp2(m_ref - mt) : 1.f;
+                    if (need) {
+                        l *= f;
+                        m_ref = mt;
+                    }
+#pragma unroll
+                    for (int cb = 0; cb < D / 32; ++cb) {
+                        float o[32];
+                        tc_ld32(o_base + 32 * cb, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] *= f;
+                        tc_st32(o_base + 32 * cb, o);
+                    }
+                    tc_wait_st();
+                }
+                // P over the S buffer it came from: columns 0-31 the high part,
+                // 32-63 the low part, keys 2k and 2k + 1 in column k.
+                float ps[4] = {0.f, 0.f, 0.f, 0.f};
+                {
+                    uint32_t ph[32], pl[32];
+#pragma unroll
+                    for (int k = 0; k < kNK / 2; ++k) {
+                        const float p0 = fast_exp2(fmaf(sv[2 * k], sc, -m_ref));
+                        const float p1 = fast_exp2(fmaf(sv[2 * k + 1], sc, -m_ref));
+                        ps[k & 3] += p0 + p1;
+                        pack_split<DT>(p0, p1, ph[k], pl[k]);
+                    }
+                    tc_st32u(lane_base + b * kNK, ph);
+                    tc_st32u(lane_base + b * kNK + 32, pl);
+                }
+                l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B->p_full[b]);  // one arrival per warp (count 4)
+            }
+            i += n;
+            // Both groups' accumulators into one part: group g writes half of
+            // the columns.
+            B->ml[grp][r] = make_float2(m_ref, l);
+            named_barrier_sync(1, 2 * kBM);
+            if (ok) ok = __all_sync(0xffffffffu, wait(&B->pv_done[(i - 1) % kS], (i - 1) / kS, abort, a.status));
+            if (ok && n > 1) ok = __all_sync(0xffffffffu, wait(&B->pv_done[(i - 2) % kS], (i - 2) / kS, abort, a.status));
+            if (ok) {
+                tc_fence_after();
+                const float2 e = B->ml[0][r], o = B->ml[1][r];
+                const float M = fmaxf(e.x, o.x);
+                const float we = fast_exp2(e.x - M), wo = fast_exp2(o.x - M);
+                const float vs = a.v_scale * (kFP8 ? 256.f : 1.f);
+                const float se = we * vs, so = wo * vs;
+                // A segment of one tile leaves the other group's accumulator as it was.
+                const bool has_e = n > 1 || ((i - 1) & 1) == 0, has_o = n > 1 || ((i - 1) & 1) == 1;
+                const int64_t row = t.row0 + static_cast<int64_t>(cta - cta_of_tile(t.tile0, units.W, units.P)) * t.rows + r;
+                const bool row_ok = r < nrows && row < a.max_rows;
+                float* po = a.part_o + row * D + grp * (D / 2);
+#pragma unroll
+                for (int cb = 0; cb < D / 64; ++cb) {
+                    float v0[32], v1[32];
+                    tc_ld32(lane_base + kO + grp * (D / 2) + 32 * cb, v0);
+                    tc_ld32(lane_base + kO + D + grp * (D / 2) + 32 * cb, v1);
+                    tc_wait_ld();
+                    if (row_ok) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v0[k] = (has_e ? v0[k] * se : 0.f) + (has_o ? v1[k] * so : 0.f);
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) store_32(po + 32 * cb + k, v0 + k);
+                    }
+                }
+                if (row_ok && grp == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * row) = make_float2(M, we * e.y + wo * o.y);
+                tc_fence_before();
+            }
+            named_barrier_sync(1, 2 * kBM);  // both accumulators read before the next segment's P is announced
+            x += n;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tc_dealloc(taddr, kTmemCols);
+    }
+}
+
+// CTAs first .. are tails, the others parts (see decode_cta).
+template <class Policy, int QT, int D, bool kFP8>
+__global__ void __launch_bounds__(kPartsThreads, 1)
+    shared_prefix_attend_kernel(const __grid_constant__ SharedPrefixArgs a, const __grid_constant__ DecodeArgs d,
+                                const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+    static_assert(Policy::kMaxThreads == kPartsThreads && !Policy::kScratch);
+    extern __shared__ uint8_t smem_raw[];
+    pdl_allow_next();
+    pdl_wait();
+    uint8_t* base = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    Units units;
+    if (decode_cta<Policy, true>(d, tmk, tmv, base, &units)) return;
+    parts_cta<QT, D, kFP8>(a, base, units, static_cast<int>(blockIdx.x) - (d.num_ctas - units.P));
+}
+
+template <class Policy, int QT, int D, bool kFP8>
+cudaError_t launch_attend_t(const SharedPrefixArgs& a, const DecodeArgs& d, const CUtensorMap& tmk,
+                            const CUtensorMap& tmv, cudaStream_t stream) {
+    static std::atomic<int> configured[64];
+    auto kern = shared_prefix_attend_kernel<Policy, QT, D, kFP8>;
+    const bool cacheable = d.device >= 0 && d.device < 64;
+    if (!cacheable || configured[d.device].load() < d.smem_bytes) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem_bytes);
+        if (e == cudaSuccess) e = prefer_shared_memory(kern);
+        if (e != cudaSuccess) return e;
+        if (cacheable) configured[d.device].store(d.smem_bytes);
+    }
+    return launch_kernel(kern, dim3(d.num_ctas), dim3(kPartsThreads), static_cast<size_t>(d.smem_bytes), stream, true,
+                         a, d, tmk, tmv);
+}
+
+}  // namespace
+
+}  // namespace pkv
