@@ -35,8 +35,7 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kRows = 3;  // rows a thread loads before it uses the first
+constexpr int kThreads = 128;  // kMaxRopePairs: a thread makes one cosine and sine at most
 
 // V elements of T as raw words.
 template <int kBytes>
@@ -124,8 +123,10 @@ __device__ __forceinline__ float2 rotor(uint64_t turn, float amplitude) {
     return make_float2(cs * amplitude, sn * amplitude);
 }
 
-template <int DT, int V, bool kInter>
+// kRows: rows a thread loads before it uses the first.
+template <int DT, int V, bool kInter, int kRows>
 __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const __grid_constant__ RopeArgs a) {
+    static_assert(kThreads >= kMaxRopePairs);
     using T = typename Elem<DT>::T;
     constexpr int kE = static_cast<int>(sizeof(T));
     __shared__ float2 cs[kMaxRopePairs];
@@ -133,14 +134,12 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const __grid_c
     pdl_wait();
     const int tid = threadIdx.x;
     const int64_t i = blockIdx.x;  // token
-    if (a.seq_ids != nullptr && a.seq_ids[i] < 0) return;
     const int n = a.rot_dim >> 1;
-    const int64_t slot = a.slot_mapping[i];
-    const int64_t num_slots = static_cast<int64_t>(a.num_blocks) * a.block_size;
-    const bool keep = slot >= 0 && slot < num_slots;
-    if (slot >= num_slots && tid == 0 && blockIdx.y == 0) raise_flag(a.status, kFlagBadSlot);
-    const int64_t blk = keep ? slot / a.block_size : 0;
-    const int64_t off = keep ? slot - blk * a.block_size : 0;
+    // What the token is, its positions and its first rows are asked for at
+    // once; nothing waits for an answer before the loads are on their way.
+    const int32_t id = a.seq_ids ? a.seq_ids[i] : 0;
+    const int32_t slot = a.slot_mapping[i];
+    const int32_t pos = tid < n ? a.positions[a.axis[tid] * a.positions_stride + i] : 0;
 
     const int nrot = n / V;                             // items of V pairs
     const int items = nrot + (a.head_dim - 2 * n) / V;  // and items of V copied elements
@@ -150,21 +149,22 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const __grid_c
     const int r0 = static_cast<int>(blockIdx.y) * a.rows_per_cta;
     const int r1 = min(H, r0 + a.rows_per_cta);
 
-    // Where row r comes from and goes to; null where nothing is to be done.
     auto source = [&](int r) -> const char* {
         if (r < Hq) return static_cast<const char*>(a.q) + (i * a.q_stride + static_cast<int64_t>(r) * a.head_dim) * kE;
-        if (!keep) return nullptr;
         r -= Hq;
         if (r < Hkv) return static_cast<const char*>(a.k) + (i * a.k_stride + static_cast<int64_t>(r) * a.head_dim) * kE;
         return static_cast<const char*>(a.v) + (i * a.v_stride + static_cast<int64_t>(r - Hkv) * a.head_dim) * kE;
     };
     const int ce = a.quant ? 1 : kE;  // bytes of a cached element
+    const int64_t num_slots = static_cast<int64_t>(a.num_blocks) * a.block_size;
+    int blk = 0, off = 0;
+    bool keep = false;
     auto target = [&](int r) -> char* {
         if (r < Hq)
             return static_cast<char*>(a.q_out) + (i * a.q_out_stride + static_cast<int64_t>(r) * a.head_dim) * kE;
         r -= Hq;
         const bool v = r >= Hkv;
-        const int64_t row = (blk * Hkv + (v ? r - Hkv : r)) * a.block_size + off;
+        const int64_t row = (static_cast<int64_t>(blk) * Hkv + (v ? r - Hkv : r)) * a.block_size + off;
         return static_cast<char*>(v ? a.v_cache : a.k_cache) + row * a.head_dim * ce;
     };
 
@@ -181,19 +181,21 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const __grid_c
 #pragma unroll
             for (int u = 0; u < kRows; ++u) {
                 const int r = rb + u * slots + my;
-                const char* src = active && r < r1 ? source(r) : nullptr;
-                if (src) {
+                if (active && r < r1) {
+                    const char* src = source(r);
                     x0[u].load(src + e0 * kE);
                     if (turn) x1[u].load(src + e1 * kE);
                 }
             }
             if (!angles) {  // the first time round: every thread of the CTA is here
                 angles = true;
-                for (int j = tid; j < n; j += kThreads) {
-                    const int64_t p = a.positions[a.axis[j] * a.positions_stride + i];
-                    cs[j] = rotor(static_cast<uint64_t>(p) * a.phase[j], a.amplitude);
-                }
+                if (tid < n) cs[tid] = rotor(static_cast<uint64_t>(static_cast<int64_t>(pos)) * a.phase[tid], a.amplitude);
                 __syncthreads();
+                if (id < 0) return;  // padding
+                keep = slot >= 0 && slot < num_slots;
+                if (slot >= num_slots && tid == 0 && blockIdx.y == 0) raise_flag(a.status, kFlagBadSlot);
+                blk = keep ? slot / a.block_size : 0;
+                off = slot - blk * a.block_size;
             }
             if (rb == r0 && active && turn) {
 #pragma unroll
@@ -238,10 +240,11 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const __grid_c
     }
 }
 
-template <int DT, int V>
+template <int DT, int V, int kRows>
 cudaError_t launch_v(const RopeArgs& a, dim3 grid, cudaStream_t stream) {
-    if (a.interleaved) return launch_kernel(kv_append_rope_kernel<DT, V, true>, grid, dim3(kThreads), 0, stream, a.pdl != 0, a);
-    return launch_kernel(kv_append_rope_kernel<DT, V, false>, grid, dim3(kThreads), 0, stream, a.pdl != 0, a);
+    if (a.interleaved)
+        return launch_kernel(kv_append_rope_kernel<DT, V, true, kRows>, grid, dim3(kThreads), 0, stream, a.pdl != 0, a);
+    return launch_kernel(kv_append_rope_kernel<DT, V, false, kRows>, grid, dim3(kThreads), 0, stream, a.pdl != 0, a);
 }
 
 // Pairs an item holds: 16 bytes a side, or as many as the sizes and the
@@ -255,22 +258,24 @@ cudaError_t launch_dt(RopeArgs a, int align, int num_sms, cudaStream_t stream) {
     const int items = (a.head_dim - a.rot_dim / 2) / v;
     const int slots = items < kThreads ? kThreads / items : 1;
     const int H = a.num_q_heads + 2 * a.num_kv_heads;
-    // Rows of one token go to several CTAs while that leaves no more CTAs than
-    // two for each SM: with few tokens a call is bound by its latency, and a
-    // thread that takes one row waits once for its load.
+    // A CTA takes the rows of one token that its threads load in one round, two
+    // or three rows a thread (three where that takes fewer CTAs), one while
+    // that leaves no more CTAs than two for each SM: with few tokens a call is
+    // bound by its latency.
     const int passes = (H + slots - 1) / slots;
-    int split = 2 * num_sms / a.n_tokens;
-    split = split < 1 ? 1 : split > passes ? passes : split;
-    const int per = (passes + split - 1) / split;
+    int per = (passes + 2) / 3 < (passes + 1) / 2 ? 3 : 2;
+    while (per > 1 && static_cast<int64_t>(a.n_tokens) * ((passes + per - 2) / (per - 1)) <= 2 * num_sms) --per;
+    while ((passes + per - 1) / per > 65535) per *= 2;  // the grid's limit in y
     a.rows_per_cta = per * slots;
     const dim3 grid(static_cast<unsigned>(a.n_tokens), static_cast<unsigned>((passes + per - 1) / per));
+    const bool three = per >= 3;
     switch (v) {
         case 8:
-            if constexpr (kE == 2) return launch_v<DT, 8>(a, grid, stream);
+            if constexpr (kE == 2) return three ? launch_v<DT, 8, 3>(a, grid, stream) : launch_v<DT, 8, 2>(a, grid, stream);
             return cudaErrorInvalidValue;
-        case 4: return launch_v<DT, 4>(a, grid, stream);
-        case 2: return launch_v<DT, 2>(a, grid, stream);
-        default: return launch_v<DT, 1>(a, grid, stream);
+        case 4: return three ? launch_v<DT, 4, 3>(a, grid, stream) : launch_v<DT, 4, 2>(a, grid, stream);
+        case 2: return three ? launch_v<DT, 2, 3>(a, grid, stream) : launch_v<DT, 2, 2>(a, grid, stream);
+        default: return three ? launch_v<DT, 1, 3>(a, grid, stream) : launch_v<DT, 1, 2>(a, grid, stream);
     }
 }
 
