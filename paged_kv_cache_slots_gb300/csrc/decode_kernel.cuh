@@ -122,7 +122,7 @@ static __device__ int build_prefix(const DecodeArgs& a, int chunks, int32_t* cum
         *units = plan_units(a, a.num_q_heads / a.num_kv_heads);
         if (units->bad && threadIdx.x == 0 && blockIdx.x == 0) raise_flag(a.status, kFlagBadGroup);
     }
-    [[maybe_unused]] int64_t tokens = 0;  // of this thread's sequences, after their shared blocks
+    [[maybe_unused]] int tail_blocks = 0;  // of this thread's sequences
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int nwarps = blockDim.x >> 5;
     int carry = 0;
@@ -136,7 +136,7 @@ static __device__ int build_prefix(const DecodeArgs& a, int chunks, int32_t* cum
                 const int sb = units->bad ? 0 : shared_blocks(a, s, c);
                 skip[s] = sb;
                 nb -= sb;
-                tokens += c - sb * a.block_size;
+                tail_blocks += nb;
             }
             v = nb > 0 ? (nb + a.phantom) * chunks : 0;
         }
@@ -166,14 +166,13 @@ static __device__ int build_prefix(const DecodeArgs& a, int chunks, int32_t* cum
     if (tid == 0) cum[a.num_seqs] = carry;
     int ctas = a.num_ctas;
     if constexpr (kTails) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) tokens += __shfl_xor_sync(0xffffffffu, tokens, o);
-        int64_t* sums = reinterpret_cast<int64_t*>(scan);  // 16 warps at most
-        if (lane == 0) sums[wid] = tokens;
+        // (The warps' sums sit where the scan's totals were: their last readers
+        // are past a barrier.)
+        tail_blocks = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(tail_blocks)));
+        if (lane == 0) scan[wid] = tail_blocks;
         __syncthreads();
-        tokens = 0;
-        for (int w = 0; w < nwarps; ++w) tokens += sums[w];
-        divide_sms(a, tokens, units);
+        tail_blocks = static_cast<int>(__reduce_add_sync(0xffffffffu, lane < nwarps ? static_cast<unsigned>(scan[lane]) : 0u));
+        divide_sms(a, tail_blocks, units);
         ctas -= units->P;
     }
     __syncthreads();

@@ -1157,6 +1157,7 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     int dev = 0, sms = 0, max_smem = 0;
     uint32_t* status = nullptr;
     if (kv_status_t st = device_info(&dev, &status, &sms, &max_smem, nullptr)) return st;
+    max_smem -= prefix_static_smem_bytes();
     const SharedWs w = shared_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, sms);
     if (workspace_bytes < w.total)
         return fail(KV_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, w.total);

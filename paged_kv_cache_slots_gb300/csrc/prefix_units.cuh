@@ -20,7 +20,6 @@ namespace pkv {
 
 constexpr int kPrefixRows = 128;  // query rows of a row tile
 constexpr int kPrefixTile = 64;   // keys of a tile
-constexpr int kMinChunk = 4;      // key tiles a CTA: fewer cost less than its start and the merge of its parts
 
 // a * b / c for 0 <= a, b and c > 0.
 __device__ __forceinline__ int mul_div(int a, int b, int c) {
@@ -109,23 +108,22 @@ __device__ __forceinline__ Units plan_units(const Args& a, int G) {
 }
 
 // The parts kernel's share of the SMs, u->P; the tails kernel takes the rest.
-// tail_tokens: tokens of all sequences after their shared blocks.
+// tail_blocks: cache blocks of all sequences after their shared ones.
 //
 // A tile costs a parts CTA about kTileNs (of 128-element rows), the start and
 // end of a triple kTripleNs; the tails' bytes cost their time at an SM's share
 // of the memory rate.
 template <class Args>
-__device__ __forceinline__ void divide_sms(const Args& a, int64_t tail_tokens, Units* u) {
+__device__ __forceinline__ void divide_sms(const Args& a, int tail_blocks, Units* u) {
     constexpr float kTripleNs = 3000.f, kNsPerByte = 1.f / 42.f;
-    const float kTileNs = a.head_dim == 64 ? 560.f : 1000.f;
+    const float kTileNs = a.head_dim == 64 ? 560.f : 1150.f;
     const int sms = a.num_ctas;
     if (u->W == 0) return;
     const float parts = kTileNs * static_cast<float>(u->W) + kTripleNs * static_cast<float>(u->triples);
-    const float tails = kNsPerByte * 2.f * static_cast<float>(tail_tokens) *
+    const float tails = kNsPerByte * 2.f * static_cast<float>(tail_blocks) * static_cast<float>(a.block_size) *
                         static_cast<float>(a.num_kv_heads * a.head_dim * dtype_bytes(a.kv_dtype));
     int P = static_cast<int>(static_cast<float>(sms) * parts / (parts + tails) + 0.5f);
-    P = min(P, (u->W + kMinChunk - 1) / kMinChunk);
-    P = max(1, min(P, sms - 1));  // a tails CTA there always is: it writes the merge's tables
+    P = max(1, min(min(P, u->W), sms - 1));  // a tails CTA there always is: it writes the merge's tables
     // CTAs that begin with a triple have one segment: worth up to a quarter of
     // them while a CTA has few tiles, a sixteenth always.
     if (u->triples <= P) {

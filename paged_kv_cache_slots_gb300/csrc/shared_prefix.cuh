@@ -26,7 +26,8 @@ struct SharedPrefixArgs {
     int max_rows;                // capacity of the partial rows
 };
 
-// Shared memory of the parts role.
+// Shared memory of the parts role: dynamic, and what the kernel holds besides.
+int prefix_static_smem_bytes();
 int prefix_smem_bytes(int head_dim, bool fp8);
 cudaError_t launch_attend_f16(const SharedPrefixArgs& a, const DecodeArgs& d, const CUtensorMap& tmap_k,
                               const CUtensorMap& tmap_v, cudaStream_t stream);

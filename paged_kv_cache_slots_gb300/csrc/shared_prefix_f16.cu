@@ -10,9 +10,11 @@ cudaError_t launch_attend_f16(const SharedPrefixArgs& a, const DecodeArgs& d, co
     return launch_attend_t<MmaPolicy<kF16, 128, kPartsThreads>, kF16, 128, false>(a, d, tmk, tmv, stream);
 }
 
+int prefix_static_smem_bytes() { return static_cast<int>(sizeof(Bars)) + 64; }
+
 int prefix_smem_bytes(int head_dim, bool fp8) {
-    const uint32_t off = fp8 ? Shape<128, true>::kBarOff : head_dim == 64 ? Shape<64, false>::kBarOff : Shape<128, false>::kBarOff;
-    return static_cast<int>(off + sizeof(Bars) + 1024);
+    const uint32_t off = fp8 ? Shape<128, true>::kBytes : head_dim == 64 ? Shape<64, false>::kBytes : Shape<128, false>::kBytes;
+    return static_cast<int>(off + 1024);
 }
 
 }  // namespace pkv

@@ -67,12 +67,12 @@ struct Shape {
     static constexpr uint32_t kKOff = kSlices * kBM * 128;
     static constexpr uint32_t kVOff = kKOff + kKRing * kTile;
     static constexpr uint32_t kRawOff = kVOff + kVRing * kTile;
-    static constexpr uint32_t kBarOff = kRawOff + (kFP8 ? kProducers * kRawRing * kRawStage : 0);
+    static constexpr uint32_t kBytes = kRawOff + (kFP8 ? kProducers * kRawRing * kRawStage : 0);
 };
 
 struct Bars {
     uint64_t kfull[10], kempty[10], vfull[10], vempty[10];
-    uint64_t s_full[kS], p_full[kS], pv_done[kS], q_full;
+    uint64_t s_full[kS], p_full[kS], pv_done[kS], q_full, tmem_ready;
     float2 ml[2][kBM];  // (reference, sum) of each row in each softmax group
     uint32_t tmem;
     int abort;
@@ -94,6 +94,15 @@ __device__ __forceinline__ void store_32(float* p, const float* v) {
                  "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])),
                  "r"(__float_as_uint(v[7]))
                  : "memory");
+}
+
+// Whole warp: 16 consecutive 32-bit columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
 }
 
 // One lane of a converged warp.
@@ -130,52 +139,52 @@ __device__ __forceinline__ void mma_commit(uint32_t leader, uint32_t bar) {
         : "memory");
 }
 
-// Eight E4M3 codes -> eight f16 values, exactly, times 2^-8.
+// Eight E4M3 codes -> eight f16 values, exactly.
 __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
-    return make_uint4(e4m3x2_odd_bytes_to_half2_shifted(__byte_perm(lo, 0u, 0x1404)),
-                      e4m3x2_odd_bytes_to_half2_shifted(__byte_perm(lo, 0u, 0x3424)),
-                      e4m3x2_odd_bytes_to_half2_shifted(__byte_perm(hi, 0u, 0x1404)),
-                      e4m3x2_odd_bytes_to_half2_shifted(__byte_perm(hi, 0u, 0x3424)));
+    return make_uint4(e4m3x2_to_half2(static_cast<uint16_t>(lo)), e4m3x2_to_half2(static_cast<uint16_t>(lo >> 16)),
+                      e4m3x2_to_half2(static_cast<uint16_t>(hi)), e4m3x2_to_half2(static_cast<uint16_t>(hi >> 16)));
 }
 
 // QT: q's type.  The tensor cores work in it, or in f16 over an E4M3 cache
-// (whose codes widen to f16 in a few integer operations); a bf16 q is then
-// brought to f16 with a power of two for each row that puts its largest
-// element at 2^13: exact down to 2^-27 of that element.
+// (whose values all are f16); a bf16 q is then brought to f16 with a power of
+// two for each row that puts its largest element at 2^13: exact down to 2^-27
+// of that element.
+
+// One thread, before the roles are known.
+template <int D, bool kFP8>
+__device__ __forceinline__ void init_bars(Bars* B) {
+    using S = Shape<D, kFP8>;
+    // A tile is full with one arrival of its producer warp, or one a copying lane.
+    for (int i = 0; i < S::kKRing; ++i) {
+        mbar_init(&B->kfull[i], kFP8 ? 1 : 32);
+        mbar_init(&B->kempty[i], 1);
+    }
+    for (int i = 0; i < S::kVRing; ++i) {
+        mbar_init(&B->vfull[i], kFP8 ? 1 : 32);
+        mbar_init(&B->vempty[i], 1);
+    }
+    for (int i = 0; i < kS; ++i) {
+        mbar_init(&B->s_full[i], 1);
+        mbar_init(&B->p_full[i], 4);
+        mbar_init(&B->pv_done[i], 1);
+    }
+    mbar_init(&B->q_full, kSoftmaxWarps);
+    mbar_init(&B->tmem_ready, 1);
+    B->abort = 0;
+    fence_barrier_init();
+}
+
 template <int QT, int D, bool kFP8>
-__device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* base, const Units& units, int cta) {
+__device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* base, Bars* B, const Units& units, int cta) {
     using T = typename Elem<QT>::T;
     using S = Shape<D, kFP8>;
     constexpr int DT = kFP8 ? static_cast<int>(kF16) : QT;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = a.num_q_heads / a.num_kv_heads;
     const int start = mul_div(cta, units.W, units.P), end = mul_div(cta + 1, units.W, units.P);
-    Bars* B = reinterpret_cast<Bars*>(base + S::kBarOff);
     volatile int* abort = &B->abort;
-    if (tid == 0) {
-        // A tile is full with one arrival of its producer warp, or one a copying lane.
-        for (int i = 0; i < S::kKRing; ++i) {
-            mbar_init(&B->kfull[i], kFP8 ? 1 : 32);
-            mbar_init(&B->kempty[i], 1);
-        }
-        for (int i = 0; i < S::kVRing; ++i) {
-            mbar_init(&B->vfull[i], kFP8 ? 1 : 32);
-            mbar_init(&B->vempty[i], 1);
-        }
-        for (int i = 0; i < kS; ++i) {
-            mbar_init(&B->s_full[i], 1);
-            mbar_init(&B->p_full[i], 4);
-            mbar_init(&B->pv_done[i], 1);
-        }
-        mbar_init(&B->q_full, 8);
-        B->abort = 0;
-        fence_barrier_init();
-    }
-    if (warp == 0) tc_alloc(&B->tmem, kTmemCols);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t taddr = B->tmem;
+    // All of tensor memory is taken, so its addresses start at 0.
+    constexpr uint32_t taddr = 0;
 
     // Every role walks the CTA's segments; tiles are counted from the CTA's
     // first (i), so rings and buffers go on over segments.
@@ -327,7 +336,6 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
         const uint32_t leader = elect_one();
         const uint32_t sbase = smem_addr(base), bars = smem_addr(B);
         auto bar_of = [&](const uint64_t* p) { return bars + static_cast<uint32_t>(reinterpret_cast<const uint8_t*>(p) - reinterpret_cast<const uint8_t*>(B)); };
-        // All tensor memory is this CTA's: its addresses start at 0.
         const uint64_t qd = tc_sdesc(sbase + S::kQOff, 16, 1024);
         auto ready = [&](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, wait(bar, phase, abort, a.status)) != 0; };
         auto score = [&](int i) -> bool {
@@ -366,6 +374,15 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
         };
         int i = 0, seg = 0;
         bool ok = true;
+        if (me == 0) {
+            tc_alloc(&B->tmem, kTmemCols);
+            tc_fence_before();
+            if (lane == 0) mbar_arrive(&B->tmem_ready);
+            __syncwarp();
+        } else {
+            ok = ready(&B->tmem_ready, 0);
+            tc_fence_after();
+        }
         for (int x = start; x < end && ok; ++seg) {
             const Triple t = find_triple(a, units, G, x);
             const int n = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(min(end, t.tile0 + t.keys) - x)));
@@ -388,7 +405,7 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
         const uint32_t o_base = lane_base + kO + grp * D;
         // |scale| in log2 units; a zero scale is taken as 1e-30, which leaves
         // every finite score's exponent at 0 while masked scores stay -inf.
-        const float sc0 = fmaxf(fabsf(a.scale_log2), 1e-30f) * (kFP8 ? 256.f : 1.f);  // widened codes are 2^-8 of the value
+        const float sc0 = fmaxf(fabsf(a.scale_log2), 1e-30f);
         int i = 0;
         bool ok = true;  // (a failed wait skips the work, not the barriers)
         for (int x = start; x < end;) {
@@ -517,17 +534,18 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
                 // P over the S buffer it came from: columns 0-31 the high part,
                 // 32-63 the low part, keys 2k and 2k + 1 in column k.
                 float ps[4] = {0.f, 0.f, 0.f, 0.f};
-                {
-                    uint32_t ph[32], pl[32];
 #pragma unroll
-                    for (int k = 0; k < kNK / 2; ++k) {
-                        const float p0 = fast_exp2(fmaf(sv[2 * k], sc, -m_ref));
-                        const float p1 = fast_exp2(fmaf(sv[2 * k + 1], sc, -m_ref));
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t ph[16], pl[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float p0 = fast_exp2(fmaf(sv[32 * half + 2 * k], sc, -m_ref));
+                        const float p1 = fast_exp2(fmaf(sv[32 * half + 2 * k + 1], sc, -m_ref));
                         ps[k & 3] += p0 + p1;
                         pack_split<DT>(p0, p1, ph[k], pl[k]);
                     }
-                    tc_st32u(lane_base + b * kNK, ph);
-                    tc_st32u(lane_base + b * kNK + 32, pl);
+                    tmem_st16(lane_base + b * kNK + 16 * half, ph);
+                    tmem_st16(lane_base + b * kNK + 32 + 16 * half, pl);
                 }
                 l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
                 tc_wait_st();
@@ -547,7 +565,7 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
                 const float2 e = B->ml[0][r], o = B->ml[1][r];
                 const float M = fmaxf(e.x, o.x);
                 const float we = fast_exp2(e.x - M), wo = fast_exp2(o.x - M);
-                const float vs = a.v_scale * (kFP8 ? 256.f : 1.f);
+                const float vs = a.v_scale;
                 const float se = we * vs, so = wo * vs;
                 // A segment of one tile leaves the other group's accumulator as it was.
                 const bool has_e = n > 1 || ((i - 1) & 1) == 0, has_o = n > 1 || ((i - 1) & 1) == 1;
@@ -576,7 +594,7 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == kSoftmaxWarps) {
         tc_fence_after();
         tc_dealloc(taddr, kTmemCols);
     }
@@ -589,13 +607,15 @@ __global__ void __launch_bounds__(kPartsThreads, 1)
                                 const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
     static_assert(Policy::kMaxThreads == kPartsThreads && !Policy::kScratch);
     extern __shared__ uint8_t smem_raw[];
+    __shared__ Bars bars;  // of the parts role
+    if (threadIdx.x == 0) init_bars<D, kFP8>(&bars);
     pdl_allow_next();
     pdl_wait();
     uint8_t* base = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     Units units;
     if (decode_cta<Policy, true>(d, tmk, tmv, base, &units)) return;
-    parts_cta<QT, D, kFP8>(a, base, units, static_cast<int>(blockIdx.x) - (d.num_ctas - units.P));
+    parts_cta<QT, D, kFP8>(a, base, &bars, units, static_cast<int>(blockIdx.x) - (d.num_ctas - units.P));
 }
 
 template <class Policy, int QT, int D, bool kFP8>
