@@ -122,7 +122,6 @@ static __device__ int build_prefix(const DecodeArgs& a, int chunks, int32_t* cum
         *units = plan_units(a, a.num_q_heads / a.num_kv_heads);
         if (units->bad && threadIdx.x == 0 && blockIdx.x == 0) raise_flag(a.status, kFlagBadGroup);
     }
-    [[maybe_unused]] int tail_blocks = 0;  // of this thread's sequences
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int nwarps = blockDim.x >> 5;
     int carry = 0;
@@ -136,7 +135,6 @@ static __device__ int build_prefix(const DecodeArgs& a, int chunks, int32_t* cum
                 const int sb = units->bad ? 0 : shared_blocks(a, s, c);
                 skip[s] = sb;
                 nb -= sb;
-                tail_blocks += nb;
             }
             v = nb > 0 ? (nb + a.phantom) * chunks : 0;
         }
@@ -166,13 +164,7 @@ static __device__ int build_prefix(const DecodeArgs& a, int chunks, int32_t* cum
     if (tid == 0) cum[a.num_seqs] = carry;
     int ctas = a.num_ctas;
     if constexpr (kTails) {
-        // (The warps' sums sit where the scan's totals were: their last readers
-        // are past a barrier.)
-        tail_blocks = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(tail_blocks)));
-        if (lane == 0) scan[wid] = tail_blocks;
-        __syncthreads();
-        tail_blocks = static_cast<int>(__reduce_add_sync(0xffffffffu, lane < nwarps ? static_cast<unsigned>(scan[lane]) : 0u));
-        divide_sms(a, tail_blocks, units);
+        divide_sms(a, carry, 2 * a.heads_per_stage * a.block_size * a.head_dim * dtype_bytes(a.kv_dtype), chunks, units);
         ctas -= units->P;
     }
     __syncthreads();

@@ -107,21 +107,22 @@ __device__ __forceinline__ Units plan_units(const Args& a, int G) {
     return u;
 }
 
-// The parts kernel's share of the SMs, u->P; the tails kernel takes the rest.
-// tail_blocks: cache blocks of all sequences after their shared ones.
+// The parts role's share of the SMs, u->P; the tails take the rest, `items` of
+// item_bytes of cache, with phantoms among them (DecodeArgs).
 //
 // A tile costs a parts CTA about kTileNs (of 128-element rows), the start and
-// end of a triple kTripleNs; the tails' bytes cost their time at an SM's share
-// of the memory rate.
+// end of a triple kTripleNs; the tails cost their bytes at the rate that an SM
+// reaches, and kSequenceNs for every (sequence, heads of a stage).
 template <class Args>
-__device__ __forceinline__ void divide_sms(const Args& a, int tail_blocks, Units* u) {
-    constexpr float kTripleNs = 3000.f, kNsPerByte = 1.f / 42.f;
-    const float kTileNs = a.head_dim == 64 ? 560.f : 1150.f;
+__device__ __forceinline__ void divide_sms(const Args& a, int items, int item_bytes, int chunks, Units* u) {
+    constexpr float kTripleNs = 3000.f, kSequenceNs = 3700.f, kNsPerByte = 1.f / 55.f;
+    const float kTileNs = a.head_dim == 64 ? 560.f : 1000.f;
     const int sms = a.num_ctas;
     if (u->W == 0) return;
     const float parts = kTileNs * static_cast<float>(u->W) + kTripleNs * static_cast<float>(u->triples);
-    const float tails = kNsPerByte * 2.f * static_cast<float>(tail_blocks) * static_cast<float>(a.block_size) *
-                        static_cast<float>(a.num_kv_heads * a.head_dim * dtype_bytes(a.kv_dtype));
+    const int pairs = a.num_seqs * chunks;
+    const float tails = kNsPerByte * static_cast<float>(max(items - a.phantom * pairs, 0)) * static_cast<float>(item_bytes) +
+                        kSequenceNs * static_cast<float>(pairs);
     int P = static_cast<int>(static_cast<float>(sms) * parts / (parts + tails) + 0.5f);
     P = max(1, min(min(P, u->W), sms - 1));  // a tails CTA there always is: it writes the merge's tables
     // CTAs that begin with a triple have one segment: worth up to a quarter of

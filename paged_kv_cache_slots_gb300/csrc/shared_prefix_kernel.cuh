@@ -96,13 +96,10 @@ __device__ __forceinline__ void store_32(float* p, const float* v) {
                  : "memory");
 }
 
-// Whole warp: 16 consecutive 32-bit columns of this warp's 32 lanes.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // One lane of a converged warp.
@@ -115,20 +112,22 @@ __device__ __forceinline__ uint32_t elect_one() {
 // tc_mma, tc_mma_ts and tc_commit issued by the lane with leader != 0 while the
 // whole warp walks the loop: addresses and descriptors are then the same on
 // every lane, and the compiler can keep them in uniform registers.
-__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                       bool accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint32_t alo, uint32_t blo, uint32_t hi,
+                                       uint32_t idesc, bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+        "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
-                                       bool accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t blo, uint32_t hi,
+                                       uint32_t idesc, bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(blo), "r"(hi), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
         : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint32_t leader, uint32_t bar) {
@@ -336,7 +335,10 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
         const uint32_t leader = elect_one();
         const uint32_t sbase = smem_addr(base), bars = smem_addr(B);
         auto bar_of = [&](const uint64_t* p) { return bars + static_cast<uint32_t>(reinterpret_cast<const uint8_t*>(p) - reinterpret_cast<const uint8_t*>(B)); };
-        const uint64_t qd = tc_sdesc(sbase + S::kQOff, 16, 1024);
+        // Descriptors: the low word holds the address and the slice distance, the
+        // high word (the row groups' distance) is the same for all.
+        constexpr uint32_t kHi = static_cast<uint32_t>((1024u >> 4) | (1u << 14) | (2u << 29));
+        const uint32_t qd = ((sbase + S::kQOff) >> 4) | (1u << 16);
         auto ready = [&](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, wait(bar, phase, abort, a.status)) != 0; };
         auto score = [&](int i) -> bool {
             const int sk = i % S::kKRing, b = i % kS;
@@ -345,11 +347,11 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
             if (i >= kS && !ready(&B->pv_done[b], i / kS - 1)) return false;
             if constexpr (!kFP8) fence_proxy_async_smem();  // lane copies before the tensor cores read them
             tc_fence_after();
-            const uint64_t kd = tc_sdesc(sbase + S::kKOff + sk * S::kTile, 16, 1024);
+            const uint32_t kd = ((sbase + S::kKOff + sk * S::kTile) >> 4) | (1u << 16);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
                 mma_ss(leader, b * kNK, qd + (((ks >> 2) * (kBM * 128) + (ks & 3) * 32) >> 4),
-                       kd + (((ks >> 2) * (kNK * 128) + (ks & 3) * 32) >> 4), idS, ks > 0);
+                       kd + (((ks >> 2) * (kNK * 128) + (ks & 3) * 32) >> 4), kHi, idS, ks > 0);
             mma_commit(leader, bar_of(&B->s_full[b]));
             mma_commit(leader, bar_of(&B->kempty[sk]));
             return true;
@@ -360,13 +362,13 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
             if (!ready(&B->vfull[sv], i / S::kVRing)) return false;
             if constexpr (!kFP8) fence_proxy_async_smem();
             tc_fence_after();
-            const uint64_t vd = tc_sdesc(sbase + S::kVOff + sv * S::kTile, kNK * 128, 1024);
+            const uint32_t vd = ((sbase + S::kVOff + sv * S::kTile) >> 4) | ((kNK * 128 >> 4) << 16);
             const uint32_t o = kO + (i & 1) * D;
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
                 for (int kk = 0; kk < kNK / 16; ++kk)
-                    mma_ts(leader, o, b * kNK + part * 32 + kk * 8, vd + ((kk * 16 * 128) >> 4), idPV,
+                    mma_ts(leader, o, b * kNK + part * 32 + kk * 8, vd + ((kk * 16 * 128) >> 4), kHi, idPV,
                            !(first && part == 0 && kk == 0));
             mma_commit(leader, bar_of(&B->pv_done[b]));
             mma_commit(leader, bar_of(&B->vempty[sv]));
@@ -497,13 +499,14 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
                 // Row maximum as eight independent chains (short dependency path).
                 float mx[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mx[k] = sv[k];
+                for (int k = 0; k < 8; ++k) mx[k] = fmaxf(sv[k], sv[8 + k]);
 #pragma unroll
-                for (int k = 8; k < kNK; ++k) mx[k & 7] = fmaxf(mx[k & 7], sv[k]);
+                for (int k = 16; k < kNK; k += 16)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) mx[c] = max3(mx[c], sv[k + c], sv[k + 8 + c]);
                 // (The lower limit keeps the exponents of a row whose scores
                 // are all -inf so far at -inf, not NaN.)
-                const float mt = fmaxf(fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                             fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sc,
+                const float mt = fmaxf(max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sc,
                                        -1e30f);
                 bool need = false;
                 if (j < 2)
@@ -534,18 +537,17 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
                 // P over the S buffer it came from: columns 0-31 the high part,
                 // 32-63 the low part, keys 2k and 2k + 1 in column k.
                 float ps[4] = {0.f, 0.f, 0.f, 0.f};
+                {
+                    uint32_t ph[32], pl[32];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t ph[16], pl[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float p0 = fast_exp2(fmaf(sv[32 * half + 2 * k], sc, -m_ref));
-                        const float p1 = fast_exp2(fmaf(sv[32 * half + 2 * k + 1], sc, -m_ref));
+                    for (int k = 0; k < kNK / 2; ++k) {
+                        const float p0 = fast_exp2(fmaf(sv[2 * k], sc, -m_ref));
+                        const float p1 = fast_exp2(fmaf(sv[2 * k + 1], sc, -m_ref));
                         ps[k & 3] += p0 + p1;
                         pack_split<DT>(p0, p1, ph[k], pl[k]);
                     }
-                    tmem_st16(lane_base + b * kNK + 16 * half, ph);
-                    tmem_st16(lane_base + b * kNK + 32 + 16 * half, pl);
+                    tc_st32u(lane_base + b * kNK, ph);
+                    tc_st32u(lane_base + b * kNK + 32, pl);
                 }
                 l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
                 tc_wait_st();
