@@ -1082,23 +1082,21 @@ kv_status_t paged_prefill_attention_fp8(const void* q, kv_dtype_t q_dtype, const
 namespace {
 
 struct SharedWs {
-    size_t parts, tails, part_o, part_ml, decode, total;
+    size_t parts, tails, part_o, part_ml, total;
     int max_rows;
-    WsLayout d;
 };
 
 SharedWs shared_workspace(int B, int Hq, int Hkv, int D, int sms) {
     SharedWs w;
     // 128 rows for each CTA's share of the work, and two parts more of every
-    // row (see prefix_units.cuh).
+    // row (see prefix_units.cuh); then the tails' partials (WsLayout).
     w.max_rows = static_cast<int>(int64_t{128} * sms + 2 * static_cast<int64_t>(B) * Hq);
+    const size_t rows = static_cast<size_t>(w.max_rows) + (static_cast<size_t>(sms) + B) * Hq;
     w.parts = 0;
     w.tails = align256(static_cast<size_t>(B) * Hkv * sizeof(int4));
     w.part_o = w.tails + align256(static_cast<size_t>(B) * Hkv * sizeof(int4));
-    w.part_ml = w.part_o + align256(static_cast<size_t>(w.max_rows) * D * 4);
-    w.decode = w.part_ml + align256(static_cast<size_t>(w.max_rows) * 8);
-    w.d = workspace_layout(B, Hq, Hkv, D, sms);
-    w.total = w.decode + w.d.total;
+    w.part_ml = w.part_o + align256(rows * D * 4);
+    w.total = w.part_ml + align256(rows * 8);
     return w;
 }
 
@@ -1215,10 +1213,8 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     d.tail_parts = reinterpret_cast<int4*>(ws + w.tails);
     d.prefix_parts = a.parts;
     d.out = out;
-    d.counters = reinterpret_cast<int32_t*>(ws + w.decode + w.d.counters);
-    d.part_o = reinterpret_cast<float*>(ws + w.decode + w.d.part_o);
-    d.part_ml = reinterpret_cast<float*>(ws + w.decode + w.d.part_ml);
-    d.cum = reinterpret_cast<int32_t*>(ws + w.decode + w.d.cum);
+    d.part_o = a.part_o + static_cast<size_t>(w.max_rows) * head_dim;
+    d.part_ml = a.part_ml + static_cast<size_t>(w.max_rows) * 2;
     d.status = status;
     d.num_blocks = num_blocks;
     d.max_blocks = max_blocks;

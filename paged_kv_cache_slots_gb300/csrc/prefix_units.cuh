@@ -142,12 +142,30 @@ struct Triple {
     int row0;        // partial row of the row tile's first row, part 0
 };
 
+// Tile x of a group whose first tile and partial row are `first` and row0, with
+// `parts` parts of each row: its head, row tile and places.
+__device__ __forceinline__ void place_in_group(Triple* t, int x, int first, int row0, int tiles, int parts) {
+    const int k = (x - first) / t->keys;
+    t->h = tiles == 1 ? k : k / tiles;
+    t->rt = k - t->h * tiles;
+    t->tile0 = first + k * t->keys;
+    t->row0 = row0 + t->h * parts * t->rows + t->rt * kPrefixRows;
+}
+
 // The triple of tile x, by the whole warp (0 <= x < W).  Part k of row r of its
 // row tile is partial row row0 + k * rows + r.
 template <class Args>
 __device__ __forceinline__ Triple find_triple(const Args& a, const Units& u, int G, int x) {
     const int lane = threadIdx.x & 31;
     Triple t{};
+    if (a.num_groups == 1) {
+        t.seq0 = __shfl_sync(0xffffffffu, u.first.seq0, 0);
+        t.rows = __shfl_sync(0xffffffffu, u.first.rows, 0);
+        t.blocks = __shfl_sync(0xffffffffu, u.first.blocks, 0);
+        t.keys = __shfl_sync(0xffffffffu, u.first.keys, 0);
+        place_in_group(&t, x, 0, 0, (t.rows + kPrefixRows - 1) / kPrefixRows, mul_div(t.keys, u.P, u.W) + 2);
+        return t;
+    }
     int tile0 = 0, row0 = 0;
     bool bad = false;
     for (int g0 = 0; g0 < a.num_groups; g0 += 32) {
@@ -171,11 +189,7 @@ __device__ __forceinline__ Triple find_triple(const Args& a, const Units& u, int
             const int tiles = __shfl_sync(0xffffffffu, p.tiles, src);
             const int np = __shfl_sync(0xffffffffu, parts, src);
             const int first = tile0 + __shfl_sync(0xffffffffu, w - work, src);
-            const int k = (x - first) / t.keys;
-            t.h = k / tiles;
-            t.rt = k - t.h * tiles;
-            t.tile0 = first + k * t.keys;
-            t.row0 = row0 + __shfl_sync(0xffffffffu, r - rows, src) + t.h * np * t.rows + t.rt * kPrefixRows;
+            place_in_group(&t, x, first, row0 + __shfl_sync(0xffffffffu, r - rows, src), tiles, np);
             return t;
         }
         tile0 += __shfl_sync(0xffffffffu, w, 31);

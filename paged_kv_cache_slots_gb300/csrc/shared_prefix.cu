@@ -9,58 +9,52 @@ namespace pkv {
 
 namespace {
 
-// One warp a (sequence, query head): the prefix's parts, then the parts the
-// decode kernel left of the tail.  Lane l holds (max, sum) of part l of 32;
-// every lane sums D / 32 output elements.
+// One warp a (sequence, query head): the prefix's parts, then the parts that
+// the tails left.  Lane l holds (max, sum) and the row of part l of 32; every
+// lane sums D / 32 output elements, four parts' loads at a time, the first four
+// asked for together with the (max, sum) pairs.  Bound by the latency of its
+// two rounds of loads: few registers, so that many warps wait at once.
 template <int D>
-__global__ void __launch_bounds__(128, 6) shared_prefix_merge_kernel(const SharedPrefixArgs a, const DecodeArgs d) {
+__global__ void __launch_bounds__(256, 4) shared_prefix_merge_kernel(const SharedPrefixArgs a, const DecodeArgs d) {
     constexpr int VD = D / 32;
     pdl_allow_next();
     pdl_wait();
-    const int64_t row = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    const int row = static_cast<int>((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
     const int lane = threadIdx.x & 31;
-    if (row >= static_cast<int64_t>(a.num_seqs) * a.num_q_heads) return;
-    const int s = static_cast<int>(row / a.num_q_heads);
-    const int hq = static_cast<int>(row - static_cast<int64_t>(s) * a.num_q_heads);
+    if (row >= a.num_seqs * a.num_q_heads) return;
+    const int s = row / a.num_q_heads;
+    const int hq = row - s * a.num_q_heads;
     const int G = a.num_q_heads / a.num_kv_heads;
     const int h = hq / G, g = hq - h * G;
-    const int Hc = d.heads_per_stage, chunks = d.num_kv_heads / Hc;
+    const int Hc = d.heads_per_stage;
     const int hc = h / Hc, hw = h - hc * Hc;
-    const int pair = s * chunks + hc;
-    const int4 pp = a.parts[static_cast<int64_t>(s) * a.num_kv_heads + h];
+    const int pair = s * (d.num_kv_heads / Hc) + hc;
+    const int4 pp = a.parts[s * a.num_kv_heads + h];
     const int4 tp = d.tail_parts[pair];
     const int n = pp.z + tp.y;
     float M = -INFINITY, L = 0.f, acc[VD];
 #pragma unroll
     for (int i = 0; i < VD; ++i) acc[i] = 0.f;
     for (int base = 0; base < n; base += 32) {
-        // This lane's part: its (max, sum) and its outputs.
+        // This lane's part: its row among all partial rows (the tails' follow the prefix's).
         const int p = base + lane;
-        const float* po = nullptr;
-        float2 ml = make_float2(-INFINITY, 0.f);
+        int r = -1;
         if (p < pp.z) {
-            const int64_t r = pp.x + static_cast<int64_t>(p) * pp.y + g;
-            if (r < a.max_rows) {
-                po = a.part_o + r * D;
-                ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + 2 * r));
-            }
+            r = pp.x + p * pp.y + g;
+            if (r >= a.max_rows) r = -1;
         } else if (p < n) {
             const int k = p - pp.z;
-            const int64_t c = tp.w == 0 ? tp.x + k : cta_of_tile(tp.z + k, tp.w, tp.x);
-            const int64_t r = ((c + pair) * Hc + hw) * G + g;
-            po = d.part_o + r * D;
-            ml = __ldcg(reinterpret_cast<const float2*>(d.part_ml + 2 * r));
+            const int c = tp.w == 0 ? tp.x + k : cta_of_tile(tp.z + k, tp.w, tp.x);
+            r = a.max_rows + ((c + pair) * Hc + hw) * G + g;
         }
-        const uint64_t addr = reinterpret_cast<uint64_t>(po);
         const int cnt = min(32, n - base);
-        // Outputs of eight parts; the first eight are asked for together with
-        // the (max, sum) pairs.
-        float v[8][VD];
+        float v[4][VD];
         auto fetch = [&](int k0) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, addr, (k0 + k) & 31));
-                const bool get = k0 + k < cnt && src != nullptr;
+            for (int k = 0; k < 4; ++k) {
+                const int rk = __shfl_sync(0xffffffffu, r, (k0 + k) & 31);
+                const bool get = k0 + k < cnt && rk >= 0;
+                const float* src = a.part_o + static_cast<int64_t>(get ? rk : 0) * D;
                 if constexpr (VD == 4) {
                     const float4 t = get ? __ldcg(reinterpret_cast<const float4*>(src) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
                     v[k][0] = t.x, v[k][1] = t.y, v[k][2] = t.z, v[k][3] = t.w;
@@ -70,12 +64,13 @@ __global__ void __launch_bounds__(128, 6) shared_prefix_merge_kernel(const Share
                 }
             }
         };
+        const float2 ml = r >= 0 ? __ldcg(reinterpret_cast<const float2*>(a.part_ml) + r) : make_float2(-INFINITY, 0.f);
         fetch(0);
         float mx = ml.x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         const float Mn = fmaxf(M, mx);
-        const float w = po ? fast_exp2(ml.x - Mn) : 0.f;
+        const float w = r >= 0 ? fast_exp2(ml.x - Mn) : 0.f;
         const float al = base == 0 ? 0.f : fast_exp2(M - Mn);
         float ls = w * ml.y;
 #pragma unroll
@@ -84,10 +79,11 @@ __global__ void __launch_bounds__(128, 6) shared_prefix_merge_kernel(const Share
         M = Mn;
 #pragma unroll
         for (int i = 0; i < VD; ++i) acc[i] *= al;
-        for (int k0 = 0; k0 < cnt; k0 += 8) {
+#pragma unroll 1
+        for (int k0 = 0; k0 < cnt; k0 += 4) {
             if (k0 > 0) fetch(k0);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < 4; ++k) {
                 const float wk = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
                 if (k0 + k < cnt) {
 #pragma unroll
@@ -97,7 +93,7 @@ __global__ void __launch_bounds__(128, 6) shared_prefix_merge_kernel(const Share
         }
     }
     const float inv = n > 0 ? 1.f / L : 0.f;  // a sequence without tokens: zeros
-    const int64_t o0 = row * D + lane * VD;
+    const int64_t o0 = static_cast<int64_t>(row) * D + lane * VD;
 #pragma unroll
     for (int i = 0; i < VD; ++i) acc[i] = n > 0 ? acc[i] * inv : 0.f;
     if (a.out_dtype == kF32) {
@@ -137,7 +133,7 @@ cudaError_t launch_merge_t(const SharedPrefixArgs& a, const DecodeArgs& tails, c
         if (cacheable) configured[tails.device].store(1);
     }
     const int64_t warps = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
-    return launch_kernel(kern, dim3(static_cast<unsigned>((warps + 3) / 4)), dim3(128), 0, stream, true, a, tails);
+    return launch_kernel(kern, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, stream, true, a, tails);
 }
 
 }  // namespace

@@ -18,8 +18,8 @@ struct SharedPrefixArgs {
     // Workspace.
     int4* parts;                 // [B][Hkv] (x, y, z, -): part k < z of query head g of the KV head is
                                  // partial row x + k * y + g
-    float* part_o;               // [max_rows][D]
-    float* part_ml;              // [max_rows][2]
+    float* part_o;               // [max_rows, then the tails'][D]
+    float* part_ml;              // [max_rows, then the tails'][2]
     int num_seqs, num_groups, num_blocks, max_blocks, num_q_heads, num_kv_heads, head_dim, block_size;
     int dtype, out_dtype, kv_dtype;
     float scale_log2, v_scale;

@@ -74,6 +74,7 @@ struct Bars {
     uint64_t kfull[10], kempty[10], vfull[10], vempty[10];
     uint64_t s_full[kS], p_full[kS], pv_done[kS], q_full, tmem_ready;
     float2 ml[2][kBM];  // (reference, sum) of each row in each softmax group
+    float down[kBM];    // E4M3 with a bf16 q: what undoes each row's power of two
     uint32_t tmem;
     int abort;
 };
@@ -415,58 +416,59 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
             const int n = min(end, t.tile0 + t.keys) - x;
             const int nrows = min(kBM, t.rows - t.rt * kBM);
             const int keys = min(t.blocks * a.block_size - (x - t.tile0) * kNK, n * kNK);  // of the segment
-            float sc = sc0;
             {
-                // Half of Q row r of the tile (member (rt * 128 + r) / G, query
-                // head h * G + r % G) into shared memory, 128-byte swizzled
-                // K-major.  (The previous segment's S are complete: all were
-                // read before its barriers.)
-                const int rr = t.rt * kBM + min(r, nrows - 1);
-                const int s = t.seq0 + rr / G;
-                const T* qrow = static_cast<const T*>(a.q) + (static_cast<int64_t>(s) * a.num_q_heads + t.h * G + rr % G) * D;
+                // Q rows of the tile (row r: member (rt * 128 + r) / G, query head
+                // h * G + r % G) into shared memory, 128-byte swizzled K-major:
+                // 16 rows a warp, whole rows at a time.  (The previous segment's S
+                // are complete: all were read before its barriers.)
+                constexpr int kChunks = D / 8, kRowsAtOnce = 32 / kChunks, kLoads = 16 / kRowsAtOnce;
+                const int chunk = lane % kChunks, sub = lane / kChunks;
                 // A negative scale is applied as |scale| to the scores of -q (a
                 // sign flip is exact), so the row maximum is taken on unscaled
                 // scores.
                 const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-                float up = 1.f;
-                if constexpr (kFP8 && QT == kBF16) {
-                    uint32_t top = 0;  // largest |q|, as the bits of a bf16
+                uint4 q[kLoads];
 #pragma unroll
-                    for (int q16 = 0; q16 < D / 8; ++q16) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(qrow + 8 * q16);
-                        const uint32_t b[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) top = max(top, max(b[k] & 0x7FFFu, (b[k] >> 16) & 0x7FFFu));
-                    }
-                    const int e = min(max(static_cast<int>(top >> 7) - 127, -100), 127);  // its exponent
-                    up = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
-                    sc *= __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
+                for (int k = 0; k < kLoads; ++k) {
+                    const int rr = t.rt * kBM + min(warp * 16 + k * kRowsAtOnce + sub, nrows - 1);
+                    q[k] = *reinterpret_cast<const uint4*>(
+                        static_cast<const T*>(a.q) +
+                        (static_cast<int64_t>(t.seq0 + rr / G) * a.num_q_heads + t.h * G + rr % G) * D + 8 * chunk);
                 }
 #pragma unroll
-                for (int q = 0; q < D / 16; ++q) {
-                    const int q16 = grp * (D / 16) + q;
-                    uint4 v = *reinterpret_cast<const uint4*>(qrow + 8 * q16);
+                for (int k = 0; k < kLoads; ++k) {
+                    const int row = warp * 16 + k * kRowsAtOnce + sub;
+                    uint4 v = q[k];
                     if constexpr (kFP8 && QT == kBF16) {
                         uint32_t* b = &v.x;
+                        uint32_t top = 0;  // the row's largest |q|, as the bits of a bf16
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const __half2 h = __floats2half2_rn(__uint_as_float(b[k] << 16) * up,
-                                                                __uint_as_float(b[k] & 0xFFFF0000u) * up);
-                            b[k] = *reinterpret_cast<const uint32_t*>(&h);
+                        for (int c = 0; c < 4; ++c) top = max(top, max(b[c] & 0x7FFFu, (b[c] >> 16) & 0x7FFFu));
+#pragma unroll
+                        for (int o = 1; o < kChunks; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const int e = min(max(static_cast<int>(top >> 7) - 127, -100), 127);  // its exponent
+                        const float up = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
+                        if (chunk == 0) B->down[row] = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const __half2 h = __floats2half2_rn(__uint_as_float(b[c] << 16) * up,
+                                                                __uint_as_float(b[c] & 0xFFFF0000u) * up);
+                            b[c] = *reinterpret_cast<const uint32_t*>(&h);
                         }
                     }
                     v.x ^= flip;
                     v.y ^= flip;
                     v.z ^= flip;
                     v.w ^= flip;
-                    *reinterpret_cast<uint4*>(base + S::kQOff + (q16 >> 3) * (kBM * 128) + r * 128 +
-                                              (((q16 & 7) ^ (r & 7)) << 4)) = v;
+                    *reinterpret_cast<uint4*>(base + S::kQOff + (chunk >> 3) * (kBM * 128) + row * 128 +
+                                              (((chunk & 7) ^ (row & 7)) << 4)) = v;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&B->q_full);  // one arrival per warp (count 8)
                 // The CTA with a triple's first tile says where its parts are,
                 // for the members of the row tile.
+                const int rr = t.rt * kBM + r, s = t.seq0 + rr / G;
                 if (x == t.tile0 && grp == 0 && r < nrows && rr % G == 0 && a.context_lens[s] / a.block_size >= t.blocks)
                     a.parts[static_cast<int64_t>(s) * a.num_kv_heads + t.h] =
                         make_int4(t.row0 + r, t.rows, cta_of_tile(t.tile0 + t.keys - 1, units.W, units.P) - cta + 1, 0);
@@ -479,6 +481,8 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
                 ok = __all_sync(0xffffffffu, wait(&B->s_full[b], k0 / kS, abort, a.status));
                 if (!ok) break;
                 tc_fence_after();
+                float sc = sc0;
+                if constexpr (kFP8 && QT == kBF16) sc *= B->down[r];  // written before the S that has come
                 float sv[kNK];
                 {
                     float t0[32], t1[32];
