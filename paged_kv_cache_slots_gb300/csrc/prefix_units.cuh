@@ -116,7 +116,7 @@ __device__ __forceinline__ Units plan_units(const Args& a, int G) {
 template <class Args>
 __device__ __forceinline__ void divide_sms(const Args& a, int items, int item_bytes, int chunks, Units* u) {
     constexpr float kTripleNs = 3000.f, kSequenceNs = 3700.f, kNsPerByte = 1.f / 55.f;
-    const float kTileNs = a.head_dim == 64 ? 560.f : 1000.f;
+    const float kTileNs = a.head_dim == 64 ? 700.f : a.kv_dtype == kFP8 ? 1400.f : 1000.f;
     const int sms = a.num_ctas;
     if (u->W == 0) return;
     const float parts = kTileNs * static_cast<float>(u->W) + kTripleNs * static_cast<float>(u->triples);

@@ -6,8 +6,8 @@ namespace pkv {
 
 cudaError_t launch_attend_f16(const SharedPrefixArgs& a, const DecodeArgs& d, const CUtensorMap& tmk,
                                const CUtensorMap& tmv, cudaStream_t stream) {
-    if (d.head_dim == 64) return launch_attend_t<MmaPolicy<kF16, 64, kPartsThreads>, kF16, 64, false>(a, d, tmk, tmv, stream);
-    return launch_attend_t<MmaPolicy<kF16, 128, kPartsThreads>, kF16, 128, false>(a, d, tmk, tmv, stream);
+    if (d.head_dim == 64) return launch_attend_t<MmaPolicy<kF16, 64, parts_threads(false)>, kF16, 64, false>(a, d, tmk, tmv, stream);
+    return launch_attend_t<MmaPolicy<kF16, 128, parts_threads(false)>, kF16, 128, false>(a, d, tmk, tmv, stream);
 }
 
 int prefix_static_smem_bytes() { return static_cast<int>(sizeof(Bars)) + 64; }

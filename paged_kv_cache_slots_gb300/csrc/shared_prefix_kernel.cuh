@@ -51,11 +51,12 @@ constexpr int kS = 4;                // S / P buffers in tensor memory, 64 colum
 constexpr uint32_t kO = kS * kNK;    // the two accumulators, D columns each
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLazy = 8.f;
-constexpr int kSoftmaxWarps = 8, kProducers = 2;
+constexpr int kSoftmaxWarps = 8;
 // E4M3: codes on their way to be widened, tiles a producer warp.
 constexpr int kRawRing = 5;
-constexpr uint32_t kRawStage = kNK * 128;
-constexpr int kPartsThreads = 32 * (kSoftmaxWarps + 2 + kProducers);
+// Producer warps of K and of V: an E4M3 tile is widened by two of each.
+__host__ __device__ constexpr int producers(bool fp8) { return fp8 ? 2 : 1; }
+__host__ __device__ constexpr int parts_threads(bool fp8) { return 32 * (kSoftmaxWarps + 2 + 2 * producers(fp8)); }
 
 template <int D, bool kFP8>
 struct Shape {
@@ -67,7 +68,7 @@ struct Shape {
     static constexpr uint32_t kKOff = kSlices * kBM * 128;
     static constexpr uint32_t kVOff = kKOff + kKRing * kTile;
     static constexpr uint32_t kRawOff = kVOff + kVRing * kTile;
-    static constexpr uint32_t kBytes = kRawOff + (kFP8 ? kProducers * kRawRing * kRawStage : 0);
+    static constexpr uint32_t kBytes = kRawOff + (kFP8 ? 2 * kRawRing * kNK * 128 : 0);
 };
 
 struct Bars {
@@ -154,13 +155,13 @@ __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
 template <int D, bool kFP8>
 __device__ __forceinline__ void init_bars(Bars* B) {
     using S = Shape<D, kFP8>;
-    // A tile is full with one arrival of its producer warp, or one a copying lane.
+    // A tile is full with one arrival of each of its producer warps, or one a copying lane.
     for (int i = 0; i < S::kKRing; ++i) {
-        mbar_init(&B->kfull[i], kFP8 ? 1 : 32);
+        mbar_init(&B->kfull[i], kFP8 ? producers(true) : 32);
         mbar_init(&B->kempty[i], 1);
     }
     for (int i = 0; i < S::kVRing; ++i) {
-        mbar_init(&B->vfull[i], kFP8 ? 1 : 32);
+        mbar_init(&B->vfull[i], kFP8 ? producers(true) : 32);
         mbar_init(&B->vempty[i], 1);
     }
     for (int i = 0; i < kS; ++i) {
@@ -194,8 +195,7 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
         // zeros.
         const int bs = a.block_size;
         const int ch = lane & 7, l8 = lane >> 3;
-        const int w = warp - kSoftmaxWarps - 2;
-        // One warp brings the K tiles, the other the V tiles.
+        const int w = (warp - kSoftmaxWarps - 2) & 1;  // 0: K tiles, 1: V tiles
         const char* cache = static_cast<const char*>(w == 0 ? a.k_cache : a.v_cache);
         uint8_t* tiles = base + (w == 0 ? S::kKOff : S::kVOff);
         uint64_t* full = w == 0 ? B->kfull : B->vfull;
@@ -270,17 +270,21 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
                 }
             } else {
                 // E4M3: the codes travel through a ring of this warp's own (each
-                // lane reads back what it copied) and are widened into the
-                // tile; lane e takes codes 16 (e % 8) .. of a row.
+                // lane reads back what it copied) and are widened into its
+                // share of the tile's runs; lane e takes codes 16 (e % 8) .. of a
+                // row.
+                constexpr int kRuns = 4 / producers(true);
+                constexpr uint32_t kStage = kRuns * 16 * 128;
+                const int share = (warp - kSoftmaxWarps - 2) >> 1;
                 const char* c0 = cache + l8 * D + ch * 16;
-                const uint32_t raw0 = smem_addr(base + S::kRawOff + w * (kRawRing * kRawStage)) + lane * 16;
+                const uint32_t raw0 = smem_addr(base + S::kRawOff) + (share * 2 + w) * (kRawRing * kStage) + lane * 16;
                 auto ask = [&](int j) {  // in order; an empty group past the end
                     if (j < n) {
                         advance(j);
-                        const uint32_t d = raw0 + j % kRawRing * kRawStage;
+                        const uint32_t d = raw0 + j % kRawRing * kStage;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int row = __shfl_sync(0xffffffffu, now, (j & 7) * 4 + k);
+                        for (int k = 0; k < kRuns; ++k) {
+                            const int row = __shfl_sync(0xffffffffu, now, (j & 7) * 4 + share * kRuns + k);
                             const bool real = row >= 0;
                             const char* src = c0 + (real ? static_cast<int64_t>(row) * D : 0);
 #pragma unroll
@@ -294,25 +298,22 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
                 for (int j = 0; j < n; ++j) {
                     ask(j + kRawRing - 1);
                     asm volatile("cp.async.wait_group %0;" ::"n"(kRawRing - 1) : "memory");  // tile j is here
-                    const uint32_t raw = raw0 + j % kRawRing * kRawStage;
+                    const uint32_t raw = raw0 + j % kRawRing * kStage;
                     uint8_t* t0 = tiles + st * S::kTile + (ch >> 2) * (kNK * 128);
+                    uint4 r[4 * kRuns];
+#pragma unroll
+                    for (int q = 0; q < 4 * kRuns; ++q)
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(r[q].x), "=r"(r[q].y), "=r"(r[q].z), "=r"(r[q].w)
+                                     : "r"(raw + q * 512));
                     ok = vacant();
                     if (!ok) break;
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        uint4 r[8];
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(r[q].x), "=r"(r[q].y), "=r"(r[q].z), "=r"(r[q].w)
-                                         : "r"(raw + (8 * hf + q) * 512));
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const int row = 32 * hf + 4 * q + l8;
-                            const int c2 = (ch & 3) * 2;
-                            *reinterpret_cast<uint4*>(t0 + row * 128 + ((c2 ^ (row & 7)) << 4)) = widen8(r[q].x, r[q].y);
-                            *reinterpret_cast<uint4*>(t0 + row * 128 + (((c2 + 1) ^ (row & 7)) << 4)) = widen8(r[q].z, r[q].w);
-                        }
+                    for (int q = 0; q < 4 * kRuns; ++q) {
+                        const int row = 16 * kRuns * share + 4 * q + l8;
+                        const int c2 = (ch & 3) * 2;
+                        *reinterpret_cast<uint4*>(t0 + row * 128 + ((c2 ^ (row & 7)) << 4)) = widen8(r[q].x, r[q].y);
+                        *reinterpret_cast<uint4*>(t0 + row * 128 + (((c2 + 1) ^ (row & 7)) << 4)) = widen8(r[q].z, r[q].w);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -608,10 +609,10 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
 
 // CTAs first .. are tails, the others parts (see decode_cta).
 template <class Policy, int QT, int D, bool kFP8>
-__global__ void __launch_bounds__(kPartsThreads, 1)
+__global__ void __launch_bounds__(parts_threads(kFP8), 1)
     shared_prefix_attend_kernel(const __grid_constant__ SharedPrefixArgs a, const __grid_constant__ DecodeArgs d,
                                 const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
-    static_assert(Policy::kMaxThreads == kPartsThreads && !Policy::kScratch);
+    static_assert(Policy::kMaxThreads == parts_threads(kFP8) && !Policy::kScratch);
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars bars;  // of the parts role
     if (threadIdx.x == 0) init_bars<D, kFP8>(&bars);
@@ -636,7 +637,7 @@ cudaError_t launch_attend_t(const SharedPrefixArgs& a, const DecodeArgs& d, cons
         if (e != cudaSuccess) return e;
         if (cacheable) configured[d.device].store(d.smem_bytes);
     }
-    return launch_kernel(kern, dim3(d.num_ctas), dim3(kPartsThreads), static_cast<size_t>(d.smem_bytes), stream, true,
+    return launch_kernel(kern, dim3(d.num_ctas), dim3(parts_threads(kFP8)), static_cast<size_t>(d.smem_bytes), stream, true,
                          a, d, tmk, tmv);
 }
 
