@@ -164,7 +164,7 @@ static __device__ int build_prefix(const DecodeArgs& a, int chunks, int32_t* cum
     if (tid == 0) cum[a.num_seqs] = carry;
     int ctas = a.num_ctas;
     if constexpr (kTails) {
-        divide_sms(a, carry, 2 * a.heads_per_stage * a.block_size * a.head_dim * dtype_bytes(a.kv_dtype), chunks, units);
+        divide_sms(a, carry, a.heads_per_stage * a.block_size, a.num_seqs * chunks, units);
         ctas -= units->P;
     }
     __syncthreads();

@@ -107,21 +107,23 @@ __device__ __forceinline__ Units plan_units(const Args& a, int G) {
     return u;
 }
 
-// The parts role's share of the SMs, u->P; the tails take the rest, `items` of
-// item_bytes of cache, with phantoms among them (DecodeArgs).
+// The parts role's share of the SMs, u->P; the tails take the rest: `items` of
+// `tokens` (token, KV head) rows, with phantoms among them (DecodeArgs), of
+// `pairs` (sequence, heads of a stage).
 //
-// A tile costs a parts CTA about kTileNs (of 128-element rows), the start and
-// end of a triple kTripleNs; the tails cost their bytes at the rate that an SM
-// reaches, and kSequenceNs for every (sequence, heads of a stage).
+// Measured costs on one SM: a tile of the parts role kTileNs, the start and end
+// of a triple kTripleNs; the tails kTokenNs for each row, whatever its length
+// (the consumer's arithmetic or the memory's rate), and kSequenceNs for each pair.
 template <class Args>
-__device__ __forceinline__ void divide_sms(const Args& a, int items, int item_bytes, int chunks, Units* u) {
-    constexpr float kTripleNs = 3000.f, kSequenceNs = 3700.f, kNsPerByte = 1.f / 55.f;
-    const float kTileNs = a.head_dim == 64 ? 700.f : a.kv_dtype == kFP8 ? 1400.f : 1000.f;
+__device__ __forceinline__ void divide_sms(const Args& a, int items, int tokens, int pairs, Units* u) {
+    constexpr float kTripleNs = 3000.f, kSequenceNs = 3700.f;
+    const bool fp8 = a.kv_dtype == kFP8;
+    const float kTileNs = a.head_dim == 64 ? 560.f : fp8 ? 1400.f : 1000.f;
+    const float kTokenNs = fp8 ? 7.f : 10.f;
     const int sms = a.num_ctas;
     if (u->W == 0) return;
     const float parts = kTileNs * static_cast<float>(u->W) + kTripleNs * static_cast<float>(u->triples);
-    const int pairs = a.num_seqs * chunks;
-    const float tails = kNsPerByte * static_cast<float>(max(items - a.phantom * pairs, 0)) * static_cast<float>(item_bytes) +
+    const float tails = kTokenNs * static_cast<float>(max(items - a.phantom * pairs, 0)) * static_cast<float>(tokens) +
                         kSequenceNs * static_cast<float>(pairs);
     int P = static_cast<int>(static_cast<float>(sms) * parts / (parts + tails) + 0.5f);
     P = max(1, min(min(P, u->W), sms - 1));  // a tails CTA there always is: it writes the merge's tables

@@ -477,10 +477,15 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
             // Unless it has a tile, a group weighs nothing.
             float m_ref = -1e30f, l = 0.f;
             const int j0 = (grp ^ i) & 1;
+            const bool idle = 32 * (warp & 3) >= nrows;  // none of the warp's rows is anybody's: P stays as it is
             for (int j = j0; j < n && ok; j += 2) {
                 const int k0 = i + j, b = k0 % kS;
                 ok = __all_sync(0xffffffffu, wait(&B->s_full[b], k0 / kS, abort, a.status));
                 if (!ok) break;
+                if (idle) {
+                    if (lane == 0) mbar_arrive(&B->p_full[b]);
+                    continue;
+                }
                 tc_fence_after();
                 float sc = sc0;
                 if constexpr (kFP8 && QT == kBF16) sc *= B->down[r];  // written before the S that has come
