@@ -234,7 +234,7 @@ class KVPool:
         self.dtype = dtype
         self.device = device
         self.shape = (num_blocks, num_kv_heads, block_size, head_dim)
-        self._kv_heads, self._head_dim = num_kv_heads, head_dim
+        self._kv_heads, self._head_dim, self._index = num_kv_heads, head_dim, device.index
         handle = ctypes.c_void_p()
         _check(lib.kv_pool_create(ctypes.byref(self.cfg), _ptr(buffer), buffer.numel(),
                                   ctypes.byref(handle)), lib)
@@ -354,59 +354,65 @@ class KVPool:
         contiguous).  positions: int32 [n], or [axes, n] for a rope with several axes.  A negative
         slot writes no K and V; a token with a negative seq_id writes nothing, q_out neither
         (a new q_out holds zeros there).  Returns q_out, or None without q."""
-        n, dt, fp8 = slot_mapping.shape[0], k.dtype, self.dtype == FP8
-        rows = (n, self._kv_heads, self._head_dim)
-        if fp8:
+        n, dt, D, index = slot_mapping.shape[0], k.dtype, self._head_dim, self._index
+        ks, vs = k.stride(), v.stride()
+        flat = rope.num_axes == 1
+        # The usual call in one expression; _check_append_rope says what is wrong with any other.
+        if not (k.shape == v.shape == (n, self._kv_heads, D) and ks[1:] == vs[1:] == (D, 1) and v.dtype == dt
+                and slot_mapping.dtype == positions.dtype == torch.int32 and slot_mapping.is_contiguous()
+                and positions.shape == ((n,) if flat else (rope.num_axes, n)) and positions.stride(-1) == 1
+                and (dt == self.dtype and dt != FP8 or self.dtype == FP8 and dt in _ROW_DTYPES
+                     and k_scale is not None and v_scale is not None)
+                and k.get_device() == v.get_device() == slot_mapping.get_device() == positions.get_device() == index):
+            positions = self._check_append_rope(k, v, slot_mapping, positions, rope, k_scale, v_scale)
+            ks, vs = k.stride(), v.stride()
+        ids = None
+        if seq_ids is not None:
+            _need(seq_ids.dtype == torch.int32 and seq_ids.shape == (n,) and seq_ids.is_contiguous()
+                  and seq_ids.get_device() == index, "seq_ids must be int32 [n_tokens] on the pool's device")
+            ids = seq_ids.data_ptr()
+        if q is not None:
+            if q_out is None:
+                make = torch.empty if seq_ids is None else torch.zeros
+                q_out = make(q.shape, dtype=q.dtype, device=q.device)
+            _need(q.dtype == dt and q.dim() == 3 and q.shape[0] == n and q.shape[2] == D and _rows_whole(q)
+                  and q.get_device() == index,
+                  "q must be [n_tokens, num_q_heads, head_dim] of k's dtype on the pool's device, a token's rows contiguous")
+            _need(q_out.dtype == dt and q_out.shape == q.shape and _rows_whole(q_out) and q_out.get_device() == index,
+                  "q_out must be like q")
+            query = (q.data_ptr(), q.stride(0), q_out.data_ptr(), q_out.stride(0), q.shape[1])
+        else:
+            _need(q_out is None, "q_out without q")
+            query = (None, 0, None, 0, 0)
+        if self.dtype != FP8:
+            k_scale = v_scale = 1.0
+        status = self._lib.kv_append_rope(
+            self._handle, layer, rope._handle, ids, n, k.data_ptr(), ks[0], v.data_ptr(), vs[0], DTYPE_CODE[dt],
+            slot_mapping.data_ptr(), positions.data_ptr(), n if flat else positions.stride(0), *query, float(k_scale),
+            float(v_scale), _stream(self.buffer, stream))
+        if status:
+            _check(status, self._lib)
+        return q_out
+
+    def _check_append_rope(self, k, v, slot_mapping, positions, rope, k_scale, v_scale):
+        """append_rope's checks one by one; returns positions, contiguous along tokens."""
+        n, dt, rows = slot_mapping.shape[0], k.dtype, (slot_mapping.shape[0], self._kv_heads, self._head_dim)
+        if self.dtype == FP8:
             _need(k_scale is not None and v_scale is not None, "an E4M3 pool needs k_scale and v_scale")
             _need(dt in _ROW_DTYPES, "k/v must be f32, f16 or bf16")
-            k_scale, v_scale = float(k_scale), float(v_scale)
         else:
             _need(dt == self.dtype, "k/v dtype must match the pool")
-            k_scale = v_scale = 1.0
         _need(v.dtype == dt, "k, v and q share a dtype")
         _need(k.shape == rows and v.shape == rows, "k and v must be [n_tokens, num_kv_heads, head_dim]")
         _need(_rows_whole(k) and _rows_whole(v), "a token's k and v rows must be contiguous")
         _need(slot_mapping.dtype == torch.int32 and slot_mapping.dim() == 1 and slot_mapping.is_contiguous(),
               "slot_mapping must be int32 [n_tokens]")
         _need(positions.dtype == torch.int32, "positions must be int32")
-        axes = rope.num_axes
-        if positions.dim() == 2:
-            _need(positions.shape == (axes, n), "positions must be [n_tokens], or [axes, n_tokens]")
-        else:
-            _need(axes == 1 and positions.shape == (n,), "positions must be [n_tokens], or [axes, n_tokens]")
-        if n > 1 and positions.stride(-1) != 1:
-            positions = positions.contiguous()
-        positions_stride = positions.stride(0) if axes > 1 else n
-        index = self.device.index
-        on = (k.get_device() == index and v.get_device() == index and slot_mapping.get_device() == index
-              and positions.get_device() == index)
-        ids = None
-        if seq_ids is not None:
-            _need(seq_ids.dtype == torch.int32 and seq_ids.shape == (n,) and seq_ids.is_contiguous(),
-                  "seq_ids must be int32 [n_tokens]")
-            on = on and seq_ids.get_device() == index
-            ids = seq_ids.data_ptr()
-        if q is not None:
-            _need(q.dtype == dt, "k, v and q share a dtype")
-            _need(q.dim() == 3 and q.shape[0] == n and q.shape[2] == rows[2] and _rows_whole(q),
-                  "q must be [n_tokens, num_q_heads, head_dim], a token's rows contiguous")
-            if q_out is None:
-                make = torch.empty if seq_ids is None else torch.zeros
-                q_out = make(q.shape, dtype=dt, device=q.device)
-            _need(q_out.dtype == dt and q_out.shape == q.shape and _rows_whole(q_out), "q_out must be like q")
-            on = on and q.get_device() == index and q_out.get_device() == index
-            query = (q.data_ptr(), q.stride(0), q_out.data_ptr(), q_out.stride(0), q.shape[1])
-        else:
-            _need(q_out is None, "q_out without q")
-            query = (None, 0, None, 0, 0)
-        _need(on, "every tensor must be on the pool's device")
-        status = self._lib.kv_append_rope(
-            self._handle, layer, rope._handle, ids, n, k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0),
-            DTYPE_CODE[dt], slot_mapping.data_ptr(), positions.data_ptr(), positions_stride, *query, k_scale, v_scale,
-            _stream(self.buffer, stream))
-        if status:
-            _check(status, self._lib)
-        return q_out
+        _need(positions.shape == (rope.num_axes, n) or (rope.num_axes == 1 and positions.shape == (n,)),
+              "positions must be [n_tokens], or [axes, n_tokens]")
+        _need(all(t.get_device() == self._index for t in (k, v, slot_mapping, positions)),
+              "every tensor must be on the pool's device")
+        return positions if n < 2 or positions.stride(-1) == 1 else positions.contiguous()
 
     def close(self):
         if getattr(self, "_handle", None):
@@ -422,9 +428,11 @@ class KVPool:
 
 def _rows_whole(t: torch.Tensor) -> bool:
     """[n, heads, D] whose heads lie one after the other (any stride between tokens)."""
-    if t.is_contiguous():
-        return True
-    return t.dim() == 3 and (t.shape[2] == 1 or t.stride(2) == 1) and (t.shape[1] == 1 or t.stride(1) == t.shape[2])
+    if t.dim() != 3:
+        return False
+    st, sh = t.stride(), t.shape
+    return (st[1] == sh[2] and st[2] == 1) or t.is_contiguous() or (
+        (sh[2] == 1 or st[2] == 1) and (sh[1] == 1 or st[1] == sh[2]))
 
 
 class Rope:
@@ -702,35 +710,29 @@ def paged_shared_prefix_attention(q, k_cache, v_cache, block_tables, context_len
     lib = _lib or load_library()
     B, Hq, D = q.shape
     NB, Hkv, bs, D2 = k_cache.shape
-    _need(D == D2 and v_cache.shape == k_cache.shape, "cache shapes")
     fp8 = k_cache.dtype == FP8
-    if fp8:
-        _need(v_cache.dtype == FP8 and k_scale is not None and v_scale is not None,
-              "an E4M3 cache needs both caches E4M3 and k_scale, v_scale")
-    else:
-        _need(q.dtype == k_cache.dtype == v_cache.dtype, "q and the caches share a dtype")
-    i32 = torch.int32
-    _need(block_tables.dtype == i32 and context_lens.dtype == i32 and group_start.dtype == i32
-          and prefix_lens.dtype == i32, "int32 tables")
+    i32, index = torch.int32, q.get_device()
+    groups = prefix_lens.shape[0] if prefix_lens.dim() == 1 else -1
+    out_dtype = out_dtype or q.dtype
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
+    if workspace is None:
+        workspace = make_shared_prefix_workspace(B, max(groups, 0), Hq, Hkv, D, q.device)
+    _need(D == D2 and v_cache.shape == k_cache.shape, "cache shapes")
+    _need((v_cache.dtype == FP8 and k_scale is not None and v_scale is not None) if fp8
+          else q.dtype == k_cache.dtype == v_cache.dtype,
+          "q and the caches share a dtype, or both caches are E4M3 with k_scale and v_scale")
+    _need(block_tables.dtype == context_lens.dtype == group_start.dtype == prefix_lens.dtype == i32, "int32 tables")
     _need(q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous() and block_tables.is_contiguous()
           and context_lens.is_contiguous() and group_start.is_contiguous() and prefix_lens.is_contiguous(),
           "contiguous inputs")
     _need(block_tables.dim() == 2 and block_tables.shape[0] == B and context_lens.shape == (B,),
           "one table row and length per sequence")
-    _need(prefix_lens.dim() == 1, "prefix_lens [groups]")
-    groups = prefix_lens.shape[0]
-    _need(group_start.shape == (groups + 1,), "group_start [groups + 1]")
-    out_dtype = out_dtype or q.dtype
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
+    _need(groups >= 0 and group_start.shape == (groups + 1,), "group_start [groups + 1], prefix_lens [groups]")
     _need(out.dtype == out_dtype and out.shape == q.shape and out.is_contiguous(), "out")
-    if workspace is None:
-        workspace = make_shared_prefix_workspace(B, groups, Hq, Hkv, D, q.device)
-    index = q.get_device()
-    _need(k_cache.get_device() == index and v_cache.get_device() == index and out.get_device() == index
-          and workspace.get_device() == index and block_tables.get_device() == index
-          and context_lens.get_device() == index and group_start.get_device() == index
-          and prefix_lens.get_device() == index, "every tensor must be on q's device")
+    _need(k_cache.get_device() == v_cache.get_device() == out.get_device() == workspace.get_device()
+          == block_tables.get_device() == context_lens.get_device() == group_start.get_device()
+          == prefix_lens.get_device() == index, "every tensor must be on q's device")
     sizes = (NB, block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, group_start.data_ptr(),
              prefix_lens.data_ptr(), groups, Hq, Hkv, D, bs)
     rest = (float(scale), out.data_ptr(), DTYPE_CODE[out_dtype], workspace.data_ptr(),

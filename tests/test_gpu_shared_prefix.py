@@ -182,6 +182,63 @@ def test_more_groups_than_plan_threads():
     b.check(b.run(), "1100 groups")
 
 
+@pytest.mark.parametrize("seed", range(12))
+def test_random_batches(seed):
+    """Sizes drawn over their ranges: many and few sequences, long and short prefixes and tails, any division of the SMs."""
+    rng = np.random.default_rng(1000 + seed)
+    n = int(rng.integers(1, 7))
+    sizes = [int(x) for x in rng.integers(0, 40 if seed % 2 else 9, n)]
+    bs = int(rng.choice([16, 32, 48, 64]))
+    plens = [int(np.exp(rng.uniform(0, 9 if seed % 3 else 7))) for _ in range(n)]
+    before, after = int(rng.integers(0, 3)), int(rng.integers(0, 3))
+    top = int(np.exp(rng.uniform(0, 8)))
+    ctx = [int(rng.integers(0, top + 1)) for _ in range(before)]
+    for m, p in zip(sizes, plens):
+        ctx += [p + int(rng.integers(0, top + 1)) if rng.random() < 0.9 else int(rng.integers(0, p + 1)) for _ in range(m)]
+    ctx += [int(rng.integers(0, top + 1)) for _ in range(after)]
+    fp8 = seed % 4 == 3
+    b = Batch(sizes, plens, ctx, str(rng.choice(["f16", "bf16"])), int(rng.choice([1, 2, 4, 8])), int(rng.choice([1, 2, 3, 5, 8])),
+              128 if fp8 else int(rng.choice([64, 128])), bs=bs, fp8=fp8, seed=seed, before=before, after=after) if ctx else None
+    if b is not None:
+        b.check(b.run(), f"seed {seed}")
+
+
+def test_the_mixed_prefix_workload():
+    """The workload of 64 sequences in groups of 8 with 2,048 shared tokens: as paged_decode_attention over the same tables."""
+    from workloads import SPECS, make_placement, step_layer_values
+
+    spec = SPECS["mixed_prefix_b64"]
+    pl = make_placement(spec)
+    pool = pkv.KVPool(1, pl.num_blocks, spec.block_size, spec.num_kv_heads, spec.head_dim, spec.torch_dtype)
+    kc, vc = pool.layer(0)
+    kc.normal_()
+    vc.normal_()
+    q = step_layer_values(spec, 64, 0, "cpu")[0].cuda()
+    tables, ctx = torch.from_numpy(pl.block_tables).cuda(), torch.from_numpy(pl.context_lens).cuda()
+    starts = torch.arange(0, 65, 8, dtype=torch.int32, device="cuda")
+    plens = torch.full((8,), 2048, dtype=torch.int32, device="cuda")
+    want = pkv.paged_decode_attention(q, kc, vc, tables, ctx, spec.attn_scale, out_dtype=torch.float32)
+    got = pkv.paged_shared_prefix_attention(q, kc, vc, tables, ctx, starts, plens, spec.attn_scale, out_dtype=torch.float32)
+    assert pkv.device_status() == (0, 0)
+    # Both are within the tolerance above of the formula: A is below 1 and E below 2^-13 here, n up to 16,384.
+    assert float((got - want).abs().max()) <= 2 * (4 * 2.0 ** -13 + 2.0 ** -15 + 2 * 16384 * 2.0 ** -24)
+
+
+def test_two_streams_at_once():
+    """Eager calls on two streams, each with a workspace of its own."""
+    b = Batch([7, 5], [1000, 2500], [1000 + 40 * i for i in range(7)] + [2500 + 60 * i for i in range(5)], "f16", 4, 4, 128)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    spaces = [b.workspace(), b.workspace()]
+    outs = [torch.full(b.q.shape, float("nan"), dtype=torch.float32, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st, w, o in zip(streams, spaces, outs):
+            b.run(workspace=w, out=o, stream=st)
+    torch.cuda.synchronize()
+    for o in outs:
+        b.check(o)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("G,bs", [(1, 16), (4, 32), (8, 48), (4, 128)])
 def test_e4m3(dtype, G, bs):
