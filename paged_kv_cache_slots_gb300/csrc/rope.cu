@@ -125,7 +125,7 @@ __device__ __forceinline__ float2 rotor(uint64_t turn, float amplitude) {
 
 // kRows: rows a thread loads before it uses the first.
 template <int DT, int V, bool kInter, int kRows>
-__global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 7) kv_append_rope_kernel(const __grid_constant__ RopeArgs a) {
     static_assert(kThreads >= kMaxRopePairs);
     using T = typename Elem<DT>::T;
     constexpr int kE = static_cast<int>(sizeof(T));
