@@ -1,6 +1,5 @@
-// How the shared-prefix attention divides its work, worked out alike by every
-// CTA of the parts kernel (shared_prefix.cu) and of the tails kernel
-// (decode_kernel.cuh) from the groups and lengths.
+// How the shared-prefix attention (shared_prefix_kernel.cuh) divides its work,
+// worked out alike by every CTA from the groups and lengths.
 //
 // The prefix part's work is key tiles: every (group, KV head, row tile) triple
 // has its group's tiles, triples in that order.  CTA c of P takes tiles
@@ -10,8 +9,8 @@
 // that has tiles of it; a group reserves keys P / W + 2 parts of each of its
 // rows, so all groups together reserve at most 128 P + 2 (all rows).
 //
-// The SMs are divided between the two kernels, one CTA on each, so that they
-// run side by side and end together.
+// The SMs are divided between the two roles, one CTA on each, so that they run
+// side by side and end together.
 #pragma once
 
 #include "device_utils.cuh"
@@ -83,7 +82,7 @@ struct Units {
     int W;             // tiles; 0: nothing is shared
     int triples;       // (group, KV head, row tile) triples with tiles
     bool bad;          // the groups are out of order
-    int P;             // CTAs of the parts kernel with work (divide_sms)
+    int P;             // CTAs of the parts role (divide_sms)
 };
 
 template <class Args>

@@ -28,7 +28,12 @@
 // sines stay in registers; kRows rows are loaded before the first is used.
 // V pairs are 16 bytes on each side where sizes and addresses allow it.
 //
-// Bound: HBM.  Every row is read and written once.
+// Bound: HBM.  Every row is read and written once: 16,384 tokens of 32 query
+// and 8 KV heads of 128 bf16 elements move 403 MB in 68 us, 5.9 TB/s (88 % of
+// the measured copy rate; 112 us when the slot and the padding flag were waited
+// for before the rows were asked for, 74 without a bound on the registers).
+// Small calls are bound by their launch and two rounds of loads (2.3 us for one
+// token).
 #include "device_utils.cuh"
 
 namespace pkv {

@@ -33,7 +33,21 @@
 // 356 us with one issuing lane, 290 with one warp walking the issue loop
 // converged, so that descriptors stay in uniform registers, 214 with two.)
 // P enters the product as a high and a low half-precision part, so that the
-// result carries fp32-like weights whatever the output type.
+// result carries fp32-like weights whatever the output type: 1.5 times the
+// matrix work of one part, whose rounding (2^-9 of each weight in bf16) would
+// be as large as that of a bf16 output.
+//
+// Bounds and measurements (128-dim heads, 32 query and 8 KV heads, bf16, both
+// launches):
+// - up to 128 query rows a KV head: the memory, and below some 10 us the start
+//   of the roles, one after another latency, and the merge (32 sequences,
+//   4,096 shared tokens: 22 us; 65,536 shared: 65 us, 4.1 TB/s of K and V);
+// - more: the tensor pipe, 50 % active by its counter (256 sequences, 32,768
+//   shared: 188 us, 740 TFLOP/s, or 1,110 of matrix work).
+// Tried and left: 2 KB tensor copies for K and V (61 ns each on one SM, slower
+// than 16-byte copies by 10 % where matrix work bounds), one softmax group a CTA
+// with two CTAs an SM (219 us on the wide case, and no room for tails beside
+// it), packed fp32 pairs in the softmax (-5 % on the wide case, +3 % on small).
 #pragma once
 
 #include "decode_kernel.cuh"
