@@ -87,7 +87,8 @@ struct Shape {
 
 struct Bars {
     uint64_t kfull[10], kempty[10], vfull[10], vempty[10];
-    uint64_t s_full[kS], p_full[kS], pv_done[kS], q_full, tmem_ready;
+    uint64_t s_full[kS], p_full[kS], pv_done[kS], tmem_ready;
+    uint64_t q_full[2];  // segments in turn: an issuing warp without a tile in one may be a segment late
     float2 ml[2][kBM];  // (reference, sum) of each row in each softmax group
     float down[kBM];    // E4M3 with a bf16 q: what undoes each row's power of two
     uint32_t tmem;
@@ -183,7 +184,7 @@ __device__ __forceinline__ void init_bars(Bars* B) {
         mbar_init(&B->p_full[i], 4);
         mbar_init(&B->pv_done[i], 1);
     }
-    mbar_init(&B->q_full, kSoftmaxWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(&B->q_full[i], kSoftmaxWarps);
     mbar_init(&B->tmem_ready, 1);
     B->abort = 0;
     fence_barrier_init();
@@ -405,7 +406,7 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
             const Triple t = find_triple(a, units, G, x);
             const int n = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(min(end, t.tile0 + t.keys) - x)));
             const int j0 = (me ^ i) & 1;
-            ok = ready(&B->q_full, seg);
+            ok = ready(&B->q_full[seg & 1], seg >> 1);
             if (ok && j0 < n) ok = score(i + j0);
             for (int j = j0; j < n && ok; j += 2) {
                 if (j + 2 < n) ok = score(i + j + 2);
@@ -424,9 +425,9 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
         // |scale| in log2 units; a zero scale is taken as 1e-30, which leaves
         // every finite score's exponent at 0 while masked scores stay -inf.
         const float sc0 = fmaxf(fabsf(a.scale_log2), 1e-30f);
-        int i = 0;
+        int i = 0, seg = 0;
         bool ok = true;  // (a failed wait skips the work, not the barriers)
-        for (int x = start; x < end;) {
+        for (int x = start; x < end; ++seg) {
             const Triple t = find_triple(a, units, G, x);
             const int n = min(end, t.tile0 + t.keys) - x;
             const int nrows = min(kBM, t.rows - t.rt * kBM);
@@ -480,7 +481,7 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&B->q_full);  // one arrival per warp (count 8)
+                if (lane == 0) mbar_arrive(&B->q_full[seg & 1]);  // one arrival per warp (count 8)
                 // The CTA with a triple's first tile says where its parts are,
                 // for the members of the row tile.
                 const int rr = t.rt * kBM + r, s = t.seq0 + rr / G;
