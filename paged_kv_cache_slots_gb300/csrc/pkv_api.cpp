@@ -1201,7 +1201,7 @@ kv_status_t shared_prefix_impl(const void* q, kv_dtype_t dtype, const void* k_ca
     const int parts_smem = prefix_smem_bytes(head_dim, fp8);
     if (parts_smem > max_smem) return fail(KV_ERR_UNSUPPORTED, "%s: not enough shared memory on this device", what);
 
-    DecodeArgs d{};
+    TailArgs d{};
     d.q = q;
     d.k_cache = k_cache;
     d.v_cache = v_cache;

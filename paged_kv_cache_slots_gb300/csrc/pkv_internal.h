@@ -129,7 +129,10 @@ struct DecodeArgs {
     int test_stall;       // testing only: see kv_decode_options_t
     int device;           // CUDA ordinal the launch targets
     int phantom;          // items without data at the start of every (sequence, head chunk) pair
-    // Tails of shared prefixes only: the groups (see paged_shared_prefix_attention).
+};
+
+// The tails of shared prefixes (see paged_shared_prefix_attention).
+struct TailArgs : DecodeArgs {
     const int32_t* group_start;  // [num_groups + 1]
     const int32_t* prefix_lens;  // [num_groups]
     int num_groups;

@@ -15,7 +15,7 @@ namespace {
 // asked for together with the (max, sum) pairs.  Bound by the latency of its
 // two rounds of loads: few registers, so that many warps wait at once.
 template <int D>
-__global__ void __launch_bounds__(256, 4) shared_prefix_merge_kernel(const SharedPrefixArgs a, const DecodeArgs d) {
+__global__ void __launch_bounds__(256, 4) shared_prefix_merge_kernel(const SharedPrefixArgs a, const TailArgs d) {
     constexpr int VD = D / 32;
     pdl_allow_next();
     pdl_wait();
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(256, 4) shared_prefix_merge_kernel(const Share
 }
 
 template <int D>
-cudaError_t launch_merge_t(const SharedPrefixArgs& a, const DecodeArgs& tails, cudaStream_t stream) {
+cudaError_t launch_merge_t(const SharedPrefixArgs& a, const TailArgs& tails, cudaStream_t stream) {
     static std::atomic<int> configured[64];
     auto kern = shared_prefix_merge_kernel<D>;
     const bool cacheable = tails.device >= 0 && tails.device < 64;
@@ -138,7 +138,7 @@ cudaError_t launch_merge_t(const SharedPrefixArgs& a, const DecodeArgs& tails, c
 
 }  // namespace
 
-cudaError_t launch_shared_prefix(const SharedPrefixArgs& a, const DecodeArgs& d, const CUtensorMap& tmk,
+cudaError_t launch_shared_prefix(const SharedPrefixArgs& a, const TailArgs& d, const CUtensorMap& tmk,
                                  const CUtensorMap& tmv, cudaStream_t stream) {
     cudaError_t e = d.kv_dtype == kFP8    ? launch_attend_fp8(a, d, tmk, tmv, stream)
                     : d.dtype == kBF16 ? launch_attend_bf16(a, d, tmk, tmv, stream)

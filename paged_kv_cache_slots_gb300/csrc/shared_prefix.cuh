@@ -29,13 +29,13 @@ struct SharedPrefixArgs {
 // Shared memory of the parts role: dynamic, and what the kernel holds besides.
 int prefix_static_smem_bytes();
 int prefix_smem_bytes(int head_dim, bool fp8);
-cudaError_t launch_attend_f16(const SharedPrefixArgs& a, const DecodeArgs& d, const CUtensorMap& tmap_k,
+cudaError_t launch_attend_f16(const SharedPrefixArgs& a, const TailArgs& d, const CUtensorMap& tmap_k,
                               const CUtensorMap& tmap_v, cudaStream_t stream);
-cudaError_t launch_attend_bf16(const SharedPrefixArgs& a, const DecodeArgs& d, const CUtensorMap& tmap_k,
+cudaError_t launch_attend_bf16(const SharedPrefixArgs& a, const TailArgs& d, const CUtensorMap& tmap_k,
                                const CUtensorMap& tmap_v, cudaStream_t stream);
-cudaError_t launch_attend_fp8(const SharedPrefixArgs& a, const DecodeArgs& d, const CUtensorMap& tmap_k,
+cudaError_t launch_attend_fp8(const SharedPrefixArgs& a, const TailArgs& d, const CUtensorMap& tmap_k,
                               const CUtensorMap& tmap_v, cudaStream_t stream);
-cudaError_t launch_shared_prefix(const SharedPrefixArgs& a, const DecodeArgs& d, const CUtensorMap& tmap_k,
+cudaError_t launch_shared_prefix(const SharedPrefixArgs& a, const TailArgs& d, const CUtensorMap& tmap_k,
                                  const CUtensorMap& tmap_v, cudaStream_t stream);
 
 }  // namespace pkv

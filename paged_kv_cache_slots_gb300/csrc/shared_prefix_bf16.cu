@@ -4,7 +4,7 @@
 
 namespace pkv {
 
-cudaError_t launch_attend_bf16(const SharedPrefixArgs& a, const DecodeArgs& d, const CUtensorMap& tmk,
+cudaError_t launch_attend_bf16(const SharedPrefixArgs& a, const TailArgs& d, const CUtensorMap& tmk,
                                const CUtensorMap& tmv, cudaStream_t stream) {
     if (d.head_dim == 64) return launch_attend_t<MmaPolicy<kBF16, 64, parts_threads(false)>, kBF16, 64, false>(a, d, tmk, tmv, stream);
     return launch_attend_t<MmaPolicy<kBF16, 128, parts_threads(false)>, kBF16, 128, false>(a, d, tmk, tmv, stream);

@@ -4,7 +4,7 @@
 
 namespace pkv {
 
-cudaError_t launch_attend_fp8(const SharedPrefixArgs& a, const DecodeArgs& d, const CUtensorMap& tmk,
+cudaError_t launch_attend_fp8(const SharedPrefixArgs& a, const TailArgs& d, const CUtensorMap& tmk,
                               const CUtensorMap& tmv, cudaStream_t stream) {
     constexpr int kT = parts_threads(true);
     if (d.dtype == kF16) return launch_attend_t<MmaFp8Policy<kF16, 128, false, kT>, kF16, 128, true>(a, d, tmk, tmv, stream);

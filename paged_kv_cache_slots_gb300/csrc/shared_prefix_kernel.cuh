@@ -627,10 +627,10 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
     }
 }
 
-// CTAs first .. are tails, the others parts (see decode_cta).
+// CTAs first .. are tails, the others parts (see decode_tails).
 template <class Policy, int QT, int D, bool kFP8>
 __global__ void __launch_bounds__(parts_threads(kFP8), 1)
-    shared_prefix_attend_kernel(const __grid_constant__ SharedPrefixArgs a, const __grid_constant__ DecodeArgs d,
+    shared_prefix_attend_kernel(const __grid_constant__ SharedPrefixArgs a, const __grid_constant__ TailArgs d,
                                 const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
     static_assert(Policy::kMaxThreads == parts_threads(kFP8) && !Policy::kScratch);
     extern __shared__ uint8_t smem_raw[];
@@ -641,12 +641,14 @@ __global__ void __launch_bounds__(parts_threads(kFP8), 1)
     uint8_t* base = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     Units units;
-    if (decode_cta<Policy, true>(d, tmk, tmv, base, &units)) return;
+    bool parts = false;
+    decode_tails<Policy>(d, tmk, tmv, base, &units, &parts);
+    if (!parts) return;
     parts_cta<QT, D, kFP8>(a, base, &bars, units, static_cast<int>(blockIdx.x) - (d.num_ctas - units.P));
 }
 
 template <class Policy, int QT, int D, bool kFP8>
-cudaError_t launch_attend_t(const SharedPrefixArgs& a, const DecodeArgs& d, const CUtensorMap& tmk,
+cudaError_t launch_attend_t(const SharedPrefixArgs& a, const TailArgs& d, const CUtensorMap& tmk,
                             const CUtensorMap& tmv, cudaStream_t stream) {
     static std::atomic<int> configured[64];
     auto kern = shared_prefix_attend_kernel<Policy, QT, D, kFP8>;
