@@ -43,7 +43,7 @@
 //   of the roles, one after another latency, and the merge (32 sequences,
 //   4,096 shared tokens: 22 us; 65,536 shared: 65 us, 4.1 TB/s of K and V);
 // - more: the tensor pipe, 50 % active by its counter (256 sequences, 32,768
-//   shared: 188 us, 740 TFLOP/s, or 1,110 of matrix work).
+//   shared: 191 us, 725 TFLOP/s, or 1,090 of matrix work).
 // Tried and left: 2 KB tensor copies for K and V (61 ns each on one SM, slower
 // than 16-byte copies by 10 % where matrix work bounds), one softmax group a CTA
 // with two CTAs an SM (219 us on the wide case, and no room for tails beside
