@@ -422,9 +422,10 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
         const int r = tid & (kBM - 1), grp = tid / kBM;
         const uint32_t lane_base = taddr + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         const uint32_t o_base = lane_base + kO + grp * D;
-        // |scale| in log2 units; a zero scale is taken as 1e-30, which leaves
+        // |scale| in log2 units; a zero multiplier is taken as 1e-30, which leaves
         // every finite score's exponent at 0 while masked scores stay -inf.
-        const float sc0 = fmaxf(fabsf(a.scale_log2), 1e-30f);
+        constexpr float kLeast = 1e-30f;
+        const float sc0 = fmaxf(fabsf(a.scale_log2), kLeast);
         int i = 0, seg = 0;
         bool ok = true;  // (a failed wait skips the work, not the barriers)
         for (int x = start; x < end; ++seg) {
@@ -503,7 +504,10 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
                 }
                 tc_fence_after();
                 float sc = sc0;
-                if constexpr (kFP8 && QT == kBF16) sc *= B->down[r];  // written before the S that has come
+                // (down was written before the S that has come.  The product may
+                // underflow to 0, and the scores over codes are below 2^14 * 448 *
+                // 128 < 2^30: kLeast leaves their exponents at 0 as well.)
+                if constexpr (kFP8 && QT == kBF16) sc = fmaxf(sc * B->down[r], kLeast);
                 float sv[kNK];
                 {
                     float t0[32], t1[32];
