@@ -181,6 +181,25 @@ def _stream(t: torch.Tensor, stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _made(t: torch.Tensor, stream, make) -> torch.Tensor:
+    """make(), a tensor of a call's own on t's device, on the stream that the call is given.
+
+    On a stream other than torch's current one this puts the fill or copy that make() does, and whatever held the
+    memory before, in order with the call's kernels.  The current stream, where the caller may read what is returned,
+    has to reach the point of its release too before the memory is used again."""
+    if stream is None:
+        return make()
+    handle, current = _stream(t, stream), torch.cuda.current_stream(t.device)
+    if handle == current.cuda_stream:
+        return make()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, device=t.device) if handle else torch.cuda.default_stream(t.device)
+    with torch.cuda.stream(stream):
+        made = make()
+    made.record_stream(current)
+    return made
+
+
 def _call_on(t: torch.Tensor, lib, fn, *args):
     """Call a library entry point with t's device current: the library takes
     the SM count, the status word and the static scratch of the current
@@ -353,7 +372,11 @@ class KVPool:
         k, v and q may be slices of a packed projection (any stride between tokens, heads
         contiguous).  positions: int32 [n], or [axes, n] for a rope with several axes.  A negative
         slot writes no K and V; a token with a negative seq_id writes nothing, q_out neither
-        (a new q_out holds zeros there).  Returns q_out, or None without q."""
+        (a new q_out holds zeros there).  Returns q_out, or None without q.
+
+        Everything runs on `stream` (torch's current one unless given), a new q_out's zeros and the
+        copy of positions that are not contiguous too: order the inputs before it, and what reads
+        the outputs behind it."""
         n, dt, D, index = slot_mapping.shape[0], k.dtype, self._head_dim, self._index
         ks, vs = k.stride(), v.stride()
         flat = rope.num_axes == 1
@@ -364,7 +387,7 @@ class KVPool:
                 and (dt == self.dtype and dt != FP8 or self.dtype == FP8 and dt in _ROW_DTYPES
                      and k_scale is not None and v_scale is not None)
                 and k.get_device() == v.get_device() == slot_mapping.get_device() == positions.get_device() == index):
-            positions = self._check_append_rope(k, v, slot_mapping, positions, rope, k_scale, v_scale)
+            positions = self._check_append_rope(k, v, slot_mapping, positions, rope, k_scale, v_scale, stream)
             ks, vs = k.stride(), v.stride()
         ids = None
         if seq_ids is not None:
@@ -374,7 +397,7 @@ class KVPool:
         if q is not None:
             if q_out is None:
                 make = torch.empty if seq_ids is None else torch.zeros
-                q_out = make(q.shape, dtype=q.dtype, device=q.device)
+                q_out = _made(self.buffer, stream, lambda: make(q.shape, dtype=q.dtype, device=q.device))
             _need(q.dtype == dt and q.dim() == 3 and q.shape[0] == n and q.shape[2] == D and _rows_whole(q)
                   and q.get_device() == index,
                   "q must be [n_tokens, num_q_heads, head_dim] of k's dtype on the pool's device, a token's rows contiguous")
@@ -394,7 +417,7 @@ class KVPool:
             _check(status, self._lib)
         return q_out
 
-    def _check_append_rope(self, k, v, slot_mapping, positions, rope, k_scale, v_scale):
+    def _check_append_rope(self, k, v, slot_mapping, positions, rope, k_scale, v_scale, stream):
         """append_rope's checks one by one; returns positions, contiguous along tokens."""
         n, dt, rows = slot_mapping.shape[0], k.dtype, (slot_mapping.shape[0], self._kv_heads, self._head_dim)
         if self.dtype == FP8:
@@ -412,7 +435,7 @@ class KVPool:
               "positions must be [n_tokens], or [axes, n_tokens]")
         _need(all(t.get_device() == self._index for t in (k, v, slot_mapping, positions)),
               "every tensor must be on the pool's device")
-        return positions if n < 2 or positions.stride(-1) == 1 else positions.contiguous()
+        return positions if n < 2 or positions.stride(-1) == 1 else _made(self.buffer, stream, positions.contiguous)
 
     def close(self):
         if getattr(self, "_handle", None):

@@ -1,0 +1,137 @@
+"""GPU tests of calls that are given a stream other than torch's current one, and make a tensor of their own.
+
+The current stream is kept busy for some milliseconds, so that whatever a call leaves on it comes late."""
+import pytest
+import torch
+
+import paged_kv_cache_slots_gb300 as pkv
+from test_gpu_append_rope import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    yield
+    torch.cuda.empty_cache()
+
+
+class Busy:
+    """Matrix products on the stream that is current at the call."""
+
+    def __init__(self):
+        self.a = torch.randn((4096, 4096), device="cuda").half()
+        self.c = torch.empty_like(self.a)
+        torch.mm(self.a, self.a, out=self.c)
+        torch.cuda.synchronize()
+
+    def __call__(self):
+        for _ in range(60):
+            torch.mm(self.a, self.a, out=self.c)
+
+
+@pytest.fixture(scope="module")
+def busy():
+    return Busy()
+
+
+def _handles(side):
+    return [side, side.cuda_stream, torch.cuda.ExternalStream(side.cuda_stream)]
+
+
+@pytest.mark.parametrize("which", range(3))
+def test_new_query_rows_with_padding(busy, which):
+    c = Case(300, 8, 2, 128, 128, "bf16", packed=True)
+    ids = torch.arange(300, dtype=torch.int32, device="cuda")
+    ids[[7, 299]] = -1
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy()
+    q_out = c.run(seq_ids=ids, stream=_handles(side)[which])
+    side.synchronize()
+    torch.cuda.synchronize()
+    c.check(q_out, ids)
+    assert bool((q_out[[7, 299]] == 0).all())
+
+
+def test_new_query_rows_without_padding(busy):
+    c = Case(64, 8, 2, 128, 64, "f16")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy()
+    q_out = c.run(stream=side)
+    torch.cuda.synchronize()
+    c.check(q_out)
+
+
+@pytest.mark.parametrize("axes", [1, 3])
+def test_positions_that_are_copied(busy, axes):
+    """Columns of [tokens, axes], copied into rows: the copy comes before the kernel, and its memory stays until then."""
+    c = Case(500, 8, 2, 64, 64, "bf16", axes=axes)
+    base = torch.full((500, axes + 2), 9, dtype=torch.int32, device="cuda")
+    base[:, 1:axes + 1] = c.pos.t()
+    keep = c.pos
+    c.pos = base[:, 1:axes + 1].t()
+    q_out = torch.empty_like(c.q)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy()
+    with torch.cuda.stream(side):
+        busy()
+    c.run(q_out=q_out, stream=side)
+    late = [torch.full((axes, 500), 77, dtype=torch.int32, device="cuda") for _ in range(8)]  # may take freed memory
+    torch.cuda.synchronize()
+    c.pos = keep
+    c.check(q_out)
+    assert all(bool((x == 77).all()) for x in late)
+
+
+def test_the_default_stream_by_number(busy):
+    c = Case(300, 4, 2, 128, 128, "f16")
+    ids = torch.arange(300, dtype=torch.int32, device="cuda")
+    ids[3] = -1
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        busy()
+        q_out = c.run(seq_ids=ids, stream=0)
+    torch.cuda.synchronize()
+    c.check(q_out, ids)
+    assert bool((q_out[3] == 0).all())
+
+
+def test_a_forked_stream_in_a_captured_graph():
+    c = Case(40, 8, 2, 128, 128, "bf16", axes=2)
+    ids = torch.arange(40, dtype=torch.int32, device="cuda")
+    ids[5] = -1
+    base = c.pos.t().contiguous()
+    keep, c.pos = c.pos, base.t()
+    c.run(seq_ids=ids)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        q_out = c.run(seq_ids=ids, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    c.q.normal_()
+    c.k.normal_()
+    base.add_(31)
+    c.pool.buffer.fill_(0x2B)
+    graph.replay()
+    torch.cuda.synchronize()
+    c.pos = keep + 31
+    c.check(q_out, ids)
+    assert bool((q_out[5] == 0).all())
+
+
+def test_outputs_filled_before_the_other_stream_waits():
+    """The order that a caller has to keep: fill, let the other stream wait, call, wait for it."""
+    c = Case(19, 8, 2, 128, 128, "bf16")
+    side = torch.cuda.Stream()
+    q_out = torch.full_like(c.q, float("nan"))
+    side.wait_stream(torch.cuda.current_stream())
+    c.run(q_out=q_out, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    c.check(q_out)
+    assert pkv.device_status() == (0, 0)
