@@ -738,9 +738,9 @@ def paged_shared_prefix_attention(q, k_cache, v_cache, block_tables, context_len
     groups = prefix_lens.shape[0] if prefix_lens.dim() == 1 else -1
     out_dtype = out_dtype or q.dtype
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
+        out = _made(q, stream, lambda: torch.empty((B, Hq, D), dtype=out_dtype, device=q.device))
     if workspace is None:
-        workspace = make_shared_prefix_workspace(B, max(groups, 0), Hq, Hkv, D, q.device)
+        workspace = _made(q, stream, lambda: make_shared_prefix_workspace(B, max(groups, 0), Hq, Hkv, D, q.device))
     _need(D == D2 and v_cache.shape == k_cache.shape, "cache shapes")
     _need((v_cache.dtype == FP8 and k_scale is not None and v_scale is not None) if fp8
           else q.dtype == k_cache.dtype == v_cache.dtype,

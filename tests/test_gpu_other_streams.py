@@ -6,6 +6,7 @@ import torch
 
 import paged_kv_cache_slots_gb300 as pkv
 from test_gpu_append_rope import Case
+from test_gpu_shared_prefix import Batch
 
 pytestmark = pytest.mark.gpu
 
@@ -135,3 +136,52 @@ def test_outputs_filled_before_the_other_stream_waits():
     torch.cuda.current_stream().wait_stream(side)
     c.check(q_out)
     assert pkv.device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_shared_prefix_attention_with_tensors_of_its_own(busy, fp8):
+    """out and workspace are made by the call: what the current stream still does with their memory, or does with memory
+    that it takes after the call, does not reach them."""
+    b = Batch([9, 4], [700, 2000], [700 + 30 * i for i in range(9)] + [2000, 2100, 2500, 1999], "bf16", 4, 4, 128, fp8=fp8)
+    n = b.workspace().numel()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    # Memory that is free for the current stream's next tensors, and that the stream has yet to write.
+    busy()
+    early = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    early += [torch.full(b.q.shape, float("nan"), dtype=torch.float32, device="cuda") for _ in range(3)]
+    del early
+    with torch.cuda.stream(side):
+        busy()
+    out = pkv.paged_shared_prefix_attention(b.q, b.kc, b.vc, b.tables, b.ctx, b.starts, b.plens, b.scale,
+                                            out_dtype=torch.float32, stream=side, **b.scales)
+    late = [torch.full((n,), 0x55, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    b.check(out)
+    assert all(bool((x == 0x55).all()) for x in late)
+
+
+def test_shared_prefix_attention_on_a_forked_stream_in_a_captured_graph():
+    b = Batch([6, 3], [800, 320], [800 + 50 * i for i in range(6)] + [320, 400, 330], "f16", 4, 2, 128)
+    b.run()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        out = pkv.paged_shared_prefix_attention(b.q, b.kc, b.vc, b.tables, b.ctx, b.starts, b.plens, b.scale,
+                                                out_dtype=torch.float32, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    b.q.normal_()
+    graph.replay()
+    torch.cuda.synchronize()
+    b.check(out)
+
+
+def test_shared_prefix_out_filled_before_the_other_stream_waits():
+    b = Batch([6], [800], [800 + 50 * i for i in range(6)], "bf16", 4, 2, 128)
+    ws, side = b.workspace(), torch.cuda.Stream()
+    out = torch.full(b.q.shape, float("nan"), dtype=torch.float32, device="cuda")
+    side.wait_stream(torch.cuda.current_stream())
+    b.run(workspace=ws, out=out, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    b.check(out)
