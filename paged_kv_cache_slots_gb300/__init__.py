@@ -309,7 +309,7 @@ class KVPool:
 
         Returns the host buffer (uint8, kv_swap_bytes(n) bytes; a new pinned
         tensor unless `host` is given).  Asynchronous on `stream`."""
-        ids = self._swap_ids(block_ids)
+        ids = _made(self.buffer, stream, lambda: self._swap_ids(block_ids))
         n = ids.numel()
         need = self.swap_bytes(n)
         if host is None:
@@ -323,7 +323,7 @@ class KVPool:
 
     def swap_in(self, block_ids, host: torch.Tensor, stream=None):
         """Copy swapped records from host memory into the listed blocks."""
-        ids = self._swap_ids(block_ids)
+        ids = _made(self.buffer, stream, lambda: self._swap_ids(block_ids))
         n = ids.numel()
         _need(host.dtype == torch.uint8 and host.is_contiguous() and host.numel() >= self.swap_bytes(n),
               "host must be a contiguous uint8 tensor of at least swap_bytes(n) bytes")
@@ -504,7 +504,7 @@ def slot_mapping(block_tables: torch.Tensor, context_lens: torch.Tensor, block_s
     _need(block_tables.dtype == torch.int32 and context_lens.dtype == torch.int32, "int32 inputs")
     _need(block_tables.is_contiguous() and block_tables.shape[0] == B, "block_tables [B, max_blocks]")
     if out is None:
-        out = torch.empty(B, dtype=torch.int32, device=context_lens.device)
+        out = _made(context_lens, stream, lambda: torch.empty(B, dtype=torch.int32, device=context_lens.device))
     _call_on(context_lens, lib, lib.kv_slot_mapping,
              _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), B,
              block_size, num_blocks, _ptr(out), _stream(out, stream))
@@ -568,11 +568,11 @@ def paged_decode_attention(q, k_cache, v_cache, block_tables, context_lens, scal
     _need(block_tables.shape[0] == B and context_lens.shape[0] == B, "one table row and length per sequence")
     out_dtype = out_dtype or q.dtype
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
+        out = _made(q, stream, lambda: torch.empty((B, Hq, D), dtype=out_dtype, device=q.device))
     _need(out.dtype == out_dtype and tuple(out.shape) == (B, Hq, D) and out.is_contiguous(), "out")
     o = _options(**opts)
     if workspace is None:
-        workspace = make_workspace(B, Hq, Hkv, D, q.device, **opts)
+        workspace = _made(q, stream, lambda: make_workspace(B, Hq, Hkv, D, q.device, **opts))
     if fp8:
         _call_on(q, lib, lib.paged_decode_attention_fp8,
             _ptr(q), DTYPE_CODE[q.dtype], _ptr(k_cache), _ptr(v_cache), float(k_scale), float(v_scale),
@@ -619,11 +619,11 @@ def paged_decode_append_attention(q, k_new, v_new, k_cache, v_cache, block_table
           "slot_mapping int32 [B]")
     out_dtype = out_dtype or q.dtype
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
+        out = _made(q, stream, lambda: torch.empty((B, Hq, D), dtype=out_dtype, device=q.device))
     _need(out.dtype == out_dtype and tuple(out.shape) == (B, Hq, D) and out.is_contiguous(), "out")
     o = _options(**opts)
     if workspace is None:
-        workspace = make_workspace(B, Hq, Hkv, D, q.device, **opts)
+        workspace = _made(q, stream, lambda: make_workspace(B, Hq, Hkv, D, q.device, **opts))
     if fp8:
         _call_on(q, lib, lib.paged_decode_append_attention_fp8,
             _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(seq_ids), DTYPE_CODE[q.dtype], _ptr(k_cache),
@@ -653,7 +653,8 @@ def slot_mapping_varlen(block_tables: torch.Tensor, query_start: torch.Tensor, c
     if num_tokens is None:
         num_tokens = int(query_start[-1].item())
     if out is None:
-        out = torch.empty(max(num_tokens, 1), dtype=torch.int32, device=context_lens.device)[:num_tokens]
+        out = _made(context_lens, stream, lambda: torch.empty(max(num_tokens, 1), dtype=torch.int32,
+                                                              device=context_lens.device))[:num_tokens]
     _call_on(context_lens, lib, lib.kv_slot_mapping_varlen,
              _ptr(block_tables), block_tables.shape[1], _ptr(query_start),
              _ptr(context_lens), B, num_tokens, block_size, num_blocks, _ptr(out),
@@ -684,11 +685,11 @@ def paged_prefill_attention(q, k_cache, v_cache, block_tables, query_start, cont
     _need(block_tables.shape[0] == B and query_start.shape[0] == B + 1, "table rows / query_start")
     out_dtype = out_dtype or q.dtype
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=out_dtype, device=q.device)
+        out = _made(q, stream, lambda: torch.empty((T, Hq, D), dtype=out_dtype, device=q.device))
     _need(out.dtype == out_dtype and tuple(out.shape) == (T, Hq, D) and out.is_contiguous(), "out")
     if workspace is None:
-        workspace = torch.empty(max(16, int(lib.paged_prefill_workspace_bytes(B))), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _made(q, stream, lambda: torch.empty(max(16, int(lib.paged_prefill_workspace_bytes(B))),
+                                                         dtype=torch.uint8, device=q.device))
     if fp8:
         _call_on(q, lib, lib.paged_prefill_attention_fp8,
                  _ptr(q), DTYPE_CODE[q.dtype], _ptr(k_cache), _ptr(v_cache), float(k_scale), float(v_scale), NB,

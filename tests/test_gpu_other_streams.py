@@ -185,3 +185,93 @@ def test_shared_prefix_out_filled_before_the_other_stream_waits():
     b.run(workspace=ws, out=out, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     b.check(out)
+
+
+class Cache:
+    """One layer's cache with sequences of these lengths in blocks of any order."""
+
+    def __init__(self, ctx, Hq=8, Hkv=2, D=128, bs=16, dtype=torch.bfloat16, seed=0):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.Hq, self.Hkv, self.D, self.bs, self.dt = Hq, Hkv, D, bs, dtype
+        n = [-(-c // bs) for c in ctx]
+        self.NB = sum(n) + 3
+        perm = torch.randperm(self.NB, generator=g, device="cuda", dtype=torch.int32).cpu()
+        self.tables = torch.full((len(ctx), max(n)), -1, dtype=torch.int32)
+        at = 0
+        for s, m in enumerate(n):
+            self.tables[s, :m] = perm[at:at + m]
+            at += m
+        self.tables = self.tables.cuda()
+        self.ctx = torch.tensor(ctx, dtype=torch.int32, device="cuda")
+        self.kc, self.vc = (torch.randn((self.NB, Hkv, bs, D), generator=g, device="cuda").to(dtype) for _ in range(2))
+        self.new = lambda *shape: torch.randn(shape, generator=g, device="cuda").to(dtype)  # noqa: E731
+
+
+def _early_and_busy(busy, sizes, side):
+    """Freed memory that the current stream has yet to write, and both streams busy."""
+    torch.cuda.synchronize()
+    busy()
+    early = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+    del early
+    with torch.cuda.stream(side):
+        busy()
+
+
+@pytest.mark.parametrize("append", [False, True])
+def test_decode_attention_with_tensors_of_its_own(busy, append):
+    """The counters of the merge are zeroed before the kernel counts on them."""
+    c = Cache([4000, 900, 17, 2500])
+    q, k, v = c.new(4, c.Hq, c.D), c.new(4, c.Hkv, c.D), c.new(4, c.Hkv, c.D)
+    scale = c.D ** -0.5
+
+    def call(**kw):
+        if append:
+            return pkv.paged_decode_append_attention(q, k, v, c.kc, c.vc, c.tables, c.ctx, scale, **kw)
+        return pkv.paged_decode_attention(q, c.kc, c.vc, c.tables, c.ctx, scale, **kw)
+
+    want = call()
+    n = pkv.workspace_bytes(4, c.Hq, c.Hkv, c.D)
+    side = torch.cuda.Stream()
+    _early_and_busy(busy, (n, q.nbytes), side)
+    got = call(stream=side)
+    late = [torch.full((n,), 0x55, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert pkv.device_status() == (0, 0)
+    assert torch.equal(got, want)
+    assert all(bool((x == 0x55).all()) for x in late)
+
+
+def test_prefill_attention_and_slots_with_tensors_of_their_own(busy):
+    c = Cache([300, 129, 700])
+    starts = torch.tensor([0, 100, 129, 329], dtype=torch.int32, device="cuda")
+    q = c.new(329, c.Hq, c.D)
+
+    def call(**kw):
+        return (pkv.slot_mapping(c.tables, c.ctx, c.bs, c.NB, **kw),
+                pkv.slot_mapping_varlen(c.tables, starts, c.ctx, c.bs, c.NB, num_tokens=329, **kw),
+                pkv.paged_prefill_attention(q, c.kc, c.vc, c.tables, starts, c.ctx, c.D ** -0.5, **kw))
+
+    want = call()
+    side = torch.cuda.Stream()
+    _early_and_busy(busy, (16, 329 * 4, 65536, q.nbytes), side)
+    got = call(stream=side)
+    late = [torch.full((n,), 0x55, dtype=torch.uint8, device="cuda") for n in (512, 2048, 65536) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert pkv.device_status() == (0, 0)
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+    assert all(bool((x == 0x55).all()) for x in late)
+
+
+def test_swap_of_listed_blocks_that_are_copied(busy):
+    pool = pkv.KVPool(2, 12, 16, 2, 64, torch.float16)
+    pool.buffer.copy_(torch.randint(0, 256, pool.buffer.shape, dtype=torch.uint8, device="cuda"))
+    ids = torch.tensor([[3, 0], [11, 1], [5, 2]], dtype=torch.int32, device="cuda")[:, 0]
+    want = pool.swap_out(ids)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy()
+    got = pool.swap_out(ids, stream=side)
+    side.synchronize()
+    n = pool.swap_bytes(3)
+    assert torch.equal(got[:n], want[:n])
+    torch.cuda.synchronize()
