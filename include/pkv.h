@@ -209,7 +209,8 @@ void kv_rope_destroy(kv_rope_t* rope);
  *                 itself with the same stride, but overlap q, k or v in no
  *                 other way.  q NULL: no query rows
  *   positions     device int32 [num_axes][positions_stride], any sign; the
- *                 first n_tokens of each row are read
+ *                 first n_tokens of each row are read.  positions_stride 0:
+ *                 one row for all axes
  *   slot_mapping  device int32[n_tokens]; a negative slot writes no K and V
  *                 (the query rows are rotated all the same), a slot >=
  *                 num_blocks*block_size neither, and sets KV_FLAG_BAD_SLOT

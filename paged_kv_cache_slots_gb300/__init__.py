@@ -370,9 +370,10 @@ class KVPool:
         rows q ([n, Hq, D]) rotated into q_out (a new tensor unless given; may be q itself).
 
         k, v and q may be slices of a packed projection (any stride between tokens, heads
-        contiguous).  positions: int32 [n], or [axes, n] for a rope with several axes.  A negative
-        slot writes no K and V; a token with a negative seq_id writes nothing, q_out neither
-        (a new q_out holds zeros there).  Returns q_out, or None without q.
+        contiguous).  positions: int32 [n], or [axes, n] for a rope with several axes (text tokens:
+        one row expanded to all axes).  A negative slot writes no K and V; a token with a negative
+        seq_id writes nothing, q_out neither (a new q_out holds zeros there).  Returns q_out, or None
+        without q.
 
         Everything runs on `stream` (torch's current one unless given), a new q_out's zeros and the
         copy of positions that are not contiguous too: order the inputs before it, and what reads

@@ -589,8 +589,8 @@ kv_status_t kv_append_rope(kv_pool_t* p, int layer, const kv_rope_t* rope, const
         return fail(KV_ERR_UNSUPPORTED, "kv_append_rope: more than 2^31 elements a token");
     if (n_tokens > 1 && (k_stride < krow || v_stride < krow || (q && (q_stride < qrow || q_out_stride < qrow))))
         return fail(KV_ERR_INVALID_ARG, "kv_append_rope: a stride is shorter than a token's rows");
-    if (rope->num_axes > 1 && positions_stride < n_tokens)
-        return fail(KV_ERR_INVALID_ARG, "kv_append_rope: positions_stride %lld < %d tokens",
+    if (rope->num_axes > 1 && positions_stride != 0 && positions_stride < n_tokens)
+        return fail(KV_ERR_INVALID_ARG, "kv_append_rope: positions_stride %lld (0, or from %d tokens on)",
                     static_cast<long long>(positions_stride), n_tokens);
     if (!aligned(k, eb) || !aligned(v, eb) || (q && (!aligned(q, eb) || !aligned(q_out, eb))) ||
         !aligned(slot_mapping, 4) || !aligned(positions, 4) || !aligned(seq_ids, 4))
