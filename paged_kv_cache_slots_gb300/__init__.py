@@ -730,7 +730,8 @@ def paged_shared_prefix_attention(q, k_cache, v_cache, block_tables, context_len
     Sequences group_start[g] .. group_start[g + 1] - 1 (int32 [groups + 1]) hold the same blocks in their
     first prefix_lens[g] / block_size table entries (int32 [groups]); a sequence shorter than that, or in
     no group, is read through its own table throughout.  The other arguments are those of
-    paged_decode_attention; q f16 or bf16, block_size a multiple of 16.
+    paged_decode_attention; q f16 or bf16, block_size a multiple of 16.  Everything runs on `stream`
+    (torch's current one unless given): order the inputs before it, and what reads out behind it.
     """
     lib = _lib or load_library()
     B, Hq, D = q.shape
@@ -739,6 +740,11 @@ def paged_shared_prefix_attention(q, k_cache, v_cache, block_tables, context_len
     i32, index = torch.int32, q.get_device()
     groups = prefix_lens.shape[0] if prefix_lens.dim() == 1 else -1
     out_dtype = out_dtype or q.dtype
+    # (The library cannot tell a host address from a device one.)
+    _need(0 <= index == k_cache.get_device() == v_cache.get_device() == block_tables.get_device()
+          == context_lens.get_device() == group_start.get_device() == prefix_lens.get_device()
+          and (out is None or out.get_device() == index) and (workspace is None or workspace.get_device() == index),
+          "every tensor must be on q's GPU")
     if out is None:
         out = _made(q, stream, lambda: torch.empty((B, Hq, D), dtype=out_dtype, device=q.device))
     if workspace is None:
@@ -755,9 +761,7 @@ def paged_shared_prefix_attention(q, k_cache, v_cache, block_tables, context_len
           "one table row and length per sequence")
     _need(groups >= 0 and group_start.shape == (groups + 1,), "group_start [groups + 1], prefix_lens [groups]")
     _need(out.dtype == out_dtype and out.shape == q.shape and out.is_contiguous(), "out")
-    _need(k_cache.get_device() == v_cache.get_device() == out.get_device() == workspace.get_device()
-          == block_tables.get_device() == context_lens.get_device() == group_start.get_device()
-          == prefix_lens.get_device() == index, "every tensor must be on q's device")
+    _need(workspace.is_contiguous(), "a contiguous workspace")
     sizes = (NB, block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, group_start.data_ptr(),
              prefix_lens.data_ptr(), groups, Hq, Hkv, D, bs)
     rest = (float(scale), out.data_ptr(), DTYPE_CODE[out_dtype], workspace.data_ptr(),
