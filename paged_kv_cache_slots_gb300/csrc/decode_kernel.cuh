@@ -36,8 +36,6 @@
 // the end of a segment (no merge when R == 1).
 #pragma once
 
-#include <atomic>
-
 #include "device_utils.cuh"
 #include "prefix_units.cuh"
 
@@ -701,21 +699,14 @@ __device__ __forceinline__ void decode_tails(const Args& a, const CUtensorMap& t
 #include "decode_body.cuh"
 }
 
-// Launch the partial kernel of `Policy`.  The dynamic shared-memory limit is
-// raised once per device (not on every launch, so that launches captured in
-// a CUDA graph make no attribute calls).
+// Launch the partial kernel of `Policy`.
 template <class Policy>
 cudaError_t launch_partial(const DecodeArgs& a, const CUtensorMap& tmk, const CUtensorMap& tmv,
                            cudaStream_t stream) {
-    static std::atomic<int> configured[64];
+    static RaisedLimit limit;
     auto kern = paged_decode_partial_kernel<Policy>;
-    const bool cacheable = a.device >= 0 && a.device < 64;
-    if (!cacheable || configured[a.device].load() < a.smem_bytes) {
-        cudaError_t e =
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, a.smem_bytes);
-        if (e != cudaSuccess) return e;
-        if (cacheable) configured[a.device].store(a.smem_bytes);
-    }
+    const cudaError_t e = allow_shared_memory(kern, a.device, a.smem_bytes, &limit);
+    if (e != cudaSuccess) return e;
     if (32 * (1 + a.consumer_warps) > Policy::kMaxThreads) return cudaErrorInvalidValue;
     return launch_kernel(kern, dim3(a.num_ctas), dim3(32 * (1 + a.consumer_warps)),
                          static_cast<size_t>(a.smem_bytes), stream, a.pdl != 0, a, tmk, tmv);

@@ -12,6 +12,7 @@
 #include <utility>
 
 #include "pkv_internal.h"
+#include "raised_limit.h"
 
 namespace pkv {
 
@@ -288,8 +289,19 @@ __device__ __forceinline__ void store_out(void* out, int64_t idx, float v, int o
 // Kernels that follow one another without a pause divide an SM's memory alike
 // (all of it shared): an SM divides anew only when it is empty.
 template <class Kernel>
-cudaError_t prefer_shared_memory(Kernel kernel) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+cudaError_t prefer_shared_memory(Kernel kernel, int device, RaisedLimit* carveout) {
+    return carveout->at_least(device, cudaSharedmemCarveoutMaxShared, [&](int percent) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, percent);
+    });
+}
+
+// Lets launches of `kernel` on `device` ask for `bytes` of dynamic shared
+// memory; `limit` is the kernel's own.
+template <class Kernel>
+cudaError_t allow_shared_memory(Kernel kernel, int device, int bytes, RaisedLimit* limit) {
+    return limit->at_least(device, bytes, [&](int b) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, b);
+    });
 }
 
 // Launch `kernel` on `stream`, optionally as a programmatic dependent of the

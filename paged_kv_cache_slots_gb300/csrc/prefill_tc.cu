@@ -424,14 +424,10 @@ __global__ void __launch_bounds__(192, 2) paged_prefill_tc_kernel(const PrefillA
 
 template <int DT, int G, int kBS>
 cudaError_t launch_tc_l(const PrefillArgs& a, const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t stream) {
-    static std::atomic<int> configured[64];
+    static RaisedLimit limit;
     auto kern = paged_prefill_tc_kernel<DT, G, kBS>;
-    const bool cacheable = a.device >= 0 && a.device < 64;
-    if (!cacheable || configured[a.device].load() < a.smem_bytes) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, a.smem_bytes);
-        if (e != cudaSuccess) return e;
-        if (cacheable) configured[a.device].store(a.smem_bytes);
-    }
+    const cudaError_t e = allow_shared_memory(kern, a.device, a.smem_bytes, &limit);
+    if (e != cudaSuccess) return e;
     return launch_kernel(kern, dim3(a.grid_tiles, a.num_kv_heads), dim3(192), static_cast<size_t>(a.smem_bytes),
                          stream, a.pdl != 0, a, tmk, tmv);
 }

@@ -1,7 +1,5 @@
 // The merge of the shared-prefix attention's parts and the choice of its
 // kernels (see shared_prefix_kernel.cuh).
-#include <atomic>
-
 #include "prefix_units.cuh"
 #include "shared_prefix.cuh"
 
@@ -124,14 +122,10 @@ __global__ void __launch_bounds__(256, 4) shared_prefix_merge_kernel(const Share
 
 template <int D>
 cudaError_t launch_merge_t(const SharedPrefixArgs& a, const TailArgs& tails, cudaStream_t stream) {
-    static std::atomic<int> configured[64];
+    static RaisedLimit carveout;
     auto kern = shared_prefix_merge_kernel<D>;
-    const bool cacheable = tails.device >= 0 && tails.device < 64;
-    if (!cacheable || !configured[tails.device].load()) {
-        const cudaError_t e = prefer_shared_memory(kern);
-        if (e != cudaSuccess) return e;
-        if (cacheable) configured[tails.device].store(1);
-    }
+    const cudaError_t e = prefer_shared_memory(kern, tails.device, &carveout);
+    if (e != cudaSuccess) return e;
     const int64_t warps = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
     return launch_kernel(kern, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, stream, true, a, tails);
 }

@@ -654,15 +654,11 @@ __global__ void __launch_bounds__(parts_threads(kFP8), 1)
 template <class Policy, int QT, int D, bool kFP8>
 cudaError_t launch_attend_t(const SharedPrefixArgs& a, const TailArgs& d, const CUtensorMap& tmk,
                             const CUtensorMap& tmv, cudaStream_t stream) {
-    static std::atomic<int> configured[64];
+    static RaisedLimit limit, carveout;
     auto kern = shared_prefix_attend_kernel<Policy, QT, D, kFP8>;
-    const bool cacheable = d.device >= 0 && d.device < 64;
-    if (!cacheable || configured[d.device].load() < d.smem_bytes) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem_bytes);
-        if (e == cudaSuccess) e = prefer_shared_memory(kern);
-        if (e != cudaSuccess) return e;
-        if (cacheable) configured[d.device].store(d.smem_bytes);
-    }
+    cudaError_t e = allow_shared_memory(kern, d.device, d.smem_bytes, &limit);
+    if (e == cudaSuccess) e = prefer_shared_memory(kern, d.device, &carveout);
+    if (e != cudaSuccess) return e;
     return launch_kernel(kern, dim3(d.num_ctas), dim3(parts_threads(kFP8)), static_cast<size_t>(d.smem_bytes), stream, true,
                          a, d, tmk, tmv);
 }
