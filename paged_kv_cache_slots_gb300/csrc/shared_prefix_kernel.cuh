@@ -32,10 +32,12 @@
 // (Measured on 256 sequences, 32 query and 8 KV heads, 32,768 shared tokens:
 // 356 us with one issuing lane, 290 with one warp walking the issue loop
 // converged, so that descriptors stay in uniform registers, 214 with two.)
-// P enters the product as a high and a low half-precision part, so that the
-// result carries fp32-like weights whatever the output type: 1.5 times the
+// P enters the product as a high and a low half-precision part, 1.5 times the
 // matrix work of one part, whose rounding (2^-9 of each weight in bf16) would
-// be as large as that of a bf16 output.
+// be as large as that of a bf16 output.  Two bf16 parts hold a weight to 2^-17
+// of it.  Two f16 parts hold it to 2^-22, but nothing below half of f16's
+// smallest step: the reference lies weight_shift below the score that it stands
+// for, so that what a weight loses there is at most 2^-32 of the largest.
 //
 // Bounds and measurements (128-dim heads, 32 query and 8 KV heads, bf16, both
 // launches):
@@ -64,7 +66,9 @@ constexpr int kNK = kPrefixTile;
 constexpr int kS = 4;                // S / P buffers in tensor memory, 64 columns each
 constexpr uint32_t kO = kS * kNK;    // the two accumulators, D columns each
 constexpr uint32_t kTmemCols = 512;
-constexpr float kLazy = 8.f;
+constexpr float kLazy = 8.f;  // a row's scores may pass its reference by this much (log2) before the sums are rescaled
+// log2 of a weight at the reference: the f16 parts' range is used up to 2^(kLazy + 7) = 2^15.
+__host__ __device__ constexpr float weight_shift(int dt) { return dt == static_cast<int>(kF16) ? 7.f : 0.f; }
 constexpr int kSoftmaxWarps = 8;
 // E4M3: codes on their way to be widened, tiles a producer warp.
 constexpr int kRawRing = 5;
@@ -426,6 +430,7 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
         // every finite score's exponent at 0 while masked scores stay -inf.
         constexpr float kLeast = 1e-30f;
         const float sc0 = fmaxf(fabsf(a.scale_log2), kLeast);
+        constexpr float kUp = weight_shift(DT);
         int i = 0, seg = 0;
         bool ok = true;  // (a failed wait skips the work, not the barriers)
         for (int x = start; x < end; ++seg) {
@@ -535,13 +540,13 @@ __device__ __forceinline__ void parts_cta(const SharedPrefixArgs& a, uint8_t* ba
                     for (int c = 0; c < 8; ++c) mx[c] = max3(mx[c], sv[k + c], sv[k + 8 + c]);
                 // (The lower limit keeps the exponents of a row whose scores
                 // are all -inf so far at -inf, not NaN.)
-                const float mt = fmaxf(max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sc,
-                                       -1e30f);
+                const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+                const float mt = fmaxf(top * sc, -1e30f) - kUp;
                 bool need = false;
                 if (j < 2)
                     m_ref = mt;
-                else
-                    need = mt > m_ref + kLazy;
+                else  // the largest exponent, as the weights' below: no weight passes 2^(kLazy + kUp)
+                    need = fmaf(top, sc, -m_ref) > kLazy + kUp;
                 if (__any_sync(0xffffffffu, need)) {
                     // O must be complete up to the group's tile before it is rescaled.
                     ok = __all_sync(0xffffffffu, wait(&B->pv_done[(k0 - 2) % kS], (k0 - 2) / kS, abort, a.status));
