@@ -194,11 +194,12 @@ kv_status_t kv_rope_create(const kv_rope_config_t* cfg, kv_rope_t** rope_out);
 void kv_rope_destroy(kv_rope_t* rope);
 
 /* kv_append (kv_append_fp8 for an E4M3 pool) with the K rows rotated on the
- * way, and the step's query rows rotated into q_out, in one kernel.  Angles
- * are good to 2^-32 of a turn at any position (|inv_freq| up to 2^20); the
- * rotation is computed in fp32 and rounded once, to the pool's type, or to the E4M3 code nearest to
- * the fp32 quotient by k_scale.  V rows are stored as kv_append (kv_append_fp8)
- * stores them.
+ * way, and the step's query rows rotated into q_out, in one kernel.  An angle
+ * is worked out to 2^-32 of a turn at any position (|inv_freq| up to 2^20) and
+ * rounded to the fp32 argument of its cosine and sine, at most 2^-28 of a turn
+ * away; the rotation is computed in fp32 and rounded once, to the pool's type,
+ * or to the E4M3 code nearest to the fp32 quotient by k_scale.  V rows are
+ * stored as kv_append (kv_append_fp8) stores them.
  *   k, v          device, n_tokens rows [num_kv_heads][head_dim] in src_dtype
  *                 (the pool's type; for an E4M3 pool KV_F32, KV_F16 or
  *                 KV_BF16), consecutive tokens k_stride (v_stride) elements
@@ -443,7 +444,10 @@ kv_status_t paged_prefill_attention(const void* q, const void* k_cache, const vo
  * 128, block_size a multiple of 16 up to 256 (two stages of a block's K and V
  * must fit shared memory, as for paged_decode_attention: up to 208 with
  * head_dim 128), num_q_heads / num_kv_heads in {1, 2, 4, 8}; out_dtype KV_F32
- * or dtype.  Softmax statistics and sums are fp32.  workspace: device, 256-byte aligned, of at least
+ * or dtype.  Softmax statistics and sums are fp32; a weight meets V as two
+ * halves of the product's type, which hold it to 2^-17 of it (bf16) or 2^-22 (f16
+ * and E4M3 caches, down to 2^-32 of the row's largest in the prefix, 2^-25 in the
+ * tails).  workspace: device, 256-byte aligned, of at least
  * paged_shared_prefix_workspace_bytes, needs no initialisation, not to be
  * shared by two calls in flight at once (two captured graphs that may run at
  * the same time included).  Worth it from a prefix of a few hundred tokens and
@@ -464,7 +468,10 @@ kv_status_t paged_shared_prefix_attention(const void* q, const void* k_cache, co
 
 /* The same over an E4M3 cache (see paged_decode_attention_fp8): q_dtype KV_F16
  * or KV_BF16, head_dim 128, out_dtype KV_F32 or q_dtype.  The prefix's codes
- * are widened exactly to q's type in shared memory. */
+ * are widened to f16 in shared memory, exactly, whatever q's type.  A bf16 query
+ * row meets them in f16 too, times a power of two that puts its largest element
+ * at 2^13: exact down to 2^-30 of that element, and off by at most 2^-38 of it
+ * below. */
 kv_status_t paged_shared_prefix_attention_fp8(const void* q, kv_dtype_t q_dtype, const void* k_cache,
                                               const void* v_cache, float k_scale, float v_scale,
                                               int num_blocks, const int32_t* block_tables,

@@ -670,6 +670,8 @@ __device__ __forceinline__ bool append_row(const DecodeArgs& a, const Policy& po
 // Policy provides: State, begin(), tile(), write_state(), write_partial(),
 // write_final(), kTensor, kScratch, kPairs (and tile2() when kPairs), and
 // kMaxThreads, the largest block it is launched with (its register budget).
+// kTails and Args are what the included text tests and reads (see decode_tails
+// below); this kernel is built with their defaults.
 template <class Policy, bool kTails = false, class Args = DecodeArgs>
 __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
     paged_decode_partial_kernel(const Args a, const __grid_constant__ CUtensorMap tmk,

@@ -110,9 +110,15 @@ __device__ __forceinline__ Units plan_units(const Args& a, int G) {
 // `tokens` (token, KV head) rows, with phantoms among them (DecodeArgs), of
 // `pairs` (sequence, heads of a stage).
 //
-// Measured costs on one SM: a tile of the parts role kTileNs, the start and end
-// of a triple kTripleNs; the tails kTokenNs for each row, whatever its length
-// (the consumer's arithmetic or the memory's rate), and kSequenceNs for each pair.
+// Measured costs on one SM, of 128-dim heads and 4 query heads a KV head: a tile
+// of the parts role kTileNs (64 dims: their own), the start and end of a triple
+// kTripleNs; the tails kTokenNs for each row, whatever its length (the consumer's
+// arithmetic or the memory's rate), and kSequenceNs for each pair.  The one figure
+// for a tails row is rough for other heads: in a graph, with 0.5 / 0.75 / 1 / 1.5
+// times it, 256 sequences over 32,768 shared tokens take 312 / 188 / 190 / 213 us,
+// 64 in groups of 8 with long tails 266 / 267 / 269 / 311; 32 over 4,096 with tails
+// of 2,048, 4 query heads a KV head and 128 dims 34 / 40 / 38 / 48, with 64 dims 29 /
+// 33 / 39 / 46.
 template <class Args>
 __device__ __forceinline__ void divide_sms(const Args& a, int items, int tokens, int pairs, Units* u) {
     constexpr float kTripleNs = 3000.f, kSequenceNs = 3700.f;

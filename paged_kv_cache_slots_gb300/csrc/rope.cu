@@ -18,7 +18,7 @@
 // fraction of a turn to p * 2^-64: one integer multiplication, with no
 // reduction and no table of positions to read.  The nearest quarter turn is
 // taken off in integers, and sincospif sees at most an eighth of a turn, where
-// the conversion to fp32 costs 2^-25 of the argument.
+// the conversion to fp32 is off by at most 2^-28 of a turn.
 //
 // Work split.  One CTA of 128 threads a token (several, by rows, when there
 // are too few tokens to fill the GPU).  The first n threads make the token's
@@ -31,9 +31,14 @@
 // Bound: HBM.  Every row is read and written once: 16,384 tokens of 32 query
 // and 8 KV heads of 128 bf16 elements move 403 MB in 68 us, 5.9 TB/s (88 % of
 // the measured copy rate; 112 us when the slot and the padding flag were waited
-// for before the rows were asked for, 74 without a bound on the registers).
-// Small calls are bound by their launch and two rounds of loads (2.3 us for one
-// token).
+// for before the rows were asked for).  Small calls are bound by their launch and
+// two rounds of loads (2.3 us for one token).
+//
+// Registers are bounded for seven CTAs an SM (72 each) in every variant.  In a
+// graph, with 6 / 7 / 8 CTAs: the chunk above 72.1 / 67.7 / 71.4 us, 1,023 tokens
+// into E4M3 6.6 / 5.1 / 5.5, 4,099 tokens of 16 and 2 heads on three axes 13.9 /
+// 13.7 / 13.3, f32 heads of 80 10.2 / 9.6 / 9.4.  Seven costs the variants of eight
+// 16-bit elements and three rows 24 bytes of spills.
 #include "device_utils.cuh"
 
 namespace pkv {

@@ -40,12 +40,16 @@
 // for, so that what a weight loses there is at most 2^-32 of the largest.
 //
 // Bounds and measurements (128-dim heads, 32 query and 8 KV heads, bf16, both
-// launches):
+// launches, calls in a graph; after 256 MB of other reads in brackets, which is
+// how a layer finds a cache that the layers before it have put out of L2):
 // - up to 128 query rows a KV head: the memory, and below some 10 us the start
 //   of the roles, one after another latency, and the merge (32 sequences,
-//   4,096 shared tokens: 22 us; 65,536 shared: 65 us, 4.1 TB/s of K and V);
+//   4,096 shared tokens: 22 us [36]; 65,536 shared: 66 us [70], 4.1 TB/s of K
+//   and V);
 // - more: the tensor pipe, 50 % active by its counter (256 sequences, 32,768
-//   shared: 191 us, 725 TFLOP/s, or 1,090 of matrix work).
+//   shared: 188 us [191], 740 TFLOP/s, or 1,110 of matrix work).
+// Registers: 168 a thread over 16-bit caches, with 68 bytes of spill stores (32
+// with 64 dims); 128 a thread over E4M3, with 344 to 364.
 // Tried and left: 2 KB tensor copies for K and V (61 ns each on one SM, slower
 // than 16-byte copies by 10 % where matrix work bounds), one softmax group a CTA
 // with two CTAs an SM (219 us on the wide case, and no room for tails beside
@@ -167,8 +171,8 @@ __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
 
 // QT: q's type.  The tensor cores work in it, or in f16 over an E4M3 cache
 // (whose values all are f16); a bf16 q is then brought to f16 with a power of
-// two for each row that puts its largest element at 2^13: exact down to 2^-27
-// of that element.
+// two for each row that puts its largest element at 2^13: exact down to 2^-30
+// of that element (f16's steps of 2^-24 hold a bf16's eight bits from 2^-17 on).
 
 // One thread, before the roles are known.
 template <int D, bool kFP8>
