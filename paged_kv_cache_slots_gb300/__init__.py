@@ -205,7 +205,7 @@ def _call_on(t: torch.Tensor, lib, fn, *args):
     the SM count, the status word and the static scratch of the current
     device, and the stream passed is t's."""
     index = t.get_device()
-    # A host tensor (index -1): the library rejects host pointers where it needs device memory.
+    # (A host tensor has index -1.  The library does not see what an address is: tensors are the caller's to check.)
     if index < 0 or index == torch.cuda.current_device():
         status = fn(*args)
         if status:
