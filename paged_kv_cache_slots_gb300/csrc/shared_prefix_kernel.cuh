@@ -42,8 +42,8 @@
 // The sums in tensor memory are fp32, but each step of them drops what lies past
 // the last place, so that a long sum of one sign comes out low: with V = 1 and 256
 // sequences of 32 query and 8 KV heads, 1.3e-6 over 4,096 shared tokens (bf16),
-// 9.6e-6 over 32,768 and 4.1e-5 over 131,072; twice that in f16, 4.1e-4 (a half
-// step of an f16 output is 4.9e-4) over 524,288.  The decode kernel's warp MMAs
+// 9.6e-6 over 32,768 and 4.1e-5 over 131,072; up to twice that in f16, 4.1e-4 (half
+// a step of an f16 output is 4.9e-4) over 524,288.  The decode kernel's warp MMAs
 // do the same (f16, 524,288 tokens: 4.3e-4).
 //
 // Bounds and measurements (128-dim heads, 32 query and 8 KV heads, bf16, both
