@@ -89,6 +89,7 @@ typedef enum {
 #define KV_FLAG_BAD_CONTEXT    0x4u /* context_lens[s] < 0 or > max_blocks_per_seq*block_size */
 #define KV_FLAG_TIMEOUT        0x8u /* a kernel gave up a bounded wait */
 #define KV_FLAG_BAD_GROUP      0x20u /* groups that do not cut the sequences into runs in order, or a prefix length < 0 */
+#define KV_FLAG_BAD_QUEUE      0x40u /* a free queue's state or an id in it is out of range, or more blocks come back than there are */
 #define KV_FLAG_BAD_PLAN       0x10u /* a launch plan the kernel refuses (never set by this library's own planning) */
 
 /* Human-readable name of a status code (static string). */
@@ -228,6 +229,86 @@ kv_status_t kv_append_rope(kv_pool_t* pool, int layer, const kv_rope_t* rope, co
                            const int32_t* positions, int64_t positions_stride, const void* q,
                            int64_t q_stride, void* q_out, int64_t q_out_stride, int num_q_heads,
                            float k_scale, float v_scale, void* stream);
+
+/* kv_append_rope with each head's query and key rows normalised before they are
+ * rotated, in the same pass: a row x of head_dim elements becomes
+ *   z = x / sqrt(mean(x^2) + eps) * weight,
+ * the mean over the whole row, and z is rotated as kv_append_rope rotates x
+ * (elements from rot_dim on are z's).  Sum, norm and rotation are fp32 and the
+ * result is rounded once; a row's sum of squares must be finite in fp32.  V rows
+ * are stored as kv_append_rope stores them.
+ *   q_weight, k_weight  device, in weight_dtype (src_dtype or KV_F32):
+ *                       [head_dim] for all heads (a stride of 0), or a row for
+ *                       each head, q_weight_stride (k_weight_stride) elements
+ *                       apart; NULL: all 1.  q_out overlaps neither
+ *   eps                 finite, >= 0
+ * The other arguments are those of kv_append_rope.  Weights that are 16-byte
+ * aligned are the fast ones. */
+kv_status_t kv_append_norm_rope(kv_pool_t* pool, int layer, const kv_rope_t* rope,
+                                const int32_t* seq_ids, int n_tokens, const void* k, int64_t k_stride,
+                                const void* v, int64_t v_stride, kv_dtype_t src_dtype,
+                                const int32_t* slot_mapping, const int32_t* positions,
+                                int64_t positions_stride, const void* q, int64_t q_stride, void* q_out,
+                                int64_t q_out_stride, int num_q_heads, const void* q_weight,
+                                int64_t q_weight_stride, const void* k_weight, int64_t k_weight_stride,
+                                kv_dtype_t weight_dtype, float eps, float k_scale, float v_scale,
+                                void* stream);
+
+/* ----------------------------------------- tables built on the device */
+
+/* The block allocator's bookkeeping on the device, for engines that keep the
+ * tables there (and for steps captured in a CUDA graph): the semantics of
+ * kv_allocator_extend for all sequences of a step, in order ("vLLM Architecture
+ * and Installation", Example 3).
+ *   free_queue   int32[num_blocks]: a ring of block ids; its queue_state[1]
+ *                blocks are free, the first of them at index queue_state[0], the
+ *                next behind it modulo num_blocks
+ *   new_lens     int32[num_seqs]: tokens that sequence s brings, on top of
+ *                cached_lens[s]
+ * Sequence s is granted its tokens when (a) it needs no new block, or the blocks
+ * needed by all sequences up to s are free, and (b) the new tokens of all sequences
+ * up to s are at most num_tokens.  So blocks go out in the sequences' order, and
+ * behind the first sequence that is refused only those are granted that need none.
+ * A refused sequence stays as it is: a caller sees it by its empty run in
+ * query_start.  Lengths < 0, or past the table's max_blocks_per_seq * block_size,
+ * are refused, count for nothing, and set KV_FLAG_BAD_CONTEXT.
+ * Written (all device memory):
+ *   block_tables     the entries of the new blocks; the others stay as they are
+ *   context_lens     int32[num_seqs]: cached_lens and the granted tokens
+ *   query_start      int32[num_seqs + 1]: where each sequence's tokens start
+ *   slot_mapping, positions, seq_ids  int32[num_tokens]: of each new token, in the
+ *                    sequences' order, its slot, position and sequence; behind the
+ *                    last one -1, 0 and -1 (padding to kv_append_rope).  A token in a
+ *                    cached block whose entry is no block gets slot -1
+ *                    (KV_FLAG_BAD_BLOCK_ID), one from a queue entry that is none
+ *                    likewise (KV_FLAG_BAD_QUEUE)
+ *   queue_state_out  int32[2]: the queue's new front and number of free blocks
+ * context_lens may be cached_lens itself and queue_state_out queue_state itself (a
+ * step in place); nothing else may overlap.  A queue_state out of range counts as an
+ * empty queue and sets KV_FLAG_BAD_QUEUE.  At most 8192 sequences. */
+kv_status_t kv_tables_extend(int32_t* block_tables, int max_blocks_per_seq, const int32_t* cached_lens,
+                             const int32_t* new_lens, int num_seqs, int block_size, int num_blocks,
+                             const int32_t* free_queue, const int32_t* queue_state, int num_tokens,
+                             int32_t* context_lens, int32_t* query_start, int32_t* slot_mapping,
+                             int32_t* positions, int32_t* seq_ids, int32_t* queue_state_out,
+                             void* stream);
+
+/* Blocks back to the end of the queue, in the order of the sequences and of each
+ * one's table; their entries become -1.
+ *   finished  int32[num_seqs], or NULL: a sequence with a non-zero entry gives
+ *             back all its blocks and its length becomes 0
+ *   window, sinks  window > 0: the other sequences give back the blocks that no
+ *             later query sees, those wholly behind the first `sinks` tokens and
+ *             before position context_lens[s] - window + 1 (with layers of several
+ *             windows: the largest)
+ * Entries that are negative are passed over, so what was given back once is not
+ * given back again.  Blocks that several sequences share must not be given back
+ * here.  If more blocks would stand in the queue than there are, nothing changes
+ * and KV_FLAG_BAD_QUEUE is set.  No two buffers may overlap. */
+kv_status_t kv_tables_release(int32_t* block_tables, int max_blocks_per_seq, int32_t* context_lens,
+                              int num_seqs, int block_size, int num_blocks, const int32_t* finished,
+                              int window, int sinks, int32_t* free_queue, int32_t* queue_state,
+                              void* stream);
 
 /* ------------------------------------------------------- decode attention */
 
@@ -418,6 +499,74 @@ kv_status_t paged_prefill_attention(const void* q, const void* k_cache, const vo
                                     int block_size, kv_dtype_t dtype, float scale, void* out,
                                     kv_dtype_t out_dtype, void* workspace, size_t workspace_bytes,
                                     void* stream);
+
+/* --------------------------------------------------------- sliding window */
+
+/* paged_decode_attention for a layer with a sliding window and a few first
+ * tokens that stay visible.  The query of sequence s stands at position
+ * p = context_lens[s] - 1 and sees the cached positions j <= p with
+ *   j > p - window   (the last `window` tokens, itself among them), or
+ *   j < sinks        (the first `sinks` tokens).
+ * What it does not see takes no part, whatever K and V hold there (infinities
+ * and NaN too).  Of a table row only the entries of blocks with a token in sight
+ * are read: blocks in between may have been given to other sequences and their
+ * entries be anything (-1, say; see kv_tables_release).
+ *   window  >= 1; one of at least the context sees all of it
+ *   sinks   >= 0; 0: the window alone
+ * max_blocks_per_seq * block_size must be below 2^31.  The other arguments, the
+ * workspace and the options are those of paged_decode_attention (of
+ * paged_decode_attention_fp8 for an E4M3 cache), and so is the result when the
+ * window reaches back to the first token. */
+kv_status_t paged_window_decode_attention(const void* q, const void* k_cache, const void* v_cache,
+                                          int num_blocks, const int32_t* block_tables,
+                                          int max_blocks_per_seq, const int32_t* context_lens,
+                                          int num_seqs, int num_q_heads, int num_kv_heads,
+                                          int head_dim, int block_size, kv_dtype_t dtype,
+                                          float scale, int window, int sinks, void* out,
+                                          kv_dtype_t out_dtype, void* workspace,
+                                          size_t workspace_bytes, const kv_decode_options_t* opts,
+                                          void* stream);
+kv_status_t paged_window_decode_attention_fp8(const void* q, kv_dtype_t q_dtype, const void* k_cache,
+                                              const void* v_cache, float k_scale, float v_scale,
+                                              int num_blocks, const int32_t* block_tables,
+                                              int max_blocks_per_seq, const int32_t* context_lens,
+                                              int num_seqs, int num_q_heads, int num_kv_heads,
+                                              int head_dim, int block_size, float scale, int window,
+                                              int sinks, void* out, kv_dtype_t out_dtype,
+                                              void* workspace, size_t workspace_bytes,
+                                              const kv_decode_options_t* opts, void* stream);
+
+/* paged_prefill_attention (_fp8) with the same rule for each new token: row
+ * t = query_start[s] + i stands at position p = context_lens[s] - n_s + i and
+ * sees the positions j <= p with j > p - window or j < sinks.  Of a table row
+ * the entries of blocks that none of the sequence's new tokens sees are not
+ * read.  A K or V row that a token does not see takes no part in its row of out,
+ * infinities and NaN included (a later new token's, say).  Rows of q behind the
+ * last sequence are not read, and those rows of out left as they are.
+ * workspace: device, 256-byte aligned, of at least
+ * paged_window_prefill_workspace_bytes, needs no initialisation, not to be
+ * shared by two calls in flight at once.  The other arguments and what is
+ * refused are those of paged_prefill_attention (_fp8). */
+kv_status_t paged_window_prefill_workspace_bytes(int num_seqs, int num_tokens, int num_q_heads,
+                                                 int num_kv_heads, int head_dim, int device,
+                                                 size_t* bytes_out);
+kv_status_t paged_window_prefill_attention(const void* q, const void* k_cache, const void* v_cache,
+                                           int num_blocks, const int32_t* block_tables,
+                                           int max_blocks_per_seq, const int32_t* query_start,
+                                           const int32_t* context_lens, int num_seqs, int num_tokens,
+                                           int num_q_heads, int num_kv_heads, int head_dim,
+                                           int block_size, kv_dtype_t dtype, float scale, int window,
+                                           int sinks, void* out, kv_dtype_t out_dtype,
+                                           void* workspace, size_t workspace_bytes, void* stream);
+kv_status_t paged_window_prefill_attention_fp8(const void* q, kv_dtype_t q_dtype, const void* k_cache,
+                                               const void* v_cache, float k_scale, float v_scale,
+                                               int num_blocks, const int32_t* block_tables,
+                                               int max_blocks_per_seq, const int32_t* query_start,
+                                               const int32_t* context_lens, int num_seqs,
+                                               int num_tokens, int num_q_heads, int num_kv_heads,
+                                               int head_dim, int block_size, float scale, int window,
+                                               int sinks, void* out, kv_dtype_t out_dtype,
+                                               void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------- shared prefixes */
 

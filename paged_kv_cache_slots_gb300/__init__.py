@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -21,6 +22,8 @@ __all__ = [
     "paged_decode_attention", "device_status", "library_path", "load_library", "workspace_init",
     "make_workspace", "paged_decode_append_attention", "paged_prefill_attention", "slot_mapping_varlen",
     "paged_shared_prefix_attention", "shared_prefix_workspace_bytes", "make_shared_prefix_workspace",
+    "paged_window_decode_attention", "paged_window_prefill_attention", "window_prefill_workspace_bytes",
+    "make_window_prefill_workspace", "StepTables", "make_step_tables", "make_free_queue", "extend_tables", "release_tables",
 ]
 
 KV_F32, KV_F16, KV_BF16, KV_FP8_E4M3 = 0, 1, 2, 3
@@ -33,7 +36,7 @@ FP8 = torch.float8_e4m3fn
 _ROW_DTYPES = (torch.float32, torch.float16, torch.bfloat16)
 KERNELS = {"auto": 0, "ffma": 1, "mma": 2}
 FLAG_BAD_BLOCK_ID, FLAG_BAD_SLOT, FLAG_BAD_CONTEXT, FLAG_TIMEOUT = 0x1, 0x2, 0x4, 0x8
-FLAG_BAD_GROUP = 0x20
+FLAG_BAD_GROUP, FLAG_BAD_QUEUE = 0x20, 0x40
 
 _lock = threading.Lock()
 _lib = None
@@ -88,6 +91,10 @@ def _declare(lib):
         "kv_rope_destroy": (None, [P]),
         "kv_append_rope": (I, [P, I, P, P, I, P, I64, P, I64, I, P, P, I64, P, I64, P, I64, I, ctypes.c_float,
                                ctypes.c_float, P]),
+        "kv_append_norm_rope": (I, [P, I, P, P, I, P, I64, P, I64, I, P, P, I64, P, I64, P, I64, I, P, I64, P, I64, I,
+                                    ctypes.c_float, ctypes.c_float, ctypes.c_float, P]),
+        "kv_tables_extend": (I, [P, I, P, P, I, I, I, P, P, I, P, P, P, P, P, P, P]),
+        "kv_tables_release": (I, [P, I, P, I, I, I, P, I, I, P, P, P]),
         "paged_decode_workspace_bytes": (I, [I, I, I, I, I, ctypes.POINTER(_DecodeOptions),
                                              ctypes.POINTER(SZ)]),
         "paged_decode_attention": (I, [P, P, P, I, P, I, P, I, I, I, I, I, I, ctypes.c_float, P,
@@ -127,6 +134,15 @@ def _declare(lib):
                                               SZ, P]),
         "paged_shared_prefix_attention_fp8": (I, [P, I, P, P, ctypes.c_float, ctypes.c_float, I, P, I, P, I, P, P, I,
                                                   I, I, I, I, ctypes.c_float, P, I, P, SZ, P]),
+        "paged_window_decode_attention": (I, [P, P, P, I, P, I, P, I, I, I, I, I, I, ctypes.c_float, I, I, P, I, P, SZ,
+                                              ctypes.POINTER(_DecodeOptions), P]),
+        "paged_window_decode_attention_fp8": (I, [P, I, P, P, ctypes.c_float, ctypes.c_float, I, P, I, P, I, I, I, I, I,
+                                                  ctypes.c_float, I, I, P, I, P, SZ, ctypes.POINTER(_DecodeOptions), P]),
+        "paged_window_prefill_workspace_bytes": (I, [I, I, I, I, I, I, ctypes.POINTER(SZ)]),
+        "paged_window_prefill_attention": (I, [P, P, P, I, P, I, P, P, I, I, I, I, I, I, I, ctypes.c_float, I, I, P, I, P,
+                                               SZ, P]),
+        "paged_window_prefill_attention_fp8": (I, [P, I, P, P, ctypes.c_float, ctypes.c_float, I, P, I, P, P, I, I, I, I,
+                                                   I, I, ctypes.c_float, I, I, P, I, P, SZ, P]),
         "kv_swap_bytes": (SZ, [P, I]),
         "kv_swap_out": (I, [P, P, I, P, SZ, P]),
         "kv_swap_in": (I, [P, P, I, P, SZ, P]),
@@ -378,6 +394,44 @@ class KVPool:
         Everything runs on `stream` (torch's current one unless given), a new q_out's zeros and the
         copy of positions that are not contiguous too: order the inputs before it, and what reads
         the outputs behind it."""
+        head, tail, q_out, _keep = self._rope_call(k, v, slot_mapping, positions, rope, q, q_out, seq_ids, stream, k_scale, v_scale)
+        status = self._lib.kv_append_rope(self._handle, layer, rope._handle, *head, *tail)
+        if status:
+            _check(status, self._lib)
+        return q_out
+
+    def append_norm_rope(self, layer: int, k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
+                         positions: torch.Tensor, rope: "Rope", k_weight: torch.Tensor | None, q: torch.Tensor | None = None,
+                         q_weight: torch.Tensor | None = None, eps: float = 1e-6, q_out: torch.Tensor | None = None,
+                         seq_ids: torch.Tensor | None = None, stream=None, k_scale=None, v_scale=None) -> torch.Tensor | None:
+        """append_rope() with each head's K and q rows normalised first: x / sqrt(mean(x^2) + eps) times the
+        weights, then rotated, rounded once.
+
+        k_weight, q_weight: [head_dim], or [heads, head_dim] with a row for each head, of k's dtype or float32
+        (both the same; None: all 1).  The other arguments and the result are append_rope's."""
+        head, tail, q_out, _keep = self._rope_call(k, v, slot_mapping, positions, rope, q, q_out, seq_ids, stream, k_scale, v_scale)
+        _need(q is not None or q_weight is None, "q_weight without q")
+        wt, given = k.dtype, [w for w in (k_weight, q_weight) if w is not None]
+        if given:
+            wt = given[0].dtype
+            _need(all(w.dtype == wt for w in given) and wt in (k.dtype, torch.float32), "weights must be of k's dtype or float32")
+        weights = []
+        for w, heads in ((q_weight, 0 if q is None else q.shape[1]), (k_weight, self._kv_heads)):
+            if w is None:
+                weights += [None, 0]
+                continue
+            _need(w.shape in ((self._head_dim,), (heads, self._head_dim)) and w.stride(-1) == 1 and w.get_device() == self._index,
+                  "weights must be [head_dim] or [heads, head_dim], contiguous along head_dim, on the pool's device")
+            _need(w.dim() == 1 or heads == 1 or w.stride(0) == 0 or w.stride(0) >= self._head_dim, "rows of weights overlap")
+            weights += [w.data_ptr(), w.stride(0) if w.dim() == 2 else 0]
+        status = self._lib.kv_append_norm_rope(self._handle, layer, rope._handle, *head, *weights, DTYPE_CODE[wt], float(eps), *tail)
+        if status:
+            _check(status, self._lib)
+        return q_out
+
+    def _rope_call(self, k, v, slot_mapping, positions, rope, q, q_out, seq_ids, stream, k_scale, v_scale):
+        """Checks of append_rope and append_norm_rope; their arguments from seq_ids to num_q_heads, those from
+        k_scale on, q_out, and positions (a copy made here has to live until the call)."""
         n, dt, D, index = slot_mapping.shape[0], k.dtype, self._head_dim, self._index
         ks, vs = k.stride(), v.stride()
         flat = rope.num_axes == 1
@@ -410,13 +464,9 @@ class KVPool:
             query = (None, 0, None, 0, 0)
         if self.dtype != FP8:
             k_scale = v_scale = 1.0
-        status = self._lib.kv_append_rope(
-            self._handle, layer, rope._handle, ids, n, k.data_ptr(), ks[0], v.data_ptr(), vs[0], DTYPE_CODE[dt],
-            slot_mapping.data_ptr(), positions.data_ptr(), n if flat else positions.stride(0), *query, float(k_scale),
-            float(v_scale), _stream(self.buffer, stream))
-        if status:
-            _check(status, self._lib)
-        return q_out
+        return ((ids, n, k.data_ptr(), ks[0], v.data_ptr(), vs[0], DTYPE_CODE[dt], slot_mapping.data_ptr(),
+                 positions.data_ptr(), n if flat else positions.stride(0), *query),
+                (float(k_scale), float(v_scale), _stream(self.buffer, stream)), q_out, positions)
 
     def _check_append_rope(self, k, v, slot_mapping, positions, rope, k_scale, v_scale, stream):
         """append_rope's checks one by one; returns positions, contiguous along tokens."""
@@ -510,6 +560,85 @@ def slot_mapping(block_tables: torch.Tensor, context_lens: torch.Tensor, block_s
              _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), B,
              block_size, num_blocks, _ptr(out), _stream(out, stream))
     return out
+
+
+class StepTables(NamedTuple):
+    """What extend_tables makes of a step: int32 tensors on the GPU."""
+
+    context_lens: torch.Tensor  # [sequences] cached and granted tokens
+    query_start: torch.Tensor   # [sequences + 1] where each sequence's new tokens start
+    slot_mapping: torch.Tensor  # [tokens] slot of each new token; -1 behind the last
+    positions: torch.Tensor     # [tokens] its position; 0 behind the last
+    seq_ids: torch.Tensor       # [tokens] its sequence; -1 behind the last
+    queue_state: torch.Tensor   # [2] front of the free queue and number of free blocks
+
+
+def make_step_tables(num_seqs: int, num_tokens: int, device=None) -> StepTables:
+    """Buffers for extend_tables' results with room for num_tokens new tokens."""
+    dev = torch.device(device if device is not None else "cuda")
+    return StepTables(*(torch.empty(n, dtype=torch.int32, device=dev)
+                        for n in (num_seqs, num_seqs + 1, num_tokens, num_tokens, num_tokens, 2)))
+
+
+def make_free_queue(num_blocks: int, reserve_null_block: bool = False, device=None):
+    """(free_queue, queue_state) with every block free, in increasing order (block 0 held back as the null
+    block if asked for), as a new BlockAllocator has them."""
+    dev = torch.device(device if device is not None else "cuda")
+    first = int(bool(reserve_null_block))
+    _need(num_blocks > first, "no block is left")
+    queue = torch.full((num_blocks,), -1, dtype=torch.int32, device=dev)
+    queue[:num_blocks - first] = torch.arange(first, num_blocks, dtype=torch.int32, device=dev)
+    return queue, torch.tensor([0, num_blocks - first], dtype=torch.int32, device=dev)
+
+
+def _check_tables(block_tables, lens, *rest):
+    _need(block_tables.dim() == 2 and lens.shape == (block_tables.shape[0],), "block_tables [B, max_blocks], lengths [B]")
+    index = block_tables.get_device()
+    _need(index >= 0 and all(t is None or (t.dtype == torch.int32 and t.is_contiguous() and t.get_device() == index)
+                             for t in (block_tables, lens, *rest)),
+          "every tensor must be contiguous int32 on block_tables' GPU")
+
+
+def extend_tables(block_tables: torch.Tensor, cached_lens: torch.Tensor, new_lens: torch.Tensor, free_queue: torch.Tensor,
+                  queue_state: torch.Tensor, block_size: int, num_tokens: int, out: StepTables | None = None,
+                  stream=None) -> StepTables:
+    """Blocks from the free queue for each sequence's new tokens, into block_tables, and the step's lists.
+
+    Sequence s ([B], int32) has cached_lens[s] tokens and brings new_lens[s]; blocks go out in the sequences'
+    order, and a sequence that needs more than are left, or whose tokens do not fit num_tokens, is refused (an
+    empty run in query_start; see kv_tables_extend).  The lists have num_tokens entries, those behind the last
+    token padding (slot -1, position 0, sequence -1), so they go as they are to KVPool.append_rope,
+    append_norm_rope and paged_window_prefill_attention, in a captured graph too.  out: buffers to write to
+    (make_step_tables); out.context_lens may be cached_lens itself and out.queue_state queue_state itself.
+    Everything runs on `stream` (torch's current one unless given)."""
+    lib = _lib or load_library()
+    if out is None:
+        out = _made(block_tables, stream, lambda: make_step_tables(block_tables.shape[0], num_tokens, block_tables.device))
+    _check_tables(block_tables, cached_lens, new_lens, free_queue, queue_state, *out)
+    B = block_tables.shape[0]
+    _need(new_lens.shape == out.context_lens.shape == (B,) and out.query_start.shape == (B + 1,)
+          and out.slot_mapping.shape == out.positions.shape == out.seq_ids.shape == (num_tokens,)
+          and queue_state.shape == out.queue_state.shape == (2,) and free_queue.dim() == 1, "shapes of the lists (see make_step_tables)")
+    _call_on(block_tables, lib, lib.kv_tables_extend, block_tables.data_ptr(), block_tables.shape[1], cached_lens.data_ptr(),
+             new_lens.data_ptr(), B, block_size, free_queue.shape[0], free_queue.data_ptr(), queue_state.data_ptr(), num_tokens,
+             out.context_lens.data_ptr(), out.query_start.data_ptr(), out.slot_mapping.data_ptr(), out.positions.data_ptr(),
+             out.seq_ids.data_ptr(), out.queue_state.data_ptr(), _stream(block_tables, stream))
+    return out
+
+
+def release_tables(block_tables: torch.Tensor, context_lens: torch.Tensor, free_queue: torch.Tensor, queue_state: torch.Tensor,
+                   block_size: int, finished: torch.Tensor | None = None, window: int = 0, sinks: int = 0, stream=None):
+    """Give blocks back to the free queue, in place: all blocks of sequences whose `finished` entry (int32 [B])
+    is not 0, their lengths becoming 0; and with window > 0, of the others the blocks that no later query of a
+    layer with this window and these first tokens sees (see kv_tables_release)."""
+    lib = _lib or load_library()
+    _check_tables(block_tables, context_lens, free_queue, queue_state, finished)
+    _need(queue_state.shape == (2,) and free_queue.dim() == 1 and (finished is None or finished.shape == context_lens.shape),
+          "queue_state [2], free_queue [blocks], finished [B]")
+    _need(window >= 0 and sinks >= 0, "window and sinks from 0 on")
+    _call_on(block_tables, lib, lib.kv_tables_release, block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
+             context_lens.shape[0], block_size, free_queue.shape[0], _ptr(finished), min(int(window), 0x7FFFFFFF),
+             min(int(sinks), 0x7FFFFFFF), free_queue.data_ptr(), queue_state.data_ptr(), _stream(block_tables, stream))
 
 
 def _options(num_ctas=0, ctas_per_sm=0, consumer_warps=0, kernel="auto", heads_per_stage=0,
@@ -772,6 +901,129 @@ def paged_shared_prefix_attention(q, k_cache, v_cache, block_tables, context_len
     else:
         _call_on(q, lib, lib.paged_shared_prefix_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                  *sizes, DTYPE_CODE[q.dtype], *rest)
+    return out
+
+
+def _same_gpu(q, *tensors):
+    """Every tensor (None aside) on q's GPU: the library cannot tell a host address from a device one."""
+    index = q.get_device()
+    _need(index >= 0 and all(t is None or t.get_device() == index for t in tensors), "every tensor must be on q's GPU")
+
+
+def _check_caches(q, k_cache, v_cache, k_scale, v_scale) -> bool:
+    """Shapes and types of q and one layer's caches; whether they are E4M3."""
+    _need(q.dim() == 3 and k_cache.dim() == 4 and k_cache.shape[3] == q.shape[2] and v_cache.shape == k_cache.shape,
+          "q [n, Hq, D], caches [NB, Hkv, bs, D]")
+    fp8 = k_cache.dtype == FP8
+    _need((q.dtype in _ROW_DTYPES and v_cache.dtype == FP8 and k_scale is not None and v_scale is not None) if fp8
+          else (q.dtype in _ROW_DTYPES and q.dtype == k_cache.dtype == v_cache.dtype),
+          "q and the caches share a dtype, or both caches are E4M3 with k_scale and v_scale")
+    _need(q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous(), "contiguous q and caches")
+    return fp8
+
+
+def _check_out(q, out, out_dtype, workspace):
+    _need(out.dtype == out_dtype and out_dtype in _ROW_DTYPES and out.shape == q.shape and out.is_contiguous(),
+          "out must be contiguous, of q's shape and of out_dtype")
+    _need(workspace.is_contiguous(), "a contiguous workspace")
+
+
+def _check_sight(window, sinks):
+    _need(0 < window and 0 <= sinks, "window from 1 on, sinks from 0 on")
+    return min(int(window), 0x7FFFFFFF), min(int(sinks), 0x7FFFFFFF)
+
+
+def paged_window_decode_attention(q, k_cache, v_cache, block_tables, context_lens, scale: float, window: int,
+                                  sinks: int = 0, out=None, out_dtype=None, workspace=None, stream=None, k_scale=None,
+                                  v_scale=None, **opts):
+    """paged_decode_attention over the last `window` cached tokens of each sequence (the newest
+    among them) and its first `sinks` ones.
+
+    Table entries of blocks out of sight are not read and may be anything.  The other arguments are
+    those of paged_decode_attention, the workspace too (make_workspace).  Everything runs on
+    `stream` (torch's current one unless given)."""
+    lib = _lib or load_library()
+    _same_gpu(q, k_cache, v_cache, block_tables, context_lens, out, workspace)
+    fp8 = _check_caches(q, k_cache, v_cache, k_scale, v_scale)
+    B, Hq, D = q.shape
+    NB, Hkv, bs, _ = k_cache.shape
+    window, sinks = _check_sight(window, sinks)
+    _need(block_tables.dtype == context_lens.dtype == torch.int32 and block_tables.is_contiguous()
+          and context_lens.is_contiguous(), "contiguous int32 tables and lengths")
+    _need(block_tables.dim() == 2 and block_tables.shape[0] == B and context_lens.shape == (B,),
+          "one table row and length per sequence")
+    out_dtype = out_dtype or q.dtype
+    if out is None:
+        out = _made(q, stream, lambda: torch.empty((B, Hq, D), dtype=out_dtype, device=q.device))
+    if workspace is None:
+        workspace = _made(q, stream, lambda: make_workspace(B, Hq, Hkv, D, q.device, **opts))
+    _check_out(q, out, out_dtype, workspace)
+    o = ctypes.byref(_options(**opts)) if opts else None
+    sizes = (NB, block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, Hq, Hkv, D, bs)
+    rest = (float(scale), window, sinks, out.data_ptr(), DTYPE_CODE[out_dtype], workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), o, _stream(q, stream))
+    if fp8:
+        _call_on(q, lib, lib.paged_window_decode_attention_fp8, q.data_ptr(), DTYPE_CODE[q.dtype], k_cache.data_ptr(),
+                 v_cache.data_ptr(), float(k_scale), float(v_scale), *sizes, *rest)
+    else:
+        _call_on(q, lib, lib.paged_window_decode_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *sizes,
+                 DTYPE_CODE[q.dtype], *rest)
+    return out
+
+
+def window_prefill_workspace_bytes(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, device=None) -> int:
+    lib = load_library()
+    dev = torch.device(device if device is not None else "cuda")
+    idx = dev.index if dev.index is not None else torch.cuda.current_device()
+    n = ctypes.c_size_t()
+    _check(lib.paged_window_prefill_workspace_bytes(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, idx,
+                                                    ctypes.byref(n)), lib)
+    return int(n.value)
+
+
+def make_window_prefill_workspace(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, device=None) -> torch.Tensor:
+    """A workspace for paged_window_prefill_attention with these sizes (or smaller ones)."""
+    dev = torch.device(device if device is not None else "cuda")
+    n = window_prefill_workspace_bytes(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, dev)
+    return torch.empty(n, dtype=torch.uint8, device=dev)
+
+
+def paged_window_prefill_attention(q, k_cache, v_cache, block_tables, query_start, context_lens, scale: float, window: int,
+                                   sinks: int = 0, out=None, out_dtype=None, workspace=None, stream=None, k_scale=None,
+                                   v_scale=None):
+    """paged_prefill_attention in which each new token sees the last `window` tokens up to itself and
+    the first `sinks` ones of its sequence.
+
+    Table entries of blocks that none of a sequence's new tokens sees are not read.  Rows of q behind
+    the last sequence (query_start[-1]) are padding: those rows of out stay as they are (a new out holds
+    zeros there).  Everything runs on `stream` (torch's current one unless given)."""
+    lib = _lib or load_library()
+    _same_gpu(q, k_cache, v_cache, block_tables, query_start, context_lens, out, workspace)
+    fp8 = _check_caches(q, k_cache, v_cache, k_scale, v_scale)
+    T, Hq, D = q.shape
+    NB, Hkv, bs, _ = k_cache.shape
+    B = context_lens.shape[0]
+    window, sinks = _check_sight(window, sinks)
+    _need(block_tables.dtype == context_lens.dtype == query_start.dtype == torch.int32 and block_tables.is_contiguous()
+          and context_lens.is_contiguous() and query_start.is_contiguous(), "contiguous int32 tables and lengths")
+    _need(block_tables.dim() == 2 and block_tables.shape[0] == B and context_lens.shape == (B,)
+          and query_start.shape == (B + 1,), "one table row and length per sequence, query_start [sequences + 1]")
+    out_dtype = out_dtype or q.dtype
+    if out is None:
+        out = _made(q, stream, lambda: torch.zeros((T, Hq, D), dtype=out_dtype, device=q.device))
+    if workspace is None:
+        workspace = _made(q, stream, lambda: make_window_prefill_workspace(B, T, Hq, Hkv, D, q.device))
+    _check_out(q, out, out_dtype, workspace)
+    sizes = (NB, block_tables.data_ptr(), block_tables.shape[1], query_start.data_ptr(), context_lens.data_ptr(), B, T,
+             Hq, Hkv, D, bs)
+    rest = (float(scale), window, sinks, out.data_ptr(), DTYPE_CODE[out_dtype], workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream(q, stream))
+    if fp8:
+        _call_on(q, lib, lib.paged_window_prefill_attention_fp8, q.data_ptr(), DTYPE_CODE[q.dtype], k_cache.data_ptr(),
+                 v_cache.data_ptr(), float(k_scale), float(v_scale), *sizes, *rest)
+    else:
+        _call_on(q, lib, lib.paged_window_prefill_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *sizes,
+                 DTYPE_CODE[q.dtype], *rest)
     return out
 
 

@@ -1,12 +1,13 @@
-// The body of the decode kernel and, with kTails, of the shared-prefix kernel's
-// tails (decode_kernel.cuh includes it in both functions).  In scope: Policy,
-// Args, kTails, a, tmk, tmv, base, units, others (the last two set with kTails).
+// The body of the decode kernel, with kTails of the shared-prefix kernel's tails
+// and with kWindow of the windowed decode kernel (decode_kernel.cuh includes it in
+// each of the functions).  In scope: Policy, Args, kTails, kWindow, a, tmk, tmv,
+// base, units, others (the last two set with kTails).
     const int G = a.num_q_heads / a.num_kv_heads;
     const int Hc = a.heads_per_stage, R = a.warps_per_head, NC = a.consumer_warps;
     const int chunks = a.num_kv_heads / Hc;
     const int D = a.head_dim;
     const int half_bytes = Hc * a.block_size * D * dtype_bytes(a.kv_dtype);
-    const SmemLayout L = smem_layout(a.stages, half_bytes, kTails ? 2 * a.num_seqs : a.num_seqs, NC, R, G, D,
+    const SmemLayout L = smem_layout(a.stages, half_bytes, kTails || kWindow ? 2 * a.num_seqs : a.num_seqs, NC, R, G, D,
                                      a.block_size, Policy::kScratch);
     uint8_t* ring = base + L.ring;
     uint64_t* full = reinterpret_cast<uint64_t*>(base + L.full_bar);
@@ -14,7 +15,7 @@
     volatile int* abort = reinterpret_cast<volatile int*>(base + L.flags);
     int32_t* scan = reinterpret_cast<int32_t*>(base + L.scan);
     int32_t* cum = reinterpret_cast<int32_t*>(base + L.cum);
-    int32_t* skip = cum + a.num_seqs + 1;  // kTails only
+    int32_t* skip = cum + a.num_seqs + 1;  // kTails and kWindow only
     float* merge = reinterpret_cast<float*>(base + L.merge);
 
     const int tid = threadIdx.x;
@@ -24,7 +25,7 @@
     }
     int P = a.num_ctas;
     if constexpr (kTails) {
-        P = build_prefix<true>(a, chunks, cum, scan, skip, units);  // ends with __syncthreads
+        P = build_prefix<true, false>(a, chunks, cum, scan, skip, units);  // ends with __syncthreads
         if (static_cast<int>(blockIdx.x) >= P) {
             *others = true;
             return;
@@ -52,14 +53,14 @@
         // launch finishes; everything else (q, the new rows, the workspace, the
         // outputs) is touched only after waiting for it.
         if (!a.early_reads) pdl_wait();
-        build_prefix<false>(a, chunks, cum, scan, skip, nullptr);  // ends with __syncthreads
+        build_prefix<false, kWindow>(a, chunks, cum, scan, skip, nullptr);  // ends with __syncthreads
     }
     const int64_t W = cum[a.num_seqs];
     const int start = static_cast<int>(static_cast<int64_t>(blockIdx.x) * W / P);
     const int end = static_cast<int>((static_cast<int64_t>(blockIdx.x) + 1) * W / P);
     const int warp = tid >> 5, lane = tid & 31;
     if (warp == 0 && start < end) {
-        produce<Policy::kTensor, kTails>(a, ring, full, empty, cum, skip, chunks, start, end, half_bytes, &tmk,
+        produce<Policy::kTensor, kTails, kWindow>(a, ring, full, empty, cum, skip, chunks, start, end, half_bytes, &tmk,
                                  &tmv, abort);
         return;
     }
@@ -112,6 +113,20 @@
         const int seg_end = min(pair_b, end);
         const int h = hc * Hc + hw;
         const int ctx = clamp_context(a, s, false) - (kTails ? skip[s] * a.block_size : 0);
+        // kWindow: the first token of block j of the list, and what of the block is hidden.
+        auto first_token = [&](int j) {
+            if constexpr (kWindow) return (j + (j >= a.sink_blocks ? skip[s] : 0)) * a.block_size;
+            return j * a.block_size;
+        };
+        auto hidden_in = [&](int j) {
+            Hidden r{0, 0};
+            if constexpr (kWindow) {
+                const int t0 = first_token(j);
+                r.from = max(a.sinks - t0, 0);
+                r.to = min(ctx - a.window - t0, a.block_size);
+            }
+            return r;
+        };
         pol.begin(st, a, s, h, G);
         const int first = seg + (((rr - (seg - start)) % R) + R) % R;
         // Ring position of item `first` (item t = i - start sits in stage
@@ -137,20 +152,29 @@
             bool ok = mbar_wait_bounded(&full[stage], phase, abort, a.status);
             if (ok && two) ok = mbar_wait_bounded(&full[stage2], phase2, abort, a.status);
             if (ok && j >= 0) {
-                const int n_valid = min(a.block_size, ctx - j * a.block_size);
+                const int n_valid = min(a.block_size, ctx - first_token(j));
                 uint8_t* kt = ring + stage * 2 * half_bytes;
-                bool patched = !kTails && a.k_new && j == nb - 1 && append_row(a, pol, kt, kt + half_bytes, s, h, hw, j, n_valid - 1);
+                bool patched = !kTails && !kWindow && a.k_new && j == nb - 1 && append_row(a, pol, kt, kt + half_bytes, s, h, hw, j, n_valid - 1);
                 if constexpr (Policy::kPairs) {
                     if (two) {
                         const int j1 = j + R;
-                        const int n1 = min(a.block_size, ctx - j1 * a.block_size);
+                        const int n1 = min(a.block_size, ctx - first_token(j1));
                         uint8_t* kt1 = ring + stage2 * 2 * half_bytes;
-                        if (!kTails && a.k_new && j1 == nb - 1)
+                        if (!kTails && !kWindow && a.k_new && j1 == nb - 1)
                             patched |= append_row(a, pol, kt1, kt1 + half_bytes, s, h, hw, j1, n1 - 1);
-                        pol.tile2(st, a, kt, kt + half_bytes, n_valid, kt1, kt1 + half_bytes, n1, hw, G);
+                        if constexpr (kWindow)
+                            pol.template tile2<true>(st, a, kt, kt + half_bytes, n_valid, kt1, kt1 + half_bytes, n1,
+                                                     hw, G, hidden_in(j), hidden_in(j1));
+                        else
+                            pol.tile2(st, a, kt, kt + half_bytes, n_valid, kt1, kt1 + half_bytes, n1, hw, G);
                     }
                 }
-                if (!two) pol.tile(st, a, kt, kt + half_bytes, hw, n_valid, G, scratch);
+                if constexpr (kWindow) {
+                    if (!two)
+                        pol.template tile<true>(st, a, kt, kt + half_bytes, hw, n_valid, G, scratch, hidden_in(j));
+                } else {
+                    if (!two) pol.tile(st, a, kt, kt + half_bytes, hw, n_valid, G, scratch);
+                }
                 if (patched) fence_proxy_async_smem();  // generic writes before the next TMA fill
             }
             __syncwarp();

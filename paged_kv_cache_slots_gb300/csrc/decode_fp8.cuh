@@ -193,9 +193,16 @@ struct MmaFp8Policy {
     // online-softmax update covers all their tokens, and the independent MMA
     // chains of the slices interleave, which keeps the warp's dependent
     // instruction chains short.
-    template <int NS>
+    // kHole: tokens [hole[n].from, hole[n].to) of slice n are hidden; one token at
+    // least of the slices is not.
+    template <int NS, bool kHole = false>
     __device__ __forceinline__ void slices(State& st, const DecodeArgs& a, const uint32_t (&kb)[NS],
-                                           const uint32_t (&vb)[NS], const int (&nv)[NS], int G) {
+                                           const uint32_t (&vb)[NS], const int (&nv)[NS], int G,
+                                           [[maybe_unused]] const Hidden* hole = nullptr) {
+        auto seen = [&](int n, int t) {
+            if constexpr (kHole) return t < nv[n] && (t < hole[n].from || t >= hole[n].to);
+            return t < nv[n];
+        };
         const int lane = threadIdx.x & 31;
         const uint32_t sw = lane & 7;  // swizzle key of the rows this lane addresses
         // Lanes 0-7 / 8-15 / 16-23 / 24-31 address rows 0-7 / 8-15 / 0-7 / 8-15
@@ -246,8 +253,8 @@ struct MmaFp8Policy {
 #pragma unroll
             for (int n = 0; n < NS; ++n) {
                 const int t0 = lane >> 2;
-                x[n][0] = t0 < nv[n] ? acc[n][0] * sl : -INFINITY;
-                x[n][1] = t0 + 8 < nv[n] ? acc[n][2] * sl : -INFINITY;
+                x[n][0] = seen(n, t0) ? acc[n][0] * sl : -INFINITY;
+                x[n][1] = seen(n, t0 + 8) ? acc[n][2] * sl : -INFINITY;
                 mx = fmaxf(mx, fmaxf(x[n][0], x[n][1]));
             }
 #pragma unroll
@@ -281,7 +288,7 @@ struct MmaFp8Policy {
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
             const int t0 = lane >> 2;
-            const bool v0 = t0 < nv[n], v1 = t0 + 8 < nv[n];
+            const bool v0 = seen(n, t0), v1 = seen(n, t0 + 8);
             x[n][0] = v0 ? acc[n][0] * sl0 : -INFINITY;
             x[n][1] = v0 ? acc[n][1] * sl1 : -INFINITY;
             x[n][2] = v1 ? acc[n][2] * sl0 : -INFINITY;
@@ -357,34 +364,54 @@ struct MmaFp8Policy {
     // One head's part of a stage: kt/vt point at the stage's K/V codes,
     // [Hc*bs rows][128 B]; this warp's head owns rows hw*bs .. hw*bs+bs-1,
     // taken two 16-token slices at a time.
+    // kHole: rows [hole.from, hole.to) are hidden from the query.
+    template <bool kHole = false>
     __device__ __forceinline__ void tile(State& st, const DecodeArgs& a, uint8_t* kt, uint8_t* vt,
-                                         int hw, int n_valid, int G, float*) {
+                                         int hw, int n_valid, int G, float*, [[maybe_unused]] Hidden hole = {}) {
         const int bs = a.block_size;
         uint8_t* kh = kt + hw * bs * 128;
         uint8_t* vh = vt + hw * bs * 128;
         if (n_valid < bs) zero_tail(vh, n_valid, bs);
+        if constexpr (kHole) {
+            if (hole.from < hole.to) zero_tail(vh, hole.from, hole.to);
+        }
         const uint32_t kb = smem_addr(kh), vb = smem_addr(vh);
         int mt = 0;
         for (; mt + 2 <= bs / 16; mt += 2) {
             const uint32_t k2[2] = {kb + mt * 2048u, kb + (mt + 1) * 2048u};
             const uint32_t v2[2] = {vb + mt * 2048u, vb + (mt + 1) * 2048u};
             const int n2[2] = {n_valid - 16 * mt, n_valid - 16 * (mt + 1)};
-            slices<2>(st, a, k2, v2, n2, G);
+            if constexpr (kHole) {
+                if (hole.from <= 16 * mt && 16 * mt + 32 <= hole.to) continue;
+                const Hidden h2[2] = {{hole.from - 16 * mt, hole.to - 16 * mt},
+                                      {hole.from - 16 * (mt + 1), hole.to - 16 * (mt + 1)}};
+                slices<2, true>(st, a, k2, v2, n2, G, h2);
+            } else {
+                slices<2>(st, a, k2, v2, n2, G);
+            }
         }
         if (mt < bs / 16) {
             const uint32_t k1[1] = {kb + mt * 2048u};
             const uint32_t v1[1] = {vb + mt * 2048u};
             const int n1[1] = {n_valid - 16 * mt};
-            slices<1>(st, a, k1, v1, n1, G);
+            if constexpr (kHole) {
+                const Hidden h1[1] = {{hole.from - 16 * mt, hole.to - 16 * mt}};
+                if (!(hole.from <= 16 * mt && 16 * mt + 16 <= hole.to)) slices<1, true>(st, a, k1, v1, n1, G, h1);
+            } else {
+                slices<1>(st, a, k1, v1, n1, G);
+            }
         }
-        if (n_valid < bs) fence_proxy_async_smem();  // generic writes before the next TMA fill
+        if (n_valid < bs || (kHole && hole.from < hole.to))
+            fence_proxy_async_smem();  // generic writes before the next TMA fill
     }
 
     // Two 16-token blocks (block_size 16) from two stages of one (sequence,
     // head) run, processed together.
     static constexpr bool kPairs = true;
+    template <bool kHole = false>
     __device__ __forceinline__ void tile2(State& st, const DecodeArgs& a, uint8_t* kt0, uint8_t* vt0,
-                                          int n0, uint8_t* kt1, uint8_t* vt1, int n1, int hw, int G) {
+                                          int n0, uint8_t* kt1, uint8_t* vt1, int n1, int hw, int G,
+                                          [[maybe_unused]] Hidden hole0 = {}, [[maybe_unused]] Hidden hole1 = {}) {
         uint8_t* kh0 = kt0 + hw * 16 * 128;
         uint8_t* vh0 = vt0 + hw * 16 * 128;
         uint8_t* kh1 = kt1 + hw * 16 * 128;
@@ -394,8 +421,17 @@ struct MmaFp8Policy {
         const uint32_t k2[2] = {smem_addr(kh0), smem_addr(kh1)};
         const uint32_t v2[2] = {smem_addr(vh0), smem_addr(vh1)};
         const int n2[2] = {n0, n1};
-        slices<2>(st, a, k2, v2, n2, G);
-        if (n0 < 16 || n1 < 16) fence_proxy_async_smem();
+        if constexpr (kHole) {
+            const bool holes = hole0.from < hole0.to || hole1.from < hole1.to;
+            if (hole0.from < hole0.to) zero_tail(vh0, hole0.from, hole0.to);
+            if (hole1.from < hole1.to) zero_tail(vh1, hole1.from, hole1.to);
+            const Hidden h2[2] = {hole0, hole1};
+            slices<2, true>(st, a, k2, v2, n2, G, h2);
+            if (n0 < 16 || n1 < 16 || holes) fence_proxy_async_smem();
+        } else {
+            slices<2>(st, a, k2, v2, n2, G);
+            if (n0 < 16 || n1 < 16) fence_proxy_async_smem();
+        }
     }
 
     // 16-byte chunk q of row r of head hw's tile (chunk c of a row lands at c ^ (row % 8)).

@@ -107,11 +107,17 @@ __device__ __forceinline__ int clamp_context(const DecodeArgs& a, int s, bool fl
     return c;
 }
 
+// Tokens [from, to) of a block that a windowed query does not see (none if from >= to).
+struct Hidden {
+    int from, to;
+};
+
 // cum[s] = chunks * sum_{s' < s, ctx_s' > 0} (ceil(ctx_s' / bs) + phantom);
 // cum[num_seqs] = W.  kTails: ctx is what follows skip[s] shared blocks.
+// kWindow: skip[s] blocks behind the first sink_blocks hold nothing in sight.
 // Returns the CTAs that share the items (kTails: those that the prefix's parts
 // leave, see *units; else the grid).
-template <bool kTails, class Args>
+template <bool kTails, bool kWindow, class Args>
 static __device__ int build_prefix(const Args& a, int chunks, int32_t* cum, int32_t* scan, int32_t* skip,
                                    [[maybe_unused]] Units* units) {
     [[maybe_unused]] int first_ctx = 0;  // of this thread's first sequence, asked for before the groups are looked at
@@ -133,6 +139,11 @@ static __device__ int build_prefix(const Args& a, int chunks, int32_t* cum, int3
                 const int sb = units->bad ? 0 : shared_blocks(a, s, c);
                 skip[s] = sb;
                 nb -= sb;
+            }
+            if constexpr (kWindow) {
+                const int out = max(0, max(0, c - a.window) / a.block_size - a.sink_blocks);
+                skip[s] = out;
+                nb -= out;
             }
             v = nb > 0 ? (nb + a.phantom) * chunks : 0;
         }
@@ -184,9 +195,10 @@ __device__ __forceinline__ int4 tail_parts_of(int pair_r, int blocks, int64_t W,
 // kTensor: stages arrive through 2-D tensor maps with a 128-byte swizzle (box
 // of 128 bytes x Hc*bs rows, one box per 128-byte slice of the row);
 // otherwise as two plain contiguous bulk copies.
-// kTails: the first skip[s] entries of a sequence's table row are left out.
-template <bool kTensor, bool kTails>
-static __device__ void produce(const DecodeArgs& a, uint8_t* ring, uint64_t* full, uint64_t* empty,
+// kTails: the first skip[s] entries of a sequence's table row are left out;
+// kWindow: skip[s] entries behind the first sink_blocks.
+template <bool kTensor, bool kTails, bool kWindow, class Args>
+static __device__ void produce(const Args& a, uint8_t* ring, uint64_t* full, uint64_t* empty,
                         const int32_t* cum, const int32_t* skip, int chunks, int start, int end, int half_bytes,
                         const CUtensorMap* tmk, const CUtensorMap* tmv, volatile int* abort) {
     const int lane = threadIdx.x & 31;
@@ -206,7 +218,10 @@ static __device__ void produce(const DecodeArgs& a, uint8_t* ring, uint64_t* ful
             const int hc = r / nbv;
             const int j = r - hc * nbv - a.phantom;
             if (j >= 0) {
-                const int64_t entry = static_cast<int64_t>(s) * a.max_blocks + j + (kTails ? skip[s] : 0);
+                int64_t entry = static_cast<int64_t>(s) * a.max_blocks + j + (kTails ? skip[s] : 0);
+                if constexpr (kWindow) {
+                    if (j >= a.sink_blocks) entry += skip[s];
+                }
                 int blk = __ldg(a.block_tables + entry);
                 if (blk < 0 || blk >= a.num_blocks) {
                     raise_flag(a.status, kFlagBadBlock);
@@ -670,9 +685,9 @@ __device__ __forceinline__ bool append_row(const DecodeArgs& a, const Policy& po
 // Policy provides: State, begin(), tile(), write_state(), write_partial(),
 // write_final(), kTensor, kScratch, kPairs (and tile2() when kPairs), and
 // kMaxThreads, the largest block it is launched with (its register budget).
-// kTails and Args are what the included text tests and reads (see decode_tails
-// below); this kernel is built with their defaults.
-template <class Policy, bool kTails = false, class Args = DecodeArgs>
+// kTails, kWindow and Args are what the included text tests and reads (see
+// decode_tails below); this kernel is built with their defaults.
+template <class Policy, bool kTails = false, bool kWindow = false, class Args = DecodeArgs>
 __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
     paged_decode_partial_kernel(const Args a, const __grid_constant__ CUtensorMap tmk,
                                 const __grid_constant__ CUtensorMap tmv) {
@@ -695,10 +710,40 @@ __global__ void __launch_bounds__(Policy::kMaxThreads, 1)
 // 0.8 % slower that way (32 sequences of 8k: 5200 instead of 5245 GB/s), and
 // with the parts in one __global__ function with the tails the shared-prefix
 // case of 256 sequences over a prefix of 32k took 204 us instead of 191.
-template <class Policy, bool kTails = true, class Args = TailArgs>
+template <class Policy, bool kTails = true, bool kWindow = false, class Args = TailArgs>
 __device__ __forceinline__ void decode_tails(const Args& a, const CUtensorMap& tmk, const CUtensorMap& tmv,
                                              uint8_t* base, Units* units, bool* others) {
 #include "decode_body.cuh"
+}
+
+// The variant that attends to a window and the first tokens.  Of a sequence's
+// table row it takes the first sink_blocks entries and those from the block of
+// the window's first token on: skip[s] entries between them are not read, so
+// what they name may have been given away.  The first block of the window and the
+// last one of the first tokens are in part hidden: their scores are masked and
+// their V rows zeroed (0 * V has to stay 0 whatever the row holds).
+template <class Policy, bool kTails = false, bool kWindow = true, class Args = WindowArgs>
+__global__ void __launch_bounds__(Policy::kMaxThreads, 1)
+    paged_window_decode_kernel(const Args a, const __grid_constant__ CUtensorMap tmk,
+                               const __grid_constant__ CUtensorMap tmv) {
+    extern __shared__ uint8_t smem_raw[];
+    pdl_allow_next();
+    uint8_t* base = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    [[maybe_unused]] Units* units = nullptr;
+    [[maybe_unused]] bool* others = nullptr;
+#include "decode_body.cuh"
+}
+
+template <class Policy>
+cudaError_t launch_window(const WindowArgs& a, const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t stream) {
+    static RaisedLimit limit;
+    auto kern = paged_window_decode_kernel<Policy>;
+    const cudaError_t e = allow_shared_memory(kern, a.device, a.smem_bytes, &limit);
+    if (e != cudaSuccess) return e;
+    if (32 * (1 + a.consumer_warps) > Policy::kMaxThreads) return cudaErrorInvalidValue;
+    return launch_kernel(kern, dim3(a.num_ctas), dim3(32 * (1 + a.consumer_warps)),
+                         static_cast<size_t>(a.smem_bytes), stream, a.pdl != 0, a, tmk, tmv);
 }
 
 // Launch the partial kernel of `Policy`.

@@ -61,8 +61,10 @@ struct MmaPolicy {
     // One head's part of a stage: kt/vt point at the stage's K/V, laid out as
     // [64-element slice][Hc*bs rows][128 B] (128-byte swizzled by the tensor
     // copy); this warp's head owns rows hw*bs .. hw*bs+bs-1 of every slice.
+    // kHole: rows [hole.from, hole.to) are hidden from the query.
+    template <bool kHole = false>
     __device__ __forceinline__ void tile(State& st, const DecodeArgs& a, uint8_t* kt, uint8_t* vt,
-                                         int hw, int n_valid, int G, float*) {
+                                         int hw, int n_valid, int G, float*, [[maybe_unused]] Hidden hole = {}) {
         const int lane = threadIdx.x & 31;
         const int bs = a.block_size;
         const uint32_t slice_bytes = static_cast<uint32_t>(a.heads_per_stage * bs) * 128u;
@@ -81,10 +83,23 @@ struct MmaPolicy {
             }
             __syncwarp();
         }
+        if constexpr (kHole) {
+            if (hole.from < hole.to) {
+                const int rows = hole.to - hole.from;
+                for (int e = lane; e < rows * 8 * (D / 64); e += 32) {
+                    const int sl = e / (rows * 8);
+                    const int r = e - sl * rows * 8;
+                    *reinterpret_cast<uint4*>(vh + sl * slice_bytes + (hole.from + (r >> 3)) * 128 + ((r & 7) << 4)) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                }
+                __syncwarp();
+            }
+        }
         const uint32_t kb = smem_addr(kh), vb = smem_addr(vh);
         const uint32_t sw = lane & 7;  // 128-byte swizzle key of the rows this lane addresses
         const float sl = a.scale_log2;
         for (int mt = 0; mt < bs / 16; ++mt) {
+            if (kHole && hole.from <= 16 * mt && 16 * mt + 16 <= hole.to) continue;
             // ---- S^T = K . Q^T for tokens 16mt .. 16mt+15.  The warp-level MMA
             // has a long latency: the k-steps accumulate into up to 4
             // independent chains, summed at the end.
@@ -113,7 +128,11 @@ struct MmaPolicy {
             }
             // ---- online softmax (heads 2c, 2c+1; tokens g and g+8 of the slice)
             const int t0 = mt * 16 + (lane >> 2);
-            const bool v0 = t0 < n_valid, v1 = t0 + 8 < n_valid;
+            bool v0 = t0 < n_valid, v1 = t0 + 8 < n_valid;
+            if constexpr (kHole) {
+                v0 = v0 && (t0 < hole.from || t0 >= hole.to);
+                v1 = v1 && (t0 + 8 < hole.from || t0 + 8 >= hole.to);
+            }
             const float x0 = v0 ? acc[0] * sl : -INFINITY;
             const float x1 = v0 ? acc[1] * sl : -INFINITY;
             const float x2 = v1 ? acc[2] * sl : -INFINITY;
@@ -125,6 +144,7 @@ struct MmaPolicy {
                 mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
             }
             const float mn0 = fmaxf(st.m[0], mx0), mn1 = fmaxf(st.m[1], mx1);
+            // (Every slice that is not skipped has a token in sight, so the maxima are finite.)
             const float al0 = fast_exp2(st.m[0] - mn0), al1 = fast_exp2(st.m[1] - mn1);
             st.m[0] = mn0;
             st.m[1] = mn1;
@@ -171,7 +191,8 @@ struct MmaPolicy {
                 }
             }
         }
-        if (n_valid < bs) fence_proxy_async_smem();  // generic writes before the next TMA fill
+        if (n_valid < bs || (kHole && hole.from < hole.to))
+            fence_proxy_async_smem();  // generic writes before the next TMA fill
     }
 
     // 16-byte chunk q of row r of head hw's tile (the stage's 128-byte

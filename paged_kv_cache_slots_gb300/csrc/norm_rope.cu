@@ -1,0 +1,304 @@
+// Append with the norms of query and key rows and the position rotation on the
+// way: each head's row x of a new token becomes, in one pass over the step's rows,
+//   z = w x / sqrt(mean(x^2) + eps),   y = the rotation of z by the token's position
+// (rope.cu), K rows into the token's slot with V copied beside them, query rows into
+// q_out.  The sum of squares, the norm and the rotation are fp32; y is rounded once,
+// to the row's type or to an E4M3 code of y / scale.
+//
+// Work split.  One CTA of 128 threads a token (several, by rows, while there are
+// few tokens).  A row belongs to L lanes of a warp, L the power of two from the
+// row's items on: an item is V pairs of the rotation (elements i and i + n, or 2i
+// and 2i + 1), or 2 V elements behind them, 16 bytes on each side where sizes and
+// addresses allow it.  A lane keeps its item in registers from the load to the
+// store, so the norm costs log2(L) shuffles and no second look at the row; kRows
+// rows are loaded before the first is used.  Weights are read beside the rows, from
+// L1 after a CTA's first ones.  Rows of more than 32 items (heads whose sizes leave
+// narrow items) take the loop at the end, which reads a row twice.
+//
+// Bound: HBM.  Every row is read and written once.
+#include "rope.cuh"
+
+namespace pkv {
+
+namespace {
+
+// The item `it` of a row: element offsets of its two halves and whether it turns.
+struct Item {
+    int e0, e1;
+    bool turn;
+};
+
+template <int V, bool kInter>
+__device__ __forceinline__ Item item_of(int it, int nrot, int n) {
+    const bool turn = it < nrot;
+    const int e0 = turn ? (kInter ? 2 * V * it : V * it) : 2 * n + (it - nrot) * 2 * V;
+    return {e0, turn && !kInter ? e0 + n : e0 + V, turn};
+}
+
+// V weights of a head from element e on.
+template <int DT, int V>
+__device__ __forceinline__ void load_weights(const void* w, int64_t e, bool wide, float* f) {
+    using T = typename Elem<DT>::T;
+    if (w == nullptr) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = 1.f;
+    } else if (wide) {
+        const float* p = static_cast<const float*>(w) + e;
+        if constexpr (V >= 4) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                const float4 x = __ldg(reinterpret_cast<const float4*>(p + i));
+                f[i] = x.x, f[i + 1] = x.y, f[i + 2] = x.z, f[i + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[i] = __ldg(p + i);
+        }
+    } else {
+        Raw<V * static_cast<int>(sizeof(T))> r;
+        r.load(static_cast<const char*>(w) + e * static_cast<int64_t>(sizeof(T)));
+        unpack<DT, V>(r, f);
+    }
+}
+
+template <int DT, int V, bool kInter, int kRows>
+__global__ void __launch_bounds__(kThreads) kv_append_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+    static_assert(kThreads >= kMaxRopePairs);
+    using T = typename Elem<DT>::T;
+    constexpr int kE = static_cast<int>(sizeof(T));
+    __shared__ float2 cs[kMaxRopePairs];
+    pdl_allow_next();
+    pdl_wait();
+    const int tid = threadIdx.x;
+    const int64_t i = blockIdx.x;  // token
+    const int n = a.rot_dim >> 1;
+    const int32_t id = a.seq_ids ? a.seq_ids[i] : 0;
+    const int32_t slot = a.slot_mapping[i];
+    const int32_t pos = tid < n ? a.positions[a.axis[tid] * a.positions_stride + i] : 0;
+
+    const int D = a.head_dim;
+    const int nrot = n / V, items = D / (2 * V);
+    const int Hq = a.num_q_heads, Hkv = a.num_kv_heads, H = Hq + 2 * Hkv;
+    int L = 1;
+    while (L < items && L < 32) L <<= 1;
+    const int groups = kThreads / L;
+    const int my = tid / L, it = tid & (L - 1);
+    const int r0 = static_cast<int>(blockIdx.y) * a.rows_per_cta;
+    const int r1 = min(H, r0 + a.rows_per_cta);
+
+    auto source = [&](int r) -> const char* {
+        if (r < Hq) return static_cast<const char*>(a.q) + (i * a.q_stride + static_cast<int64_t>(r) * D) * kE;
+        r -= Hq;
+        if (r < Hkv) return static_cast<const char*>(a.k) + (i * a.k_stride + static_cast<int64_t>(r) * D) * kE;
+        return static_cast<const char*>(a.v) + (i * a.v_stride + static_cast<int64_t>(r - Hkv) * D) * kE;
+    };
+    auto weights = [&](int r, int e, float* f) {
+        if (r < Hq)
+            load_weights<DT, V>(a.q_weight, r * a.q_weight_stride + e, a.wide_weights, f);
+        else
+            load_weights<DT, V>(a.k_weight, (r - Hq) * a.k_weight_stride + e, a.wide_weights, f);
+    };
+    const int ce = a.quant ? 1 : kE;  // bytes of a cached element
+    const int64_t num_slots = static_cast<int64_t>(a.num_blocks) * a.block_size;
+    int blk = 0, off = 0;
+    bool keep = false;
+    auto target = [&](int r) -> char* {
+        if (r < Hq) return static_cast<char*>(a.q_out) + (i * a.q_out_stride + static_cast<int64_t>(r) * D) * kE;
+        r -= Hq;
+        const bool v = r >= Hkv;
+        const int64_t row = (static_cast<int64_t>(blk) * Hkv + (v ? r - Hkv : r)) * a.block_size + off;
+        return static_cast<char*>(v ? a.v_cache : a.k_cache) + row * D * ce;
+    };
+    auto sum_of_squares = [](const float* f) {
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2 * V; ++j) s = fmaf(f[j], f[j], s);
+        return s;
+    };
+    const float inv_dim = 1.f / static_cast<float>(D);
+    auto factor = [&](float ss) { return rsqrtf(fmaf(ss, inv_dim, a.eps)); };
+    // f (an item's 2 V elements) times scale and weights, and turned.
+    auto finish = [&](const Item& x, const float* w, float scale, float* f) {
+#pragma unroll
+        for (int j = 0; j < 2 * V; ++j) f[j] *= scale * w[j];
+        if (!x.turn) return;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int ja = kInter ? 2 * j : j, jb = kInter ? 2 * j + 1 : j + V;
+            const float2 c = cs[x.e0 / (kInter ? 2 : 1) + j];
+            const float xa = f[ja], xb = f[jb];
+            f[ja] = xa * c.x - xb * c.y;
+            f[jb] = xb * c.x + xa * c.y;
+        }
+    };
+    auto store = [&](const Item& x, int r, const float* f) {
+        char* dst = target(r);
+        if (a.quant && r >= Hq) {
+            const float scale = r >= Hq + Hkv ? a.v_scale : a.k_scale;
+            quantize<V>(f, scale).store(dst + x.e0);
+            quantize<V>(f + V, scale).store(dst + x.e1);
+        } else {
+            pack<DT, V>(f).store(dst + x.e0 * kE);
+            pack<DT, V>(f + V).store(dst + x.e1 * kE);
+        }
+    };
+
+    bool known = false;  // the token's angles and slot (the first time round: every thread of the CTA is here)
+    auto know = [&]() -> bool {
+        known = true;
+        if (tid < n) cs[tid] = rotor(static_cast<uint64_t>(static_cast<int64_t>(pos)) * a.phase[tid], a.amplitude);
+        __syncthreads();
+        keep = slot >= 0 && slot < num_slots;
+        if (id >= 0 && slot >= num_slots && tid == 0 && blockIdx.y == 0) raise_flag(a.status, kFlagBadSlot);
+        blk = keep ? slot / a.block_size : 0;
+        off = slot - blk * a.block_size;
+        return id >= 0;
+    };
+
+    if (items <= 32) {
+        const Item x = item_of<V, kInter>(it, nrot, n);
+        const bool active = it < items;
+        for (int rb = r0; rb < r1; rb += groups * kRows) {
+            Raw<V * kE> x0[kRows], x1[kRows];
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                const int r = rb + u * groups + my;
+                if (active && r < r1) {
+                    const char* src = source(r);
+                    x0[u].load(src + x.e0 * kE);
+                    x1[u].load(src + x.e1 * kE);
+                }
+            }
+            if (!known && !know()) return;  // padding
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                const int r = rb + u * groups + my;
+                const bool mine = active && r < r1;
+                float f[2 * V];
+                float ss = 0.f;
+                if (mine) {
+                    unpack<DT, V>(x0[u], f);
+                    unpack<DT, V>(x1[u], f + V);
+                    ss = sum_of_squares(f);
+                }
+                for (int o = L >> 1; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                if (!mine || (r >= Hq && !keep)) continue;
+                if (r >= Hq + Hkv) {  // a V row
+                    if (a.quant) {
+                        store(x, r, f);
+                    } else {  // bit for bit
+                        char* dst = target(r);
+                        x0[u].store(dst + x.e0 * kE);
+                        x1[u].store(dst + x.e1 * kE);
+                    }
+                    continue;
+                }
+                float w[2 * V];
+                weights(r, x.e0, w);
+                weights(r, x.e1, w + V);
+                finish(x, w, factor(ss), f);
+                store(x, r, f);
+            }
+        }
+        return;
+    }
+    // More items than lanes: a warp a row, which is read again for its second use.
+    if (!know()) return;
+    for (int r = r0 + my; r < r1; r += groups) {
+        const char* src = source(r);
+        float ss = 0.f;
+        if (r < Hq + Hkv) {
+            for (int k = it; k < items; k += 32) {
+                const Item x = item_of<V, kInter>(k, nrot, n);
+                Raw<V * kE> x0, x1;
+                float f[2 * V];
+                x0.load(src + x.e0 * kE);
+                x1.load(src + x.e1 * kE);
+                unpack<DT, V>(x0, f);
+                unpack<DT, V>(x1, f + V);
+                ss += sum_of_squares(f);
+            }
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        }
+        if (r >= Hq && !keep) continue;
+        const float scale = factor(ss);
+        for (int k = it; k < items; k += 32) {
+            const Item x = item_of<V, kInter>(k, nrot, n);
+            Raw<V * kE> x0, x1;
+            float f[2 * V];
+            x0.load(src + x.e0 * kE);
+            x1.load(src + x.e1 * kE);
+            unpack<DT, V>(x0, f);
+            unpack<DT, V>(x1, f + V);
+            if (r < Hq + Hkv) {
+                float w[2 * V];
+                weights(r, x.e0, w);
+                weights(r, x.e1, w + V);
+                finish(x, w, scale, f);
+            } else if (!a.quant) {
+                char* dst = target(r);
+                x0.store(dst + x.e0 * kE);
+                x1.store(dst + x.e1 * kE);
+                continue;
+            }
+            store(x, r, f);
+        }
+    }
+}
+
+template <int DT, int V, int kRows>
+cudaError_t launch_v(const NormRopeArgs& a, dim3 grid, cudaStream_t stream) {
+    if (a.interleaved)
+        return launch_kernel(kv_append_norm_rope_kernel<DT, V, true, kRows>, grid, dim3(kThreads), 0, stream, a.pdl != 0, a);
+    return launch_kernel(kv_append_norm_rope_kernel<DT, V, false, kRows>, grid, dim3(kThreads), 0, stream, a.pdl != 0, a);
+}
+
+template <int DT>
+cudaError_t launch_dt(NormRopeArgs a, int align, int weight_align, int num_sms, cudaStream_t stream) {
+    constexpr int kE = static_cast<int>(sizeof(typename Elem<DT>::T));
+    auto weights_fit = [&](int v) {
+        const int need = a.wide_weights ? (v >= 4 ? 16 : 4) : v * kE;
+        return (!a.q_weight && !a.k_weight) || weight_align >= need;
+    };
+    int v = 16 / kE;
+    while (v > 1 && ((a.rot_dim / 2) % v || (a.head_dim - a.rot_dim) % (2 * v) || a.head_dim % v || align < v * kE ||
+                     !weights_fit(v)))
+        v >>= 1;
+    const int items = a.head_dim / (2 * v);
+    int L = 1;
+    while (L < items && L < 32) L <<= 1;
+    const int groups = kThreads / L;
+    const int H = a.num_q_heads + 2 * a.num_kv_heads;
+    // As in rope.cu: the rows that the threads load in one round, two or three a
+    // thread, one while that leaves no more CTAs than two for each SM.
+    const int passes = (H + groups - 1) / groups;
+    int per = (passes + 2) / 3 < (passes + 1) / 2 ? 3 : 2;
+    while (per > 1 && static_cast<int64_t>(a.n_tokens) * ((passes + per - 2) / (per - 1)) <= 2 * num_sms) --per;
+    while ((passes + per - 1) / per > 65535) per *= 2;  // the grid's limit in y
+    a.rows_per_cta = per * groups;
+    const dim3 grid(static_cast<unsigned>(a.n_tokens), static_cast<unsigned>((passes + per - 1) / per));
+    const bool three = per >= 3;
+    switch (v) {
+        case 8:
+            if constexpr (kE == 2) return three ? launch_v<DT, 8, 3>(a, grid, stream) : launch_v<DT, 8, 2>(a, grid, stream);
+            return cudaErrorInvalidValue;
+        case 4: return three ? launch_v<DT, 4, 3>(a, grid, stream) : launch_v<DT, 4, 2>(a, grid, stream);
+        case 2: return three ? launch_v<DT, 2, 3>(a, grid, stream) : launch_v<DT, 2, 2>(a, grid, stream);
+        default: return three ? launch_v<DT, 1, 3>(a, grid, stream) : launch_v<DT, 1, 2>(a, grid, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_append_norm_rope(const NormRopeArgs& a, int align, int weight_align, int num_sms,
+                                    cudaStream_t stream) {
+    switch (a.src_dtype) {
+        case kF32: return launch_dt<kF32>(a, align, weight_align, num_sms, stream);
+        case kF16: return launch_dt<kF16>(a, align, weight_align, num_sms, stream);
+        case kBF16: return launch_dt<kBF16>(a, align, weight_align, num_sms, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace pkv

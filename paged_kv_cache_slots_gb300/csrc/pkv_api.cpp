@@ -185,6 +185,28 @@ int phantom_items(int num_seqs, int chunks, int max_blocks, int ctas, int stage_
     return max_items >= 2 * static_cast<int64_t>(ctas) ? (ph > 8 ? 8 : ph) : 0;
 }
 
+// What a windowed query sees: see paged_window_decode_attention.
+struct Sight {
+    int window, sinks;
+};
+
+kv_status_t check_sight(const Sight& w, int max_blocks, int block_size) {
+    if (w.window < 1 || w.sinks < 0)
+        return fail(KV_ERR_INVALID_ARG, "window %d (from 1 on), sinks %d (from 0 on)", w.window, w.sinks);
+    if (static_cast<int64_t>(max_blocks) * block_size >= (int64_t{1} << 31))
+        return fail(KV_ERR_UNSUPPORTED, "a table row of more than 2^31 tokens");
+    return KV_OK;
+}
+
+// The same in a kernel's arguments, each no larger than a table row.
+template <class Args>
+void set_sight(const Sight& w, int max_blocks, int block_size, Args* a) {
+    const int cap = max_blocks * block_size;
+    a->window = w.window < cap ? w.window : cap;
+    a->sinks = w.sinks < cap ? w.sinks : cap;
+    a->sink_blocks = (a->sinks + block_size - 1) / block_size;
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
@@ -559,95 +581,278 @@ kv_status_t kv_rope_create(const kv_rope_config_t* c, kv_rope_t** out) {
 
 void kv_rope_destroy(kv_rope_t* r) { delete r; }
 
-kv_status_t kv_append_rope(kv_pool_t* p, int layer, const kv_rope_t* rope, const int32_t* seq_ids, int n_tokens,
-                           const void* k, int64_t k_stride, const void* v, int64_t v_stride, kv_dtype_t src_dtype,
-                           const int32_t* slot_mapping, const int32_t* positions, int64_t positions_stride,
-                           const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int num_q_heads,
-                           float k_scale, float v_scale, void* stream) {
-    if (!p || !rope) return fail(KV_ERR_INVALID_ARG, "kv_append_rope: null pool or rope");
-    if (n_tokens < 0) return fail(KV_ERR_INVALID_ARG, "kv_append_rope: n_tokens %d", n_tokens);
+// The checks and arguments that kv_append_rope and kv_append_norm_rope (`what`)
+// share.  *align: the largest power of two that divides the address of every
+// token's rows.  n_tokens 0: nothing but the first checks, *a stays as it is.
+static kv_status_t rope_args(const char* what, kv_pool_t* p, int layer, const kv_rope_t* rope, const int32_t* seq_ids,
+                             int n_tokens, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             kv_dtype_t src_dtype, const int32_t* slot_mapping, const int32_t* positions,
+                             int64_t positions_stride, const void* q, int64_t q_stride, void* q_out,
+                             int64_t q_out_stride, int num_q_heads, float k_scale, float v_scale, RopeArgs* a,
+                             int* align) {
+    if (!p || !rope) return fail(KV_ERR_INVALID_ARG, "%s: null pool or rope", what);
+    if (n_tokens < 0) return fail(KV_ERR_INVALID_ARG, "%s: n_tokens %d", what, n_tokens);
     const int D = p->cfg.head_dim, Hkv = p->cfg.num_kv_heads;
     const bool quant = p->cfg.dtype == KV_FP8_E4M3;
-    if (!valid_dtype(src_dtype)) return fail(KV_ERR_INVALID_ARG, "kv_append_rope: source dtype %d", src_dtype);
+    if (!valid_dtype(src_dtype)) return fail(KV_ERR_INVALID_ARG, "%s: source dtype %d", what, src_dtype);
     if (!quant && src_dtype != p->cfg.dtype)
-        return fail(KV_ERR_INVALID_ARG, "kv_append_rope: rows must have the pool's dtype (or the pool be E4M3)");
+        return fail(KV_ERR_INVALID_ARG, "%s: rows must have the pool's dtype (or the pool be E4M3)", what);
     if (quant && (!valid_scale(k_scale) || !valid_scale(v_scale)))
-        return fail(KV_ERR_INVALID_ARG, "kv_append_rope: scales must be finite and > 0");
+        return fail(KV_ERR_INVALID_ARG, "%s: scales must be finite and > 0", what);
     if (rope->rot_dim > D)
-        return fail(KV_ERR_INVALID_ARG, "kv_append_rope: rot_dim %d > head_dim %d", rope->rot_dim, D);
+        return fail(KV_ERR_INVALID_ARG, "%s: rot_dim %d > head_dim %d", what, rope->rot_dim, D);
     void *kc = nullptr, *vc = nullptr;
     if (kv_status_t st = kv_pool_layer(p, layer, &kc, &vc)) return st;
     if (!q) num_q_heads = 0;
     if (num_q_heads < 0 || (q && num_q_heads == 0))
-        return fail(KV_ERR_INVALID_ARG, "kv_append_rope: %d query heads", num_q_heads);
+        return fail(KV_ERR_INVALID_ARG, "%s: %d query heads", what, num_q_heads);
     if (n_tokens == 0) return KV_OK;
     if (!k || !v || !slot_mapping || !positions || (q && !q_out))
-        return fail(KV_ERR_INVALID_ARG, "kv_append_rope: null pointer");
+        return fail(KV_ERR_INVALID_ARG, "%s: null pointer", what);
     const int eb = dtype_bytes(src_dtype);
     const int64_t krow = static_cast<int64_t>(Hkv) * D, qrow = static_cast<int64_t>(num_q_heads) * D;
     if (krow >= (int64_t{1} << 31) || qrow >= (int64_t{1} << 31))
-        return fail(KV_ERR_UNSUPPORTED, "kv_append_rope: more than 2^31 elements a token");
+        return fail(KV_ERR_UNSUPPORTED, "%s: more than 2^31 elements a token", what);
     if (n_tokens > 1 && (k_stride < krow || v_stride < krow || (q && (q_stride < qrow || q_out_stride < qrow))))
-        return fail(KV_ERR_INVALID_ARG, "kv_append_rope: a stride is shorter than a token's rows");
+        return fail(KV_ERR_INVALID_ARG, "%s: a stride is shorter than a token's rows", what);
     if (rope->num_axes > 1 && positions_stride != 0 && positions_stride < n_tokens)
-        return fail(KV_ERR_INVALID_ARG, "kv_append_rope: positions_stride %lld (0, or from %d tokens on)",
+        return fail(KV_ERR_INVALID_ARG, "%s: positions_stride %lld (0, or from %d tokens on)", what,
                     static_cast<long long>(positions_stride), n_tokens);
     if (!aligned(k, eb) || !aligned(v, eb) || (q && (!aligned(q, eb) || !aligned(q_out, eb))) ||
         !aligned(slot_mapping, 4) || !aligned(positions, 4) || !aligned(seq_ids, 4))
-        return fail(KV_ERR_INVALID_ARG, "kv_append_rope: a pointer is not aligned to its type");
+        return fail(KV_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", what);
     if (q) {
         const bool in_place = q == q_out && (n_tokens == 1 || q_stride == q_out_stride);
         if ((!in_place && rows_overlap(q, q_stride * eb, qrow * eb, q_out, q_out_stride * eb, qrow * eb, n_tokens)) ||
             rows_overlap(k, k_stride * eb, krow * eb, q_out, q_out_stride * eb, qrow * eb, n_tokens) ||
             rows_overlap(v, v_stride * eb, krow * eb, q_out, q_out_stride * eb, qrow * eb, n_tokens))
-            return fail(KV_ERR_INVALID_ARG, "kv_append_rope: q_out overlaps q (other than in place), k or v");
+            return fail(KV_ERR_INVALID_ARG, "%s: q_out overlaps q (other than in place), k or v", what);
     }
-    DeviceGuard g(p->cfg.device);
-    if (!g.ok) return fail(KV_ERR_CUDA, "cannot select device %d", p->cfg.device);
-    uint32_t* status = nullptr;
-    int sms = 0;
-    if (kv_status_t st = device_info(nullptr, &status, &sms, nullptr, nullptr)) return st;
-    RopeArgs a{};
-    a.seq_ids = seq_ids;
-    a.slot_mapping = slot_mapping;
-    a.positions = positions;
-    a.q = q;
-    a.q_out = q_out;
-    a.k = k;
-    a.v = v;
-    a.k_cache = kc;
-    a.v_cache = vc;
-    a.status = status;
-    a.q_stride = q_stride;
-    a.q_out_stride = q_out_stride;
-    a.k_stride = k_stride;
-    a.v_stride = v_stride;
-    a.positions_stride = positions_stride;
-    a.n_tokens = n_tokens;
-    a.num_q_heads = num_q_heads;
-    a.num_kv_heads = Hkv;
-    a.head_dim = D;
-    a.rot_dim = rope->rot_dim;
-    a.block_size = p->cfg.block_size;
-    a.num_blocks = p->cfg.num_blocks;
-    a.src_dtype = src_dtype;
-    a.quant = quant ? 1 : 0;
-    a.interleaved = rope->interleaved;
-    a.pdl = 1;
-    a.k_scale = k_scale;
-    a.v_scale = v_scale;
-    a.amplitude = rope->amplitude;
-    memcpy(a.phase, rope->phase, sizeof a.phase);
-    memcpy(a.axis, rope->axis, sizeof a.axis);
+    a->seq_ids = seq_ids;
+    a->slot_mapping = slot_mapping;
+    a->positions = positions;
+    a->q = q;
+    a->q_out = q_out;
+    a->k = k;
+    a->v = v;
+    a->k_cache = kc;
+    a->v_cache = vc;
+    a->q_stride = q_stride;
+    a->q_out_stride = q_out_stride;
+    a->k_stride = k_stride;
+    a->v_stride = v_stride;
+    a->positions_stride = positions_stride;
+    a->n_tokens = n_tokens;
+    a->num_q_heads = num_q_heads;
+    a->num_kv_heads = Hkv;
+    a->head_dim = D;
+    a->rot_dim = rope->rot_dim;
+    a->block_size = p->cfg.block_size;
+    a->num_blocks = p->cfg.num_blocks;
+    a->src_dtype = src_dtype;
+    a->quant = quant ? 1 : 0;
+    a->interleaved = rope->interleaved;
+    a->pdl = 1;
+    a->k_scale = k_scale;
+    a->v_scale = v_scale;
+    a->amplitude = rope->amplitude;
+    memcpy(a->phase, rope->phase, sizeof a->phase);
+    memcpy(a->axis, rope->axis, sizeof a->axis);
     uintptr_t bits = 16 | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v);
     if (n_tokens > 1) bits |= static_cast<uintptr_t>(k_stride * eb) | static_cast<uintptr_t>(v_stride * eb);
     if (q) {
         bits |= reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(q_out);
         if (n_tokens > 1) bits |= static_cast<uintptr_t>(q_stride * eb) | static_cast<uintptr_t>(q_out_stride * eb);
     }
-    const int align = static_cast<int>(bits & (~bits + 1));
+    *align = static_cast<int>(bits & (~bits + 1));
+    return KV_OK;
+}
+
+kv_status_t kv_append_rope(kv_pool_t* p, int layer, const kv_rope_t* rope, const int32_t* seq_ids, int n_tokens,
+                           const void* k, int64_t k_stride, const void* v, int64_t v_stride, kv_dtype_t src_dtype,
+                           const int32_t* slot_mapping, const int32_t* positions, int64_t positions_stride,
+                           const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int num_q_heads,
+                           float k_scale, float v_scale, void* stream) {
+    RopeArgs a{};
+    int align = 0, sms = 0;
+    if (kv_status_t st = rope_args("kv_append_rope", p, layer, rope, seq_ids, n_tokens, k, k_stride, v, v_stride,
+                                   src_dtype, slot_mapping, positions, positions_stride, q, q_stride, q_out,
+                                   q_out_stride, num_q_heads, k_scale, v_scale, &a, &align))
+        return st;
+    if (n_tokens == 0) return KV_OK;
+    DeviceGuard g(p->cfg.device);
+    if (!g.ok) return fail(KV_ERR_CUDA, "cannot select device %d", p->cfg.device);
+    if (kv_status_t st = device_info(nullptr, &a.status, &sms, nullptr, nullptr)) return st;
     cudaError_t e = launch_append_rope(a, align, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rope append launch");
+    return KV_OK;
+}
+
+kv_status_t kv_append_norm_rope(kv_pool_t* p, int layer, const kv_rope_t* rope, const int32_t* seq_ids, int n_tokens,
+                                const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                kv_dtype_t src_dtype, const int32_t* slot_mapping, const int32_t* positions,
+                                int64_t positions_stride, const void* q, int64_t q_stride, void* q_out,
+                                int64_t q_out_stride, int num_q_heads, const void* q_weight,
+                                int64_t q_weight_stride, const void* k_weight, int64_t k_weight_stride,
+                                kv_dtype_t weight_dtype, float eps, float k_scale, float v_scale, void* stream) {
+    const char* what = "kv_append_norm_rope";
+    NormRopeArgs a{};
+    int align = 0, sms = 0;
+    if (kv_status_t st = rope_args(what, p, layer, rope, seq_ids, n_tokens, k, k_stride, v, v_stride, src_dtype,
+                                   slot_mapping, positions, positions_stride, q, q_stride, q_out, q_out_stride,
+                                   num_q_heads, k_scale, v_scale, &a, &align))
+        return st;
+    const int D = p->cfg.head_dim;
+    if (weight_dtype != KV_F32 && weight_dtype != src_dtype)
+        return fail(KV_ERR_INVALID_ARG, "%s: weights must be KV_F32 or have the rows' dtype", what);
+    if (!std::isfinite(eps) || eps < 0.f) return fail(KV_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", what);
+    if (!q) q_weight = nullptr;
+    const int wb = dtype_bytes(weight_dtype);
+    uintptr_t wbits = 16;
+    const struct {
+        const void* w;
+        int64_t stride;
+        int heads;
+    } weights[2] = {{q_weight, q_weight_stride, num_q_heads}, {k_weight, k_weight_stride, p->cfg.num_kv_heads}};
+    for (const auto& x : weights) {
+        if (!x.w) continue;
+        if (!aligned(x.w, wb)) return fail(KV_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", what);
+        if (x.heads > 1 && x.stride != 0 && x.stride < D)
+            return fail(KV_ERR_INVALID_ARG, "%s: a weight stride of %lld (0, or from head_dim on)", what,
+                        static_cast<long long>(x.stride));
+        wbits |= reinterpret_cast<uintptr_t>(x.w) | static_cast<uintptr_t>(x.heads > 1 ? x.stride * wb : 0);
+    }
+    if (n_tokens == 0) return KV_OK;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.q_weight_stride = num_q_heads > 1 ? q_weight_stride : 0;
+    a.k_weight_stride = p->cfg.num_kv_heads > 1 ? k_weight_stride : 0;
+    a.wide_weights = weight_dtype != src_dtype;
+    a.eps = eps;
+    DeviceGuard g(p->cfg.device);
+    if (!g.ok) return fail(KV_ERR_CUDA, "cannot select device %d", p->cfg.device);
+    if (kv_status_t st = device_info(nullptr, &a.status, &sms, nullptr, nullptr)) return st;
+    cudaError_t e = launch_append_norm_rope(a, align, static_cast<int>(wbits & (~wbits + 1)), sms,
+                                            static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "norm and rope append launch");
+    return KV_OK;
+}
+
+static kv_status_t check_tables(const char* what, int num_seqs, int max_blocks, int block_size, int num_blocks) {
+    if (num_seqs < 0 || max_blocks <= 0 || block_size <= 0 || num_blocks <= 0)
+        return fail(KV_ERR_INVALID_ARG, "%s: sizes out of range", what);
+    if (num_seqs > kMaxTableSeqs)
+        return fail(KV_ERR_UNSUPPORTED, "%s: %d sequences (at most %d)", what, num_seqs, kMaxTableSeqs);
+    if (static_cast<int64_t>(num_blocks) * block_size >= (int64_t{1} << 31) ||
+        static_cast<int64_t>(max_blocks) * block_size >= (int64_t{1} << 31))
+        return fail(KV_ERR_UNSUPPORTED, "%s: slots or positions do not fit in int32", what);
+    return KV_OK;
+}
+
+// Whether n words at p and m words at o can touch one another.
+static bool words_overlap(const int32_t* p, int64_t n, const int32_t* o, int64_t m) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o);
+    return a < b + 4 * static_cast<uintptr_t>(m) && b < a + 4 * static_cast<uintptr_t>(n);
+}
+
+kv_status_t kv_tables_extend(int32_t* block_tables, int max_blocks, const int32_t* cached_lens,
+                             const int32_t* new_lens, int num_seqs, int block_size, int num_blocks,
+                             const int32_t* free_queue, const int32_t* queue_state, int num_tokens,
+                             int32_t* context_lens, int32_t* query_start, int32_t* slot_mapping,
+                             int32_t* positions, int32_t* seq_ids, int32_t* queue_state_out, void* stream) {
+    const char* what = "kv_tables_extend";
+    if (kv_status_t st = check_tables(what, num_seqs, max_blocks, block_size, num_blocks)) return st;
+    if (num_tokens < 0) return fail(KV_ERR_INVALID_ARG, "%s: num_tokens %d", what, num_tokens);
+    if (!free_queue || !queue_state || !query_start || !queue_state_out ||
+        (num_seqs > 0 && (!block_tables || !cached_lens || !new_lens || !context_lens)) ||
+        (num_tokens > 0 && (!slot_mapping || !positions || !seq_ids)))
+        return fail(KV_ERR_INVALID_ARG, "%s: null pointer", what);
+    const int64_t B = num_seqs, T = num_tokens, M = static_cast<int64_t>(num_seqs) * max_blocks;
+    // What is written, and what is read besides: no two may touch, but for an
+    // input that is updated in place.
+    const struct {
+        const int32_t* p;
+        int64_t n;
+        const int32_t* may_be;  // the input that this output may stand in place of
+    } out[7] = {{block_tables, M, nullptr},    {context_lens, B, cached_lens}, {query_start, B + 1, nullptr},
+                {slot_mapping, T, nullptr},    {positions, T, nullptr},        {seq_ids, T, nullptr},
+                {queue_state_out, 2, queue_state}};
+    const struct {
+        const int32_t* p;
+        int64_t n;
+    } in[4] = {{cached_lens, B}, {new_lens, B}, {free_queue, num_blocks}, {queue_state, 2}};
+    for (int i = 0; i < 7; ++i) {
+        if (!aligned(out[i].p, 4)) return fail(KV_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", what);
+        if (out[i].n == 0) continue;
+        for (int j = 0; j < i; ++j)
+            if (out[j].n > 0 && words_overlap(out[i].p, out[i].n, out[j].p, out[j].n))
+                return fail(KV_ERR_INVALID_ARG, "%s: two outputs overlap", what);
+        for (const auto& x : in)
+            if (x.n > 0 && !(x.p == out[i].p && x.p == out[i].may_be) && words_overlap(out[i].p, out[i].n, x.p, x.n))
+                return fail(KV_ERR_INVALID_ARG, "%s: an output overlaps an input that it cannot stand in place of", what);
+    }
+    for (const auto& x : in)
+        if (!aligned(x.p, 4)) return fail(KV_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", what);
+    TablesArgs a{};
+    if (kv_status_t st = device_info(&a.device, &a.status, nullptr, nullptr, nullptr)) return st;
+    a.block_tables = block_tables;
+    a.cached_lens = cached_lens;
+    a.new_lens = new_lens;
+    a.free_queue = free_queue;
+    a.queue_state = queue_state;
+    a.context_lens = context_lens;
+    a.query_start = query_start;
+    a.slot_mapping = slot_mapping;
+    a.positions = positions;
+    a.seq_ids = seq_ids;
+    a.queue_state_out = queue_state_out;
+    a.num_seqs = num_seqs;
+    a.max_blocks = max_blocks;
+    a.block_size = block_size;
+    a.num_blocks = num_blocks;
+    a.num_tokens = num_tokens;
+    cudaError_t e = launch_tables_extend(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "tables launch");
+    return KV_OK;
+}
+
+kv_status_t kv_tables_release(int32_t* block_tables, int max_blocks, int32_t* context_lens, int num_seqs,
+                              int block_size, int num_blocks, const int32_t* finished, int window, int sinks,
+                              int32_t* free_queue, int32_t* queue_state, void* stream) {
+    const char* what = "kv_tables_release";
+    if (kv_status_t st = check_tables(what, num_seqs, max_blocks, block_size, num_blocks)) return st;
+    if (window < 0 || sinks < 0) return fail(KV_ERR_INVALID_ARG, "%s: window %d, sinks %d", what, window, sinks);
+    if (num_seqs == 0) return KV_OK;
+    if (!block_tables || !context_lens || !free_queue || !queue_state)
+        return fail(KV_ERR_INVALID_ARG, "%s: null pointer", what);
+    const int64_t B = num_seqs, M = B * max_blocks;
+    const struct {
+        const int32_t* p;
+        int64_t n;
+    } all[5] = {{block_tables, M}, {context_lens, B}, {free_queue, num_blocks}, {queue_state, 2}, {finished, B}};
+    for (int i = 0; i < 5; ++i) {
+        if (!all[i].p) continue;
+        if (!aligned(all[i].p, 4)) return fail(KV_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", what);
+        for (int j = 0; j < i; ++j)
+            if (words_overlap(all[i].p, all[i].n, all[j].p, all[j].n))
+                return fail(KV_ERR_INVALID_ARG, "%s: two buffers overlap", what);
+    }
+    TablesArgs a{};
+    if (kv_status_t st = device_info(&a.device, &a.status, nullptr, nullptr, nullptr)) return st;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.finished = finished;
+    a.queue_state = queue_state;
+    a.free_queue_out = free_queue;
+    a.queue_state_out = queue_state;
+    a.num_seqs = num_seqs;
+    a.max_blocks = max_blocks;
+    a.block_size = block_size;
+    a.num_blocks = num_blocks;
+    a.window = window;
+    a.sinks = sinks;
+    cudaError_t e = launch_tables_release(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "tables launch");
     return KV_OK;
 }
 
@@ -704,7 +909,7 @@ static kv_status_t decode_impl(const void* q, const void* k_cache, const void* v
                                const kv_decode_options_t* opts, void* stream, const void* k_new,
                                const void* v_new, const int32_t* append_ids, int32_t* slot_out,
                                kv_dtype_t kv_dtype, float k_scale, float v_scale,
-                               bool clear_counters = false) {
+                               bool clear_counters = false, const Sight* sight = nullptr) {
     const bool fp8 = kv_dtype == KV_FP8_E4M3;
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_blocks <= 0 || max_blocks <= 0)
         return fail(KV_ERR_INVALID_ARG, "paged_decode_attention: sizes out of range");
@@ -730,6 +935,9 @@ static kv_status_t decode_impl(const void* q, const void* k_cache, const void* v
     if (out_dtype != KV_F32 && out_dtype != dtype)
         return fail(KV_ERR_UNSUPPORTED, "out_dtype must be KV_F32 or the input dtype");
     if (!std::isfinite(scale)) return fail(KV_ERR_INVALID_ARG, "scale is not finite");
+    if (sight) {
+        if (kv_status_t st = check_sight(*sight, max_blocks, block_size)) return st;
+    }
     if (static_cast<int64_t>(num_seqs) * num_kv_heads * max_blocks >= (int64_t{1} << 31) ||
         static_cast<int64_t>(num_blocks) * num_kv_heads * block_size >= (int64_t{1} << 31))
         return fail(KV_ERR_UNSUPPORTED, "sizes exceed 32-bit tile / row indices");
@@ -782,12 +990,18 @@ static kv_status_t decode_impl(const void* q, const void* k_cache, const void* v
         if (share < budget) budget = share;
     }
     DecodePlan plan{};
-    const bool planned = plan_warps(kernel, kv_dtype, head_dim, block_size, G, num_seqs, hc, budget,
-                                    o.consumer_warps != 0, &R, &plan);
+    const bool planned = plan_warps(kernel, kv_dtype, head_dim, block_size, G, sight ? 2 * num_seqs : num_seqs,
+                                    hc, budget, o.consumer_warps != 0, &R, &plan);
     if (!planned) return fail(KV_ERR_UNSUPPORTED, "shared memory cannot hold two stages for these sizes");
 
     char* ws = static_cast<char*>(workspace);
-    DecodeArgs a{};
+    WindowArgs a{};
+    int row_blocks = max_blocks;  // the most that one query reads
+    if (sight) {
+        set_sight(*sight, max_blocks, block_size, &a);
+        const int64_t seen = int64_t{a.sink_blocks} + a.window / block_size + 2;
+        if (seen < row_blocks) row_blocks = static_cast<int>(seen);
+    }
     a.q = q;
     a.k_cache = k_cache;
     a.v_cache = v_cache;
@@ -823,7 +1037,7 @@ static kv_status_t decode_impl(const void* q, const void* k_cache, const void* v
     a.pdl = o.no_pdl ? 0 : 1;
     a.early_reads = (o.early_reads && !o.no_pdl) ? 1 : 0;
     a.test_stall = o.test_stall;
-    a.phantom = phantom_items(num_seqs, num_kv_heads / hc, max_blocks, P, plan.stage_half_bytes);
+    a.phantom = phantom_items(num_seqs, num_kv_heads / hc, row_blocks, P, plan.stage_half_bytes);
     a.device = dev;
     a.k_new = k_new;
     a.v_new = v_new;
@@ -842,7 +1056,9 @@ static kv_status_t decode_impl(const void* q, const void* k_cache, const void* v
         e = cudaMemsetAsync(ws + wl.counters, 0, static_cast<size_t>(num_seqs) * num_kv_heads * 4, s);
         if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
     }
-    if (kernel == KV_KERNEL_MMA) {
+    if (sight) {
+        e = kernel == KV_KERNEL_MMA ? launch_window_decode_mma(a, tk, tv, s) : launch_window_decode_ffma(a, s);
+    } else if (kernel == KV_KERNEL_MMA) {
         e = fp8 ? launch_decode_fp8(a, tk, tv, s) : launch_decode_mma(a, tk, tv, s);
     } else {
         e = launch_decode_ffma(a, s);
@@ -915,6 +1131,34 @@ kv_status_t paged_decode_append_attention_fp8(const void* q, const void* k_new, 
                        KV_FP8_E4M3, k_scale, v_scale);
 }
 
+kv_status_t paged_window_decode_attention(const void* q, const void* k_cache, const void* v_cache, int num_blocks,
+                                          const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
+                                          int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                          int block_size, kv_dtype_t dtype, float scale, int window, int sinks,
+                                          void* out, kv_dtype_t out_dtype, void* workspace, size_t workspace_bytes,
+                                          const kv_decode_options_t* opts, void* stream) {
+    const Sight sight{window, sinks};
+    return decode_impl(q, k_cache, v_cache, num_blocks, block_tables, max_blocks, context_lens, num_seqs,
+                       num_q_heads, num_kv_heads, head_dim, block_size, dtype, scale, out, out_dtype,
+                       workspace, workspace_bytes, opts, stream, nullptr, nullptr, nullptr, nullptr,
+                       dtype, 1.f, 1.f, false, &sight);
+}
+
+kv_status_t paged_window_decode_attention_fp8(const void* q, kv_dtype_t q_dtype, const void* k_cache,
+                                              const void* v_cache, float k_scale, float v_scale, int num_blocks,
+                                              const int32_t* block_tables, int max_blocks,
+                                              const int32_t* context_lens, int num_seqs, int num_q_heads,
+                                              int num_kv_heads, int head_dim, int block_size, float scale,
+                                              int window, int sinks, void* out, kv_dtype_t out_dtype,
+                                              void* workspace, size_t workspace_bytes,
+                                              const kv_decode_options_t* opts, void* stream) {
+    const Sight sight{window, sinks};
+    return decode_impl(q, k_cache, v_cache, num_blocks, block_tables, max_blocks, context_lens, num_seqs,
+                       num_q_heads, num_kv_heads, head_dim, block_size, q_dtype, scale, out, out_dtype,
+                       workspace, workspace_bytes, opts, stream, nullptr, nullptr, nullptr, nullptr,
+                       KV_FP8_E4M3, k_scale, v_scale, false, &sight);
+}
+
 // ------------------------------------------------------ multi-token queries
 size_t paged_prefill_workspace_bytes(int num_seqs) {
     if (num_seqs < 0) return 0;
@@ -952,7 +1196,8 @@ static kv_status_t prefill_impl(const void* q, const void* k_cache, const void* 
                                 const int32_t* context_lens, int num_seqs, int num_tokens, int num_q_heads,
                                 int num_kv_heads, int head_dim, int block_size, kv_dtype_t dtype,
                                 kv_dtype_t kv_dtype, float k_scale, float v_scale, float scale, void* out,
-                                kv_dtype_t out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+                                kv_dtype_t out_dtype, void* workspace, size_t workspace_bytes, void* stream,
+                                const Sight* sight = nullptr) {
     const bool fp8 = kv_dtype == KV_FP8_E4M3;
     if (num_seqs < 0 || num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_blocks <= 0 ||
         max_blocks <= 0)
@@ -982,6 +1227,9 @@ static kv_status_t prefill_impl(const void* q, const void* k_cache, const void* 
     if (out_dtype != KV_F32 && out_dtype != dtype)
         return fail(KV_ERR_UNSUPPORTED, "out_dtype must be KV_F32 or the input dtype");
     if (!std::isfinite(scale)) return fail(KV_ERR_INVALID_ARG, "scale is not finite");
+    if (sight) {
+        if (kv_status_t st = check_sight(*sight, max_blocks, block_size)) return st;
+    }
     if (static_cast<int64_t>(num_blocks) * num_kv_heads * block_size >= (int64_t{1} << 31))
         return fail(KV_ERR_UNSUPPORTED, "sizes exceed 32-bit row indices");
     if (num_seqs == 0 || num_tokens == 0) return KV_OK;
@@ -997,7 +1245,7 @@ static kv_status_t prefill_impl(const void* q, const void* k_cache, const void* 
     uint32_t* status = nullptr;
     if (kv_status_t st = device_info(&dev, &status, nullptr, &max_smem, nullptr)) return st;
     // The tcgen05 kernel: f16/bf16 cache, head_dim 128, blocks that tile 64-key tiles evenly.
-    const bool tc = !fp8 && dtype != KV_F32 && head_dim == 128 &&
+    const bool tc = !sight && !fp8 && dtype != KV_F32 && head_dim == 128 &&
                     (block_size % 64 == 0 || 64 % block_size == 0) && prefill_tc_smem_bytes() <= max_smem;
     // Stages of the warp-MMA kernel hold K and V in q's 2-byte type (an E4M3
     // block converted); E4M3 adds two raw slots of codes.
@@ -1007,6 +1255,7 @@ static kv_status_t prefill_impl(const void* q, const void* k_cache, const void* 
     if (stages > 4) stages = 4;
     if (!tc && dtype != KV_F32 && stages < 2) return fail(KV_ERR_UNSUPPORTED, "shared memory cannot hold two stages");
     PrefillArgs a{};
+    if (sight) set_sight(*sight, max_blocks, block_size, &a);
     a.q = q;
     a.k_cache = k_cache;
     a.v_cache = v_cache;
@@ -1076,6 +1325,49 @@ kv_status_t paged_prefill_attention_fp8(const void* q, kv_dtype_t q_dtype, const
     return prefill_impl(q, k_cache, v_cache, num_blocks, block_tables, max_blocks, query_start, context_lens,
                         num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, q_dtype,
                         KV_FP8_E4M3, k_scale, v_scale, scale, out, out_dtype, workspace, workspace_bytes, stream);
+}
+
+// The workspace has room for what the sizes may need later; today it is the
+// prefix of tiles alone.
+kv_status_t paged_window_prefill_workspace_bytes(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads,
+                                                 int head_dim, int device, size_t* bytes) {
+    if (!bytes) return fail(KV_ERR_INVALID_ARG, "null bytes_out");
+    if (num_seqs < 0 || num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || device < 0 ||
+        num_q_heads % num_kv_heads)
+        return fail(KV_ERR_INVALID_ARG, "workspace: sizes out of range");
+    *bytes = paged_prefill_workspace_bytes(num_seqs);
+    return KV_OK;
+}
+
+kv_status_t paged_window_prefill_attention(const void* q, const void* k_cache, const void* v_cache, int num_blocks,
+                                           const int32_t* block_tables, int max_blocks, const int32_t* query_start,
+                                           const int32_t* context_lens, int num_seqs, int num_tokens,
+                                           int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                           kv_dtype_t dtype, float scale, int window, int sinks, void* out,
+                                           kv_dtype_t out_dtype, void* workspace, size_t workspace_bytes,
+                                           void* stream) {
+    if (dtype == KV_FP8_E4M3)
+        return fail(KV_ERR_INVALID_ARG,
+                    "paged_window_prefill_attention: an E4M3 cache goes to paged_window_prefill_attention_fp8");
+    const Sight sight{window, sinks};
+    return prefill_impl(q, k_cache, v_cache, num_blocks, block_tables, max_blocks, query_start, context_lens,
+                        num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, dtype, dtype, 1.f,
+                        1.f, scale, out, out_dtype, workspace, workspace_bytes, stream, &sight);
+}
+
+kv_status_t paged_window_prefill_attention_fp8(const void* q, kv_dtype_t q_dtype, const void* k_cache,
+                                               const void* v_cache, float k_scale, float v_scale, int num_blocks,
+                                               const int32_t* block_tables, int max_blocks,
+                                               const int32_t* query_start, const int32_t* context_lens,
+                                               int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads,
+                                               int head_dim, int block_size, float scale, int window, int sinks,
+                                               void* out, kv_dtype_t out_dtype, void* workspace,
+                                               size_t workspace_bytes, void* stream) {
+    const Sight sight{window, sinks};
+    return prefill_impl(q, k_cache, v_cache, num_blocks, block_tables, max_blocks, query_start, context_lens,
+                        num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, q_dtype,
+                        KV_FP8_E4M3, k_scale, v_scale, scale, out, out_dtype, workspace, workspace_bytes, stream,
+                        &sight);
 }
 
 // ------------------------------------------------------- shared prefixes

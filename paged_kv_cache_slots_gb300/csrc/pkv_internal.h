@@ -60,6 +60,15 @@ struct RopeArgs {
     uint8_t axis[kMaxRopePairs];    // axis whose position turns each pair
 };
 
+// The same with the norms of query and key rows before the rotation (norm_rope.cu).
+struct NormRopeArgs : RopeArgs {
+    const void* q_weight;  // [heads] x head_dim, q_weight_stride elements apart (0: one for all), or nullptr: 1
+    const void* k_weight;
+    int64_t q_weight_stride, k_weight_stride;
+    int wide_weights;      // weights are f32, the rows are not
+    float eps;
+};
+
 // Block swap between the pool and a device-addressable host buffer.
 struct SwapArgs {
     char* pool;               // pool base: layer l's K at 2l * layer_bytes, V at (2l + 1) * layer_bytes
@@ -80,6 +89,29 @@ struct SlotArgs {
     uint32_t* status;
     int max_blocks, num_seqs, block_size, num_blocks;
     int pdl;
+};
+
+// Block tables and slots from request lengths, and blocks given back (tables.cu).
+constexpr int kMaxTableSeqs = 8192;
+
+struct TablesArgs {
+    int32_t* block_tables;        // [num_seqs][max_blocks]
+    const int32_t* cached_lens;   // [num_seqs]
+    const int32_t* new_lens;      // [num_seqs]
+    const int32_t* free_queue;    // [num_blocks], a ring
+    const int32_t* queue_state;   // front, blocks
+    const int32_t* finished;      // [num_seqs] or nullptr
+    int32_t* context_lens;        // [num_seqs]
+    int32_t* query_start;         // [num_seqs + 1]
+    int32_t* slot_mapping;        // [num_tokens]
+    int32_t* positions;
+    int32_t* seq_ids;
+    int32_t* free_queue_out;      // releasing: free_queue
+    int32_t* queue_state_out;
+    uint32_t* status;
+    int num_seqs, max_blocks, block_size, num_blocks, num_tokens;
+    int window, sinks;            // releasing: see kv_tables_release
+    int device;
 };
 
 // Everything the split-context decode kernels need.
@@ -140,6 +172,15 @@ struct TailArgs : DecodeArgs {
     int4* prefix_parts;          // [num_seqs][Hkv] zeroed for sequences that share nothing
 };
 
+// Attention to a sliding window and the first tokens (see
+// paged_window_decode_attention): position p sees the positions above p - window
+// and those below sinks.  Both are at most what a table row holds.
+struct WindowArgs : DecodeArgs {
+    int window;
+    int sinks;
+    int sink_blocks;  // blocks that hold the first `sinks` tokens
+};
+
 // Multi-token (chunked-prefill) attention and its plan.
 struct PrefillArgs {
     const void* q;               // [T][Hq][D]
@@ -161,6 +202,8 @@ struct PrefillArgs {
     int tensor_cores;  // 1: the tcgen05 kernel (head_dim 128)
     int pdl;
     int device;
+    int window, sinks;  // window > 0: a sliding window (see WindowArgs)
+    int sink_blocks;
 };
 
 // Shared-memory plan of the partial kernel.
@@ -176,10 +219,17 @@ bool decode_plan(int kernel, int dtype, int head_dim, int block_size, int group,
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
 // align: largest power of two that divides the address of every token's rows.
 cudaError_t launch_append_rope(const RopeArgs& a, int align, int num_sms, cudaStream_t stream);
+// weight_align: the same of every head's weights.
+cudaError_t launch_append_norm_rope(const NormRopeArgs& a, int align, int weight_align, int num_sms,
+                                    cudaStream_t stream);
 cudaError_t launch_slot_mapping(const SlotArgs& a, cudaStream_t stream);
+cudaError_t launch_tables_extend(const TablesArgs& a, cudaStream_t stream);
+cudaError_t launch_tables_release(const TablesArgs& a, cudaStream_t stream);
 cudaError_t launch_swap(const SwapArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
                            cudaStream_t stream);
+cudaError_t launch_window_prefill(const PrefillArgs& a, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
+                                  cudaStream_t stream);
 cudaError_t launch_slot_mapping_varlen(const PrefillArgs& a, int32_t* slots, cudaStream_t stream);
 cudaError_t launch_prefill_tc(const PrefillArgs& a, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
                               cudaStream_t stream);
@@ -189,6 +239,9 @@ cudaError_t launch_decode_mma(const DecodeArgs& a, const CUtensorMap& tmap_k,
                               const CUtensorMap& tmap_v, cudaStream_t stream);
 cudaError_t launch_decode_fp8(const DecodeArgs& a, const CUtensorMap& tmap_k,
                               const CUtensorMap& tmap_v, cudaStream_t stream);
+cudaError_t launch_window_decode_mma(const WindowArgs& a, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
+                                     cudaStream_t stream);
+cudaError_t launch_window_decode_ffma(const WindowArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_reduce(const DecodeArgs& a, cudaStream_t stream);
 
 // Largest dynamic shared memory a CTA may request on `device`.
