@@ -244,6 +244,24 @@ kv_status_t encode_cache_map(CUtensorMap* map, const void* base, int dtype, int 
     return KV_OK;
 }
 
+// 3-D view of the query rows [tokens][heads][head_dim]; box = 64 elements x
+// box_heads x box_tokens, 128-byte swizzle.
+kv_status_t encode_query_map(CUtensorMap* map, const void* q, int dtype, int tokens, int heads, int head_dim,
+                             int box_heads, int box_tokens) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return fail(KV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t row = static_cast<cuuint64_t>(head_dim) * 2;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+    cuuint64_t strides[2] = {row, row * heads};
+    cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
+    cuuint32_t estr[3] = {1u, 1u, 1u};
+    CUresult r = enc(map, dtype == KV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                     const_cast<void*>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(KV_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+    return KV_OK;
+}
+
 }  // namespace
 
 kv_status_t pkv::report_error(kv_status_t st, const char* fmt, ...) {
@@ -1191,6 +1209,13 @@ kv_status_t kv_slot_mapping_varlen(const int32_t* block_tables, int max_blocks, 
     return KV_OK;
 }
 
+// The windowed prefill's: the prefix of tiles, and eight words for each tile of the tcgen05 kernel.
+constexpr int kWindowRows = 256;  // rows of its tile: new tokens times query heads of a KV head
+static size_t window_prefill_workspace(int num_seqs, int num_tokens, int G) {
+    const size_t per = G < kWindowRows ? kWindowRows / G : 1;
+    return paged_prefill_workspace_bytes(num_seqs) + align256(((num_tokens + per - 1) / per + num_seqs) * 32);
+}
+
 static kv_status_t prefill_impl(const void* q, const void* k_cache, const void* v_cache, int num_blocks,
                                 const int32_t* block_tables, int max_blocks, const int32_t* query_start,
                                 const int32_t* context_lens, int num_seqs, int num_tokens, int num_q_heads,
@@ -1238,12 +1263,12 @@ static kv_status_t prefill_impl(const void* q, const void* k_cache, const void* 
     if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(q, 16) || !aligned(out, 16) ||
         !aligned(workspace, 16))
         return fail(KV_ERR_INVALID_ARG, "alignment: caches, q, out and the workspace need 16 bytes");
-    if (workspace_bytes < paged_prefill_workspace_bytes(num_seqs))
-        return fail(KV_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes,
-                    paged_prefill_workspace_bytes(num_seqs));
-    int dev = 0, max_smem = 0;
+    const size_t need = sight ? window_prefill_workspace(num_seqs, num_tokens, G) : paged_prefill_workspace_bytes(num_seqs);
+    if (workspace_bytes < need)
+        return fail(KV_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    int dev = 0, sms = 0, max_smem = 0;
     uint32_t* status = nullptr;
-    if (kv_status_t st = device_info(&dev, &status, nullptr, &max_smem, nullptr)) return st;
+    if (kv_status_t st = device_info(&dev, &status, &sms, &max_smem, nullptr)) return st;
     // The tcgen05 kernel: f16/bf16 cache, head_dim 128, blocks that tile 64-key tiles evenly.
     const bool tc = !sight && !fp8 && dtype != KV_F32 && head_dim == 128 &&
                     (block_size % 64 == 0 || 64 % block_size == 0) && prefill_tc_smem_bytes() <= max_smem;
@@ -1253,7 +1278,8 @@ static kv_status_t prefill_impl(const void* q, const void* k_cache, const void* 
     const int raw_bytes = fp8 ? 4 * block_size * head_dim : 0;
     int stages = (max_smem - 2048 - 64 - raw_bytes) / stage_bytes;
     if (stages > 4) stages = 4;
-    if (!tc && dtype != KV_F32 && stages < 2) return fail(KV_ERR_UNSUPPORTED, "shared memory cannot hold two stages");
+    const bool window_tc = sight && !fp8 && dtype != KV_F32;
+    if (!tc && !window_tc && dtype != KV_F32 && stages < 2) return fail(KV_ERR_UNSUPPORTED, "shared memory cannot hold two stages");
     PrefillArgs a{};
     if (sight) set_sight(*sight, max_blocks, block_size, &a);
     a.q = q;
@@ -1284,13 +1310,27 @@ static kv_status_t prefill_impl(const void* q, const void* k_cache, const void* 
                       : fp8 ? 1024 + stages * stage_bytes + 1024 + raw_bytes
                             : 1024 + stages * stage_bytes + stages * 16 + 32;
     a.tensor_cores = tc ? 1 : 0;
-    a.tile_tokens = tc ? 128 / G : 16;
+    a.tile_tokens = window_tc ? kWindowRows / G : tc ? 128 / G : 16;
     const int64_t tiles = (static_cast<int64_t>(num_tokens) + a.tile_tokens - 1) / a.tile_tokens + num_seqs;
     if (tiles >= (int64_t{1} << 31)) return fail(KV_ERR_UNSUPPORTED, "too many query tiles");
     a.grid_tiles = static_cast<int>(tiles);
     a.pdl = 1;
     a.device = dev;
     CUtensorMap tk{}, tv{};
+    if (window_tc) {
+        a.smem_bytes = window_prefill_tc_smem_bytes(head_dim);
+        if (a.smem_bytes > max_smem) return fail(KV_ERR_UNSUPPORTED, "%d bytes of shared memory needed", a.smem_bytes);
+        a.tiles = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + paged_prefill_workspace_bytes(num_seqs));
+        a.box = block_size % 32 ? 16 : 32;
+        const int rows = num_blocks * num_kv_heads * block_size;
+        CUtensorMap tq{};
+        if (kv_status_t st = encode_query_map(&tq, q, dtype, num_tokens, num_q_heads, head_dim, G, 128 / G)) return st;
+        if (kv_status_t st = encode_cache_map(&tk, k_cache, dtype, rows, head_dim, a.box)) return st;
+        if (kv_status_t st = encode_cache_map(&tv, v_cache, dtype, rows, head_dim, a.box)) return st;
+        cudaError_t e = launch_window_prefill_tc(a, tq, tk, tv, sms, static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) return cuda_fail(e, "windowed prefill launch");
+        return KV_OK;
+    }
     if (!fp8 && dtype != KV_F32) {  // E4M3 tiles come by bulk copies, f32 rows by plain loads
         const int rows = num_blocks * num_kv_heads * block_size;
         const int box_rows = tc ? (block_size < 64 ? block_size : 64) : block_size;
@@ -1327,15 +1367,13 @@ kv_status_t paged_prefill_attention_fp8(const void* q, kv_dtype_t q_dtype, const
                         KV_FP8_E4M3, k_scale, v_scale, scale, out, out_dtype, workspace, workspace_bytes, stream);
 }
 
-// The workspace has room for what the sizes may need later; today it is the
-// prefix of tiles alone.
 kv_status_t paged_window_prefill_workspace_bytes(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads,
                                                  int head_dim, int device, size_t* bytes) {
     if (!bytes) return fail(KV_ERR_INVALID_ARG, "null bytes_out");
     if (num_seqs < 0 || num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || device < 0 ||
         num_q_heads % num_kv_heads)
         return fail(KV_ERR_INVALID_ARG, "workspace: sizes out of range");
-    *bytes = paged_prefill_workspace_bytes(num_seqs);
+    *bytes = window_prefill_workspace(num_seqs, num_tokens, num_q_heads / num_kv_heads);
     return KV_OK;
 }
 

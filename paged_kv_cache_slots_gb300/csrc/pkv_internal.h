@@ -204,6 +204,8 @@ struct PrefillArgs {
     int device;
     int window, sinks;  // window > 0: a sliding window (see WindowArgs)
     int sink_blocks;
+    int32_t* tiles;     // windowed tcgen05 kernel: eight words for each tile of tokens
+    int box;            // ... and rows of a K or V box (a power of two that divides block_size)
 };
 
 // Shared-memory plan of the partial kernel.
@@ -230,6 +232,9 @@ cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tmap_k, cons
                            cudaStream_t stream);
 cudaError_t launch_window_prefill(const PrefillArgs& a, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
                                   cudaStream_t stream);
+cudaError_t launch_window_prefill_tc(const PrefillArgs& a, const CUtensorMap& tmap_q, const CUtensorMap& tmap_k,
+                                     const CUtensorMap& tmap_v, int num_sms, cudaStream_t stream);
+int window_prefill_tc_smem_bytes(int head_dim);
 cudaError_t launch_slot_mapping_varlen(const PrefillArgs& a, int32_t* slots, cudaStream_t stream);
 cudaError_t launch_prefill_tc(const PrefillArgs& a, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
                               cudaStream_t stream);

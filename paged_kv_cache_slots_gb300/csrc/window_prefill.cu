@@ -1,24 +1,14 @@
-// Launchers of the warp-MMA kernel of multi-token queries with a sliding window
-// (prefill_mma.cuh).
+// Launchers of the warp-MMA kernel of multi-token queries with a sliding window over
+// an E4M3 cache (prefill_mma.cuh).
 #include "prefill_mma.cuh"
 
 namespace pkv {
 
 cudaError_t launch_window_prefill(const PrefillArgs& a, const CUtensorMap& tmk, const CUtensorMap& tmv,
                                   cudaStream_t stream) {
-    if (a.kv_dtype == kFP8) {
-        if (a.head_dim != 128) return cudaErrorInvalidValue;
-        if (a.dtype == kF16) return launch_prefill_t<kF16, 128, true, true>(a, tmk, tmv, stream);
-        if (a.dtype == kBF16) return launch_prefill_t<kBF16, 128, true, true>(a, tmk, tmv, stream);
-        return cudaErrorInvalidValue;
-    }
-    if (a.dtype == kF16) {
-        if (a.head_dim == 64) return launch_prefill_t<kF16, 64, false, true>(a, tmk, tmv, stream);
-        if (a.head_dim == 128) return launch_prefill_t<kF16, 128, false, true>(a, tmk, tmv, stream);
-    } else if (a.dtype == kBF16) {
-        if (a.head_dim == 64) return launch_prefill_t<kBF16, 64, false, true>(a, tmk, tmv, stream);
-        if (a.head_dim == 128) return launch_prefill_t<kBF16, 128, false, true>(a, tmk, tmv, stream);
-    }
+    if (a.kv_dtype != kFP8 || a.head_dim != 128) return cudaErrorInvalidValue;
+    if (a.dtype == kF16) return launch_prefill_t<kF16, 128, true, true>(a, tmk, tmv, stream);
+    if (a.dtype == kBF16) return launch_prefill_t<kBF16, 128, true, true>(a, tmk, tmv, stream);
     return cudaErrorInvalidValue;
 }
 
