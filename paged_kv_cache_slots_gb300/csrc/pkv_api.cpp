@@ -244,6 +244,24 @@ kv_status_t encode_cache_map(CUtensorMap* map, const void* base, int dtype, int 
     return KV_OK;
 }
 
+// 4-D view of one layer's cache for the windowed prefill: 64 elements, 8 rows, the
+// row's 64-element slices, groups of 8 rows; box = `box_rows` rows with all slices,
+// 128-byte swizzle, so that a box lands group by group, slice by slice within one.
+kv_status_t encode_group_map(CUtensorMap* map, const void* base, int dtype, int rows, int head_dim, int box_rows) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return fail(KV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t row = static_cast<cuuint64_t>(head_dim) * 2;
+    cuuint64_t dims[4] = {64, 8, static_cast<cuuint64_t>(head_dim / 64), static_cast<cuuint64_t>(rows / 8)};
+    cuuint64_t strides[3] = {row, 128, 8 * row};
+    cuuint32_t box[4] = {64u, 8u, static_cast<cuuint32_t>(head_dim / 64), static_cast<cuuint32_t>(box_rows / 8)};
+    cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    CUresult r = enc(map, dtype == KV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                     const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(KV_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+    return KV_OK;
+}
+
 // 3-D view of the query rows [tokens][heads][head_dim]; box = 64 elements x
 // box_heads x box_tokens, 128-byte swizzle.
 kv_status_t encode_query_map(CUtensorMap* map, const void* q, int dtype, int tokens, int heads, int head_dim,
@@ -1325,8 +1343,8 @@ static kv_status_t prefill_impl(const void* q, const void* k_cache, const void* 
         const int rows = num_blocks * num_kv_heads * block_size;
         CUtensorMap tq{};
         if (kv_status_t st = encode_query_map(&tq, q, dtype, num_tokens, num_q_heads, head_dim, G, 128 / G)) return st;
-        if (kv_status_t st = encode_cache_map(&tk, k_cache, dtype, rows, head_dim, a.box)) return st;
-        if (kv_status_t st = encode_cache_map(&tv, v_cache, dtype, rows, head_dim, a.box)) return st;
+        if (kv_status_t st = encode_group_map(&tk, k_cache, dtype, rows, head_dim, a.box)) return st;
+        if (kv_status_t st = encode_group_map(&tv, v_cache, dtype, rows, head_dim, a.box)) return st;
         cudaError_t e = launch_window_prefill_tc(a, tq, tk, tv, sms, static_cast<cudaStream_t>(stream));
         if (e != cudaSuccess) return cuda_fail(e, "windowed prefill launch");
         return KV_OK;

@@ -47,13 +47,15 @@ constexpr int kThreads = 384;  // (warps 10 and 11 fill the third warpgroup and 
 // Registers of a thread of the first two warpgroups and of the third: the launch's
 // 168 each (65,536 over 384 threads) divided anew, 2 x 208 + 88 = 3 x 168.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
-constexpr uint32_t kSlice = kKeys * 128;  // 128 rows of 64 elements: 16 KiB
+constexpr uint32_t kSlice = kRowsTile * 128;  // Q: 128 rows of 64 elements, 16 KiB
+constexpr uint32_t kGroup = 8 * 128;          // 8 rows of 64 elements: the swizzle's atom
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLazy = 8.f;
 
 template <int D>
 struct Layout {
     static constexpr uint32_t kTile = (D / 64) * kSlice;  // Q of a row tile, K or V of 128 keys
+    static constexpr uint32_t kRowGroup = (D / 64) * kGroup;  // K and V: 8 rows of all slices, slice by slice
     static constexpr int kStages = D == 128 ? 5 : 8;
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kRing = 2 * kTile;
@@ -63,10 +65,19 @@ struct Layout {
 template <int kStages>
 struct Bars {
     uint64_t full[kStages], empty[kStages];
-    uint64_t q_full, q_empty;
+    uint64_t q_full[2], q_empty[2];  // of each row tile
     uint64_t s_full[2], p_full[2], o_full[2];
     uint32_t tmem;
     int abort;
+};
+
+// A place in the ring, going round.
+template <int kStages>
+struct Place {
+    uint32_t stage = 0, round = 0;
+    __device__ __forceinline__ Place next() const {
+        return stage + 1 == kStages ? Place{0, round + 1} : Place{stage + 1, round};
+    }
 };
 
 // What an item needs to know, the same in every role.
@@ -93,26 +104,62 @@ __device__ __forceinline__ void tensor_load_3d(void* dst, const CUtensorMap* map
         : "memory");
 }
 
-// Operand descriptors (see tc_sdesc) from their low words: the high word is the
-// same for every operand here (8-row groups 1024 bytes apart, 128-byte swizzle), and
-// a step along an operand adds its bytes / 16 to the low one.
-constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+// Operand descriptors (see tc_sdesc) from their two words: the high one holds the
+// distance of the 8-row groups (and version and swizzle), and a step along an operand
+// adds its bytes / 16 to the low one.
+__host__ __device__ constexpr uint32_t desc_high(uint32_t group_bytes) { return (group_bytes >> 4) | (1u << 14) | (2u << 29); }
 __device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) { return ((addr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16); }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc, bool accumulate) {
+
+// Four MMAs, issued by one elected lane of a converged warp: the whole warp makes the
+// descriptors, so they stay in uniform registers and nothing stands between two
+// issues (an issue returns about when the MMA before it completes; with the loop in
+// a branch of one lane an MMA of 64 cycles took 100).  A and B in shared memory, 32
+// bytes (16 elements) a step:
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint32_t a_low, uint32_t a_high, uint32_t b_low, uint32_t b_high,
+                                        uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %5, 0;\n\t"
-        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d),
-        "r"(a_low), "r"(b_low), "r"(kDescHigh), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        "{\n\t.reg .pred lead, p;\n\t.reg .b64 da, db;\n\t"
+        "elect.sync _|lead, 0xffffffff;\n\t"
+        "setp.ne.u32 p, %6, 0;\n\t"
+        "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+        "@lead tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t"
+        "setp.eq.u32 p, 0, 0;\n\t"
+        "add.s64 da, da, 2;\n\tadd.s64 db, db, 2;\n\t"
+        "@lead tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t"
+        "add.s64 da, da, 2;\n\tadd.s64 db, db, 2;\n\t"
+        "@lead tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t"
+        "add.s64 da, da, 2;\n\tadd.s64 db, db, 2;\n\t"
+        "@lead tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+        "r"(a_low), "r"(a_high), "r"(b_low), "r"(b_high), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, bool accumulate) {
+// A in tensor memory, 8 columns (16 elements) a step; B kStep / 16 further a step.
+template <uint32_t kStep>
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a_tmem, uint32_t b_low, uint32_t b_high, uint32_t idesc,
+                                        uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %5, 0;\n\t"
-        "mov.b64 db, {%2, %3};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
-        "r"(a_tmem), "r"(b_low), "r"(kDescHigh), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        "{\n\t.reg .pred lead, p;\n\t.reg .b64 db;\n\t.reg .b32 ta;\n\t"
+        "elect.sync _|lead, 0xffffffff;\n\t"
+        "setp.ne.u32 p, %5, 0;\n\t"
+        "mov.b32 ta, %1;\n\tmov.b64 db, {%2, %3};\n\t"
+        "@lead tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %4, p;\n\t"
+        "setp.eq.u32 p, 0, 0;\n\t"
+        "add.s32 ta, ta, 8;\n\tadd.s64 db, db, %6;\n\t"
+        "@lead tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %4, p;\n\t"
+        "add.s32 ta, ta, 8;\n\tadd.s64 db, db, %6;\n\t"
+        "@lead tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %4, p;\n\t"
+        "add.s32 ta, ta, 8;\n\tadd.s64 db, db, %6;\n\t"
+        "@lead tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %4, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b_low), "r"(b_high), "r"(idesc), "r"(accumulate), "n"(kStep >> 4)
+        : "memory");
+}
+
+// tc_commit by one elected lane of a converged warp.
+__device__ __forceinline__ void commit_elected(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred lead;\n\telect.sync _|lead, 0xffffffff;\n\t"
+        "@lead tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
         : "memory");
 }
 
@@ -123,6 +170,23 @@ __device__ __forceinline__ void tc_st16u(uint32_t taddr, const uint32_t (&v)[16]
             taddr),
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_ld16(uint32_t taddr, float (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr));
+}
+
+// Rows 8 y .. of a cache, all 64-element slices (the map's third axis).
+__device__ __forceinline__ void tensor_load_4d(void* dst, const CUtensorMap* map, int y, uint64_t* bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %2, %2, %3}], [%4], %5;" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(smem_addr(bar)), "l"(policy)
         : "memory");
 }
 
@@ -175,9 +239,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
             mbar_init(&B->full[i], 1);
             mbar_init(&B->empty[i], 1);
         }
-        mbar_init(&B->q_full, 1);
-        mbar_init(&B->q_empty, 1);
         for (int t = 0; t < 2; ++t) {
+            mbar_init(&B->q_full[t], 1);
+            mbar_init(&B->q_empty[t], 1);
             mbar_init(&B->s_full[t], 1);
             mbar_init(&B->p_full[t], 4);
             mbar_init(&B->o_full[t], 1);
@@ -197,24 +261,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
 
     const int tiles = a.tile_cum[a.num_seqs];
     const int64_t items = static_cast<int64_t>(tiles) * a.num_kv_heads;
-    const int box = a.box;
-    const int per_tile = kKeys / box;  // boxes of a tile
+    const int sh = a.box == 32 ? 5 : 4, box = 1 << sh;
+    const int per_tile = kKeys >> sh;  // boxes of a tile
     auto item_at = [&](int64_t i) {
         Item it;
         it.h = static_cast<int>(i / tiles);
         const int4* d = reinterpret_cast<const int4*>(a.tiles) + 2 * (i - static_cast<int64_t>(it.h) * tiles);
-        const int4 u = d[0], v = d[1];
+        const int4 u = __ldcg(d), v = __ldcg(d + 1);
         it.s = u.x;
         it.tok0 = u.y;
         it.ntok = u.z;
         it.pos0 = u.w;
         it.ctx = v.x;
-        const int lo = max(0, it.pos0 - a.window + 1) / box, sb = (a.sinks + box - 1) / box;
+        const int lo = max(0, it.pos0 - a.window + 1) >> sh, sb = static_cast<int>((static_cast<int64_t>(a.sinks) + box - 1) >> sh);
         const int skip = max(0, lo - sb);
-        it.skip = skip * box;
-        it.sink_keys = sb * box;
-        it.boxes = (it.pos0 + it.ntok - 1) / box + 1 - skip;
-        it.tiles = (it.boxes + per_tile - 1) / per_tile;
+        it.skip = skip << sh;
+        it.sink_keys = static_cast<int>(min(static_cast<int64_t>(sb) << sh, int64_t{0x7fffffff}));
+        it.boxes = ((it.pos0 + it.ntok - 1) >> sh) + 1 - skip;
+        it.tiles = (it.boxes + per_tile - 1) >> (7 - sh);
         return it;
     };
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity & 1u, abort, a.status); };
@@ -224,67 +288,67 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
         if (warp == 8) {
             // ---- producer
             const uint64_t keep = policy_evict_last();
-            uint32_t stage = 0, round = 0, nq = 0;
+            Place<kStages> at;
+            uint32_t nq[2] = {0, 0};
             bool ok = true;
-            // K or V of 128 keys: lane e issues box e / kSlices, slice e % kSlices.
-            auto load = [&](const Item& it, int j, const CUtensorMap* map) -> bool {
-                const int b = j * per_tile + lane / kSlices;
-                const bool mine = lane < per_tile * kSlices && b < it.boxes;
-                int y = 0;
-                if (mine) {
-                    const int cg = b * box;
-                    const int key = cg + (cg >= it.sink_keys ? it.skip : 0);
-                    const int lb = key / a.block_size;
-                    int blk = a.block_tables[static_cast<int64_t>(it.s) * a.max_blocks + lb];
-                    if (blk < 0 || blk >= a.num_blocks) {
-                        raise_flag(a.status, kFlagBadBlock);
-                        blk = 0;
-                    }
-                    y = (blk * a.num_kv_heads + it.h) * a.block_size + (key - lb * a.block_size);
+            // The cache's 8-row group of box `lane` of tile j (the same for K and V); a box lies within a block.
+            auto group_of = [&](const Item& it, int j) {
+                const int b = j * per_tile + lane;
+                if (lane >= per_tile || b >= it.boxes) return 0;
+                const int cg = b << sh;
+                const int key = cg + (cg >= it.sink_keys ? it.skip : 0);
+                const int lb = key / a.block_size;
+                int blk = a.block_tables[static_cast<int64_t>(it.s) * a.max_blocks + lb];
+                if (blk < 0 || blk >= a.num_blocks) {
+                    raise_flag(a.status, kFlagBadBlock);
+                    blk = 0;
                 }
+                return ((blk * a.num_kv_heads + it.h) * a.block_size + (key - lb * a.block_size)) >> 3;
+            };
+            // K or V of a tile: `n` boxes, one a lane.
+            auto load = [&](int n, int y, const CUtensorMap* map) -> bool {
                 int good = 1;
                 if (lane == 0) {
-                    if (round > 0) good = wait(&B->empty[stage], round - 1);
-                    if (good) {
-                        const int n = min(per_tile, it.boxes - j * per_tile);
-                        mbar_arrive_expect_tx(&B->full[stage], static_cast<uint32_t>(n * box) * 128u * kSlices);
-                    }
+                    if (at.round > 0) good = wait(&B->empty[at.stage], at.round - 1);
+                    if (good) mbar_arrive_expect_tx(&B->full[at.stage], static_cast<uint32_t>(n) * (box / 8) * L::kRowGroup);
                 }
                 good = __shfl_sync(0xffffffffu, good, 0);
                 if (!good) return false;
-                if (mine) {
-                    const int sl = lane % kSlices;
-                    tensor_load_2d(base + L::kRing + stage * L::kTile + sl * kSlice + (lane / kSlices) * box * 128, map, sl * 64, y,
-                                   &B->full[stage], keep);
-                }
+                if (lane < n)
+                    tensor_load_4d(base + L::kRing + at.stage * L::kTile + lane * (box / 8) * L::kRowGroup, map, y,
+                                   &B->full[at.stage], keep);
                 __syncwarp();
-                if (++stage == kStages) {
-                    stage = 0;
-                    ++round;
-                }
+                at = at.next();
                 return true;
             };
             for (int64_t i = blockIdx.x; i < items && ok; i += gridDim.x) {
                 const Item it = item_at(i);
                 const int row_tiles = it.ntok > kTileTokens ? 2 : 1;
+                int y = group_of(it, 0);
                 for (int j = 0; j < it.tiles && ok; ++j) {
-                    ok = load(it, j, &tmk) && load(it, j, &tmv);
+                    const int n = min(per_tile, it.boxes - j * per_tile);
+                    const int y_next = group_of(it, j + 1);  // (asked for while this tile's stages become free)
+                    ok = load(n, y, &tmk);
                     if (ok && j == 0) {
-                        // Q, once the S of the item before are done with the buffer.
+                        // A row tile of Q, once the S of the item before are done with its buffer.
                         int good = 1;
                         if (lane == 0) {
-                            if (nq > 0) good = wait(&B->q_empty, nq - 1);
-                            if (good) {
-                                mbar_arrive_expect_tx(&B->q_full, static_cast<uint32_t>(row_tiles) * L::kTile);
-                                for (int t = 0; t < row_tiles; ++t)
-                                    for (int sl = 0; sl < kSlices; ++sl)
-                                        tensor_load_3d(base + L::kQ + t * L::kTile + sl * kSlice, &tmq, sl * 64, it.h * G,
-                                                       static_cast<int>(it.tok0) + t * kTileTokens, &B->q_full, keep);
-                                ++nq;
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+                                if (t >= row_tiles || !good) continue;
+                                if (nq[t] > 0) good = wait(&B->q_empty[t], nq[t] - 1);
+                                if (!good) continue;
+                                mbar_arrive_expect_tx(&B->q_full[t], L::kTile);
+                                for (int sl = 0; sl < kSlices; ++sl)
+                                    tensor_load_3d(base + L::kQ + t * L::kTile + sl * kSlice, &tmq, sl * 64, it.h * G,
+                                                   static_cast<int>(it.tok0) + t * kTileTokens, &B->q_full[t], keep);
+                                ++nq[t];
                             }
                         }
                         ok = __shfl_sync(0xffffffffu, good, 0) != 0;
                     }
+                    ok = ok && load(n, y, &tmv);
+                    y = y_next;
                 }
             }
             // Every copy issued must land before the CTA can exit.
@@ -299,78 +363,93 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                     }
                 };
                 for (uint32_t st = 0; st < kStages; ++st) {
-                    const uint32_t fills = round + (st < stage ? 1u : 0u);
+                    const uint32_t fills = at.round + (st < at.stage ? 1u : 0u);
                     if (fills > 0) drain(&B->full[st], fills - 1);
                 }
-                if (nq > 0) drain(&B->q_full, nq - 1);
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    if (nq[t] > 0) drain(&B->q_full[t], nq[t] - 1);
             }
             __syncwarp();
         } else if (warp == 9) {
-            // ---- MMA issue
-            if (lane == 0) {
-                constexpr int bf = DT == kBF16 ? 1 : 0;
-                constexpr uint32_t idS = tc_idesc_f16(bf, false, kKeys, kRowsTile);
-                constexpr uint32_t idPV = tc_idesc_f16(bf, true, D, kRowsTile);
-                const uint32_t qa = smem_addr(base + L::kQ), ring = smem_addr(base + L::kRing);
-                uint32_t nq = 0, np[2] = {0, 0};
-                uint32_t at = 0;  // ring position of the next stage to be used
-                auto stage_of = [&](uint32_t x) { return x % kStages; };
-                auto ready = [&](uint32_t x) { return wait(&B->full[stage_of(x)], x / kStages); };
-                auto qk = [&](int t, uint32_t x) {
-                    const uint32_t k = desc_low(ring + stage_of(x) * L::kTile, 16), q = desc_low(qa + t * L::kTile, 16);
-    #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t step = ((ks >> 2) * kSlice + (ks & 3) * 32) >> 4;
-                        mma_ss(taddr + t * kKeys, q + step, k + step, idS, ks > 0);
-                    }
-                    tc_commit(&B->s_full[t]);
-                };
-                auto pv = [&](int t, uint32_t x, bool first) {
-                    const uint32_t va = desc_low(ring + stage_of(x) * L::kTile, kSlice);
-    #pragma unroll
-                    for (int part = 0; part < (kTwo ? 2 : 1); ++part)
-    #pragma unroll
-                        for (int kk = 0; kk < kKeys / 16; ++kk)
-                            mma_ts(taddr + 256 + t * 128, taddr + t * kKeys + part * 64 + kk * 8, va + ((kk * 16 * 128) >> 4), idPV,
-                                   !(first && part == 0 && kk == 0));
-                };
-                bool ok = true;
-                for (int64_t i = blockIdx.x; i < items && ok; i += gridDim.x) {
-                    const Item it = item_at(i);
-                    const int row_tiles = it.ntok > kTileTokens ? 2 : 1;
-                    ok = wait(&B->q_full, nq++) && ready(at);
-                    if (!ok) break;
-                    tc_fence_after();
-                    for (int t = 0; t < row_tiles; ++t) qk(t, at);
-                    tc_commit(&B->empty[stage_of(at)]);
-                    if (it.tiles == 1) tc_commit(&B->q_empty);
-                    for (int j = 0; j < it.tiles && ok; ++j) {
-                        const uint32_t v = at + 1, k = at + 2;  // this tile's V, the next one's K
-                        const bool more = j + 1 < it.tiles;
+            // ---- MMA issue: the warp as one, an elected lane where an instruction is one thread's
+            constexpr int bf = DT == kBF16 ? 1 : 0;
+            constexpr uint32_t idS = tc_idesc_f16(bf, false, kKeys, kRowsTile);
+            constexpr uint32_t idPV = tc_idesc_f16(bf, true, D, kRowsTile);
+            const uint32_t qa = smem_addr(base + L::kQ), ring = smem_addr(base + L::kRing);
+            uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+            using At = Place<kStages>;
+            At at;  // of the step's K; its V and the next step's K follow
+            auto done = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+            auto ready = [&](const At& x) { return done(&B->full[x.stage], x.round); };
+            auto qk = [&](int t, const At& x) {
+                const uint32_t k = desc_low(ring + x.stage * L::kTile, 16), q = desc_low(qa + t * L::kTile, 16);
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            if (t >= row_tiles || !ok) continue;
-                            if (t == 0) ok = ready(v);
-                            ok = ok && wait(&B->p_full[t], np[t]++);
-                            if (!ok) continue;
+                for (int sl = 0; sl < kSlices; ++sl)
+                    mma4_ss(taddr + t * kKeys, q + (sl * kSlice >> 4), desc_high(kGroup), k + (sl * kGroup >> 4),
+                            desc_high(L::kRowGroup), idS, sl > 0);
+                commit_elected(&B->s_full[t]);
+            };
+            auto pv = [&](int t, const At& x, bool first) {
+                const uint32_t va = desc_low(ring + x.stage * L::kTile, kGroup);
+#pragma unroll
+                for (int part = 0; part < (kTwo ? 2 : 1); ++part)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+                        mma4_ts<2 * L::kRowGroup>(taddr + 256 + t * 128, taddr + t * kKeys + part * 64 + hf * 32,
+                                                  va + (hf * 8 * L::kRowGroup >> 4), desc_high(L::kRowGroup), idPV,
+                                                  !(first && part == 0 && hf == 0));
+            };
+            // S of the row tiles of a step (a tile of an item's keys), K at ring position x; `fresh`: the
+            // item's first, `left` 1: its last.
+            struct Step {
+                int row_tiles, left;  // tiles of the item from this one on
+                bool fresh;
+            };
+            auto qk_of = [&](int t, const At& x, const Step& n) -> bool {
+                if (t == 0 && !ready(x)) return false;
+                if (n.fresh && !done(&B->q_full[t], nq[t]++)) return false;
+                tc_fence_after();
+                qk(t, x);
+                if (n.left == 1) commit_elected(&B->q_empty[t]);
+                if (t == n.row_tiles - 1) commit_elected(&B->empty[x.stage]);
+                return true;
+            };
+            int64_t i = blockIdx.x;
+            auto first_step = [&](int64_t x) {
+                if (x >= items) return Step{0, 0, true};
+                const Item it = item_at(x);
+                return Step{it.ntok > kTileTokens ? 2 : 1, it.tiles, true};
+            };
+            Step now = first_step(i), item_next = first_step(i + gridDim.x);
+            bool ok = true;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) ok = ok && (t >= now.row_tiles || qk_of(t, at, now));
+            while (ok && now.row_tiles > 0) {
+                // P . V of this step, and S of the next one, row tile by row tile: an item's first S stand between
+                // the last P . V of the item before, while its rows are written out.
+                const bool ends = now.left == 1;
+                const At v = at.next(), k = v.next();
+                const Step next = ends ? item_next : Step{now.row_tiles, now.left - 1, false};
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (ok && t < now.row_tiles) {
+                        if (t == 0) ok = ready(v);
+                        ok = ok && done(&B->p_full[t], np[t]++);
+                        if (ok) {
                             tc_fence_after();
-                            pv(t, v, j == 0);
-                            if (t == row_tiles - 1) tc_commit(&B->empty[stage_of(v)]);
-                            if (!more) {
-                                tc_commit(&B->o_full[t]);
-                                continue;
-                            }
-                            if (t == 0) ok = ready(k);
-                            if (!ok) continue;
-                            tc_fence_after();
-                            qk(t, k);
-                            if (t == row_tiles - 1) {
-                                tc_commit(&B->empty[stage_of(k)]);
-                                if (j + 2 == it.tiles) tc_commit(&B->q_empty);
-                            }
+                            pv(t, v, now.fresh);
+                            if (t == now.row_tiles - 1) commit_elected(&B->empty[v.stage]);
+                            if (ends) commit_elected(&B->o_full[t]);
                         }
-                        at += 2;
                     }
+                    if (ok && t < next.row_tiles) ok = qk_of(t, k, next);
+                }
+                at = k;
+                now = next;
+                if (ends) {
+                    i += gridDim.x;
+                    item_next = first_step(i + gridDim.x);
                 }
             }
             __syncwarp();
@@ -385,24 +464,31 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
         const bool negative = a.scale_log2 < 0.f;
         uint32_t ns = 0, no = 0, at = 0;
         bool ok = true;
+        Item it;
+        if (blockIdx.x < items) it = item_at(blockIdx.x);
         for (int64_t i = blockIdx.x; i < items && ok; i += gridDim.x) {
-            const Item it = item_at(i);
-            const int first = t * kTileTokens;  // of this row tile, among the item's tokens
-            if (first >= it.ntok) {             // (row tile 1 of a short item)
+            if (t * kTileTokens >= it.ntok) {  // (row tile 1 of a short item)
                 at += 2 * it.tiles;
+                if (i + gridDim.x < items) it = item_at(i + gridDim.x);
                 continue;
             }
-            const int tr = first + r / G;
-            const bool mine = tr < it.ntok;
-            const int qpos = it.pos0 + min(tr, it.ntok - 1);
-            const int p_first = it.pos0 + first, p_last = it.pos0 + min(first + kTileTokens, it.ntok) - 1;
-            // Keys in sight, as places in the list: [0, va) and [vb, vc).
-            const int va = min(a.sinks, qpos + 1), vb = max(0, qpos - a.window + 1 - it.skip), vc = qpos + 1 - it.skip;
-            const int all_from = max(0, p_last - a.window + 1 - it.skip), all_to = p_first + 1 - it.skip;
-            const int all_sinks = min(a.sinks, p_first + 1);
-            const int live = min(it.ctx - it.skip, it.boxes * box);  // places behind it hold no token
+            const int num_tiles = it.tiles;
+            // Keys in sight of the row, as places in the list: [0, va) and [vb, vc); and of all rows of the
+            // warp (32 / G tokens): [0, wa) and [wb, wc).
+            int va, vb, vc, wa, wb, wc;
+            {
+                const int w0 = t * kTileTokens + (warp & 3) * 32 / G, tr = t * kTileTokens + r / G;
+                const int p = it.pos0 + min(tr, it.ntok - 1);
+                const int p0 = it.pos0 + min(w0, it.ntok - 1), p1 = it.pos0 + min(w0 + 31 / G, it.ntok - 1);
+                va = min(a.sinks, p + 1);
+                vb = max(0, p - a.window + 1 - it.skip);
+                vc = p + 1 - it.skip;
+                wa = min(a.sinks, p0 + 1);
+                wb = max(0, p1 - a.window + 1 - it.skip);
+                wc = p0 + 1 - it.skip;
+            }
             float m_ref = -INFINITY, l = 0.f;
-            for (int j = 0; j < it.tiles; ++j, at += 2) {
+            for (int j = 0; j < num_tiles; ++j, at += 2) {
                 ok = __all_sync(0xffffffffu, wait(&B->s_full[t], ns++));
                 if (!ok) break;
                 tc_fence_after();
@@ -420,24 +506,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
 #pragma unroll
                     for (int c = 0; c < kKeys; ++c) sv[c] = -sv[c];
                 }
-                if (!((k0 >= all_from && k0 + kKeys <= all_to) || k0 + kKeys <= all_sinks)) {
 #pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4) {
-                        const int c0 = k0 + 32 * q4;
-                        const uint32_t seen = columns(0, va - c0) | columns(vb - c0, vc - c0);
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    const int c0 = k0 + 32 * q4;
+                    if ((c0 >= wb && c0 + 32 <= wc) || c0 + 32 <= wa) continue;  // every row of the warp sees them all
+                    const uint32_t seen = columns(0, va - c0) | columns(vb - c0, vc - c0);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            sv[32 * q4 + c] = (seen >> c) & 1u ? sv[32 * q4 + c] : -INFINITY;
-                    }
+                    for (int c = 0; c < 32; ++c) sv[32 * q4 + c] = (seen >> c) & 1u ? sv[32 * q4 + c] : -INFINITY;
                 }
                 float mx[8];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) mx[c] = sv[c];
+                for (int e = 0; e < 8; ++e) {
+                    mx[e] = fmaxf(sv[e], sv[e + 8]);
 #pragma unroll
-                for (int c = 8; c < kKeys; c += 16)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        mx[e] = c + 8 + e < kKeys ? fmaxf(fmaxf(mx[e], sv[c + e]), sv[c + 8 + e]) : fmaxf(mx[e], sv[c + e]);
+                    for (int c = 16; c < kKeys; c += 16) mx[e] = fmaxf(mx[e], fmaxf(sv[c + e], sv[c + 8 + e]));
+                }
                 const float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                                        fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) *
                                  sc;
@@ -452,13 +535,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                             m_ref = mt;
                         }
 #pragma unroll
-                        for (int cb = 0; cb < D / 32; ++cb) {
-                            float o[32];
-                            tc_ld32(o_col + 32 * cb, o);
+                        for (int cb = 0; cb < D / 16; ++cb) {
+                            float o[16];
+                            tc_ld16(o_col + 16 * cb, o);
                             tc_wait_ld();
+                            uint32_t u[16];
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) o[c] *= f;
-                            tc_st32(o_col + 32 * cb, o);
+                            for (int c = 0; c < 16; ++c) u[c] = __float_as_uint(o[c] * f);
+                            tc_st16u(o_col + 16 * cb, u);
                         }
                     }
                 }
@@ -484,7 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                 }
                 const float2 both = add2(sum[0], sum[1]);
                 l += both.x + both.y;
-                if (t == 0 && k0 + kKeys > live) {
+                if (t == 0 && j == num_tiles - 1) {
+                    const Item z = item_at(i);
+                    const int live = min(z.ctx - z.skip, z.boxes * box);  // places behind it hold no token
                     const uint32_t st = (at + 1) % kStages;
                     ok = __all_sync(0xffffffffu, wait(&B->full[st], (at + 1) / kStages));
                     if (!ok) break;
@@ -492,7 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                     uint8_t* vd = base + L::kRing + st * L::kTile;
                     for (int e = r; e < (kKeys - from) * 8 * kSlices; e += 128) {
                         const int row = from + e / (8 * kSlices), c = e % (8 * kSlices);
-                        *reinterpret_cast<uint4*>(vd + (c >> 3) * kSlice + row * 128 + ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4*>(vd + (row >> 3) * L::kRowGroup + (c >> 3) * kGroup + (row & 7) * 128 +
+                                                  ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
                     }
                     fence_proxy_async_smem();
                 }
@@ -502,11 +589,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                 if (lane == 0) mbar_arrive(&B->p_full[t]);
             }
             if (!ok) break;
+            const Item z = item_at(i);  // (not held through the loop above: its registers are all in use)
+            if (i + gridDim.x < items) it = item_at(i + gridDim.x);
             ok = __all_sync(0xffffffffu, wait(&B->o_full[t], no++));
             if (!ok) break;
             tc_fence_after();
+            const int first = t * kTileTokens, tr = first + r / G;
+            const bool mine = tr < z.ntok;
             const float inv = 1.f / l;
-            const int64_t o0 = ((it.tok0 + tr) * a.num_q_heads + it.h * G + r % G) * D;
+            const int64_t o0 = ((z.tok0 + tr) * a.num_q_heads + z.h * G + r % G) * D;
             bool nan = false;
 #pragma unroll
             for (int cb = 0; cb < D / 32; ++cb) {
@@ -537,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
             __syncwarp();
             for (; bad; bad &= bad - 1) {
                 const int row = first * G + (warp & 3) * 32 + __ffs(bad) - 1;
-                exact_row<DT, DT, D>(a, it.s, it.h, it.tok0 + row / G, it.h * G + row % G, it.pos0 + row / G);
+                exact_row<DT, DT, D>(a, z.s, z.h, z.tok0 + row / G, z.h * G + row % G, z.pos0 + row / G);
             }
         }
     }
