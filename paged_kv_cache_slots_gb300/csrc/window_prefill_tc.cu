@@ -4,9 +4,10 @@
 // For a row (new token at position p, query head g) over the keys j in sight,
 // j <= p and (j > p - window or j < sinks):
 //   s_j = scale q . k_j,  m = max s_j,  out = sum 2^(s_j - m) v_j / sum 2^(s_j - m)
-// in base 2, with one pass over the keys: the running reference m only moves when a
-// row's maximum grows by more than 2^8 (the weights stay <= 256), and O and the sum
-// are rescaled then.
+// in base 2, with one pass over the keys.  m is a reference that moves seldom: it is
+// the maximum of the first keys that the row sees, and that of later ones when the
+// weights of 64 keys sum to more than 2^12 (O and the sum are rescaled then), so that
+// the usual 64 keys need no maximum at all.
 //
 // Work split.  An item is 256 / G new tokens of one sequence with the G query heads
 // of one KV head: 256 rows, two tiles of 128, so that a K and V tile read from L2
@@ -16,9 +17,10 @@
 // then those of the window), taken 128 keys at a time:
 //   warp 8       producer: Q, K and V by TMA into a Q buffer and a ring of stages
 //                (a stage is the K or the V of 128 keys), ahead into the next item;
-//   warp 9       (one lane) issues the MMAs.  S = Q . K^T of one row tile (M 128,
-//                N 128) while the other's softmax runs, then O += P . V with P read
-//                from tensor memory over the S it came from;
+//   warp 9       issues the MMAs: S = Q . K^T of one row tile (M 128, N 128) while the
+//                other's softmax runs, then O += P . V with P read from tensor memory
+//                over the S it came from (an issuing warp for each row tile: the long
+//                chunk 997 us instead of 888);
 //   warps 0-3, 4-7  softmax of the two row tiles, a thread a row: load S, mask (the
 //                tiles at the edges of the window alone), maximum, weights, P; at the
 //                end of an item O / l.
@@ -50,23 +52,26 @@ constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr uint32_t kSlice = kRowsTile * 128;  // Q: 128 rows of 64 elements, 16 KiB
 constexpr uint32_t kGroup = 8 * 128;          // 8 rows of 64 elements: the swizzle's atom
 constexpr uint32_t kTmemCols = 512;
-constexpr float kLazy = 8.f;
+constexpr float kMoveAt = 4096.f;  // sum of half a tile's weights above which a row's reference moves
 
 template <int D>
 struct Layout {
     static constexpr uint32_t kTile = (D / 64) * kSlice;  // Q of a row tile, K or V of 128 keys
     static constexpr uint32_t kRowGroup = (D / 64) * kGroup;  // K and V: 8 rows of all slices, slice by slice
-    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kStages = D == 128 ? 4 : 8;
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kRing = 2 * kTile;
-    static constexpr uint32_t kBars = kRing + kStages * kTile;
+    static constexpr uint32_t kOut = kRing + kStages * kTile;  // 4 KiB for each softmax warp: 32 rows of 128 bytes
+    static constexpr uint32_t kBars = kOut + 8 * 4096;
 };
 
 template <int kStages>
 struct Bars {
     uint64_t full[kStages], empty[kStages];
     uint64_t q_full[2], q_empty[2];  // of each row tile
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], o_full[2];
+    uint64_t p_full[2];
+    int4 note[8][2];                    // what each softmax warp needs of its item at the end
     uint32_t tmem;
     int abort;
 };
@@ -79,6 +84,11 @@ struct Place {
         return stage + 1 == kStages ? Place{0, round + 1} : Place{stage + 1, round};
     }
 };
+
+// The rest of a wait that the first look did not end, kept out of the issuing loop.
+__device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+    return mbar_wait_bounded(bar, parity, abort, status);
+}
 
 // What an item needs to know, the same in every role.
 struct Item {
@@ -218,6 +228,17 @@ __device__ __forceinline__ uint32_t pack2(float x0, float x1) {
     }
 }
 
+template <int DT>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if constexpr (DT == kBF16) {
+        const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&w);
+        return make_float2(__low2float(h), __high2float(h));
+    } else {
+        const __half2 h = *reinterpret_cast<const __half2*>(&w);
+        return make_float2(__low2float(h), __high2float(h));
+    }
+}
+
 // kTwo: P in two parts.
 template <int DT, int D, int G, bool kTwo>
 __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(const PrefillArgs a,
@@ -293,9 +314,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
             bool ok = true;
             // The cache's 8-row group of box `lane` of tile j (the same for K and V); a box lies within a block.
             auto group_of = [&](const Item& it, int j) {
+                if (lane >= per_tile || j >= it.tiles) return 0;
                 const int b = j * per_tile + lane;
-                if (lane >= per_tile || b >= it.boxes) return 0;
-                const int cg = b << sh;
+                const int cg = b < it.boxes ? b << sh : 0;  // (behind the last box: the first again, masked)
                 const int key = cg + (cg >= it.sink_keys ? it.skip : 0);
                 const int lb = key / a.block_size;
                 int blk = a.block_tables[static_cast<int64_t>(it.s) * a.max_blocks + lb];
@@ -305,16 +326,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                 }
                 return ((blk * a.num_kv_heads + it.h) * a.block_size + (key - lb * a.block_size)) >> 3;
             };
-            // K or V of a tile: `n` boxes, one a lane.
-            auto load = [&](int n, int y, const CUtensorMap* map) -> bool {
+            // K or V of a tile, a box a lane.
+            auto load = [&](int y, const CUtensorMap* map) -> bool {
                 int good = 1;
                 if (lane == 0) {
                     if (at.round > 0) good = wait(&B->empty[at.stage], at.round - 1);
-                    if (good) mbar_arrive_expect_tx(&B->full[at.stage], static_cast<uint32_t>(n) * (box / 8) * L::kRowGroup);
+                    if (good) mbar_arrive_expect_tx(&B->full[at.stage], L::kTile);
                 }
                 good = __shfl_sync(0xffffffffu, good, 0);
                 if (!good) return false;
-                if (lane < n)
+                if (lane < per_tile)
                     tensor_load_4d(base + L::kRing + at.stage * L::kTile + lane * (box / 8) * L::kRowGroup, map, y,
                                    &B->full[at.stage], keep);
                 __syncwarp();
@@ -326,9 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                 const int row_tiles = it.ntok > kTileTokens ? 2 : 1;
                 int y = group_of(it, 0);
                 for (int j = 0; j < it.tiles && ok; ++j) {
-                    const int n = min(per_tile, it.boxes - j * per_tile);
                     const int y_next = group_of(it, j + 1);  // (asked for while this tile's stages become free)
-                    ok = load(n, y, &tmk);
+                    ok = load(y, &tmk);
                     if (ok && j == 0) {
                         // A row tile of Q, once the S of the item before are done with its buffer.
                         int good = 1;
@@ -347,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                         }
                         ok = __shfl_sync(0xffffffffu, good, 0) != 0;
                     }
-                    ok = ok && load(n, y, &tmv);
+                    ok = ok && load(y, &tmv);
                     y = y_next;
                 }
             }
@@ -377,10 +397,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
             constexpr uint32_t idS = tc_idesc_f16(bf, false, kKeys, kRowsTile);
             constexpr uint32_t idPV = tc_idesc_f16(bf, true, D, kRowsTile);
             const uint32_t qa = smem_addr(base + L::kQ), ring = smem_addr(base + L::kRing);
-            uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+            uint32_t nq = 0, np = 0;  // phases of Q's and P's barriers, row tile 1's in the upper halves
+            auto count = [](uint32_t& n, int t) {
+                const uint32_t x = n >> (16 * t);
+                n = t ? n + 0x10000u : (n & 0xffff0000u) | ((n + 1) & 0xffffu);
+                return x;
+            };
             using At = Place<kStages>;
             At at;  // of the step's K; its V and the next step's K follow
-            auto done = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+            auto done = [&](uint64_t* bar, uint32_t parity) {
+                const bool there = mbar_try_wait(bar, parity & 1u) || wait_longer(bar, parity & 1u, abort, a.status);
+                return __all_sync(0xffffffffu, there) != 0;
+            };
             auto ready = [&](const At& x) { return done(&B->full[x.stage], x.round); };
             auto qk = [&](int t, const At& x) {
                 const uint32_t k = desc_low(ring + x.stage * L::kTile, 16), q = desc_low(qa + t * L::kTile, 16);
@@ -393,10 +421,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
             auto pv = [&](int t, const At& x, bool first) {
                 const uint32_t va = desc_low(ring + x.stage * L::kTile, kGroup);
 #pragma unroll
-                for (int part = 0; part < (kTwo ? 2 : 1); ++part)
+                for (int hf = 0; hf < 2; ++hf)  // half the keys
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf)
-                        mma4_ts<2 * L::kRowGroup>(taddr + 256 + t * 128, taddr + t * kKeys + part * 64 + hf * 32,
+                    for (int part = 0; part < (kTwo ? 2 : 1); ++part)
+                        mma4_ts<2 * L::kRowGroup>(taddr + 256 + t * 128, taddr + t * kKeys + hf * 64 + part * 32,
                                                   va + (hf * 8 * L::kRowGroup >> 4), desc_high(L::kRowGroup), idPV,
                                                   !(first && part == 0 && hf == 0));
             };
@@ -406,14 +434,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                 int row_tiles, left;  // tiles of the item from this one on
                 bool fresh;
             };
-            auto qk_of = [&](int t, const At& x, const Step& n) -> bool {
-                if (t == 0 && !ready(x)) return false;
-                if (n.fresh && !done(&B->q_full[t], nq[t]++)) return false;
+            auto qk_of = [&](int t, const At& x, const Step& n) {
                 tc_fence_after();
                 qk(t, x);
                 if (n.left == 1) commit_elected(&B->q_empty[t]);
                 if (t == n.row_tiles - 1) commit_elected(&B->empty[x.stage]);
-                return true;
             };
             int64_t i = blockIdx.x;
             auto first_step = [&](int64_t x) {
@@ -422,20 +447,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                 return Step{it.ntok > kTileTokens ? 2 : 1, it.tiles, true};
             };
             Step now = first_step(i), item_next = first_step(i + gridDim.x);
-            bool ok = true;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) ok = ok && (t >= now.row_tiles || qk_of(t, at, now));
+            bool ok = now.row_tiles == 0 || ready(at);
+#pragma unroll 1
+            for (int t = 0; t < now.row_tiles && ok; ++t) {
+                ok = done(&B->q_full[t], count(nq, t));
+                if (ok) qk_of(t, at, now);
+            }
             while (ok && now.row_tiles > 0) {
                 // P . V of this step, and S of the next one, row tile by row tile: an item's first S stand between
                 // the last P . V of the item before, while its rows are written out.
                 const bool ends = now.left == 1;
                 const At v = at.next(), k = v.next();
                 const Step next = ends ? item_next : Step{now.row_tiles, now.left - 1, false};
-#pragma unroll
+#pragma unroll 1
                 for (int t = 0; t < 2; ++t) {
+                    // Every wait before the first issue: an issue returns when the MMA before it is done, so that
+                    // the tensor cores stand still while this warp looks at a barrier.
+                    const bool more = t < next.row_tiles;
+                    if (ok && t == 0) ok = ready(v) && (!more || ready(k));
+                    if (ok && more && next.fresh) ok = done(&B->q_full[t], count(nq, t));
                     if (ok && t < now.row_tiles) {
-                        if (t == 0) ok = ready(v);
-                        ok = ok && done(&B->p_full[t], np[t]++);
+                        ok = done(&B->p_full[t], count(np, t));
                         if (ok) {
                             tc_fence_after();
                             pv(t, v, now.fresh);
@@ -443,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                             if (ends) commit_elected(&B->o_full[t]);
                         }
                     }
-                    if (ok && t < next.row_tiles) ok = qk_of(t, k, next);
+                    if (ok && more) qk_of(t, k, next);
                 }
                 at = k;
                 now = next;
@@ -473,9 +505,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                 continue;
             }
             const int num_tiles = it.tiles;
-            // Keys in sight of the row, as places in the list: [0, va) and [vb, vc); and of all rows of the
-            // warp (32 / G tokens): [0, wa) and [wb, wc).
-            int va, vb, vc, wa, wb, wc;
+            // Keys in sight of the row, as places in the list: [0, va) and [vb, vc).  All rows of the warp (32 / G
+            // tokens) see all keys of the halves of tiles [whole_from, whole_to); with a negative scale, whose sign
+            // the masking applies, there are none.
+            int va, vb, vc, whole_from, whole_to;
             {
                 const int w0 = t * kTileTokens + (warp & 3) * 32 / G, tr = t * kTileTokens + r / G;
                 const int p = it.pos0 + min(tr, it.ntok - 1);
@@ -483,57 +516,69 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                 va = min(a.sinks, p + 1);
                 vb = max(0, p - a.window + 1 - it.skip);
                 vc = p + 1 - it.skip;
-                wa = min(a.sinks, p0 + 1);
-                wb = max(0, p1 - a.window + 1 - it.skip);
-                wc = p0 + 1 - it.skip;
+                whole_from = (max(0, p1 - a.window + 1 - it.skip) + 63) >> 6;
+                whole_to = negative ? 0 : (p0 + 1 - it.skip) >> 6;
             }
+            if (lane == 0) {
+                B->note[warp][0] = make_int4(it.s, it.h, it.ntok, it.pos0);
+                B->note[warp][1] = make_int4(static_cast<int>(it.tok0), 0, 0, 0);
+            }
+            const int live = it.ctx - it.skip;  // places from there on hold no token
             float m_ref = -INFINITY, l = 0.f;
-            for (int j = 0; j < num_tiles; ++j, at += 2) {
-                ok = __all_sync(0xffffffffu, wait(&B->s_full[t], ns++));
-                if (!ok) break;
-                tc_fence_after();
-                float sv[kKeys];
+            float limit = -1.f;  // of a half tile's sum of weights: kMoveAt once there is a reference
+            // Half a tile's keys: mask, weights, P.
+            auto half = [&](float (&sv)[64], int j, int hf) -> bool {
+                if (2 * j + hf < whole_from || 2 * j + hf >= whole_to) {  // (else every row of the warp sees all 64)
+                    const int k0 = j * kKeys + hf * 64;
 #pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4) {
-                    float x[32];
-                    tc_ld32(s_col + 32 * q4, x);
+                    for (int q = 0; q < 2; ++q) {
+                        const int c0 = k0 + 32 * q;
+                        const uint32_t seen = columns(0, va - c0) | columns(vb - c0, vc - c0);
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) sv[32 * q4 + c] = x[c];
-                }
-                tc_wait_ld();
-                const int k0 = j * kKeys;
-                if (negative) {
-#pragma unroll
-                    for (int c = 0; c < kKeys; ++c) sv[c] = -sv[c];
-                }
-#pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4) {
-                    const int c0 = k0 + 32 * q4;
-                    if ((c0 >= wb && c0 + 32 <= wc) || c0 + 32 <= wa) continue;  // every row of the warp sees them all
-                    const uint32_t seen = columns(0, va - c0) | columns(vb - c0, vc - c0);
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) sv[32 * q4 + c] = (seen >> c) & 1u ? sv[32 * q4 + c] : -INFINITY;
-                }
-                float mx[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    mx[e] = fmaxf(sv[e], sv[e + 8]);
-#pragma unroll
-                    for (int c = 16; c < kKeys; c += 16) mx[e] = fmaxf(mx[e], fmaxf(sv[c + e], sv[c + 8 + e]));
-                }
-                const float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                       fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) *
-                                 sc;
-                if (j == 0) {
-                    m_ref = mt;  // -inf: nothing in sight so far
-                } else {
-                    const bool need = mt > m_ref + kLazy;
-                    if (__any_sync(0xffffffffu, need)) {
-                        const float f = need ? fast_exp2(m_ref - mt) : 1.f;  // (0 from -inf)
-                        if (need) {
-                            l *= f;
-                            m_ref = mt;
+                        for (int c = 0; c < 32; ++c) {
+                            const float x = negative ? -sv[32 * q + c] : sv[32 * q + c];
+                            sv[32 * q + c] = (seen >> c) & 1u ? x : -INFINITY;
                         }
+                    }
+                }
+                uint32_t hi[32];
+                [[maybe_unused]] uint32_t lo[kTwo ? 32 : 1];
+                float sum = 0.f;
+                auto weights = [&]() {
+                    const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+                    const float2 sc2 = make_float2(sc, sc), neg2 = make_float2(neg, neg);
+                    float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const float2 e = fma2(make_float2(sv[2 * c], sv[2 * c + 1]), sc2, neg2);
+                        const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+                        part[c & 1] = add2(part[c & 1], p);
+                        if constexpr (kTwo)
+                            pack_split<DT>(p.x, p.y, hi[c], lo[c]);
+                        else
+                            hi[c] = pack2<DT>(p.x, p.y);
+                    }
+                    const float2 both = add2(part[0], part[1]);
+                    sum = both.x + both.y;
+                };
+                weights();
+                if (__any_sync(0xffffffffu, !(sum <= limit))) {
+                    // A new reference, the maximum of these scores.  (S being there says that the P . V before are
+                    // done.)
+                    float mx = sv[0];
+#pragma unroll
+                    for (int c = 1; c < 64; ++c) mx = fmaxf(mx, sv[c]);
+                    mx *= sc;
+                    const bool move = mx > m_ref && !(sum <= limit);
+                    // The step is a whole number, so that it scales what stands in P exactly.
+                    if (m_ref > -INFINITY) mx = m_ref + ceilf(mx - m_ref);
+                    const float f = move ? fast_exp2(m_ref - mx) : 1.f;  // (0 from -inf)
+                    if (move) {
+                        l *= f;
+                        m_ref = mx;
+                        limit = kMoveAt;
+                    }
+                    if (j > 0) {
 #pragma unroll
                         for (int cb = 0; cb < D / 16; ++cb) {
                             float o[16];
@@ -545,36 +590,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                             tc_st16u(o_col + 16 * cb, u);
                         }
                     }
-                }
-                const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
-                const float2 sc2 = make_float2(sc, sc), neg2 = make_float2(neg, neg);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    if (hf == 1) {  // the first half's weights
 #pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4) {
-                    uint32_t hi[16];
-                    [[maybe_unused]] uint32_t lo[16];
+                        for (int cb = 0; cb < (kTwo ? 4 : 2); ++cb) {
+                            float w[16];
+                            tc_ld16(s_col + 16 * cb, w);
+                            tc_wait_ld();
+                            uint32_t u[16];
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const float2 e = fma2(make_float2(sv[32 * q4 + 2 * c], sv[32 * q4 + 2 * c + 1]), sc2, neg2);
-                        const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
-                        sum[c & 1] = add2(sum[c & 1], p);
-                        if constexpr (kTwo)
-                            pack_split<DT>(p.x, p.y, hi[c], lo[c]);
-                        else
-                            hi[c] = pack2<DT>(p.x, p.y);
+                            for (int c = 0; c < 16; ++c) {
+                                const float2 x = unpack2<DT>(__float_as_uint(w[c]));
+                                u[c] = pack2<DT>(x.x * f, x.y * f);
+                            }
+                            tc_st16u(s_col + 16 * cb, u);
+                        }
                     }
-                    tc_st16u(s_col + 16 * q4, hi);
-                    if constexpr (kTwo) tc_st16u(s_col + 64 + 16 * q4, lo);
+                    weights();
                 }
-                const float2 both = add2(sum[0], sum[1]);
-                l += both.x + both.y;
-                if (t == 0 && j == num_tiles - 1) {
-                    const Item z = item_at(i);
-                    const int live = min(z.ctx - z.skip, z.boxes * box);  // places behind it hold no token
+                l += sum;
+                tc_st32u(s_col + 64 * hf, hi);  // over the S that it came from
+                if constexpr (kTwo) tc_st32u(s_col + 64 * hf + 32, lo);
+                if (hf == 0 && t == 0 && (j + 1) * kKeys > live) {
                     const uint32_t st = (at + 1) % kStages;
-                    ok = __all_sync(0xffffffffu, wait(&B->full[st], (at + 1) / kStages));
-                    if (!ok) break;
-                    const int from = max(0, live - k0);
+                    if (!__all_sync(0xffffffffu, wait(&B->full[st], (at + 1) / kStages))) return false;
+                    const int from = max(0, live - j * kKeys);
                     uint8_t* vd = base + L::kRing + st * L::kTile;
                     for (int e = r; e < (kKeys - from) * 8 * kSlices; e += 128) {
                         const int row = from + e / (8 * kSlices), c = e % (8 * kSlices);
@@ -583,52 +622,92 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                     }
                     fence_proxy_async_smem();
                 }
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&B->p_full[t]);
+                return true;
+            };
+            // (One text for all halves: the roles' loops have to share the instruction cache.)
+#pragma unroll 1
+            for (int hh = 0; hh < 2 * num_tiles && ok; ++hh) {
+                const int j = hh >> 1, hf = hh & 1;
+                if (hf == 0) {
+                    ok = __all_sync(0xffffffffu, wait(&B->s_full[t], ns++));
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                float sv[64];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float x[32];
+                    tc_ld32(s_col + 64 * hf + 32 * q, x);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) sv[32 * q + c] = x[c];
+                }
+                tc_wait_ld();
+                ok = half(sv, j, hf);
+                if (hf == 1) {
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&B->p_full[t]);
+                    at += 2;
+                }
             }
             if (!ok) break;
-            const Item z = item_at(i);  // (not held through the loop above: its registers are all in use)
+            __syncwarp();
+            const int4 n0 = B->note[warp][0];  // (not held through the loop above: its registers are all in use)
+            const int64_t tok0 = B->note[warp][1].x;
             if (i + gridDim.x < items) it = item_at(i + gridDim.x);
             ok = __all_sync(0xffffffffu, wait(&B->o_full[t], no++));
             if (!ok) break;
             tc_fence_after();
-            const int first = t * kTileTokens, tr = first + r / G;
-            const bool mine = tr < z.ntok;
+            const int w0 = t * kRowsTile + (warp & 3) * 32;  // the warp's first row of the item
+            const int rows = min(32, n0.z * G - w0);         // its rows that are the item's
             const float inv = 1.f / l;
-            const int64_t o0 = ((z.tok0 + tr) * a.num_q_heads + z.h * G + r % G) * D;
             bool nan = false;
+            // 32 rows of 128 bytes at a time through shared memory, so that a store takes whole rows' pieces.
+            uint8_t* stage = base + L::kOut + warp * 4096;
+            constexpr int kPer = kTwo ? 32 : 64;  // elements of 128 bytes
 #pragma unroll
-            for (int cb = 0; cb < D / 32; ++cb) {
-                float o[32];
-                tc_ld32(o_col + 32 * cb, o);
-                tc_wait_ld();
+            for (int cb = 0; cb < D / kPer; ++cb) {
+                uint32_t w[32];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    o[c] *= inv;
-                    nan = nan || o[c] != o[c];
+                for (int q = 0; q < kPer / 32; ++q) {
+                    float o[32];
+                    tc_ld32(o_col + kPer * cb + 32 * q, o);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        o[c] *= inv;
+                        nan = nan || o[c] != o[c];
+                    }
+                    if constexpr (kTwo) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) w[c] = __float_as_uint(o[c]);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) w[16 * q + c] = pack2<DT>(o[2 * c], o[2 * c + 1]);
+                    }
                 }
-                if (!mine) continue;
-                if constexpr (kTwo) {
-                    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + o0 + 32 * cb);
+                if (cb == D / kPer - 1) tc_fence_before();  // O is read before this thread lets the next P . V begin
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) dst[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-                } else {
-                    using T = typename Elem<DT>::T;
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + o0 + 32 * cb);
+                for (int c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                        make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+                __syncwarp();
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        dst[c] = make_uint4(pack2<DT>(o[8 * c], o[8 * c + 1]), pack2<DT>(o[8 * c + 2], o[8 * c + 3]),
-                                            pack2<DT>(o[8 * c + 4], o[8 * c + 5]), pack2<DT>(o[8 * c + 6], o[8 * c + 7]));
+                for (int q = 0; q < 8; ++q) {
+                    const int row = 4 * q + (lane >> 3), c = lane & 7;
+                    if (row < rows) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(stage + row * 128 + ((c ^ (row & 7)) << 4));
+                        const int64_t o0 = ((tok0 + (w0 + row) / G) * a.num_q_heads + n0.y * G + (w0 + row) % G) * D;
+                        *reinterpret_cast<uint4*>(static_cast<char*>(a.out) + (o0 + kPer * cb) * (kTwo ? 4 : 2) + 16 * c) = x;
+                    }
                 }
+                __syncwarp();
             }
-            tc_fence_before();  // O is read before this thread lets the next P . V begin
-            uint32_t bad = __ballot_sync(0xffffffffu, nan && mine);
-            __syncwarp();
+            uint32_t bad = __ballot_sync(0xffffffffu, nan && lane < rows);
             for (; bad; bad &= bad - 1) {
-                const int row = first * G + (warp & 3) * 32 + __ffs(bad) - 1;
-                exact_row<DT, DT, D>(a, z.s, z.h, z.tok0 + row / G, z.h * G + row % G, z.pos0 + row / G);
+                const int row = w0 + __ffs(bad) - 1;
+                exact_row<DT, DT, D>(a, n0.x, n0.y, tok0 + row / G, n0.y * G + row % G, n0.w + row / G);
             }
         }
     }
