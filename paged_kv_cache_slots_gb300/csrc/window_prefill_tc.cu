@@ -58,10 +58,12 @@ template <int D>
 struct Layout {
     static constexpr uint32_t kTile = (D / 64) * kSlice;  // Q of a row tile, K or V of 128 keys
     static constexpr uint32_t kRowGroup = (D / 64) * kGroup;  // K and V: 8 rows of all slices, slice by slice
-    static constexpr int kStages = D == 128 ? 4 : 8;
+    // A stage of the ring holds the V of a tile of keys and the K of the next one.
+    static constexpr uint32_t kStage = 2 * kTile;
+    static constexpr int kStages = D == 128 ? 2 : 4;
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kRing = 2 * kTile;
-    static constexpr uint32_t kOut = kRing + kStages * kTile;  // 4 KiB for each softmax warp: 32 rows of 128 bytes
+    static constexpr uint32_t kOut = kRing + kStages * kStage;  // 4 KiB for each softmax warp: 32 rows of 128 bytes
     static constexpr uint32_t kBars = kOut + 8 * 4096;
 };
 
@@ -326,50 +328,61 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                 }
                 return ((blk * a.num_kv_heads + it.h) * a.block_size + (key - lb * a.block_size)) >> 3;
             };
-            // K or V of a tile, a box a lane.
-            auto load = [&](int y, const CUtensorMap* map) -> bool {
+            // A stage: the V of a tile (groups yv, a box a lane; first time round: none) and the K of the next (yk).
+            auto load = [&](bool v, int yv, bool k, int yk) -> bool {
                 int good = 1;
                 if (lane == 0) {
                     if (at.round > 0) good = wait(&B->empty[at.stage], at.round - 1);
-                    if (good) mbar_arrive_expect_tx(&B->full[at.stage], L::kTile);
+                    if (good) mbar_arrive_expect_tx(&B->full[at.stage], (v ? L::kTile : 0u) + (k ? L::kTile : 0u));
                 }
                 good = __shfl_sync(0xffffffffu, good, 0);
                 if (!good) return false;
-                if (lane < per_tile)
-                    tensor_load_4d(base + L::kRing + at.stage * L::kTile + lane * (box / 8) * L::kRowGroup, map, y,
-                                   &B->full[at.stage], keep);
+                if (lane < per_tile) {
+                    uint8_t* dst = base + L::kRing + at.stage * L::kStage + lane * (box / 8) * L::kRowGroup;
+                    if (v) tensor_load_4d(dst, &tmv, yv, &B->full[at.stage], keep);
+                    if (k) tensor_load_4d(dst + L::kTile, &tmk, yk, &B->full[at.stage], keep);
+                }
                 __syncwarp();
                 at = at.next();
                 return true;
             };
-            for (int64_t i = blockIdx.x; i < items && ok; i += gridDim.x) {
-                const Item it = item_at(i);
-                const int row_tiles = it.ntok > kTileTokens ? 2 : 1;
-                int y = group_of(it, 0);
-                for (int j = 0; j < it.tiles && ok; ++j) {
-                    const int y_next = group_of(it, j + 1);  // (asked for while this tile's stages become free)
-                    ok = load(y, &tmk);
-                    if (ok && j == 0) {
-                        // A row tile of Q, once the S of the item before are done with its buffer.
-                        int good = 1;
-                        if (lane == 0) {
+            // The row tiles of an item's Q, each once the S of the item before are done with its buffer.
+            auto load_q = [&](const Item& it) -> bool {
+                int good = 1;
+                if (lane == 0) {
 #pragma unroll
-                            for (int t = 0; t < 2; ++t) {
-                                if (t >= row_tiles || !good) continue;
-                                if (nq[t] > 0) good = wait(&B->q_empty[t], nq[t] - 1);
-                                if (!good) continue;
-                                mbar_arrive_expect_tx(&B->q_full[t], L::kTile);
-                                for (int sl = 0; sl < kSlices; ++sl)
-                                    tensor_load_3d(base + L::kQ + t * L::kTile + sl * kSlice, &tmq, sl * 64, it.h * G,
-                                                   static_cast<int>(it.tok0) + t * kTileTokens, &B->q_full[t], keep);
-                                ++nq[t];
-                            }
-                        }
-                        ok = __shfl_sync(0xffffffffu, good, 0) != 0;
+                    for (int t = 0; t < 2; ++t) {
+                        if (t * kTileTokens >= it.ntok || !good) continue;
+                        if (nq[t] > 0) good = wait(&B->q_empty[t], nq[t] - 1);
+                        if (!good) continue;
+                        mbar_arrive_expect_tx(&B->q_full[t], L::kTile);
+                        for (int sl = 0; sl < kSlices; ++sl)
+                            tensor_load_3d(base + L::kQ + t * L::kTile + sl * kSlice, &tmq, sl * 64, it.h * G,
+                                           static_cast<int>(it.tok0) + t * kTileTokens, &B->q_full[t], keep);
+                        ++nq[t];
                     }
-                    ok = ok && load(y, &tmv);
+                }
+                return __shfl_sync(0xffffffffu, good, 0) != 0;
+            };
+            Item it;
+            int y = 0;
+            if (blockIdx.x < items) {
+                it = item_at(blockIdx.x);
+                y = group_of(it, 0);
+                ok = load(false, 0, true, y) && load_q(it);
+            }
+            for (int64_t i = blockIdx.x; i < items && ok; i += gridDim.x) {
+                const bool more = i + gridDim.x < items;
+                Item next = it;
+                if (more) next = item_at(i + gridDim.x);
+                for (int j = 0; j < it.tiles && ok; ++j) {
+                    const bool ends = j + 1 == it.tiles;
+                    const int y_next = !ends ? group_of(it, j + 1) : more ? group_of(next, 0) : 0;
+                    ok = load(true, y, !ends || more, y_next);
                     y = y_next;
                 }
+                if (ok && more) ok = load_q(next);
+                it = next;
             }
             // Every copy issued must land before the CTA can exit.
             if (lane == 0) {
@@ -404,14 +417,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                 return x;
             };
             using At = Place<kStages>;
-            At at;  // of the step's K; its V and the next step's K follow
+            At at;  // stage of a step's V and of the next step's K
+            // (A wait is as few instructions as it can be: the softmax warps of this sub-partition issue in between.)
             auto done = [&](uint64_t* bar, uint32_t parity) {
-                const bool there = mbar_try_wait(bar, parity & 1u) || wait_longer(bar, parity & 1u, abort, a.status);
-                return __all_sync(0xffffffffu, there) != 0;
+                while (!mbar_try_wait(bar, parity & 1u))
+                    if (!wait_longer(bar, parity & 1u, abort, a.status)) break;  // (the flag is set: see the end of a step)
+                __syncwarp();
             };
-            auto ready = [&](const At& x) { return done(&B->full[x.stage], x.round); };
             auto qk = [&](int t, const At& x) {
-                const uint32_t k = desc_low(ring + x.stage * L::kTile, 16), q = desc_low(qa + t * L::kTile, 16);
+                const uint32_t k = desc_low(ring + x.stage * L::kStage + L::kTile, 16), q = desc_low(qa + t * L::kTile, 16);
 #pragma unroll
                 for (int sl = 0; sl < kSlices; ++sl)
                     mma4_ss(taddr + t * kKeys, q + (sl * kSlice >> 4), desc_high(kGroup), k + (sl * kGroup >> 4),
@@ -419,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                 commit_elected(&B->s_full[t]);
             };
             auto pv = [&](int t, const At& x, bool first) {
-                const uint32_t va = desc_low(ring + x.stage * L::kTile, kGroup);
+                const uint32_t va = desc_low(ring + x.stage * L::kStage, kGroup);
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf)  // half the keys
 #pragma unroll
@@ -435,10 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                 bool fresh;
             };
             auto qk_of = [&](int t, const At& x, const Step& n) {
-                tc_fence_after();
                 qk(t, x);
                 if (n.left == 1) commit_elected(&B->q_empty[t]);
-                if (t == n.row_tiles - 1) commit_elected(&B->empty[x.stage]);
             };
             int64_t i = blockIdx.x;
             auto first_step = [&](int64_t x) {
@@ -447,37 +459,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                 return Step{it.ntok > kTileTokens ? 2 : 1, it.tiles, true};
             };
             Step now = first_step(i), item_next = first_step(i + gridDim.x);
-            bool ok = now.row_tiles == 0 || ready(at);
+            if (now.row_tiles > 0) {
+                done(&B->full[at.stage], at.round);
 #pragma unroll 1
-            for (int t = 0; t < now.row_tiles && ok; ++t) {
-                ok = done(&B->q_full[t], count(nq, t));
-                if (ok) qk_of(t, at, now);
+                for (int t = 0; t < now.row_tiles; ++t) {
+                    done(&B->q_full[t], count(nq, t));
+                    tc_fence_after();
+                    qk_of(t, at, now);
+                }
+                commit_elected(&B->empty[at.stage]);
+                at = at.next();
             }
-            while (ok && now.row_tiles > 0) {
+            while (now.row_tiles > 0 && !*abort) {
                 // P . V of this step, and S of the next one, row tile by row tile: an item's first S stand between
-                // the last P . V of the item before, while its rows are written out.
+                // the last P . V of the item before, while its rows are written out.  Waits come before the first
+                // issue: an issue returns when the MMA before it is done, so that the tensor cores stand still
+                // while this warp looks at a barrier.
                 const bool ends = now.left == 1;
-                const At v = at.next(), k = v.next();
                 const Step next = ends ? item_next : Step{now.row_tiles, now.left - 1, false};
+                done(&B->full[at.stage], at.round);
 #pragma unroll 1
                 for (int t = 0; t < 2; ++t) {
-                    // Every wait before the first issue: an issue returns when the MMA before it is done, so that
-                    // the tensor cores stand still while this warp looks at a barrier.
                     const bool more = t < next.row_tiles;
-                    if (ok && t == 0) ok = ready(v) && (!more || ready(k));
-                    if (ok && more && next.fresh) ok = done(&B->q_full[t], count(nq, t));
-                    if (ok && t < now.row_tiles) {
-                        ok = done(&B->p_full[t], count(np, t));
-                        if (ok) {
-                            tc_fence_after();
-                            pv(t, v, now.fresh);
-                            if (t == now.row_tiles - 1) commit_elected(&B->empty[v.stage]);
-                            if (ends) commit_elected(&B->o_full[t]);
-                        }
+                    if (more && next.fresh) done(&B->q_full[t], count(nq, t));
+                    if (t < now.row_tiles) {
+                        done(&B->p_full[t], count(np, t));
+                        tc_fence_after();
+                        pv(t, at, now.fresh);
+                        if (ends) commit_elected(&B->o_full[t]);
+                    } else {
+                        tc_fence_after();
                     }
-                    if (ok && more) qk_of(t, k, next);
+                    if (more) qk_of(t, at, next);
                 }
-                at = k;
+                commit_elected(&B->empty[at.stage]);
+                at = at.next();
                 now = next;
                 if (ends) {
                     i += gridDim.x;
@@ -500,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
         if (blockIdx.x < items) it = item_at(blockIdx.x);
         for (int64_t i = blockIdx.x; i < items && ok; i += gridDim.x) {
             if (t * kTileTokens >= it.ntok) {  // (row tile 1 of a short item)
-                at += 2 * it.tiles;
+                at += it.tiles;
                 if (i + gridDim.x < items) it = item_at(i + gridDim.x);
                 continue;
             }
@@ -611,10 +627,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                 tc_st32u(s_col + 64 * hf, hi);  // over the S that it came from
                 if constexpr (kTwo) tc_st32u(s_col + 64 * hf + 32, lo);
                 if (hf == 0 && t == 0 && (j + 1) * kKeys > live) {
-                    const uint32_t st = (at + 1) % kStages;
+                    const uint32_t st = (at + 1) % kStages;  // (stage 0 of round 0 holds the first K alone)
                     if (!__all_sync(0xffffffffu, wait(&B->full[st], (at + 1) / kStages))) return false;
                     const int from = max(0, live - j * kKeys);
-                    uint8_t* vd = base + L::kRing + st * L::kTile;
+                    uint8_t* vd = base + L::kRing + st * L::kStage;
                     for (int e = r; e < (kKeys - from) * 8 * kSlices; e += 128) {
                         const int row = from + e / (8 * kSlices), c = e % (8 * kSlices);
                         *reinterpret_cast<uint4*>(vd + (row >> 3) * L::kRowGroup + (c >> 3) * kGroup + (row & 7) * 128 +
@@ -648,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&B->p_full[t]);
-                    at += 2;
+                    ++at;
                 }
             }
             if (!ok) break;
