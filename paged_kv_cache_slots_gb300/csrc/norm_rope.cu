@@ -62,7 +62,7 @@ __device__ __forceinline__ void load_weights(const void* w, int64_t e, bool wide
 }
 
 template <int DT, int V, bool kInter, int kRows>
-__global__ void __launch_bounds__(kThreads) kv_append_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) kv_append_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
     static_assert(kThreads >= kMaxRopePairs);
     using T = typename Elem<DT>::T;
     constexpr int kE = static_cast<int>(sizeof(T));
@@ -117,18 +117,21 @@ __global__ void __launch_bounds__(kThreads) kv_append_norm_rope_kernel(const __g
     };
     const float inv_dim = 1.f / static_cast<float>(D);
     auto factor = [&](float ss) { return rsqrtf(fmaf(ss, inv_dim, a.eps)); };
-    // f (an item's 2 V elements) times scale and weights, and turned.
-    auto finish = [&](const Item& x, const float* w, float scale, float* f) {
+    // The item's cosines and sines; those of an item that does not turn are 1 and 0.
+    auto angles = [&](const Item& x, float2* c) {
 #pragma unroll
-        for (int j = 0; j < 2 * V; ++j) f[j] *= scale * w[j];
-        if (!x.turn) return;
+        for (int j = 0; j < V; ++j) c[j] = x.turn ? cs[x.e0 / (kInter ? 2 : 1) + j] : make_float2(1.f, 0.f);
+    };
+    // f (an item's 2 V elements) times scale and weights, and turned.
+    auto finish = [&](const Item& x, const float2* c, const float* w, float scale, float* f) {
+#pragma unroll
+        for (int j = 0; j < 2 * V; ++j) f[j] *= w[j];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int ja = kInter ? 2 * j : j, jb = kInter ? 2 * j + 1 : j + V;
-            const float2 c = cs[x.e0 / (kInter ? 2 : 1) + j];
-            const float xa = f[ja], xb = f[jb];
-            f[ja] = xa * c.x - xb * c.y;
-            f[jb] = xb * c.x + xa * c.y;
+            const float xa = f[ja] * scale, xb = f[jb] * scale;
+            f[ja] = xa * c[j].x - xb * c[j].y;
+            f[jb] = xb * c[j].x + xa * c[j].y;
         }
     };
     auto store = [&](const Item& x, int r, const float* f) {
@@ -158,6 +161,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_norm_rope_kernel(const __g
     if (items <= 32) {
         const Item x = item_of<V, kInter>(it, nrot, n);
         const bool active = it < items;
+        float2 c[V];
         for (int rb = r0; rb < r1; rb += groups * kRows) {
             Raw<V * kE> x0[kRows], x1[kRows];
 #pragma unroll
@@ -169,7 +173,10 @@ __global__ void __launch_bounds__(kThreads) kv_append_norm_rope_kernel(const __g
                     x1[u].load(src + x.e1 * kE);
                 }
             }
-            if (!known && !know()) return;  // padding
+            if (!known) {
+                if (!know()) return;  // padding
+                if (active) angles(x, c);
+            }
 #pragma unroll
             for (int u = 0; u < kRows; ++u) {
                 const int r = rb + u * groups + my;
@@ -196,7 +203,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_norm_rope_kernel(const __g
                 float w[2 * V];
                 weights(r, x.e0, w);
                 weights(r, x.e1, w + V);
-                finish(x, w, factor(ss), f);
+                finish(x, c, w, factor(ss), f);
                 store(x, r, f);
             }
         }
@@ -235,7 +242,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_norm_rope_kernel(const __g
                 float w[2 * V];
                 weights(r, x.e0, w);
                 weights(r, x.e1, w + V);
-                finish(x, w, scale, f);
+                float2 c[V];
+                angles(x, c);
+                finish(x, c, w, scale, f);
             } else if (!a.quant) {
                 char* dst = target(r);
                 x0.store(dst + x.e0 * kE);
@@ -245,6 +254,176 @@ __global__ void __launch_bounds__(kThreads) kv_append_norm_rope_kernel(const __g
             store(x, r, f);
         }
     }
+}
+
+constexpr int kRing = 2;  // tokens in shared memory
+
+// The same for many tokens whose rows are whole 16-byte chunks: persistent CTAs that
+// bring the rows of a token (three contiguous pieces: q, k, v) into shared memory by
+// bulk copies while they work on the token before, so that loads never pause and no
+// register waits for one.
+template <int DT, bool kInter>
+__global__ void __launch_bounds__(kThreads, 6) kv_append_norm_rope_ring_kernel(const __grid_constant__ NormRopeArgs a) {
+    using T = typename Elem<DT>::T;
+    constexpr int kE = static_cast<int>(sizeof(T)), V = 16 / kE;
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ uint64_t full[kRing];
+    __shared__ int abort_flag;
+    __shared__ float2 cs[2][kMaxRopePairs];
+    volatile int* abort = &abort_flag;
+    pdl_allow_next();
+    const int tid = threadIdx.x;
+    const int n = a.rot_dim >> 1;
+    const int D = a.head_dim, Hq = a.num_q_heads, Hkv = a.num_kv_heads, H = Hq + 2 * Hkv;
+    const uint32_t row = static_cast<uint32_t>(D) * kE;
+    const uint32_t bytes = static_cast<uint32_t>(H) * row;
+    if (tid == 0) {
+        for (int i = 0; i < kRing; ++i) mbar_init(&full[i], 1);
+        *abort = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    pdl_wait();
+    const uint64_t policy = policy_evict_first();
+    auto fetch = [&](int64_t i, uint32_t stage) {  // thread 0
+        uint8_t* dst = ring + stage * bytes;
+        mbar_arrive_expect_tx(&full[stage], bytes);
+        if (Hq) bulk_load(dst, static_cast<const char*>(a.q) + i * a.q_stride * kE, Hq * row, &full[stage], policy);
+        bulk_load(dst + Hq * row, static_cast<const char*>(a.k) + i * a.k_stride * kE, Hkv * row, &full[stage], policy);
+        bulk_load(dst + (Hq + Hkv) * row, static_cast<const char*>(a.v) + i * a.v_stride * kE, Hkv * row, &full[stage], policy);
+    };
+    const int64_t step = gridDim.x;
+    if (tid == 0)
+        for (int k = 0; k < kRing; ++k)
+            if (blockIdx.x + k * step < a.n_tokens) fetch(blockIdx.x + k * step, k);
+
+    const int nrot = n / V, items = D / (2 * V);
+    int L = 1;
+    while (L < items) L <<= 1;
+    const int groups = kThreads / L;
+    const int my = tid / L, it = tid & (L - 1);
+    const bool active = it < items;
+    const Item x = item_of<V, kInter>(it, nrot, n);
+    const float inv_dim = 1.f / static_cast<float>(D);
+    const int ce = a.quant ? 1 : kE;
+    const int64_t num_slots = static_cast<int64_t>(a.num_blocks) * a.block_size;
+    const int32_t* my_positions = a.positions + (tid < n ? a.axis[tid] * a.positions_stride : 0);
+    const uint64_t my_phase = tid < n ? a.phase[tid] : 0;
+    // What the next token is, asked for a token ahead.
+    int32_t id = 0, slot = 0, pos = 0;
+    auto ask = [&](int64_t i) {
+        if (i >= a.n_tokens) return;
+        id = a.seq_ids ? a.seq_ids[i] : 0;
+        slot = a.slot_mapping[i];
+        if (tid < n) pos = my_positions[i];
+    };
+    auto turn = [&](int k) {
+        if (tid < n) cs[k][tid] = rotor(static_cast<uint64_t>(static_cast<int64_t>(pos)) * my_phase, a.amplitude);
+    };
+    ask(blockIdx.x);
+    turn(0);
+    __syncthreads();
+    uint32_t stage = 0, round = 0;
+    int k = 0;
+    for (int64_t i = blockIdx.x; i < a.n_tokens; i += step) {
+        const int32_t now_id = id, now_slot = slot;
+        ask(i + step);
+        float2 c[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) c[j] = active && x.turn ? cs[k][x.e0 / (kInter ? 2 : 1) + j] : make_float2(1.f, 0.f);
+        const bool keep = now_slot >= 0 && now_slot < num_slots;
+        if (now_id >= 0 && now_slot >= num_slots && tid == 0) raise_flag(a.status, kFlagBadSlot);
+        const int blk = keep ? now_slot / a.block_size : 0, off = now_slot - blk * a.block_size;
+        if (!mbar_wait_bounded(&full[stage], round & 1u, abort, a.status)) break;
+        const uint8_t* src = ring + stage * bytes;
+        if (now_id >= 0) {
+            for (int rb = 0; rb < H; rb += groups) {
+                const int r = rb + my;
+                const bool mine = active && r < H;
+                Raw<16> x0, x1;
+                float f[2 * V];
+                float ss = 0.f;
+                if (mine) {
+                    x0.load(reinterpret_cast<const char*>(src) + r * row + x.e0 * kE);
+                    x1.load(reinterpret_cast<const char*>(src) + r * row + x.e1 * kE);
+                    unpack<DT, V>(x0, f);
+                    unpack<DT, V>(x1, f + V);
+#pragma unroll
+                    for (int j = 0; j < 2 * V; ++j) ss = fmaf(f[j], f[j], ss);
+                }
+                for (int o = L >> 1; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                if (!mine || (r >= Hq && !keep)) continue;
+                const bool copy = r >= Hq + Hkv;
+                char* dst;
+                if (r < Hq) {
+                    dst = static_cast<char*>(a.q_out) + (i * a.q_out_stride + static_cast<int64_t>(r) * D) * kE;
+                } else {
+                    const int h = r - Hq - (copy ? Hkv : 0);
+                    const int64_t at = (static_cast<int64_t>(blk) * Hkv + h) * a.block_size + off;
+                    dst = static_cast<char*>(copy ? a.v_cache : a.k_cache) + at * D * ce;
+                }
+                if (!copy) {
+                    float w[2 * V];
+                    const void* wp = r < Hq ? a.q_weight : a.k_weight;
+                    const int64_t w0 = r < Hq ? r * a.q_weight_stride : (r - Hq) * a.k_weight_stride;
+                    load_weights<DT, V>(wp, w0 + x.e0, a.wide_weights, w);
+                    load_weights<DT, V>(wp, w0 + x.e1, a.wide_weights, w + V);
+                    const float scale = rsqrtf(fmaf(ss, inv_dim, a.eps));
+#pragma unroll
+                    for (int j = 0; j < 2 * V; ++j) f[j] *= w[j];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const int ja = kInter ? 2 * j : j, jb = kInter ? 2 * j + 1 : j + V;
+                        const float xa = f[ja] * scale, xb = f[jb] * scale;
+                        f[ja] = xa * c[j].x - xb * c[j].y;
+                        f[jb] = xb * c[j].x + xa * c[j].y;
+                    }
+                } else if (!a.quant) {  // bit for bit
+                    x0.store(dst + x.e0 * kE);
+                    x1.store(dst + x.e1 * kE);
+                    continue;
+                }
+                if (a.quant && r >= Hq) {
+                    const float scale = copy ? a.v_scale : a.k_scale;
+                    quantize<V>(f, scale).store(dst + x.e0);
+                    quantize<V>(f + V, scale).store(dst + x.e1);
+                } else {
+                    pack<DT, V>(f).store(dst + x.e0 * kE);
+                    pack<DT, V>(f + V).store(dst + x.e1 * kE);
+                }
+            }
+        }
+        if (i + step < a.n_tokens) turn(k ^ 1);
+        __syncthreads();  // the stage and cs[k] are read, cs[k ^ 1] is there
+        if (tid == 0 && i + kRing * step < a.n_tokens) fetch(i + kRing * step, stage);
+        k ^= 1;
+        if (++stage == kRing) {
+            stage = 0;
+            ++round;
+        }
+    }
+    // (Every copy that was issued has been waited for, unless a wait gave up.)
+    if (*abort && tid == 0)
+        for (int q = 0; q < kRing; ++q) {
+            const uint64_t t0 = global_timer_ns();
+            const uint32_t parity = (round + (static_cast<uint32_t>(q) < stage ? 1u : 0u)) & 1u;
+            while (!mbar_try_wait(&full[q], parity) && global_timer_ns() - t0 < kWaitLimitNs) {
+            }
+        }
+}
+
+template <int DT>
+cudaError_t launch_ring(const NormRopeArgs& a, int bytes, int num_sms, cudaStream_t stream) {
+    static RaisedLimit limits[2];
+    auto kern = a.interleaved ? kv_append_norm_rope_ring_kernel<DT, true> : kv_append_norm_rope_ring_kernel<DT, false>;
+    const int smem = kRing * bytes;
+    const cudaError_t e = allow_shared_memory(kern, a.device, smem, &limits[a.interleaved ? 1 : 0]);
+    if (e != cudaSuccess) return e;
+    int per_sm = (220 * 1024) / (smem + 4096);
+    if (per_sm > 6) per_sm = 6;
+    const int64_t ctas = static_cast<int64_t>(num_sms) * per_sm;
+    return launch_kernel(kern, dim3(static_cast<unsigned>(ctas < a.n_tokens ? ctas : a.n_tokens)), dim3(kThreads),
+                         static_cast<size_t>(smem), stream, a.pdl != 0, a);
 }
 
 template <int DT, int V, int kRows>
@@ -266,6 +445,10 @@ cudaError_t launch_dt(NormRopeArgs a, int align, int weight_align, int num_sms, 
                      !weights_fit(v)))
         v >>= 1;
     const int items = a.head_dim / (2 * v);
+    // Many tokens of whole 16-byte items: the ring, while it holds at least two CTAs an SM.
+    const int64_t bytes = static_cast<int64_t>(a.num_q_heads + 2 * a.num_kv_heads) * a.head_dim * kE;
+    if (v == 16 / kE && items <= 32 && kRing * bytes <= 100 * 1024 && a.n_tokens >= 2 * num_sms)
+        return launch_ring<DT>(a, static_cast<int>(bytes), num_sms, stream);
     int L = 1;
     while (L < items && L < 32) L <<= 1;
     const int groups = kThreads / L;

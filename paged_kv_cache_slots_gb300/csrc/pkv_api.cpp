@@ -767,7 +767,7 @@ kv_status_t kv_append_norm_rope(kv_pool_t* p, int layer, const kv_rope_t* rope, 
     a.eps = eps;
     DeviceGuard g(p->cfg.device);
     if (!g.ok) return fail(KV_ERR_CUDA, "cannot select device %d", p->cfg.device);
-    if (kv_status_t st = device_info(nullptr, &a.status, &sms, nullptr, nullptr)) return st;
+    if (kv_status_t st = device_info(&a.device, &a.status, &sms, nullptr, nullptr)) return st;
     cudaError_t e = launch_append_norm_rope(a, align, static_cast<int>(wbits & (~wbits + 1)), sms,
                                             static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "norm and rope append launch");

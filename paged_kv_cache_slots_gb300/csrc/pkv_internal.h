@@ -67,6 +67,7 @@ struct NormRopeArgs : RopeArgs {
     int64_t q_weight_stride, k_weight_stride;
     int wide_weights;      // weights are f32, the rows are not
     float eps;
+    int device;
 };
 
 // Block swap between the pool and a device-addressable host buffer.

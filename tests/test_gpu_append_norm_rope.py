@@ -109,6 +109,13 @@ SHAPES = plain.SHAPES + [
     (64, 4, 2, 128, 128, "bf16", dict(spread=1e4)),
     (64, 4, 2, 96, 32, "f32", dict(spread=1e6, eps=0.0)),
     (64, 4, 2, 64, 64, "f16", dict(spread=1e-3, eps=1e-5)),
+    # many tokens of whole 16-byte items
+    (333, 7, 3, 128, 128, "f16", dict(packed=True, interleaved=True)),
+    (700, 5, 2, 96, 32, "f16", dict(packed=True, axes=3)),
+    (2100, 16, 2, 128, 64, "bf16", dict(weights="f32", per_head=True, packed=True)),
+    (701, 8, 8, 64, 64, "f32", dict(per_head=True, amplitude=1.5)),
+    (400, 3, 1, 256, 256, "bf16", dict(weights=None, interleaved=True)),
+    (400, 2, 1, 512, 128, "f16", {}),
     (9, 2, 1, 1040, 16, "f16", {}),
     (9, 3, 1, 1032, 6, "bf16", dict(weights="f32", per_head=True)),
 ]
@@ -123,19 +130,20 @@ def test_against_the_formula(T, Hq, Hkv, D, rot, dtype, kw):
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("T,Hq,Hkv,D,rot,kw", [
     (1, 8, 2, 128, 128, {}), (130, 8, 2, 128, 64, dict(interleaved=True, packed=True)), (45, 2, 3, 80, 20, dict(bs=8)),
+    (900, 6, 3, 128, 64, dict(packed=True, weights="f32")), (310, 4, 2, 64, 64, dict(interleaved=True)),
     (45, 2, 1, 48, 2, dict(interleaved=True, weights="f32")), (20, 1, 2, 16, 16, dict(shift=1)), (6, 1, 1, 1040, 2, {})])
 def test_quantized(T, Hq, Hkv, D, rot, dtype, kw):
     c = Case(T, Hq, Hkv, D, rot, dtype, fp8=True, **kw)
     c.check(c.run())
 
 
-@pytest.mark.parametrize("D", [64, 1040])
+@pytest.mark.parametrize("T,D", [(40, 64), (40, 1040), (650, 128)])
 @pytest.mark.parametrize("fp8", [False, True])
-def test_negative_slots_and_padding(fp8, D):
-    c = Case(40, 8, 2, D, 64, "bf16", fp8=fp8)
+def test_negative_slots_and_padding(fp8, T, D):
+    c = Case(T, 8, 2, D, 64, "bf16", fp8=fp8)
     c.slots[3] = c.slots[17] = -1
     c.slots[18] = -(2 ** 31)
-    ids = torch.arange(40, dtype=torch.int32, device="cuda")
+    ids = torch.arange(T, dtype=torch.int32, device="cuda")
     ids[5] = ids[39] = -1
     q_out = torch.full_like(c.q, 7.0)
     assert c.run(q_out=q_out, seq_ids=ids) is q_out
@@ -145,8 +153,9 @@ def test_negative_slots_and_padding(fp8, D):
     assert bool((fresh[[5, 39]] == 0).all())
 
 
-def test_slots_past_the_pool_are_flagged():
-    c = Case(12, 4, 2, 64, 64, "f16")
+@pytest.mark.parametrize("T", [12, 400])
+def test_slots_past_the_pool_are_flagged(T):
+    c = Case(T, 4, 2, 64, 64, "f16")
     n = c.NB * c.bs
     c.slots[2], c.slots[7] = n, 2 ** 31 - 1
     q_out = c.run()
@@ -155,10 +164,10 @@ def test_slots_past_the_pool_are_flagged():
     c.check(q_out)
 
 
-@pytest.mark.parametrize("D", [128, 1040])
+@pytest.mark.parametrize("T,D", [(77, 128), (77, 1040), (1200, 128)])
 @pytest.mark.parametrize("inter", [False, True])
-def test_in_place_and_without_q(inter, D):
-    c = Case(77, 8, 2, D, 128, "bf16", packed=True, interleaved=inter)
+def test_in_place_and_without_q(inter, T, D):
+    c = Case(T, 8, 2, D, 128, "bf16", packed=True, interleaved=inter)
     want = c.run()
     before = c.q.clone()
     got = c.run(q_out=c.q)
@@ -170,15 +179,16 @@ def test_in_place_and_without_q(inter, D):
     c.check(want)
 
 
-def test_rows_are_apart():
+@pytest.mark.parametrize("T", [30, 500])
+def test_rows_are_apart(T):
     """Zero rows, and rows with an infinity or a NaN, leave the others alone."""
-    c = Case(30, 8, 2, 128, 128, "bf16")
+    c = Case(T, 8, 2, 128, 128, "bf16")
     want = c.run()
     c.q[3, 1] = 0
     c.q[4, 2, 5] = float("inf")
     c.q[5, 3, 77] = float("nan")
     got = c.run()
-    same = torch.ones((30, 8), dtype=torch.bool, device="cuda")
+    same = torch.ones((T, 8), dtype=torch.bool, device="cuda")
     same[3, 1] = same[4, 2] = same[5, 3] = False
     assert torch.equal(got[same], want[same])
     assert bool((got[3, 1] == 0).all())
