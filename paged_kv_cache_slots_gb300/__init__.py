@@ -186,6 +186,7 @@ def _ptr(t: torch.Tensor | None):
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(t: torch.Tensor, stream) -> int:
@@ -223,6 +224,17 @@ def _call_on(t: torch.Tensor, lib, fn, *args):
     index = t.get_device()
     # (A host tensor has index -1.  The library does not see what an address is: tensors are the caller's to check.)
     if index < 0 or index == torch.cuda.current_device():
+        status = fn(*args)
+        if status:
+            _check(status, lib)
+        return
+    with torch.cuda.device(index):
+        _check(fn(*args), lib)
+
+
+def _call(index: int, lib, fn, *args):
+    """_call_on for an index that is known to be a GPU's."""
+    if index == _current_device():
         status = fn(*args)
         if status:
             _check(status, lib)
@@ -410,24 +422,33 @@ class KVPool:
         k_weight, q_weight: [head_dim], or [heads, head_dim] with a row for each head, of k's dtype or float32
         (both the same; None: all 1).  The other arguments and the result are append_rope's."""
         head, tail, q_out, _keep = self._rope_call(k, v, slot_mapping, positions, rope, q, q_out, seq_ids, stream, k_scale, v_scale)
-        _need(q is not None or q_weight is None, "q_weight without q")
-        wt, given = k.dtype, [w for w in (k_weight, q_weight) if w is not None]
-        if given:
-            wt = given[0].dtype
-            _need(all(w.dtype == wt for w in given) and wt in (k.dtype, torch.float32), "weights must be of k's dtype or float32")
-        weights = []
-        for w, heads in ((q_weight, 0 if q is None else q.shape[1]), (k_weight, self._kv_heads)):
-            if w is None:
-                weights += [None, 0]
-                continue
-            _need(w.shape in ((self._head_dim,), (heads, self._head_dim)) and w.stride(-1) == 1 and w.get_device() == self._index,
-                  "weights must be [head_dim] or [heads, head_dim], contiguous along head_dim, on the pool's device")
-            _need(w.dim() == 1 or heads == 1 or w.stride(0) == 0 or w.stride(0) >= self._head_dim, "rows of weights overlap")
-            weights += [w.data_ptr(), w.stride(0) if w.dim() == 2 else 0]
-        status = self._lib.kv_append_norm_rope(self._handle, layer, rope._handle, *head, *weights, DTYPE_CODE[wt], float(eps), *tail)
+        wt = k.dtype if k_weight is None and q_weight is None else (q_weight if k_weight is None else k_weight).dtype
+        if wt != k.dtype:
+            _need(wt == torch.float32, "weights must be of k's dtype or float32")
+        kw, ks = self._weights(k_weight, self._kv_heads, wt)
+        if q is not None:
+            qw, qs = self._weights(q_weight, q.shape[1], wt)
+        else:
+            _need(q_weight is None, "q_weight without q")
+            qw, qs = None, 0
+        status = self._lib.kv_append_norm_rope(self._handle, layer, rope._handle, *head, qw, qs, kw, ks, DTYPE_CODE[wt], float(eps), *tail)
         if status:
             _check(status, self._lib)
         return q_out
+
+    def _weights(self, w, heads, dtype):
+        """Address and stride of a head's norm weights."""
+        if w is None:
+            return None, 0
+        D = self._head_dim
+        flat = w.dim() == 1
+        _need(w.dtype == dtype and w.shape == ((D,) if flat else (heads, D)) and w.stride(-1) == 1 and w.get_device() == self._index,
+              "weights must be [head_dim] or [heads, head_dim], both of one dtype, contiguous along head_dim, on the pool's device")
+        if flat:
+            return w.data_ptr(), 0
+        step = w.stride(0)
+        _need(heads == 1 or step == 0 or step >= D, "rows of weights overlap")
+        return w.data_ptr(), step
 
     def _rope_call(self, k, v, slot_mapping, positions, rope, q, q_out, seq_ids, stream, k_scale, v_scale):
         """Checks of append_rope and append_norm_rope; their arguments from seq_ids to num_q_heads, those from
@@ -466,7 +487,8 @@ class KVPool:
             k_scale = v_scale = 1.0
         return ((ids, n, k.data_ptr(), ks[0], v.data_ptr(), vs[0], DTYPE_CODE[dt], slot_mapping.data_ptr(),
                  positions.data_ptr(), n if flat else positions.stride(0), *query),
-                (float(k_scale), float(v_scale), _stream(self.buffer, stream)), q_out, positions)
+                (float(k_scale), float(v_scale), _raw_stream(index) if stream is None and _raw_stream else _stream(self.buffer, stream)),
+                q_out, positions)
 
     def _check_append_rope(self, k, v, slot_mapping, positions, rope, k_scale, v_scale, stream):
         """append_rope's checks one by one; returns positions, contiguous along tokens."""
@@ -593,10 +615,11 @@ def make_free_queue(num_blocks: int, reserve_null_block: bool = False, device=No
 
 def _check_tables(block_tables, lens, *rest):
     _need(block_tables.dim() == 2 and lens.shape == (block_tables.shape[0],), "block_tables [B, max_blocks], lengths [B]")
-    index = block_tables.get_device()
-    _need(index >= 0 and all(t is None or (t.dtype == torch.int32 and t.is_contiguous() and t.get_device() == index)
-                             for t in (block_tables, lens, *rest)),
-          "every tensor must be contiguous int32 on block_tables' GPU")
+    index, i32 = block_tables.get_device(), torch.int32
+    good = index >= 0 and block_tables.dtype == i32 and block_tables.is_contiguous()
+    for t in (lens, *rest):
+        good = good and (t is None or (t.dtype == i32 and t.get_device() == index and t.is_contiguous()))
+    _need(good, "every tensor must be contiguous int32 on block_tables' GPU")
 
 
 def extend_tables(block_tables: torch.Tensor, cached_lens: torch.Tensor, new_lens: torch.Tensor, free_queue: torch.Tensor,
@@ -615,14 +638,16 @@ def extend_tables(block_tables: torch.Tensor, cached_lens: torch.Tensor, new_len
     if out is None:
         out = _made(block_tables, stream, lambda: make_step_tables(block_tables.shape[0], num_tokens, block_tables.device))
     _check_tables(block_tables, cached_lens, new_lens, free_queue, queue_state, *out)
-    B = block_tables.shape[0]
-    _need(new_lens.shape == out.context_lens.shape == (B,) and out.query_start.shape == (B + 1,)
-          and out.slot_mapping.shape == out.positions.shape == out.seq_ids.shape == (num_tokens,)
-          and queue_state.shape == out.queue_state.shape == (2,) and free_queue.dim() == 1, "shapes of the lists (see make_step_tables)")
-    _call_on(block_tables, lib, lib.kv_tables_extend, block_tables.data_ptr(), block_tables.shape[1], cached_lens.data_ptr(),
-             new_lens.data_ptr(), B, block_size, free_queue.shape[0], free_queue.data_ptr(), queue_state.data_ptr(), num_tokens,
-             out.context_lens.data_ptr(), out.query_start.data_ptr(), out.slot_mapping.data_ptr(), out.positions.data_ptr(),
-             out.seq_ids.data_ptr(), out.queue_state.data_ptr(), _stream(block_tables, stream))
+    lens, start, slots, positions, seqs, state = out
+    B, width = block_tables.shape
+    if not (new_lens.shape == lens.shape == (B,) and start.shape == (B + 1,)
+            and slots.shape == positions.shape == seqs.shape == (num_tokens,)
+            and queue_state.shape == state.shape == (2,) and free_queue.dim() == 1):
+        raise ValueError("shapes of the lists (see make_step_tables)")
+    _call(block_tables.get_device(), lib, lib.kv_tables_extend, block_tables.data_ptr(), width, cached_lens.data_ptr(),
+          new_lens.data_ptr(), B, block_size, free_queue.shape[0], free_queue.data_ptr(), queue_state.data_ptr(), num_tokens,
+          lens.data_ptr(), start.data_ptr(), slots.data_ptr(), positions.data_ptr(), seqs.data_ptr(), state.data_ptr(),
+          _stream(block_tables, stream))
     return out
 
 
@@ -904,33 +929,31 @@ def paged_shared_prefix_attention(q, k_cache, v_cache, block_tables, context_len
     return out
 
 
-def _same_gpu(q, *tensors):
-    """Every tensor (None aside) on q's GPU: the library cannot tell a host address from a device one."""
+def _check_window(q, k_cache, v_cache, block_tables, context_lens, query_start, window, sinks, k_scale, v_scale):
+    """The checks of the windowed attention calls one by one; returns window and sinks within 32 bits."""
     index = q.get_device()
-    _need(index >= 0 and all(t is None or t.get_device() == index for t in tensors), "every tensor must be on q's GPU")
-
-
-def _check_caches(q, k_cache, v_cache, k_scale, v_scale) -> bool:
-    """Shapes and types of q and one layer's caches; whether they are E4M3."""
-    _need(q.dim() == 3 and k_cache.dim() == 4 and k_cache.shape[3] == q.shape[2] and v_cache.shape == k_cache.shape,
+    lists = (block_tables, context_lens) if query_start is None else (block_tables, context_lens, query_start)
+    # (The library cannot tell a host address from a device one.)
+    _need(index >= 0 and all(t.get_device() == index for t in (k_cache, v_cache, *lists)), "every tensor must be on q's GPU")
+    _need(k_cache.dim() == 4 and k_cache.shape[3] == q.shape[2] and v_cache.shape == k_cache.shape,
           "q [n, Hq, D], caches [NB, Hkv, bs, D]")
-    fp8 = k_cache.dtype == FP8
-    _need((q.dtype in _ROW_DTYPES and v_cache.dtype == FP8 and k_scale is not None and v_scale is not None) if fp8
-          else (q.dtype in _ROW_DTYPES and q.dtype == k_cache.dtype == v_cache.dtype),
+    _need((q.dtype in _ROW_DTYPES and v_cache.dtype == FP8 and k_scale is not None and v_scale is not None)
+          if k_cache.dtype == FP8 else (q.dtype in _ROW_DTYPES and q.dtype == k_cache.dtype == v_cache.dtype),
           "q and the caches share a dtype, or both caches are E4M3 with k_scale and v_scale")
-    _need(q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous(), "contiguous q and caches")
-    return fp8
-
-
-def _check_out(q, out, out_dtype, workspace):
-    _need(out.dtype == out_dtype and out_dtype in _ROW_DTYPES and out.shape == q.shape and out.is_contiguous(),
-          "out must be contiguous, of q's shape and of out_dtype")
-    _need(workspace.is_contiguous(), "a contiguous workspace")
-
-
-def _check_sight(window, sinks):
+    _need(all(t.is_contiguous() for t in (q, k_cache, v_cache, *lists)), "contiguous inputs")
+    _need(all(t.dtype == torch.int32 for t in lists), "int32 tables and lengths")
+    B = context_lens.shape[0] if query_start is not None else q.shape[0]
+    _need(block_tables.dim() == 2 and block_tables.shape[0] == B and context_lens.shape == (B,)
+          and (query_start is None or query_start.shape == (B + 1,)),
+          "one table row and length per sequence, query_start [sequences + 1]")
     _need(0 < window and 0 <= sinks, "window from 1 on, sinks from 0 on")
     return min(int(window), 0x7FFFFFFF), min(int(sinks), 0x7FFFFFFF)
+
+
+def _check_out(index, shape, out, out_dtype, workspace):
+    if not (out.dtype == out_dtype and out_dtype in _ROW_DTYPES and out.shape == shape and out.is_contiguous()
+            and workspace.is_contiguous() and out.get_device() == index == workspace.get_device()):
+        raise ValueError("out must be contiguous, of q's shape and of out_dtype, the workspace contiguous, both on q's GPU")
 
 
 def paged_window_decode_attention(q, k_cache, v_cache, block_tables, context_lens, scale: float, window: int,
@@ -943,31 +966,35 @@ def paged_window_decode_attention(q, k_cache, v_cache, block_tables, context_len
     those of paged_decode_attention, the workspace too (make_workspace).  Everything runs on
     `stream` (torch's current one unless given)."""
     lib = _lib or load_library()
-    _same_gpu(q, k_cache, v_cache, block_tables, context_lens, out, workspace)
-    fp8 = _check_caches(q, k_cache, v_cache, k_scale, v_scale)
-    B, Hq, D = q.shape
-    NB, Hkv, bs, _ = k_cache.shape
-    window, sinks = _check_sight(window, sinks)
-    _need(block_tables.dtype == context_lens.dtype == torch.int32 and block_tables.is_contiguous()
-          and context_lens.is_contiguous(), "contiguous int32 tables and lengths")
-    _need(block_tables.dim() == 2 and block_tables.shape[0] == B and context_lens.shape == (B,),
-          "one table row and length per sequence")
-    out_dtype = out_dtype or q.dtype
+    B, Hq, D = shape = q.shape
+    cache = k_cache.shape
+    index, dt, kdt, i32 = q.get_device(), q.dtype, k_cache.dtype, torch.int32
+    # The usual call in one expression; _check_window says what is wrong with any other.
+    if not (kdt == v_cache.dtype and dt in _ROW_DTYPES and (dt == kdt or kdt == FP8 and k_scale is not None and v_scale is not None)
+            and len(cache) == 4 and cache[3] == D and v_cache.shape == cache
+            and block_tables.dtype == i32 and context_lens.dtype == i32 and block_tables.dim() == 2
+            and block_tables.shape[0] == B and context_lens.shape == (B,) and 0 < window <= 0x7FFFFFFF
+            and 0 <= sinks <= 0x7FFFFFFF and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and block_tables.is_contiguous() and context_lens.is_contiguous()
+            and 0 <= index == k_cache.get_device() == v_cache.get_device() == block_tables.get_device()
+            == context_lens.get_device()):
+        window, sinks = _check_window(q, k_cache, v_cache, block_tables, context_lens, None, window, sinks, k_scale, v_scale)
+    if out_dtype is None:
+        out_dtype = dt
     if out is None:
-        out = _made(q, stream, lambda: torch.empty((B, Hq, D), dtype=out_dtype, device=q.device))
+        out = _made(q, stream, lambda: torch.empty(shape, dtype=out_dtype, device=q.device))
     if workspace is None:
-        workspace = _made(q, stream, lambda: make_workspace(B, Hq, Hkv, D, q.device, **opts))
-    _check_out(q, out, out_dtype, workspace)
-    o = ctypes.byref(_options(**opts)) if opts else None
-    sizes = (NB, block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, Hq, Hkv, D, bs)
+        workspace = _made(q, stream, lambda: make_workspace(B, Hq, cache[1], D, q.device, **opts))
+    _check_out(index, shape, out, out_dtype, workspace)
+    sizes = (cache[0], block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, Hq, cache[1], D, cache[2])
     rest = (float(scale), window, sinks, out.data_ptr(), DTYPE_CODE[out_dtype], workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), o, _stream(q, stream))
-    if fp8:
-        _call_on(q, lib, lib.paged_window_decode_attention_fp8, q.data_ptr(), DTYPE_CODE[q.dtype], k_cache.data_ptr(),
-                 v_cache.data_ptr(), float(k_scale), float(v_scale), *sizes, *rest)
+            workspace.numel() * workspace.element_size(), ctypes.byref(_options(**opts)) if opts else None, _stream(q, stream))
+    if kdt == FP8:
+        _call(index, lib, lib.paged_window_decode_attention_fp8, q.data_ptr(), DTYPE_CODE[dt], k_cache.data_ptr(),
+              v_cache.data_ptr(), float(k_scale), float(v_scale), *sizes, *rest)
     else:
-        _call_on(q, lib, lib.paged_window_decode_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *sizes,
-                 DTYPE_CODE[q.dtype], *rest)
+        _call(index, lib, lib.paged_window_decode_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *sizes,
+              DTYPE_CODE[dt], *rest)
     return out
 
 
@@ -998,32 +1025,37 @@ def paged_window_prefill_attention(q, k_cache, v_cache, block_tables, query_star
     the last sequence (query_start[-1]) are padding: those rows of out stay as they are (a new out holds
     zeros there).  Everything runs on `stream` (torch's current one unless given)."""
     lib = _lib or load_library()
-    _same_gpu(q, k_cache, v_cache, block_tables, query_start, context_lens, out, workspace)
-    fp8 = _check_caches(q, k_cache, v_cache, k_scale, v_scale)
-    T, Hq, D = q.shape
-    NB, Hkv, bs, _ = k_cache.shape
+    T, Hq, D = shape = q.shape
+    cache = k_cache.shape
     B = context_lens.shape[0]
-    window, sinks = _check_sight(window, sinks)
-    _need(block_tables.dtype == context_lens.dtype == query_start.dtype == torch.int32 and block_tables.is_contiguous()
-          and context_lens.is_contiguous() and query_start.is_contiguous(), "contiguous int32 tables and lengths")
-    _need(block_tables.dim() == 2 and block_tables.shape[0] == B and context_lens.shape == (B,)
-          and query_start.shape == (B + 1,), "one table row and length per sequence, query_start [sequences + 1]")
-    out_dtype = out_dtype or q.dtype
+    index, dt, kdt, i32 = q.get_device(), q.dtype, k_cache.dtype, torch.int32
+    if not (kdt == v_cache.dtype and dt in _ROW_DTYPES and (dt == kdt or kdt == FP8 and k_scale is not None and v_scale is not None)
+            and len(cache) == 4 and cache[3] == D and v_cache.shape == cache
+            and block_tables.dtype == i32 and context_lens.dtype == i32 and query_start.dtype == i32
+            and block_tables.dim() == 2 and block_tables.shape[0] == B and context_lens.shape == (B,)
+            and query_start.shape == (B + 1,) and 0 < window <= 0x7FFFFFFF and 0 <= sinks <= 0x7FFFFFFF
+            and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous() and block_tables.is_contiguous()
+            and context_lens.is_contiguous() and query_start.is_contiguous()
+            and 0 <= index == k_cache.get_device() == v_cache.get_device() == block_tables.get_device()
+            == context_lens.get_device() == query_start.get_device()):
+        window, sinks = _check_window(q, k_cache, v_cache, block_tables, context_lens, query_start, window, sinks, k_scale, v_scale)
+    if out_dtype is None:
+        out_dtype = dt
     if out is None:
-        out = _made(q, stream, lambda: torch.zeros((T, Hq, D), dtype=out_dtype, device=q.device))
+        out = _made(q, stream, lambda: torch.zeros(shape, dtype=out_dtype, device=q.device))
     if workspace is None:
-        workspace = _made(q, stream, lambda: make_window_prefill_workspace(B, T, Hq, Hkv, D, q.device))
-    _check_out(q, out, out_dtype, workspace)
-    sizes = (NB, block_tables.data_ptr(), block_tables.shape[1], query_start.data_ptr(), context_lens.data_ptr(), B, T,
-             Hq, Hkv, D, bs)
+        workspace = _made(q, stream, lambda: make_window_prefill_workspace(B, T, Hq, cache[1], D, q.device))
+    _check_out(index, shape, out, out_dtype, workspace)
+    sizes = (cache[0], block_tables.data_ptr(), block_tables.shape[1], query_start.data_ptr(), context_lens.data_ptr(), B, T,
+             Hq, cache[1], D, cache[2])
     rest = (float(scale), window, sinks, out.data_ptr(), DTYPE_CODE[out_dtype], workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), _stream(q, stream))
-    if fp8:
-        _call_on(q, lib, lib.paged_window_prefill_attention_fp8, q.data_ptr(), DTYPE_CODE[q.dtype], k_cache.data_ptr(),
-                 v_cache.data_ptr(), float(k_scale), float(v_scale), *sizes, *rest)
+    if kdt == FP8:
+        _call(index, lib, lib.paged_window_prefill_attention_fp8, q.data_ptr(), DTYPE_CODE[dt], k_cache.data_ptr(),
+              v_cache.data_ptr(), float(k_scale), float(v_scale), *sizes, *rest)
     else:
-        _call_on(q, lib, lib.paged_window_prefill_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *sizes,
-                 DTYPE_CODE[q.dtype], *rest)
+        _call(index, lib, lib.paged_window_prefill_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *sizes,
+              DTYPE_CODE[dt], *rest)
     return out
 
 

@@ -190,6 +190,9 @@ struct Sight {
     int window, sinks;
 };
 
+// Bytes of K and V in sight up to which a windowed decode takes the kernel for small calls.
+constexpr int64_t kSmallWindowBytes = int64_t{1} << 40;
+
 kv_status_t check_sight(const Sight& w, int max_blocks, int block_size) {
     if (w.window < 1 || w.sinks < 0)
         return fail(KV_ERR_INVALID_ARG, "window %d (from 1 on), sinks %d (from 0 on)", w.window, w.sinks);
@@ -830,7 +833,8 @@ kv_status_t kv_tables_extend(int32_t* block_tables, int max_blocks, const int32_
     for (const auto& x : in)
         if (!aligned(x.p, 4)) return fail(KV_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", what);
     TablesArgs a{};
-    if (kv_status_t st = device_info(&a.device, &a.status, nullptr, nullptr, nullptr)) return st;
+    int sms = 0;
+    if (kv_status_t st = device_info(&a.device, &a.status, &sms, nullptr, nullptr)) return st;
     a.block_tables = block_tables;
     a.cached_lens = cached_lens;
     a.new_lens = new_lens;
@@ -847,7 +851,7 @@ kv_status_t kv_tables_extend(int32_t* block_tables, int max_blocks, const int32_
     a.block_size = block_size;
     a.num_blocks = num_blocks;
     a.num_tokens = num_tokens;
-    cudaError_t e = launch_tables_extend(a, static_cast<cudaStream_t>(stream));
+    cudaError_t e = launch_tables_extend(a, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "tables launch");
     return KV_OK;
 }
@@ -1083,6 +1087,21 @@ static kv_status_t decode_impl(const void* q, const void* k_cache, const void* v
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     CUtensorMap tk, tv;
+    if (sight && kernel == KV_KERNEL_MMA && !(opts && (o.num_ctas || o.ctas_per_sm > 1 || o.consumer_warps || o.heads_per_stage ||
+                                                       o.separate_reduce || o.test_stall))) {
+        SmallPlan small{};
+        const int half = block_size * head_dim * dtype_bytes(kv_dtype);
+        const int64_t bytes = static_cast<int64_t>(num_seqs) * row_blocks * num_kv_heads * 2 * half;
+        if (bytes <= kSmallWindowBytes && plan_window_small(num_seqs, num_kv_heads, row_blocks, half, sms, max_smem, &small)) {
+            const int rows = num_blocks * num_kv_heads * block_size;
+            if (kv_status_t st = encode_cache_map(&tk, k_cache, kv_dtype, rows, head_dim, block_size)) return st;
+            if (kv_status_t st = encode_cache_map(&tv, v_cache, kv_dtype, rows, head_dim, block_size)) return st;
+            a.heads_per_stage = 1;
+            e = launch_window_decode_small(a, tk, tv, small, s);
+            if (e != cudaSuccess) return cuda_fail(e, "windowed decode launch");
+            return KV_OK;
+        }
+    }
     if (kernel == KV_KERNEL_MMA) {
         const int rows = num_blocks * num_kv_heads * block_size;
         if (kv_status_t st = encode_cache_map(&tk, k_cache, kv_dtype, rows, head_dim, hc * block_size)) return st;

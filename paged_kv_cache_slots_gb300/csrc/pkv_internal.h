@@ -226,7 +226,7 @@ cudaError_t launch_append_rope(const RopeArgs& a, int align, int num_sms, cudaSt
 cudaError_t launch_append_norm_rope(const NormRopeArgs& a, int align, int weight_align, int num_sms,
                                     cudaStream_t stream);
 cudaError_t launch_slot_mapping(const SlotArgs& a, cudaStream_t stream);
-cudaError_t launch_tables_extend(const TablesArgs& a, cudaStream_t stream);
+cudaError_t launch_tables_extend(const TablesArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_tables_release(const TablesArgs& a, cudaStream_t stream);
 cudaError_t launch_swap(const SwapArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
@@ -247,6 +247,15 @@ cudaError_t launch_decode_fp8(const DecodeArgs& a, const CUtensorMap& tmap_k,
                               const CUtensorMap& tmap_v, cudaStream_t stream);
 cudaError_t launch_window_decode_mma(const WindowArgs& a, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
                                      cudaStream_t stream);
+// Small calls (window_decode_small.cu): CTAs of a cluster and warps of a CTA for each
+// (sequence, KV head).  row_blocks: the most blocks that a query sees.
+struct SmallPlan {
+    int ctas, warps, smem_bytes;
+};
+bool plan_window_small(int num_seqs, int num_kv_heads, int row_blocks, int stage_half_bytes, int num_sms, int max_smem,
+                       SmallPlan* plan);
+cudaError_t launch_window_decode_small(const WindowArgs& a, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
+                                       const SmallPlan& plan, cudaStream_t stream);
 cudaError_t launch_window_decode_ffma(const WindowArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_reduce(const DecodeArgs& a, cudaStream_t stream);
 

@@ -12,12 +12,14 @@
 // The sums never decrease, so a granted sequence's blocks start where those of the
 // granted ones before it end, and two prefix sums settle everything.
 //
-// Work split.  One cluster of up to 8 CTAs, so that a step is one launch without a
-// workspace: each CTA makes both prefix sums of the whole batch in its shared
-// memory (a few loads and shuffles a thread), the cluster meets once, so that
-// outputs may be the inputs' own buffers, and each CTA fills its share of the token
-// lists and new table entries, finding a token's sequence by bisection.  Bound:
-// latency (a launch, three dependent rounds of loads); a token costs 12 bytes.
+// Work split.  Every CTA makes both prefix sums of the whole batch in its shared
+// memory (a few loads and shuffles a thread), so that the CTAs need neither each
+// other nor a workspace, and fills its share of the token lists and new table
+// entries, finding a token's sequence by bisection.  The lengths and the queue's
+// state, which may be updated in place, are written by the CTA itself where there
+// is one, and else by a launch behind it (one cluster of 8 CTAs that meets before
+// it writes took 35 us for 262,144 tokens of 1,000 sequences).  Bound: latency (a
+// launch, three dependent rounds of loads); a token costs 12 bytes.
 #include <cooperative_groups.h>
 
 #include "device_utils.cuh"
@@ -108,18 +110,23 @@ __device__ __forceinline__ int ring(int head, int x, int capacity) {
     return static_cast<int>(y >= static_cast<uint32_t>(capacity) ? y - static_cast<uint32_t>(capacity) : y);
 }
 
+// What a launch writes: the lists and table entries, or the lengths and the queue's
+// state, or both (one CTA).
+enum Part { kBoth, kLists, kLengths };
+
+template <Part kPart>
 __global__ void __launch_bounds__(kThreads, 1) kv_tables_extend_kernel(const TablesArgs a) {
     extern __shared__ int32_t lists[];
     __shared__ int64_t tmp[2 * kWarps];
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
+    const int rank = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
     const int B = a.num_seqs, bs = a.block_size, tid = threadIdx.x;
     int32_t* first_token = lists;              // [B] of each sequence, among the step's
     int32_t* first_block = lists + B;          // [B] of each sequence, among the step's new ones
     int32_t* held = lists + 2 * B;             // [B] cached tokens
     pdl_allow_next();
     pdl_wait();
-    const Queue q = queue_of(a.queue_state, a.num_blocks, rank == 0 ? a.status : nullptr);
+    const bool reports = rank == 0 && kPart != kLengths;
+    const Queue q = queue_of(a.queue_state, a.num_blocks, reports ? a.status : nullptr);
 
     int64_t asked_tokens = 0, asked_blocks = 0;  // of the sequences before this round's
     int tokens = 0, blocks = 0;                  // granted
@@ -131,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tables_extend_kernel(const Tab
             n = a.new_lens[s];
             const int64_t end = static_cast<int64_t>(c) + n;
             if (c < 0 || n < 0 || end > static_cast<int64_t>(a.max_blocks) * bs) {
-                if (rank == 0) raise_flag(a.status, kFlagBadContext);
+                if (reports) raise_flag(a.status, kFlagBadContext);
                 n = 0;
             } else {
                 need = static_cast<int>((end + bs - 1) / bs) - (c + bs - 1) / bs;
@@ -154,13 +161,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tables_extend_kernel(const Tab
         tokens += t_all;
         blocks += b_all;
     }
-    // Every CTA has read what it needs of the buffers that are now written.
-    if (ctas > 1)
-        cluster.sync();
-    else
-        __syncthreads();
-
-    if (rank == 0) {
+    __syncthreads();  // the CTA has read what it needs of the buffers that are now written
+    if constexpr (kPart != kLists) {
         for (int s = tid; s < B; s += kThreads) {
             const int n = (s + 1 < B ? first_token[s + 1] : tokens) - first_token[s];
             a.query_start[s] = first_token[s];
@@ -172,6 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tables_extend_kernel(const Tab
             a.queue_state_out[1] = q.count - blocks;
         }
     }
+    if constexpr (kPart == kLengths) return;
     // New block x of the step, as its table entry (-1: the queue holds no block there).
     auto block_at = [&](int x) {
         const int id = a.free_queue[ring(q.head, x, a.num_blocks)];
@@ -313,11 +316,20 @@ cudaError_t launch_cluster(void (*kernel)(const TablesArgs), RaisedLimit* limit,
 
 }  // namespace
 
-cudaError_t launch_tables_extend(const TablesArgs& a, cudaStream_t stream) {
-    static RaisedLimit limit;
-    int ctas = 1;  // one while a thread has two tokens at most
-    while (ctas < kMaxCluster && static_cast<int64_t>(a.num_tokens) > int64_t{2} * kThreads * ctas) ctas <<= 1;
-    return launch_cluster(kv_tables_extend_kernel, &limit, a, 3 * 4 * a.num_seqs, ctas, stream);
+cudaError_t launch_tables_extend(const TablesArgs& a, int num_sms, cudaStream_t stream) {
+    static RaisedLimit limits[3];
+    const int smem = 3 * 4 * a.num_seqs;
+    auto launch = [&](auto kernel, RaisedLimit* limit, int ctas) {
+        const cudaError_t e = allow_shared_memory(kernel, a.device, smem, limit);
+        if (e != cudaSuccess) return e;
+        return launch_kernel(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), static_cast<size_t>(smem), stream, true, a);
+    };
+    // One CTA while a thread has four tokens at most; else two tokens a thread, on one CTA an SM at most.
+    const int64_t ctas = (static_cast<int64_t>(a.num_tokens) + 2 * kThreads - 1) / (2 * kThreads);
+    if (ctas <= 2) return launch(kv_tables_extend_kernel<kBoth>, &limits[0], 1);
+    const cudaError_t e = launch(kv_tables_extend_kernel<kLists>, &limits[1], static_cast<int>(ctas < num_sms ? ctas : num_sms));
+    if (e != cudaSuccess) return e;
+    return launch(kv_tables_extend_kernel<kLengths>, &limits[2], 1);
 }
 
 cudaError_t launch_tables_release(const TablesArgs& a, cudaStream_t stream) {

@@ -193,14 +193,37 @@ def test_decode_outputs_and_repetition():
 def test_decode_whole_context_is_the_plain_decode():
     b = Batch([3000, 150, 1, 0, 999], 1 << 20, 0, dtype="f16", Hkv=4)
     full = pkv.paged_decode_attention(b.q, b.kc, b.vc, b.tables, b.ctx, b.scale)
+    b.check(full)
     for sinks in (0, 4, 5000):
-        assert torch.equal(full, b.run(torch.float16, sinks=sinks))
+        # with a launch shape the same kernel, bit for bit; else one that sums in another order
+        assert torch.equal(full, b.run(torch.float16, sinks=sinks, consumer_warps=8))
+        b.check(b.run(torch.float16, sinks=sinks))
 
 
 def test_decode_many_sequences():
     rng = np.random.default_rng(5)
     b = Batch(rng.integers(0, 3000, 300).tolist(), 129, 3, dtype="bf16", G=8, Hkv=1)
     b.check(b.run(torch.bfloat16))
+    b.check(b.run(torch.bfloat16, consumer_warps=8))
+
+
+@pytest.mark.parametrize("shape", [dict(consumer_warps=8), dict(num_ctas=40)])
+@pytest.mark.parametrize("dtype,D,G,bs,fp8", [("f16", 64, 2, 16, False), ("bf16", 128, 8, 32, False), ("bf16", 128, 4, 16, True),
+                                              ("f16", 128, 8, 48, True), ("bf16", 128, 8, 16, True)])
+def test_decode_with_a_launch_shape(shape, dtype, D, G, bs, fp8):
+    """The persistent kernel, at sizes that otherwise go to the one for small calls."""
+    for window, sinks in ((40, 20), (1, 0), (300, 5)):
+        b = Batch(LENGTHS + [3000], window, sinks, dtype=dtype, G=G, D=D, bs=bs, fp8=fp8)
+        b.check(b.run(**shape))
+
+
+@pytest.mark.parametrize("B", [1, 2, 5, 40])
+@pytest.mark.parametrize("dtype,bs,fp8", [("bf16", 16, False), ("f16", 128, False), ("bf16", 64, True)])
+def test_decode_small_calls(B, dtype, bs, fp8):
+    """Clusters of every size: few and many heads, more blocks than warps."""
+    for Hkv in (1, 8):
+        b = Batch([(i * 977) % 5000 + 1 for i in range(B)], 2000, 17, dtype=dtype, Hkv=Hkv, bs=bs, fp8=fp8)
+        b.check(b.run())
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.7, 3.0])
