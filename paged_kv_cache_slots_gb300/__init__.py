@@ -474,12 +474,15 @@ class KVPool:
             if q_out is None:
                 make = torch.empty if seq_ids is None else torch.zeros
                 q_out = _made(self.buffer, stream, lambda: make(q.shape, dtype=q.dtype, device=q.device))
-            _need(q.dtype == dt and q.dim() == 3 and q.shape[0] == n and q.shape[2] == D and _rows_whole(q)
-                  and q.get_device() == index,
-                  "q must be [n_tokens, num_q_heads, head_dim] of k's dtype on the pool's device, a token's rows contiguous")
-            _need(q_out.dtype == dt and q_out.shape == q.shape and _rows_whole(q_out) and q_out.get_device() == index,
-                  "q_out must be like q")
-            query = (q.data_ptr(), q.stride(0), q_out.data_ptr(), q_out.stride(0), q.shape[1])
+            shape, qs, os = q.shape, q.stride(), q_out.stride()
+            if not (q.dtype == dt == q_out.dtype and q_out.shape == shape and len(shape) == 3 and shape[0] == n and shape[2] == D
+                    and qs[1:] == os[1:] == (D, 1) and q.get_device() == index == q_out.get_device()):
+                _need(q.dtype == dt and q.dim() == 3 and q.shape[0] == n and q.shape[2] == D and _rows_whole(q)
+                      and q.get_device() == index,
+                      "q must be [n_tokens, num_q_heads, head_dim] of k's dtype on the pool's device, a token's rows contiguous")
+                _need(q_out.dtype == dt and q_out.shape == q.shape and _rows_whole(q_out) and q_out.get_device() == index,
+                      "q_out must be like q")
+            query = (q.data_ptr(), qs[0], q_out.data_ptr(), os[0], shape[1])
         else:
             _need(q_out is None, "q_out without q")
             query = (None, 0, None, 0, 0)

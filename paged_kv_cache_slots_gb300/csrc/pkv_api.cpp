@@ -190,8 +190,19 @@ struct Sight {
     int window, sinks;
 };
 
-// Bytes of K and V in sight up to which a windowed decode takes the kernel for small calls.
-constexpr int64_t kSmallWindowBytes = int64_t{1} << 40;
+// Whether a windowed decode takes the kernel for small calls (window_decode_small.cu) rather than the persistent
+// one.  By what a head's K rows of a block take (half) and what is in sight; both measured in graphs, inputs out of
+// L2, 8 KV heads of 128, microseconds small / persistent:
+//   4 KiB (16 tokens of 16 bits, 32 codes): 16 sequences x 1,024 (67 MB) 17.3 / 19.8, 32 x 1,024 (134 MB) 31.5 / 27.1,
+//     8 x 4,096 (134 MB) 29.0 / 29.0, 16 x 4,096 51 / 44; 32 x 512 (67 MB) 21.1 / 18.7, E4M3 64 x 128 (17 MB) 15.5 / 16.6,
+//     E4M3 128 x 128 (34 MB) 28.2 / 20.7;
+//   8 KiB: 16 x 4,096 (268 MB) 45 / 57, 64 x 1,024 (268 MB) 55.1 / 55.2, 32 x 4,096 (537 MB) 90 / 87;
+//   from 16 KiB on, where the persistent kernel's stages hold one or two heads: 128 x 1,024 (537 MB) 101 / 138.
+bool small_window(int64_t bytes, int64_t pairs, int half, int sms) {
+    if (half >= 16384) return true;
+    if (half >= 8192) return bytes <= int64_t{256} << 20;
+    return bytes <= (pairs <= sms ? int64_t{128} << 20 : pairs <= 4 * sms ? int64_t{32} << 20 : 0);
+}
 
 kv_status_t check_sight(const Sight& w, int max_blocks, int block_size) {
     if (w.window < 1 || w.sinks < 0)
@@ -1092,7 +1103,8 @@ static kv_status_t decode_impl(const void* q, const void* k_cache, const void* v
         SmallPlan small{};
         const int half = block_size * head_dim * dtype_bytes(kv_dtype);
         const int64_t bytes = static_cast<int64_t>(num_seqs) * row_blocks * num_kv_heads * 2 * half;
-        if (bytes <= kSmallWindowBytes && plan_window_small(num_seqs, num_kv_heads, row_blocks, half, sms, max_smem, &small)) {
+        if (small_window(bytes, static_cast<int64_t>(num_seqs) * num_kv_heads, half, sms) &&
+            plan_window_small(num_seqs, num_kv_heads, row_blocks, half, sms, max_smem, &small)) {
             const int rows = num_blocks * num_kv_heads * block_size;
             if (kv_status_t st = encode_cache_map(&tk, k_cache, kv_dtype, rows, head_dim, block_size)) return st;
             if (kv_status_t st = encode_cache_map(&tv, v_cache, kv_dtype, rows, head_dim, block_size)) return st;

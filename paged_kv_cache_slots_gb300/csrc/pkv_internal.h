@@ -250,7 +250,7 @@ cudaError_t launch_window_decode_mma(const WindowArgs& a, const CUtensorMap& tma
 // Small calls (window_decode_small.cu): CTAs of a cluster and warps of a CTA for each
 // (sequence, KV head).  row_blocks: the most blocks that a query sees.
 struct SmallPlan {
-    int ctas, warps, smem_bytes;
+    int ctas, warps, stages, smem_bytes;
 };
 bool plan_window_small(int num_seqs, int num_kv_heads, int row_blocks, int stage_half_bytes, int num_sms, int max_smem,
                        SmallPlan* plan);

@@ -22,15 +22,21 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kMaxWarps = 8;
-constexpr int kStages = 2;  // of each warp
+constexpr int kMaxStages = 2;  // of each warp
+
+// Shared memory of a warp: its stages, or its state if that is larger (8 heads of 130 floats).
+__host__ __device__ inline uint32_t warp_bytes(int stages, uint32_t half) {
+    return stages * 2 * half < 5120u ? 5120u : stages * 2 * half;
+}
 
 template <class Policy>
-__global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_window_decode_small_kernel(const WindowArgs a,
+__global__ void __launch_bounds__(32 * kMaxWarps, 2) paged_window_decode_small_kernel(const WindowArgs a,
                                                                                        const __grid_constant__ CUtensorMap tmk,
                                                                                        const __grid_constant__ CUtensorMap tmv) {
+    const int kStages = a.stages;
     constexpr int D = Policy::kD;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[kMaxWarps][kStages];
+    __shared__ uint64_t full[kMaxWarps][kMaxStages];
     __shared__ int abort_flag;
     __shared__ float joined[8 * (D + 2)];  // the CTA's state: [head][O, maximum, sum]
     cg::cluster_group cluster = cg::this_cluster();
@@ -68,7 +74,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_window_decode_small_k
     auto logical = [&](int j) { return j + (j >= a.sink_blocks ? skip : 0); };
     const int first = warp * ctas + rank, step = warps * ctas;
     const int mine = first < blocks ? (blocks - first + step - 1) / step : 0;
-    uint8_t* stages = base + warp * (kStages * 2 * half);
+    uint8_t* stages = base + warp * warp_bytes(kStages, half);
     const uint64_t policy = policy_evict_first();
     // Row of block `k` of this warp's in the caches' tensor maps.
     auto row_of = [&](int k) {
@@ -90,9 +96,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_window_decode_small_k
         }
     };
     if (lane == 0 && mine > 0) {
-        const int r0 = row_of(0), r1 = mine > 1 ? row_of(1) : 0;
+        const bool second = mine > 1 && kStages > 1;
+        const int r0 = row_of(0), r1 = second ? row_of(1) : 0;
         fetch(0, r0);
-        if (mine > 1) fetch(1, r1);
+        if (second) fetch(1, r1);
     }
     Policy pol;
     typename Policy::State st;
@@ -135,7 +142,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_window_decode_small_k
         *m = M;
         *l = L;
     };
-    const int floats = kStages * 2 * static_cast<int>(half) / 4;  // between two warps' states
+    const int floats = static_cast<int>(warp_bytes(kStages, half)) / 4;  // between two warps' states
     auto of_warp = [&](int i) { return reinterpret_cast<const float*>(base) + static_cast<int64_t>(i) * floats; };
     if (ctas == 1) {
         for (int e = tid; e < G * D; e += blockDim.x) {
@@ -167,9 +174,11 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_window_decode_small_k
 }
 
 template <class Policy>
-cudaError_t launch(const WindowArgs& a, const CUtensorMap& tmk, const CUtensorMap& tmv, const SmallPlan& plan,
+cudaError_t launch(const WindowArgs& args, const CUtensorMap& tmk, const CUtensorMap& tmv, const SmallPlan& plan,
                    cudaStream_t stream) {
     static RaisedLimit limit;
+    WindowArgs a = args;
+    a.stages = plan.stages;
     auto kern = paged_window_decode_small_kernel<Policy>;
     const cudaError_t e = allow_shared_memory(kern, a.device, plan.smem_bytes, &limit);
     if (e != cudaSuccess) return e;
@@ -194,18 +203,27 @@ cudaError_t launch(const WindowArgs& a, const CUtensorMap& tmk, const CUtensorMa
 bool plan_window_small(int num_seqs, int num_kv_heads, int row_blocks, int stage_half_bytes, int num_sms, int max_smem,
                        SmallPlan* plan) {
     const int64_t pairs = static_cast<int64_t>(num_seqs) * num_kv_heads;
-    const int per_warp = kStages * 2 * stage_half_bytes;
-    // A warp for each block up to eight, as far as shared memory goes.
-    int warps = (max_smem - 8 * 1024) / per_warp;
+    auto bytes = [&](int stages) { return static_cast<int>(warp_bytes(stages, stage_half_bytes)); };
+    const int room = max_smem - 8 * 1024;
+    // A warp for each block up to eight, as far as shared memory goes; two stages for a warp with several blocks.
+    int warps = room / bytes(1);
     if (warps > kMaxWarps) warps = kMaxWarps;
     if (warps > row_blocks) warps = row_blocks;
     if (warps < 1) return false;
+    auto stages = [&](int ctas) { return row_blocks > ctas * warps && warps * bytes(2) <= room ? 2 : 1; };
+    auto smem = [&](int ctas) { return warps * bytes(stages(ctas)) + 1024; };
+    // Larger clusters while warps have more than one block and the grid stays within what the SMs hold at once.
     int ctas = 1;
-    while (ctas < 8 && row_blocks > ctas * warps && 2 * ctas * pairs <= 2 * num_sms) ctas *= 2;
+    while (ctas < 8 && row_blocks > ctas * warps) {
+        const int per_sm = 2 * (smem(2 * ctas) + 8 * 1024) <= max_smem ? 2 : 1;
+        if (2 * ctas * pairs > static_cast<int64_t>(num_sms) * per_sm) break;
+        ctas *= 2;
+    }
     if (pairs * ctas >= (int64_t{1} << 31)) return false;
     plan->warps = warps;
     plan->ctas = ctas;
-    plan->smem_bytes = warps * per_warp + 1024;
+    plan->stages = stages(ctas);
+    plan->smem_bytes = smem(ctas);
     return true;
 }
 
