@@ -18,7 +18,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "lib")
 LIBRARY = os.path.join(LIB_DIR, "libpkv.so")
 SOURCES = ["append.cu", "rope.cu", "norm_rope.cu", "tables.cu", "decode_plan.cu", "decode_ffma.cu", "decode_mma.cu", "decode_fp8.cu",
-           "decode_static.cu", "window_decode.cu", "window_decode_ffma.cu", "window_decode_small.cu", "window_prefill.cu", "window_prefill_tc.cu", "shared_prefix.cu", "shared_prefix_f16.cu",
+           "decode_static.cu", "window_decode.cu", "window_decode_ffma.cu", "window_decode_small.cu", "window_prefill_tc.cu", "window_prefill_tc_fp8.cu", "shared_prefix.cu", "shared_prefix_f16.cu",
            "shared_prefix_bf16.cu", "shared_prefix_fp8.cu",
            "prefix_pool.cpp", "swap.cu", "prefill.cu", "prefill_tc.cu",
            "pkv_api.cpp"]

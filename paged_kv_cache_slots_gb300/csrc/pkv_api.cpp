@@ -1327,7 +1327,7 @@ static kv_status_t prefill_impl(const void* q, const void* k_cache, const void* 
     const int raw_bytes = fp8 ? 4 * block_size * head_dim : 0;
     int stages = (max_smem - 2048 - 64 - raw_bytes) / stage_bytes;
     if (stages > 4) stages = 4;
-    const bool window_tc = sight && !fp8 && dtype != KV_F32;
+    const bool window_tc = sight && dtype != KV_F32;
     if (!tc && !window_tc && dtype != KV_F32 && stages < 2) return fail(KV_ERR_UNSUPPORTED, "shared memory cannot hold two stages");
     PrefillArgs a{};
     if (sight) set_sight(*sight, max_blocks, block_size, &a);
@@ -1374,8 +1374,10 @@ static kv_status_t prefill_impl(const void* q, const void* k_cache, const void* 
         const int rows = num_blocks * num_kv_heads * block_size;
         CUtensorMap tq{};
         if (kv_status_t st = encode_query_map(&tq, q, dtype, num_tokens, num_q_heads, head_dim, G, 128 / G)) return st;
-        if (kv_status_t st = encode_group_map(&tk, k_cache, dtype, rows, head_dim, a.box)) return st;
-        if (kv_status_t st = encode_group_map(&tv, v_cache, dtype, rows, head_dim, a.box)) return st;
+        if (!fp8) {  // (E4M3 codes come by bulk copies)
+            if (kv_status_t st = encode_group_map(&tk, k_cache, dtype, rows, head_dim, a.box)) return st;
+            if (kv_status_t st = encode_group_map(&tv, v_cache, dtype, rows, head_dim, a.box)) return st;
+        }
         cudaError_t e = launch_window_prefill_tc(a, tq, tk, tv, sms, static_cast<cudaStream_t>(stream));
         if (e != cudaSuccess) return cuda_fail(e, "windowed prefill launch");
         return KV_OK;

@@ -231,10 +231,9 @@ cudaError_t launch_tables_release(const TablesArgs& a, cudaStream_t stream);
 cudaError_t launch_swap(const SwapArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
                            cudaStream_t stream);
-cudaError_t launch_window_prefill(const PrefillArgs& a, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
-                                  cudaStream_t stream);
 cudaError_t launch_window_prefill_tc(const PrefillArgs& a, const CUtensorMap& tmap_q, const CUtensorMap& tmap_k,
                                      const CUtensorMap& tmap_v, int num_sms, cudaStream_t stream);
+cudaError_t launch_window_prefill_tc_fp8(const PrefillArgs& a, const CUtensorMap& tmap_q, int ctas, cudaStream_t stream);
 int window_prefill_tc_smem_bytes(int head_dim);
 cudaError_t launch_slot_mapping_varlen(const PrefillArgs& a, int32_t* slots, cudaStream_t stream);
 cudaError_t launch_prefill_tc(const PrefillArgs& a, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
