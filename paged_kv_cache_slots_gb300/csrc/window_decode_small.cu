@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) paged_window_decode_small_k
     typename Policy::State st;
     pol.begin(st, a, s, h, G);
     bool ok = true;
-    for (int k = 0; k < mine; ++k) {
+    int k = 0;
+    for (; k < mine; ++k) {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[warp][k % kStages], (k / kStages) & 1, abort, a.status));
         if (!ok) break;
         int row = 0;
@@ -118,9 +119,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) paged_window_decode_small_k
         if (lane == 0 && k + kStages < mine) fetch(k + kStages, row);
     }
     if (!ok && lane == 0) {  // what was issued lands before the CTA ends (a wait gave up; bounded)
-        for (int k = 0; k < kStages && k < mine; ++k) {
+        for (int j = k; j < mine && j < k + kStages; ++j) {
             const uint64_t t0 = global_timer_ns();
-            while (!mbar_try_wait(&full[warp][k], 0) && global_timer_ns() - t0 < kWaitLimitNs) {
+            while (!mbar_try_wait(&full[warp][j % kStages], (j / kStages) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {
             }
         }
     }

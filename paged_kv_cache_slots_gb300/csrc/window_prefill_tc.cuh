@@ -56,50 +56,74 @@ __device__ __forceinline__ float cached(const void* row, int i) {
 }
 
 // One output row on the CUDA cores, by one warp: query head `head` of token `tok`
-// (position pos of sequence s), lane l's dims VD*l .. VD*l + VD - 1; only the keys
-// in sight are read.
+// (position pos of sequence s); only the keys in sight are read, 32 at a time: a lane
+// a key for the scores, then lane l's dims VD*l .. VD*l + VD - 1 of all 32.  What
+// makes every element NaN ends it (rows come here by the thousand where a model's
+// values are NaN throughout).
 template <int DT, int KT, int D>
 __device__ __noinline__ void exact_row(const PrefillArgs& a, int s, int h, int64_t tok, int head, int pos) {
     constexpr int VD = D / 32;
     using T = typename Elem<DT>::T;
     const int lane = threadIdx.x & 31;
     const int eb = KT == kFP8 ? 1 : static_cast<int>(sizeof(T));
-    const int64_t row = (tok * a.num_q_heads + head) * D + VD * lane;
-    float q[VD], o[VD];
+    const int64_t row = (tok * a.num_q_heads + head) * D;
+    const T* q = static_cast<const T*>(a.q) + row;
+    const int from = max(0, pos - a.window + 1), first = min(a.sinks, from);
+    const int total = first + pos - from + 1;
+    float o[VD];
 #pragma unroll
-    for (int i = 0; i < VD; ++i) {
-        q[i] = Elem<DT>::to_float(static_cast<const T*>(a.q)[row + i]) * a.scale_log2;
-        o[i] = 0.f;
-    }
+    for (int i = 0; i < VD; ++i) o[i] = 0.f;
     float m = -INFINITY, l = 0.f;
-    const int from = max(0, pos - a.window + 1);
-    for (int t = a.sinks > 0 ? 0 : from; t <= pos; ++t) {
-        if (t >= a.sinks && t < from) t = from;
-        int blk = a.block_tables[static_cast<int64_t>(s) * a.max_blocks + t / a.block_size];
-        if (blk < 0 || blk >= a.num_blocks) {
-            if (lane == 0) raise_flag(a.status, kFlagBadBlock);
-            blk = 0;
+    for (int base = 0; base < total; base += 32) {
+        const int i = base + lane;
+        int64_t r = 0;  // the key's row in the caches
+        float x = -INFINITY;
+        if (i < total) {
+            const int t = i < first ? i : from + i - first;
+            int blk = a.block_tables[static_cast<int64_t>(s) * a.max_blocks + t / a.block_size];
+            if (blk < 0 || blk >= a.num_blocks) {
+                raise_flag(a.status, kFlagBadBlock);
+                blk = 0;
+            }
+            r = (static_cast<int64_t>(blk) * a.num_kv_heads + h) * a.block_size + t % a.block_size;
+            const char* k = static_cast<const char*>(a.k_cache) + r * D * eb;
+            x = 0.f;
+#pragma unroll 8
+            for (int d = 0; d < D; ++d) x = fmaf(Elem<DT>::to_float(q[d]) * a.scale_log2, cached<KT>(k, d), x);
         }
-        const int64_t r = (static_cast<int64_t>(blk) * a.num_kv_heads + h) * a.block_size + t % a.block_size;
-        const char* k = static_cast<const char*>(a.k_cache) + (r * D + VD * lane) * eb;
-        const char* v = static_cast<const char*>(a.v_cache) + (r * D + VD * lane) * eb;
-        float x = 0.f;
+        float mn = x;
 #pragma unroll
-        for (int i = 0; i < VD; ++i) x = fmaf(q[i], cached<KT>(k, i), x);
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-        const float mn = fmaxf(m, x);
+        for (int off = 16; off >= 1; off >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+        mn = fmaxf(m, mn);
         const float ref = mn == -INFINITY ? 0.f : mn;
         const float al = fast_exp2(m - ref);
-        const float p = fast_exp2(x - ref);
-        l = fmaf(l, al, p);
-#pragma unroll
-        for (int i = 0; i < VD; ++i) o[i] = fmaf(o[i], al, p * cached<KT>(v, i));
+        const float p = i < total ? fast_exp2(x - ref) : 0.f;
         m = mn;
+        float sum = p;
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        l = fmaf(l, al, sum);
+#pragma unroll
+        for (int e = 0; e < VD; ++e) o[e] *= al;
+        const int n = min(32, total - base);
+        for (int k = 0; k < n; ++k) {
+            const float pk = __shfl_sync(0xffffffffu, p, k);
+            const int64_t rk = __shfl_sync(0xffffffffu, r, k);
+            const char* v = static_cast<const char*>(a.v_cache) + (rk * D + VD * lane) * eb;
+#pragma unroll
+            for (int e = 0; e < VD; ++e) o[e] = fmaf(pk, cached<KT>(v, e), o[e]);
+        }
+        bool gone = l != l;
+        if (!gone) {
+            gone = true;
+#pragma unroll
+            for (int e = 0; e < VD; ++e) gone = gone && o[e] != o[e];
+        }
+        if (__all_sync(0xffffffffu, gone)) break;
     }
     const float inv = (KT == kFP8 ? a.v_scale : 1.f) / l;
 #pragma unroll
-    for (int i = 0; i < VD; ++i) store_out(a.out, row + i, o[i] * inv, a.out_dtype);
+    for (int e = 0; e < VD; ++e) store_out(a.out, row + VD * lane + e, o[e] * inv, a.out_dtype);
 }
 
 namespace {

@@ -393,3 +393,34 @@ def test_refuses_host_and_wrong_tensors():
             call(make.q.half(), *good[1:], make.scale, 30)
         with pytest.raises(ValueError):
             call(make.q[:, :, :64], *good[1:], make.scale, 30)
+
+
+@pytest.mark.parametrize("D,dtype,fp8", [(128, "bf16", False), (64, "f16", False), (128, "f16", True)])
+def test_chunk_of_nan_values(D, dtype, fp8):
+    """Every V that a chunk sees NaN: every row is NaN, and the call ends soon."""
+    b = Batch([3000, 400], 700, 4, new=[2500, 400], dtype=dtype, D=D, Hkv=4, fp8=fp8)
+    if fp8:
+        b.q.fill_(float("nan"))
+    else:
+        b.vc.fill_(float("nan"))
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    b.run(DT[dtype])
+    start.record()
+    out = b.run(DT[dtype])
+    end.record()
+    torch.cuda.synchronize()
+    assert bool(out.isnan().all()) and pkv.device_status() == (0, 0)
+    assert start.elapsed_time(end) < 1000.0
+
+
+def test_chunk_with_one_nan_far_back():
+    """Rows of 4,000 keys computed again, each 32 keys at a time, against the formula without the NaN's dimension."""
+    b = Batch([4500], 4096, 4, new=[300], dtype="bf16", spread=2.0)
+    clean, bound = b.expected()
+    at = 4350  # seen by the rows from 150 on
+    b.vc[int(b.tables[0, at // b.bs]), 1, at % b.bs, 7] = float("nan")
+    out = b.run().double()
+    off = (out - clean).abs() - bound
+    off[150:, b.G:, 7] = -1
+    assert float(off.max()) <= 0
+    assert bool(out[150:, b.G:, 7].isnan().all())
