@@ -516,7 +516,7 @@ kv_status_t paged_prefill_attention(const void* q, const void* k_cache, const vo
  * max_blocks_per_seq * block_size must be below 2^31.  The other arguments, the
  * workspace and the options are those of paged_decode_attention (of
  * paged_decode_attention_fp8 for an E4M3 cache), and so is the result when the
- * window reaches back to the first token. */
+ * window reaches back to the first token, up to the order of the sums. */
 kv_status_t paged_window_decode_attention(const void* q, const void* k_cache, const void* v_cache,
                                           int num_blocks, const int32_t* block_tables,
                                           int max_blocks_per_seq, const int32_t* context_lens,
@@ -545,8 +545,8 @@ kv_status_t paged_window_decode_attention_fp8(const void* q, kv_dtype_t q_dtype,
  * last sequence are not read, and those rows of out left as they are.
  * workspace: device, 256-byte aligned, of at least
  * paged_window_prefill_workspace_bytes, needs no initialisation, not to be
- * shared by two calls in flight at once.  The other arguments and what is
- * refused are those of paged_prefill_attention (_fp8). */
+ * shared by two calls in flight at once.  out may not overlap q.  The other
+ * arguments and what is refused are those of paged_prefill_attention (_fp8). */
 kv_status_t paged_window_prefill_workspace_bytes(int num_seqs, int num_tokens, int num_q_heads,
                                                  int num_kv_heads, int head_dim, int device,
                                                  size_t* bytes_out);

@@ -1315,6 +1315,12 @@ static kv_status_t prefill_impl(const void* q, const void* k_cache, const void* 
     const size_t need = sight ? window_prefill_workspace(num_seqs, num_tokens, G) : paged_prefill_workspace_bytes(num_seqs);
     if (workspace_bytes < need)
         return fail(KV_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    if (sight) {  // (rows computed again read q after out has been written)
+        const uintptr_t n = static_cast<uintptr_t>(num_tokens) * num_q_heads * head_dim;
+        const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
+        if (q0 < o0 + n * dtype_bytes(out_dtype) && o0 < q0 + n * dtype_bytes(dtype))
+            return fail(KV_ERR_INVALID_ARG, "paged_window_prefill_attention: out overlaps q");
+    }
     int dev = 0, sms = 0, max_smem = 0;
     uint32_t* status = nullptr;
     if (kv_status_t st = device_info(&dev, &status, &sms, &max_smem, nullptr)) return st;

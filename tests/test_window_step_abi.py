@@ -64,6 +64,14 @@ def test_prefill_refuses(lib, kw, status):
     assert lib.kv_last_error()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("kw", [dict(out=A), dict(out=A + 9 * 8 * 128 * 2 - 16), dict(out=A - 16),
+                                dict(out=A - 9 * 8 * 128 * 4 + 16, out_dtype=F32)])
+def test_prefill_refuses_out_over_q(lib, fp8, kw):
+    assert _prefill(lib, fp8, **kw) == INVALID
+    assert b"overlaps" in lib.kv_last_error()
+
+
 @pytest.mark.parametrize("call", [_decode, _prefill])
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=F32), UNSUPPORTED), (dict(dtype=E4M3), UNSUPPORTED), (dict(D=64), UNSUPPORTED), (dict(ks=0.0), INVALID),
