@@ -19,7 +19,8 @@
 // state, which may be updated in place, are written by the CTA itself where there
 // is one, and else by a launch behind it (one cluster of 8 CTAs that meets before
 // it writes took 35 us for 262,144 tokens of 1,000 sequences).  Bound: latency (a
-// launch, three dependent rounds of loads); a token costs 12 bytes.
+// launch, three dependent rounds of loads); a token costs 12 bytes.  256 tokens of as
+// many sequences take 4.2 us in a graph, 262,144 tokens of 1,000 sequences 9.4.
 #include <cooperative_groups.h>
 
 #include "device_utils.cuh"

@@ -9,7 +9,9 @@
 // CTA joins its warps' states in shared memory, the cluster joins its CTAs' through
 // distributed shared memory, every CTA a part of the output's elements.  So nothing
 // goes through L2 but K, V, q and out, and no counter has to be kept: the persistent
-// kernel's merge by the last arrival took most of a small call's time.
+// kernel's merge by the last arrival took most of a small call's time.  Bound: latency
+// (table entry, TMA, tile, joins).  One sequence under a window of 1,024, 8 KV heads of
+// 128, bf16: 8.0 us in a graph, the persistent kernel 35.
 #include <cooperative_groups.h>
 
 #include "decode_fp8.cuh"
