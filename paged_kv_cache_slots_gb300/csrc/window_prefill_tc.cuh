@@ -39,9 +39,9 @@
 // whose cycles it uses on long windows; the rest is the softmax of a tile, the issuing
 // warp's looks at its barriers, and at short windows the ends of the items.  32 query
 // heads of 128 over 8 KV heads: 16,384 tokens of one prompt behind 16,384 under a window
-// of 4,096 in 850 us (1.29 PFLOP/s), eight chunks of 2,048 under one of 1,024 in 264 us
-// (1.04 PFLOP/s, 48 % of the cycles); over E4M3 caches, where two warps widen the codes,
-// 1,259 and 412 us (0.87 and 0.67 PFLOP/s, 31 %).
+// of 4,096 in 835 us (1.32 PFLOP/s), eight chunks of 2,048 under one of 1,024 in 262 us
+// (1.05 PFLOP/s, 48 % of the cycles); over E4M3 caches, where two warps widen the codes,
+// 1,254 and 408 us (0.88 and 0.67 PFLOP/s, 31 %).
 #pragma once
 
 #include "decode_kernel.cuh"
@@ -311,6 +311,24 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "=l"(reinterpret_cast<uint64_t&>(d))
         : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
     return d;
+}
+
+// 64 columns of tensor memory; what reads them stays behind the wait for them (hold64).
+__device__ __forceinline__ void load64(uint32_t col, float (&s)[64]) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        float x[32];
+        tc_ld32(col + 32 * q, x);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) s[32 * q + c] = x[c];
+    }
+}
+__device__ __forceinline__ void hold64(float (&s)[64]) {
+#pragma unroll
+    for (int c = 0; c < 64; c += 16)
+        asm volatile("" : "+f"(s[c]), "+f"(s[c + 1]), "+f"(s[c + 2]), "+f"(s[c + 3]), "+f"(s[c + 4]), "+f"(s[c + 5]),
+                          "+f"(s[c + 6]), "+f"(s[c + 7]), "+f"(s[c + 8]), "+f"(s[c + 9]), "+f"(s[c + 10]), "+f"(s[c + 11]),
+                          "+f"(s[c + 12]), "+f"(s[c + 13]), "+f"(s[c + 14]), "+f"(s[c + 15]));
 }
 
 template <int DT>
@@ -765,8 +783,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                     const float2 both = add2(part[0], part[1]);
                     sum = both.x + both.y;
                 };
+                auto store = [&]() {  // over the S that they came from
+                    tc_st32u(s_col + 64 * hf, hi);
+                    if constexpr (kTwo) tc_st32u(s_col + 64 * hf + 32, lo);
+                };
                 weights();
+                store();  // (before it is known whether they stand, so that the vote costs nothing)
                 if (__any_sync(0xffffffffu, !(sum <= limit))) {
+                    tc_wait_st();
                     // A new reference, the maximum of these scores.  (S being there says that the P . V before are
                     // done.)
                     float mx = sv[0];
@@ -810,10 +834,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                         }
                     }
                     weights();
+                    store();
                 }
                 l += sum;
-                tc_st32u(s_col + 64 * hf, hi);  // over the S that it came from
-                if constexpr (kTwo) tc_st32u(s_col + 64 * hf + 32, lo);
                 if (hf == 0 && t == 0 && (j + 1) * kKeys > live) {
                     const uint32_t st = (at + 1) % kStages;  // (stage 0 of round 0 holds the first K alone)
                     if (!__all_sync(0xffffffffu, wait(&B->full[st], (at + 1) / kStages))) return false;
@@ -828,31 +851,49 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                 }
                 return true;
             };
-            // (One text for all halves: the roles' loops have to share the instruction cache.)
+            auto give = [&]() {  // P to the issuing warp
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B->p_full[t]);
+                ++at;
+            };
+            // With a P of one part the second half's S is on its way while the first is worked on (long chunk 819 ->
+            // 783 us); a P of two parts and the E4M3 kernel's roles, which need the registers and the instruction
+            // cache, take one text for both halves (two-part chunks 369 us, 413 with the other).
+            if constexpr (!kTwo && !kFP8) {
 #pragma unroll 1
-            for (int hh = 0; hh < 2 * num_tiles && ok; ++hh) {
-                const int j = hh >> 1, hf = hh & 1;
-                if (hf == 0) {
+                for (int j = 0; j < num_tiles && ok; ++j) {
                     ok = __all_sync(0xffffffffu, wait(&B->s_full[t], ns++));
                     if (!ok) break;
                     tc_fence_after();
+                    float s0[64], s1[64];
+                    load64(s_col, s0);
+                    tc_wait_ld();
+                    hold64(s0);
+                    load64(s_col + 64, s1);
+                    ok = half(s0, j, 0);
+                    tc_wait_ld();
+                    hold64(s1);
+                    if (!ok) break;
+                    half(s1, j, 1);
+                    give();
                 }
-                float sv[64];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float x[32];
-                    tc_ld32(s_col + 64 * hf + 32 * q, x);
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) sv[32 * q + c] = x[c];
-                }
-                tc_wait_ld();
-                ok = half(sv, j, hf);
-                if (hf == 1) {
-                    tc_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&B->p_full[t]);
-                    ++at;
+            } else {
+#pragma unroll 1
+                for (int hh = 0; hh < 2 * num_tiles && ok; ++hh) {
+                    const int j = hh >> 1, hf = hh & 1;
+                    if (hf == 0) {
+                        ok = __all_sync(0xffffffffu, wait(&B->s_full[t], ns++));
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    float sv[64];
+                    load64(s_col + 64 * hf, sv);
+                    tc_wait_ld();
+                    hold64(sv);
+                    ok = half(sv, j, hf);
+                    if (hf == 1) give();
                 }
             }
             if (!ok) break;
