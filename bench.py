@@ -49,8 +49,8 @@ NOMINAL_HBM_GBS = 8000.0
 CLOCK_FIELDS = ("index,clocks.sm,clocks.max.sm,power.draw,clocks_event_reasons.active,"
                 "clocks_event_reasons.hw_slowdown,clocks_event_reasons.hw_thermal_slowdown,"
                 "clocks_event_reasons.sw_thermal_slowdown,clocks_event_reasons.sw_power_cap")
-KERNEL_SOURCES = ("decode_kernel.cuh", "decode_body.cuh", "decode_mma.cuh", "decode_mma.cu", "decode_ffma.cu", "decode_fp8.cuh",
-                  "decode_fp8.cu", "mma_frag.cuh", "device_utils.cuh", "decode_plan.cu")
+KERNEL_SOURCES = ("decode_kernel.cuh", "decode_body.cuh", "decode_mma.cuh", "decode_mma.cu", "decode_ffma.cuh", "decode_ffma.cu",
+                  "decode_fp8.cuh", "decode_fp8.cu", "mma_frag.cuh", "device_utils.cuh", "decode_plan.cu")
 L2_BYTES = 129 * 10**6  # GB300 L2
 PREFILL_SOURCES = ("prefill_tc.cu", "prefill.cu", "tc_utils.cuh", "decode_kernel.cuh", "mma_frag.cuh",
                    "device_utils.cuh")
