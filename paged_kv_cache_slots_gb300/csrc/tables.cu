@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tables_extend_kernel(const Tab
     const bool reports = rank == 0 && kPart != kLengths;
     const Queue q = queue_of(a.queue_state, a.num_blocks, reports ? a.status : nullptr);
 
-    int64_t asked_tokens = 0, asked_blocks = 0;  // of the sequences before this round's
+    int64_t asked_tokens = 0, asked_blocks = 0;  // of the sequences before these
     int tokens = 0, blocks = 0;                  // granted
     for (int base = 0; base < B; base += kThreads) {
         const int s = base + tid;
