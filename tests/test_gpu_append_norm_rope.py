@@ -116,6 +116,8 @@ SHAPES = plain.SHAPES + [
     (701, 8, 8, 64, 64, "f32", dict(per_head=True, amplitude=1.5)),
     (400, 3, 1, 256, 256, "bf16", dict(weights=None, interleaved=True)),
     (400, 2, 1, 512, 128, "f16", {}),
+    (320, 122, 8, 128, 128, "bf16", dict(packed=True)),
+    (320, 123, 8, 128, 128, "bf16", dict(packed=True)),
     (9, 2, 1, 1040, 16, "f16", {}),
     (9, 3, 1, 1032, 6, "bf16", dict(weights="f32", per_head=True)),
 ]
