@@ -240,7 +240,7 @@ kv_status_t kv_append_rope(kv_pool_t* pool, int layer, const kv_rope_t* rope, co
  *   q_weight, k_weight  device, in weight_dtype (src_dtype or KV_F32):
  *                       [head_dim] for all heads (a stride of 0), or a row for
  *                       each head, q_weight_stride (k_weight_stride) elements
- *                       apart; NULL: all 1.  q_out overlaps neither
+ *                       apart; NULL: all 1.  q_out may overlap neither
  *   eps                 finite, >= 0
  * The other arguments are those of kv_append_rope.  Weights that are 16-byte
  * aligned are the fast ones. */

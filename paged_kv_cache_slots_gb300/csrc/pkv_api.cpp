@@ -355,6 +355,14 @@ bool rows_overlap(const void* p, int64_t p_stride, int64_t p_row, const void* o,
     return true;
 }
 
+// Whether `bytes` bytes at p touch one of `n` rows of `row` bytes, `stride` apart, at o.
+bool touches_rows(const void* p, int64_t bytes, const void* o, int64_t stride, int64_t row, int64_t n) {
+    const int64_t a = reinterpret_cast<intptr_t>(p), b = reinterpret_cast<intptr_t>(o);
+    if (a + bytes <= b || b + (n - 1) * stride + row <= a) return false;
+    const int64_t d = a - b;
+    return d < 0 || d % stride < row || d % stride + bytes > stride;
+}
+
 }  // namespace
 
 // ---------------------------------------------------------------- allocator
@@ -773,6 +781,15 @@ kv_status_t kv_append_norm_rope(kv_pool_t* p, int layer, const kv_rope_t* rope, 
         wbits |= reinterpret_cast<uintptr_t>(x.w) | static_cast<uintptr_t>(x.heads > 1 ? x.stride * wb : 0);
     }
     if (n_tokens == 0) return KV_OK;
+    if (q) {  // a weight is read once for each token, also behind the first ones' writes to q_out
+        const int64_t row = static_cast<int64_t>(num_q_heads) * D * dtype_bytes(src_dtype);
+        const int64_t step = n_tokens > 1 ? q_out_stride * dtype_bytes(src_dtype) : row;
+        for (const auto& x : weights) {
+            const int64_t bytes = ((x.heads > 1 ? (x.heads - 1) * x.stride : 0) + D) * wb;
+            if (x.w && touches_rows(x.w, bytes, q_out, step, row, n_tokens))
+                return fail(KV_ERR_INVALID_ARG, "%s: q_out overlaps the weights", what);
+        }
+    }
     a.q_weight = q_weight;
     a.k_weight = k_weight;
     a.q_weight_stride = num_q_heads > 1 ? q_weight_stride : 0;
