@@ -4,10 +4,11 @@
 // For a row (new token at position p, query head g) over the keys j in sight,
 // j <= p and (j > p - window or j < sinks):
 //   s_j = scale q . k_j,  m = max s_j,  out = sum 2^(s_j - m) v_j / sum 2^(s_j - m)
-// in base 2, with one pass over the keys.  m is a reference that moves seldom: it is
-// the maximum of the first keys that the row sees, and that of later ones when the
-// weights of 64 keys sum to more than 2^12 (O and the sum are rescaled then), so that
-// the usual 64 keys need no maximum at all.
+// in base 2, with one pass over the keys.  Instead of m there stands a reference that
+// moves seldom: it is the maximum of the first keys that the row sees (f16: 7 below
+// it, see kLower), and that of later ones when the weights of 64 keys sum to more than
+// move_at (O and the sum are rescaled then), so that the usual 64 keys need no maximum
+// at all.
 //
 // Work split.  An item is 256 / G new tokens of one sequence with the G query heads
 // of one KV head: 256 rows, two tiles of 128, so that a K and V tile read from L2
@@ -29,7 +30,8 @@
 //
 // Roundings.  S, O, the maxima and sums are fp32.  With a 16-bit output a weight
 // meets V rounded to q's type (half a step: as much as the output's own rounding),
-// with an fp32 output in two parts, which hold it to 2^-17 (bf16), 2^-22 (f16).
+// with an fp32 output in two parts, which hold it to 2^-17 (bf16), 2^-22 (f16); f16
+// parts end at 2^-24, so that no weight is held to less than 2^-32 of the row's largest.
 //
 // V rows that a tile holds behind the sequence's last token are zeroed.  A row that
 // comes out as NaN (a V row that another row of its tile sees may hold an infinity or
@@ -143,7 +145,17 @@ constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr uint32_t kSlice = kRowsTile * 128;  // Q: 128 rows of 64 elements, 16 KiB
 constexpr uint32_t kGroup = 8 * 128;          // 8 rows of 64 elements: the swizzle's atom
 constexpr uint32_t kTmemCols = 512;
-constexpr float kMoveAt = 4096.f;  // sum of half a tile's weights above which a row's reference moves
+// How far below the maximum a row's reference is set, and the sum of half a tile's
+// weights above which it moves.  f16 weights are 2^7 at the maximum then: the largest may
+// be 65,504, and below 2^-25 they are lost.  A first token that every query looks at lies
+// far above the keys of the window, which may be all that the output is made of where its
+// V is near zero: with weights of 1 at the maximum 4,096 keys 2^25.5 below it came out as
+// 0 instead of 8.7e-5.  (Another 2^2 leaves too little room before the reference has to
+// move: the long chunk took 982 us instead of 841.)  bf16 weights have fp32's exponents.
+template <int DT>
+__device__ constexpr float kLower = DT == kF16 ? 7.f : 0.f;
+template <int DT>
+__device__ constexpr float kMoveAt = DT == kF16 ? 65504.f : 4096.f;
 
 template <int D, bool kFP8>
 struct Layout {
@@ -791,20 +803,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                 store();  // (before it is known whether they stand, so that the vote costs nothing)
                 if (__any_sync(0xffffffffu, !(sum <= limit))) {
                     tc_wait_st();
-                    // A new reference, the maximum of these scores.  (S being there says that the P . V before are
+                    // A new reference by the maximum of these scores.  (S being there says that the P . V before are
                     // done.)
                     float mx = sv[0];
 #pragma unroll
                     for (int c = 1; c < 64; ++c) mx = fmaxf(mx, sv[c]);
-                    mx *= sc;
+                    mx = mx * sc - kLower<DT>;
                     const bool move = mx > m_ref && !(sum <= limit);
-                    // The step is a whole number, so that it scales what stands in P exactly.
-                    if (m_ref > -INFINITY) mx = m_ref + ceilf(mx - m_ref);
+                    // The step is a whole number, so that it scales what stands in P exactly (down to f16's last place);
+                    // it is 3 at least, or the sum would not have passed the limit.
+                    if (m_ref > -INFINITY) mx = m_ref + floorf(mx - m_ref);
                     const float f = move ? fast_exp2(m_ref - mx) : 1.f;  // (0 from -inf)
                     if (move) {
                         l *= f;
                         m_ref = mx;
-                        limit = kMoveAt;
+                        limit = kMoveAt<DT>;
                     }
                     if (j > 0) {
 #pragma unroll
