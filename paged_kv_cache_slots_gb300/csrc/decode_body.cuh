@@ -119,11 +119,12 @@
             return j * a.block_size;
         };
         auto hidden_in = [&](int j) {
-            Hidden r{0, 0};
+            Hidden r{0, 0, 0.f};
             if constexpr (kWindow) {
                 const int t0 = first_token(j);
                 r.from = max(a.sinks - t0, 0);
                 r.to = min(ctx - a.window - t0, a.block_size);
+                r.lower = lower_of(ctx, a.window);
             }
             return r;
         };

@@ -259,6 +259,7 @@ struct MmaFp8Policy {
             }
 #pragma unroll
             for (int off = 4; off <= 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            if constexpr (kHole) mx -= hole[0].lower;  // st.m: the references
             const float mn = fmaxf(st.m[0], mx);
             const float al = fast_exp2(st.m[0] - mn);
             st.m[0] = mn;
@@ -300,6 +301,10 @@ struct MmaFp8Policy {
         for (int off = 4; off <= 16; off <<= 1) {
             mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
             mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+        }
+        if constexpr (kHole) {
+            mx0 -= hole[0].lower;
+            mx1 -= hole[0].lower;
         }
         const float mn0 = fmaxf(st.m[0], mx0), mn1 = fmaxf(st.m[1], mx1);
         const float al0 = fast_exp2(st.m[0] - mn0), al1 = fast_exp2(st.m[1] - mn1);
@@ -383,8 +388,8 @@ struct MmaFp8Policy {
             const int n2[2] = {n_valid - 16 * mt, n_valid - 16 * (mt + 1)};
             if constexpr (kHole) {
                 if (hole.from <= 16 * mt && 16 * mt + 32 <= hole.to) continue;
-                const Hidden h2[2] = {{hole.from - 16 * mt, hole.to - 16 * mt},
-                                      {hole.from - 16 * (mt + 1), hole.to - 16 * (mt + 1)}};
+                const Hidden h2[2] = {{hole.from - 16 * mt, hole.to - 16 * mt, hole.lower},
+                                      {hole.from - 16 * (mt + 1), hole.to - 16 * (mt + 1), hole.lower}};
                 slices<2, true>(st, a, k2, v2, n2, G, h2);
             } else {
                 slices<2>(st, a, k2, v2, n2, G);
@@ -395,7 +400,7 @@ struct MmaFp8Policy {
             const uint32_t v1[1] = {vb + mt * 2048u};
             const int n1[1] = {n_valid - 16 * mt};
             if constexpr (kHole) {
-                const Hidden h1[1] = {{hole.from - 16 * mt, hole.to - 16 * mt}};
+                const Hidden h1[1] = {{hole.from - 16 * mt, hole.to - 16 * mt, hole.lower}};
                 if (!(hole.from <= 16 * mt && 16 * mt + 16 <= hole.to)) slices<1, true>(st, a, k1, v1, n1, G, h1);
             } else {
                 slices<1>(st, a, k1, v1, n1, G);

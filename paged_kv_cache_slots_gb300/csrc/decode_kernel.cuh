@@ -107,10 +107,22 @@ __device__ __forceinline__ int clamp_context(const DecodeArgs& a, int s, bool fl
     return c;
 }
 
-// Tokens [from, to) of a block that a windowed query does not see (none if from >= to).
+// How far below the maximum of its scores a windowed query's reference is set where its
+// weights are split into f16 parts: they are 2^15 at the maximum then, and the parts'
+// last place, 2^-24, is 2^-39 of it.  A first token that every query looks at lies far
+// above the keys of the window, which may be all that the output is made of where its V
+// is near zero: with weights of 1 at the maximum 4,096 keys 2^25.5 below it came out as
+// half of what they are, and 2^28 below it as 0.  A query that sees all of its context
+// keeps weights of 1 and with them the plain decode's result bit for bit.
+constexpr float kLowerF16 = 15.f;
+
+// Tokens [from, to) of a block that a windowed query does not see (none if from >= to);
+// its reference stands `lower` below the maximum of its scores, in every block of its.
 struct Hidden {
     int from, to;
+    float lower;
 };
+__device__ __forceinline__ float lower_of(int ctx, int window) { return ctx > window ? kLowerF16 : 0.f; }
 
 // cum[s] = chunks * sum_{s' < s, ctx_s' > 0} (ceil(ctx_s' / bs) + phantom);
 // cum[num_seqs] = W.  kTails: ctx is what follows skip[s] shared blocks.

@@ -143,6 +143,10 @@ struct MmaPolicy {
                 mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
                 mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
             }
+            if constexpr (kHole && DT == kF16) {  // st.m: the references
+                mx0 -= hole.lower;
+                mx1 -= hole.lower;
+            }
             const float mn0 = fmaxf(st.m[0], mx0), mn1 = fmaxf(st.m[1], mx1);
             // (Every slice that is not skipped has a token in sight, so the maxima are finite.)
             const float al0 = fast_exp2(st.m[0] - mn0), al1 = fast_exp2(st.m[1] - mn1);

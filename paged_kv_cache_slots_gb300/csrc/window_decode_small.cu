@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) paged_window_decode_small_k
         const int t0 = logical(first + k * step) * bs;
         uint8_t* kt = stages + (k % kStages) * 2 * half;
         pol.template tile<true>(st, a, kt, kt + half, 0, min(bs, ctx - t0), G, nullptr,
-                                Hidden{max(a.sinks - t0, 0), min(ctx - a.window - t0, bs)});
+                                Hidden{max(a.sinks - t0, 0), min(ctx - a.window - t0, bs), lower_of(ctx, a.window)});
         __syncwarp();
         if (lane == 0 && k + kStages < mine) fetch(k + kStages, row);
     }

@@ -2,8 +2,9 @@
 make up the whole output: what a first token that every query looks at, and whose V is near zero, does to a window.
 
 Tolerance: that of test_gpu_window_attention.py, and what f16 parts of a weight lose below their smallest step, 2^-24.
-The largest weight in sight of a chunk's row enters them as 2^7 at least, so a weight loses at most 2^-25 / 2^7 of the
-largest one, n of them n * 2^-32 of max |v| of the output.  bf16 parts keep fp32's exponents and lose nothing more."""
+The largest weight in sight of a row enters them as 2^15 (single tokens) or as 2^7 at least (chunks), so a weight loses at
+most 2^-25 / 2^15 or 2^-25 / 2^7 of the largest one, n of them n * 2^-40 or n * 2^-32 of max |v| of the output.  bf16 parts
+keep fp32's exponents and lose nothing more."""
 import math
 
 import pytest
@@ -61,6 +62,18 @@ def test_chunks(dtype, D, fp8, place, apart):
         b = one_large_weight(key, apart, dtype, D, fp8, G, n, new=[new, 3])
         check(b, b.run(), floor)
         check(b, b.run(DT[dtype]), floor)
+
+
+@pytest.mark.parametrize("dtype,D,fp8", FORMS)
+@pytest.mark.parametrize("place", ["first", "middle", "last"])
+@pytest.mark.parametrize("apart", [15.0, 20.0, 25.5, 28.0])
+@pytest.mark.parametrize("opts", [{}, dict(consumer_warps=8)])
+def test_single_tokens(dtype, D, fp8, place, apart, opts):
+    n = 8192
+    key = {"first": 1, "middle": n - 2000, "last": n - 1}[place]
+    for G in (1, 4, 8):
+        b = one_large_weight(key, apart, dtype, D, fp8, G, n)
+        check(b, b.run(**opts), 0.0 if dtype == "bf16" and not fp8 else 2.0 ** -40)
 
 
 @pytest.mark.parametrize("dtype,fp8", [("f16", False), ("bf16", False), ("f16", True), ("bf16", True)])
