@@ -35,7 +35,9 @@
 //
 // V rows that a tile holds behind the sequence's last token are zeroed.  A row that
 // comes out as NaN (a V row that another row of its tile sees may hold an infinity or
-// a NaN, and 0 * V is NaN then) is computed again by exact_row.
+// a NaN, and 0 * V is NaN then) is computed again by exact_row, once the CTA's items are
+// done: a row takes 9 us for each 32 keys in sight (128 dims), and the other roles' waits,
+// which give up after two seconds, must not span that.
 //
 // Tensor memory: S / P 2 x 128 columns, O 2 x 128.  Bound: the tensor cores, 58 % of
 // whose cycles it uses on long windows; the rest is the softmax of a tile, the issuing
@@ -179,7 +181,8 @@ struct Bars {
     uint64_t s_full[2], o_full[2];
     uint64_t p_full[2];
     uint64_t raw_full[2], raw_empty[2];  // E4M3: the codes of V and of K
-    int4 note[8][2];                    // what each softmax warp needs of its item at the end
+    int4 note[8];                       // what each softmax warp needs of its item at the end
+    int64_t nan_from[8];                // the first item in which it wrote a row that is NaN, or none (-1)
     uint32_t tmem;
     int abort;
 };
@@ -730,6 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
         const bool negative = a.scale_log2 < 0.f;
         uint32_t ns = 0, no = 0, at = 0;
         bool ok = true;
+        if (lane == 0) B->nan_from[warp] = -1;
         Item it;
         if (blockIdx.x < items) it = item_at(blockIdx.x);
         for (int64_t i = blockIdx.x; i < items && ok; i += gridDim.x) {
@@ -753,10 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                 whole_from = (max(0, p1 - a.window + 1 - it.skip) + 63) >> 6;
                 whole_to = negative ? 0 : (p0 + 1 - it.skip) >> 6;
             }
-            if (lane == 0) {
-                B->note[warp][0] = make_int4(it.s, it.h, it.ntok, it.pos0);
-                B->note[warp][1] = make_int4(static_cast<int>(it.tok0), 0, 0, 0);
-            }
+            if (lane == 0) B->note[warp] = make_int4(it.h, it.ntok, static_cast<int>(it.tok0), 0);
             const int live = it.ctx - it.skip;  // places from there on hold no token
             float m_ref = -INFINITY, l = 0.f;
             float limit = -1.f;  // of a half tile's sum of weights: kMoveAt once there is a reference
@@ -911,14 +912,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
             }
             if (!ok) break;
             __syncwarp();
-            const int4 n0 = B->note[warp][0];  // (not held through the loop above: its registers are all in use)
-            const int64_t tok0 = B->note[warp][1].x;
+            const int4 note = B->note[warp];  // (not held through the loop above: its registers are all in use)
+            const int64_t tok0 = note.z;
             if (i + gridDim.x < items) it = item_at(i + gridDim.x);
             ok = __all_sync(0xffffffffu, wait(&B->o_full[t], no++));
             if (!ok) break;
             tc_fence_after();
             const int w0 = t * kRowsTile + (warp & 3) * 32;  // the warp's first row of the item
-            const int rows = min(32, n0.z * G - w0);         // its rows that are the item's
+            const int rows = min(32, note.y * G - w0);       // its rows that are the item's
             const float inv = (kFP8 ? a.v_scale * code_scale<DT, kFP8>() : 1.f) / l;
             bool nan = false;
             // 32 rows of 128 bytes at a time through shared memory, so that a store takes whole rows' pieces (an E4M3
@@ -949,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                 if (cb == D / kPer - 1) tc_fence_before();  // O is read before this thread lets the next P . V begin
                 if constexpr (kFP8) {
                     if (lane < rows) {
-                        const int64_t o0 = ((tok0 + (w0 + lane) / G) * a.num_q_heads + n0.y * G + (w0 + lane) % G) * D;
+                        const int64_t o0 = ((tok0 + (w0 + lane) / G) * a.num_q_heads + note.x * G + (w0 + lane) % G) * D;
                         char* dst = static_cast<char*>(a.out) + (o0 + kPer * cb) * (kTwo ? 4 : 2);
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
@@ -967,16 +968,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                     const int row = 4 * q + (lane >> 3), c = lane & 7;
                     if (row < rows) {
                         const uint4 x = *reinterpret_cast<const uint4*>(stage + row * 128 + ((c ^ (row & 7)) << 4));
-                        const int64_t o0 = ((tok0 + (w0 + row) / G) * a.num_q_heads + n0.y * G + (w0 + row) % G) * D;
+                        const int64_t o0 = ((tok0 + (w0 + row) / G) * a.num_q_heads + note.x * G + (w0 + row) % G) * D;
                         *reinterpret_cast<uint4*>(static_cast<char*>(a.out) + (o0 + kPer * cb) * (kTwo ? 4 : 2) + 16 * c) = x;
                     }
                 }
                 __syncwarp();
             }
-            uint32_t bad = __ballot_sync(0xffffffffu, nan && lane < rows);
-            for (; bad; bad &= bad - 1) {
-                const int row = w0 + __ffs(bad) - 1;
-                exact_row<DT, kFP8 ? static_cast<int>(pkv::kFP8) : DT, D>(a, n0.x, n0.y, tok0 + row / G, n0.y * G + row % G, n0.w + row / G);
+            if (__any_sync(0xffffffffu, nan && lane < rows) && lane == 0 && B->nan_from[warp] < 0) B->nan_from[warp] = i;
+        }
+        // The rows that this warp wrote as NaN, again (see above).
+        __syncwarp();
+        for (int64_t i = ok ? B->nan_from[warp] : -1; i >= 0 && i < items; i += gridDim.x) {
+            const Item x = item_at(i);
+            const int w0 = t * kRowsTile + (warp & 3) * 32;
+            const int rows = min(32, x.ntok * G - w0);
+            for (int row = w0; row < w0 + rows; ++row) {
+                const int64_t o0 = ((x.tok0 + row / G) * a.num_q_heads + x.h * G + row % G) * D;
+                bool nan = false;
+                for (int d = lane; d < D; d += 32) {
+                    float o;
+                    if constexpr (kTwo)
+                        o = static_cast<const float*>(a.out)[o0 + d];
+                    else
+                        o = Elem<DT>::to_float(static_cast<const typename Elem<DT>::T*>(a.out)[o0 + d]);
+                    nan = nan || o != o;
+                }
+                if (__any_sync(0xffffffffu, nan))
+                    exact_row<DT, kFP8 ? static_cast<int>(pkv::kFP8) : DT, D>(a, x.s, x.h, x.tok0 + row / G, x.h * G + row % G,
+                                                                              x.pos0 + row / G);
             }
         }
     }
