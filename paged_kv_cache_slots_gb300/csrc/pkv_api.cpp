@@ -191,17 +191,41 @@ struct Sight {
 };
 
 // Whether a windowed decode takes the kernel for small calls (window_decode_small.cu) rather than the persistent
-// one.  By what a head's K rows of a block take (half) and what is in sight; both measured in graphs, inputs out of
-// L2, 8 KV heads of 128, microseconds small / persistent:
-//   4 KiB (16 tokens of 16 bits, 32 codes): 16 sequences x 1,024 (67 MB) 17.3 / 19.8, 32 x 1,024 (134 MB) 31.5 / 27.1,
-//     8 x 4,096 (134 MB) 29.0 / 29.0, 16 x 4,096 51 / 44; 32 x 512 (67 MB) 21.1 / 18.7, E4M3 64 x 128 (17 MB) 15.5 / 16.6,
-//     E4M3 128 x 128 (34 MB) 28.2 / 20.7;
-//   8 KiB: 16 x 4,096 (268 MB) 45 / 57, 64 x 1,024 (268 MB) 55.1 / 55.2, 32 x 4,096 (537 MB) 90 / 87;
-//   from 16 KiB on, where the persistent kernel's stages hold one or two heads: 128 x 1,024 (537 MB) 101 / 138.
-bool small_window(int64_t bytes, int64_t pairs, int half, int sms) {
-    if (half >= 16384) return true;
-    if (half >= 8192) return bytes <= int64_t{256} << 20;
-    return bytes <= (pairs <= sms ? int64_t{128} << 20 : pairs <= 4 * sms ? int64_t{32} << 20 : 0);
+// one: by estimates of both kernels' times with every sequence as long as its window.  From 892 calls measured with
+// either kernel (graphs, inputs out of L2; 1, 2 and 8 KV heads, windows of 128 to 131,072, batches of 1 to 256):
+//   Small: a wave of CTAs takes 5 us and, for each block that its warps take one after the other, 0.4 us and 0.18 a KiB
+//   of the block's K rows (0.25 over E4M3; 0.65 of it where three warps or fewer share an SM's shared memory), and
+//   all of them no less than 5 TB/s allow (E4M3), or 5.5.  Of 8-CTA clusters three quarters fit at once (16 pairs: 70
+//   us, 4 pairs: 33).
+//   Persistent: 15 us and the rate that its stages reach: blocks of few heads make small stages (64 sequences, one KV head of
+//   128, blocks of 16, window 8,192: 126 us, small 53), blocks of 24 KiB a head leave it two (16 sequences, 8 KV heads,
+//   blocks of 128, window 8,192: 188, small 107); one long sequence is cut into so many parts that the merge takes 60.
+// The small kernel gives a sequence of any length the same CTAs, and lengths are not known here: one long sequence
+// among short ones waits for its own CTAs alone, where the persistent kernel spreads it over every SM (window 32,768,
+// 1 of 32, 8 KV heads, blocks of 64: 237 us, persistent 47).  So what a CTA may have to stream is bounded: 1.1 MB,
+// or 4.4 MB where the persistent kernel would take a quarter longer on equal lengths.  Of the measured calls 59 are more
+// than 10 % above the faster kernel: lengths far apart (up to 2.5x), or small waves beyond that bound.
+bool small_window(const SmallPlan& plan, int num_seqs, int kv_heads, int row_blocks, int half, bool fp8, int sms) {
+    const double bytes = 2.0 * half * row_blocks * num_seqs * kv_heads, h = half / 1024.0;
+    const double fit = static_cast<double>(sms) * plan.per_sm * (plan.ctas == 8 ? 0.75 : 1.0);
+    double waves = static_cast<double>(num_seqs) * kv_heads * plan.ctas / fit;
+    waves = waves < 1 ? 1 : waves < 3 ? std::ceil(waves) : waves;
+    const double step = 0.4 + h * (fp8 ? 0.25 : 0.18) * (plan.warps <= 3 ? 0.65 : 1.0);
+    const int chain = (row_blocks + plan.ctas * plan.warps - 1) / (plan.ctas * plan.warps);
+    double small = waves * (5 + chain * step);  // us
+    const double stream = 5 + bytes / (fp8 ? 5.0e6 : 5.5e6);
+    if (small < stream) small = stream;
+    double rate;  // GB/s
+    if (h >= 24)
+        rate = 2900;
+    else if (h >= 16)
+        rate = fp8 ? (kv_heads > 1 ? 3400 : 4700) : (kv_heads > 1 ? 4700 : 6000);
+    else
+        rate = h * kv_heads < 8 ? 2300 : h * kv_heads < 16 ? 4200 : h * kv_heads < 32 ? 5500 : 6300;
+    double persistent = 15 + bytes / rate / 1000;
+    if (num_seqs == 1 && bytes > 4e6 && persistent < 60) persistent = 60;
+    const double kib = 2 * h * row_blocks / plan.ctas;
+    return small < persistent && (kib <= 1100 || (kib <= 4400 && 1.25 * small < persistent));
 }
 
 kv_status_t check_sight(const Sight& w, int max_blocks, int block_size) {
@@ -1119,9 +1143,8 @@ static kv_status_t decode_impl(const void* q, const void* k_cache, const void* v
                                                        o.separate_reduce || o.test_stall))) {
         SmallPlan small{};
         const int half = block_size * head_dim * dtype_bytes(kv_dtype);
-        const int64_t bytes = static_cast<int64_t>(num_seqs) * row_blocks * num_kv_heads * 2 * half;
-        if (small_window(bytes, static_cast<int64_t>(num_seqs) * num_kv_heads, half, sms) &&
-            plan_window_small(num_seqs, num_kv_heads, row_blocks, half, sms, max_smem, &small)) {
+        if (plan_window_small(num_seqs, num_kv_heads, row_blocks, half, sms, max_smem, &small) &&
+            small_window(small, num_seqs, num_kv_heads, row_blocks, half, fp8, sms)) {
             const int rows = num_blocks * num_kv_heads * block_size;
             if (kv_status_t st = encode_cache_map(&tk, k_cache, kv_dtype, rows, head_dim, block_size)) return st;
             if (kv_status_t st = encode_cache_map(&tv, v_cache, kv_dtype, rows, head_dim, block_size)) return st;

@@ -247,9 +247,9 @@ cudaError_t launch_decode_fp8(const DecodeArgs& a, const CUtensorMap& tmap_k,
 cudaError_t launch_window_decode_mma(const WindowArgs& a, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
                                      cudaStream_t stream);
 // Small calls (window_decode_small.cu): CTAs of a cluster and warps of a CTA for each
-// (sequence, KV head).  row_blocks: the most blocks that a query sees.
+// (sequence, KV head), CTAs that an SM holds at once.  row_blocks: the most blocks that a query sees.
 struct SmallPlan {
-    int ctas, warps, stages, smem_bytes;
+    int ctas, warps, stages, smem_bytes, per_sm;
 };
 bool plan_window_small(int num_seqs, int num_kv_heads, int row_blocks, int stage_half_bytes, int num_sms, int max_smem,
                        SmallPlan* plan);

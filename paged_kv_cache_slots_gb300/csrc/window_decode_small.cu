@@ -215,11 +215,11 @@ bool plan_window_small(int num_seqs, int num_kv_heads, int row_blocks, int stage
     if (warps < 1) return false;
     auto stages = [&](int ctas) { return row_blocks > ctas * warps && warps * bytes(2) <= room ? 2 : 1; };
     auto smem = [&](int ctas) { return warps * bytes(stages(ctas)) + 1024; };
+    auto per_sm = [&](int ctas) { return 2 * (smem(ctas) + 8 * 1024) <= max_smem ? 2 : 1; };
     // Larger clusters while warps have more than one block and the grid stays within what the SMs hold at once.
     int ctas = 1;
     while (ctas < 8 && row_blocks > ctas * warps) {
-        const int per_sm = 2 * (smem(2 * ctas) + 8 * 1024) <= max_smem ? 2 : 1;
-        if (2 * ctas * pairs > static_cast<int64_t>(num_sms) * per_sm) break;
+        if (2 * ctas * pairs > static_cast<int64_t>(num_sms) * per_sm(2 * ctas)) break;
         ctas *= 2;
     }
     if (pairs * ctas >= (int64_t{1} << 31)) return false;
@@ -227,6 +227,7 @@ bool plan_window_small(int num_seqs, int num_kv_heads, int row_blocks, int stage
     plan->ctas = ctas;
     plan->stages = stages(ctas);
     plan->smem_bytes = smem(ctas);
+    plan->per_sm = per_sm(ctas);
     return true;
 }
 
