@@ -416,6 +416,12 @@ __global__ void __launch_bounds__(kThreads, 6) kv_append_norm_rope_ring_kernel(c
         }
 }
 
+// CTAs of the ring kernel that an SM holds, tokens of `bytes` bytes.
+int ring_ctas(int bytes) {
+    const int fit = (220 * 1024) / (kRing * bytes + 4096);
+    return fit < 6 ? fit : 6;
+}
+
 template <int DT>
 cudaError_t launch_ring(const NormRopeArgs& a, int bytes, int num_sms, cudaStream_t stream) {
     static RaisedLimit limits[2];
@@ -423,9 +429,7 @@ cudaError_t launch_ring(const NormRopeArgs& a, int bytes, int num_sms, cudaStrea
     const int smem = kRing * bytes;
     const cudaError_t e = allow_shared_memory(kern, a.device, smem, &limits[a.interleaved ? 1 : 0]);
     if (e != cudaSuccess) return e;
-    int per_sm = (220 * 1024) / (smem + 4096);
-    if (per_sm > 6) per_sm = 6;
-    const int64_t ctas = static_cast<int64_t>(num_sms) * per_sm;
+    const int64_t ctas = static_cast<int64_t>(num_sms) * ring_ctas(bytes);
     return launch_kernel(kern, dim3(static_cast<unsigned>(ctas < a.n_tokens ? ctas : a.n_tokens)), dim3(kThreads),
                          static_cast<size_t>(smem), stream, a.pdl != 0, a);
 }
@@ -449,14 +453,24 @@ cudaError_t launch_dt(NormRopeArgs a, int align, int weight_align, int num_sms, 
                      !weights_fit(v)))
         v >>= 1;
     const int items = a.head_dim / (2 * v);
-    // Many tokens of whole 16-byte items: the ring, while three of its CTAs fit an SM.  Ring / plain kernel, us in
-    // graphs, heads of 128, bf16, 32 query and 8 KV heads: 152 tokens 4.3 / 4.3, 304 4.7 / 6.0, 1,023 9.5 / 11.0,
-    // 4,096 25.6 / 30.9, 16,384 79.8 / 105 (f32 140 / 172, f16 into E4M3 88 / 120).  By CTAs an SM at 1,023 and
-    // 4,096 tokens: six (48 query heads) 12.3 / 13.2 and 33 / 43, four (80) 16.8 / 17.0 and 49 / 55, three (112)
-    // 25.3 / 22.1 and 68 / 74, two (128) 34.8 / 23.6 and 109 / 80.
+    // Many tokens of whole 16-byte items: the ring, while three of its CTAs fit an SM.  Its time goes in rounds of one
+    // token a CTA, so with few CTAs an SM, or f32 rows, it is ahead in the first round where that is nearly full, and
+    // then only from many rounds on.  Ring / plain kernel, us in graphs, heads of 128 and 8 KV heads:
+    //   bf16, 32 query heads (six CTAs an SM): 304 tokens 4.4 / 5.9, 608 6.5 / 6.1, 912 6.5 / 9.9, 1,216 10.7 / 10.6,
+    //     4,096 24.9 / 29.0, 16,384 78.9 / 103; f16 into E4M3: 1,023 9.9 / 11.8, 16,384 87.5 / 118;
+    //   64 (five): 304 7.7 / 6.3, 456 8.0 / 8.9, 1,023 15.4 / 14.2, 4,096 38 / 48; 80 (four): 1,023 16.5 / 15.7, 4,096 47 / 54;
+    //   112 (three): 456 9.5 / 10.5, 608 17.1 / 14.0, 1,023 24.5 / 20.8, 2,048 38.6 / 37.6, 4,096 65 / 73; 128 (two): 456
+    //     15.7 / 11.1, 16,384 382 / 303;
+    //   f32, 32 (four): 304 5.4 / 4.9, 608 6.9 / 8.4, 1,023 14.0 / 12.4, 2,048 24.7 / 22.0, 4,096 40 / 43, 16,384 138 / 165.
     const int64_t bytes = static_cast<int64_t>(a.num_q_heads + 2 * a.num_kv_heads) * a.head_dim * kE;
-    if (v == 16 / kE && items <= 32 && kRing * bytes <= 69 * 1024 && a.n_tokens >= 2 * num_sms)
-        return launch_ring<DT>(a, static_cast<int>(bytes), num_sms, stream);
+    if (v == 16 / kE && items <= 32 && kRing * bytes <= 69 * 1024) {
+        const int per_sm = ring_ctas(static_cast<int>(bytes));
+        const int each = (a.n_tokens + num_sms - 1) / num_sms;  // tokens an SM
+        const bool first_round = each <= per_sm && each >= (kE == 4 ? 4 : 3);
+        const int from = kE == 4 ? 24 : per_sm >= 6 ? 2 : per_sm >= 4 ? 3 : 16;
+        if (first_round || a.n_tokens >= from * num_sms)
+            return launch_ring<DT>(a, static_cast<int>(bytes), num_sms, stream);
+    }
     int L = 1;
     while (L < items && L < 32) L <<= 1;
     const int groups = kThreads / L;
