@@ -136,7 +136,7 @@ struct FfmaPolicy {
         }
         __syncwarp();
         // Tile max per head, new running max, rescale, weights.
-        float mx[G], alpha[G], ps[G];
+        float mx[G], alpha[G], ps[G], ref[G];
 #pragma unroll
         for (int g = 0; g < G; ++g) mx[g] = -INFINITY;
         for (int t = lane; t < n_valid; t += 32) {
@@ -147,7 +147,8 @@ struct FfmaPolicy {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             const float mn = fmaxf(st.m[g], warp_max(mx[g]));
-            alpha[g] = fast_exp2(st.m[g] - mn);
+            ref[g] = kHole ? finite_reference(mn) : mn;
+            alpha[g] = fast_exp2(st.m[g] - ref[g]);
             st.m[g] = mn;
             ps[g] = 0.f;
         }
@@ -156,7 +157,7 @@ struct FfmaPolicy {
             if (hidden(t)) continue;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                const float p = fast_exp2(sc[t * G + g] - st.m[g]);
+                const float p = fast_exp2(sc[t * G + g] - ref[g]);
                 sc[t * G + g] = p;
                 ps[g] += p;
             }

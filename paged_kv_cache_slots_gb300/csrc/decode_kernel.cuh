@@ -122,6 +122,9 @@ struct Hidden {
     int from, to;
     float lower;
 };
+// What a windowed query's weights, and the parts of any query, are taken relative to while the reference is m: where
+// every score so far is -inf (a K row may be) they are 0 then, not NaN.
+__device__ __forceinline__ float finite_reference(float m) { return m == -INFINITY ? 0.f : m; }
 __device__ __forceinline__ float lower_of(int ctx, int window) { return ctx > window ? kLowerF16 : 0.f; }
 
 // cum[s] = chunks * sum_{s' < s, ctx_s' > 0} (ceil(ctx_s' / bs) + phantom);
@@ -396,12 +399,13 @@ __device__ __forceinline__ void merge_parts(const DecodeArgs& a, int s, int h, i
             float mg = -INFINITY;
             for (int k = 0; k < n; ++k) mg = fmaxf(mg, __shfl_sync(0xffffffffu, ml.x, k * G + g));
             const float mn = fmaxf(M[g], mg);
-            const float al = fast_exp2(M[g] - mn);
+            const float ref = finite_reference(mn);
+            const float al = fast_exp2(M[g] - ref);
             M[g] = mn;
             Lsum[g] *= al;
 #pragma unroll
             for (int i = 0; i < VD; ++i) acc[g][i] *= al;
-            if (kg == g && my_c >= 0) w_lane = fast_exp2(ml.x - mn);
+            if (kg == g && my_c >= 0) w_lane = fast_exp2(ml.x - ref);
         }
         const float wl = w_lane * ml.y;
 #pragma unroll
@@ -634,17 +638,18 @@ static __device__ void combine_replicas(const DecodeArgs& a, const float* merge,
     for (int g = 0; g < G; ++g) {
         float M = -INFINITY;
         for (int r = 0; r < R; ++r) M = fmaxf(M, merge[((hw + r * Hc) * G + g) * (D + 2) + D]);
+        const float ref = finite_reference(M);
         float Lsum = 0.f;
         for (int r = 0; r < R; ++r) {
             const float* mr = merge + ((hw + r * Hc) * G + g) * (D + 2);
-            Lsum += fast_exp2(mr[D] - M) * mr[D + 1];
+            Lsum += fast_exp2(mr[D] - ref) * mr[D + 1];
         }
         const int64_t o0 = (static_cast<int64_t>(s) * a.num_q_heads + h * G + g) * D;
         for (int d = lane; d < D; d += 32) {
             float O = 0.f;
             for (int r = 0; r < R; ++r) {
                 const float* mr = merge + ((hw + r * Hc) * G + g) * (D + 2);
-                O += fast_exp2(mr[D] - M) * mr[d];
+                O += fast_exp2(mr[D] - ref) * mr[d];
             }
             if (whole)
                 store_out(a.out, o0 + d, O / Lsum, a.out_dtype);

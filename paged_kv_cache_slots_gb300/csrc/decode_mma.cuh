@@ -148,12 +148,12 @@ struct MmaPolicy {
                 mx1 -= hole.lower;
             }
             const float mn0 = fmaxf(st.m[0], mx0), mn1 = fmaxf(st.m[1], mx1);
-            // (Every slice that is not skipped has a token in sight, so the maxima are finite.)
-            const float al0 = fast_exp2(st.m[0] - mn0), al1 = fast_exp2(st.m[1] - mn1);
+            const float rf0 = kHole ? finite_reference(mn0) : mn0, rf1 = kHole ? finite_reference(mn1) : mn1;
+            const float al0 = fast_exp2(st.m[0] - rf0), al1 = fast_exp2(st.m[1] - rf1);
             st.m[0] = mn0;
             st.m[1] = mn1;
-            const float p0 = fast_exp2(x0 - mn0), p1 = fast_exp2(x1 - mn1);
-            const float p2 = fast_exp2(x2 - mn0), p3 = fast_exp2(x3 - mn1);
+            const float p0 = fast_exp2(x0 - rf0), p1 = fast_exp2(x1 - rf1);
+            const float p2 = fast_exp2(x2 - rf0), p3 = fast_exp2(x3 - rf1);
             st.l[0] = st.l[0] * al0 + (p0 + p2);
             st.l[1] = st.l[1] * al1 + (p1 + p3);
             if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {

@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(128) paged_decode_reduce_kernel(const DecodeAr
                 for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                 const float m_old = run_m[g];
                 const float m_new = fmaxf(m_old, mx);
-                const float w = valid ? fast_exp2(m - m_new) : 0.f;
+                const float w = valid ? fast_exp2(m - finite_reference(m_new)) : 0.f;
                 wgt[tid][g] = w;
                 float ls = w * l;
 #pragma unroll

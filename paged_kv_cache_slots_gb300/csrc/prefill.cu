@@ -558,8 +558,9 @@ __global__ void __launch_bounds__(256) paged_prefill_f32_kernel(const PrefillArg
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
         const float mn = fmaxf(m, x);
-        const float al = fast_exp2(m - mn);  // 0 while m is -inf
-        const float p = fast_exp2(x - mn);
+        const float ref = kWindow && mn == -INFINITY ? 0.f : mn;  // (a score of -inf has a weight of 0)
+        const float al = fast_exp2(m - ref);  // 0 while m is -inf
+        const float p = fast_exp2(x - ref);
         l = fmaf(l, al, p);
 #pragma unroll
         for (int i = 0; i < VD; ++i) o[i] = fmaf(o[i], al, p * __ldg(v + i));
