@@ -7,7 +7,7 @@
 // in base 2, with one pass over the keys.  Instead of m there stands a reference that
 // moves seldom: it is the maximum of the first keys that the row sees (f16: 7 below
 // it, see kLower), and that of later ones when the weights of 64 keys sum to more than
-// move_at (O and the sum are rescaled then), so that the usual 64 keys need no maximum
+// kMoveAt (O and the sum are rescaled then), so that the usual 64 keys need no maximum
 // at all.
 //
 // Work split.  An item is 256 / G new tokens of one sequence with the G query heads
@@ -30,8 +30,9 @@
 //
 // Roundings.  S, O, the maxima and sums are fp32.  With a 16-bit output a weight
 // meets V rounded to q's type (half a step: as much as the output's own rounding),
-// with an fp32 output in two parts, which hold it to 2^-17 (bf16), 2^-22 (f16); f16
-// parts end at 2^-24, so that no weight is held to less than 2^-32 of the row's largest.
+// with an fp32 output in two parts, which hold it to 2^-17 (bf16), 2^-22 (f16).  f16 parts
+// end at 2^-24, where the row's largest weight is 2^7 at least: a weight loses up to 2^-32
+// of the largest besides.
 //
 // V rows that a tile holds behind the sequence's last token are zeroed.  A row that
 // comes out as NaN (a V row that another row of its tile sees may hold an infinity or
@@ -182,7 +183,6 @@ struct Bars {
     uint64_t p_full[2];
     uint64_t raw_full[2], raw_empty[2];  // E4M3: the codes of V and of K
     int4 note[8];                       // what each softmax warp needs of its item at the end
-    int64_t nan_from[8];                // the first item in which it wrote a row that is NaN, or none (-1)
     uint32_t tmem;
     int abort;
 };
@@ -385,6 +385,30 @@ __device__ __forceinline__ uint32_t widen2(uint32_t codes) {
 template <int DT, bool kFP8>
 __host__ __device__ constexpr float code_scale() {
     return kFP8 && DT == kF16 ? 256.f : 1.f;
+}
+
+// The rows from w0 on, 32 at most, of each of the CTA's items, as the calling warp wrote them: where they are NaN, again.
+// (Out of the kernel's text: there it took registers from the softmax, eight chunks 267 us instead of 253.)
+template <int DT, int KT, int D, int G, bool kTwo>
+__device__ __noinline__ void nan_rows_again(const PrefillArgs& a, int64_t items, int tiles, int w0) {
+    const int lane = threadIdx.x & 31;
+    for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+        const int h = static_cast<int>(i / tiles);
+        const int4 u = __ldcg(reinterpret_cast<const int4*>(a.tiles) + 2 * (i - static_cast<int64_t>(h) * tiles));
+        for (int row = w0; row < min(w0 + 32, u.z * G); ++row) {  // (u: sequence, first token, tokens, position)
+            const int64_t tok = u.y + row / G, o0 = (tok * a.num_q_heads + h * G + row % G) * D;
+            bool nan = false;
+            for (int d = lane; d < D; d += 32) {
+                float o;
+                if constexpr (kTwo)
+                    o = static_cast<const float*>(a.out)[o0 + d];
+                else
+                    o = Elem<DT>::to_float(static_cast<const typename Elem<DT>::T*>(a.out)[o0 + d]);
+                nan = nan || o != o;
+            }
+            if (__any_sync(0xffffffffu, nan)) exact_row<DT, KT, D>(a, u.x, h, tok, h * G + row % G, u.w + row / G);
+        }
+    }
 }
 
 // kTwo: P in two parts.  kFP8: an E4M3 cache; its codes come by bulk copies, and warps
@@ -733,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
         const bool negative = a.scale_log2 < 0.f;
         uint32_t ns = 0, no = 0, at = 0;
         bool ok = true;
-        if (lane == 0) B->nan_from[warp] = -1;
+        bool again = false;  // this warp wrote a row that is NaN
         Item it;
         if (blockIdx.x < items) it = item_at(blockIdx.x);
         for (int64_t i = blockIdx.x; i < items && ok; i += gridDim.x) {
@@ -974,30 +998,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                 }
                 __syncwarp();
             }
-            if (__any_sync(0xffffffffu, nan && lane < rows) && lane == 0 && B->nan_from[warp] < 0) B->nan_from[warp] = i;
+            again = again || (nan && lane < rows);
         }
         // The rows that this warp wrote as NaN, again (see above).
         __syncwarp();
-        for (int64_t i = ok ? B->nan_from[warp] : -1; i >= 0 && i < items; i += gridDim.x) {
-            const Item x = item_at(i);
-            const int w0 = t * kRowsTile + (warp & 3) * 32;
-            const int rows = min(32, x.ntok * G - w0);
-            for (int row = w0; row < w0 + rows; ++row) {
-                const int64_t o0 = ((x.tok0 + row / G) * a.num_q_heads + x.h * G + row % G) * D;
-                bool nan = false;
-                for (int d = lane; d < D; d += 32) {
-                    float o;
-                    if constexpr (kTwo)
-                        o = static_cast<const float*>(a.out)[o0 + d];
-                    else
-                        o = Elem<DT>::to_float(static_cast<const typename Elem<DT>::T*>(a.out)[o0 + d]);
-                    nan = nan || o != o;
-                }
-                if (__any_sync(0xffffffffu, nan))
-                    exact_row<DT, kFP8 ? static_cast<int>(pkv::kFP8) : DT, D>(a, x.s, x.h, x.tok0 + row / G, x.h * G + row % G,
-                                                                              x.pos0 + row / G);
-            }
-        }
+        if (ok && __any_sync(0xffffffffu, again))
+            nan_rows_again<DT, kFP8 ? static_cast<int>(pkv::kFP8) : DT, D, G, kTwo>(a, items, tiles,
+                                                                                   t * kRowsTile + (warp & 3) * 32);
     }
     tc_fence_before();
     __syncthreads();
