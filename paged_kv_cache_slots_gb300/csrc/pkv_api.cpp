@@ -193,27 +193,27 @@ struct Sight {
 // Whether a windowed decode takes the kernel for small calls (window_decode_small.cu) rather than the persistent
 // one: by estimates of both kernels' times with every sequence as long as its window.  From 892 calls measured with
 // either kernel (graphs, inputs out of L2; 1, 2 and 8 KV heads, windows of 128 to 131,072, batches of 1 to 256):
-//   Small: a wave of CTAs takes 5 us and, for each block that its warps take one after the other, 0.4 us and 0.18 a KiB
-//   of the block's K rows (0.25 over E4M3; 0.65 of it where three warps or fewer share an SM's shared memory), and
-//   all of them no less than 5 TB/s allow (E4M3), or 5.5.  Of 8-CTA clusters three quarters fit at once (16 pairs: 70
-//   us, 4 pairs: 33).
+//   Small: a wave of CTAs takes 6 us and, for each block that its warps take one after the other, 0.3 us and 0.16 a KiB
+//   of the block's K rows (0.21 over E4M3; 0.65 of it where three warps or fewer share an SM's shared memory); all of
+//   them no less than 4.5 TB/s allow (5 with blocks from 16 KiB on, 5.5 with smaller ones and one wave; over E4M3 0.92 of
+//   that).  Of 8-CTA clusters three quarters fit at once (16 pairs: 70 us, 4 pairs: 33).
 //   Persistent: 15 us and the rate that its stages reach: blocks of few heads make small stages (64 sequences, one KV head of
 //   128, blocks of 16, window 8,192: 126 us, small 53), blocks of 24 KiB a head leave it two (16 sequences, 8 KV heads,
 //   blocks of 128, window 8,192: 188, small 107); one long sequence is cut into so many parts that the merge takes 60.
 // The small kernel gives a sequence of any length the same CTAs, and lengths are not known here: one long sequence
 // among short ones waits for its own CTAs alone, where the persistent kernel spreads it over every SM (window 32,768,
 // 1 of 32, 8 KV heads, blocks of 64: 237 us, persistent 47).  So what a CTA may have to stream is bounded: 1.1 MB,
-// or 4.4 MB where the persistent kernel would take a quarter longer on equal lengths.  Of the measured calls 59 are more
-// than 10 % above the faster kernel: lengths far apart (up to 2.5x), or small waves beyond that bound.
+// or 4.4 MB where the persistent kernel would take a quarter longer on equal lengths.  Of the measured calls 55 are more
+// than 10 % above the faster kernel: lengths far apart (up to 2.6x), and what that bound costs equal ones.
 bool small_window(const SmallPlan& plan, int num_seqs, int kv_heads, int row_blocks, int half, bool fp8, int sms) {
     const double bytes = 2.0 * half * row_blocks * num_seqs * kv_heads, h = half / 1024.0;
     const double fit = static_cast<double>(sms) * plan.per_sm * (plan.ctas == 8 ? 0.75 : 1.0);
     double waves = static_cast<double>(num_seqs) * kv_heads * plan.ctas / fit;
     waves = waves < 1 ? 1 : waves < 3 ? std::ceil(waves) : waves;
-    const double step = 0.4 + h * (fp8 ? 0.25 : 0.18) * (plan.warps <= 3 ? 0.65 : 1.0);
+    const double step = 0.3 + h * (fp8 ? 0.21 : 0.16) * (plan.warps <= 3 ? 0.65 : 1.0);
     const int chain = (row_blocks + plan.ctas * plan.warps - 1) / (plan.ctas * plan.warps);
-    double small = waves * (5 + chain * step);  // us
-    const double stream = 5 + bytes / (fp8 ? 5.0e6 : 5.5e6);
+    double small = waves * (6 + chain * step);  // us
+    const double stream = 5 + bytes / ((h >= 16 ? 5.0e6 : waves > 1 ? 4.5e6 : 5.5e6) * (fp8 ? 0.92 : 1.0));
     if (small < stream) small = stream;
     double rate;  // GB/s
     if (h >= 24)
