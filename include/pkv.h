@@ -235,8 +235,9 @@ kv_status_t kv_append_rope(kv_pool_t* pool, int layer, const kv_rope_t* rope, co
  *   z = x / sqrt(mean(x^2) + eps) * weight,
  * the mean over the whole row, and z is rotated as kv_append_rope rotates x
  * (elements from rot_dim on are z's).  Sum, norm and rotation are fp32 and the
- * result is rounded once; a row's sum of squares must be finite in fp32.  V rows
- * are stored as kv_append_rope stores them.
+ * result is rounded once; a row's sum of squares must be finite in fp32, and with
+ * eps 0 not below 2^-126 (a row of zeros gives NaN then).  V rows are stored as
+ * kv_append_rope stores them.
  *   q_weight, k_weight  device, in weight_dtype (src_dtype or KV_F32):
  *                       [head_dim] for all heads (a stride of 0), or a row for
  *                       each head, q_weight_stride (k_weight_stride) elements
@@ -516,7 +517,10 @@ kv_status_t paged_prefill_attention(const void* q, const void* k_cache, const vo
  * max_blocks_per_seq * block_size must be below 2^31.  The other arguments, the
  * workspace and the options are those of paged_decode_attention (of
  * paged_decode_attention_fp8 for an E4M3 cache), and so is the result when the
- * window reaches back to the first token, up to the order of the sums. */
+ * window reaches back to the first token, up to the order of the sums.  Where it
+ * does not, weights in two f16 parts (f16 and E4M3 caches) are held down to 2^-40
+ * of the largest in sight, not 2^-25: a first token that every query looks at may
+ * lie far above the window's.  A score of -inf has a weight of 0. */
 kv_status_t paged_window_decode_attention(const void* q, const void* k_cache, const void* v_cache,
                                           int num_blocks, const int32_t* block_tables,
                                           int max_blocks_per_seq, const int32_t* context_lens,
@@ -541,8 +545,17 @@ kv_status_t paged_window_decode_attention_fp8(const void* q, kv_dtype_t q_dtype,
  * sees the positions j <= p with j > p - window or j < sinks.  Of a table row
  * the entries of blocks that none of the sequence's new tokens sees are not
  * read.  A K or V row that a token does not see takes no part in its row of out,
- * infinities and NaN included (a later new token's, say).  Rows of q behind the
- * last sequence are not read, and those rows of out left as they are.
+ * infinities and NaN included (a later new token's, say; a row that has to be
+ * computed apart for that takes a warp some 9 us for each 32 keys in sight).  A
+ * score of -inf has a weight of 0.  Rows of q behind the last sequence may hold
+ * anything, and those rows of out are left as they are.
+ * Statistics and sums are fp32.  With out_dtype KV_F32 a weight meets V in two
+ * parts of q's type, as in paged_prefill_attention: 2^-17 of it (bf16), 2^-22 (f16,
+ * down to 2^-32 of the row's largest).  With a 16-bit out it meets V rounded once
+ * to q's type, half a step, so such an out lies up to two half steps from the exact
+ * one where paged_prefill_attention's lies one: 2.3e-3 (bf16) and 2.9e-4 (f16) of
+ * the norm over random rows, not 1.7e-3 and 2.1e-4.  KV_F32 caches are summed in
+ * fp32 throughout.
  * workspace: device, 256-byte aligned, of at least
  * paged_window_prefill_workspace_bytes, needs no initialisation, not to be
  * shared by two calls in flight at once.  out may not overlap q.  The other

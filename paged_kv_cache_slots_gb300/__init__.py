@@ -1025,8 +1025,9 @@ def paged_window_prefill_attention(q, k_cache, v_cache, block_tables, query_star
     the first `sinks` ones of its sequence.
 
     Table entries of blocks that none of a sequence's new tokens sees are not read.  Rows of q behind
-    the last sequence (query_start[-1]) are padding: those rows of out stay as they are (a new out holds
-    zeros there).  Everything runs on `stream` (torch's current one unless given)."""
+    the last sequence (query_start[-1]) are padding and may hold anything: those rows of out stay as they
+    are (a new out holds zeros there).  With a 16-bit out_dtype weights are rounded to it before they meet V;
+    out_dtype=torch.float32 keeps twice as many bits of them.  Everything runs on `stream` (torch's current one unless given)."""
     lib = _lib or load_library()
     T, Hq, D = shape = q.shape
     cache = k_cache.shape

@@ -203,7 +203,7 @@ struct Sight {
 // The small kernel gives a sequence of any length the same CTAs, and lengths are not known here: one long sequence
 // among short ones waits for its own CTAs alone, where the persistent kernel spreads it over every SM (window 32,768,
 // 1 of 32, 8 KV heads, blocks of 64: 237 us, persistent 47).  So what a CTA may have to stream is bounded: 1.1 MB,
-// or 4.4 MB where the persistent kernel would take a quarter longer on equal lengths.  Of the measured calls 55 are more
+// or 4.4 MB where the persistent kernel would take a quarter longer on equal lengths.  Of the measured calls some 55 are more
 // than 10 % above the faster kernel: lengths far apart (up to 2.6x), and what that bound costs equal ones.
 bool small_window(const SmallPlan& plan, int num_seqs, int kv_heads, int row_blocks, int half, bool fp8, int sms) {
     const double bytes = 2.0 * half * row_blocks * num_seqs * kv_heads, h = half / 1024.0;

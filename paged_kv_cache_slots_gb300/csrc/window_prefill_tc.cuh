@@ -40,13 +40,16 @@
 // done: a row takes 9 us for each 32 keys in sight (128 dims), and the other roles' waits,
 // which give up after two seconds, must not span that.
 //
-// Tensor memory: S / P 2 x 128 columns, O 2 x 128.  Bound: the tensor cores, 58 % of
-// whose cycles it uses on long windows; the rest is the softmax of a tile, the issuing
-// warp's looks at its barriers, and at short windows the ends of the items.  32 query
-// heads of 128 over 8 KV heads: 16,384 tokens of one prompt behind 16,384 under a window
-// of 4,096 in 835 us (1.32 PFLOP/s), eight chunks of 2,048 under one of 1,024 in 262 us
-// (1.05 PFLOP/s, 48 % of the cycles); over E4M3 caches, where two warps widen the codes,
-// 1,254 and 408 us (0.88 and 0.67 PFLOP/s, 31 %).
+// Tensor memory: S / P 2 x 128 columns, O 2 x 128.  Registers: 168 a thread as launched,
+// 208 in the softmax warps.  With a 16-bit output nothing spills at 128 dims (64: 52 bytes);
+// with an fp32 one 12 bytes are stored and 36 to 124 loaded, over E4M3 16 and 104.
+// Bound: the tensor cores, 61 % of whose cycles it uses on long windows; the rest is the
+// softmax of a tile, the issuing warp's looks at its barriers, and at short windows the
+// ends of the items.  32 query heads of 128 over 8 KV heads: 16,384 tokens of one prompt
+// behind 16,384 under a window of 4,096 in 771 us (1.43 PFLOP/s), eight chunks of 2,048
+// under one of 1,024 in 253 us (1.09 PFLOP/s, 51 % of the cycles), with fp32 outputs 1,076
+// and 348; over E4M3 caches, where two warps widen the codes, 1,224 and 399 us (0.90 and
+// 0.69 PFLOP/s, 32 %).
 #pragma once
 
 #include "decode_kernel.cuh"
