@@ -465,7 +465,7 @@ cudaError_t launch_dt(NormRopeArgs a, int align, int weight_align, int num_sms, 
     const int64_t bytes = static_cast<int64_t>(a.num_q_heads + 2 * a.num_kv_heads) * a.head_dim * kE;
     if (v == 16 / kE && items <= 32 && kRing * bytes <= 69 * 1024) {
         const int per_sm = ring_ctas(static_cast<int>(bytes));
-        const int each = (a.n_tokens + num_sms - 1) / num_sms;  // tokens an SM
+        const int each = (a.n_tokens - 1) / num_sms + 1;  // tokens an SM
         const bool first_round = each <= per_sm && each >= (kE == 4 ? 4 : 3);
         const int from = kE == 4 ? 24 : per_sm >= 6 ? 2 : per_sm >= 4 ? 3 : 16;
         if (first_round || a.n_tokens >= from * num_sms)

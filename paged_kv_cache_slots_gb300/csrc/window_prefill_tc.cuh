@@ -839,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_window_prefill_tc_kernel(co
                     mx = mx * sc - kLower<DT>;
                     const bool move = mx > m_ref && !(sum <= limit);
                     // The step is a whole number, so that it scales what stands in P exactly (down to f16's last place);
-                    // it is 3 at least, or the sum would not have passed the limit.
+                    // it is 2 at least, or the sum would not have passed the limit.
                     if (m_ref > -INFINITY) mx = m_ref + floorf(mx - m_ref);
                     const float f = move ? fast_exp2(m_ref - mx) : 1.f;  // (0 from -inf)
                     if (move) {
